@@ -20,12 +20,14 @@ Q4K_OK = 0
 STATUS_NAMES = {
     0: "Q4K_OK", 1: "Q4K_ERR_NULL", 2: "Q4K_ERR_SHAPE", 3: "Q4K_ERR_TOPK", 4: "Q4K_ERR_WORKSPACE",
     5: "Q4K_ERR_CUDA", 6: "Q4K_ERR_EXPERT_ID", 7: "Q4K_ERR_ALIGN", 8: "Q4K_ERR_MODE", 9: "Q4K_ERR_LIMIT",
-    10: "Q4K_ERR_TIMEOUT",
+    10: "Q4K_ERR_TIMEOUT", 11: "Q4K_ERR_PAGE", 12: "Q4K_ERR_SEQ", 13: "Q4K_ERR_DTYPE",
 }
 SHARED_NONE, SHARED_SIGMOID, SHARED_UNSCALED = 0, 1, 2
 PATH_TWO_LAUNCH, PATH_PERSISTENT, PATH_PERSISTENT_WIDE = 0, 1, 2
 ROUTE_SOFTMAX, ROUTE_SIGMOID_GROUPED = 0, 1
 FMT_AFFINE4, FMT_Q4TP = 1, 2
+F32, BF16 = 0, 1
+ROPE_HALVES, ROPE_PAIRS = 0, 1
 
 # Exported C symbols and their signatures (restype, argtypes).
 _P, _I, _I64, _U64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_size_t
@@ -58,6 +60,13 @@ SIGNATURES = {
                                           _P, _P, _SZ, _P, _P]),
     "q4k_moe_router": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, ctypes.c_float, _I, _I, _P, _P, _P, _P, _P]),
     "q4k_rms_norm": (_I, [_P, _P, _I, _I, ctypes.c_float, _P, _P]),
+    "q4k_qk_norm_rope": (_I, [_P, _P, _I, _I, _I, _I, _I, _I64, _I64, _P, _P, ctypes.c_float, _P, _P, _I, _I, _P, _P, _I,
+                              _I64, _I64, _P]),
+    "q4k_kv_append": (_I, [_P, _P, _I, _I, _I, _I, _I64, _I64, _P, ctypes.c_float, _P, _I, _I, _P, _P, _P, _I, _I, _I, _I,
+                           _P, _P, _P, _P, _P, _P]),
+    "q4k_paged_attention_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "q4k_paged_attention": (_I, [_P, _I, _I, _I, _I, _I, _I64, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I,
+                                 ctypes.c_float, _I, _P, _I64, _P, _SZ, _P, _P]),
     "q4k_quantize_rows": (_I, [_P, _I64, _I, _P, _P]),
     "q4k_stream_ceiling_sink_words": (_I, []),
     "q4k_stream_ceiling": (_I, [_P, _U64, _P, _P]),
@@ -120,6 +129,25 @@ def _cuda(*tensors) -> None:
     for t in tensors:
         if t is not None and not isinstance(t, int) and not t.is_cuda:
             raise ValueError("device tensor expected")
+
+
+def _dtype(*tensors) -> int:
+    """The library's element type of the tensors given (all of one type)."""
+    import torch
+    kinds = {t.dtype for t in tensors if t is not None}
+    if len(kinds) == 1:
+        kind = kinds.pop()
+        if kind == torch.float32:
+            return F32
+        if kind == torch.bfloat16:
+            return BF16
+    raise ValueError("float32 or bfloat16 tensors of one type expected")
+
+
+def _of_type(name, t, *dtypes):
+    """The kernels read these as raw words: a tensor of another element type is refused here."""
+    if t is not None and not isinstance(t, int) and str(t.dtype).replace("torch.", "") not in dtypes:
+        raise ValueError(f"{name}: {' or '.join(dtypes)} expected, got {t.dtype}")
 
 
 # ---- sizes -------------------------------------------------------------------------------------
@@ -281,6 +309,65 @@ def q4k_moe_layer_down(w_down, num_experts, ws_down, shared_inter, act, act_shar
     _check(load().q4k_moe_layer_down(_ptr(w_down), num_experts, _ptr(ws_down), shared_inter, _ptr(act),
                                      _ptr(act_shared), _ptr(ids), m, top_k, hidden, inter, _ptr(expert_out),
                                      _ptr(shared_out), _ptr(workspace), ws_bytes, _ptr(err_flag), _stream(stream)))
+
+
+_BF16_BITS = ("bfloat16", "uint16", "int16")
+_E4M3 = ("float8_e4m3fn", "uint8", "int8")
+
+
+def _paged_types(q_start, seq_lens, page_table, k_cache, v_cache, k_scale, v_scale):
+    for name, t in (("q_start", q_start), ("seq_lens", seq_lens), ("page_table", page_table)):
+        _of_type(name, t, "int32")
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _of_type(name, t, *_E4M3)
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _of_type(name, t, "float32")
+
+
+def q4k_qk_norm_rope(q, k, m, q_heads, kv_heads, head_dim, q_stride, k_stride, w_q, w_k, eps, pos, inv_freq, rot_dim,
+                     rope_mode, q_out, k_out, q_out_stride, k_out_stride, stream=None):
+    """Per-head RMS norm of queries and keys (w_q / w_k bf16 or None) and the position rotation in one pass; strides in
+    elements between tokens; q and k, and q_out and k_out, are float32 or bfloat16; a side with 0 heads may be None."""
+    _cuda(q, k, w_q, w_k, pos, inv_freq, q_out, k_out)
+    _of_type("w_q", w_q, *_BF16_BITS)
+    _of_type("w_k", w_k, *_BF16_BITS)
+    _of_type("pos", pos, "int32")
+    _of_type("inv_freq", inv_freq, "float64")
+    _check(load().q4k_qk_norm_rope(_ptr(q), _ptr(k), _dtype(q, k), m, q_heads, kv_heads, head_dim, q_stride, k_stride,
+                                   _ptr(w_q), _ptr(w_k), float(eps), _ptr(pos), _ptr(inv_freq), rot_dim, rope_mode,
+                                   _ptr(q_out), _ptr(k_out), _dtype(q_out, k_out), q_out_stride, k_out_stride,
+                                   _stream(stream)))
+
+
+def q4k_kv_append(k, v, m, kv_heads, head_dim, k_stride, v_stride, w_k, eps, inv_freq, rot_dim, rope_mode, q_start,
+                  seq_lens, page_table, batch, max_pages, page_size, num_pages, k_cache, v_cache, k_scale, v_scale,
+                  err_flag=None, stream=None):
+    """The new tokens' keys (normed and rotated on the way) and values into the paged e4m3 cache."""
+    _cuda(k, v, w_k, inv_freq, q_start, seq_lens, page_table, k_cache, v_cache, k_scale, v_scale, err_flag)
+    _of_type("w_k", w_k, *_BF16_BITS)
+    _of_type("inv_freq", inv_freq, "float64")
+    _paged_types(q_start, seq_lens, page_table, k_cache, v_cache, k_scale, v_scale)
+    _check(load().q4k_kv_append(_ptr(k), _ptr(v), _dtype(k, v), m, kv_heads, head_dim, k_stride, v_stride, _ptr(w_k),
+                                float(eps), _ptr(inv_freq), rot_dim, rope_mode, _ptr(q_start), _ptr(seq_lens),
+                                _ptr(page_table), batch, max_pages, page_size, num_pages, _ptr(k_cache), _ptr(v_cache),
+                                _ptr(k_scale), _ptr(v_scale), _ptr(err_flag), _stream(stream)))
+
+
+def q4k_paged_attention_workspace_size(batch, m, q_heads, kv_heads, head_dim) -> int:
+    return int(load().q4k_paged_attention_workspace_size(batch, m, q_heads, kv_heads, head_dim))
+
+
+def q4k_paged_attention(q, m, q_heads, kv_heads, head_dim, q_stride, k_cache, v_cache, k_scale, v_scale, q_start,
+                        seq_lens, page_table, batch, max_pages, page_size, num_pages, max_q_len, max_len, scale, window,
+                        out, out_stride, workspace, ws_bytes, err_flag=None, stream=None):
+    """Causal attention of the new tokens over the paged e4m3 cache (window 0: every earlier token)."""
+    _cuda(q, k_cache, v_cache, k_scale, v_scale, q_start, seq_lens, page_table, out, workspace, err_flag)
+    _paged_types(q_start, seq_lens, page_table, k_cache, v_cache, k_scale, v_scale)
+    _check(load().q4k_paged_attention(_ptr(q), _dtype(q, out), m, q_heads, kv_heads, head_dim, q_stride, _ptr(k_cache),
+                                      _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(q_start), _ptr(seq_lens),
+                                      _ptr(page_table), batch, max_pages, page_size, num_pages, max_q_len, max_len,
+                                      float(scale), window, _ptr(out), out_stride, _ptr(workspace), ws_bytes,
+                                      _ptr(err_flag), _stream(stream)))
 
 
 def q4k_quantize_rows(x, rows, k, out, stream=None):

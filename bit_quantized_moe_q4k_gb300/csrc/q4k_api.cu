@@ -7,6 +7,7 @@
 #include <string>
 
 #include "q4k_internal.cuh"
+#include "q4k_paged.cuh"
 
 using namespace q4k;
 
@@ -339,6 +340,65 @@ int check_layer(const void* w_a, const void* w_b, int num_experts, int shared_in
     }
     if (!w_a) return fail(Q4K_ERR_NULL, "NULL slab");
     if (!aligned16(w_a) || (w_b && !aligned16(w_b))) return fail(Q4K_ERR_ALIGN, "slabs must be 16-byte aligned");
+    return Q4K_OK;
+}
+
+// ---- the attention side -------------------------------------------------------------------------
+int elem_bytes(int dtype) { return dtype == Q4K_F32 ? 4 : 2; }
+
+int check_dtype(int dtype) {
+    if (dtype == Q4K_F32 || dtype == Q4K_BF16) return Q4K_OK;
+    return fail(Q4K_ERR_DTYPE, "dtype must be Q4K_F32 or Q4K_BF16 (got %d)", dtype);
+}
+
+// Rows of `heads` heads, `stride` elements apart.
+int check_rows(const char* name, const void* p, int64_t stride, int64_t width, int dtype) {
+    if (!p) return fail(Q4K_ERR_NULL, "%s is NULL", name);
+    if (stride < width) return fail(Q4K_ERR_SHAPE, "%s rows of %lld elements overlap at stride %lld", name, (long long)width, (long long)stride);
+    if (!aligned16(p) || stride * elem_bytes(dtype) % 16 != 0)
+        return fail(Q4K_ERR_ALIGN, "%s must be 16-byte aligned with a stride of a multiple of 16 bytes", name);
+    return Q4K_OK;
+}
+
+int check_rope(const double* inv_freq, int rot_dim, int rope_mode, int head_dim) {
+    if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16 != 0)
+        return fail(Q4K_ERR_SHAPE, "rot_dim must be a multiple of 16 in [0, head_dim] (got %d)", rot_dim);
+    if (rope_mode != Q4K_ROPE_HALVES && rope_mode != Q4K_ROPE_PAIRS)
+        return fail(Q4K_ERR_MODE, "rope_mode must be Q4K_ROPE_HALVES or Q4K_ROPE_PAIRS (got %d)", rope_mode);
+    if (rot_dim > 0 && !inv_freq) return fail(Q4K_ERR_NULL, "inv_freq is NULL");
+    if (rot_dim > 0 && (reinterpret_cast<uintptr_t>(inv_freq) & 7u)) return fail(Q4K_ERR_ALIGN, "inv_freq must be 8-byte aligned");
+    return Q4K_OK;
+}
+
+int check_norm_weight(const uint16_t* w) {
+    if (reinterpret_cast<uintptr_t>(w) & 7u) return fail(Q4K_ERR_ALIGN, "norm weights must be 8-byte aligned");
+    return Q4K_OK;
+}
+
+// The sizes and pointers of a paged cache and the batch that reads or fills it.
+int check_paged(int m, int batch, int kv_heads, int head_dim, int max_pages, int page_size, int num_pages,
+                const void* q_start, const void* seq_lens, const void* table, const void* k_cache, const void* v_cache,
+                const void* k_scale, const void* v_scale, PagedBatch* B) {
+    if (m < 0 || batch < 0) return fail(Q4K_ERR_SHAPE, "m and batch must be >= 0 (got %d, %d)", m, batch);
+    if (head_dim != 64 && head_dim != 128) return fail(Q4K_ERR_SHAPE, "head_dim must be 64 or 128 (got %d)", head_dim);
+    if (kv_heads < 1) return fail(Q4K_ERR_SHAPE, "kv_heads must be >= 1 (got %d)", kv_heads);
+    if (kv_heads > 65535) return fail(Q4K_ERR_LIMIT, "kv_heads must be <= 65535 (got %d)", kv_heads);
+    if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
+        return fail(Q4K_ERR_SHAPE, "page_size must be 16, 32, 64 or 128 (got %d)", page_size);
+    if (num_pages < 1 || max_pages < 1) return fail(Q4K_ERR_SHAPE, "num_pages and max_pages must be >= 1 (got %d, %d)", num_pages, max_pages);
+    if ((int64_t)max_pages * page_size > (int64_t)1 << 30) return fail(Q4K_ERR_LIMIT, "max_pages*page_size must be <= 2^30");
+    if (m > 1 << 24 || batch > 1 << 24) return fail(Q4K_ERR_LIMIT, "m and batch must be <= 2^24 (got %d, %d)", m, batch);
+    if (m == 0 || batch == 0) return Q4K_OK;
+    if (!q_start || !seq_lens || !table || !k_cache || !v_cache || !k_scale || !v_scale)
+        return fail(Q4K_ERR_NULL, "q_start, seq_lens, page_table, the caches and their scales are required");
+    if (!aligned16(k_cache) || !aligned16(v_cache)) return fail(Q4K_ERR_ALIGN, "caches must be 16-byte aligned");
+    for (const void* p : {q_start, seq_lens, table, k_scale, v_scale})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return fail(Q4K_ERR_ALIGN, "q_start, seq_lens, page_table and scales must be 4-byte aligned");
+    B->q_start = static_cast<const int32_t*>(q_start);
+    B->seq_lens = static_cast<const int32_t*>(seq_lens);
+    B->table = static_cast<const int32_t*>(table);
+    B->batch = batch; B->m = m; B->max_pages = max_pages; B->num_pages = num_pages;
+    B->page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
     return Q4K_OK;
 }
 
@@ -748,6 +808,91 @@ int q4k_rms_norm(const float* d_x, const uint16_t* d_w, int m, int hidden, float
     if (!aligned16(d_x) || !aligned16(d_out) || (reinterpret_cast<uintptr_t>(d_w) & 7u))
         return fail(Q4K_ERR_ALIGN, "x and out must be 16-byte aligned, w 8-byte aligned");
     return cuda_status(launch_rms_norm(d_x, d_w, m, hidden, eps, d_out, stream), "rms_norm launch");
+}
+
+int q4k_qk_norm_rope(const void* d_q, const void* d_k, int dtype, int m, int q_heads, int kv_heads, int head_dim,
+                     int64_t q_stride, int64_t k_stride, const uint16_t* d_w_q, const uint16_t* d_w_k, float eps,
+                     const int32_t* d_pos, const double* d_inv_freq, int rot_dim, int rope_mode, void* d_q_out,
+                     void* d_k_out, int out_dtype, int64_t q_out_stride, int64_t k_out_stride, cudaStream_t stream) {
+    int st = check_dtype(dtype);
+    if (!st) st = check_dtype(out_dtype);
+    if (st) return st;
+    if (m < 0) return fail(Q4K_ERR_SHAPE, "m must be >= 0 (got %d)", m);
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return fail(Q4K_ERR_SHAPE, "head_dim must be 64, 128 or 256 (got %d)", head_dim);
+    if (q_heads < 0 || kv_heads < 0 || q_heads + (int64_t)kv_heads < 1) return fail(Q4K_ERR_SHAPE, "q_heads and kv_heads must be >= 0, not both 0");
+    if (q_heads > 65535 || kv_heads > 65535) return fail(Q4K_ERR_LIMIT, "q_heads and kv_heads must be <= 65535");
+    if (!st) st = check_rope(d_inv_freq, rot_dim, rope_mode, head_dim);
+    if (!st) st = check_norm_weight(d_w_q);
+    if (!st) st = check_norm_weight(d_w_k);
+    if (st || m == 0) return st;
+    if (q_heads > 0) {
+        st = check_rows("q", d_q, q_stride, (int64_t)q_heads * head_dim, dtype);
+        if (!st) st = check_rows("q_out", d_q_out, q_out_stride, (int64_t)q_heads * head_dim, out_dtype);
+    }
+    if (!st && kv_heads > 0) {
+        st = check_rows("k", d_k, k_stride, (int64_t)kv_heads * head_dim, dtype);
+        if (!st) st = check_rows("k_out", d_k_out, k_out_stride, (int64_t)kv_heads * head_dim, out_dtype);
+    }
+    if (st) return st;
+    if (rot_dim > 0 && !d_pos) return fail(Q4K_ERR_NULL, "pos is NULL");
+    return cuda_status(launch_norm_rope(d_q, d_k, dtype, out_dtype, m, q_heads, kv_heads, head_dim, q_stride, k_stride,
+                                        d_w_q, d_w_k, eps, d_pos, d_inv_freq, rot_dim, rope_mode, d_q_out, d_k_out,
+                                        q_out_stride, k_out_stride, stream),
+                       "norm and rotation launch");
+}
+
+int q4k_kv_append(const void* d_k, const void* d_v, int dtype, int m, int kv_heads, int head_dim, int64_t k_stride,
+                  int64_t v_stride, const uint16_t* d_w_k, float eps, const double* d_inv_freq, int rot_dim,
+                  int rope_mode, const int32_t* d_q_start, const int32_t* d_seq_lens, const int32_t* d_page_table,
+                  int batch, int max_pages, int page_size, int num_pages, void* d_k_cache, void* d_v_cache,
+                  float* d_k_scale, float* d_v_scale, int* d_err_flag, cudaStream_t stream) {
+    PagedBatch B{};
+    int st = check_dtype(dtype);
+    if (!st) st = check_paged(m, batch, kv_heads, head_dim, max_pages, page_size, num_pages, d_q_start, d_seq_lens,
+                              d_page_table, d_k_cache, d_v_cache, d_k_scale, d_v_scale, &B);
+    if (!st) st = check_rope(d_inv_freq, rot_dim, rope_mode, head_dim);
+    if (!st) st = check_norm_weight(d_w_k);
+    if (st || m == 0 || batch == 0) return st;
+    st = check_rows("k", d_k, k_stride, (int64_t)kv_heads * head_dim, dtype);
+    if (!st) st = check_rows("v", d_v, v_stride, (int64_t)kv_heads * head_dim, dtype);
+    if (st) return st;
+    return cuda_status(launch_kv_append(B, d_k, d_v, dtype, k_stride, v_stride, kv_heads, head_dim, d_w_k, eps,
+                                        d_inv_freq, rot_dim, rope_mode, static_cast<uint8_t*>(d_k_cache),
+                                        static_cast<uint8_t*>(d_v_cache), d_k_scale, d_v_scale, d_err_flag, stream),
+                       "cache append launch");
+}
+
+size_t q4k_paged_attention_workspace_size(int batch, int m, int q_heads, int kv_heads, int head_dim) {
+    if (batch < 0 || m < 0 || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128))
+        return 0;
+    return align_up(attn_workspace_bytes(head_dim));
+}
+
+int q4k_paged_attention(const void* d_q, int dtype, int m, int q_heads, int kv_heads, int head_dim, int64_t q_stride,
+                        const void* d_k_cache, const void* d_v_cache, const float* d_k_scale, const float* d_v_scale,
+                        const int32_t* d_q_start, const int32_t* d_seq_lens, const int32_t* d_page_table, int batch,
+                        int max_pages, int page_size, int num_pages, int max_q_len, int max_len, float scale,
+                        int window, void* d_out, int64_t out_stride, void* d_workspace, size_t ws_bytes,
+                        int* d_err_flag, cudaStream_t stream) {
+    PagedBatch B{};
+    int st = check_dtype(dtype);
+    if (!st) st = check_paged(m, batch, kv_heads, head_dim, max_pages, page_size, num_pages, d_q_start, d_seq_lens,
+                              d_page_table, d_k_cache, d_v_cache, d_k_scale, d_v_scale, &B);
+    if (st) return st;
+    if (q_heads < kv_heads || q_heads % kv_heads != 0) return fail(Q4K_ERR_SHAPE, "kv_heads must divide q_heads (got %d, %d)", q_heads, kv_heads);
+    if (q_heads > 65535) return fail(Q4K_ERR_LIMIT, "q_heads must be <= 65535 (got %d)", q_heads);
+    if ((int64_t)m * (q_heads / kv_heads) > (int64_t)1 << 30) return fail(Q4K_ERR_LIMIT, "m*q_heads/kv_heads must be <= 2^30");
+    if (max_q_len < 0 || max_len < 0 || window < 0) return fail(Q4K_ERR_SHAPE, "max_q_len, max_len and window must be >= 0");
+    if (m == 0 || batch == 0) return Q4K_OK;
+    st = check_rows("q", d_q, q_stride, (int64_t)q_heads * head_dim, dtype);
+    if (!st) st = check_rows("out", d_out, out_stride, (int64_t)q_heads * head_dim, dtype);
+    if (!st) st = check_workspace(d_workspace, ws_bytes, q4k_paged_attention_workspace_size(batch, m, q_heads, kv_heads, head_dim));
+    if (st) return st;
+    return cuda_status(launch_attention(B, d_q, dtype, q_stride, q_heads, kv_heads, head_dim,
+                                        static_cast<const uint8_t*>(d_k_cache), static_cast<const uint8_t*>(d_v_cache),
+                                        d_k_scale, d_v_scale, max_len, scale, window, d_out, out_stride, d_workspace,
+                                        d_err_flag, stream),
+                       "attention launch");
 }
 
 int q4k_quantize_rows(const float* d_x, int64_t rows, int k, void* d_out, cudaStream_t stream) {

@@ -47,6 +47,22 @@ cudaError_t launch_router(const float* x, const uint16_t* w, const float* bias, 
 int router_max_hidden();
 cudaError_t launch_rms_norm(const float* x, const uint16_t* w, int m, int hidden, float eps, float* out,
                             cudaStream_t stream);
+// The attention side (q4k_qkrope.cu, q4k_kv.cu, q4k_attn.cu); PagedBatch: q4k_paged.cuh.
+struct PagedBatch;
+cudaError_t launch_norm_rope(const void* q, const void* k, int dtype, int out_dtype, int m, int q_heads, int kv_heads,
+                             int head_dim, int64_t q_stride, int64_t k_stride, const uint16_t* w_q,
+                             const uint16_t* w_k, float eps, const int32_t* pos, const double* inv_freq, int rot_dim,
+                             int rope_mode, void* q_out, void* k_out, int64_t q_out_stride, int64_t k_out_stride,
+                             cudaStream_t stream);
+cudaError_t launch_kv_append(const PagedBatch& B, const void* k, const void* v, int dtype, int64_t k_stride,
+                             int64_t v_stride, int kv_heads, int head_dim, const uint16_t* w_k, float eps,
+                             const double* inv_freq, int rot_dim, int rope_mode, uint8_t* k_cache, uint8_t* v_cache,
+                             float* k_scale, float* v_scale, int* err_flag, cudaStream_t stream);
+size_t attn_workspace_bytes(int head_dim);
+cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int64_t q_stride, int q_heads, int kv_heads,
+                             int head_dim, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
+                             const float* v_scale, int max_len, float scale, int window, void* out, int64_t out_stride,
+                             void* workspace, int* err_flag, cudaStream_t stream);
 cudaError_t launch_quantize(const float* x, int64_t rows, int k, uint8_t* out, cudaStream_t stream);
 cudaError_t launch_stream_ceiling(const void* src, uint64_t bytes, uint32_t* sink, cudaStream_t stream);
 // Up to 5 small copies (sizes multiples of 4 bytes) in one launch; sources may be host memory

@@ -1,0 +1,227 @@
+// q4k_paged.cuh -- what the attention-side kernels share: the sequences of a batch, the paged
+// 8-bit cache's addresses and scales, and the position rotation's angles.
+//
+// The cache: codes in e4m3, [num_pages][kv_heads][page_size][head_dim], one scale per (page, kv
+// head); value = code * scale. Sequence i's cached tokens lie in the pages table[i][0], table[i][1],
+// ... in order; its new tokens are rows q_start[i] .. q_start[i+1] of the inputs and the last ones
+// of its seq_lens[i] cached tokens.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "q4k_internal.cuh"
+
+namespace q4k {
+
+struct PagedBatch {
+    const int32_t* q_start;
+    const int32_t* seq_lens;
+    const int32_t* table;
+    int batch, m, max_pages, page_shift, num_pages;
+};
+
+// Sequence i's new rows [start, start + n) and cached length; the first new token's position is
+// len - n (negative: the first rows have no token). Values that leave their ranges are clamped
+// (no access leaves its buffer) and `bad` is set.
+struct SeqSpan {
+    int start, n, len;
+};
+__device__ __forceinline__ SeqSpan seq_span(const PagedBatch& B, int i, bool* bad) {
+    const int a = __ldcg(B.q_start + i), b = __ldcg(B.q_start + i + 1), l = __ldcg(B.seq_lens + i);
+    SeqSpan s;
+    s.start = min(max(a, 0), B.m);
+    s.n = min(max(b, s.start), B.m) - s.start;
+    s.len = min(max(l, 0), B.max_pages << B.page_shift);
+    *bad = s.start != a || s.start + s.n != b || s.len != l || s.len < s.n;
+    return s;
+}
+
+// Page of the sequence, or -1 (flag raised) when the table holds an id outside [0, num_pages).
+__device__ __forceinline__ int page_id(const PagedBatch& B, int seq, int page, int* err_flag) {
+    const int p = __ldcg(B.table + (int64_t)seq * B.max_pages + page);
+    if ((unsigned)p < (unsigned)B.num_pages) return p;
+    raise_flag(err_flag, Q4K_ERR_PAGE);
+    return -1;
+}
+
+// ---- element access -----------------------------------------------------------------------------
+// What an earlier kernel of the stream may have written is read through L2 (ld.global.cg) here and
+// in the kernels: a programmatic dependent launch starts before that kernel ends, so its SM's L1
+// may hold lines from before the writes.
+template <typename T> struct Vec;  // N consecutive elements of an input row as fp32
+template <> struct Vec<float> {
+    template <int N> static __device__ __forceinline__ void load(const float* p, float (&v)[N]) {
+        if constexpr (N == 2) {
+            const float2 a = __ldcg(reinterpret_cast<const float2*>(p));
+            v[0] = a.x; v[1] = a.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                const float4 a = __ldcg(reinterpret_cast<const float4*>(p + i));
+                v[i] = a.x; v[i + 1] = a.y; v[i + 2] = a.z; v[i + 3] = a.w;
+            }
+        }
+    }
+    template <int N> static __device__ __forceinline__ void store(float* p, const float (&v)[N]) {
+        if constexpr (N == 2) {
+            *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i += 4)
+                *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
+    }
+};
+template <> struct Vec<__nv_bfloat16> {
+    template <int N> static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&v)[N]) {
+        uint32_t w[N / 2];
+        if constexpr (N == 2) {
+            w[0] = __ldcg(reinterpret_cast<const unsigned*>(p));
+        } else if constexpr (N == 4) {
+            const uint2 a = __ldcg(reinterpret_cast<const uint2*>(p));
+            w[0] = a.x; w[1] = a.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i += 8) {
+                const uint4 a = __ldcg(reinterpret_cast<const uint4*>(p + i));
+                w[i / 2] = a.x; w[i / 2 + 1] = a.y; w[i / 2 + 2] = a.z; w[i / 2 + 3] = a.w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+    template <int N> static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[N]) {
+        uint32_t w[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        if constexpr (N == 2) {
+            *reinterpret_cast<uint32_t*>(p) = w[0];
+        } else if constexpr (N == 4) {
+            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i += 8)
+                *reinterpret_cast<uint4*>(p + i) = make_uint4(w[i / 2], w[i / 2 + 1], w[i / 2 + 2], w[i / 2 + 3]);
+        }
+    }
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// ---- rotation -----------------------------------------------------------------------------------
+// The angle pos * f is needed only modulo one turn. With F = f / 2pi mod 1 as a 64-bit fraction,
+// pos * F mod 2^64 is that fraction of a turn: integer wrap-around is the range reduction, exact
+// but for F's own rounding (|pos| * 2^-53 of f, below 2^-22 of a turn at pos = 2^31 for f <= 1).
+// F comes from f's 53 significant bits by one 64 x 64 bit product with 2/pi * 2^64 (fp64
+// arithmetic is two orders of magnitude slower than integers here).
+__device__ __forceinline__ uint64_t turn_fraction(double f) {
+    const uint64_t bits = (uint64_t)__double_as_longlong(f);
+    const int e = (int)((bits >> 52) & 0x7FF);                             // f = M * 2^(e - 1086)
+    const uint64_t M = ((bits & 0xFFFFFFFFFFFFFull) | (e ? 1ull << 52 : 0)) << 11;
+    const uint64_t hi = __umul64hi(M, 0xA2F9836E4E441529ull);              // M * 2/pi
+    const int sh = 1024 - e;                                               // turns * 2^64 = hi * 2^(e - 1024)
+    uint64_t F = sh >= 64 ? 0 : sh >= 0 ? hi >> sh : sh > -64 ? hi << -sh : 0;
+    return (bits >> 63) ? 0 - F : F;
+}
+__device__ __forceinline__ void turn_sincos(int pos, uint64_t F, float* s, float* c) {
+    const int t = (int)(((uint64_t)(int64_t)pos * F) >> 32);               // turn * 2^32, in [-1/2, 1/2)
+    sincospif((float)t * 4.656612873077393e-10f, s, c);                    // 2^-31: half turns
+}
+
+// A lane's N consecutive dims (c0 = N * lane) of a head spread over a warp: the sine and cosine
+// that each of them takes. Dims at or past rot_dim get (0, 1).
+template <int N>
+__device__ __forceinline__ void lane_angles(int c0, int pos, const double* inv_freq, int rot_dim, int pairs_mode,
+                                            float (&sn)[N], float (&cs)[N]) {
+    const int half = rot_dim >> 1;
+#pragma unroll
+    for (int i = 0; i < N; ++i) { sn[i] = 0.0f; cs[i] = 1.0f; }
+    if (c0 >= rot_dim) return;
+    if (pairs_mode) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            turn_sincos(pos, turn_fraction(inv_freq[(c0 + i) >> 1]), &sn[i], &cs[i]);
+            sn[i + 1] = sn[i];
+            cs[i + 1] = cs[i];
+        }
+    } else {
+        const int j0 = c0 < half ? c0 : c0 - half;
+#pragma unroll
+        for (int i = 0; i < N; ++i) turn_sincos(pos, turn_fraction(inv_freq[j0 + i]), &sn[i], &cs[i]);
+    }
+}
+// Rotate the lane's dims: (a, b) -> (a cos - b sin, b cos + a sin). rot_dim is a multiple of 16
+// (2N <= 16), so the partner dims of a lane are those of one other lane ("halves") or its own.
+template <int N>
+__device__ __forceinline__ void lane_rotate(int c0, int rot_dim, int pairs_mode, const float (&sn)[N],
+                                            const float (&cs)[N], float (&v)[N]) {
+    if (pairs_mode) {
+        if (c0 >= rot_dim) return;
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const float a = v[i], b = v[i + 1];
+            v[i] = a * cs[i] - b * sn[i];
+            v[i + 1] = b * cs[i] + a * sn[i];
+        }
+    } else {
+        const int half = rot_dim >> 1, lane = threadIdx.x & 31;
+        const bool lo = c0 < half;
+        const int src = c0 < rot_dim ? lane + (lo ? half / N : -(half / N)) : lane;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float o = __shfl_sync(0xffffffffu, v[i], src);
+            if (c0 < rot_dim) v[i] = lo ? v[i] * cs[i] - o * sn[i] : v[i] * cs[i] + o * sn[i];
+        }
+    }
+}
+// The head's norm over a warp: v * w / sqrt(mean v^2 + eps)
+template <int N>
+__device__ __forceinline__ void lane_norm(const float (&w)[N], int dim, float eps, float (&v)[N]) {
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) ss = fmaf(v[i], v[i], ss);
+    ss = warp_sum(ss);
+    const float r = 1.0f / sqrtf(ss / (float)dim + eps);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = v[i] * r * w[i];
+}
+
+// ---- e4m3 ---------------------------------------------------------------------------------------
+// Two e4m3 codes (low byte first) to two halves, and back (round to nearest even, saturating).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t lo16) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(lo16));
+    return r;
+}
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 h;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %2, %1;\n\tcvt.u32.u16 %0, h;\n\t}"
+        : "=r"(r)
+        : "f"(lo), "f"(hi));
+    return r;
+}
+
+constexpr int kMinScaleExp = -64;  // the scale of a page of zeros, and the smallest one
+
+// The least e >= kMinScaleExp with amax <= 448 * 2^e; amax finite and >= 0. (448 = 1.75 * 2^8.)
+__device__ __forceinline__ int scale_exponent(float amax) {
+    const uint32_t b = __float_as_uint(amax);
+    const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return max(e, kMinScaleExp);
+}
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // |e| <= 126
+
+}  // namespace q4k

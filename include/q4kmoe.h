@@ -75,7 +75,10 @@ typedef enum {
     Q4K_ERR_ALIGN = 7,     /* slab not 16-byte aligned, or activation rows not 16-byte aligned */
     Q4K_ERR_MODE = 8,      /* shared_mode not in {0, 1, 2}                                   */
     Q4K_ERR_LIMIT = 9,     /* a size beyond an implementation limit (see each call)          */
-    Q4K_ERR_TIMEOUT = 10   /* device flag value: a pipeline wait in a kernel gave up (bounded) */
+    Q4K_ERR_TIMEOUT = 10,  /* device flag value: a pipeline wait in a kernel gave up (bounded) */
+    Q4K_ERR_PAGE = 11,     /* device flag value: a page id was outside [0, num_pages)          */
+    Q4K_ERR_SEQ = 12,      /* device flag value: q_start or seq_lens do not fit together       */
+    Q4K_ERR_DTYPE = 13     /* dtype not Q4K_F32 or Q4K_BF16                                    */
 } q4k_status;
 
 #define Q4K_MAX_TOP_K 16
@@ -390,6 +393,91 @@ int q4k_moe_layer_forward_routed(const void* d_w_gate, const void* d_w_up, const
  */
 int q4k_rms_norm(const float* d_x, const uint16_t* d_w, int m, int hidden, float eps, float* d_out,
                  cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * The attention half of a decoder layer: q4k_qk_norm_rope, q4k_kv_append, q4k_paged_attention
+ * (no counterpart in the studied pages; additions of this library).
+ *
+ * Element types: Q4K_F32 or Q4K_BF16 inputs; arithmetic in fp32, rounded once at the store.
+ * Rows: a token's heads lie side by side, head h's head_dim elements at row + h*head_dim; rows
+ * are `*_stride` elements apart, so the parts of a fused projection's output can be passed as
+ * they are. Every pointer to rows is 16-byte aligned, every stride a multiple of 16 bytes.
+ *
+ * The paged cache (caller-owned device memory):
+ *   k_cache, v_cache: e4m3 codes [num_pages][kv_heads][page_size][head_dim], 16-byte aligned
+ *   k_scale, v_scale: fp32 [num_pages][kv_heads]; value = code * scale. q4k_kv_append writes
+ *     powers of two; q4k_paged_attention takes any positive normal scale up to 2^120.
+ *   page_size 16, 32, 64 or 128; head_dim 64 or 128.
+ * A batch of sequences (device memory, read on the device only):
+ *   q_start   [batch + 1]: sequence i's new tokens are rows q_start[i] .. q_start[i+1] - 1 of the
+ *     inputs; rising, within [0, m]. A sequence may have no new tokens.
+ *   seq_lens  [batch]: its cached tokens, the new ones (its last) included.
+ *   page_table[batch][max_pages]: token j is in page page_table[i][j / page_size], slot
+ *     j % page_size. Entries past a sequence's last page are not read.
+ * A new token's position is its index in the sequence.
+ * Device flags: a page id outside [0, num_pages) raises Q4K_ERR_PAGE (the append drops the
+ * page's tokens, the attention sees none in it); q_start falling or outside [0, m], seq_lens
+ * negative, above max_pages*page_size or below the new tokens raise Q4K_ERR_SEQ (the values are
+ * clamped to what fits; new tokens before position 0 are dropped, their output rows zero). No
+ * access leaves its buffer. Two sequences may share pages they only read; a page that receives
+ * tokens belongs to one sequence.
+ * Launches are programmatic dependents that wait for the previous kernel before reading.
+ * Limits: max_pages*page_size <= 2^30, kv_heads <= 65535.
+ */
+#define Q4K_F32 0
+#define Q4K_BF16 1
+#define Q4K_ROPE_HALVES 0 /* dims j and j + rot_dim/2 turn together */
+#define Q4K_ROPE_PAIRS 1  /* dims 2j and 2j + 1 turn together       */
+
+/* q4k_qk_norm_rope -- the norm of each query and key head with the position rotation in the
+ * same pass. For every token t and head:
+ *   y[c] = x[c] * bf16(w[c]) / sqrt(sum_c x[c]^2 / head_dim + eps)      (w NULL: y = x)
+ *   (a, b) -> (a cos - b sin, b cos + a sin), angle pos[t] * inv_freq[j], over the rot_dim/2
+ *   pairs of the first rot_dim dims (rope_mode); the other dims stay as they are.
+ *   d_q / d_q_out: q_heads heads; d_k / d_k_out: kv_heads heads; either count may be 0 (its
+ *     pointers are then not read). A result may replace its input (same type and stride).
+ *   d_w_q, d_w_k: bf16 [head_dim] (8-byte aligned) or NULL; d_pos: int32 [m];
+ *   d_inv_freq: fp64 [rot_dim/2], radians per position, so any scaling of the frequencies is a
+ *     table (the angle is reduced exactly: far positions lose nothing); rot_dim 0: no rotation,
+ *     both unused.
+ * head_dim 64, 128 or 256; rot_dim a multiple of 16, at most head_dim. One launch. */
+int q4k_qk_norm_rope(const void* d_q, const void* d_k, int dtype, int m, int q_heads, int kv_heads, int head_dim,
+                     int64_t q_stride, int64_t k_stride, const uint16_t* d_w_q, const uint16_t* d_w_k, float eps,
+                     const int32_t* d_pos, const double* d_inv_freq, int rot_dim, int rope_mode, void* d_q_out,
+                     void* d_k_out, int out_dtype, int64_t q_out_stride, int64_t k_out_stride, cudaStream_t stream);
+
+/* q4k_kv_append -- the new tokens' keys and values into the paged cache. Keys are normed
+ * (d_w_k, NULL: not) and rotated by their positions (rot_dim 0: not) on the way, as by
+ * q4k_qk_norm_rope; values go as they are. The scale of a (page, head) is 2^e, e the least
+ * integer >= -64 with max |x| <= 448 * 2^e over the finite x written to it; a page that held
+ * tokens of the sequence already keeps the larger of its scale and that one, and its codes are
+ * rounded again when the scale grows (exact but for e4m3's subnormals). Codes are rounded to
+ * nearest even; infinities become the largest code, NaN stays NaN. Slots past a sequence's last
+ * token are left as they are. Calling it again with the same arguments changes nothing. One launch. */
+int q4k_kv_append(const void* d_k, const void* d_v, int dtype, int m, int kv_heads, int head_dim, int64_t k_stride,
+                  int64_t v_stride, const uint16_t* d_w_k, float eps, const double* d_inv_freq, int rot_dim,
+                  int rope_mode, const int32_t* d_q_start, const int32_t* d_seq_lens, const int32_t* d_page_table,
+                  int batch, int max_pages, int page_size, int num_pages, void* d_k_cache, void* d_v_cache,
+                  float* d_k_scale, float* d_v_scale, int* d_err_flag, cudaStream_t stream);
+
+/* q4k_paged_attention -- causal attention of the new tokens over the cache (their own keys and
+ * values appended before):
+ *   out[t, h] = sum_j softmax_j(scale * q[t, h] . k[j, h / (q_heads/kv_heads)]) v[j, ..]
+ * over the tokens j of t's sequence with pos(t) - window < j <= pos(t) (window 0: all j <= pos(t)).
+ * A row that sees no token is zero. What the tokens a row does not see hold (NaN included) does
+ * not reach it.
+ *   d_q [m, q_heads*head_dim], d_out the same type; d_out must not overlap d_q.
+ *   max_q_len, max_len: upper bounds on a sequence's new and cached tokens that choose the
+ *     kernels and their grids; results do not depend on their being tight or right.
+ *   fp32 queries keep 22 bits of q and of the softmax weights; bf16 ones are exact.
+ * kv_heads divides q_heads. Workspace: q4k_paged_attention_workspace_size bytes, any contents. */
+size_t q4k_paged_attention_workspace_size(int batch, int m, int q_heads, int kv_heads, int head_dim);
+int q4k_paged_attention(const void* d_q, int dtype, int m, int q_heads, int kv_heads, int head_dim, int64_t q_stride,
+                        const void* d_k_cache, const void* d_v_cache, const float* d_k_scale, const float* d_v_scale,
+                        const int32_t* d_q_start, const int32_t* d_seq_lens, const int32_t* d_page_table, int batch,
+                        int max_pages, int page_size, int num_pages, int max_q_len, int max_len, float scale,
+                        int window, void* d_out, int64_t out_stride, void* d_workspace, size_t ws_bytes,
+                        int* d_err_flag, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------------
  * q4k_quantize_rows -- fp32 [rows, k] -> Q4_K bytes [rows, k/256*144] on the device

@@ -1,0 +1,688 @@
+"""GPU parity of the attention side (q4k_qk_norm_rope, q4k_kv_append, q4k_paged_attention) with
+plain fp64 implementations written here, through the C ABI.
+
+Tolerances are counted from the kernels' roundings, u = 2^-24 (half a step of fp32):
+  * norm and rotation: the sum of squares has at most 13 additions, all terms positive (13 u,
+    halved by the root), mean, eps, root and reciprocal 3.5 u, two products 2 u: 12 u of the normed
+    value; sine and cosine are within 5.4 u (pi u from rounding the turn to fp32, 2 u of sincospi,
+    0.3 u of the 32-bit turn); two products and a sum: 2 u. Together below 24 u (|a| + |b|).
+  * the append adds half a step of e4m3: 2^-4 |x|, or 2^-10 of the scale where that is larger.
+  * attention, per row: |ds| <= S (2^-22 + (d/16 + 8) 2^-23) with S the largest sum_c |q_c k_c| *
+    scale (the split of q, the chain of tensor-core sums, truncating), x's own rounding
+    2^-23 (|x| + |e|), ex2 2^-22; a weight error dp / p moves the result by at most twice that times
+    sum_j p_j |v_j|; summing n tokens adds (n/64 + 40) u of the same. fp16 weights (bf16 rows)
+    add 2^-11 of it, and the store half a step of the output type.
+"""
+import math
+
+import numpy as np
+import pytest
+
+import bit_quantized_moe_q4k_gb300 as q4k
+from bit_quantized_moe_q4k_gb300 import inputs
+
+from helpers import dev, err_flag, host
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+EPS = 1e-6
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+STEP = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def rows(x, dtype, stride=None):
+    """Device rows of x [m, n] in `dtype`, `stride` elements apart (the gap holds NaN)."""
+    m, n = x.shape
+    t = torch.full((max(m, 1), stride or n), float("nan"), dtype=DT[dtype], device="cuda")
+    t[:m, :n] = dev(x.astype(np.float32)).to(DT[dtype])
+    return t
+
+
+# ---- e4m3 --------------------------------------------------------------------------------------
+
+def e4m3_values():
+    c = np.arange(256)
+    s, e, f = np.where(c & 128, -1.0, 1.0), (c >> 3) & 15, c & 7
+    v = s * np.where(e == 0, f * 2.0 ** -9, (1 + f / 8) * 2.0 ** (e - 7.0))
+    v[[0x7F, 0xFF]] = np.nan
+    return v
+
+
+E4M3 = e4m3_values()
+
+
+def e4m3_round(x):
+    """Codes of x: nearest, ties to even, saturating (finite x)."""
+    pos = E4M3[:0x7F]
+    a = np.minimum(np.abs(x), 448.0)
+    hi = np.clip(np.searchsorted(pos, a), 1, 0x7E)
+    lo = hi - 1
+    d0, d1 = a - pos[lo], pos[hi] - a
+    code = np.where(d0 < d1, lo, np.where(d1 < d0, hi, np.where(lo % 2 == 0, lo, hi)))
+    return (code | np.where(np.signbit(x), 128, 0)).astype(np.uint8)
+
+
+def exponent(amax):
+    if amax == 0:
+        return -64
+    return max(-64, math.ceil(math.log2(amax / 448.0) - 1e-13))
+
+
+# ---- norm and rotation -------------------------------------------------------------------------
+
+def norm_rope_ref(x, w, pos, inv_freq, mode):
+    """x [m, heads, d] in fp64 -> (result, |a| + |b| of each element's pair)."""
+    y = x if w is None else x / np.sqrt((x * x).mean(-1, keepdims=True) + EPS) * w
+    out, mag = y.copy(), np.abs(y)
+    half = len(inv_freq)
+    if half:
+        ang = pos.astype(np.float64)[:, None] * inv_freq
+        turn = np.exp(1j * ang)[:, None, :]
+        a, b = (slice(0, half), slice(half, 2 * half)) if mode == "halves" else (slice(0, 2 * half, 2), slice(1, 2 * half, 2))
+        z = (y[..., a] + 1j * y[..., b]) * turn
+        out[..., a], out[..., b] = z.real, z.imag
+        mag[..., a] = mag[..., b] = np.abs(y[..., a]) + np.abs(y[..., b])
+    return out, mag
+
+
+def freqs(rot, theta=1e6):
+    return theta ** (-np.arange(rot // 2, dtype=np.float64) / max(1, rot // 2))
+
+
+MODES = {"halves": q4k.ROPE_HALVES, "pairs": q4k.ROPE_PAIRS}
+
+
+def run_norm_rope(seed, m, hq, hk, d, rot, mode, dtype, odtype, norm=True, pos=None, pad=0, theta=1e6):
+    g = np.random.default_rng(seed)
+    row = (hq + hk) * d + pad
+    x = rows(g.standard_normal((m, row)) * np.exp(g.standard_normal((1, row))), dtype)
+    pos = g.integers(0, 1 << 20, m).astype(np.int32) if pos is None else np.asarray(pos, np.int32)
+    wq, wk = (inputs.to_bf16_bits((1 + 0.2 * g.standard_normal(d)).astype(np.float32)) for _ in range(2))
+    f = freqs(rot, theta)
+    qo = torch.full((m, hq * d + 16), float("nan"), dtype=DT[odtype], device="cuda")
+    ko = torch.full((m, hk * d + 16), float("nan"), dtype=DT[odtype], device="cuda")
+    q4k.q4k_qk_norm_rope(x if hq else None, x[:, hq * d:] if hk else None, m, hq, hk, d, row, row,
+                         dev(wq.view(np.int16)) if norm else None, dev(wk.view(np.int16)) if norm else None, EPS,
+                         dev(pos), dev(f) if rot else None, rot, MODES[mode], qo if hq else None, ko if hk else None,
+                         hq * d + 16, hk * d + 16)
+    xs = f64(x)
+    for out, heads, w, at in ((qo, hq, wq, 0), (ko, hk, wk, hq * d)):
+        if not heads:
+            continue
+        wf = (w.astype(np.uint32) << 16).view(np.float32).astype(np.float64) if norm else None
+        ref, mag = norm_rope_ref(xs[:, at:at + heads * d].reshape(m, heads, d), wf, pos, f, mode)
+        got = f64(out)
+        assert np.isnan(got[:, heads * d:]).all(), "wrote past the heads"
+        got = got[:, :heads * d].reshape(m, heads, d)
+        tol = 24 * U * mag + (STEP[odtype] * np.abs(ref) * (1 + 2.0 ** -10) if odtype == "bf16" else 0)
+        worst = np.max(np.abs(got - ref) - tol)
+        assert worst <= 0, f"off by {worst} beyond the bound"
+
+
+@pytest.mark.parametrize("dtype,odtype", [("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("mode", ["halves", "pairs"])
+def test_norm_rope_types(d, mode, dtype, odtype):
+    run_norm_rope(d, 5, 3, 2, d, d, mode, dtype, odtype)
+
+
+@pytest.mark.parametrize("m,hq,hk,rot,mode,norm,pad", [
+    (1, 32, 4, 128, "halves", True, 0), (1, 1, 0, 128, "pairs", True, 8), (7, 0, 5, 64, "halves", True, 0),
+    (33, 5, 1, 16, "pairs", True, 24), (2, 7, 7, 48, "halves", False, 8), (3, 2, 2, 0, "halves", True, 0),
+    (3, 2, 2, 112, "pairs", False, 0), (300, 9, 3, 128, "halves", True, 64),
+])
+def test_norm_rope_shapes(m, hq, hk, rot, mode, norm, pad):
+    run_norm_rope(m + rot, m, hq, hk, 128, rot, mode, "f32", "f32", norm, pad=pad)
+
+
+def test_norm_rope_far_and_negative_positions():
+    """Positions to the ends of int32: the angle loses nothing to its size (fp64's own product is
+    off by 2^-53 of up to 2^31 radians here, 2^-22: the reference is formed from exact integers)."""
+    pos = np.array([0, 1, -1, 2 ** 24 + 1, 2 ** 31 - 1, -2 ** 31, 123456789], np.int64)
+    d, theta = 64, 10000.0
+    x = np.random.default_rng(3).standard_normal((len(pos), d))
+    f = freqs(d, theta)
+    xt = rows(x, "f32")
+    out = torch.empty_like(xt)
+    q4k.q4k_qk_norm_rope(xt, None, len(pos), 1, 0, d, d, d, None, None, EPS, dev(pos.astype(np.int32)), dev(f), d,
+                         q4k.ROPE_HALVES, out, None, d, d)
+    from fractions import Fraction
+    tau = Fraction(62831853071795864769252867665590057683943387987502116419498891846156328125724, 10 ** 76)
+    ang = np.empty((len(pos), d // 2))
+    for i, p in enumerate(pos):
+        for j, v in enumerate(f):
+            turns = Fraction(float(v)) * int(p) / tau
+            ang[i, j] = float((turns - math.floor(turns)) * tau)
+    xs = f64(xt)
+    z = (xs[:, :d // 2] + 1j * xs[:, d // 2:]) * np.exp(1j * ang)
+    ref = np.concatenate([z.real, z.imag], 1)
+    mag = np.tile(np.abs(xs[:, :d // 2]) + np.abs(xs[:, d // 2:]), (1, 2))
+    # F is cut to 2^-64 of a turn and its 53-bit source: |pos| * 2^-63 turns at most
+    assert (np.abs(f64(out) - ref) <= (24 * U + 2 * math.pi * 2.0 ** -31) * mag).all()
+
+
+def test_norm_rope_in_place_and_nonfinite():
+    """A result may replace its input; an infinity or NaN in one head leaves the other heads alone."""
+    m, d = 4, 128
+    g = np.random.default_rng(5)
+    x = rows(g.standard_normal((m, 3 * d)), "f32")
+    x[1, d + 5] = float("nan")
+    x[2, 2 * d] = float("inf")
+    pos, f = dev(np.arange(m, dtype=np.int32)), dev(freqs(64))
+    out = torch.empty_like(x)
+    q4k.q4k_qk_norm_rope(x, None, m, 3, 0, d, 3 * d, 3 * d, None, None, EPS, pos, f, 64, 0, out, None, 3 * d, 3 * d)
+    y = x.clone()
+    q4k.q4k_qk_norm_rope(y, None, m, 3, 0, d, 3 * d, 3 * d, None, None, EPS, pos, f, 64, 0, y, None, 3 * d, 3 * d)
+    assert torch.equal(out.view(torch.int32), y.view(torch.int32))
+    bad = ~np.isfinite(host(out))
+    assert set(zip(*np.where(bad))) <= {(1, d + 5), (1, d + 37), (2, 2 * d), (2, 2 * d + 32)} and bad.sum() >= 2
+
+
+# ---- the paged cache ---------------------------------------------------------------------------
+
+class Cache:
+    """Random codes and power-of-two scales; every slot filled (recycled pages), NaN codes in none."""
+
+    def __init__(self, seed, pages, heads, page, d, pow2=True):
+        g = np.random.default_rng(seed)
+        self.heads, self.page, self.d, self.pages = heads, page, d, pages
+        shape = (pages, heads, page, d)
+        self.codes = {s: e4m3_round(g.standard_normal(shape) * 60) for s in "kv"}
+        self.scale = {"k": 2.0 ** g.integers(-9, -5, shape[:2]), "v": 2.0 ** g.integers(-12, -4, shape[:2])}
+        if not pow2:
+            self.scale = {s: v * g.uniform(1, 2, shape[:2]) for s, v in self.scale.items()}
+        self.scale = {s: v.astype(np.float32) for s, v in self.scale.items()}
+        self.order = g.permutation(pages).astype(np.int32)
+
+    def upload(self):
+        self.dev = {s: dev(self.codes[s]) for s in "kv"}
+        self.dev_scale = {s: dev(self.scale[s]) for s in "kv"}
+
+    def values(self, side, ids, length):
+        """[heads, length, d] fp64 values of the pages `ids`."""
+        v = E4M3[self.codes[side][ids]] * self.scale[side][ids].astype(np.float64)[..., None, None]
+        return v.transpose(1, 0, 2, 3).reshape(self.heads, -1, self.d)[:, :length]
+
+
+def tables(cache, lens, extra=1):
+    """Page table rows taken from the cache's permutation; entries past the last page are junk."""
+    need = [-(-n // cache.page) for n in lens]
+    t = np.full((len(lens), max(need + [1]) + extra), 0x7FFFFFF0, np.int32)
+    at = 0
+    for i, n in enumerate(need):
+        t[i, :n] = cache.order[at:at + n]
+        at += n
+    assert at <= cache.pages
+    return t
+
+
+def q_starts(new):
+    return np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+
+
+# ---- append ------------------------------------------------------------------------------------
+
+def run_append(seed, new, ctx, heads, d, page, dtype, rot=None, mode="halves", norm=True, gain=1.0, times=1):
+    g = np.random.default_rng(seed)
+    lens = [n + c for n, c in zip(new, ctx)]
+    pages = sum(-(-n // page) for n in lens) + 2
+    c = Cache(seed, pages, heads, page, d)
+    c.upload()
+    table = tables(c, lens)
+    m = sum(new)
+    rot = d if rot is None else rot
+    kv = rows(g.standard_normal((m, 2 * heads * d)) * gain, dtype, 2 * heads * d + 8)
+    w = inputs.to_bf16_bits((1 + 0.2 * g.standard_normal(d)).astype(np.float32))
+    f = freqs(rot)
+    flag = err_flag()
+    for _ in range(times):
+        q4k.q4k_kv_append(kv, kv[:, heads * d:], m, heads, d, 2 * heads * d + 8, 2 * heads * d + 8,
+                          dev(w.view(np.int16)) if norm else None, EPS, dev(f) if rot else None, rot, MODES[mode],
+                          dev(q_starts(new)), dev(np.array(lens, np.int32)), dev(table), len(new), table.shape[1], page,
+                          pages, c.dev["k"], c.dev["v"], c.dev_scale["k"], c.dev_scale["v"], flag)
+    assert int(host(flag)[0]) == 0
+    codes = {s: host(c.dev[s]) for s in "kv"}
+    scale = {s: host(c.dev_scale[s]) for s in "kv"}
+    x = f64(kv)[:m, :2 * heads * d].reshape(m, 2, heads, d)
+    wf = (w.astype(np.uint32) << 16).view(np.float32).astype(np.float64) if norm else None
+    seen = {s: np.zeros(c.codes[s].shape[:3], bool) for s in "kv"}
+    row = 0
+    for i, (n, length) in enumerate(zip(new, lens)):
+        pos = np.arange(length - n, length)
+        k, mag = norm_rope_ref(x[row:row + n, 0], wf, pos, f, mode)
+        err = {"k": 24 * U * mag, "v": np.zeros_like(mag)}
+        val = {"k": k, "v": x[row:row + n, 1]}
+        for p in range((length - n) // page, -(-length // page)) if n else ():
+            lo, hi = max(length - n, p * page), min(length, (p + 1) * page)
+            pid, held = table[i, p], max(length - n, p * page) - p * page
+            for s in "kv":
+                for h in range(heads):
+                    part = val[s][lo - (length - n):hi - (length - n), h]
+                    slack = err[s][lo - (length - n):hi - (length - n), h]
+                    amax = np.abs(part).max()
+                    ok = {exponent(amax), exponent(max(0, amax - slack.max())), exponent(amax + slack.max())}
+                    old = c.scale[s][pid, h]
+                    want = {max(2.0 ** e, old) if held else 2.0 ** e for e in ok}
+                    sc = float(scale[s][pid, h])
+                    assert sc in want, (s, pid, h, sc, want)
+                    got = E4M3[codes[s][pid, h, held:hi - p * page]] * sc
+                    tol = np.maximum(2.0 ** -4 * np.abs(part), 2.0 ** -10 * sc) * (1 + 2.0 ** -20) + slack
+                    assert (np.abs(got - part) <= tol).all()
+                    again = e4m3_round(E4M3[c.codes[s][pid, h, :held]] * (old / sc)) if held else None
+                    if held:
+                        assert np.array_equal(E4M3[codes[s][pid, h, :held]], E4M3[again])
+                    seen[s][pid, h, :hi - p * page] = True
+        row += n
+    for s in "kv":  # every other slot as it was
+        assert np.array_equal(codes[s][~seen[s]], c.codes[s][~seen[s]])
+        touched = seen[s].any(-1)
+        assert np.array_equal(scale[s][~touched], c.scale[s][~touched])
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_append_pages_and_types(page, d, dtype):
+    run_append(page + d, [1, 5, page, 2 * page + 3], [0, page - 2, 7, 1], 2, d, page, dtype)
+
+
+@pytest.mark.parametrize("new,ctx,kw", [
+    ([1], [0], {}), ([1], [15], {}), ([1], [16], {}), ([1, 0, 1], [3, 9, 0], {}),
+    ([300], [0], dict(mode="pairs")), ([2, 40, 1], [31, 0, 200], dict(rot=32, norm=False)),
+    ([3, 3], [5, 20], dict(rot=0)), ([4], [6], dict(gain=1e-6, norm=False, rot=0)),
+    ([4], [6], dict(gain=1e5, norm=False, rot=0)), ([4, 1], [6, 9], dict(gain=0.0, norm=False)),
+    ([1] * 70, list(range(70)), {}),
+])
+def test_append_lengths(new, ctx, kw):
+    run_append(len(new) + new[0], new, ctx, 3, 128, 16, "f32", **kw)
+
+
+def test_append_twice_changes_nothing():
+    run_append(9, [5, 1], [3, 18], 2, 128, 16, "f32", gain=1e3, norm=False, times=3)
+
+
+def test_append_token_by_token_equals_at_once():
+    """Power-of-two scales: a page filled one token at a time holds the values of one call, but
+    where a code passed through e4m3's subnormals under a larger scale."""
+    heads, d, page, n = 2, 64, 32, 32
+    g = np.random.default_rng(12)
+    kv = rows(g.standard_normal((n, 2 * heads * d)) * np.exp(0.3 * g.standard_normal((n, 1))), "f32")
+    table = dev(np.array([[1]], np.int32))
+    got = []
+    for steps in ([n], [1] * n):
+        c = Cache(1, 2, heads, page, d)
+        c.upload()
+        at = 0
+        for s in steps:
+            q4k.q4k_kv_append(kv[at:], kv[at:, heads * d:], s, heads, d, 2 * heads * d, 2 * heads * d, None, EPS, None, 0,
+                              0, dev(np.array([0, s], np.int32)), dev(np.array([at + s], np.int32)), table, 1, 1, page,
+                              2, c.dev["k"], c.dev["v"], c.dev_scale["k"], c.dev_scale["v"])
+            at += s
+        got.append([E4M3[host(c.dev[s])[1]] * host(c.dev_scale[s])[1].astype(np.float64)[:, None, None] for s in "kv"]
+                   + [host(c.dev_scale[s])[1] for s in "kv"])
+    a, b = got
+    for i in (2, 3):
+        assert np.array_equal(a[i], b[i])
+    for i in (0, 1):
+        unit = a[i + 2].astype(np.float64)[:, None, None]
+        assert (np.abs(a[i] - b[i]) <= np.where(np.abs(a[i]) >= unit * 2.0 ** -6, 0.0, unit * 2.0 ** -9)).all()
+
+
+def test_append_nonfinite():
+    """Infinities saturate at the scale of the finite values, NaN stays NaN, the rest is as ever."""
+    heads, d, page = 1, 64, 16
+    x = np.ones((3, 2 * d))
+    x[0, 3], x[1, 4], x[2, d + 1], x[1, d + 2] = np.inf, np.nan, -np.inf, np.nan
+    kv = rows(x, "f32")
+    c = Cache(2, 1, heads, page, d)
+    c.upload()
+    q4k.q4k_kv_append(kv, kv[:, d:], 3, heads, d, 2 * d, 2 * d, None, EPS, None, 0, 0, dev(np.array([0, 3], np.int32)),
+                      dev(np.array([3], np.int32)), dev(np.zeros((1, 1), np.int32)), 1, 1, page, 1, c.dev["k"],
+                      c.dev["v"], c.dev_scale["k"], c.dev_scale["v"])
+    for s, at in (("k", 0), ("v", d)):
+        sc = float(host(c.dev_scale[s])[0, 0])
+        assert sc == 2.0 ** exponent(1.0)
+        got = E4M3[host(c.dev[s])[0, 0, :3]] * sc
+        want = x[:, at:at + d].copy()
+        want[np.isinf(want)] = np.sign(want[np.isinf(want)]) * 448 * sc
+        assert np.array_equal(got, want, equal_nan=True)
+
+
+@pytest.mark.parametrize("what", ["page_high", "page_negative", "len_short", "len_long", "start_falls", "start_past"])
+def test_append_bad_indexes_raise_the_flag(what):
+    """Indexes that do not fit: the flag is raised, nothing outside the right pages is written."""
+    heads, d, page, pages = 2, 64, 16, 6
+    c = Cache(4, pages, heads, page, d)
+    c.upload()
+    start, lens = np.array([0, 3, 6], np.int32), np.array([3, 20], np.int32)
+    table = np.array([[0, 1], [2, 3]], np.int32)
+    status = 12
+    if what == "page_high":
+        table[0, 0], status = pages, 11
+    elif what == "page_negative":
+        table[0, 0], status = -1, 11
+    elif what == "len_short":
+        lens[0] = 2
+    elif what == "len_long":
+        lens[1] = 33
+    elif what == "start_falls":
+        start[:] = [0, 7, 6]
+    else:
+        start[2] = 9
+    kv = rows(np.random.default_rng(1).standard_normal((6, 2 * heads * d)), "f32")
+    flag = err_flag()
+    q4k.q4k_kv_append(kv, kv[:, heads * d:], 6, heads, d, 2 * heads * d, 2 * heads * d, None, EPS, None, 0, 0, dev(start),
+                      dev(lens), dev(table), 2, 2, page, pages, c.dev["k"], c.dev["v"], c.dev_scale["k"],
+                      c.dev_scale["v"], flag)
+    assert int(host(flag)[0]) == status
+    for s in "kv":
+        assert np.array_equal(host(c.dev[s])[4:], c.codes[s][4:])
+        if what.startswith("page"):
+            assert np.array_equal(host(c.dev[s])[:2], c.codes[s][:2])  # dropped, not written elsewhere
+
+
+# ---- attention ---------------------------------------------------------------------------------
+
+def attention_ref(q, cache, table, new, lens, group, scale, window, dtype):
+    """fp64 result and bound, [m, q_heads, d]."""
+    m, hq, d = q.shape
+    out, tol = np.zeros((m, hq, d)), np.zeros((m, hq, d))
+    row = 0
+    for i, (n, length) in enumerate(zip(new, lens)):
+        ids = table[i, :-(-length // cache.page)]
+        k, v = (cache.values(s, ids, length) for s in "kv")
+        for r in range(n):
+            pos = length - n + r
+            lo = max(0, pos - window + 1) if window else 0
+            if pos < 0:
+                continue
+            for h in range(hq):
+                kk, vv, qq = k[h // group, lo:pos + 1], v[h // group, lo:pos + 1], q[row + r, h]
+                s = kk @ qq * scale
+                p = np.exp(s - s.max())
+                p /= p.sum()
+                big = scale * (np.abs(kk) @ np.abs(qq)).max()
+                ds = big * (2.0 ** -22 + (d / 16 + 8) * 2.0 ** -23)
+                x = (np.abs(s).max() * 1.45 + 64 + 14) * 2.0 ** -23 + 2.0 ** -22
+                mean_abs = p @ np.abs(vv)
+                rel = 2 * (ds + x) + ((pos + 1 - lo) / 64 + 40) * U
+                if dtype == "bf16":
+                    rel += 2.0 ** -11 * 1.01
+                out[row + r, h] = p @ vv
+                tol[row + r, h] = rel * mean_abs + STEP[dtype] * np.abs(out[row + r, h]) * 1.01
+        row += n
+    return out, tol
+
+
+def run_attention(seed, new, lens, hq, hk, d, page, dtype, window=0, q_gain=1.0, pow2=True, pad=0, hints=None,
+                  cache=None, table=None, check=True, flagged=0, codes_after=None):
+    g = np.random.default_rng(seed)
+    c = cache or Cache(seed, sum(-(-n // page) for n in lens) + 2, hk, page, d, pow2)
+    if codes_after:
+        codes_after(c)
+    c.upload()
+    table = tables(c, lens) if table is None else table
+    m = sum(new)
+    q = rows(g.standard_normal((m, hq * d)) * q_gain, dtype, hq * d + pad)
+    out = torch.full((max(m, 1), hq * d + pad), 7.0, dtype=DT[dtype], device="cuda")
+    nbytes = q4k.q4k_paged_attention_workspace_size(len(new), m, hq, hk, d)
+    ws = torch.full((nbytes,), 0xFF, dtype=torch.uint8, device="cuda")
+    flag = err_flag()
+    scale = 1 / math.sqrt(d)
+    maxq, maxl = hints or (max(new), max(lens))
+    for _ in range(2):
+        q4k.q4k_paged_attention(q, m, hq, hk, d, hq * d + pad, c.dev["k"], c.dev["v"], c.dev_scale["k"],
+                                c.dev_scale["v"], dev(q_starts(new)), dev(np.array(lens, np.int32)), dev(table),
+                                len(new), table.shape[1], page, c.pages, maxq, maxl, scale, window, out, hq * d + pad,
+                                ws, nbytes, flag)
+    got = f64(out)
+    assert int(host(flag)[0]) == flagged
+    if pad:
+        assert (got[:, hq * d:] == 7.0).all()
+    got = got[:m, :hq * d].reshape(m, hq, d)
+    if check:
+        ref, tol = attention_ref(f64(q)[:m, :hq * d].reshape(m, hq, d), c, table, new, lens, hq // hk, scale, window, dtype)
+        worst = np.max(np.abs(got - ref) / np.maximum(tol, 1e-300))
+        assert np.isfinite(got).all() and worst <= 1, f"{worst} of the bound"
+    return got
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("length", [1, 2, 15, 16, 17, 63, 64, 65, 129, 700])
+def test_attention_single_token_lengths(length, d, dtype):
+    run_attention(length, [1], [length], 8, 2, d, 16, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("hq,hk", [(1, 1), (2, 2), (3, 1), (14, 2), (16, 2), (32, 4), (16, 1), (20, 1), (40, 1)])
+def test_attention_head_groups(hq, hk, dtype):
+    run_attention(hq, [1, 1, 2], [40, 3, 90], hq, hk, 128, 32, dtype)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attention_pages_ragged_batch(page, dtype):
+    run_attention(page, [1] * 7, [1, 16, 127, 128, 129, 500, 33], 6, 2, 128, page, dtype, pad=16)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new,lens,window", [
+    ([3], [3], 0), ([5, 1, 4], [50, 1, 4], 0), ([9], [300], 0), ([1, 2], [200, 100], 1), ([4], [200], 16),
+    ([4, 1], [200, 129], 17), ([6], [100], 100), ([6], [100], 1000), ([0, 1, 0], [5, 9, 0], 0),
+    ([33], [33], 0), ([70, 1, 40], [70, 300, 111], 0), ([130], [200], 0), ([130], [200], 33), ([257, 129], [257, 700], 0),
+    ([300], [421], 150),
+])
+def test_attention_several_tokens_and_windows(new, lens, window, dtype):
+    run_attention(sum(lens), new, lens, 8, 2, 128, 32, dtype, window)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new,lens,hq,hk,page,window", [
+    ([100], [100], 4, 4, 16, 0), ([90, 300], [90, 300], 7, 1, 64, 0), ([150], [1000], 3, 3, 128, 64),
+    ([65, 66, 1, 200], [65, 400, 50, 201], 10, 2, 16, 0),
+])
+def test_attention_prompts_short_heads(new, lens, hq, hk, page, window, dtype):
+    run_attention(sum(lens), new, lens, hq, hk, 64, page, dtype, window)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attention_long_axis_is_split(dtype):
+    run_attention(5, [1], [20011], 8, 1, 128, 64, dtype)
+    run_attention(6, [1, 1, 1], [9000, 2, 4097], 4, 2, 64, 16, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("gain", [0.0, 1e-30, 30.0, 1e20])
+def test_attention_query_magnitudes(gain, dtype):
+    """Queries of any size; at 1e20 the softmax is a choice of one token."""
+    if gain < 1e10:
+        run_attention(8, [1, 2], [70, 90], 8, 2, 128, 16, dtype, q_gain=gain)
+        run_attention(9, [140], [180], 8, 2, 128, 16, dtype, q_gain=gain)
+    else:
+        assert np.isfinite(run_attention(8, [1, 2], [70, 90], 8, 2, 128, 16, dtype, q_gain=gain, check=False)).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attention_any_positive_scale(dtype):
+    run_attention(21, [1, 3, 100], [130, 90, 120], 8, 2, 128, 16, dtype, pow2=False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attention_value_scales_far_apart(dtype):
+    """Pages of tiny values next to pages of large ones: each keeps its weight in the sum."""
+    def spread(c):
+        c.scale["v"][:] = (2.0 ** np.resize([-40.0, 0.0, 30.0, -64.0, -3.0], c.scale["v"].size)).reshape(c.scale["v"].shape)
+    run_attention(22, [1, 2, 90], [130, 90, 200], 8, 2, 128, 16, dtype, codes_after=spread)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new,lens", [([1, 1], [5, 33]), ([3], [40]), ([80], [100]), ([200, 2], [200, 18])])
+def test_attention_nan_in_slots_past_the_end(new, lens, dtype):
+    page = 16
+
+    def spoil(c):
+        at = 0
+        for n in lens:
+            k = -(-n // page)
+            last = c.order[at + k - 1]
+            at += k
+            for s in "kv":
+                c.codes[s][last, :, n - (k - 1) * page:] = 0x7F
+    run_attention(sum(lens), new, lens, 8, 2, 128, page, dtype, codes_after=spoil)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,length,window", [(4, 40, 0), (6, 200, 20), (150, 200, 0), (150, 300, 40)])
+def test_attention_nan_reaches_only_the_rows_that_see_it(n, length, window, d, dtype):
+    """NaN in one value dim of one token: that dim of the rows that see the token, nothing else;
+    NaN in a key: every dim of those rows."""
+    page, hq, hk, dim = 16, 4, 2, 5
+    lens = [length]
+    clean = run_attention(n, [n], lens, hq, hk, d, page, dtype, window)
+    for side in "vk":
+        for tok in (length - n // 2, length - 1, length - n - 3 if window else length - n + 1):
+            def spoil(c):
+                c.codes[side][c.order[tok // page], 1, tok % page, dim] = 0xFF
+            got = run_attention(n, [n], lens, hq, hk, d, page, dtype, window, codes_after=spoil, check=False)
+            pos = np.arange(length - n, length)
+            sees = (tok <= pos) & (tok > pos - window if window else True)
+            want = np.zeros_like(clean, bool)
+            want[sees, hq // hk:, dim if side == "v" else slice(None)] = True
+            assert np.array_equal(np.isnan(got), want), (side, tok)
+            if side == "v":
+                assert np.array_equal(got[~want], clean[~want])
+            else:
+                assert np.array_equal(got[~sees], clean[~sees]) and np.array_equal(got[:, :hq // hk], clean[:, :hq // hk])
+
+
+def test_attention_results_do_not_depend_on_hints_or_neighbours():
+    """Hints choose kernels and grids: a sequence's result stays within the bound whatever they say."""
+    for hints in ((1, 1), (300, 100000), (0, 0)):
+        run_attention(31, [1, 40, 2], [400, 90, 17], 8, 2, 128, 16, "f32", hints=hints)
+        run_attention(32, [1, 140, 2], [400, 190, 17], 8, 2, 128, 16, "bf16", hints=hints)
+
+
+def test_attention_rows_before_the_sequence_are_zero():
+    got = run_attention(3, [4, 2], [2, 0], 8, 2, 128, 16, "f32", flagged=12, table=np.array([[1], [0]], np.int32),
+                        cache=Cache(3, 2, 2, 16, 128))
+    assert (got[:2] == 0).all() and (got[4:] == 0).all() and (got[2:4] != 0).any()
+
+
+@pytest.mark.parametrize("new", [[1, 1], [90, 1]])
+def test_attention_bad_page_ids(new):
+    """A page id outside the cache: flagged, its tokens are not seen; the other sequence is right."""
+    page, lens = 16, [100, 40]
+    c = Cache(6, 12, 2, page, 128)
+    table = tables(c, lens)
+    good = run_attention(6, new, lens, 8, 2, 128, page, "f32", cache=c, table=table)
+    for bad in (-1, 12, 0x7FFFFFFF):
+        t = table.copy()
+        t[0, 2] = bad
+        got = run_attention(6, new, lens, 8, 2, 128, page, "f32", cache=c, table=t, check=False, flagged=11)
+        assert np.isfinite(got).all() and np.array_equal(got[new[0]:], good[new[0]:])
+        assert not np.array_equal(got[:new[0]], good[:new[0]])
+
+
+def test_attention_bad_lengths():
+    """Lengths past the page table's row are cut to it and flagged."""
+    page = 16
+    c = Cache(7, 6, 2, page, 128)
+    table = np.array([[0, 1]], np.int32)
+    run_attention(7, [1], [32], 8, 2, 128, page, "f32", cache=c, table=table)
+    got = run_attention(7, [1], [1 << 30], 8, 2, 128, page, "f32", cache=c, table=table, check=False, flagged=12)
+    assert np.array_equal(got, run_attention(7, [1], [32], 8, 2, 128, page, "f32", cache=c, table=table))
+
+
+def test_attention_same_bits_every_call_and_on_another_stream():
+    a = run_attention(40, [1, 1, 60], [5000, 70, 64], 8, 2, 128, 32, "f32", check=False)
+    b = run_attention(40, [1, 1, 60], [5000, 70, 64], 8, 2, 128, 32, "f32", check=False)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        c = run_attention(40, [1, 1, 60], [5000, 70, 64], 8, 2, 128, 32, "f32", check=False)
+    torch.cuda.current_stream().wait_stream(s)
+    assert np.array_equal(a, b) and np.array_equal(a, c)
+
+
+def test_attention_offsets_past_32_bits():
+    """A cache whose last pages lie beyond 2^32 bytes."""
+    hk, page, d = 8, 128, 128
+    pages = (1 << 32) // (hk * page * d) + 64
+    k = torch.zeros((pages, hk, page, d), dtype=torch.uint8, device="cuda")
+    v = torch.zeros_like(k)
+    ks = torch.ones((pages, hk), device="cuda")
+    vs = torch.ones((pages, hk), device="cuda")
+    g = np.random.default_rng(2)
+    ids = np.array([[pages - 1, 3, pages - 40]], np.int32)
+    small = Cache(9, 3, hk, page, d)
+    for i in range(3):
+        for full, s in ((k, "k"), (v, "v")):
+            full[int(ids[0, i])] = dev(small.codes[s][i])
+        ks[int(ids[0, i])] = dev(small.scale["k"][i])
+        vs[int(ids[0, i])] = dev(small.scale["v"][i])
+    for n in (1, 160):
+        q = rows(g.standard_normal((n, hk * d)), "f32")
+        out = torch.empty_like(q)
+        nbytes = q4k.q4k_paged_attention_workspace_size(1, n, hk, hk, d)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        q4k.q4k_paged_attention(q, n, hk, hk, d, hk * d, k, v, ks, vs, dev(np.array([0, n], np.int32)),
+                                dev(np.array([300], np.int32)), dev(ids), 1, 3, page, pages, n, 300, 0.09, 0, out,
+                                hk * d, ws, nbytes)
+        ref, tol = attention_ref(f64(q).reshape(n, hk, d), small, np.array([[0, 1, 2]]), [n], [300], 1, 0.09, 0, "f32")
+        assert (np.abs(f64(out).reshape(n, hk, d) - ref) <= tol).all()
+    # an append into the last page
+    kv = rows(g.standard_normal((1, 2 * hk * d)), "f32")
+    q4k.q4k_kv_append(kv, kv[:, hk * d:], 1, hk, d, 2 * hk * d, 2 * hk * d, None, EPS, None, 0, 0,
+                      dev(np.array([0, 1], np.int32)), dev(np.array([1], np.int32)),
+                      dev(np.array([[pages - 1]], np.int32)), 1, 1, page, pages, k, v, ks, vs)
+    got = E4M3[host(v[pages - 1, :, 0])] * host(vs[pages - 1]).astype(np.float64)[:, None]
+    x = f64(kv)[0, hk * d:].reshape(hk, d)
+    assert (np.abs(got - x) <= np.maximum(2.0 ** -4 * np.abs(x), 2.0 ** -10 * host(vs[pages - 1])[:, None])).all()
+
+
+def test_the_three_calls_in_a_graph():
+    """Append and attend captured once and replayed with new inputs in the same buffers."""
+    hq, hk, d, page = 8, 2, 128, 16
+    c = Cache(50, 8, hk, page, d)
+    c.upload()
+    qkv = torch.empty((2, (hq + 2 * hk) * d), device="cuda")
+    row = (hq + 2 * hk) * d
+    q = torch.empty((2, hq * d), device="cuda")
+    out = torch.empty_like(q)
+    f, pos = dev(freqs(d)), dev(np.array([20, 40], np.int32))
+    w = dev(inputs.to_bf16_bits(np.ones(d, np.float32)).view(np.int16))
+    lens, start, table = dev(np.array([21, 41], np.int32)), dev(np.array([0, 1, 2], np.int32)), dev(np.arange(6, dtype=np.int32).reshape(2, 3))
+    nbytes = q4k.q4k_paged_attention_workspace_size(2, 2, hq, hk, d)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+
+    def step():
+        q4k.q4k_qk_norm_rope(qkv, None, 2, hq, 0, d, row, row, w, None, EPS, pos, f, d, 0, q, None, hq * d, hq * d)
+        q4k.q4k_kv_append(qkv[:, hq * d:], qkv[:, (hq + hk) * d:], 2, hk, d, row, row, w, EPS, f, d, 0, start, lens,
+                          table, 2, 3, page, 8, c.dev["k"], c.dev["v"], c.dev_scale["k"], c.dev_scale["v"])
+        q4k.q4k_paged_attention(q, 2, hq, hk, d, hq * d, c.dev["k"], c.dev["v"], c.dev_scale["k"], c.dev_scale["v"],
+                                start, lens, table, 2, 3, page, 8, 1, 48, 0.09, 0, out, hq * d, ws, nbytes)
+
+    qkv.normal_()
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (1, 2):
+        torch.manual_seed(seed)
+        qkv.normal_()
+        keep = [t.clone() for t in (*c.dev.values(), *c.dev_scale.values())]
+        graph.replay()
+        got = out.clone()
+        for t, k in zip((*c.dev.values(), *c.dev_scale.values()), keep):
+            t.copy_(k)
+        step()
+        assert torch.equal(got, out)
