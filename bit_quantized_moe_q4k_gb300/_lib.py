@@ -113,7 +113,7 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -131,23 +131,46 @@ def _cuda(*tensors) -> None:
             raise ValueError("device tensor expected")
 
 
-def _dtype(*tensors) -> int:
-    """The library's element type of the tensors given (all of one type)."""
-    import torch
-    kinds = {t.dtype for t in tensors if t is not None}
-    if len(kinds) == 1:
-        kind = kinds.pop()
-        if kind == torch.float32:
-            return F32
-        if kind == torch.bfloat16:
-            return BF16
-    raise ValueError("float32 or bfloat16 tensors of one type expected")
+class _Kinds:
+    """The torch element types behind the attention-side calls' arguments."""
+
+    def __init__(self):
+        import torch
+        self.rows = {torch.float32: F32, torch.bfloat16: BF16}
+        self.bf16 = frozenset((torch.bfloat16, torch.uint16, torch.int16))
+        self.e4m3 = frozenset((torch.float8_e4m3fn, torch.uint8, torch.int8))
+        self.i32, self.f32, self.f64 = (frozenset((t,)) for t in (torch.int32, torch.float32, torch.float64))
+        self.u8 = frozenset((torch.uint8,))
 
 
-def _of_type(name, t, *dtypes):
-    """The kernels read these as raw words: a tensor of another element type is refused here."""
-    if t is not None and not isinstance(t, int) and str(t.dtype).replace("torch.", "") not in dtypes:
-        raise ValueError(f"{name}: {' or '.join(dtypes)} expected, got {t.dtype}")
+_kinds_made = None
+
+
+def _kinds() -> _Kinds:
+    global _kinds_made
+    if _kinds_made is None:
+        _kinds_made = _Kinds()
+    return _kinds_made
+
+
+def _dev(t, kinds) -> int | None:
+    """Address of a device tensor of one of the types given (None and raw addresses pass): the kernels
+    read raw words, so a tensor of another type is refused here."""
+    if t is None or t.__class__ is int:
+        return t
+    if not t.is_cuda:
+        raise ValueError("device tensor expected")
+    if t.dtype not in kinds:
+        raise ValueError(f"element type {' or '.join(str(k) for k in kinds)} expected, got {t.dtype}")
+    return t.data_ptr()
+
+
+def _row_type(kinds, a, b) -> int:
+    """The library's element type of one or two row tensors."""
+    t = a if b is None else b
+    if t is None or t.dtype not in kinds.rows or (a is not None and a.dtype is not t.dtype):
+        raise ValueError("float32 or bfloat16 tensors of one type expected")
+    return kinds.rows[t.dtype]
 
 
 # ---- sizes -------------------------------------------------------------------------------------
@@ -311,46 +334,28 @@ def q4k_moe_layer_down(w_down, num_experts, ws_down, shared_inter, act, act_shar
                                      _ptr(shared_out), _ptr(workspace), ws_bytes, _ptr(err_flag), _stream(stream)))
 
 
-_BF16_BITS = ("bfloat16", "uint16", "int16")
-_E4M3 = ("float8_e4m3fn", "uint8", "int8")
-
-
-def _paged_types(q_start, seq_lens, page_table, k_cache, v_cache, k_scale, v_scale):
-    for name, t in (("q_start", q_start), ("seq_lens", seq_lens), ("page_table", page_table)):
-        _of_type(name, t, "int32")
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _of_type(name, t, *_E4M3)
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _of_type(name, t, "float32")
-
-
 def q4k_qk_norm_rope(q, k, m, q_heads, kv_heads, head_dim, q_stride, k_stride, w_q, w_k, eps, pos, inv_freq, rot_dim,
                      rope_mode, q_out, k_out, q_out_stride, k_out_stride, stream=None):
     """Per-head RMS norm of queries and keys (w_q / w_k bf16 or None) and the position rotation in one pass; strides in
     elements between tokens; q and k, and q_out and k_out, are float32 or bfloat16; a side with 0 heads may be None."""
-    _cuda(q, k, w_q, w_k, pos, inv_freq, q_out, k_out)
-    _of_type("w_q", w_q, *_BF16_BITS)
-    _of_type("w_k", w_k, *_BF16_BITS)
-    _of_type("pos", pos, "int32")
-    _of_type("inv_freq", inv_freq, "float64")
-    _check(load().q4k_qk_norm_rope(_ptr(q), _ptr(k), _dtype(q, k), m, q_heads, kv_heads, head_dim, q_stride, k_stride,
-                                   _ptr(w_q), _ptr(w_k), float(eps), _ptr(pos), _ptr(inv_freq), rot_dim, rope_mode,
-                                   _ptr(q_out), _ptr(k_out), _dtype(q_out, k_out), q_out_stride, k_out_stride,
-                                   _stream(stream)))
+    K = _kinds()
+    _check((_lib or load()).q4k_qk_norm_rope(
+        _dev(q, K.rows), _dev(k, K.rows), _row_type(K, q, k), m, q_heads, kv_heads, head_dim, q_stride, k_stride,
+        _dev(w_q, K.bf16), _dev(w_k, K.bf16), eps, _dev(pos, K.i32), _dev(inv_freq, K.f64), rot_dim, rope_mode,
+        _dev(q_out, K.rows), _dev(k_out, K.rows), _row_type(K, q_out, k_out), q_out_stride, k_out_stride,
+        _stream(stream)))
 
 
 def q4k_kv_append(k, v, m, kv_heads, head_dim, k_stride, v_stride, w_k, eps, inv_freq, rot_dim, rope_mode, q_start,
                   seq_lens, page_table, batch, max_pages, page_size, num_pages, k_cache, v_cache, k_scale, v_scale,
                   err_flag=None, stream=None):
     """The new tokens' keys (normed and rotated on the way) and values into the paged e4m3 cache."""
-    _cuda(k, v, w_k, inv_freq, q_start, seq_lens, page_table, k_cache, v_cache, k_scale, v_scale, err_flag)
-    _of_type("w_k", w_k, *_BF16_BITS)
-    _of_type("inv_freq", inv_freq, "float64")
-    _paged_types(q_start, seq_lens, page_table, k_cache, v_cache, k_scale, v_scale)
-    _check(load().q4k_kv_append(_ptr(k), _ptr(v), _dtype(k, v), m, kv_heads, head_dim, k_stride, v_stride, _ptr(w_k),
-                                float(eps), _ptr(inv_freq), rot_dim, rope_mode, _ptr(q_start), _ptr(seq_lens),
-                                _ptr(page_table), batch, max_pages, page_size, num_pages, _ptr(k_cache), _ptr(v_cache),
-                                _ptr(k_scale), _ptr(v_scale), _ptr(err_flag), _stream(stream)))
+    K = _kinds()
+    _check((_lib or load()).q4k_kv_append(
+        _dev(k, K.rows), _dev(v, K.rows), _row_type(K, k, v), m, kv_heads, head_dim, k_stride, v_stride,
+        _dev(w_k, K.bf16), eps, _dev(inv_freq, K.f64), rot_dim, rope_mode, _dev(q_start, K.i32), _dev(seq_lens, K.i32),
+        _dev(page_table, K.i32), batch, max_pages, page_size, num_pages, _dev(k_cache, K.e4m3), _dev(v_cache, K.e4m3),
+        _dev(k_scale, K.f32), _dev(v_scale, K.f32), _dev(err_flag, K.i32), _stream(stream)))
 
 
 def q4k_paged_attention_workspace_size(batch, m, q_heads, kv_heads, head_dim) -> int:
@@ -361,13 +366,12 @@ def q4k_paged_attention(q, m, q_heads, kv_heads, head_dim, q_stride, k_cache, v_
                         seq_lens, page_table, batch, max_pages, page_size, num_pages, max_q_len, max_len, scale, window,
                         out, out_stride, workspace, ws_bytes, err_flag=None, stream=None):
     """Causal attention of the new tokens over the paged e4m3 cache (window 0: every earlier token)."""
-    _cuda(q, k_cache, v_cache, k_scale, v_scale, q_start, seq_lens, page_table, out, workspace, err_flag)
-    _paged_types(q_start, seq_lens, page_table, k_cache, v_cache, k_scale, v_scale)
-    _check(load().q4k_paged_attention(_ptr(q), _dtype(q, out), m, q_heads, kv_heads, head_dim, q_stride, _ptr(k_cache),
-                                      _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(q_start), _ptr(seq_lens),
-                                      _ptr(page_table), batch, max_pages, page_size, num_pages, max_q_len, max_len,
-                                      float(scale), window, _ptr(out), out_stride, _ptr(workspace), ws_bytes,
-                                      _ptr(err_flag), _stream(stream)))
+    K = _kinds()
+    _check((_lib or load()).q4k_paged_attention(
+        _dev(q, K.rows), _row_type(K, q, out), m, q_heads, kv_heads, head_dim, q_stride, _dev(k_cache, K.e4m3),
+        _dev(v_cache, K.e4m3), _dev(k_scale, K.f32), _dev(v_scale, K.f32), _dev(q_start, K.i32), _dev(seq_lens, K.i32),
+        _dev(page_table, K.i32), batch, max_pages, page_size, num_pages, max_q_len, max_len, scale, window,
+        _dev(out, K.rows), out_stride, _dev(workspace, K.u8), ws_bytes, _dev(err_flag, K.i32), _stream(stream)))
 
 
 def q4k_quantize_rows(x, rows, k, out, stream=None):

@@ -1,12 +1,16 @@
 // q4k_kv.cu -- appending keys and values to the paged 8-bit cache, keys normed and rotated on the way.
 //
 // A work item is one page that receives tokens, one kv head and one side (keys or values), so each
-// scale has one writer. Its CTA holds the page's new rows in registers (one warp per row, head_dim /
-// 32 dims a lane), takes their largest finite magnitude, and writes e4m3 codes under the scale 2^e,
-// the least power of two that maps it into e4m3's range. A page that held tokens already keeps the
-// larger of its scale and the new one; when its scale grows, its codes are read and rounded again
-// under it. The scale being a power of two, that changes a value only where its code becomes
-// subnormal, so what a page holds hardly depends on how many calls filled it.
+// scale has one writer. It holds the page's new rows in registers (head_dim / 8 lanes a row), takes
+// their largest finite magnitude, and writes e4m3 codes under the scale 2^e, the least power of two
+// that maps it into e4m3's range. A page that held tokens already keeps the larger of its scale and
+// the new one; when its scale grows, its codes are read and rounded again under it. The scale
+// being a power of two, that changes a value only where its code becomes subnormal, so what a page
+// holds hardly depends on how many calls filled it.
+//
+// Bound by latency for single tokens (a chain of four dependent reads: lengths, page, scale, row)
+// and by bytes for prompts. Item i < batch is sequence i's first page, so a decode batch finds its
+// work without a search; further pages are found by a scan over the sequences.
 #include "q4k_paged.cuh"
 
 namespace q4k {
@@ -25,22 +29,23 @@ struct AppendParams {
     int* err_flag;
 };
 
-constexpr int kAppendWarps = 8;
+// Pages of sequence i that receive tokens: the first and their number.
+__device__ __forceinline__ int touched_pages(const PagedBatch& B, int i, int* err_flag, SeqSpan* s, int* p0) {
+    bool bad;
+    *s = seq_span(B, i, &bad);
+    if (bad) raise_flag(err_flag, Q4K_ERR_SEQ);
+    const int lo = max(s->len - s->n, 0);
+    *p0 = lo >> B.page_shift;
+    return s->n > 0 && s->len > lo ? ((s->len - 1) >> B.page_shift) - *p0 + 1 : 0;
+}
 
-// Sequence and page of work item w (every warp finds them by itself); false past the last item.
-__device__ __forceinline__ bool append_item(const PagedBatch& B, int w, int* err_flag, int* seq, int* page, SeqSpan* span) {
+// The w-th page beyond the sequences' first ones (every warp finds it by itself); false past the last.
+__device__ __forceinline__ bool further_page(const PagedBatch& B, int w, int* err_flag, int* seq, int* page, SeqSpan* span) {
     const int lane = threadIdx.x & 31;
     for (int base = 0; base < B.batch; base += 32) {
         int cnt = 0, p0 = 0;
         SeqSpan s{0, 0, 0};
-        if (base + lane < B.batch) {
-            bool bad;
-            s = seq_span(B, base + lane, &bad);
-            if (bad) raise_flag(err_flag, Q4K_ERR_SEQ);
-            const int lo = max(s.len - s.n, 0);
-            p0 = lo >> B.page_shift;
-            if (s.n > 0 && s.len > lo) cnt = ((s.len - 1) >> B.page_shift) - p0 + 1;
-        }
+        if (base + lane < B.batch) cnt = max(touched_pages(B, base + lane, err_flag, &s, &p0) - 1, 0);
         int inc = cnt;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -51,7 +56,7 @@ __device__ __forceinline__ bool append_item(const PagedBatch& B, int w, int* err
         if (hit) {
             const int src = __ffs(hit) - 1;
             *seq = base + src;
-            *page = __shfl_sync(0xffffffffu, p0 + w - (inc - cnt), src);
+            *page = __shfl_sync(0xffffffffu, p0 + 1 + w - (inc - cnt), src);
             span->start = __shfl_sync(0xffffffffu, s.start, src);
             span->n = __shfl_sync(0xffffffffu, s.n, src);
             span->len = __shfl_sync(0xffffffffu, s.len, src);
@@ -62,109 +67,179 @@ __device__ __forceinline__ bool append_item(const PagedBatch& B, int w, int* err
     return false;
 }
 
-// Grid (items, kv heads, 2). P: page size.
-template <typename T, int N, int P>
-__global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const __grid_constant__ AppendParams A) {
-    constexpr int D = 32 * N, RPW = P / kAppendWarps;  // rows of the page a warp holds
-    __shared__ float s_max[kAppendWarps];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    int seq, page;
-    SeqSpan s;
-    if (!append_item(A.B, blockIdx.x, A.err_flag, &seq, &page, &s)) return;
+// One (page, head, side) by W warps (W == 1: warps of a CTA work on items of their own). Rows are
+// taken in sets of W * heads-per-warp * HELD; the rows of a single set stay in registers between
+// the two passes (largest magnitude, codes), more sets are read and computed again.
+template <typename T, int D, int P, int W, int HELD>
+__device__ __forceinline__ void append_page(const AppendParams& A, int seq, int page, const SeqSpan& s, int head,
+                                            int heads, bool keys, float* s_max) {
+    using Lane = HeadLane<D>;
+    constexpr int kSet = W * Lane::kHeads * HELD;
     const int pid = page_id(A.B, seq, page, A.err_flag);
     if (pid < 0) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = N * lane;
-    const int head = blockIdx.y, heads = gridDim.y;
-    const bool keys = blockIdx.z == 0;
+    const int lane = threadIdx.x & 31, warp = W == 1 ? 0 : threadIdx.x >> 5, sub = lane / Lane::kLanes;
     const int first = s.len - s.n;                          // position of the first new row
     const int lo = max(max(first, 0) - page * P, 0);        // slots [lo, hi) of the page are new
     const int hi = min(s.len - page * P, P);
-    const T* x = static_cast<const T*>(keys ? A.k : A.v) + head * D + c0;
+    const Lane ln(keys ? A.rot_dim : 0, A.pairs_mode);
+    float* sp = (keys ? A.k_scale : A.v_scale) + (int64_t)pid * heads + head;
+    uint8_t* codes = (keys ? A.k_cache : A.v_cache) + ((int64_t)pid * heads + head) * (P * D);
+    const float old = lo > 0 ? __ldcg(sp) : 0.0f;
     const int64_t stride = keys ? A.k_stride : A.v_stride;
-    float w[N];
-    const bool norm = keys && A.w_k != nullptr;
-    if (norm) Vec<__nv_bfloat16>::load(reinterpret_cast<const __nv_bfloat16*>(A.w_k) + c0, w);
-    float v[RPW][N];
+    const T* x = static_cast<const T*>(keys ? A.k : A.v) + (int64_t)(s.start + page * P - first) * stride + head * D;
+    float w[8];
+    uint64_t F[4];
+    const bool norm = keys && A.w_k != nullptr, rot = keys && A.rot_dim;
+    if (norm) ln.load(reinterpret_cast<const __nv_bfloat16*>(A.w_k), w);
+    if (rot) ln.fractions(A.inv_freq, F);
+    float v[HELD][8];
+    auto take = [&](int set) {
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) {
+            const int slot = set * kSet + (i * W + warp) * Lane::kHeads + sub;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+            if (slot >= lo && slot < hi) ln.load(x + slot * stride, v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) {
+            const int slot = set * kSet + (i * W + warp) * Lane::kHeads;
+            if (slot >= hi || slot + Lane::kHeads <= lo) continue;  // the same in all lanes
+            if (norm) Lane::norm(w, A.eps, v[i]);
+            if (rot) {
+                float sn[4], cs[4];
+                ln.angles(page * P + slot + sub, F, sn, cs);
+                ln.rotate(sn, cs, v[i]);
+            }
+        }
+    };
+    const int set0 = lo / kSet, set1 = (hi - 1) / kSet;
     float amax = 0.0f;
+    for (int set = set0; set <= set1; ++set) {
+        take(set);
 #pragma unroll
-    for (int i = 0; i < RPW; ++i) {
-        const int slot = warp + kAppendWarps * i;
-        if (slot < lo || slot >= hi) continue;
-        const int pos = page * P + slot;
-        Vec<T>::load(x + (int64_t)(s.start + pos - first) * stride, v[i]);
-        if (norm) lane_norm<N>(w, D, A.eps, v[i]);
-        if (keys && A.rot_dim) {
-            float sn[N], cs[N];
-            lane_angles<N>(c0, pos, A.inv_freq, A.rot_dim, A.pairs_mode, sn, cs);
-            lane_rotate<N>(c0, A.rot_dim, A.pairs_mode, sn, cs, v[i]);
-        }
+        for (int i = 0; i < HELD; ++i)
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const float a = fabsf(v[i][j]);
-            if (a <= 3.402823466e38f) amax = fmaxf(amax, a);  // infinities saturate, NaN stays NaN
-        }
+            for (int j = 0; j < 8; ++j) {
+                const float a = fabsf(v[i][j]);
+                if (a <= 3.402823466e38f) amax = fmaxf(amax, a);  // infinities saturate, NaN stays NaN
+            }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (lane == 0) s_max[warp] = amax;
-    __syncthreads();
+    if constexpr (W > 1) {
+        if (lane == 0) s_max[warp] = amax;
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kAppendWarps; ++i) amax = fmaxf(amax, s_max[i]);
-    float* sp = (keys ? A.k_scale : A.v_scale) + (int64_t)pid * heads + head;
-    uint8_t* codes = (keys ? A.k_cache : A.v_cache) + ((int64_t)pid * heads + head) * (P * D) + c0;
-    const float fresh = exp2_int(scale_exponent(amax));
-    const float old = lo > 0 ? __ldcg(sp) : 0.0f;
-    const float scale = fmaxf(fresh, old);
-    __syncthreads();  // every thread has read the old scale
-    if (threadIdx.x == 0) *sp = scale;
+        for (int i = 0; i < W; ++i) amax = fmaxf(amax, s_max[i]);
+    }
+    const float scale = fmaxf(exp2_int(scale_exponent(amax)), old);
+    if (W == 1 ? lane == 0 : threadIdx.x == 0) *sp = scale;  // every thread has read the old one
     const float inv = 1.0f / scale;  // exact: a power of two
+    for (int set = set0; set <= set1; ++set) {
+        if (set0 != set1) take(set);
 #pragma unroll
-    for (int i = 0; i < RPW; ++i) {
-        const int slot = warp + kAppendWarps * i;
-        if (slot < lo || slot >= hi) continue;
-        uint32_t q[N / 2];
+        for (int i = 0; i < HELD; ++i) {
+            const int slot = set * kSet + (i * W + warp) * Lane::kHeads + sub;
+            if (slot < lo || slot >= hi) continue;
+            uint32_t q[4];
 #pragma unroll
-        for (int j = 0; j < N / 2; ++j) q[j] = f32x2_to_e4m3x2(v[i][2 * j] * inv, v[i][2 * j + 1] * inv);
-        if constexpr (N == 4)
-            *reinterpret_cast<uint32_t*>(codes + slot * D) = q[0] | (q[1] << 16);
-        else
-            *reinterpret_cast<uint16_t*>(codes + slot * D) = (uint16_t)q[0];
+            for (int j = 0; j < 4; ++j) q[j] = f32x2_to_e4m3x2(v[i][2 * j] * inv, v[i][2 * j + 1] * inv);
+            *reinterpret_cast<uint32_t*>(codes + slot * D + ln.c0) = q[0] | (q[1] << 16);
+            *reinterpret_cast<uint32_t*>(codes + slot * D + ln.c1) = q[2] | (q[3] << 16);
+        }
     }
     if (lo == 0 || scale == old) return;
     const float ratio = old * inv;
-    for (int slot = warp; slot < lo; slot += kAppendWarps) {
-        uint16_t* p = reinterpret_cast<uint16_t*>(codes + slot * D);
+    for (int i = 16 * (32 * warp + lane); i < lo * D; i += 16 * 32 * W) {  // slots 0 .. lo - 1 lie in a row
+        uint4* p = reinterpret_cast<uint4*>(codes + i);
+        const uint4 c = __ldcg(p);
+        uint32_t r[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-        for (int j = 0; j < N / 2; ++j) {
-            const uint32_t h = e4m3x2_to_f16x2(__ldcg(p + j));
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-            p[j] = (uint16_t)f32x2_to_e4m3x2(f.x * ratio, f.y * ratio);
+        for (int j = 0; j < 4; ++j) {
+            uint32_t o = 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t h = e4m3x2_to_f16x2((r[j] >> (16 * k)) & 0xFFFFu);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                o |= f32x2_to_e4m3x2(f.x * ratio, f.y * ratio) << (16 * k);
+            }
+            r[j] = o;
         }
+        *p = make_uint4(r[0], r[1], r[2], r[3]);
     }
 }
 
-template <typename T, int N, int P>
-cudaError_t launch_page(const AppendParams& A, int items, int kv_heads, cudaStream_t stream) {
+constexpr int kPageWarps = 8, kTokenWarps = 4;
+
+// A CTA per (page, head, side): grid (batch first pages, then CTAs that walk over further pages; heads; 2).
+template <typename T, int D, int P>
+__global__ void __launch_bounds__(32 * kPageWarps) append_pages_kernel(const __grid_constant__ AppendParams A) {
+    constexpr int kRows = kPageWarps * HeadLane<D>::kHeads;
+    __shared__ float s_max[kPageWarps];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    int seq = blockIdx.x, page;
+    SeqSpan s;
+    if (seq < A.B.batch) {
+        if (touched_pages(A.B, seq, A.err_flag, &s, &page) == 0) return;
+        append_page<T, D, P, kPageWarps, (P + kRows - 1) / kRows>(A, seq, page, s, blockIdx.y, gridDim.y, blockIdx.z == 0, s_max);
+        return;
+    }
+    for (int w = blockIdx.x - A.B.batch; further_page(A.B, w, A.err_flag, &seq, &page, &s); w += gridDim.x - A.B.batch) {
+        append_page<T, D, P, kPageWarps, (P + kRows - 1) / kRows>(A, seq, page, s, blockIdx.y, gridDim.y, blockIdx.z == 0, s_max);
+        __syncthreads();  // s_max is free again
+    }
+}
+
+// A warp per (page, head, side): grid (as above; 2 * heads / kTokenWarps).
+template <typename T, int D, int P>
+__global__ void __launch_bounds__(32 * kTokenWarps) append_tokens_kernel(const __grid_constant__ AppendParams A, int heads) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int hs = blockIdx.y * kTokenWarps + (threadIdx.x >> 5);
+    if (hs >= 2 * heads) return;
+    int seq = blockIdx.x, page;
+    SeqSpan s;
+    if (seq < A.B.batch) {
+        if (touched_pages(A.B, seq, A.err_flag, &s, &page) == 0) return;
+        append_page<T, D, P, 1, 2>(A, seq, page, s, hs >> 1, heads, (hs & 1) == 0, nullptr);
+        return;
+    }
+    for (int w = blockIdx.x - A.B.batch; further_page(A.B, w, A.err_flag, &seq, &page, &s); w += gridDim.x - A.B.batch)
+        append_page<T, D, P, 1, 2>(A, seq, page, s, hs >> 1, heads, (hs & 1) == 0, nullptr);
+}
+
+template <typename T, int D, int P>
+cudaError_t launch_page(const AppendParams& A, int kv_heads, cudaStream_t stream) {
+    // CTAs for the pages beyond each sequence's first: as many as the tokens fill; where ragged
+    // sequences touch more, the CTAs walk on.
+    const int items = A.B.batch + ((A.B.m - 1) >> A.B.page_shift) + 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)items, (unsigned)kv_heads, 2);
-    cfg.blockDim = dim3(32 * kAppendWarps);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv_append_kernel<T, N, P>, A);
+    // Mostly single tokens: a warp an item; else the CTA that shares a page's rows.
+    if (A.B.m <= 2 * (int64_t)A.B.batch) {
+        cfg.gridDim = dim3((unsigned)items, (unsigned)((2 * kv_heads + kTokenWarps - 1) / kTokenWarps));
+        cfg.blockDim = dim3(32 * kTokenWarps);
+        return cudaLaunchKernelEx(&cfg, append_tokens_kernel<T, D, P>, A, kv_heads);
+    }
+    cfg.gridDim = dim3((unsigned)items, (unsigned)kv_heads, 2);
+    cfg.blockDim = dim3(32 * kPageWarps);
+    return cudaLaunchKernelEx(&cfg, append_pages_kernel<T, D, P>, A);
 }
 
-template <typename T, int N>
-cudaError_t launch_dim(const AppendParams& A, int items, int kv_heads, cudaStream_t stream) {
+template <typename T, int D>
+cudaError_t launch_dim(const AppendParams& A, int kv_heads, cudaStream_t stream) {
     switch (A.B.page_shift) {
-        case 4: return launch_page<T, N, 16>(A, items, kv_heads, stream);
-        case 5: return launch_page<T, N, 32>(A, items, kv_heads, stream);
-        case 6: return launch_page<T, N, 64>(A, items, kv_heads, stream);
-        default: return launch_page<T, N, 128>(A, items, kv_heads, stream);
+        case 4: return launch_page<T, D, 16>(A, kv_heads, stream);
+        case 5: return launch_page<T, D, 32>(A, kv_heads, stream);
+        case 6: return launch_page<T, D, 64>(A, kv_heads, stream);
+        default: return launch_page<T, D, 128>(A, kv_heads, stream);
     }
 }
 
@@ -178,14 +253,10 @@ cudaError_t launch_kv_append(const PagedBatch& B, const void* k, const void* v, 
     A.B = B; A.k = k; A.v = v; A.k_stride = k_stride; A.v_stride = v_stride; A.w_k = w_k; A.inv_freq = inv_freq;
     A.eps = eps; A.rot_dim = rot_dim; A.pairs_mode = rope_mode == Q4K_ROPE_PAIRS; A.k_cache = k_cache;
     A.v_cache = v_cache; A.k_scale = k_scale; A.v_scale = v_scale; A.err_flag = err_flag;
-    // A sequence of n new tokens touches at most (n - 1) / page + 2 pages, and at most n.
-    const int64_t most = (int64_t)(B.m >> B.page_shift) + 2 * (int64_t)B.batch;
-    const int items = (int)(most < B.m ? most : B.m);
     if (dtype == Q4K_F32)
-        return head_dim == 64 ? launch_dim<float, 2>(A, items, kv_heads, stream)
-                              : launch_dim<float, 4>(A, items, kv_heads, stream);
-    return head_dim == 64 ? launch_dim<__nv_bfloat16, 2>(A, items, kv_heads, stream)
-                          : launch_dim<__nv_bfloat16, 4>(A, items, kv_heads, stream);
+        return head_dim == 64 ? launch_dim<float, 64>(A, kv_heads, stream) : launch_dim<float, 128>(A, kv_heads, stream);
+    return head_dim == 64 ? launch_dim<__nv_bfloat16, 64>(A, kv_heads, stream)
+                          : launch_dim<__nv_bfloat16, 128>(A, kv_heads, stream);
 }
 
 }  // namespace q4k

@@ -115,12 +115,6 @@ template <> struct Vec<__nv_bfloat16> {
     }
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
 // ---- rotation -----------------------------------------------------------------------------------
 // The angle pos * f is needed only modulo one turn. With F = f / 2pi mod 1 as a 64-bit fraction,
 // pos * F mod 2^64 is that fraction of a turn: integer wrap-around is the range reduction, exact
@@ -141,63 +135,71 @@ __device__ __forceinline__ void turn_sincos(int pos, uint64_t F, float* s, float
     sincospif((float)t * 4.656612873077393e-10f, s, c);                    // 2^-31: half turns
 }
 
-// A lane's N consecutive dims (c0 = N * lane) of a head spread over a warp: the sine and cosine
-// that each of them takes. Dims at or past rot_dim get (0, 1).
-template <int N>
-__device__ __forceinline__ void lane_angles(int c0, int pos, const double* inv_freq, int rot_dim, int pairs_mode,
-                                            float (&sn)[N], float (&cs)[N]) {
-    const int half = rot_dim >> 1;
-#pragma unroll
-    for (int i = 0; i < N; ++i) { sn[i] = 0.0f; cs[i] = 1.0f; }
-    if (c0 >= rot_dim) return;
-    if (pairs_mode) {
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            turn_sincos(pos, turn_fraction(inv_freq[(c0 + i) >> 1]), &sn[i], &cs[i]);
-            sn[i + 1] = sn[i];
-            cs[i + 1] = cs[i];
-        }
-    } else {
-        const int j0 = c0 < half ? c0 : c0 - half;
-#pragma unroll
-        for (int i = 0; i < N; ++i) turn_sincos(pos, turn_fraction(inv_freq[j0 + i]), &sn[i], &cs[i]);
-    }
-}
-// Rotate the lane's dims: (a, b) -> (a cos - b sin, b cos + a sin). rot_dim is a multiple of 16
-// (2N <= 16), so the partner dims of a lane are those of one other lane ("halves") or its own.
-template <int N>
-__device__ __forceinline__ void lane_rotate(int c0, int rot_dim, int pairs_mode, const float (&sn)[N],
-                                            const float (&cs)[N], float (&v)[N]) {
-    if (pairs_mode) {
-        if (c0 >= rot_dim) return;
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            const float a = v[i], b = v[i + 1];
-            v[i] = a * cs[i] - b * sn[i];
-            v[i + 1] = b * cs[i] + a * sn[i];
-        }
-    } else {
-        const int half = rot_dim >> 1, lane = threadIdx.x & 31;
-        const bool lo = c0 < half;
-        const int src = c0 < rot_dim ? lane + (lo ? half / N : -(half / N)) : lane;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float o = __shfl_sync(0xffffffffu, v[i], src);
-            if (c0 < rot_dim) v[i] = lo ? v[i] * cs[i] - o * sn[i] : v[i] * cs[i] + o * sn[i];
+// A head spread over D/8 lanes, 8 dims a lane in two runs of 4, so that a lane holds four whole
+// pairs: (v[i], v[4 + i]) with "halves", (v[2i], v[2i + 1]) with "pairs". 32 / (D/8) heads a warp.
+template <int D>
+struct HeadLane {
+    static constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
+    int c0, c1;   // first dim of each run
+    int j0;       // first of the four pairs
+    bool turns, pairs;
+
+    __device__ __forceinline__ HeadLane(int rot_dim, int pairs_mode) {
+        const int q = threadIdx.x & (kLanes - 1);
+        pairs = pairs_mode != 0;
+        j0 = 4 * q;
+        turns = 8 * q < rot_dim;
+        if (!pairs && turns) {
+            c0 = 4 * q;
+            c1 = c0 + (rot_dim >> 1);
+        } else {  // "pairs", and the dims that do not turn (8 q >= rot_dim in either order)
+            c0 = 8 * q;
+            c1 = c0 + 4;
         }
     }
-}
-// The head's norm over a warp: v * w / sqrt(mean v^2 + eps)
-template <int N>
-__device__ __forceinline__ void lane_norm(const float (&w)[N], int dim, float eps, float (&v)[N]) {
-    float ss = 0.0f;
+    template <typename T> __device__ __forceinline__ void load(const T* head, float (&v)[8]) const {
+        float a[4], b[4];
+        Vec<T>::load(head + c0, a);
+        Vec<T>::load(head + c1, b);
 #pragma unroll
-    for (int i = 0; i < N; ++i) ss = fmaf(v[i], v[i], ss);
-    ss = warp_sum(ss);
-    const float r = 1.0f / sqrtf(ss / (float)dim + eps);
+        for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
+    }
+    template <typename T> __device__ __forceinline__ void store(T* head, const float (&v)[8]) const {
+        const float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
+        Vec<T>::store(head + c0, a);
+        Vec<T>::store(head + c1, b);
+    }
+    __device__ __forceinline__ void fractions(const double* inv_freq, uint64_t (&F)[4]) const {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = v[i] * r * w[i];
-}
+        for (int i = 0; i < 4; ++i) F[i] = turns ? turn_fraction(inv_freq[j0 + i]) : 0;
+    }
+    __device__ __forceinline__ void angles(int pos, const uint64_t (&F)[4], float (&sn)[4], float (&cs)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) turn_sincos(pos, F[i], &sn[i], &cs[i]);
+    }
+    // (a, b) -> (a cos - b sin, b cos + a sin)
+    __device__ __forceinline__ void rotate(const float (&sn)[4], const float (&cs)[4], float (&v)[8]) const {
+        if (!turns) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = pairs ? v[2 * i] : v[i], b = pairs ? v[2 * i + 1] : v[4 + i];
+            const float x = a * cs[i] - b * sn[i], y = b * cs[i] + a * sn[i];
+            if (pairs) { v[2 * i] = x; v[2 * i + 1] = y; }
+            else { v[i] = x; v[4 + i] = y; }
+        }
+    }
+    // v * w / sqrt(mean v^2 + eps), the mean over the head's lanes (the whole warp calls it)
+    __device__ __forceinline__ static void norm(const float (&w)[8], float eps, float (&v)[8]) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float r = 1.0f / sqrtf(ss / (float)D + eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = v[i] * r * w[i];
+    }
+};
 
 // ---- e4m3 ---------------------------------------------------------------------------------------
 // Two e4m3 codes (low byte first) to two halves, and back (round to nearest even, saturating).

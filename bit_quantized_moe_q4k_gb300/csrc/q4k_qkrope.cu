@@ -2,8 +2,9 @@
 //
 //   y = x * w / sqrt(mean_c x_c^2 + eps)   (per head; no weight: y = x)
 //   (a, b) -> (a cos - b sin, b cos + a sin) over the first rot_dim dims, angle pos[t] * inv_freq[j]
-// One warp per head and token, head_dim / 32 consecutive dims a lane, everything in fp32 and
-// rounded once at the store.
+// head_dim / 8 lanes hold a head (8 dims each, whole pairs, so the rotation needs no exchange), everything
+// in fp32 and rounded once at the store. A warp computes its token's angles once and walks over heads,
+// two loads ahead: with one head a warp the sines cost more than the bytes.
 #include "q4k_paged.cuh"
 
 namespace q4k {
@@ -22,35 +23,68 @@ struct NormRopeParams {
 
 constexpr int kRopeWarps = 4;
 
-template <typename TI, typename TO, int N>
+template <typename TI, typename TO, int D>
 __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
+    using Lane = HeadLane<D>;
+    constexpr int kAhead = 2;  // steps whose loads are in flight together
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int t = blockIdx.x, lane = threadIdx.x & 31, c0 = N * lane;
-    float sn[N], cs[N];
-    if (P.rot_dim) lane_angles<N>(c0, __ldcg(P.pos + t), P.inv_freq, P.rot_dim, P.pairs_mode, sn, cs);
-    for (int h = blockIdx.y * kRopeWarps + (threadIdx.x >> 5); h < P.heads; h += gridDim.y * kRopeWarps) {
-        const bool is_q = h < P.q_heads;
-        const int hh = is_q ? h : h - P.q_heads;
-        const TI* x = static_cast<const TI*>(is_q ? P.q : P.k) + t * (is_q ? P.q_stride : P.k_stride) + hh * 32 * N + c0;
-        TO* o = static_cast<TO*>(is_q ? P.q_out : P.k_out) + t * (is_q ? P.q_out_stride : P.k_out_stride) + hh * 32 * N + c0;
-        float v[N];
-        Vec<TI>::load(x, v);
-        const uint16_t* wp = is_q ? P.w_q : P.w_k;
-        if (wp) {
-            float w[N];
-            Vec<__nv_bfloat16>::load(reinterpret_cast<const __nv_bfloat16*>(wp) + c0, w);
-            lane_norm<N>(w, 32 * N, P.eps, v);
+    const int t = blockIdx.x, sub = (threadIdx.x & 31) / Lane::kLanes;
+    const Lane ln(P.rot_dim, P.pairs_mode);
+    const int stride = gridDim.y * kRopeWarps * Lane::kHeads;
+    float sn[4], cs[4], wq[8], wk[8];
+    if (P.rot_dim) {
+        uint64_t F[4];
+        ln.fractions(P.inv_freq, F);
+        ln.angles(__ldcg(P.pos + t), F, sn, cs);
+    }
+    // a side without weights multiplies by nothing: its norm is computed (the warp's lanes stay together) and dropped
+#pragma unroll
+    for (int i = 0; i < 8; ++i) wq[i] = wk[i] = 1.0f;
+    if (P.w_q) ln.load(reinterpret_cast<const __nv_bfloat16*>(P.w_q), wq);
+    if (P.w_k) ln.load(reinterpret_cast<const __nv_bfloat16*>(P.w_k), wk);
+    const TI* q = static_cast<const TI*>(P.q) + t * P.q_stride;
+    const TI* k = static_cast<const TI*>(P.k) + t * P.k_stride;
+    TO* qo = static_cast<TO*>(P.q_out) + t * P.q_out_stride;
+    TO* ko = static_cast<TO*>(P.k_out) + t * P.k_out_stride;
+    // h0 is the same in all lanes of a warp; a lane's head is h0 + its group
+    for (int h0 = (blockIdx.y * kRopeWarps + (threadIdx.x >> 5)) * Lane::kHeads; h0 < P.heads; h0 += kAhead * stride) {
+        float v[kAhead][8] = {};
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            const int h = h0 + a * stride + sub;
+            if (h < P.q_heads) ln.load(q + h * D, v[a]);
+            else if (h < P.heads) ln.load(k + (h - P.q_heads) * D, v[a]);
         }
-        if (P.rot_dim) lane_rotate<N>(c0, P.rot_dim, P.pairs_mode, sn, cs, v);
-        Vec<TO>::store(o, v);
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            const int h = h0 + a * stride + sub;
+            const bool is_q = h < P.q_heads;
+            float w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = is_q ? wq[i] : wk[i];
+            const float s[8] = {v[a][0], v[a][1], v[a][2], v[a][3], v[a][4], v[a][5], v[a][6], v[a][7]};
+            Lane::norm(w, P.eps, v[a]);
+            if (!(is_q ? P.w_q : P.w_k)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[a][i] = s[i];
+            }
+            ln.rotate(sn, cs, v[a]);
+            if (is_q) ln.store(qo + h * D, v[a]);
+            else if (h < P.heads) ln.store(ko + (h - P.q_heads) * D, v[a]);
+        }
     }
 }
 
-template <typename TI, typename TO>
-cudaError_t launch_typed(const NormRopeParams& P, int head_dim, cudaStream_t stream) {
+template <typename TI, typename TO, int D>
+cudaError_t launch_dim(const NormRopeParams& P, cudaStream_t stream) {
+    // One token's heads over as many CTAs as bring about four warps to each scheduler: a single
+    // token wants every head at once, a prompt the angles computed once.
+    const int steps = (P.heads + HeadLane<D>::kHeads - 1) / HeadLane<D>::kHeads;
+    const int most = (steps + kRopeWarps - 1) / kRopeWarps;
+    const int want = (16 * num_sms() + kRopeWarps * P.m - 1) / (kRopeWarps * P.m);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)P.m, (unsigned)((P.heads + kRopeWarps - 1) / kRopeWarps));
+    cfg.gridDim = dim3((unsigned)P.m, (unsigned)(want < most ? want : most));
     cfg.blockDim = dim3(32 * kRopeWarps);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -58,9 +92,14 @@ cudaError_t launch_typed(const NormRopeParams& P, int head_dim, cudaStream_t str
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (head_dim == 64) return cudaLaunchKernelEx(&cfg, norm_rope_kernel<TI, TO, 2>, P);
-    if (head_dim == 128) return cudaLaunchKernelEx(&cfg, norm_rope_kernel<TI, TO, 4>, P);
-    return cudaLaunchKernelEx(&cfg, norm_rope_kernel<TI, TO, 8>, P);
+    return cudaLaunchKernelEx(&cfg, norm_rope_kernel<TI, TO, D>, P);
+}
+
+template <typename TI, typename TO>
+cudaError_t launch_typed(const NormRopeParams& P, int head_dim, cudaStream_t stream) {
+    if (head_dim == 64) return launch_dim<TI, TO, 64>(P, stream);
+    if (head_dim == 128) return launch_dim<TI, TO, 128>(P, stream);
+    return launch_dim<TI, TO, 256>(P, stream);
 }
 
 }  // namespace
