@@ -890,7 +890,7 @@ int q4k_paged_attention(const void* d_q, int dtype, int m, int q_heads, int kv_h
     if (st) return st;
     return cuda_status(launch_attention(B, d_q, dtype, q_stride, q_heads, kv_heads, head_dim,
                                         static_cast<const uint8_t*>(d_k_cache), static_cast<const uint8_t*>(d_v_cache),
-                                        d_k_scale, d_v_scale, max_len, scale, window, d_out, out_stride, d_workspace,
+                                        d_k_scale, d_v_scale, max_q_len, max_len, scale, window, d_out, out_stride, d_workspace,
                                         d_err_flag, stream),
                        "attention launch");
 }

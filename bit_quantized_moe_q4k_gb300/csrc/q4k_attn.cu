@@ -10,10 +10,13 @@
 // lo in rows 8-15, scaled by a power of two so that 22 bits survive) and so are their P; bf16
 // queries are exact in one half and P is rounded to fp16 (2^-12), so 16 rows fill the tile.
 //
-// Bound by the cache's bytes. Each warp reads 16 tokens of a page at a time straight into the
-// fragments (16-byte loads, whole 128-byte lines) while the previous 16 are multiplied; nothing goes
-// through shared memory. The work (sequence, kv head, row tile, 64 tokens) is laid out on one line and cut
-// into equal pieces, one per CTA, whatever the lengths; a second kernel joins the pieces of a tile.
+// Bound by the cache's bytes. Each warp owns a ring of stages in shared memory, a stage being two chunks
+// of 16 tokens (2 KB of K and 2 KB of V each at head_dim 128), which its lanes fill by 16-byte
+// asynchronous copies one stage ahead. (Bulk copies of these pieces, 5 a chunk, held the rate to 2.3
+// TB/s: the copy engine takes about 50 ns for one, whatever its size.) The copies place 16-byte units so
+// that the fragment reads meet different banks. The work
+// (sequence, kv head, row tile, 64 tokens) is laid out on one line and cut into equal pieces, one per
+// CTA, whatever the lengths; a second kernel joins the pieces of a tile.
 #include "q4k_paged.cuh"
 
 namespace q4k {
@@ -21,7 +24,8 @@ namespace {
 
 constexpr int kAttnWarps = 4;
 constexpr int kChunk = 16;                    // tokens a warp takes at a time
-constexpr int kUnit = kChunk * kAttnWarps;    // tokens of one piece of work
+constexpr int kUnit = kChunk * kAttnWarps;    // tokens of one unit of work
+constexpr int kTileCost = 4;                  // units that starting and ending a tile are worth
 constexpr int kCtasPerSm = 3;
 constexpr int kMaxParts = 512;                // CTAs that the workspace serves
 
@@ -53,6 +57,22 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_16816_zero(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+// Two fp32 additions or products in one instruction, each rounded to nearest.
+__device__ __forceinline__ void add2(float2& a, float x, float y) {
+    float2 b = make_float2(x, y);
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(reinterpret_cast<uint64_t&>(a)) : "l"(reinterpret_cast<uint64_t&>(b)));
+}
+__device__ __forceinline__ void mul2(float2& a, float x) {
+    float2 b = make_float2(x, x);
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(reinterpret_cast<uint64_t&>(a)) : "l"(reinterpret_cast<uint64_t&>(b)));
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -61,8 +81,9 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // 0x80 in each byte that is one of e4m3's two NaN codes (0x7F, 0xFF).
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t x) { return ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
-// The work of one sequence: `tiles` row tiles per kv head, `units` pieces of kUnit tokens each,
-// from token `lo` (a multiple of kChunk: the first one any of its rows sees).
+// The work of one sequence: `tiles` row tiles per kv head, each kTileCost units of nothing (so that a
+// piece of many short tiles is not longer than one of a few long ones) and `units` units of kUnit
+// tokens, from token `lo` (a multiple of kChunk: the first one any of its rows sees).
 struct SeqWork {
     SeqSpan s;
     int lo, tiles, units;
@@ -80,7 +101,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& A, int i) {
     w.lo = A.window > 0 ? (max(first - A.window + 1, 0) & ~(kChunk - 1)) : 0;
     w.tiles = (w.s.n * A.group + RT - 1) / RT;
     w.units = max((w.s.len - w.lo + kUnit - 1) / kUnit, 1);  // an empty sequence: its rows are zeroed
-    w.total = (int64_t)w.tiles * A.kv_heads * w.units;
+    w.total = (int64_t)w.tiles * A.kv_heads * (kTileCost + w.units);
     return w;
 }
 
@@ -91,19 +112,25 @@ struct Cursor {
     int64_t begin;
     SeqWork w;
 };
-// Move the cursor to the sequence that holds u (u >= c.begin; false past the end).
+__device__ __forceinline__ int64_t warp_scan(int64_t v) {  // inclusive
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+    }
+    return v;
+}
+// Move the cursor to the sequence that holds u (u >= c.begin; false past the end). `mine`: the work
+// of sequence `lane`, read once (it is all there is up to 32 sequences).
 template <int RT>
-__device__ __forceinline__ bool seek(const AttnParams& A, int64_t u, Cursor* c) {
+__device__ __forceinline__ bool seek(const AttnParams& A, int64_t u, const SeqWork& mine, Cursor* c) {
     const int lane = threadIdx.x & 31;
     int64_t acc = c->begin;
-    for (int base = c->seq; base < A.B.batch; base += 32) {
-        const SeqWork w = seq_work<RT>(A, base + lane);
-        int64_t inc = w.total;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += x;
-        }
+    for (int base = c->seq & ~31; base < A.B.batch; base += 32) {
+        SeqWork w = base == 0 ? mine : seq_work<RT>(A, base + lane);
+        if (base + lane < c->seq) w.total = 0;
+        const int64_t inc = warp_scan(w.total);
         const unsigned hit = __ballot_sync(0xffffffffu, u < acc + inc);
         if (hit) {
             const int src = __ffs(hit) - 1;
@@ -123,70 +150,58 @@ __device__ __forceinline__ bool seek(const AttnParams& A, int64_t u, Cursor* c) 
     return false;
 }
 template <int RT>
-__device__ __forceinline__ int64_t total_work(const AttnParams& A) {
-    int64_t t = 0;
-    for (int i = threadIdx.x & 31; i < A.B.batch; i += 32) t += seq_work<RT>(A, i).total;
+__device__ __forceinline__ int64_t total_work(const AttnParams& A, const SeqWork& mine) {
+    int64_t t = mine.total;
+    for (int i = 32 + (threadIdx.x & 31); i < A.B.batch; i += 32) t += seq_work<RT>(A, i).total;
 #pragma unroll
     for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     return t;
 }
+// 64-bit values that mostly fit 32: the short division where they do.
+__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 // First unit of piece c when `total` units are cut into `pieces`.
 __device__ __forceinline__ int64_t piece_begin(int64_t total, int pieces, int c) {
-    return total / pieces * c + min((int64_t)c, total % pieces);
+    const int64_t q = div_pos(total, pieces);
+    return q * c + min((int64_t)c, total - q * pieces);
 }
 __device__ __forceinline__ int piece_of(int64_t total, int pieces, int64_t u) {
-    const int64_t q = total / pieces, r = total % pieces;
-    return (int)(u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q);
+    const int64_t q = div_pos(total, pieces), r = total - q * pieces;
+    return (int)(u < r * (q + 1) ? div_pos(u, q + 1) : r + div_pos(u - r * (q + 1), q));
 }
 
-// What a warp loads for 16 tokens: K words of its token rows, V words, and the page's scales.
-template <int D>
-struct Frag {
-    uint4 k[2][D / 64];
-    uint32_t v[4][D / 32];
-    float ks, vs;
-    bool ok;
+// The ring of a warp: kRing stages of kPair chunks, and each chunk's page: K's scale, V's scale as
+// log2 and reciprocal, whether there is such a page.
+constexpr int kRing = 2, kPair = 2;
+template <int D> constexpr int kSlot = 2 * kChunk * D;        // a chunk: K's rows, then V's
+template <int D> constexpr int kStage = kPair * kSlot<D>;
+
+// Where 16-byte unit `u` of row `r` lies in a chunk's K or V part, as 128-byte lines of 8 units: the
+// unit's place in its line is xored with the row's parity times 4 (K at head_dim 128: a read
+// meets rows of both parities) or with twice the row's group of four (V: a read meets all four groups).
+template <int D> __device__ __forceinline__ int k_unit(int r, int u) {
+    return 16 * (D == 128 ? 8 * r + (u ^ ((r & 1) << 2)) : 4 * r + u);
+}
+template <int D> __device__ __forceinline__ int v_unit(int r, int u) {
+    const int x = D / 16 * r + u;
+    return 16 * (x ^ ((r >> 2) << 1));
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+struct ChunkMeta {
+    float ks, ev, inv;
+    int ok;
 };
 
-template <int D>
-__device__ __forceinline__ void load_frag(const AttnParams& A, int seq, int head, int base, int len, Frag<D>& f) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    f.ok = false;
-    f.ks = f.vs = 1.0f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) f.k[i][h] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) f.v[i][j] = 0;
-    if (base >= len) return;
-    const int pid = page_id(A.B, seq, base >> A.B.page_shift, A.err_flag);
-    if (pid < 0) return;
-    f.ok = true;
-    const int64_t ph = (int64_t)pid * A.kv_heads + head;
-    f.ks = __ldcg(A.k_scale + ph);
-    f.vs = __ldcg(A.v_scale + ph);
-    const int slot = base & ((1 << A.B.page_shift) - 1);
-    const int64_t at = ((ph << A.B.page_shift) + slot) * D;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h)
-            f.k[i][h] = __ldcg(reinterpret_cast<const uint4*>(A.k_cache + at + (8 * i + g) * D + 64 * h + 16 * t));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint8_t* p = A.v_cache + at + (2 * t + (i & 1) + 8 * (i >> 1)) * D + D / 8 * g;
-        if constexpr (D == 128) {
-            const uint4 x = __ldcg(reinterpret_cast<const uint4*>(p));
-            f.v[i][0] = x.x; f.v[i][1] = x.y; f.v[i][2] = x.z; f.v[i][3] = x.w;
-        } else {
-            const uint2 x = __ldcg(reinterpret_cast<const uint2*>(p));
-            f.v[i][0] = x.x; f.v[i][1] = x.y;
-        }
-    }
-}
+// The pages of a warp's chunks, 32 at a time: lane i holds those of chunks i, 32 + i, ... Page ids are
+// read two batches ahead and scales one, so that no issue waits for them.
+struct PageAhead {
+    int p0, p1, p2;
+    float ks0, vs0, ks1, vs1;
+};
 
 // log2 of a page's V scale: exact for the powers of two that the append writes.
 __device__ __forceinline__ float scale_log2_of(float s) {
@@ -195,45 +210,125 @@ __device__ __forceinline__ float scale_log2_of(float s) {
     return (b & 0x7FFFFFu) ? e + log2f(__uint_as_float((b & 0x7FFFFFu) | 0x3F800000u)) : e;
 }
 
-template <typename T, int D>
+// RT: query rows of a tile. fp32: 8 (two fp16 terms fill the 16 rows); bf16: 8 where a tile has no
+// more rows, else 16.
+template <typename T, int D, int RT>
 __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const __grid_constant__ AttnParams A) {
     constexpr bool HL = sizeof(T) == 4;           // two fp16 terms
-    constexpr int RT = HL ? 8 : 16;               // query rows of a tile
-    constexpr int NR = HL ? 1 : 2;                // rows of a thread: g, and g + 8
+    constexpr int NR = RT / 8;                    // rows of a thread: g, and g + 8
+    static_assert(RT == 8 || (RT == 16 && !HL), "rows");
     constexpr int NT = D / 8;                     // output column tiles
-    extern __shared__ __align__(16) float s_mem[];
-    float* s_o = s_mem;                           // [warps][RT][D]
-    float* s_m = s_o + kAttnWarps * RT * D;       // [warps][RT]
-    float* s_l = s_m + kAttnWarps * RT;
+    extern __shared__ __align__(128) uint8_t s_mem[];
+    float* s_o = reinterpret_cast<float*>(s_mem); // [warps][RT][D], over the rings once they are read
+    __shared__ float s_m[kAttnWarps * RT], s_l[kAttnWarps * RT];
+    __shared__ ChunkMeta s_meta[kAttnWarps][kRing * kPair];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int64_t total = total_work<RT>(A);
-    const int pieces = (int)min((int64_t)min((int)gridDim.x, A.parts), total);
-    if ((int)blockIdx.x >= pieces) return;
-    const int64_t u0 = piece_begin(total, pieces, blockIdx.x), u1 = piece_begin(total, pieces, blockIdx.x + 1);
-    Cursor cur{};
-    for (int64_t u = u0; u < u1;) {
-        if (!seek<RT>(A, u, &cur)) return;
-        const SeqWork w = cur.w;
-        const int seg = (int)((u - cur.begin) / w.units);      // (row tile, kv head) of the sequence
-        const int ua = (int)((u - cur.begin) % w.units);
-        const int ub = (int)min((int64_t)w.units, ua + (u1 - u));
-        const int tile = seg / A.kv_heads, head = seg % A.kv_heads;
-        const int rows = w.s.n * A.group, first = w.s.len - w.s.n;
+    // The first warp finds the CTA's piece and its segments; what the main loop does not need stays in
+    // shared memory.
+    __shared__ SeqWork s_work[32];
+    __shared__ uint4 s_q[D / 16][32];  // the tile's query fragments, a 16-dim step of a lane each
+    __shared__ Cursor s_cur;
+    __shared__ int64_t s_u[2];
+    if (warp == 0) {
+        const SeqWork mine = seq_work<RT>(A, lane);
+        s_work[lane] = mine;
+        const int64_t total = total_work<RT>(A, mine);
+        const int pieces = (int)min((int64_t)min((int)gridDim.x, A.parts), total);
+        const bool any = (int)blockIdx.x < pieces;
+        const int64_t u0 = any ? piece_begin(total, pieces, blockIdx.x) : 0;
+        const int64_t u1 = any ? piece_begin(total, pieces, blockIdx.x + 1) : 0;
+        Cursor c{};
+        if (any) seek<RT>(A, u0, mine, &c);
+        if (lane == 0) {
+            s_cur = c;
+            s_u[0] = u0;
+            s_u[1] = u1;
+        }
+    }
+    __syncthreads();
+    uint8_t* ring = s_mem + warp * (kRing * kStage<D>);
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+    bool not_first = false;
+    while (s_u[0] < s_u[1]) {
+        const SeqSpan sp = s_cur.w.s;
+        const int w_lo = s_cur.w.lo, seq = s_cur.seq;
+        int tile, head, ua, ub, step;
+        {
+            const int64_t at = s_u[0] - s_cur.begin;
+            const int length = kTileCost + s_cur.w.units;
+            const int seg = (int)div_pos(at, length);  // (row tile, kv head) of the sequence
+            const int va = (int)(at - (int64_t)seg * length);
+            const int vb = (int)min((int64_t)length, va + (s_u[1] - s_u[0]));
+            step = vb - va;
+            ua = max(va - kTileCost, 0);
+            ub = vb - kTileCost;  // <= 0: the piece ends before the tile's first unit
+            tile = seg / A.kv_heads;
+            head = seg - tile * A.kv_heads;
+        }
+        if (ub <= 0) break;
+        const int rows = sp.n * A.group, first = sp.len - sp.n;
+
+        // positions: some row of the tile sees tokens below tile_hi, all see those in [full_lo, full_hi)
+        const int pf = first + tile * RT / A.group, pl = first + (min(rows, tile * RT + RT) - 1) / A.group;
+        const int tile_hi = max(pl + 1, 0), full_hi = max(pf + 1, 0);
+        const int full_lo = A.window > 0 ? max(pl - A.window + 1, 0) : 0;
+
+        // this warp's chunks: base0 + kUnit i, i < n
+        const int c_end = min(w_lo + ub * kUnit, tile_hi);
+        const int base0 = w_lo + ua * kUnit + warp * kChunk;
+        const int n = base0 < c_end ? (c_end - base0 + kUnit - 1) / kUnit : 0;
+        auto page_of = [&](int i) {
+            return i < n ? page_id(A.B, seq, (base0 + kUnit * i) >> A.B.page_shift, A.err_flag) : -1;
+        };
+        auto scales_of = [&](int pid, float& ks, float& vs) {
+            ks = vs = 1.0f;
+            if (pid >= 0) {
+                ks = __ldcg(A.k_scale + (int64_t)pid * A.kv_heads + head);
+                vs = __ldcg(A.v_scale + (int64_t)pid * A.kv_heads + head);
+            }
+        };
+        PageAhead ah{page_of(lane), page_of(32 + lane), page_of(64 + lane), 1.f, 1.f, 1.f, 1.f};
+        scales_of(ah.p0, ah.ks0, ah.vs0);
+        scales_of(ah.p1, ah.ks1, ah.vs1);
+        const int n_st = (n + kPair - 1) / kPair;
+        auto issue = [&](int k) {  // the copies of stage k (a group of its own, empty past the last stage)
+#pragma unroll
+            for (int c = 0; c < kPair; ++c) {
+                const int i = kPair * k + c;
+                if (i > 0 && (i & 31) == 0) {
+                    ah.p0 = ah.p1; ah.ks0 = ah.ks1; ah.vs0 = ah.vs1;
+                    ah.p1 = ah.p2;
+                    scales_of(ah.p1, ah.ks1, ah.vs1);
+                    ah.p2 = page_of(i + 64 + lane);
+                }
+                const int pid = __shfl_sync(0xffffffffu, ah.p0, i & 31);  // -1 past the last chunk
+                if (pid < 0) continue;
+                const int slot = (base0 + kUnit * i) & ((1 << A.B.page_shift) - 1);
+                const int64_t at = ((((int64_t)pid * A.kv_heads + head) << A.B.page_shift) + slot) * D + 16 * lane;
+                const uint32_t dst = ring_at + k % kRing * kStage<D> + c * kSlot<D>;
+                constexpr int kUnits = D / 16, kRows = 32 / kUnits;  // a row's units; rows of one copy instruction
+#pragma unroll
+                for (int j = 0; j < kChunk / kRows; ++j) {
+                    const int r = kRows * j + lane / kUnits, u = lane % kUnits;
+                    copy16(dst + k_unit<D>(r, u), A.k_cache + at + 512 * j);
+                    copy16(dst + kChunk * D + v_unit<D>(r, u), A.v_cache + at + 512 * j);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        auto note = [&](int k) {  // their scales, after the copies are on their way
+            const int c = (lane - kPair * k) & 31;
+            if (c < kPair)
+                s_meta[warp][k % kRing * kPair + c] = ChunkMeta{ah.ks0, scale_log2_of(ah.vs0), 1.0f / ah.vs0, ah.p0 >= 0};
+        };
+        for (int k = 0; k < kRing; ++k) issue(k);
+        for (int k = 0; k < kRing; ++k) note(k);
 
         // the thread's rows: position limits and query fragments
         int hi[NR], lo[NR];
         float crow[NR];
-        uint32_t qa[D / 16][4];
-        int tile_hi = 0, full_lo = 0, full_hi = 0x7FFFFFFF;
-        {
-            const int r0 = tile * RT, r1 = min(rows, r0 + RT) - 1;
-            const int pf = first + r0 / A.group, pl = first + r1 / A.group;
-            tile_hi = max(pl + 1, 0);
-            full_hi = max(pf + 1, 0);
-            full_lo = A.window > 0 ? max(pl - A.window + 1, 0) : 0;
-        }
 #pragma unroll
         for (int j = 0; j < NR; ++j) {
             const int r = tile * RT + g + 8 * j;
@@ -244,7 +339,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
             lo[j] = A.window > 0 ? max(pos - A.window + 1, 0) : 0;
             float x[D / 64][16];
             float amax = 0.0f;
-            const T* p = static_cast<const T*>(A.q) + (int64_t)(w.s.start + tok) * A.q_stride +
+            const T* p = static_cast<const T*>(A.q) + (int64_t)(sp.start + tok) * A.q_stride +
                          (int64_t)(head * A.group + (valid ? r % A.group : 0)) * D + 16 * t;
 #pragma unroll
             for (int h = 0; h < D / 64; ++h) {
@@ -262,178 +357,255 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
             const int e = amax > 0.0f ? min(max(134 - (int)(__float_as_uint(amax) >> 23), -120), 120) : 0;
             const float up = exp2_int(e);
             crow[j] = A.scale_log2 * exp2_int(-e);
+            // the warps share the packing: a fourth of the steps each
 #pragma unroll
             for (int h = 0; h < D / 64; ++h)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
+                    if (i != warp) continue;
                     const float a0 = x[h][4 * i] * up, a1 = x[h][4 * i + 1] * up;
                     const float a2 = x[h][4 * i + 2] * up, a3 = x[h][4 * i + 3] * up;
-                    uint32_t (&f)[4] = qa[4 * h + i];
+                    uint4 f;
                     if constexpr (HL) {
                         const __half2 h01 = __floats2half2_rn(a0, a1), h23 = __floats2half2_rn(a2, a3);
                         const float2 b01 = __half22float2(h01), b23 = __half22float2(h23);
-                        f[0] = *reinterpret_cast<const uint32_t*>(&h01);
-                        f[2] = *reinterpret_cast<const uint32_t*>(&h23);
-                        f[1] = pack_f16(a0 - b01.x, a1 - b01.y);
-                        f[3] = pack_f16(a2 - b23.x, a3 - b23.y);
+                        f.x = *reinterpret_cast<const uint32_t*>(&h01);
+                        f.z = *reinterpret_cast<const uint32_t*>(&h23);
+                        f.y = pack_f16(a0 - b01.x, a1 - b01.y);
+                        f.w = pack_f16(a2 - b23.x, a3 - b23.y);
+                        s_q[4 * h + i][lane] = f;
+                    } else if (RT == 8) {  // rows 8-15 of the products are not used
+                        s_q[4 * h + i][lane] = make_uint4(pack_f16(a0, a1), 0, pack_f16(a2, a3), 0);
+                    } else if (j == 0) {
+                        s_q[4 * h + i][lane].x = pack_f16(a0, a1);
+                        s_q[4 * h + i][lane].z = pack_f16(a2, a3);
                     } else {
-                        f[j] = pack_f16(a0, a1);
-                        f[2 + j] = pack_f16(a2, a3);
+                        s_q[4 * h + i][lane].y = pack_f16(a0, a1);
+                        s_q[4 * h + i][lane].w = pack_f16(a2, a3);
                     }
                 }
         }
+        static_assert(kAttnWarps == 4, "a step of each 64 dims a warp");
+        __syncthreads();
 
-        float o[NT][HL ? 2 : 4];
+        float2 o[NT][NR];
         float mx[NR], l[NR];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < (HL ? 2 : 4); ++i) o[n][i] = 0.0f;
+            for (int j = 0; j < NR; ++j) o[n][j] = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int j = 0; j < NR; ++j) { mx[j] = -INFINITY; l[j] = 0.0f; }
 
-        const int c_end = min(w.lo + ub * kUnit, tile_hi);
-        int base = w.lo + ua * kUnit + warp * kChunk;
-        Frag<D> f;
-        load_frag<D>(A, cur.seq, head, base, c_end, f);
-        for (; base < c_end; base += kUnit) {
-            Frag<D> nx;
-            load_frag<D>(A, cur.seq, head, base + kUnit, c_end, nx);
-            // scores: two tiles of 8 tokens
-            float s[2][4] = {};
+        // a stage at a time: one maximum, one correction and one flush of the sums for its chunks
+        constexpr int S = kPair;
+        for (int k_st = 0; k_st < n_st; ++k_st) {
+            const int stage = k_st % kRing, i = S * k_st;
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+            __syncwarp();
+            // Tokens: lane t's of a chunk are 4 t + {0, 1, 2, 3}, columns 2 t, 2 t + 1 of score tiles 0 and 1, so
+            // column c of tile j is token 4 (c / 2) + 2 j + c % 2.
+            float x[S][NR][4];
+            float inv[S];
+            bool full[S], held[S];
+            float s[S][2][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int h = 0; h < D / 64; ++h) {
+                uint4 kf[S][2];
 #pragma unroll
-                for (int h = 0; h < D / 64; ++h) {
-                    const uint32_t kw[4] = {f.k[i][h].x, f.k[i][h].y, f.k[i][h].z, f.k[i][h].w};
+                for (int c = 0; c < S; ++c)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        mma_16816(s[i], qa[4 * h + q], e4m3x2_to_f16x2(kw[q] & 0xFFFFu), e4m3x2_to_f16x2(kw[q] >> 16));
+                    for (int j = 0; j < 2; ++j)
+                        kf[c][j] = *reinterpret_cast<const uint4*>(ring + stage * kStage<D> + c * kSlot<D> +
+                                                                   k_unit<D>(4 * (g >> 1) + (g & 1) + 2 * j, 4 * h + t));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint4 qf = s_q[4 * h + q][lane];
+                    const uint32_t qa[4] = {qf.x, qf.y, qf.z, qf.w};
+#pragma unroll
+                    for (int c = 0; c < S; ++c)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t kw[4] = {kf[c][j].x, kf[c][j].y, kf[c][j].z, kf[c][j].w};
+                            uint32_t b0, b1;
+                            e4m3x4_to_f16x4(kw[q], &b0, &b1);
+                            if (h == 0 && q == 0) mma_16816_zero(s[c][j], qa, b0, b1);
+                            else mma_16816(s[c][j], qa, b0, b1);
+                        }
                 }
-            // x = c * s + e, masked: this lane's tokens base + 8 i + 2 t + {0, 1}
-            const float ev = scale_log2_of(f.vs), inv = 1.0f / f.vs;
-            const bool full = f.ok && base >= full_lo && base + kChunk <= full_hi;
-            float x[NR][4];
+            }
+#pragma unroll
+            for (int c = 0; c < S; ++c) {
+                const int base = base0 + kUnit * (i + c);
+                const ChunkMeta meta = s_meta[warp][stage * S + c];
+                // x = c * s + e, masked
+                inv[c] = meta.inv;
+                held[c] = meta.ok;
+                full[c] = meta.ok && base >= full_lo && base + kChunk <= full_hi;
+#pragma unroll
+                for (int j = 0; j < NR; ++j) {
+                    const float cr = crow[j] * meta.ks;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float sv = HL ? s[c][k >> 1][k & 1] + s[c][k >> 1][2 + (k & 1)] : s[c][k >> 1][2 * j + (k & 1)];
+                        x[c][j][k] = fmaf(sv, cr, meta.ev);
+                    }
+                }
+                if (!full[c]) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int tok = base + 4 * t + k;
+#pragma unroll
+                        for (int j = 0; j < NR; ++j)
+                            if (!meta.ok || tok < lo[j] || tok >= hi[j]) x[c][j][k] = -INFINITY;
+                    }
+                }
+            }
+            uint32_t pa[S][4];
+            bool grew = false;
+            float corr[NR];
 #pragma unroll
             for (int j = 0; j < NR; ++j) {
-                const float c = crow[j] * f.ks;
-                float top = -INFINITY;
+                float top = x[0][j][0];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float sv = HL ? s[i >> 1][i & 1] + s[i >> 1][2 + (i & 1)] : s[i >> 1][2 * j + (i & 1)];
-                    x[j][i] = fmaf(sv, c, ev);
-                    if (!full) {
-                        const int tok = base + 8 * (i >> 1) + 2 * t + (i & 1);
-                        if (!f.ok || tok < lo[j] || tok >= hi[j]) x[j][i] = -INFINITY;
-                    }
-                    top = fmaxf(top, x[j][i]);
-                }
+                for (int c = 0; c < S; ++c)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) top = fmaxf(top, x[c][j][k]);
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 const float m_new = fmaxf(mx[j], top);
+                grew = grew || m_new > mx[j];
                 const float m_use = m_new == -INFINITY ? 0.0f : m_new;
-                const float corr = ex2(mx[j] - m_use);
+                corr[j] = ex2(mx[j] - m_use);
                 mx[j] = m_new;
-                float sum = 0.0f;
+                l[j] *= corr[j];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[j][i] = ex2(x[j][i] - m_use + 7.0f);  // P * 2^7: fp16 keeps more of the small ones
-                    sum += x[j][i];
-                }
-                l[j] = fmaf(l[j], corr, sum * inv);
+                for (int c = 0; c < S; ++c) {
+                    float sum = 0.0f;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    o[n][HL ? 0 : 2 * j] *= corr;
-                    o[n][HL ? 1 : 2 * j + 1] *= corr;
-                }
-            }
-            uint32_t pa[4];
-            if constexpr (HL) {
-                const __half2 h0 = __floats2half2_rn(x[0][0], x[0][1]), h1 = __floats2half2_rn(x[0][2], x[0][3]);
-                const float2 b0 = __half22float2(h0), b1 = __half22float2(h1);
-                pa[0] = *reinterpret_cast<const uint32_t*>(&h0);
-                pa[2] = *reinterpret_cast<const uint32_t*>(&h1);
-                pa[1] = pack_f16(x[0][0] - b0.x, x[0][1] - b0.y);
-                pa[3] = pack_f16(x[0][2] - b1.x, x[0][3] - b1.y);
-            } else {
-                pa[0] = pack_f16(x[0][0], x[0][1]);
-                pa[1] = pack_f16(x[NR - 1][0], x[NR - 1][1]);
-                pa[2] = pack_f16(x[0][2], x[0][3]);
-                pa[3] = pack_f16(x[NR - 1][2], x[NR - 1][3]);
-            }
-            // tokens that no row of the tile sees hold anything: NaN codes too
-            if (!full) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int tok = base + 2 * t + (i & 1) + 8 * (i >> 1);
-                    if (tok >= tile_hi || tok < w.lo)
-#pragma unroll
-                        for (int j = 0; j < D / 32; ++j) f.v[i][j] = 0;
-                }
-                // and a token that only some rows see may hold NaN, which 0 * NaN would spread
-                uint32_t bad = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < D / 32; ++j) bad |= nan_bytes(f.v[i][j]);
-                if (__any_sync(0xffffffffu, bad != 0)) {
-                    // which rows see which tokens, times which codes are NaN: NaN where the product counts one
-                    uint32_t see[4] = {};
-#pragma unroll
-                    for (int j = 0; j < NR; ++j)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int tok = base + 8 * (i >> 1) + 2 * t + (i & 1);
-                            if (tok >= lo[j] && tok < hi[j]) see[2 * (i >> 1) + j] |= 0x3C00u << (16 * (i & 1));
-                        }
-#pragma unroll
-                    for (int wd = 0; wd < D / 32; ++wd)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t b[2];
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                b[k] = ((nan_bytes(f.v[2 * k][wd]) >> (8 * i + 7) & 1u) ? 0x3C00u : 0u) |
-                                       ((nan_bytes(f.v[2 * k + 1][wd]) >> (8 * i + 7) & 1u) ? 0x3C000000u : 0u);
-                            float acc[4] = {};
-                            mma_16816(acc, see, b[0], b[1]);
-                            float (&oo)[HL ? 2 : 4] = o[4 * wd + i];
-#pragma unroll
-                            for (int k = 0; k < (HL ? 2 : 4); ++k)
-                                if (acc[k] > 0.0f) oo[k] = __int_as_float(0x7FC00000);
-                        }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < D / 32; ++j) f.v[i][j] &= ~((nan_bytes(f.v[i][j]) >> 7) * 0xFFu);
+                    for (int k = 0; k < 4; ++k) {
+                        x[c][j][k] = ex2(x[c][j][k] - (m_use - 7.0f));  // P * 2^7: fp16 keeps more of the small ones
+                        sum += x[c][j][k];
+                    }
+                    l[j] = fmaf(sum, inv[c], l[j]);
                 }
             }
-            // sums: column tile 4 w + {0..3}, this lane's dims D/8 g + 4 w ..
+            if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-            for (int wd = 0; wd < D / 32; ++wd) {
-                const uint32_t a = __byte_perm(f.v[0][wd], f.v[1][wd], 0x5140), b = __byte_perm(f.v[0][wd], f.v[1][wd], 0x7362);
-                const uint32_t c = __byte_perm(f.v[2][wd], f.v[3][wd], 0x5140), d = __byte_perm(f.v[2][wd], f.v[3][wd], 0x7362);
+                for (int j = 0; j < NR; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t p0 = i < 2 ? a : b, p1 = i < 2 ? c : d;
-                    const uint32_t b0 = e4m3x2_to_f16x2((i & 1) ? p0 >> 16 : p0 & 0xFFFFu);
-                    const uint32_t b1 = e4m3x2_to_f16x2((i & 1) ? p1 >> 16 : p1 & 0xFFFFu);
-                    if constexpr (HL) {
-                        // a zero accumulator for each 16 tokens, added in fp32: the tensor core's own
-                        // accumulation does not round to nearest, which shows over long caches
-                        float acc[4] = {};
-                        mma_16816(acc, pa, b0, b1);
-                        o[4 * wd + i][0] += acc[0] + acc[2];
-                        o[4 * wd + i][1] += acc[1] + acc[3];
+                    for (int k = 0; k < NT; ++k) mul2(o[k][j], corr[j]);
+            }
+            uint32_t vf[S][4][D / 32];
+#pragma unroll
+            for (int c = 0; c < S; ++c) {
+                const uint8_t* vp = ring + stage * kStage<D> + c * kSlot<D> + kChunk * D;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    if constexpr (D == 128) {
+                        const uint4 a = *reinterpret_cast<const uint4*>(vp + v_unit<D>(4 * t + r, g));
+                        vf[c][r][0] = a.x; vf[c][r][1] = a.y; vf[c][r][2] = a.z; vf[c][r][3] = a.w;
                     } else {
-                        mma_16816(*reinterpret_cast<float (*)[4]>(&o[4 * wd + i][0]), pa, b0, b1);
+                        const uint2 a = *reinterpret_cast<const uint2*>(vp + v_unit<D>(4 * t + r, g >> 1) + 8 * (g & 1));
+                        vf[c][r][0] = a.x; vf[c][r][1] = a.y;
                     }
                 }
             }
-            f = nx;
+            __syncwarp();
+            issue(k_st + kRing);
+            note(k_st + kRing);
+#pragma unroll
+            for (int c = 0; c < S; ++c) {
+                if constexpr (HL) {
+                    const __half2 h0 = __floats2half2_rn(x[c][0][0], x[c][0][1]), h1 = __floats2half2_rn(x[c][0][2], x[c][0][3]);
+                    const float2 b0 = __half22float2(h0), b1 = __half22float2(h1);
+                    pa[c][0] = *reinterpret_cast<const uint32_t*>(&h0);
+                    pa[c][2] = *reinterpret_cast<const uint32_t*>(&h1);
+                    pa[c][1] = pack_f16(x[c][0][0] - b0.x, x[c][0][1] - b0.y);
+                    pa[c][3] = pack_f16(x[c][0][2] - b1.x, x[c][0][3] - b1.y);
+                } else {
+                    pa[c][0] = pack_f16(x[c][0][0], x[c][0][1]);
+                    pa[c][2] = pack_f16(x[c][0][2], x[c][0][3]);
+                    pa[c][1] = RT == 8 ? 0 : pack_f16(x[c][NR - 1][0], x[c][NR - 1][1]);
+                    pa[c][3] = RT == 8 ? 0 : pack_f16(x[c][NR - 1][2], x[c][NR - 1][3]);
+                }
+                if (!full[c]) {
+                    // tokens that no row of the tile sees hold anything: NaN codes too
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int tok = base0 + kUnit * (i + c) + 4 * t + k;
+                        if (!held[c] || tok >= tile_hi || tok < w_lo)
+#pragma unroll
+                            for (int q = 0; q < D / 32; ++q) vf[c][k][q] = 0;
+                    }
+                    // a token that only some rows see may hold NaN, which 0 * NaN would spread
+                    uint32_t bad = 0;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int q = 0; q < D / 32; ++q) bad |= nan_bytes(vf[c][r][q]);
+                    if (__any_sync(0xffffffffu, bad != 0)) {
+                        // which rows see which tokens, times which codes are NaN: NaN where the product counts one
+                        uint32_t see[4] = {};
+#pragma unroll
+                        for (int j = 0; j < NR; ++j)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int tok = base0 + kUnit * (i + c) + 4 * t + k;
+                                if (tok >= lo[j] && tok < hi[j]) see[2 * (k >> 1) + j] |= 0x3C00u << (16 * (k & 1));
+                            }
+#pragma unroll
+                        for (int q = 0; q < D / 32; ++q)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t b[2];
+#pragma unroll
+                                for (int r = 0; r < 2; ++r)
+                                    b[r] = ((nan_bytes(vf[c][2 * r][q]) >> (8 * k + 7) & 1u) ? 0x3C00u : 0u) |
+                                           ((nan_bytes(vf[c][2 * r + 1][q]) >> (8 * k + 7) & 1u) ? 0x3C000000u : 0u);
+                                float acc[4] = {};
+                                mma_16816(acc, see, b[0], b[1]);
+#pragma unroll
+                                for (int j = 0; j < NR; ++j) {
+                                    if (acc[2 * j] > 0.0f) o[4 * q + k][j].x = __int_as_float(0x7FC00000);
+                                    if (acc[2 * j + 1] > 0.0f) o[4 * q + k][j].y = __int_as_float(0x7FC00000);
+                                }
+                            }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+#pragma unroll
+                            for (int q = 0; q < D / 32; ++q) vf[c][r][q] &= ~((nan_bytes(vf[c][r][q]) >> 7) * 0xFFu);
+                    }
+                }
+            }
+            // sums: column tile 4 q + {0..3}, this lane's dims D/8 g + 4 q ..
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+                uint32_t b0[S][4], b1[S][4];
+#pragma unroll
+                for (int c = 0; c < S; ++c) {
+                    e4m3x4_to_f16x4(__byte_perm(vf[c][0][q], vf[c][1][q], 0x5140), &b0[c][0], &b0[c][1]);
+                    e4m3x4_to_f16x4(__byte_perm(vf[c][0][q], vf[c][1][q], 0x7362), &b0[c][2], &b0[c][3]);
+                    e4m3x4_to_f16x4(__byte_perm(vf[c][2][q], vf[c][3][q], 0x5140), &b1[c][0], &b1[c][1]);
+                    e4m3x4_to_f16x4(__byte_perm(vf[c][2][q], vf[c][3][q], 0x7362), &b1[c][2], &b1[c][3]);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    // A fresh accumulator for each stage, added in fp32: the tensor core's own accumulation does
+                    // not round to nearest, which shows over long caches; and rows 8-15 hold the low terms
+                    // of the same rows (fp32) or nothing (RT 8), so half the registers carry the sums.
+                    float acc[4];
+                    mma_16816_zero(acc, pa[0], b0[0][k], b1[0][k]);
+#pragma unroll
+                    for (int c = 1; c < S; ++c) mma_16816(acc, pa[c], b0[c][k], b1[c][k]);
+                    add2(o[4 * q + k][0], acc[0], acc[1]);
+                    if (HL) add2(o[4 * q + k][0], acc[2], acc[3]);
+                    if (RT == 16) add2(o[4 * q + k][NR - 1], acc[2], acc[3]);
+                }
+            }
         }
-
         // join the warps: each row's maximum, then the weighted sums
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < NR; ++j) {
@@ -447,15 +619,14 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
             float* d0 = s_o + (warp * RT + g + 8 * j) * D + D / 8 * 2 * t;
 #pragma unroll
             for (int n = 0; n < NT; n += 4) {
-                *reinterpret_cast<float4*>(d0 + n) =
-                    make_float4(o[n][HL ? 0 : 2 * j], o[n + 1][HL ? 0 : 2 * j], o[n + 2][HL ? 0 : 2 * j], o[n + 3][HL ? 0 : 2 * j]);
-                *reinterpret_cast<float4*>(d0 + D / 8 + n) =
-                    make_float4(o[n][HL ? 1 : 2 * j + 1], o[n + 1][HL ? 1 : 2 * j + 1], o[n + 2][HL ? 1 : 2 * j + 1], o[n + 3][HL ? 1 : 2 * j + 1]);
+                *reinterpret_cast<float4*>(d0 + n) = make_float4(o[n][j].x, o[n + 1][j].x, o[n + 2][j].x, o[n + 3][j].x);
+                *reinterpret_cast<float4*>(d0 + D / 8 + n) = make_float4(o[n][j].y, o[n + 1][j].y, o[n + 2][j].y, o[n + 3][j].y);
             }
         }
         __syncthreads();
-        const bool whole = ua == 0 && ub == w.units;
-        float* part = A.part + ((int64_t)blockIdx.x * 2 + (ua == 0 && u > u0 ? 1 : 0)) * (RT * (D + 2));
+        // a tile that begins in this piece, but not at its start, goes to the second slot
+        const bool whole = ua == 0 && ub == s_cur.w.units;
+        float* part = A.part + ((int64_t)blockIdx.x * 2 + (not_first ? 1 : 0)) * (RT * (D + 2));
         for (int i = threadIdx.x; i < RT * D / 4; i += 32 * kAttnWarps) {
             const int r = i / (D / 4), c = 4 * (i % (D / 4));
             float m = -INFINITY;
@@ -479,7 +650,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                     const float iv = m == -INFINITY ? 0.0f : 1.0f / den;
                     const float y[4] = {m == -INFINITY ? 0.0f : acc.x * iv, m == -INFINITY ? 0.0f : acc.y * iv,
                                         m == -INFINITY ? 0.0f : acc.z * iv, m == -INFINITY ? 0.0f : acc.w * iv};
-                    Vec<T>::store(static_cast<T*>(A.out) + (int64_t)(w.s.start + row / A.group) * A.out_stride +
+                    Vec<T>::store(static_cast<T*>(A.out) + (int64_t)(sp.start + row / A.group) * A.out_stride +
                                       (int64_t)(head * A.group + row % A.group) * D + c,
                                   y);
                 }
@@ -491,85 +662,115 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                 }
             }
         }
-        u += ub - ua;
+        not_first = true;
+        __syncthreads();  // what lies over the rings has been read
+        if (warp == 0) {
+            const int64_t u = s_u[0] + step;
+            Cursor c = s_cur;
+            __syncwarp();
+            const bool more = u < s_u[1] && (u < c.begin + c.w.total || seek<RT>(A, u, s_work[lane], &c));
+            if (lane == 0) {
+                s_cur = c;
+                s_u[0] = more ? u : s_u[1];
+            }
+        }
+        __syncthreads();
     }
 }
 
-// Join the pieces of every tile that was cut: grid (tiles of all sequences, an upper bound; rows).
-template <typename T, int D>
-__global__ void __launch_bounds__(D) attn_join_kernel(const __grid_constant__ AttnParams A, int pieces_max) {
-    constexpr int RT = sizeof(T) == 4 ? 8 : 16;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+// Join the tiles that were cut. CTA i looks at the cut between pieces i and i + 1; the CTAs whose cuts
+// lie in one tile share its rows, so a tile of many pieces has many CTAs. The lengths were complete before
+// the kernel that this one follows, so the tile is found while that kernel still runs. Warps that
+// share a row take its pieces in turn.
+constexpr int kJoinWarps = 8;
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ AttnParams A, int pieces_max) {
+    constexpr int kCols = D / 32, kPart = RT * (D + 2);
+    __shared__ float s_acc[kJoinWarps][D], s_den[kJoinWarps];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // the segment: sequence of the blockIdx.x-th (tile, head) pair
-    const int lane = threadIdx.x & 31;
-    int64_t total = total_work<RT>(A);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cut = blockIdx.x + 1;
+    const SeqWork mine = seq_work<RT>(A, lane);
+    const int64_t total = total_work<RT>(A, mine);
     const int pieces = (int)min((int64_t)pieces_max, total);
-    if (pieces == 0) return;
-    int seg = blockIdx.x;
-    int64_t begin = 0;
-    for (int base = 0; base < A.B.batch; base += 32) {
-        const SeqWork w = seq_work<RT>(A, base + lane);
-        const int n = w.tiles * A.kv_heads;
-        int inc = n;
-        int64_t inw = w.total;
+    int c0 = 0, c1 = 0, slot0 = 0, tile = 0, head = 0;
+    Cursor cur{};
+    if (cut < pieces && seek<RT>(A, piece_begin(total, pieces, cut), mine, &cur)) {
+        const int length = kTileCost + cur.w.units;
+        const int seg = (int)div_pos(piece_begin(total, pieces, cut) - cur.begin, length);
+        const int64_t begin = cur.begin + (int64_t)seg * length;
+        c0 = piece_of(total, pieces, begin + kTileCost);
+        c1 = piece_of(total, pieces, begin + length - 1);
+        slot0 = piece_begin(total, pieces, c0) >= begin ? 0 : 1;
+        tile = seg / A.kv_heads;
+        head = seg - tile * A.kv_heads;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (cut <= c0 || cut > c1) return;  // the cut lies before the tile's first unit, or no tile is cut here
+    const float* first = A.part + ((int64_t)c0 * 2 + slot0) * kPart;  // piece 0; piece i > 0 is slot 0 of CTA c0 + i
+    const float* rest = A.part + (int64_t)c0 * 2 * kPart;
+    const int np = c1 - c0 + 1, sharers = c1 - c0, mine_first = cut - c0 - 1;
+    auto part = [&](int i) { return i == 0 ? first : rest + (int64_t)i * 2 * kPart; };
+    const int rows = min(RT, cur.w.s.n * A.group - tile * RT);
+    const int here = (rows - mine_first + sharers - 1) / sharers;  // rows mine_first, mine_first + sharers, ...
+    if (here <= 0) return;
+    const int per_row = here >= kJoinWarps ? 1 : here > 4 ? 1 : here > 2 ? 2 : here > 1 ? 4 : 8;  // warps of a row
+    for (int k0 = 0; k0 < here; k0 += kJoinWarps / per_row) {
+        const int k = k0 + warp / per_row, r = mine_first + k * sharers;
+        float m = -INFINITY, acc[kCols] = {}, den = 0.0f;
+        if (k < here) {
+            for (int i = lane; i < np; i += 32) m = fmaxf(m, __ldcg(part(i) + RT * D + r));
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, inc, o);
-            const int64_t y = __shfl_up_sync(0xffffffffu, inw, o);
-            if (lane >= o) { inc += x; inw += y; }
+            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float mu = m == -INFINITY ? 0.0f : m;
+#pragma unroll 4
+            for (int i = warp % per_row; i < np; i += per_row) {
+                const float* x = part(i);
+                const float wt = ex2(__ldcg(x + RT * D + r) - mu);
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) acc[c] = fmaf(wt, __ldcg(x + r * D + 32 * c + lane), acc[c]);
+                den = fmaf(wt, __ldcg(x + RT * D + RT + r), den);
+            }
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, seg < inc);
-        if (!hit) {
-            seg -= __shfl_sync(0xffffffffu, inc, 31);
-            begin += __shfl_sync(0xffffffffu, inw, 31);
-            continue;
+        if (per_row > 1) {
+            if (lane == 0) s_den[warp] = den;
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) s_acc[warp][32 * c + lane] = acc[c];
+            __syncthreads();
+            if (warp % per_row == 0)
+                for (int i = 1; i < per_row; ++i) {
+                    den += s_den[warp + i];
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c) acc[c] += s_acc[warp + i][32 * c + lane];
+                }
+            __syncthreads();
         }
-        const int src = __ffs(hit) - 1;
-        const int local = seg - __shfl_sync(0xffffffffu, inc - n, src);
-        const int units = __shfl_sync(0xffffffffu, w.units, src);
-        const int start = __shfl_sync(0xffffffffu, w.s.start, src), cnt = __shfl_sync(0xffffffffu, w.s.n, src);
-        const int64_t a = begin + __shfl_sync(0xffffffffu, inw - w.total, src) + (int64_t)local * units;
-        const int c0 = piece_of(total, pieces, a), c1 = piece_of(total, pieces, a + units - 1);
-        const int tile = local / A.kv_heads, head = local % A.kv_heads, r = blockIdx.y;
-        const int row = tile * RT + r;
-        if (c0 == c1 || row >= cnt * A.group) return;  // written by its one CTA
-        const int slot0 = piece_begin(total, pieces, c0) == a ? 0 : 1;
-        const int64_t step = 2 * RT * (D + 2);
-        const float* p = A.part + c0 * step + slot0 * (RT * (D + 2));
-        const float* p1 = A.part + (int64_t)(c0 + 1) * step;
-        const int c = threadIdx.x;
-        float m = p[RT * D + r];
-        for (int i = 0; i < c1 - c0; ++i) m = fmaxf(m, p1[i * step + RT * D + r]);
-        const float mu = m == -INFINITY ? 0.0f : m;
-        const float w0 = ex2(p[RT * D + r] - mu);
-        float acc = w0 * p[r * D + c], den = w0 * p[RT * D + RT + r];
-        for (int i = 0; i < c1 - c0; ++i) {
-            const float* x = p1 + i * step;
-            const float wt = ex2(x[RT * D + r] - mu);
-            acc = fmaf(wt, x[r * D + c], acc);
-            den = fmaf(wt, x[RT * D + RT + r], den);
+        if (k < here && warp % per_row == 0) {
+            const int row = tile * RT + r;
+            T* out = static_cast<T*>(A.out) + (int64_t)(cur.w.s.start + row / A.group) * A.out_stride +
+                     (int64_t)(head * A.group + row % A.group) * D + lane;
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) {
+                const float y = m == -INFINITY ? 0.0f : acc[c] / den;
+                if constexpr (sizeof(T) == 4) out[32 * c] = y;
+                else out[32 * c] = __float2bfloat16_rn(y);
+            }
         }
-        const float y = m == -INFINITY ? 0.0f : acc / den;
-        T* out = static_cast<T*>(A.out) + (int64_t)(start + row / A.group) * A.out_stride +
-                 (int64_t)(head * A.group + row % A.group) * D + c;
-        if constexpr (sizeof(T) == 4) *out = y;
-        else *out = __float2bfloat16_rn(y);
-        return;
     }
 }
 
-template <typename T, int D>
-cudaError_t launch_typed(const AttnParams& P, int64_t segs, int64_t units, cudaStream_t stream) {
-    constexpr int RT = sizeof(T) == 4 ? 8 : 16;
-    const size_t smem = (size_t)kAttnWarps * RT * (D + 2) * sizeof(float);
+template <typename T, int D, int RT>
+cudaError_t launch_typed(const AttnParams& P, int64_t units, cudaStream_t stream) {
+    // an upper bound of the row tiles: a sequence's last one may be part filled
+    const int64_t segs = ((int64_t)P.B.m * P.group / RT + (P.B.m < P.B.batch ? P.B.m : P.B.batch)) * P.kv_heads;
+    const size_t rings = (size_t)kAttnWarps * kRing * kStage<D>, join = (size_t)kAttnWarps * RT * D * sizeof(float);
+    const size_t smem = rings > join ? rings : join;
     static bool set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!set[dev]) {
-        e = cudaFuncSetAttribute(attn_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = cudaFuncSetAttribute(attn_kernel<T, D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         set[dev] = true;
     }
@@ -585,12 +786,13 @@ cudaError_t launch_typed(const AttnParams& P, int64_t segs, int64_t units, cudaS
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attn_kernel<T, D>, P);
+    e = cudaLaunchKernelEx(&cfg, attn_kernel<T, D, RT>, P);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((unsigned)segs, RT);
-    cfg.blockDim = dim3(D);
+    if (grid == 1) return cudaSuccess;
+    cfg.gridDim = dim3((unsigned)(grid - 1));
+    cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D>, P, (int)grid);
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D, RT>, P, (int)grid);
 }
 
 }  // namespace
@@ -601,8 +803,8 @@ size_t attn_workspace_bytes(int head_dim) {  // two slots of up to 16 rows per C
 
 cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int64_t q_stride, int q_heads, int kv_heads,
                              int head_dim, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
-                             const float* v_scale, int max_len, float scale, int window, void* out, int64_t out_stride,
-                             void* workspace, int* err_flag, cudaStream_t stream) {
+                             const float* v_scale, int max_q_len, int max_len, float scale, int window, void* out,
+                             int64_t out_stride, void* workspace, int* err_flag, cudaStream_t stream) {
     AttnParams P{};
     P.B = B; P.q = q; P.out = out; P.q_stride = q_stride; P.out_stride = out_stride;
     P.k_cache = k_cache; P.v_cache = v_cache; P.k_scale = k_scale; P.v_scale = v_scale;
@@ -611,14 +813,15 @@ cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int6
     P.part = static_cast<float*>(workspace);
     P.parts = num_sms() * kCtasPerSm < kMaxParts ? num_sms() * kCtasPerSm : kMaxParts;
     P.err_flag = err_flag;
-    const int rt = dtype == Q4K_F32 ? 8 : 16;
-    // upper bounds: row tiles (a sequence's last one may be part filled), pieces of a tile
-    int64_t segs = ((int64_t)B.m * P.group / rt + min(B.m, B.batch)) * kv_heads;
-    const int64_t units = (max_len + kUnit - 1) / kUnit + 1;
+    const int64_t units = (max_len + kUnit - 1) / kUnit + 1 + kTileCost;
     if (dtype == Q4K_F32)
-        return head_dim == 64 ? launch_typed<float, 64>(P, segs, units, stream) : launch_typed<float, 128>(P, segs, units, stream);
-    return head_dim == 64 ? launch_typed<__nv_bfloat16, 64>(P, segs, units, stream)
-                          : launch_typed<__nv_bfloat16, 128>(P, segs, units, stream);
+        return head_dim == 64 ? launch_typed<float, 64, 8>(P, units, stream) : launch_typed<float, 128, 8>(P, units, stream);
+    // bf16: tiles of 8 rows while a sequence's rows fit one (fewer registers and half the softmax), else 16
+    if ((int64_t)max_q_len * P.group <= 8)
+        return head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 8>(P, units, stream)
+                              : launch_typed<__nv_bfloat16, 128, 8>(P, units, stream);
+    return head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 16>(P, units, stream)
+                          : launch_typed<__nv_bfloat16, 128, 16>(P, units, stream);
 }
 
 }  // namespace q4k

@@ -61,8 +61,8 @@ cudaError_t launch_kv_append(const PagedBatch& B, const void* k, const void* v, 
 size_t attn_workspace_bytes(int head_dim);
 cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int64_t q_stride, int q_heads, int kv_heads,
                              int head_dim, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
-                             const float* v_scale, int max_len, float scale, int window, void* out, int64_t out_stride,
-                             void* workspace, int* err_flag, cudaStream_t stream);
+                             const float* v_scale, int max_q_len, int max_len, float scale, int window, void* out,
+                             int64_t out_stride, void* workspace, int* err_flag, cudaStream_t stream);
 cudaError_t launch_quantize(const float* x, int64_t rows, int k, uint8_t* out, cudaStream_t stream);
 cudaError_t launch_stream_ceiling(const void* src, uint64_t bytes, uint32_t* sink, cudaStream_t stream);
 // Up to 5 small copies (sizes multiples of 4 bytes) in one launch; sources may be host memory

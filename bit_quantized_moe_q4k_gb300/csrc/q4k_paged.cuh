@@ -208,6 +208,12 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t lo16) {
     asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(lo16));
     return r;
 }
+// All four codes of a word: bytes 0 and 1, bytes 2 and 3.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t* lo, uint32_t* hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(*lo), "=r"(*hi)
+        : "r"(w));
+}
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
     uint32_t r;
     asm("{\n\t.reg .b16 h;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %2, %1;\n\tcvt.u32.u16 %0, h;\n\t}"
