@@ -27,6 +27,8 @@ constexpr int kChunk = 16;                    // tokens a warp takes at a time
 constexpr int kUnit = kChunk * kAttnWarps;    // tokens of one unit of work
 constexpr int kTileCost = 4;                  // units that starting and ending a tile are worth
 constexpr int kCtasPerSm = 3;
+// Up to this many query rows per kv head a sequence is worked on here, else by the prompt kernel.
+constexpr int kFewRows = 64;
 constexpr int kMaxParts = 512;                // CTAs that the workspace serves
 
 struct AttnParams {
@@ -38,6 +40,7 @@ struct AttnParams {
     const float *k_scale, *v_scale;
     int q_heads, kv_heads, group;
     int window;
+    int max_rows;       // sequences with more query rows per kv head are the prompt kernel's
     float scale_log2;   // softmax scale * log2(e)
     float* part;        // partial results: per CTA two slots of [rows][D] sums, rows M, rows l
     int parts;          // CTAs the partial buffer holds
@@ -96,7 +99,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& A, int i) {
     bool bad;
     w.s = seq_span(A.B, i, &bad);
     if (bad) raise_flag(A.err_flag, Q4K_ERR_SEQ);
-    if (w.s.n == 0) return w;
+    if (w.s.n == 0 || (int64_t)w.s.n * A.group > A.max_rows) return w;
     const int first = max(w.s.len - w.s.n, 0);
     w.lo = A.window > 0 ? (max(first - A.window + 1, 0) & ~(kChunk - 1)) : 0;
     w.tiles = (w.s.n * A.group + RT - 1) / RT;
@@ -805,6 +808,16 @@ cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int6
                              int head_dim, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
                              const float* v_scale, int max_q_len, int max_len, float scale, int window, void* out,
                              int64_t out_stride, void* workspace, int* err_flag, cudaStream_t stream) {
+    // Which kernel a sequence takes goes by its query rows per kv head; max_q_len says which kernels can
+    // be needed, and a kernel that is launched alone takes every sequence.
+    const int64_t most = (int64_t)max_q_len * (q_heads / kv_heads);
+    const bool prompts = most > kFewRows, few = !prompts || !(B.batch == 1 || B.m == (int64_t)B.batch * max_q_len);
+    if (prompts) {
+        const cudaError_t e = launch_attention_prompt(B, q, dtype, q_stride, q_heads, kv_heads, head_dim, k_cache, v_cache,
+                                                      k_scale, v_scale, few ? kFewRows + 1 : 1, scale, window, out,
+                                                      out_stride, err_flag, stream);
+        if (e != cudaSuccess || !few) return e;
+    }
     AttnParams P{};
     P.B = B; P.q = q; P.out = out; P.q_stride = q_stride; P.out_stride = out_stride;
     P.k_cache = k_cache; P.v_cache = v_cache; P.k_scale = k_scale; P.v_scale = v_scale;
@@ -813,11 +826,13 @@ cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int6
     P.part = static_cast<float*>(workspace);
     P.parts = num_sms() * kCtasPerSm < kMaxParts ? num_sms() * kCtasPerSm : kMaxParts;
     P.err_flag = err_flag;
+    P.max_rows = prompts ? kFewRows : 0x7FFFFFFF;
     const int64_t units = (max_len + kUnit - 1) / kUnit + 1 + kTileCost;
     if (dtype == Q4K_F32)
         return head_dim == 64 ? launch_typed<float, 64, 8>(P, units, stream) : launch_typed<float, 128, 8>(P, units, stream);
-    // bf16: tiles of 8 rows while a sequence's rows fit one (fewer registers and half the softmax), else 16
-    if ((int64_t)max_q_len * P.group <= 8)
+    // bf16: tiles of 8 rows where a sequence's rows fit one (half the softmax), else 16; next to prompts
+    // the other sequences mostly decode
+    if ((prompts ? P.group : most) <= 8)
         return head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 8>(P, units, stream)
                               : launch_typed<__nv_bfloat16, 128, 8>(P, units, stream);
     return head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 16>(P, units, stream)

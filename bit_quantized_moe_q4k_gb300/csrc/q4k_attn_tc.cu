@@ -1,0 +1,616 @@
+// q4k_attn_tc.cu -- attention over the paged 8-bit cache for many query rows per kv head (prompts), on the
+// tensor cores.
+//
+// The mathematics of q4k_attn.cu: x_j = c (code_k . q) + e_j, P_j = 2^(x_j - M + 7), out = sum P_j code_v,j /
+// sum 2^(-e_j) P_j, with the codes of both sides exact in fp16, bf16 queries in one fp16 term and fp32
+// queries (and their P) in two.
+//
+// A CTA takes 128 query rows of one kv head (row r: token r / group, head r % group, so the heads of a
+// group share each K and V tile) and walks over the tokens that some row sees, 128 at a time:
+//   S = Q K^T   tcgen05.mma, Q and K from shared memory (K-major, 128-byte swizzle)
+//   P in place of S in tensor memory, the A operand of
+//   O = P V     V from shared memory as it lies in the cache, d contiguous (N-major)
+// S and O have two tiles each in tensor memory, so that S of the next tokens is multiplied while the
+// softmax of these is computed. O of each 128 tokens is a fresh accumulator that is added to fp32 sums in
+// registers: the tensor core's own accumulation does not round to nearest, and the running maximum's
+// correction costs nothing more there.
+//
+// Roles: warps 0-3 softmax (thread = row), 4-7 the sums (thread = row) and the store, 8-11 read the
+// cache and write fp16 tiles, warp 12 issues the products (13-15 idle). Every wait is bounded; an abort flag
+// lets all roles leave together.
+//
+// Bound by shared memory and the tensor core together: a tile of 128 x 128 x 128 takes 512 cycles for
+// each product, reads 96 KB of operands and writes 64 KB of converted K and V at 128 bytes a cycle.
+#include "q4k_paged.cuh"
+#include "q4k_sm100.cuh"
+#include "q4k_sync.cuh"
+
+namespace q4k {
+using namespace sm100;
+namespace {
+
+constexpr int kRows = 128;   // query rows of a CTA
+constexpr int kToks = 128;   // tokens of a tile
+constexpr int kGroups = kToks / 16;
+constexpr int kThreads = 512;
+constexpr int kLoadWarp = 8, kMmaWarp = 12;
+// Registers a thread of each warpgroup after the split; their sum is four times what the launch gives.
+constexpr int kRegsSoftmax = 152, kRegsSums = 184, kRegsLoad = 104, kRegsMma = 72;
+static_assert(kRegsSoftmax + kRegsSums + kRegsLoad + kRegsMma <= 4 * (65536 / kThreads), "register split");
+constexpr int kMetaRing = 4;
+
+struct PromptParams {
+    PagedBatch B;
+    const void* q;
+    void* out;
+    int64_t q_stride, out_stride;
+    const uint8_t *k_cache, *v_cache;
+    const float *k_scale, *v_scale;
+    int kv_heads, group, window;
+    int min_rows;       // sequences with fewer query rows per kv head are not this kernel's
+    float scale_log2;   // |softmax scale| * log2(e)
+    float sign;         // its sign, multiplied into the queries
+    int* err_flag;
+    uint64_t wait_ns;
+};
+
+// What the softmax needs of a tile's 16-token groups.
+struct TileMeta {
+    float ks[kGroups], ev[kGroups], inv[kGroups];
+    int ok[kGroups];
+    int all_ok;
+};
+
+template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+template <bool HL, int D>
+struct Layout {
+    static constexpr int kTerms = HL ? 2 : 1;
+    static constexpr int kTile = kToks * D * 2;            // a K or V tile (and one term of Q)
+    static constexpr int kSlots = HL ? 4 : 5;              // at most 6: kMetaRing holds what is in flight
+    static constexpr int kQ = kTerms * kTile;
+    static constexpr int kBytes = 1024 + kQ + kSlots * kTile;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float log2_scale(float s) {  // exact for powers of two
+    const uint32_t b = __float_as_uint(s);
+    const float e = (float)((int)(b >> 23) - 127);
+    return (b & 0x7FFFFFu) ? e + log2f(__uint_as_float((b & 0x7FFFFFu) | 0x3F800000u)) : e;
+}
+__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+
+// 16 codes to 16 halves; NaN codes become 0 and set *nan.
+template <bool CLEAN>
+__device__ __forceinline__ void expand16(const uint4& c, uint32_t (&h)[8], bool* nan) {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e4m3x4_to_f16x4(w[i], &h[2 * i], &h[2 * i + 1]);
+    if (CLEAN) {
+        __half2 acc = __float2half2_rn(0.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc = __hfma2(*reinterpret_cast<const __half2*>(&h[i]), __float2half2_rn(0.0f), acc);
+        if (__hisnan(__low2half(acc)) || __hisnan(__high2half(acc))) {
+            *nan = true;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if ((h[i] & 0x7FFFu) > 0x7C00u) h[i] &= 0xFFFF0000u;
+                if ((h[i] & 0x7FFF0000u) > 0x7C000000u) h[i] &= 0x0000FFFFu;
+            }
+        }
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_constant__ PromptParams A) {
+    constexpr bool HL = sizeof(T) == 4;
+    using L = Layout<HL, D>;
+    constexpr uint32_t kColS = 0, kColO = 256;  // tensor memory: two S tiles, two O tiles
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* s_q = smem;
+    uint8_t* s_kv = smem + L::kQ;
+    __shared__ __align__(8) uint64_t full[L::kSlots], empty[L::kSlots], meta_full[kMetaRing];
+    __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], fin, drain;
+    __shared__ TileMeta s_meta[kMetaRing];
+    __shared__ float s_c[kRows], s_corr[2][kRows], s_inv[kRows];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_item[5];
+    __shared__ volatile int s_abort;
+    __shared__ volatile int s_nan;
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    // the item: blocks are taken from the last row tile down, the longest first
+    if (warp == 0) {
+        int at = blockIdx.x;
+        bool found = false;
+        for (int top = A.B.batch; top > 0 && !found; top -= 32) {
+            const int i = top - 1 - lane;  // lane 0: the last sequence
+            SeqSpan s{0, 0, 0};
+            int n = 0;
+            if (i >= 0) {
+                bool bad;
+                s = seq_span(A.B, i, &bad);
+                if (bad) raise_flag(A.err_flag, Q4K_ERR_SEQ);
+                const int rows = s.n * A.group;
+                if (rows >= A.min_rows) n = (rows + kRows - 1) / kRows * A.kv_heads;
+            }
+            int inc = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += x;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, at < inc);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                if (lane == src) {
+                    s_item[0] = i;
+                    s_item[1] = n - 1 - (at - (inc - n));  // row tile * kv_heads + kv head
+                    s_item[2] = s.start;
+                    s_item[3] = s.n;
+                    s_item[4] = s.len;
+                }
+                found = true;
+            }
+            at -= __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (!found && lane == 0) s_item[0] = -1;
+    }
+    if (tid == 32) {
+        for (int i = 0; i < L::kSlots; ++i) {
+            mbar_init(&full[i], 128);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < kMetaRing; ++i) mbar_init(&meta_full[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 128);
+            mbar_init(&o_full[i], 1);
+            mbar_init(&o_empty[i], 128);
+        }
+        mbar_init(&fin, 256);
+        mbar_init(&drain, 1);
+        fence_mbar_init();
+        s_abort = 0;
+        s_nan = 0;
+    }
+    __syncthreads();
+    const int seq = s_item[0];
+    if (seq < 0) return;  // the whole CTA, before any allocation
+    const int head = s_item[1] % A.kv_heads, tile = s_item[1] / A.kv_heads;
+    const int start = s_item[2], rows = s_item[3] * A.group, first = s_item[4] - s_item[3];
+    const int r0 = tile * kRows, last = min(rows, r0 + kRows) - 1;
+    // positions: some row sees tokens in [kv_lo, kv_hi), every row those in [full_lo, full_hi)
+    const int pf = first + r0 / A.group, pl = first + last / A.group;
+    const int kv_hi = max(pl + 1, 0), full_hi = max(pf + 1, 0);
+    const int kv_lo = A.window > 0 ? max(pf - A.window + 1, 0) : 0;
+    const int full_lo = A.window > 0 ? max(pl - A.window + 1, 0) : 0;
+    const int kv0 = kv_lo & ~15;
+    const int n = (kv_hi - kv0 + kToks - 1) / kToks;  // tiles; 0: no row sees anything
+
+    if (warp == kMmaWarp) {
+        tmem_alloc(&s_tmem, 512);
+        tmem_relinquish();
+    }
+    // queries: two threads a row, D/2 dims each, scaled by a power of two into fp16's range
+    if (tid < 256) {
+        const int row = tid >> 1, half = tid & 1, r = r0 + row;
+        const bool valid = r < rows;
+        const T* p = static_cast<const T*>(A.q) + (int64_t)(start + (valid ? r / A.group : 0)) * A.q_stride +
+                     (int64_t)(head * A.group + (valid ? r % A.group : 0)) * D + half * (D / 2);
+        float x[D / 2];
+        Vec<T>::load(p, x);
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 2; ++i) {
+            if (!valid) x[i] = 0.0f;
+            const float a = fabsf(x[i]);
+            if (a <= 3.402823466e38f) amax = fmaxf(amax, a);
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        const int e = amax > 0.0f ? min(max(134 - (int)(__float_as_uint(amax) >> 23), -120), 120) : 0;
+        const float up = A.sign * exp2_int(e);
+        if (half == 0) s_c[row] = A.scale_log2 * exp2_int(-e);
+#pragma unroll
+        for (int u = 0; u < D / 16; ++u) {  // 8 dims a unit
+            const int unit = half * (D / 16) + u;
+            uint8_t* dst = s_q + (unit >> 3) * (kRows * 128) + row * 128 + (((unit & 7) ^ (row & 7)) << 4);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = x[8 * u + 2 * i] * up, b = x[8 * u + 2 * i + 1] * up;
+                const __half2 h = __floats2half2_rn(a, b);
+                hi[i] = h2_bits(h);
+                if (HL) {
+                    const float2 f = __half22float2(h);
+                    lo[i] = h2_bits(__floats2half2_rn(a - f.x, b - f.y));
+                }
+            }
+            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (HL) *reinterpret_cast<uint4*>(dst + L::kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    bool ok = true;
+    // a wait of a whole warp: its lanes go on, or give up, together
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait_for(bar, parity, &s_abort, A.wait_ns)) != 0;
+    };
+
+    if (warp >= kLoadWarp && warp < kMmaWarp) {
+        regs_dec<kRegsLoad>();
+        // ---------------- cache to fp16 tiles. Order of the slots: K0, K1, V0, K2, V1, ..., V(n-1)
+        constexpr int kUnits = D / 16, kPer = 128 / kUnits, kLoads = kToks / kPer;  // 16-byte reads of a row; rows of a read
+        const int i = tid - 32 * kLoadWarp, sub = i / kUnits, chunk = i % kUnits;
+        auto page_of = [&](int j) {  // lanes 0-7: the page of each 16-token group of tile j
+            const int tok = kv0 + kToks * j + 16 * (lane & 7);
+            return j < n && tok < kv_hi ? page_id(A.B, seq, tok >> A.B.page_shift, A.err_flag) : -1;
+        };
+        auto fetch = [&](const uint8_t* cache, int j, int pid, uint4 (&r)[kLoads]) {
+#pragma unroll
+            for (int x = 0; x < kLoads; ++x) {
+                const int in = x * kPer + sub, tok = kv0 + kToks * j + in;
+                const int p = __shfl_sync(0xffffffffu, pid, in >> 4);
+                r[x] = make_uint4(0, 0, 0, 0);
+                if (p >= 0 && tok < kv_hi)
+                    r[x] = __ldcg(reinterpret_cast<const uint4*>(
+                        cache + (((((int64_t)p * A.kv_heads + head) << A.B.page_shift) + (tok & ((1 << A.B.page_shift) - 1))) * D) +
+                        16 * chunk));
+            }
+        };
+        int slot = 0, uses = 0;
+        bool nan = false;
+        auto put = [&](bool v_side, const uint4 (&r)[kLoads]) {
+            if (!wait(&empty[slot], (uses & 1) ^ 1)) return false;
+            // 16 dims are two 16-byte units of the row's 128-byte panel line; lanes of the second panel
+            // write them in the other order, which keeps a store's lanes on different banks
+            uint8_t* base = s_kv + slot * L::kTile + (chunk >> 2) * (kToks * 128);
+            const int flip = (chunk >> 2) & 1;
+#pragma unroll
+            for (int x = 0; x < kLoads; ++x) {
+                const int row = x * kPer + sub;
+                uint32_t h[8];
+                if (v_side) expand16<true>(r[x], h, &nan);
+                else expand16<false>(r[x], h, &nan);
+                const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
+                const int u = 2 * (chunk & 3);
+                *reinterpret_cast<uint4*>(base + row * 128 + (((u + flip) ^ (row & 7)) << 4)) = flip ? b : a;
+                *reinterpret_cast<uint4*>(base + row * 128 + (((u + 1 - flip) ^ (row & 7)) << 4)) = flip ? a : b;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&full[slot]);
+            if (++slot == L::kSlots) { slot = 0; ++uses; }
+            return true;
+        };
+        auto scales_of = [&](int pid, float* ks, float* vs) {
+            *ks = *vs = 1.0f;
+            if (pid >= 0) {
+                *ks = __ldcg(A.k_scale + (int64_t)pid * A.kv_heads + head);
+                *vs = __ldcg(A.v_scale + (int64_t)pid * A.kv_heads + head);
+            }
+        };
+        auto note = [&](int j, int pid, float ks, float vs) {  // the tile's scales, by the first loading warp
+            if (warp != kLoadWarp) return;
+            const bool good = pid >= 0 || kv0 + kToks * j + 16 * (lane & 7) >= kv_hi;  // past the end: masked anyway
+            const bool all = __all_sync(0xffffffffu, good);
+            TileMeta& m = s_meta[j % kMetaRing];
+            if (lane < kGroups) {
+                m.ks[lane] = ks;
+                m.ev[lane] = log2_scale(vs);
+                m.inv[lane] = 1.0f / vs;
+                m.ok[lane] = pid >= 0;
+            }
+            if (lane == 0) m.all_ok = all;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&meta_full[j % kMetaRing]);
+        };
+        if (n > 0) {
+            int p0 = page_of(0), p1 = page_of(1), p2 = page_of(2);
+            uint4 ra[kLoads], rb[kLoads];
+            float ks, vs;
+            fetch(A.k_cache, 0, p0, ra);
+            scales_of(p0, &ks, &vs);
+            fetch(A.v_cache, 0, p0, rb);
+            ok = put(false, ra);
+            if (ok) note(0, p0, ks, vs);
+            fetch(A.k_cache, 1, p1, ra);
+            scales_of(p1, &ks, &vs);
+            for (int j = 0; j < n && ok; ++j) {
+                if (j + 1 < n) {
+                    ok = put(false, ra);
+                    if (!ok) break;
+                    note(j + 1, p1, ks, vs);
+                }
+                fetch(A.k_cache, j + 2, p2, ra);
+                scales_of(p2, &ks, &vs);
+                ok = put(true, rb);
+                fetch(A.v_cache, j + 1, p1, rb);
+                p1 = p2;
+                p2 = page_of(j + 3);
+            }
+        }
+        if (nan) s_nan = 1;
+        mbar_arrive(&fin);
+    } else if (warp >= kMmaWarp) {
+        regs_dec<kRegsMma>();
+        if (warp == kMmaWarp) {
+        // ---------------- products, issued by one elected lane of the warp
+        const uint32_t idesc_s = idesc_f16_f32(kRows, kToks);
+        const uint32_t idesc_o = idesc_f16_f32(kRows, D) | kIdescBMnMajor;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t q_at = __shfl_sync(0xffffffffu, smem_u32(s_q), 0), kv_at = q_at + L::kQ;
+        int slot = 0, uses = 0;
+        bool issued = false;
+        auto next_slot = [&]() { if (++slot == L::kSlots) { slot = 0; ++uses; } };
+        auto scores = [&](int j) {
+            if (!wait(&full[slot], uses & 1)) return false;
+            tc_fence_after();
+            const uint32_t d = tm + kColS + (j & 1) * kToks;
+            const uint64_t b = desc_sw128_kmajor(kv_at + slot * L::kTile);
+#pragma unroll
+            for (int t = 0; t < L::kTerms; ++t) {
+                const uint64_t a = desc_sw128_kmajor(q_at + t * L::kTile);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = ((k >> 2) * (kToks * 128) + (k & 3) * 32) >> 4;
+                    mma_f16_ss_elect(d, a + off, b + off, idesc_s, t > 0 || k > 0);
+                }
+            }
+            mma_commit_elect(&s_full[j & 1]);
+            mma_commit_elect(&empty[slot]);
+            issued = true;
+            next_slot();
+            return true;
+        };
+        if (n > 0) ok = scores(0);
+        for (int j = 0; j < n && ok; ++j) {
+            if (j + 1 < n && !(ok = scores(j + 1))) break;
+            // P of these tokens (o_empty of the tile two before is implied: the softmax waited for it)
+            ok = wait(&p_full[j & 1], (j >> 1) & 1) && wait(&full[slot], uses & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t p = tm + kColS + (j & 1) * kToks, d = tm + kColO + (j & 1) * D;
+            const uint64_t b = desc_sw128_mnmajor(kv_at + slot * L::kTile, kToks * 128);
+#pragma unroll
+            for (int t = 0; t < L::kTerms; ++t)
+#pragma unroll
+                for (int k = 0; k < kToks / 16; ++k) {
+                    const uint32_t a = HL ? p + 32 * (k >> 1) + 8 * (k & 1) + 16 * t : p + 8 * k;
+                    mma_f16_ts_elect(d, a, b + ((k * 16 * 128) >> 4), idesc_o, t > 0 || k > 0);
+                }
+            mma_commit_elect(&o_full[j & 1]);
+            mma_commit_elect(&empty[slot]);
+            next_slot();
+        }
+        if (!ok && issued) {  // outstanding products finish before tensor memory is freed
+            volatile int never = 0;
+            mma_commit_elect(&drain);
+            mbar_wait(&drain, 0, &never);
+        }
+        __syncwarp();
+        }
+    } else if (warp < 4) {
+        regs_inc<kRegsSoftmax>();
+        // ---------------- softmax: thread = row = tensor memory lane
+        const int r = r0 + tid;
+        const bool valid = r < rows;
+        const int pos = first + (valid ? r / A.group : 0);
+        const int hi = valid ? pos + 1 : 0, lo = A.window > 0 ? max(pos - A.window + 1, 0) : 0;
+        const float crow = s_c[tid];
+        const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
+        float m = -INFINITY, l = 0.0f;
+        for (int j = 0; j < n; ++j) {
+            const int b = j & 1;
+            ok = wait(&meta_full[j % kMetaRing], (j / kMetaRing) & 1) && wait(&s_full[b], (j >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const TileMeta& meta = s_meta[j % kMetaRing];
+            const int t0 = kv0 + kToks * j;
+            const bool whole = meta.all_ok && t0 >= full_lo && t0 + kToks <= full_hi;
+            const uint32_t at = tmem + lane_base + kColS + b * kToks;
+            auto seen = [&](int g, int c) {  // column 16 g + c
+                const int tok = t0 + 16 * g + c;
+                return meta.ok[g] && tok >= lo && tok < hi;
+            };
+            float top = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < kToks / 32; ++q) {
+                uint32_t v[32];
+                tmem_ld32(at + 32 * q, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int g = 2 * q + h;
+                    float x = -INFINITY;
+                    if (whole) {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) x = fmaxf(x, __uint_as_float(v[16 * h + c]));
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) x = seen(g, c) ? fmaxf(x, __uint_as_float(v[16 * h + c])) : x;
+                    }
+                    if (x > -INFINITY) top = fmaxf(top, fmaf(x, crow * meta.ks[g], meta.ev[g]));
+                }
+            }
+            const float m_new = fmaxf(m, top), m_use = m_new == -INFINITY ? 0.0f : m_new;
+            const float corr = ex2(m - m_use);
+            m = m_new;
+            l *= corr;
+            // the sums have taken the tile two before this one
+            if (j >= 2) ok = wait(&o_empty[b], ((j >> 1) - 1) & 1);
+            if (!ok) break;
+            s_corr[b][tid] = corr;
+            uint32_t pk[32];
+#pragma unroll
+            for (int q = 0; q < kToks / 32; ++q) {
+                uint32_t v[32];
+                tmem_ld32(at + 32 * q, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int g = 2 * q + h;
+                    const float c = crow * meta.ks[g], e = meta.ev[g] - (m_use - 7.0f);
+                    float p[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float x = fmaf(__uint_as_float(v[16 * h + k]), c, e);
+                        if (!whole && !seen(g, k)) x = -INFINITY;
+                        p[k] = ex2(x);
+                    }
+                    float2 sum = make_float2(p[0], p[1]);
+#pragma unroll
+                    for (int k = 2; k < 16; k += 2) { sum.x += p[k]; sum.y += p[k + 1]; }
+                    l = fmaf(sum.x + sum.y, meta.inv[g], l);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const __half2 hh = __floats2half2_rn(p[2 * k], p[2 * k + 1]);
+                        if constexpr (HL) {
+                            const float2 f = __half22float2(hh);
+                            pk[8 * h + k] = h2_bits(hh);
+                            pk[16 + 8 * h + k] = h2_bits(__floats2half2_rn(p[2 * k] - f.x, p[2 * k + 1] - f.y));
+                        } else {
+                            pk[16 * (q & 1) + 8 * h + k] = h2_bits(hh);
+                        }
+                    }
+                }
+                // over columns of S that have been read: 32 per step (two terms) or per two steps
+                if (HL) tmem_st32(at + 32 * q, pk);
+                else if (q & 1) tmem_st32(at + 16 * (q - 1), pk);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&p_full[b]);
+        }
+        s_inv[tid] = m == -INFINITY ? 0.0f : 1.0f / l;
+        mbar_arrive(&fin);
+    } else {
+        regs_inc<kRegsSums>();
+        // ---------------- sums: thread = row
+        const int row = tid - 128, r = r0 + row;
+        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+        float acc[D];
+#pragma unroll
+        for (int c = 0; c < D; ++c) acc[c] = 0.0f;
+        for (int j = 0; j < n; ++j) {
+            const int b = j & 1;
+            ok = wait(&p_full[b], (j >> 1) & 1) && wait(&o_full[b], (j >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const float corr = s_corr[b][row];
+#pragma unroll
+            for (int q = 0; q < D / 16; ++q) {
+                uint32_t v[16];
+                tmem_ld16(tmem + lane_base + kColO + b * D + 16 * q, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 16; ++c) acc[16 * q + c] = fmaf(acc[16 * q + c], corr, __uint_as_float(v[c]));
+            }
+            tc_fence_before();
+            mbar_arrive(&o_empty[b]);
+        }
+        ok = ok && wait(&fin, 0);  // the denominators, and the loaders' report of NaN
+        if (ok && s_nan && r < rows) {
+            // some V holds NaN (written as 0 above): the dims of the rows that see it are NaN
+            const int pos = first + r / A.group;
+            for (int tok = A.window > 0 ? max(pos - A.window + 1, 0) : 0; tok <= pos; ++tok) {
+                const int p = page_id(A.B, seq, tok >> A.B.page_shift, nullptr);
+                if (p < 0) continue;
+                const uint4* v = reinterpret_cast<const uint4*>(
+                    A.v_cache + ((((int64_t)p * A.kv_heads + head) << A.B.page_shift) + (tok & ((1 << A.B.page_shift) - 1))) * D);
+#pragma unroll
+                for (int u = 0; u < D / 16; ++u) {
+                    const uint4 w = __ldcg(v + u);
+                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        if (((x[k >> 2] >> (8 * (k & 3))) & 0x7Fu) == 0x7Fu) acc[16 * u + k] = __int_as_float(0x7FC00000);
+                }
+            }
+        }
+        if (ok && r < rows) {
+            const float inv = s_inv[row];
+            T* o = static_cast<T*>(A.out) + (int64_t)(start + r / A.group) * A.out_stride +
+                   (int64_t)(head * A.group + r % A.group) * D;
+#pragma unroll
+            for (int c = 0; c < D; c += 8) {
+                float y[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = inv == 0.0f && acc[c + k] == 0.0f ? 0.0f : acc[c + k] * inv;
+                Vec<T>::store(o + c, y);
+            }
+        }
+    }
+    if (!ok) {
+        s_abort = 1;
+        raise_flag(A.err_flag, Q4K_ERR_TIMEOUT);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+template <typename T, int D>
+cudaError_t launch_typed(const PromptParams& P, cudaStream_t stream) {
+    constexpr bool HL = sizeof(T) == 4;
+    // every CTA holds all of its SM's tensor memory: enough shared memory that one fits
+    const int smem = Layout<HL, D>::kBytes < 144 * 1024 ? 144 * 1024 : Layout<HL, D>::kBytes;
+    static bool set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!set[dev]) {
+        e = cudaFuncSetAttribute(attn_prompt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        set[dev] = true;
+    }
+    // an upper bound of the row tiles: a sequence's last one may be part filled
+    const int64_t items = ((int64_t)P.B.m * P.group / kRows + (P.B.m < P.B.batch ? P.B.m : P.B.batch)) * P.kv_heads;
+    if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)items);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_prompt_kernel<T, D>, P);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_prompt(const PagedBatch& B, const void* q, int dtype, int64_t q_stride, int q_heads,
+                                    int kv_heads, int head_dim, const uint8_t* k_cache, const uint8_t* v_cache,
+                                    const float* k_scale, const float* v_scale, int min_rows, float scale, int window,
+                                    void* out, int64_t out_stride, int* err_flag, cudaStream_t stream) {
+    PromptParams P{};
+    P.B = B; P.q = q; P.out = out; P.q_stride = q_stride; P.out_stride = out_stride;
+    P.k_cache = k_cache; P.v_cache = v_cache; P.k_scale = k_scale; P.v_scale = v_scale;
+    P.kv_heads = kv_heads; P.group = q_heads / kv_heads; P.window = window; P.min_rows = min_rows;
+    P.scale_log2 = (scale < 0.0f ? -scale : scale) * 1.44269504088896340736f;
+    P.sign = scale < 0.0f ? -1.0f : 1.0f;
+    P.err_flag = err_flag;
+    P.wait_ns = wait_limit_ns();
+    if (dtype == Q4K_F32)
+        return head_dim == 64 ? launch_typed<float, 64>(P, stream) : launch_typed<float, 128>(P, stream);
+    return head_dim == 64 ? launch_typed<__nv_bfloat16, 64>(P, stream) : launch_typed<__nv_bfloat16, 128>(P, stream);
+}
+
+}  // namespace q4k

@@ -47,7 +47,7 @@ cudaError_t launch_router(const float* x, const uint16_t* w, const float* bias, 
 int router_max_hidden();
 cudaError_t launch_rms_norm(const float* x, const uint16_t* w, int m, int hidden, float eps, float* out,
                             cudaStream_t stream);
-// The attention side (q4k_qkrope.cu, q4k_kv.cu, q4k_attn.cu); PagedBatch: q4k_paged.cuh.
+// The attention side (q4k_qkrope.cu, q4k_kv.cu, q4k_attn.cu, q4k_attn_tc.cu); PagedBatch: q4k_paged.cuh.
 struct PagedBatch;
 cudaError_t launch_norm_rope(const void* q, const void* k, int dtype, int out_dtype, int m, int q_heads, int kv_heads,
                              int head_dim, int64_t q_stride, int64_t k_stride, const uint16_t* w_q,
@@ -59,6 +59,10 @@ cudaError_t launch_kv_append(const PagedBatch& B, const void* k, const void* v, 
                              const double* inv_freq, int rot_dim, int rope_mode, uint8_t* k_cache, uint8_t* v_cache,
                              float* k_scale, float* v_scale, int* err_flag, cudaStream_t stream);
 size_t attn_workspace_bytes(int head_dim);
+cudaError_t launch_attention_prompt(const PagedBatch& B, const void* q, int dtype, int64_t q_stride, int q_heads,
+                                    int kv_heads, int head_dim, const uint8_t* k_cache, const uint8_t* v_cache,
+                                    const float* k_scale, const float* v_scale, int min_rows, float scale, int window,
+                                    void* out, int64_t out_stride, int* err_flag, cudaStream_t stream);
 cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int64_t q_stride, int q_heads, int kv_heads,
                              int head_dim, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
                              const float* v_scale, int max_q_len, int max_len, float scale, int window, void* out,

@@ -179,7 +179,18 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// The same issued by one lane that elect.sync picks among the warp's 32 lanes: the whole warp
+// A and B from shared memory, issued by one elected lane of the warp.
+__device__ __forceinline__ void mma_f16_ss_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .pred p;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// A from tensor memory: the same issued by one lane that elect.sync picks among the warp's 32 lanes: the whole warp
 // runs the issuing loop, so its operands stay warp-uniform (no per-instruction transfer of a
 // lone thread's registers), and each instruction is issued once.
 __device__ __forceinline__ void mma_f16_ts_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -223,6 +234,13 @@ __device__ __forceinline__ uint64_t desc_sw128_kmajor(uint32_t smem_addr) {
     d |= (uint64_t)2 << 61;                        // 128-byte swizzle
     return d;
 }
+
+// The same layout with the operand's M/N elements contiguous (a row of 64 of them per k): panels of 64
+// M/N elements `panel_bytes` apart, 8 k rows a 1024-byte group.
+__device__ __forceinline__ uint64_t desc_sw128_mnmajor(uint32_t smem_addr, uint32_t panel_bytes) {
+    return (desc_sw128_kmajor(smem_addr) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(panel_bytes >> 4) << 16);
+}
+constexpr uint32_t kIdescBMnMajor = 1u << 16;  // instruction descriptor: B's N elements contiguous
 
 }  // namespace sm100
 }  // namespace q4k
