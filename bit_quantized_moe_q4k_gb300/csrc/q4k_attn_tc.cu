@@ -83,6 +83,21 @@ __device__ __forceinline__ float log2_scale(float s) {  // exact for powers of t
     const float e = (float)((int)(b >> 23) - 127);
     return (b & 0x7FFFFFu) ? e + log2f(__uint_as_float((b & 0x7FFFFFu) | 0x3F800000u)) : e;
 }
+// Two fp32 operations in one instruction, each rounded to nearest.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return d;
+}
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
 // 16 codes to 16 halves; NaN codes become 0 and set *nan.
@@ -255,20 +270,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         // ---------------- cache to fp16 tiles. Order of the slots: K0, K1, V0, K2, V1, ..., V(n-1)
         constexpr int kUnits = D / 16, kPer = 128 / kUnits, kLoads = kToks / kPer;  // 16-byte reads of a row; rows of a read
         const int i = tid - 32 * kLoadWarp, sub = i / kUnits, chunk = i % kUnits;
-        auto page_of = [&](int j) {  // lanes 0-7: the page of each 16-token group of tile j
+        // lanes 0-7 hold the page of each 16-token group of a tile, and where the group's rows begin
+        auto page_of = [&](int j) {
             const int tok = kv0 + kToks * j + 16 * (lane & 7);
             return j < n && tok < kv_hi ? page_id(A.B, seq, tok >> A.B.page_shift, A.err_flag) : -1;
         };
-        auto fetch = [&](const uint8_t* cache, int j, int pid, uint4 (&r)[kLoads]) {
+        auto offset_of = [&](int j, int pid) {
+            const int tok = kv0 + kToks * j + 16 * (lane & 7);
+            return pid < 0 ? (int64_t)-1
+                           : ((((int64_t)pid * A.kv_heads + head) << A.B.page_shift) + (tok & ((1 << A.B.page_shift) - 1))) * D;
+        };
+        const uint8_t* k_at = A.k_cache + (sub & 15) * D + 16 * chunk;
+        const uint8_t* v_at = A.v_cache + (sub & 15) * D + 16 * chunk;
+        auto fetch = [&](const uint8_t* cache, int j, int64_t off, uint4 (&r)[kLoads]) {
+            const int left = kv_hi - (kv0 + kToks * j);  // tokens of the tile that are there
 #pragma unroll
             for (int x = 0; x < kLoads; ++x) {
-                const int in = x * kPer + sub, tok = kv0 + kToks * j + in;
-                const int p = __shfl_sync(0xffffffffu, pid, in >> 4);
+                const int in = x * kPer + sub;
+                const int64_t o = __shfl_sync(0xffffffffu, off, in >> 4);
                 r[x] = make_uint4(0, 0, 0, 0);
-                if (p >= 0 && tok < kv_hi)
-                    r[x] = __ldcg(reinterpret_cast<const uint4*>(
-                        cache + (((((int64_t)p * A.kv_heads + head) << A.B.page_shift) + (tok & ((1 << A.B.page_shift) - 1))) * D) +
-                        16 * chunk));
+                if (o >= 0 && in < left) r[x] = __ldcg(reinterpret_cast<const uint4*>(cache + o));
             }
         };
         int slot = 0, uses = 0;
@@ -318,28 +339,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             if (lane == 0) mbar_arrive(&meta_full[j % kMetaRing]);
         };
         if (n > 0) {
-            int p0 = page_of(0), p1 = page_of(1), p2 = page_of(2);
+            int p1 = page_of(0), p2 = page_of(1), p3 = page_of(2);
+            int64_t o1 = offset_of(0, p1), o2 = offset_of(1, p2);
             uint4 ra[kLoads], rb[kLoads];
             float ks, vs;
-            fetch(A.k_cache, 0, p0, ra);
-            scales_of(p0, &ks, &vs);
-            fetch(A.v_cache, 0, p0, rb);
-            ok = put(false, ra);
-            if (ok) note(0, p0, ks, vs);
-            fetch(A.k_cache, 1, p1, ra);
+            fetch(k_at, 0, o1, ra);
             scales_of(p1, &ks, &vs);
+            fetch(v_at, 0, o1, rb);
+            ok = put(false, ra);
+            if (ok) note(0, p1, ks, vs);
+            fetch(k_at, 1, o2, ra);
+            scales_of(p2, &ks, &vs);
+            // here and at each turn: ra K of tile j + 1 (page p2, offsets o2), rb V of tile j, p3 the page of j + 2
             for (int j = 0; j < n && ok; ++j) {
                 if (j + 1 < n) {
                     ok = put(false, ra);
                     if (!ok) break;
-                    note(j + 1, p1, ks, vs);
+                    note(j + 1, p2, ks, vs);
                 }
-                fetch(A.k_cache, j + 2, p2, ra);
+                o1 = o2;
+                p2 = p3;
+                o2 = offset_of(j + 2, p2);
+                fetch(k_at, j + 2, o2, ra);
                 scales_of(p2, &ks, &vs);
+                p3 = page_of(j + 3);
                 ok = put(true, rb);
-                fetch(A.v_cache, j + 1, p1, rb);
-                p1 = p2;
-                p2 = page_of(j + 3);
+                fetch(v_at, j + 1, o1, rb);
             }
         }
         if (nan) s_nan = 1;
@@ -421,26 +446,38 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             const int t0 = kv0 + kToks * j;
             const bool whole = meta.all_ok && t0 >= full_lo && t0 + kToks <= full_hi;
             const uint32_t at = tmem + lane_base + kColS + b * kToks;
-            auto seen = [&](int g, int c) {  // column 16 g + c
-                const int tok = t0 + 16 * g + c;
-                return meta.ok[g] && tok >= lo && tok < hi;
-            };
             float top = -INFINITY;
+            if (whole) {
+                uint32_t v[2][32];
+                tmem_ld32(at, v[0]);
 #pragma unroll
-            for (int q = 0; q < kToks / 32; ++q) {
-                uint32_t v[32];
-                tmem_ld32(at + 32 * q, v);
-                tmem_wait_ld();
+                for (int q = 0; q < kToks / 32; ++q) {
+                    tmem_wait_ld();
+                    if (q + 1 < kToks / 32) tmem_ld32(at + 32 * (q + 1), v[(q + 1) & 1]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int g = 2 * q + h;
+                    for (int h = 0; h < 2; ++h) {
+                        const int g = 2 * q + h;
+                        float x[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t* w = &v[q & 1][16 * h + 4 * c];
+                            x[c] = fmaxf(fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1])),
+                                         fmaxf(__uint_as_float(w[2]), __uint_as_float(w[3])));
+                        }
+                        top = fmaxf(top, fmaf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), crow * meta.ks[g], meta.ev[g]));
+                    }
+                }
+            } else {
+#pragma unroll 1
+                for (int g = 0; g < kGroups; ++g) {
+                    uint32_t v[16];
+                    tmem_ld16(at + 16 * g, v);
+                    tmem_wait_ld();
                     float x = -INFINITY;
-                    if (whole) {
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) x = fmaxf(x, __uint_as_float(v[16 * h + c]));
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) x = seen(g, c) ? fmaxf(x, __uint_as_float(v[16 * h + c])) : x;
+                    for (int c = 0; c < 16; ++c) {
+                        const int tok = t0 + 16 * g + c;
+                        if (meta.ok[g] && tok >= lo && tok < hi) x = fmaxf(x, __uint_as_float(v[c]));
                     }
                     if (x > -INFINITY) top = fmaxf(top, fmaf(x, crow * meta.ks[g], meta.ev[g]));
                 }
@@ -453,40 +490,48 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             if (j >= 2) ok = wait(&o_empty[b], ((j >> 1) - 1) & 1);
             if (!ok) break;
             s_corr[b][tid] = corr;
-            uint32_t pk[32];
+            // P over columns of S that have been read. One term: 8 columns for 16 tokens, packed; two: hi
+            // and lo of 32 tokens in the 32 columns of their S.
+            uint32_t v[2][32], pk[32];
+            tmem_ld32(at, v[0]);
 #pragma unroll
             for (int q = 0; q < kToks / 32; ++q) {
-                uint32_t v[32];
-                tmem_ld32(at + 32 * q, v);
                 tmem_wait_ld();
+                if (q + 1 < kToks / 32) tmem_ld32(at + 32 * (q + 1), v[(q + 1) & 1]);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int g = 2 * q + h;
                     const float c = crow * meta.ks[g], e = meta.ev[g] - (m_use - 7.0f);
-                    float p[16];
+                    float2 p[8];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        float x = fmaf(__uint_as_float(v[16 * h + k]), c, e);
-                        if (!whole && !seen(g, k)) x = -INFINITY;
-                        p[k] = ex2(x);
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t* w = &v[q & 1][16 * h + 2 * k];
+                        p[k] = fma2(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), make_float2(c, c), make_float2(e, e));
                     }
-                    float2 sum = make_float2(p[0], p[1]);
+                    if (!whole) {
+                        const int tok = t0 + 16 * g, from = meta.ok[g] ? lo - tok : 16, to = hi - tok;
 #pragma unroll
-                    for (int k = 2; k < 16; k += 2) { sum.x += p[k]; sum.y += p[k + 1]; }
+                        for (int k = 0; k < 8; ++k) {
+                            if (2 * k < from || 2 * k >= to) p[k].x = -INFINITY;
+                            if (2 * k + 1 < from || 2 * k + 1 >= to) p[k].y = -INFINITY;
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) p[k] = make_float2(ex2(p[k].x), ex2(p[k].y));
+                    const float2 sum = add2(add2(add2(p[0], p[1]), add2(p[2], p[3])), add2(add2(p[4], p[5]), add2(p[6], p[7])));
                     l = fmaf(sum.x + sum.y, meta.inv[g], l);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const __half2 hh = __floats2half2_rn(p[2 * k], p[2 * k + 1]);
+                        const __half2 hh = __floats2half2_rn(p[k].x, p[k].y);
                         if constexpr (HL) {
                             const float2 f = __half22float2(hh);
                             pk[8 * h + k] = h2_bits(hh);
-                            pk[16 + 8 * h + k] = h2_bits(__floats2half2_rn(p[2 * k] - f.x, p[2 * k + 1] - f.y));
+                            pk[16 + 8 * h + k] = h2_bits(__floats2half2_rn(p[k].x - f.x, p[k].y - f.y));
                         } else {
                             pk[16 * (q & 1) + 8 * h + k] = h2_bits(hh);
                         }
                     }
                 }
-                // over columns of S that have been read: 32 per step (two terms) or per two steps
                 if (HL) tmem_st32(at + 32 * q, pk);
                 else if (q & 1) tmem_st32(at + 16 * (q - 1), pk);
             }
@@ -501,22 +546,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         // ---------------- sums: thread = row
         const int row = tid - 128, r = r0 + row;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-        float acc[D];
+        float2 acc[D / 2];
 #pragma unroll
-        for (int c = 0; c < D; ++c) acc[c] = 0.0f;
+        for (int c = 0; c < D / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
         for (int j = 0; j < n; ++j) {
             const int b = j & 1;
             ok = wait(&p_full[b], (j >> 1) & 1) && wait(&o_full[b], (j >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
             const float corr = s_corr[b][row];
+            const uint32_t at = tmem + lane_base + kColO + b * D;
+            uint32_t v[2][16];
+            tmem_ld16(at, v[0]);
 #pragma unroll
             for (int q = 0; q < D / 16; ++q) {
-                uint32_t v[16];
-                tmem_ld16(tmem + lane_base + kColO + b * D + 16 * q, v);
                 tmem_wait_ld();
+                if (q + 1 < D / 16) tmem_ld16(at + 16 * (q + 1), v[(q + 1) & 1]);
 #pragma unroll
-                for (int c = 0; c < 16; ++c) acc[16 * q + c] = fmaf(acc[16 * q + c], corr, __uint_as_float(v[c]));
+                for (int c = 0; c < 8; ++c)
+                    acc[8 * q + c] = fma2(acc[8 * q + c], make_float2(corr, corr),
+                                          make_float2(__uint_as_float(v[q & 1][2 * c]), __uint_as_float(v[q & 1][2 * c + 1])));
             }
             tc_fence_before();
             mbar_arrive(&o_empty[b]);
@@ -536,7 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
-                        if (((x[k >> 2] >> (8 * (k & 3))) & 0x7Fu) == 0x7Fu) acc[16 * u + k] = __int_as_float(0x7FC00000);
+                        if (((x[k >> 2] >> (8 * (k & 3))) & 0x7Fu) == 0x7Fu)
+                            (k & 1 ? acc[8 * u + k / 2].y : acc[8 * u + k / 2].x) = __int_as_float(0x7FC00000);
                 }
             }
         }
@@ -548,7 +598,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             for (int c = 0; c < D; c += 8) {
                 float y[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = inv == 0.0f && acc[c + k] == 0.0f ? 0.0f : acc[c + k] * inv;
+                for (int k = 0; k < 8; ++k) {
+                    const float x = k & 1 ? acc[(c + k) / 2].y : acc[(c + k) / 2].x;
+                    y[k] = x * inv;  // a row that sees nothing: 0 * 0
+                }
                 Vec<T>::store(o + c, y);
             }
         }
