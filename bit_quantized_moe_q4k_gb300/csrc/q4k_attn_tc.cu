@@ -16,8 +16,9 @@
 // correction costs nothing more there.
 //
 // Roles: warps 0-3 softmax (thread = row), 4-7 the sums (thread = row) and the store, 8-11 read the
-// cache and write fp16 tiles, warp 12 issues the products (13-15 idle). Every wait is bounded; an abort flag
-// lets all roles leave together.
+// cache and write fp16 tiles, warp 12 issues the products, warp 13 looks the pages and scales up (14-15
+// idle). Every wait is bounded; an abort flag lets all roles leave together. The loops are kept
+// short: four roles share a scheduler, and unrolled further they waited for instructions.
 //
 // Bound by shared memory and the tensor core together: a tile of 128 x 128 x 128 takes 512 cycles for
 // each product, reads 96 KB of operands and writes 64 KB of converted K and V at 128 bytes a cycle.
@@ -33,7 +34,7 @@ constexpr int kRows = 128;   // query rows of a CTA
 constexpr int kToks = 128;   // tokens of a tile
 constexpr int kGroups = kToks / 16;
 constexpr int kThreads = 512;
-constexpr int kLoadWarp = 8, kMmaWarp = 12;
+constexpr int kLoadWarp = 8, kMmaWarp = 12, kPageWarp = 13;
 // Registers a thread of each warpgroup after the split; their sum is four times what the launch gives.
 constexpr int kRegsSoftmax = 152, kRegsSums = 184, kRegsLoad = 104, kRegsMma = 72;
 static_assert(kRegsSoftmax + kRegsSums + kRegsLoad + kRegsMma <= 4 * (65536 / kThreads), "register split");
@@ -54,10 +55,11 @@ struct PromptParams {
     uint64_t wait_ns;
 };
 
-// What the softmax needs of a tile's 16-token groups.
+// A tile's 16-token groups: where their rows begin in the cache (-1: no such page), K's scale, V's as
+// log2 and reciprocal.
 struct TileMeta {
+    int64_t at[kGroups];
     float ks[kGroups], ev[kGroups], inv[kGroups];
-    int ok[kGroups];
     int all_ok;
 };
 
@@ -100,25 +102,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
-// 16 codes to 16 halves; NaN codes become 0 and set *nan.
-template <bool CLEAN>
-__device__ __forceinline__ void expand16(const uint4& c, uint32_t (&h)[8], bool* nan) {
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) e4m3x4_to_f16x4(w[i], &h[2 * i], &h[2 * i + 1]);
-    if (CLEAN) {
-        __half2 acc = __float2half2_rn(0.0f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc = __hfma2(*reinterpret_cast<const __half2*>(&h[i]), __float2half2_rn(0.0f), acc);
-        if (__hisnan(__low2half(acc)) || __hisnan(__high2half(acc))) {
-            *nan = true;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if ((h[i] & 0x7FFFu) > 0x7C00u) h[i] &= 0xFFFF0000u;
-                if ((h[i] & 0x7FFF0000u) > 0x7C000000u) h[i] &= 0x0000FFFFu;
-            }
-        }
-    }
+// 16 codes to 16 halves.
+__device__ __forceinline__ void expand16(const uint4& c, uint32_t (&h)[8]) {
+    e4m3x4_to_f16x4(c.x, &h[0], &h[1]);
+    e4m3x4_to_f16x4(c.y, &h[2], &h[3]);
+    e4m3x4_to_f16x4(c.z, &h[4], &h[5]);
+    e4m3x4_to_f16x4(c.w, &h[6], &h[7]);
 }
 
 template <typename T, int D>
@@ -130,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* s_q = smem;
     uint8_t* s_kv = smem + L::kQ;
-    __shared__ __align__(8) uint64_t full[L::kSlots], empty[L::kSlots], meta_full[kMetaRing];
+    __shared__ __align__(8) uint64_t full[L::kSlots], empty[L::kSlots], meta_full[kMetaRing], meta_empty[kMetaRing];
     __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], fin, drain;
     __shared__ TileMeta s_meta[kMetaRing];
     __shared__ float s_c[kRows], s_corr[2][kRows], s_inv[kRows];
@@ -185,7 +174,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             mbar_init(&full[i], 128);
             mbar_init(&empty[i], 1);
         }
-        for (int i = 0; i < kMetaRing; ++i) mbar_init(&meta_full[i], 1);
+        for (int i = 0; i < kMetaRing; ++i) {
+            mbar_init(&meta_full[i], 1);
+            mbar_init(&meta_empty[i], 8);  // the warps of the softmax and of the loaders
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 128);
@@ -267,104 +259,80 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
 
     if (warp >= kLoadWarp && warp < kMmaWarp) {
         regs_dec<kRegsLoad>();
-        // ---------------- cache to fp16 tiles. Order of the slots: K0, K1, V0, K2, V1, ..., V(n-1)
-        constexpr int kUnits = D / 16, kPer = 128 / kUnits, kLoads = kToks / kPer;  // 16-byte reads of a row; rows of a read
-        const int i = tid - 32 * kLoadWarp, sub = i / kUnits, chunk = i % kUnits;
-        // lanes 0-7 hold the page of each 16-token group of a tile, and where the group's rows begin
-        auto page_of = [&](int j) {
-            const int tok = kv0 + kToks * j + 16 * (lane & 7);
-            return j < n && tok < kv_hi ? page_id(A.B, seq, tok >> A.B.page_shift, A.err_flag) : -1;
-        };
-        auto offset_of = [&](int j, int pid) {
-            const int tok = kv0 + kToks * j + 16 * (lane & 7);
-            return pid < 0 ? (int64_t)-1
-                           : ((((int64_t)pid * A.kv_heads + head) << A.B.page_shift) + (tok & ((1 << A.B.page_shift) - 1))) * D;
-        };
-        const uint8_t* k_at = A.k_cache + (sub & 15) * D + 16 * chunk;
-        const uint8_t* v_at = A.v_cache + (sub & 15) * D + 16 * chunk;
-        auto fetch = [&](const uint8_t* cache, int j, int64_t off, uint4 (&r)[kLoads]) {
+        // ---------------- cache to fp16 tiles. Order of the slots: K0, K1, V0, K2, V1, ..., V(n-1). A thread
+        // reads 16 codes of rows 32 x + rs, in each 64-dim panel, and writes them as two 16-byte units of the
+        // panel's 128-byte rows; the eight threads of a store's phase hold two rows of different parity,
+        // so their units lie on different banks.
+        constexpr int kPanels = D / 64, kLoads = 4 * kPanels;
+        const int i = tid - 32 * kLoadWarp, rs = i >> 2, c = i & 3;
+        const uint8_t* k_at = A.k_cache + (rs & 15) * D + 16 * c;
+        const uint8_t* v_at = A.v_cache + (rs & 15) * D + 16 * c;
+        auto fetch = [&](const uint8_t* cache, int j, uint4 (&r)[kLoads]) {
             const int left = kv_hi - (kv0 + kToks * j);  // tokens of the tile that are there
 #pragma unroll
-            for (int x = 0; x < kLoads; ++x) {
-                const int in = x * kPer + sub;
-                const int64_t o = __shfl_sync(0xffffffffu, off, in >> 4);
-                r[x] = make_uint4(0, 0, 0, 0);
-                if (o >= 0 && in < left) r[x] = __ldcg(reinterpret_cast<const uint4*>(cache + o));
+            for (int x = 0; x < 4; ++x) {
+                const int64_t at = s_meta[j % kMetaRing].at[2 * x + (rs >> 4)];
+                const bool there = at >= 0 && 32 * x + rs < left;
+#pragma unroll
+                for (int p = 0; p < kPanels; ++p) {
+                    r[x * kPanels + p] = make_uint4(0, 0, 0, 0);
+                    if (there) r[x * kPanels + p] = __ldcg(reinterpret_cast<const uint4*>(cache + at + 64 * p));
+                }
             }
         };
         int slot = 0, uses = 0;
         bool nan = false;
+        uint8_t* const dst = s_kv + rs * 128 + (((2 * c) ^ (rs & 7)) << 4);
         auto put = [&](bool v_side, const uint4 (&r)[kLoads]) {
             if (!wait(&empty[slot], (uses & 1) ^ 1)) return false;
-            // 16 dims are two 16-byte units of the row's 128-byte panel line; lanes of the second panel
-            // write them in the other order, which keeps a store's lanes on different banks
-            uint8_t* base = s_kv + slot * L::kTile + (chunk >> 2) * (kToks * 128);
-            const int flip = (chunk >> 2) & 1;
+            uint8_t* base = dst + slot * L::kTile;
+            uint8_t* base1 = s_kv + slot * L::kTile + rs * 128 + (((2 * c + 1) ^ (rs & 7)) << 4);
+            __half2 acc[2] = {__float2half2_rn(0.0f), __float2half2_rn(0.0f)};
 #pragma unroll
             for (int x = 0; x < kLoads; ++x) {
-                const int row = x * kPer + sub;
                 uint32_t h[8];
-                if (v_side) expand16<true>(r[x], h, &nan);
-                else expand16<false>(r[x], h, &nan);
-                const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
-                const int u = 2 * (chunk & 3);
-                *reinterpret_cast<uint4*>(base + row * 128 + (((u + flip) ^ (row & 7)) << 4)) = flip ? b : a;
-                *reinterpret_cast<uint4*>(base + row * 128 + (((u + 1 - flip) ^ (row & 7)) << 4)) = flip ? a : b;
+                expand16(r[x], h);
+                if (v_side) {  // 0 * NaN: NaN if any of them is
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        acc[k & 1] = __hfma2(*reinterpret_cast<const __half2*>(&h[k]), __float2half2_rn(0.0f), acc[k & 1]);
+                }
+                const int off = (x % kPanels) * (kToks * 128) + (x / kPanels) * (32 * 128);
+                *reinterpret_cast<uint4*>(base + off) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(base1 + off) = make_uint4(h[4], h[5], h[6], h[7]);
+            }
+            if (v_side) {
+                const __half2 a = __hadd2(acc[0], acc[1]);
+                if (__hisnan(__low2half(a)) || __hisnan(__high2half(a))) {  // written again with 0 in NaN's place
+                    nan = true;
+#pragma unroll 1
+                    for (int x = 0; x < kLoads; ++x) {
+                        const int off = (x % kPanels) * (kToks * 128) + (x / kPanels) * (32 * 128);
+#pragma unroll 1
+                        for (int k = 0; k < 16; ++k) {
+                            uint16_t* w = reinterpret_cast<uint16_t*>((k < 8 ? base : base1) + off) + (k & 7);
+                            if ((*w & 0x7FFFu) > 0x7C00u) *w = 0;
+                        }
+                    }
+                }
             }
             fence_proxy_async_smem();
             mbar_arrive(&full[slot]);
             if (++slot == L::kSlots) { slot = 0; ++uses; }
             return true;
         };
-        auto scales_of = [&](int pid, float* ks, float* vs) {
-            *ks = *vs = 1.0f;
-            if (pid >= 0) {
-                *ks = __ldcg(A.k_scale + (int64_t)pid * A.kv_heads + head);
-                *vs = __ldcg(A.v_scale + (int64_t)pid * A.kv_heads + head);
+        uint4 ra[kLoads], rb[kLoads];  // K of tile j + 1, V of tile j
+#pragma unroll 1
+        for (int j = -2; j < n && ok && n > 0; ++j) {
+            if (j + 1 >= 0 && j + 1 < n) ok = put(false, ra);
+            if (ok && j + 2 < n) {
+                ok = wait(&meta_full[(j + 2) % kMetaRing], ((j + 2) / kMetaRing) & 1);
+                if (ok) fetch(k_at, j + 2, ra);
             }
-        };
-        auto note = [&](int j, int pid, float ks, float vs) {  // the tile's scales, by the first loading warp
-            if (warp != kLoadWarp) return;
-            const bool good = pid >= 0 || kv0 + kToks * j + 16 * (lane & 7) >= kv_hi;  // past the end: masked anyway
-            const bool all = __all_sync(0xffffffffu, good);
-            TileMeta& m = s_meta[j % kMetaRing];
-            if (lane < kGroups) {
-                m.ks[lane] = ks;
-                m.ev[lane] = log2_scale(vs);
-                m.inv[lane] = 1.0f / vs;
-                m.ok[lane] = pid >= 0;
-            }
-            if (lane == 0) m.all_ok = all;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&meta_full[j % kMetaRing]);
-        };
-        if (n > 0) {
-            int p1 = page_of(0), p2 = page_of(1), p3 = page_of(2);
-            int64_t o1 = offset_of(0, p1), o2 = offset_of(1, p2);
-            uint4 ra[kLoads], rb[kLoads];
-            float ks, vs;
-            fetch(k_at, 0, o1, ra);
-            scales_of(p1, &ks, &vs);
-            fetch(v_at, 0, o1, rb);
-            ok = put(false, ra);
-            if (ok) note(0, p1, ks, vs);
-            fetch(k_at, 1, o2, ra);
-            scales_of(p2, &ks, &vs);
-            // here and at each turn: ra K of tile j + 1 (page p2, offsets o2), rb V of tile j, p3 the page of j + 2
-            for (int j = 0; j < n && ok; ++j) {
-                if (j + 1 < n) {
-                    ok = put(false, ra);
-                    if (!ok) break;
-                    note(j + 1, p2, ks, vs);
-                }
-                o1 = o2;
-                p2 = p3;
-                o2 = offset_of(j + 2, p2);
-                fetch(k_at, j + 2, o2, ra);
-                scales_of(p2, &ks, &vs);
-                p3 = page_of(j + 3);
-                ok = put(true, rb);
-                fetch(v_at, j + 1, o1, rb);
+            if (ok && j >= 0) ok = put(true, rb);
+            if (ok && j + 1 >= 0 && j + 1 < n) {
+                fetch(v_at, j + 1, rb);
+                if (lane == 0) mbar_arrive(&meta_empty[(j + 1) % kMetaRing]);
             }
         }
         if (nan) s_nan = 1;
@@ -400,9 +368,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             next_slot();
             return true;
         };
-        if (n > 0) ok = scores(0);
-        for (int j = 0; j < n && ok; ++j) {
+#pragma unroll 1
+        for (int j = -1; j < n && ok; ++j) {
             if (j + 1 < n && !(ok = scores(j + 1))) break;
+            if (j < 0) continue;
             // P of these tokens (o_empty of the tile two before is implied: the softmax waited for it)
             ok = wait(&p_full[j & 1], (j >> 1) & 1) && wait(&full[slot], uses & 1);
             if (!ok) break;
@@ -426,6 +395,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             mbar_wait(&drain, 0, &never);
         }
         __syncwarp();
+        } else if (warp == kPageWarp) {
+            // ---------------- pages and scales, up to kMetaRing tiles ahead
+            auto page_of = [&](int j) {  // lanes 0-7: the page of each 16-token group
+                const int tok = kv0 + kToks * j + 16 * lane;
+                return lane < kGroups && j < n && tok < kv_hi ? page_id(A.B, seq, tok >> A.B.page_shift, A.err_flag) : -1;
+            };
+            int next = page_of(0);
+#pragma unroll 1
+            for (int j = 0; j < n && ok; ++j) {
+                const int pid = next, tok = kv0 + kToks * j + 16 * lane;
+                next = page_of(j + 1);
+                const int64_t ph = (int64_t)pid * A.kv_heads + head;
+                float ks = 1.0f, vs = 1.0f;
+                if (pid >= 0) {
+                    ks = __ldcg(A.k_scale + ph);
+                    vs = __ldcg(A.v_scale + ph);
+                }
+                const bool all = __all_sync(0xffffffffu, lane >= kGroups || pid >= 0 || tok >= kv_hi);
+                ok = wait(&meta_empty[j % kMetaRing], ((j / kMetaRing) & 1) ^ 1);
+                if (!ok) break;
+                TileMeta& m = s_meta[j % kMetaRing];
+                if (lane < kGroups) {
+                    m.at[lane] = pid < 0 ? (int64_t)-1 : ((ph << A.B.page_shift) + (tok & ((1 << A.B.page_shift) - 1))) * D;
+                    m.ks[lane] = ks;
+                    m.ev[lane] = log2_scale(vs);
+                    m.inv[lane] = 1.0f / vs;
+                }
+                if (lane == 0) m.all_ok = all;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&meta_full[j % kMetaRing]);
+            }
         }
     } else if (warp < 4) {
         regs_inc<kRegsSoftmax>();
@@ -437,6 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         const float crow = s_c[tid];
         const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
         float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
         for (int j = 0; j < n; ++j) {
             const int b = j & 1;
             ok = wait(&meta_full[j % kMetaRing], (j / kMetaRing) & 1) && wait(&s_full[b], (j >> 1) & 1);
@@ -448,19 +449,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             const uint32_t at = tmem + lane_base + kColS + b * kToks;
             float top = -INFINITY;
             if (whole) {
-                uint32_t v[2][32];
-                tmem_ld32(at, v[0]);
-#pragma unroll
-                for (int q = 0; q < kToks / 32; ++q) {
+#pragma unroll 1
+                for (int q = 0; q < kToks / 32; q += 2) {
+                    uint32_t v[2][32];
+                    tmem_ld32(at + 32 * q, v[0]);
+                    tmem_ld32(at + 32 * q + 32, v[1]);
                     tmem_wait_ld();
-                    if (q + 1 < kToks / 32) tmem_ld32(at + 32 * (q + 1), v[(q + 1) & 1]);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    for (int h = 0; h < 4; ++h) {
                         const int g = 2 * q + h;
                         float x[4];
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            const uint32_t* w = &v[q & 1][16 * h + 4 * c];
+                            const uint32_t* w = &v[h >> 1][16 * (h & 1) + 4 * c];
                             x[c] = fmaxf(fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1])),
                                          fmaxf(__uint_as_float(w[2]), __uint_as_float(w[3])));
                         }
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
                         const int tok = t0 + 16 * g + c;
-                        if (meta.ok[g] && tok >= lo && tok < hi) x = fmaxf(x, __uint_as_float(v[c]));
+                        if (meta.at[g] >= 0 && tok >= lo && tok < hi) x = fmaxf(x, __uint_as_float(v[c]));
                     }
                     if (x > -INFINITY) top = fmaxf(top, fmaf(x, crow * meta.ks[g], meta.ev[g]));
                 }
@@ -492,49 +493,54 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             s_corr[b][tid] = corr;
             // P over columns of S that have been read. One term: 8 columns for 16 tokens, packed; two: hi
             // and lo of 32 tokens in the 32 columns of their S.
-            uint32_t v[2][32], pk[32];
-            tmem_ld32(at, v[0]);
-#pragma unroll
-            for (int q = 0; q < kToks / 32; ++q) {
+#pragma unroll 1
+            for (int q0 = 0; q0 < kToks / 32; q0 += 2) {
+                uint32_t v[2][32], pk[32];
+                tmem_ld32(at + 32 * q0, v[0]);
                 tmem_wait_ld();
-                if (q + 1 < kToks / 32) tmem_ld32(at + 32 * (q + 1), v[(q + 1) & 1]);
+                tmem_ld32(at + 32 * q0 + 32, v[1]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int g = 2 * q + h;
-                    const float c = crow * meta.ks[g], e = meta.ev[g] - (m_use - 7.0f);
-                    float2 p[8];
+                for (int q = 0; q < 2; ++q) {
+                    if (q) tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t* w = &v[q & 1][16 * h + 2 * k];
-                        p[k] = fma2(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), make_float2(c, c), make_float2(e, e));
-                    }
-                    if (!whole) {
-                        const int tok = t0 + 16 * g, from = meta.ok[g] ? lo - tok : 16, to = hi - tok;
+                    for (int h = 0; h < 2; ++h) {
+                        const int g = 2 * (q0 + q) + h;
+                        const float c = crow * meta.ks[g], e = meta.ev[g] - (m_use - 7.0f);
+                        float2 p[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            if (2 * k < from || 2 * k >= to) p[k].x = -INFINITY;
-                            if (2 * k + 1 < from || 2 * k + 1 >= to) p[k].y = -INFINITY;
+                            const uint32_t* w = &v[q][16 * h + 2 * k];
+                            p[k] = fma2(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), make_float2(c, c), make_float2(e, e));
+                        }
+                        if (!whole) {
+                            const int tok = t0 + 16 * g, from = meta.at[g] >= 0 ? lo - tok : 16, to = hi - tok;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                if (2 * k < from || 2 * k >= to) p[k].x = -INFINITY;
+                                if (2 * k + 1 < from || 2 * k + 1 >= to) p[k].y = -INFINITY;
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) p[k] = make_float2(ex2(p[k].x), ex2(p[k].y));
+                        const float2 sum = add2(add2(add2(p[0], p[1]), add2(p[2], p[3])), add2(add2(p[4], p[5]), add2(p[6], p[7])));
+                        l = fmaf(sum.x + sum.y, meta.inv[g], l);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const __half2 hh = __floats2half2_rn(p[k].x, p[k].y);
+                            if constexpr (HL) {
+                                const float2 f = __half22float2(hh);
+                                pk[8 * h + k] = h2_bits(hh);
+                                pk[16 + 8 * h + k] = h2_bits(__floats2half2_rn(p[k].x - f.x, p[k].y - f.y));
+                            } else {
+                                pk[16 * q + 8 * h + k] = h2_bits(hh);
+                            }
                         }
                     }
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) p[k] = make_float2(ex2(p[k].x), ex2(p[k].y));
-                    const float2 sum = add2(add2(add2(p[0], p[1]), add2(p[2], p[3])), add2(add2(p[4], p[5]), add2(p[6], p[7])));
-                    l = fmaf(sum.x + sum.y, meta.inv[g], l);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const __half2 hh = __floats2half2_rn(p[k].x, p[k].y);
-                        if constexpr (HL) {
-                            const float2 f = __half22float2(hh);
-                            pk[8 * h + k] = h2_bits(hh);
-                            pk[16 + 8 * h + k] = h2_bits(__floats2half2_rn(p[k].x - f.x, p[k].y - f.y));
-                        } else {
-                            pk[16 * (q & 1) + 8 * h + k] = h2_bits(hh);
-                        }
-                    }
+                    if (HL) tmem_st32(at + 32 * (q0 + q), pk);
+                    else if (q) tmem_st32(at + 16 * q0, pk);
                 }
-                if (HL) tmem_st32(at + 32 * q, pk);
-                else if (q & 1) tmem_st32(at + 16 * (q - 1), pk);
             }
+            if (lane == 0) mbar_arrive(&meta_empty[j % kMetaRing]);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&p_full[b]);
@@ -549,6 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         float2 acc[D / 2];
 #pragma unroll
         for (int c = 0; c < D / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
+#pragma unroll 1
         for (int j = 0; j < n; ++j) {
             const int b = j & 1;
             ok = wait(&p_full[b], (j >> 1) & 1) && wait(&o_full[b], (j >> 1) & 1);
