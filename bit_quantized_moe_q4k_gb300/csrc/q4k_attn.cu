@@ -649,10 +649,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
             if (whole) {
                 const int row = tile * RT + r;
                 if (row < rows) {
-                    // a row that sees nothing has m = -inf: zero
-                    const float iv = m == -INFINITY ? 0.0f : 1.0f / den;
-                    const float y[4] = {m == -INFINITY ? 0.0f : acc.x * iv, m == -INFINITY ? 0.0f : acc.y * iv,
-                                        m == -INFINITY ? 0.0f : acc.z * iv, m == -INFINITY ? 0.0f : acc.w * iv};
+                    const float iv = den == 0.0f ? 0.0f : 1.0f / den;  // 0: the row sees nothing
+                    const float y[4] = {acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv};
                     Vec<T>::store(static_cast<T*>(A.out) + (int64_t)(sp.start + row / A.group) * A.out_stride +
                                       (int64_t)(head * A.group + row % A.group) * D + c,
                                   y);
@@ -753,7 +751,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
                      (int64_t)(head * A.group + row % A.group) * D + lane;
 #pragma unroll
             for (int c = 0; c < kCols; ++c) {
-                const float y = m == -INFINITY ? 0.0f : acc[c] / den;
+                const float y = den == 0.0f ? 0.0f : acc[c] / den;  // 0: the row sees nothing
                 if constexpr (sizeof(T) == 4) out[32 * c] = y;
                 else out[32 * c] = __float2bfloat16_rn(y);
             }

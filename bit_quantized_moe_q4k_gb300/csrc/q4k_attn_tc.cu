@@ -110,6 +110,264 @@ __device__ __forceinline__ void expand16(const uint4& c, uint32_t (&h)[8]) {
     e4m3x4_to_f16x4(c.w, &h[6], &h[7]);
 }
 
+// The block's item: sequence, row tile * kv_heads + kv head, its first row, new tokens and length; -1 past
+// the last. Items are taken from the last row tile of the last sequence down, so the longest come first.
+__device__ __forceinline__ void find_item(const PromptParams& A, int tile_rows, int* item) {
+    const int lane = threadIdx.x & 31;
+    int at = blockIdx.x;
+    for (int top = A.B.batch; top > 0; top -= 32) {
+        const int i = top - 1 - lane;  // lane 0: the last sequence
+        SeqSpan s{0, 0, 0};
+        int n = 0;
+        if (i >= 0) {
+            bool bad;
+            s = seq_span(A.B, i, &bad);
+            if (bad) raise_flag(A.err_flag, Q4K_ERR_SEQ);
+            const int rows = s.n * A.group;
+            if (rows >= A.min_rows) n = (rows + tile_rows - 1) / tile_rows * A.kv_heads;
+        }
+        int inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += x;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, at < inc);
+        if (hit) {
+            if (lane == __ffs(hit) - 1) {
+                item[0] = i;
+                item[1] = n - 1 - (at - (inc - n));
+                item[2] = s.start;
+                item[3] = s.n;
+                item[4] = s.len;
+            }
+            return;
+        }
+        at -= __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) item[0] = -1;
+}
+
+// A wait of a whole warp, bounded in time: its lanes go on, or give up, together.
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+    bool done = mbar_try_wait(bar, parity);
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !done; ++i) {
+        if (*abort) break;
+        if ((i & 63) == 0) {  // the limit is looked at every 64 tries
+            const uint64_t t = global_timer_ns();
+            if (t0 == 0) t0 = t;
+            else if (t - t0 > limit_ns) break;
+        }
+        done = mbar_try_wait(bar, parity);
+    }
+    return __all_sync(0xffffffffu, done) != 0;
+}
+
+// Expands half tiles (64 rows) of the cache. A thread reads 16 codes of rows 32 x + rs, in each 64-dim panel,
+// and writes them as two 16-byte units of the panel's 128-byte rows; the eight threads of a store's phase
+// hold two rows of different parity, so their units lie on different banks.
+template <int D>
+struct Loader {
+    static constexpr int kPanels = D / 64, kLoads = 2 * kPanels;
+    const uint8_t* cache;
+    int rs;
+    uint32_t u0, u1;
+    __device__ __forceinline__ Loader(const uint8_t* codes, int i) : rs(i >> 2) {
+        const int c = i & 3;
+        cache = codes + (rs & 15) * D + 16 * c;
+        u0 = rs * 128 + (((2 * c) ^ (rs & 7)) << 4);
+        u1 = rs * 128 + (((2 * c + 1) ^ (rs & 7)) << 4);
+    }
+    // left: tokens of the tile that are there
+    __device__ __forceinline__ void fetch(const TileMeta& meta, int half, int left, uint4 (&r)[kLoads], int64_t side = 0) const {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int64_t at = meta.at[4 * half + 2 * x + (rs >> 4)];
+            const bool there = at >= 0 && 64 * half + 32 * x + rs < left;
+#pragma unroll
+            for (int p = 0; p < kPanels; ++p) {
+                r[x * kPanels + p] = make_uint4(0, 0, 0, 0);
+                if (there) r[x * kPanels + p] = __ldcg(reinterpret_cast<const uint4*>(cache + side + at + 64 * p));
+            }
+        }
+    }
+    // NaN on V's side is written as 0 (0 * NaN would reach rows that do not see it) and reported.
+    __device__ __forceinline__ void put(uint8_t* base, bool v_side, const uint4 (&r)[kLoads], bool* nan) const {
+        __half2 acc[2] = {__float2half2_rn(0.0f), __float2half2_rn(0.0f)};
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) {
+            uint32_t h[8];
+            expand16(r[x], h);
+            if (v_side) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)  // 0 * NaN: NaN if any of them is
+                    acc[k & 1] = __hfma2(*reinterpret_cast<const __half2*>(&h[k]), __float2half2_rn(0.0f), acc[k & 1]);
+            }
+            const int off = (x % kPanels) * (kToks * 128) + (x / kPanels) * (32 * 128);
+            *reinterpret_cast<uint4*>(base + u0 + off) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(base + u1 + off) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        const __half2 a = __hadd2(acc[0], acc[1]);
+        if (v_side && (__hisnan(__low2half(a)) || __hisnan(__high2half(a)))) {  // written again with 0 in NaN's place
+            *nan = true;
+#pragma unroll 1
+            for (int x = 0; x < kLoads; ++x) {
+                const int off = (x % kPanels) * (kToks * 128) + (x / kPanels) * (32 * 128);
+#pragma unroll 1
+                for (int k = 0; k < 16; ++k) {
+                    uint16_t* w = reinterpret_cast<uint16_t*>(base + (k < 8 ? u0 : u1) + off) + (k & 7);
+                    if ((*w & 0x7FFFu) > 0x7C00u) *w = 0;
+                }
+            }
+        }
+    }
+};
+
+// The page warp: pages and scales of the tiles, up to kMetaRing ahead.
+template <int D>
+__device__ __forceinline__ bool page_ahead(const PromptParams& A, int seq, int head, int kv0, int kv_hi, int n, TileMeta* metas,
+                                           uint64_t* meta_full, uint64_t* meta_empty, volatile int* abort) {
+    const int lane = threadIdx.x & 31;
+    auto page_of = [&](int j) {  // lanes 0-7: the page of each 16-token group
+        const int tok = kv0 + kToks * j + 16 * lane;
+        return lane < kGroups && j < n && tok < kv_hi ? page_id(A.B, seq, tok >> A.B.page_shift, A.err_flag) : -1;
+    };
+    int next = page_of(0);
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+        const int pid = next, tok = kv0 + kToks * j + 16 * lane;
+        next = page_of(j + 1);
+        const int64_t ph = (int64_t)pid * A.kv_heads + head;
+        float ks = 1.0f, vs = 1.0f;
+        if (pid >= 0) {
+            ks = __ldcg(A.k_scale + ph);
+            vs = __ldcg(A.v_scale + ph);
+        }
+        const bool all = __all_sync(0xffffffffu, lane >= kGroups || pid >= 0 || tok >= kv_hi);
+        if (!wait_all(&meta_empty[j % kMetaRing], ((j / kMetaRing) & 1) ^ 1, abort, A.wait_ns)) return false;
+        TileMeta& m = metas[j % kMetaRing];
+        if (lane < kGroups) {
+            m.at[lane] = pid < 0 ? (int64_t)-1 : ((ph << A.B.page_shift) + (tok & ((1 << A.B.page_shift) - 1))) * D;
+            m.ks[lane] = ks;
+            m.ev[lane] = log2_scale(vs);
+            m.inv[lane] = 1.0f / vs;
+        }
+        if (lane == 0) m.all_ok = all;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&meta_full[j % kMetaRing]);
+    }
+    return true;
+}
+
+// Largest x = c s + e of a row of S (tensor memory columns at ..): whole when the row sees every token.
+__device__ __forceinline__ float row_max(uint32_t at, const TileMeta& meta, float crow, int t0, int lo, int hi, bool whole) {
+    float top = -INFINITY;
+    if (whole) {
+#pragma unroll 1
+        for (int q = 0; q < kToks / 32; ++q) {
+            uint32_t v[32];
+            tmem_ld32(at + 32 * q, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int g = 2 * q + h;
+                float x[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t* w = &v[16 * h + 4 * c];
+                    x[c] = fmaxf(fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1])),
+                                 fmaxf(__uint_as_float(w[2]), __uint_as_float(w[3])));
+                }
+                top = fmaxf(top, fmaf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), crow * meta.ks[g], meta.ev[g]));
+            }
+        }
+        return top;
+    }
+#pragma unroll 1
+    for (int g = 0; g < kGroups; ++g) {
+        uint32_t v[16];
+        tmem_ld16(at + 16 * g, v);
+        tmem_wait_ld();
+        float x = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            const int tok = t0 + 16 * g + c;
+            if (meta.at[g] >= 0 && tok >= lo && tok < hi) x = fmaxf(x, __uint_as_float(v[c]));
+        }
+        if (x > -INFINITY) top = fmaxf(top, fmaf(x, crow * meta.ks[g], meta.ev[g]));
+    }
+    return top;
+}
+
+// P = 2^(x - ref + 7) of a row in the place of its S, and the row's share of the denominator. 32 tokens' P
+// take 16 columns of one fp16 term, or the 32 of their S for two, hi then lo: columns of S that have been read.
+template <bool HL>
+__device__ __forceinline__ float weights(uint32_t at, const TileMeta& meta, float crow, float ref, int t0, int lo, int hi,
+                                         bool whole) {
+    float l = 0.0f;
+#pragma unroll 1
+    for (int q = 0; q < kToks / 32; ++q) {
+        uint32_t v[32], pk[HL ? 32 : 16];
+        tmem_ld32(at + 32 * q, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int g = 2 * q + h;
+            const float c = crow * meta.ks[g], e = meta.ev[g] - (ref - 7.0f);
+            float2 p[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t* w = &v[16 * h + 2 * k];
+                p[k] = fma2(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), make_float2(c, c), make_float2(e, e));
+            }
+            if (!whole) {
+                const int tok = t0 + 16 * g, from = meta.at[g] >= 0 ? lo - tok : 16, to = hi - tok;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (2 * k < from || 2 * k >= to) p[k].x = -INFINITY;
+                    if (2 * k + 1 < from || 2 * k + 1 >= to) p[k].y = -INFINITY;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) p[k] = make_float2(ex2(p[k].x), ex2(p[k].y));
+            const float2 sum = add2(add2(add2(p[0], p[1]), add2(p[2], p[3])), add2(add2(p[4], p[5]), add2(p[6], p[7])));
+            l = fmaf(sum.x + sum.y, meta.inv[g], l);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const __half2 hh = __floats2half2_rn(p[k].x, p[k].y);
+                pk[8 * h + k] = h2_bits(hh);
+                if constexpr (HL) {
+                    const float2 f = __half22float2(hh);
+                    pk[16 + 8 * h + k] = h2_bits(__floats2half2_rn(p[k].x - f.x, p[k].y - f.y));
+                }
+            }
+        }
+        if constexpr (HL) tmem_st32(at + 32 * q, pk);
+        else tmem_st16(at + 16 * q, pk);
+    }
+    return l;
+}
+
+// Some V holds NaN (expanded as 0): dims [c0, c0 + N) of a row that sees tokens [lo, pos] are NaN where one is.
+template <int D, int N>
+__device__ __forceinline__ void mark_nan(const PromptParams& A, int seq, int head, int lo, int pos, int c0, float (&y)[N]) {
+    for (int tok = lo; tok <= pos; ++tok) {
+        const int p = page_id(A.B, seq, tok >> A.B.page_shift, nullptr);
+        if (p < 0) continue;
+        const uint4* v = reinterpret_cast<const uint4*>(
+            A.v_cache + ((((int64_t)p * A.kv_heads + head) << A.B.page_shift) + (tok & ((1 << A.B.page_shift) - 1))) * D + c0);
+#pragma unroll
+        for (int u = 0; u < N / 16; ++u) {
+            const uint4 w = __ldcg(v + u);
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                if (((x[k >> 2] >> (8 * (k & 3))) & 0x7Fu) == 0x7Fu) y[16 * u + k] = __int_as_float(0x7FC00000);
+        }
+    }
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_constant__ PromptParams A) {
     constexpr bool HL = sizeof(T) == 4;
@@ -132,43 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-    // the item: blocks are taken from the last row tile down, the longest first
-    if (warp == 0) {
-        int at = blockIdx.x;
-        bool found = false;
-        for (int top = A.B.batch; top > 0 && !found; top -= 32) {
-            const int i = top - 1 - lane;  // lane 0: the last sequence
-            SeqSpan s{0, 0, 0};
-            int n = 0;
-            if (i >= 0) {
-                bool bad;
-                s = seq_span(A.B, i, &bad);
-                if (bad) raise_flag(A.err_flag, Q4K_ERR_SEQ);
-                const int rows = s.n * A.group;
-                if (rows >= A.min_rows) n = (rows + kRows - 1) / kRows * A.kv_heads;
-            }
-            int inc = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += x;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, at < inc);
-            if (hit) {
-                const int src = __ffs(hit) - 1;
-                if (lane == src) {
-                    s_item[0] = i;
-                    s_item[1] = n - 1 - (at - (inc - n));  // row tile * kv_heads + kv head
-                    s_item[2] = s.start;
-                    s_item[3] = s.n;
-                    s_item[4] = s.len;
-                }
-                found = true;
-            }
-            at -= __shfl_sync(0xffffffffu, inc, 31);
-        }
-        if (!found && lane == 0) s_item[0] = -1;
-    }
+    if (warp == 0) find_item(A, kRows, s_item);
     if (tid == 32) {
         for (int i = 0; i < L::kSlots; ++i) {
             mbar_init(&full[i], 128);
@@ -252,88 +474,42 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     bool ok = true;
-    // a wait of a whole warp: its lanes go on, or give up, together
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait_for(bar, parity, &s_abort, A.wait_ns)) != 0;
-    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_all(bar, parity, &s_abort, A.wait_ns); };
 
     if (warp >= kLoadWarp && warp < kMmaWarp) {
         regs_dec<kRegsLoad>();
-        // ---------------- cache to fp16 tiles. Order of the slots: K0, K1, V0, K2, V1, ..., V(n-1). A thread
-        // reads 16 codes of rows 32 x + rs, in each 64-dim panel, and writes them as two 16-byte units of the
-        // panel's 128-byte rows; the eight threads of a store's phase hold two rows of different parity,
-        // so their units lie on different banks.
-        constexpr int kPanels = D / 64, kLoads = 4 * kPanels;
-        const int i = tid - 32 * kLoadWarp, rs = i >> 2, c = i & 3;
-        const uint8_t* k_at = A.k_cache + (rs & 15) * D + 16 * c;
-        const uint8_t* v_at = A.v_cache + (rs & 15) * D + 16 * c;
-        auto fetch = [&](const uint8_t* cache, int j, uint4 (&r)[kLoads]) {
-            const int left = kv_hi - (kv0 + kToks * j);  // tokens of the tile that are there
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int64_t at = s_meta[j % kMetaRing].at[2 * x + (rs >> 4)];
-                const bool there = at >= 0 && 32 * x + rs < left;
-#pragma unroll
-                for (int p = 0; p < kPanels; ++p) {
-                    r[x * kPanels + p] = make_uint4(0, 0, 0, 0);
-                    if (there) r[x * kPanels + p] = __ldcg(reinterpret_cast<const uint4*>(cache + at + 64 * p));
-                }
-            }
+        // ---------------- cache to fp16 tiles, half a tile at a time, the other half's reads in flight. Order of
+        // the slots: K0, K1, V0, K2, V1, ..., V(n-1)
+        Loader<D> ld(A.k_cache, tid - 32 * kLoadWarp);
+        const int64_t to_v = A.v_cache - A.k_cache;
+        // step s: half s & 1 of slot s >> 1, whose tile and side are
+        auto tile_of = [&](int s) { return s < 2 ? 0 : s >= 4 * n - 2 ? n - 1 : (s >> 1) & 1 ? (s + 2) >> 2 : (s >> 2) - 1; };
+        auto is_v = [&](int s) { return s >= 4 * n - 2 || (s >= 2 && !((s >> 1) & 1)); };
+        auto fetch = [&](int s, uint4 (&r)[Loader<D>::kLoads]) {
+            const int j = tile_of(s), half = s & 1;
+            const bool v_side = is_v(s);
+            if (half == 0 && !v_side && !wait(&meta_full[j % kMetaRing], (j / kMetaRing) & 1)) return false;
+            ld.fetch(s_meta[j % kMetaRing], half, kv_hi - kv0 - kToks * j, r, v_side ? to_v : 0);
+            if (half == 1 && v_side && lane == 0) mbar_arrive(&meta_empty[j % kMetaRing]);
+            return true;
         };
         int slot = 0, uses = 0;
         bool nan = false;
-        uint8_t* const dst = s_kv + rs * 128 + (((2 * c) ^ (rs & 7)) << 4);
-        auto put = [&](bool v_side, const uint4 (&r)[kLoads]) {
-            if (!wait(&empty[slot], (uses & 1) ^ 1)) return false;
-            uint8_t* base = dst + slot * L::kTile;
-            uint8_t* base1 = s_kv + slot * L::kTile + rs * 128 + (((2 * c + 1) ^ (rs & 7)) << 4);
-            __half2 acc[2] = {__float2half2_rn(0.0f), __float2half2_rn(0.0f)};
-#pragma unroll
-            for (int x = 0; x < kLoads; ++x) {
-                uint32_t h[8];
-                expand16(r[x], h);
-                if (v_side) {  // 0 * NaN: NaN if any of them is
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        acc[k & 1] = __hfma2(*reinterpret_cast<const __half2*>(&h[k]), __float2half2_rn(0.0f), acc[k & 1]);
-                }
-                const int off = (x % kPanels) * (kToks * 128) + (x / kPanels) * (32 * 128);
-                *reinterpret_cast<uint4*>(base + off) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4*>(base1 + off) = make_uint4(h[4], h[5], h[6], h[7]);
-            }
-            if (v_side) {
-                const __half2 a = __hadd2(acc[0], acc[1]);
-                if (__hisnan(__low2half(a)) || __hisnan(__high2half(a))) {  // written again with 0 in NaN's place
-                    nan = true;
+        uint4 ra[Loader<D>::kLoads], rb[Loader<D>::kLoads];
+        const int steps = 4 * n;
+        if (n > 0) ok = fetch(0, ra);
 #pragma unroll 1
-                    for (int x = 0; x < kLoads; ++x) {
-                        const int off = (x % kPanels) * (kToks * 128) + (x / kPanels) * (32 * 128);
-#pragma unroll 1
-                        for (int k = 0; k < 16; ++k) {
-                            uint16_t* w = reinterpret_cast<uint16_t*>((k < 8 ? base : base1) + off) + (k & 7);
-                            if ((*w & 0x7FFFu) > 0x7C00u) *w = 0;
-                        }
-                    }
-                }
-            }
+        for (int s = 0; s < steps && ok; s += 2) {
+            ok = fetch(s + 1, rb) && wait(&empty[slot], (uses & 1) ^ 1);
+            if (!ok) break;
+            const bool v_side = is_v(s);
+            uint8_t* base = s_kv + slot * L::kTile;
+            ld.put(base, v_side, ra, &nan);
+            if (s + 2 < steps && !(ok = fetch(s + 2, ra))) break;
+            ld.put(base + 64 * 128, v_side, rb, &nan);
             fence_proxy_async_smem();
             mbar_arrive(&full[slot]);
             if (++slot == L::kSlots) { slot = 0; ++uses; }
-            return true;
-        };
-        uint4 ra[kLoads], rb[kLoads];  // K of tile j + 1, V of tile j
-#pragma unroll 1
-        for (int j = -2; j < n && ok && n > 0; ++j) {
-            if (j + 1 >= 0 && j + 1 < n) ok = put(false, ra);
-            if (ok && j + 2 < n) {
-                ok = wait(&meta_full[(j + 2) % kMetaRing], ((j + 2) / kMetaRing) & 1);
-                if (ok) fetch(k_at, j + 2, ra);
-            }
-            if (ok && j >= 0) ok = put(true, rb);
-            if (ok && j + 1 >= 0 && j + 1 < n) {
-                fetch(v_at, j + 1, rb);
-                if (lane == 0) mbar_arrive(&meta_empty[(j + 1) % kMetaRing]);
-            }
         }
         if (nan) s_nan = 1;
         mbar_arrive(&fin);
@@ -396,36 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         }
         __syncwarp();
         } else if (warp == kPageWarp) {
-            // ---------------- pages and scales, up to kMetaRing tiles ahead
-            auto page_of = [&](int j) {  // lanes 0-7: the page of each 16-token group
-                const int tok = kv0 + kToks * j + 16 * lane;
-                return lane < kGroups && j < n && tok < kv_hi ? page_id(A.B, seq, tok >> A.B.page_shift, A.err_flag) : -1;
-            };
-            int next = page_of(0);
-#pragma unroll 1
-            for (int j = 0; j < n && ok; ++j) {
-                const int pid = next, tok = kv0 + kToks * j + 16 * lane;
-                next = page_of(j + 1);
-                const int64_t ph = (int64_t)pid * A.kv_heads + head;
-                float ks = 1.0f, vs = 1.0f;
-                if (pid >= 0) {
-                    ks = __ldcg(A.k_scale + ph);
-                    vs = __ldcg(A.v_scale + ph);
-                }
-                const bool all = __all_sync(0xffffffffu, lane >= kGroups || pid >= 0 || tok >= kv_hi);
-                ok = wait(&meta_empty[j % kMetaRing], ((j / kMetaRing) & 1) ^ 1);
-                if (!ok) break;
-                TileMeta& m = s_meta[j % kMetaRing];
-                if (lane < kGroups) {
-                    m.at[lane] = pid < 0 ? (int64_t)-1 : ((ph << A.B.page_shift) + (tok & ((1 << A.B.page_shift) - 1))) * D;
-                    m.ks[lane] = ks;
-                    m.ev[lane] = log2_scale(vs);
-                    m.inv[lane] = 1.0f / vs;
-                }
-                if (lane == 0) m.all_ok = all;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&meta_full[j % kMetaRing]);
-            }
+            ok = page_ahead<D>(A, seq, head, kv0, kv_hi, n, s_meta, meta_full, meta_empty, &s_abort);
         }
     } else if (warp < 4) {
         regs_inc<kRegsSoftmax>();
@@ -447,42 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             const int t0 = kv0 + kToks * j;
             const bool whole = meta.all_ok && t0 >= full_lo && t0 + kToks <= full_hi;
             const uint32_t at = tmem + lane_base + kColS + b * kToks;
-            float top = -INFINITY;
-            if (whole) {
-#pragma unroll 1
-                for (int q = 0; q < kToks / 32; q += 2) {
-                    uint32_t v[2][32];
-                    tmem_ld32(at + 32 * q, v[0]);
-                    tmem_ld32(at + 32 * q + 32, v[1]);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        const int g = 2 * q + h;
-                        float x[4];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t* w = &v[h >> 1][16 * (h & 1) + 4 * c];
-                            x[c] = fmaxf(fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1])),
-                                         fmaxf(__uint_as_float(w[2]), __uint_as_float(w[3])));
-                        }
-                        top = fmaxf(top, fmaf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), crow * meta.ks[g], meta.ev[g]));
-                    }
-                }
-            } else {
-#pragma unroll 1
-                for (int g = 0; g < kGroups; ++g) {
-                    uint32_t v[16];
-                    tmem_ld16(at + 16 * g, v);
-                    tmem_wait_ld();
-                    float x = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const int tok = t0 + 16 * g + c;
-                        if (meta.at[g] >= 0 && tok >= lo && tok < hi) x = fmaxf(x, __uint_as_float(v[c]));
-                    }
-                    if (x > -INFINITY) top = fmaxf(top, fmaf(x, crow * meta.ks[g], meta.ev[g]));
-                }
-            }
+            const float top = row_max(at, meta, crow, t0, lo, hi, whole);
             const float m_new = fmaxf(m, top), m_use = m_new == -INFINITY ? 0.0f : m_new;
             const float corr = ex2(m - m_use);
             m = m_new;
@@ -491,61 +603,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             if (j >= 2) ok = wait(&o_empty[b], ((j >> 1) - 1) & 1);
             if (!ok) break;
             s_corr[b][tid] = corr;
-            // P over columns of S that have been read. One term: 8 columns for 16 tokens, packed; two: hi
-            // and lo of 32 tokens in the 32 columns of their S.
-#pragma unroll 1
-            for (int q0 = 0; q0 < kToks / 32; q0 += 2) {
-                uint32_t v[2][32], pk[32];
-                tmem_ld32(at + 32 * q0, v[0]);
-                tmem_wait_ld();
-                tmem_ld32(at + 32 * q0 + 32, v[1]);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    if (q) tmem_wait_ld();
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int g = 2 * (q0 + q) + h;
-                        const float c = crow * meta.ks[g], e = meta.ev[g] - (m_use - 7.0f);
-                        float2 p[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t* w = &v[q][16 * h + 2 * k];
-                            p[k] = fma2(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), make_float2(c, c), make_float2(e, e));
-                        }
-                        if (!whole) {
-                            const int tok = t0 + 16 * g, from = meta.at[g] >= 0 ? lo - tok : 16, to = hi - tok;
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                if (2 * k < from || 2 * k >= to) p[k].x = -INFINITY;
-                                if (2 * k + 1 < from || 2 * k + 1 >= to) p[k].y = -INFINITY;
-                            }
-                        }
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) p[k] = make_float2(ex2(p[k].x), ex2(p[k].y));
-                        const float2 sum = add2(add2(add2(p[0], p[1]), add2(p[2], p[3])), add2(add2(p[4], p[5]), add2(p[6], p[7])));
-                        l = fmaf(sum.x + sum.y, meta.inv[g], l);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const __half2 hh = __floats2half2_rn(p[k].x, p[k].y);
-                            if constexpr (HL) {
-                                const float2 f = __half22float2(hh);
-                                pk[8 * h + k] = h2_bits(hh);
-                                pk[16 + 8 * h + k] = h2_bits(__floats2half2_rn(p[k].x - f.x, p[k].y - f.y));
-                            } else {
-                                pk[16 * q + 8 * h + k] = h2_bits(hh);
-                            }
-                        }
-                    }
-                    if (HL) tmem_st32(at + 32 * (q0 + q), pk);
-                    else if (q) tmem_st32(at + 16 * q0, pk);
-                }
-            }
+            l += weights<HL>(at, meta, crow, m_use, t0, lo, hi, whole);
             if (lane == 0) mbar_arrive(&meta_empty[j % kMetaRing]);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&p_full[b]);
         }
-        s_inv[tid] = m == -INFINITY ? 0.0f : 1.0f / l;
+        s_inv[tid] = l == 0.0f ? 0.0f : 1.0f / l;  // 0: the row sees nothing
         mbar_arrive(&fin);
     } else {
         regs_inc<kRegsSums>();
@@ -579,23 +643,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         }
         ok = ok && wait(&fin, 0);  // the denominators, and the loaders' report of NaN
         if (ok && s_nan && r < rows) {
-            // some V holds NaN (written as 0 above): the dims of the rows that see it are NaN
             const int pos = first + r / A.group;
-            for (int tok = A.window > 0 ? max(pos - A.window + 1, 0) : 0; tok <= pos; ++tok) {
-                const int p = page_id(A.B, seq, tok >> A.B.page_shift, nullptr);
-                if (p < 0) continue;
-                const uint4* v = reinterpret_cast<const uint4*>(
-                    A.v_cache + ((((int64_t)p * A.kv_heads + head) << A.B.page_shift) + (tok & ((1 << A.B.page_shift) - 1))) * D);
+            float y[D];
 #pragma unroll
-                for (int u = 0; u < D / 16; ++u) {
-                    const uint4 w = __ldcg(v + u);
-                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            for (int c = 0; c < D; ++c) y[c] = c & 1 ? acc[c / 2].y : acc[c / 2].x;
+            mark_nan<D, D>(A, seq, head, A.window > 0 ? max(pos - A.window + 1, 0) : 0, pos, 0, y);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        if (((x[k >> 2] >> (8 * (k & 3))) & 0x7Fu) == 0x7Fu)
-                            (k & 1 ? acc[8 * u + k / 2].y : acc[8 * u + k / 2].x) = __int_as_float(0x7FC00000);
-                }
-            }
+            for (int c = 0; c < D; c += 2) acc[c / 2] = make_float2(y[c], y[c + 1]);
         }
         if (ok && r < rows) {
             const float inv = s_inv[row];
@@ -623,27 +677,328 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
+// ---------------------------------------------------------------------------------------------------
+// bf16 rows: 256 query rows a CTA, two tiles of 128 that share every K and V tile, so the cache is
+// expanded to fp16 half as often, and one tile's softmax runs while the other's products do. The sums stay
+// in tensor memory over all tokens (their rounding is far below a bf16 output's), scaled again only when a row's
+// maximum has grown by more than 2^8 since its reference was taken: P then stays within fp16.
+//
+// Roles: warps 0-3 and 4-7 the softmax of a tile each (thread = row) and its store, 8-11 expand K, 12-15 V,
+// warp 16 issues the products, warp 17 looks the pages and scales up (18-19 idle).
+constexpr int kThreads2 = 640;
+constexpr int kKWarp2 = 8, kVWarp2 = 12, kMmaWarp2 = 16, kPageWarp2 = 17;
+constexpr int kRegsSoftmax2 = 136, kRegsLoad2 = 72, kRegsCtrl2 = 64;
+static_assert(2 * kRegsSoftmax2 + 2 * kRegsLoad2 + kRegsCtrl2 <= 5 * (65536 / kThreads2 / 8 * 8), "register split");
+constexpr float kSlack = 8.0f;  // log2 growth of a row's maximum before its sums are scaled again
+
+template <int D>
+struct Layout2 {
+    static constexpr int kTile = kToks * D * 2;            // a K or V tile, and the queries of a row tile
+    static constexpr int kSlots = 4;
+    static constexpr int kBytes = 1024 + 2 * kTile + kSlots * kTile;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads2, 1) attn_prompt2_kernel(const __grid_constant__ PromptParams A) {
+    using L = Layout2<D>;
+    constexpr uint32_t kColS = 0, kColO = 256;  // tensor memory: S (then P) and O of both row tiles
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* s_q = smem;
+    uint8_t* s_kv = smem + 2 * L::kTile;
+    __shared__ __align__(8) uint64_t full[L::kSlots], empty[L::kSlots], meta_full[kMetaRing], meta_empty[kMetaRing];
+    __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2], fin, drain;
+    __shared__ TileMeta s_meta[kMetaRing];
+    __shared__ float s_c[2 * kRows];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_item[5];
+    __shared__ volatile int s_abort;
+    __shared__ volatile int s_nan;
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (warp == 0) find_item(A, 2 * kRows, s_item);
+    if (tid == 32) {
+        for (int i = 0; i < L::kSlots; ++i) {
+            mbar_init(&full[i], 128);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < kMetaRing; ++i) {
+            mbar_init(&meta_full[i], 1);
+            mbar_init(&meta_empty[i], 16);  // the warps of both softmaxes and of the loaders
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 128);
+            mbar_init(&o_full[i], 1);
+        }
+        mbar_init(&fin, 128);
+        mbar_init(&drain, 1);
+        fence_mbar_init();
+        s_abort = 0;
+        s_nan = 0;
+    }
+    __syncthreads();
+    const int seq = s_item[0];
+    if (seq < 0) return;  // the whole CTA, before any allocation
+    const int head = s_item[1] % A.kv_heads, tile = s_item[1] / A.kv_heads;
+    const int start = s_item[2], rows = s_item[3] * A.group, first = s_item[4] - s_item[3];
+    const int r0 = tile * 2 * kRows, last = min(rows, r0 + 2 * kRows) - 1;
+    // positions: some row sees tokens in [kv_lo, kv_hi)
+    const int pf = first + r0 / A.group, pl = first + last / A.group;
+    const int kv_hi = max(pl + 1, 0), kv_lo = A.window > 0 ? max(pf - A.window + 1, 0) : 0;
+    const int kv0 = kv_lo & ~15;
+    const int n = (kv_hi - kv0 + kToks - 1) / kToks;  // tiles; 0: no row sees anything
+
+    if (warp == kMmaWarp2) {
+        tmem_alloc(&s_tmem, 512);
+        tmem_relinquish();
+    }
+    // queries: two threads a row, D/2 dims each, scaled by a power of two into fp16's range (exact there)
+    if (tid < 512) {
+        const int row = tid >> 1, half = tid & 1, r = r0 + row;
+        const bool valid = r < rows;
+        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(A.q) +
+                                 (int64_t)(start + (valid ? r / A.group : 0)) * A.q_stride +
+                                 (int64_t)(head * A.group + (valid ? r % A.group : 0)) * D + half * (D / 2);
+        uint4 x[D / 16];
+        uint32_t top = 0;  // largest finite magnitude's bits
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            x[i] = __ldcg(reinterpret_cast<const uint4*>(p) + i);
+            if (!valid) x[i] = make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t a = w[k] & 0x7FFFu, b = (w[k] >> 16) & 0x7FFFu;
+                if (a < 0x7F80u) top = max(top, a);
+                if (b < 0x7F80u) top = max(top, b);
+            }
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        const int e = top > 0 ? min(max(134 - (int)(top >> 7), -120), 120) : 0;
+        const float up = A.sign * exp2_int(e);
+        if (half == 0) s_c[row] = A.scale_log2 * exp2_int(-e);
+        uint8_t* base = s_q + (row >> 7) * L::kTile + (row & 127) * 128;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {  // 8 dims a unit
+            const int unit = half * (D / 16) + i;
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                h[k] = h2_bits(__floats2half2_rn(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up));
+            *reinterpret_cast<uint4*>(base + (unit >> 3) * (kRows * 128) + (((unit & 7) ^ (row & 7)) << 4)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_all(bar, parity, &s_abort, A.wait_ns); };
+
+    if (warp >= kMmaWarp2) {
+        regs_dec<kRegsCtrl2>();
+        if (warp == kMmaWarp2) {
+            // ---------------- products, issued by one elected lane of the warp
+            const uint32_t idesc_s = idesc_f16_f32(kRows, kToks);
+            const uint32_t idesc_o = idesc_f16_f32(kRows, D) | kIdescBMnMajor;
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t q_at = __shfl_sync(0xffffffffu, smem_u32(s_q), 0), kv_at = q_at + 2 * L::kTile;
+            bool issued = false;
+            // slot 2 j: K of tile j, slot 2 j + 1: V
+#pragma unroll 1
+            for (int j = -1; j < n && ok && n > 0; ++j) {
+#pragma unroll 1
+                for (int x = 0; x < 2; ++x) {
+                    if (j >= 0) {
+                        const int sv = 2 * j + 1;
+                        ok = wait(&p_full[x], j & 1) && (x > 0 || wait(&full[sv % L::kSlots], (sv / L::kSlots) & 1));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t p = tm + kColS + x * kToks, d = tm + kColO + x * D;
+                        const uint64_t b = desc_sw128_mnmajor(kv_at + sv % L::kSlots * L::kTile, kToks * 128);
+#pragma unroll
+                        for (int k = 0; k < kToks / 16; ++k)
+                            mma_f16_ts_elect(d, p + 8 * k, b + ((k * 16 * 128) >> 4), idesc_o, j > 0 || k > 0);
+                        if (x) mma_commit_elect(&empty[sv % L::kSlots]);
+                        if (j == n - 1) mma_commit_elect(&o_full[x]);
+                    }
+                    if (j + 1 < n) {
+                        const int sk = 2 * j + 2;
+                        if (x == 0 && !(ok = wait(&full[sk % L::kSlots], (sk / L::kSlots) & 1))) break;
+                        tc_fence_after();
+                        const uint64_t a = desc_sw128_kmajor(q_at + x * L::kTile);
+                        const uint64_t b = desc_sw128_kmajor(kv_at + sk % L::kSlots * L::kTile);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t off = ((k >> 2) * (kToks * 128) + (k & 3) * 32) >> 4;
+                            mma_f16_ss_elect(tm + kColS + x * kToks, a + off, b + off, idesc_s, k > 0);
+                        }
+                        mma_commit_elect(&s_full[x]);
+                        if (x) mma_commit_elect(&empty[sk % L::kSlots]);
+                        issued = true;
+                    }
+                }
+            }
+            if (!ok && issued) {  // outstanding products finish before tensor memory is freed
+                volatile int never = 0;
+                mma_commit_elect(&drain);
+                mbar_wait(&drain, 0, &never);
+            }
+            __syncwarp();
+        } else if (warp == kPageWarp2) {
+            ok = page_ahead<D>(A, seq, head, kv0, kv_hi, n, s_meta, meta_full, meta_empty, &s_abort);
+        }
+    } else if (warp >= kKWarp2) {
+        regs_dec<kRegsLoad2>();
+        // ---------------- cache to fp16 tiles: a warpgroup for K, one for V
+        const bool v_side = warp >= kVWarp2;
+        const int i = tid & 127;
+        Loader<D> ld(v_side ? A.v_cache : A.k_cache, i);
+        bool nan = false;
+        uint4 ra[Loader<D>::kLoads], rb[Loader<D>::kLoads];
+        ok = n == 0 || wait(&meta_full[0], 0);
+        if (n > 0 && ok) ld.fetch(s_meta[0], 0, kv_hi - kv0, ra);
+#pragma unroll 1
+        for (int j = 0; j < n && ok; ++j) {
+            const int slot = (2 * j + v_side) % L::kSlots, m = j % kMetaRing;
+            ld.fetch(s_meta[m], 1, kv_hi - kv0 - kToks * j, rb);
+            if (lane == 0) mbar_arrive(&meta_empty[m]);
+            ok = wait(&empty[slot], (((2 * j + v_side) / L::kSlots) & 1) ^ 1);
+            if (!ok) break;
+            uint8_t* base = s_kv + slot * L::kTile;
+            ld.put(base, v_side, ra, &nan);
+            if (j + 1 < n) {
+                ok = wait(&meta_full[(j + 1) % kMetaRing], ((j + 1) / kMetaRing) & 1);
+                if (!ok) break;
+                ld.fetch(s_meta[(j + 1) % kMetaRing], 0, kv_hi - kv0 - kToks * (j + 1), ra);
+            }
+            ld.put(base + 64 * 128, v_side, rb, &nan);
+            fence_proxy_async_smem();
+            mbar_arrive(&full[slot]);
+        }
+        if (nan) s_nan = 1;
+        if (v_side) mbar_arrive(&fin);
+    } else {
+        regs_inc<kRegsSoftmax2>();
+        // ---------------- softmax: thread = row = tensor memory lane
+        const int x = warp >> 2, row = tid & 127, r = r0 + x * kRows + row;
+        const bool valid = r < rows;
+        const int pos = first + (valid ? r / A.group : 0);
+        const int hi = valid ? pos + 1 : 0, lo = A.window > 0 ? max(pos - A.window + 1, 0) : 0;
+        // every row of the tile sees [full_lo, full_hi)
+        const int t_last = min(rows, r0 + (x + 1) * kRows) - 1, t_first = min(r0 + x * kRows, t_last);
+        const int full_hi = max(first + t_first / A.group + 1, 0);
+        const int full_lo = A.window > 0 ? max(first + t_last / A.group - A.window + 1, 0) : 0;
+        const float crow = s_c[x * kRows + row];
+        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t at = tmem + lane_base + kColS + x * kToks, o_at = tmem + lane_base + kColO + x * D;
+        float ref = -INFINITY, l = 0.0f;  // the reference of P and of the sums
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+            ok = wait(&meta_full[j % kMetaRing], (j / kMetaRing) & 1) && wait(&s_full[x], j & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const TileMeta& meta = s_meta[j % kMetaRing];
+            const int t0 = kv0 + kToks * j;
+            const bool whole = meta.all_ok && t0 >= full_lo && t0 + kToks <= full_hi;
+            const float top = row_max(at, meta, crow, t0, lo, hi, whole);
+            if (__any_sync(0xffffffffu, top > ref + kSlack)) {
+                // a new reference; the sums so far (all products before this S are complete) follow it
+                const float m_new = fmaxf(ref, top), m_use = m_new == -INFINITY ? 0.0f : m_new;
+                const float corr = ex2(ref - m_use);
+                ref = m_new;
+                l *= corr;
+                if (j > 0) {
+#pragma unroll 1
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t v[32];
+                        tmem_ld32(o_at + 32 * q, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * corr);
+                        tmem_st32(o_at + 32 * q, v);
+                    }
+                }
+            }
+            l += weights<false>(at, meta, crow, ref == -INFINITY ? 0.0f : ref, t0, lo, hi, whole);
+            if (lane == 0) mbar_arrive(&meta_empty[j % kMetaRing]);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&p_full[x]);
+        }
+        ok = ok && wait(&fin, 0) && (n == 0 || wait(&o_full[x], 0));
+        if (ok) {
+            tc_fence_after();
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // 0: the row sees nothing
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(A.out) + (int64_t)(start + r / A.group) * A.out_stride +
+                               (int64_t)(head * A.group + r % A.group) * D;
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+                uint32_t v[32];
+                float y[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] = 0;
+                if (n > 0) {
+                    tmem_ld32(o_at + 32 * q, v);
+                    tmem_wait_ld();
+                }
+#pragma unroll
+                for (int c = 0; c < 32; ++c) y[c] = inv == 0.0f ? 0.0f : __uint_as_float(v[c]) * inv;
+                if (s_nan && valid) mark_nan<D, 32>(A, seq, head, lo, pos, 32 * q, y);
+                if (valid) Vec<__nv_bfloat16>::store(o + 32 * q, y);
+            }
+        }
+    }
+    if (!ok) {
+        s_abort = 1;
+        raise_flag(A.err_flag, Q4K_ERR_TIMEOUT);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp2) tmem_dealloc(tmem, 512);
+}
+
 template <typename T, int D>
 cudaError_t launch_typed(const PromptParams& P, cudaStream_t stream) {
     constexpr bool HL = sizeof(T) == 4;
+    void (*kern)(PromptParams);
+    int bytes, rows, threads;
+    if constexpr (HL) {
+        kern = attn_prompt_kernel<T, D>;
+        bytes = Layout<HL, D>::kBytes;
+        rows = kRows;
+        threads = kThreads;
+    } else {
+        kern = attn_prompt2_kernel<D>;
+        bytes = Layout2<D>::kBytes;
+        rows = 2 * kRows;
+        threads = kThreads2;
+    }
     // every CTA holds all of its SM's tensor memory: enough shared memory that one fits
-    const int smem = Layout<HL, D>::kBytes < 144 * 1024 ? 144 * 1024 : Layout<HL, D>::kBytes;
+    const int smem = bytes < 144 * 1024 ? 144 * 1024 : bytes;
     static bool set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!set[dev]) {
-        e = cudaFuncSetAttribute(attn_prompt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         set[dev] = true;
     }
     // an upper bound of the row tiles: a sequence's last one may be part filled
-    const int64_t items = ((int64_t)P.B.m * P.group / kRows + (P.B.m < P.B.batch ? P.B.m : P.B.batch)) * P.kv_heads;
+    const int64_t items = ((int64_t)P.B.m * P.group / rows + (P.B.m < P.B.batch ? P.B.m : P.B.batch)) * P.kv_heads;
     if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)items);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -651,7 +1006,7 @@ cudaError_t launch_typed(const PromptParams& P, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_prompt_kernel<T, D>, P);
+    return cudaLaunchKernelEx(&cfg, kern, P);
 }
 
 }  // namespace

@@ -563,6 +563,28 @@ def test_attention_nan_reaches_only_the_rows_that_see_it(n, length, window, d, d
                 assert np.array_equal(got[~sees], clean[~sees]) and np.array_equal(got[:, :hq // hk], clean[:, :hq // hk])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,length", [(1, 40), (1, 9000), (3, 40), (90, 120)])
+def test_attention_nan_query(n, length, dtype):
+    """A NaN in a query makes its row NaN (not the zero of a row that sees nothing), and no other row."""
+    hq, hk, d, page = 4, 2, 64, 16
+    c = Cache(1, -(-length // page), hk, page, d)
+    c.upload()
+    q = rows(np.random.default_rng(1).standard_normal((n, hq * d)), dtype)
+    q[n // 2, d + 3] = float("nan")
+    out = torch.empty_like(q)
+    nbytes = q4k.q4k_paged_attention_workspace_size(1, n, hq, hk, d)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    q4k.q4k_paged_attention(q, n, hq, hk, d, hq * d, c.dev["k"], c.dev["v"], c.dev_scale["k"], c.dev_scale["v"],
+                            dev(np.array([0, n], np.int32)), dev(np.array([length], np.int32)),
+                            dev(tables(c, [length])), 1, -(-length // page) + 1, page, c.pages, n, length, 0.125, 0, out,
+                            hq * d, ws, nbytes)
+    bad = np.isnan(f64(out).reshape(n, hq, d))
+    want = np.zeros_like(bad)
+    want[n // 2, 1] = True
+    assert np.array_equal(bad, want)
+
+
 def test_attention_results_do_not_depend_on_hints_or_neighbours():
     """Hints choose kernels and grids: a sequence's result stays within the bound whatever they say."""
     for hints in ((1, 1), (300, 100000), (0, 0)):
