@@ -349,6 +349,36 @@ __device__ __forceinline__ float weights(uint32_t at, const TileMeta& meta, floa
     return l;
 }
 
+// The same in one pass with the largest x, for a tile that the row sees whole, P left in registers (one
+// term): S stays as it is until the caller knows that the reference held.
+__device__ __forceinline__ float weights_and_max(uint32_t at, const TileMeta& meta, float crow, float ref,
+                                                 uint32_t (&pk)[2][32], float* top_out) {
+    float l = 0.0f, top[2] = {-INFINITY, -INFINITY};
+    uint32_t v[2][16];
+    tmem_ld16(at, v[0]);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        tmem_wait_ld();
+        if (g + 1 < kGroups) tmem_ld16(at + 16 * (g + 1), v[(g + 1) & 1]);
+        const float c = crow * meta.ks[g], e = meta.ev[g] - (ref - 7.0f);
+        float p[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) p[k] = fmaf(__uint_as_float(v[g & 1][k]), c, e);
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) top[k / 2 % 2] = fmaxf(fmaxf(top[k / 2 % 2], p[k]), p[k + 1]);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) p[k] = ex2(p[k]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) pk[g >> 2][8 * (g & 3) + k] = h2_bits(__floats2half2_rn(p[2 * k], p[2 * k + 1]));
+        float sum[4] = {p[0] + p[4], p[1] + p[5], p[2] + p[6], p[3] + p[7]};
+#pragma unroll
+        for (int k = 8; k < 16; ++k) sum[k % 4] += p[k];
+        l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), meta.inv[g], l);
+    }
+    *top_out = fmaxf(top[0], top[1]) + (ref - 7.0f);
+    return l;
+}
+
 // Some V holds NaN (expanded as 0): dims [c0, c0 + N) of a row that sees tokens [lo, pos] are NaN where one is.
 template <int D, int N>
 __device__ __forceinline__ void mark_nan(const PromptParams& A, int seq, int head, int lo, int pos, int c0, float (&y)[N]) {
@@ -907,26 +937,42 @@ __global__ void __launch_bounds__(kThreads2, 1) attn_prompt2_kernel(const __grid
             const TileMeta& meta = s_meta[j % kMetaRing];
             const int t0 = kv0 + kToks * j;
             const bool whole = meta.all_ok && t0 >= full_lo && t0 + kToks <= full_hi;
-            const float top = row_max(at, meta, crow, t0, lo, hi, whole);
-            if (__any_sync(0xffffffffu, top > ref + kSlack)) {
-                // a new reference; the sums so far (all products before this S are complete) follow it
-                const float m_new = fmaxf(ref, top), m_use = m_new == -INFINITY ? 0.0f : m_new;
-                const float corr = ex2(ref - m_use);
-                ref = m_new;
-                l *= corr;
-                if (j > 0) {
-#pragma unroll 1
-                    for (int q = 0; q < D / 32; ++q) {
-                        uint32_t v[32];
-                        tmem_ld32(o_at + 32 * q, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * corr);
-                        tmem_st32(o_at + 32 * q, v);
-                    }
+            // P under the reference so far, in one pass, where every row sees the whole tile and no maximum outgrows
+            // its reference; else the maximum first, a new reference, and the sums so far (all products
+            // before this S are complete) scaled to it.
+            bool done = false;
+            if (whole && !__any_sync(0xffffffffu, ref == -INFINITY)) {
+                uint32_t pk[2][32];
+                float top;
+                const float sum = weights_and_max(at, meta, crow, ref, pk, &top);
+                if (!__any_sync(0xffffffffu, top > ref + kSlack)) {
+                    l += sum;
+                    tmem_st32(at, pk[0]);
+                    tmem_st32(at + 32, pk[1]);
+                    done = true;
                 }
             }
-            l += weights<false>(at, meta, crow, ref == -INFINITY ? 0.0f : ref, t0, lo, hi, whole);
+            if (!done) {
+                const float top = row_max(at, meta, crow, t0, lo, hi, whole);
+                if (__any_sync(0xffffffffu, top > ref + kSlack)) {
+                    const float m_new = fmaxf(ref, top);
+                    const float corr = ex2(ref - (m_new == -INFINITY ? 0.0f : m_new));
+                    ref = m_new;
+                    l *= corr;
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int q = 0; q < D / 32; ++q) {
+                            uint32_t v[32];
+                            tmem_ld32(o_at + 32 * q, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * corr);
+                            tmem_st32(o_at + 32 * q, v);
+                        }
+                    }
+                }
+                l += weights<false>(at, meta, crow, ref == -INFINITY ? 0.0f : ref, t0, lo, hi, whole);
+            }
             if (lane == 0) mbar_arrive(&meta_empty[j % kMetaRing]);
             tmem_wait_st();
             tc_fence_before();
