@@ -361,19 +361,19 @@ __device__ __forceinline__ float weights_and_max(uint32_t at, const TileMeta& me
         tmem_wait_ld();
         if (g + 1 < kGroups) tmem_ld16(at + 16 * (g + 1), v[(g + 1) & 1]);
         const float c = crow * meta.ks[g], e = meta.ev[g] - (ref - 7.0f);
-        float p[16];
+        float2 p[8];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) p[k] = fmaf(__uint_as_float(v[g & 1][k]), c, e);
+        for (int k = 0; k < 8; ++k)
+            p[k] = fma2(make_float2(__uint_as_float(v[g & 1][2 * k]), __uint_as_float(v[g & 1][2 * k + 1])), make_float2(c, c),
+                        make_float2(e, e));
 #pragma unroll
-        for (int k = 0; k < 16; k += 2) top[k / 2 % 2] = fmaxf(fmaxf(top[k / 2 % 2], p[k]), p[k + 1]);
+        for (int k = 0; k < 8; ++k) top[k % 2] = fmaxf(fmaxf(top[k % 2], p[k].x), p[k].y);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) p[k] = ex2(p[k]);
+        for (int k = 0; k < 8; ++k) p[k] = make_float2(ex2(p[k].x), ex2(p[k].y));
 #pragma unroll
-        for (int k = 0; k < 8; ++k) pk[g >> 2][8 * (g & 3) + k] = h2_bits(__floats2half2_rn(p[2 * k], p[2 * k + 1]));
-        float sum[4] = {p[0] + p[4], p[1] + p[5], p[2] + p[6], p[3] + p[7]};
-#pragma unroll
-        for (int k = 8; k < 16; ++k) sum[k % 4] += p[k];
-        l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), meta.inv[g], l);
+        for (int k = 0; k < 8; ++k) pk[g >> 2][8 * (g & 3) + k] = h2_bits(__floats2half2_rn(p[k].x, p[k].y));
+        const float2 sum = add2(add2(add2(p[0], p[1]), add2(p[2], p[3])), add2(add2(p[4], p[5]), add2(p[6], p[7])));
+        l = fmaf(sum.x + sum.y, meta.inv[g], l);
     }
     *top_out = fmaxf(top[0], top[1]) + (ref - 7.0f);
     return l;
@@ -563,10 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             for (int t = 0; t < L::kTerms; ++t) {
                 const uint64_t a = desc_sw128_kmajor(q_at + t * L::kTile);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = ((k >> 2) * (kToks * 128) + (k & 3) * 32) >> 4;
-                    mma_f16_ss_elect(d, a + off, b + off, idesc_s, t > 0 || k > 0);
-                }
+                for (int k = 0; k < D / 64; ++k)
+                    mma_f16_ss_elect4(d, a + ((k * kToks * 128) >> 4), b + ((k * kToks * 128) >> 4), 2, 2, idesc_s, t + k);
             }
             mma_commit_elect(&s_full[j & 1]);
             mma_commit_elect(&empty[slot]);
@@ -584,13 +582,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             tc_fence_after();
             const uint32_t p = tm + kColS + (j & 1) * kToks, d = tm + kColO + (j & 1) * D;
             const uint64_t b = desc_sw128_mnmajor(kv_at + slot * L::kTile, kToks * 128);
+            // 32 tokens' P in the 32 columns of their S: 16 of the high term, 16 of the low
 #pragma unroll
             for (int t = 0; t < L::kTerms; ++t)
 #pragma unroll
-                for (int k = 0; k < kToks / 16; ++k) {
-                    const uint32_t a = HL ? p + 32 * (k >> 1) + 8 * (k & 1) + 16 * t : p + 8 * k;
-                    mma_f16_ts_elect(d, a, b + ((k * 16 * 128) >> 4), idesc_o, t > 0 || k > 0);
-                }
+                for (int h = 0; h < 2; ++h)  // k steps 0, 2, 4, 6, then 1, 3, 5, 7: 32 columns apart
+                    mma_f16_ts_elect4(d, p + 8 * h + 16 * t, b + ((h * 16 * 128) >> 4), 32, (32 * 128) >> 4, idesc_o, t + h);
             mma_commit_elect(&o_full[j & 1]);
             mma_commit_elect(&empty[slot]);
             next_slot();
@@ -852,9 +849,8 @@ __global__ void __launch_bounds__(kThreads2, 1) attn_prompt2_kernel(const __grid
                         tc_fence_after();
                         const uint32_t p = tm + kColS + x * kToks, d = tm + kColO + x * D;
                         const uint64_t b = desc_sw128_mnmajor(kv_at + sv % L::kSlots * L::kTile, kToks * 128);
-#pragma unroll
-                        for (int k = 0; k < kToks / 16; ++k)
-                            mma_f16_ts_elect(d, p + 8 * k, b + ((k * 16 * 128) >> 4), idesc_o, j > 0 || k > 0);
+                        mma_f16_ts_elect4(d, p, b, 8, (16 * 128) >> 4, idesc_o, j > 0);
+                        mma_f16_ts_elect4(d, p + 32, b + ((64 * 128) >> 4), 8, (16 * 128) >> 4, idesc_o, 1);
                         if (x) mma_commit_elect(&empty[sv % L::kSlots]);
                         if (j == n - 1) mma_commit_elect(&o_full[x]);
                     }
@@ -865,10 +861,9 @@ __global__ void __launch_bounds__(kThreads2, 1) attn_prompt2_kernel(const __grid
                         const uint64_t a = desc_sw128_kmajor(q_at + x * L::kTile);
                         const uint64_t b = desc_sw128_kmajor(kv_at + sk % L::kSlots * L::kTile);
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t off = ((k >> 2) * (kToks * 128) + (k & 3) * 32) >> 4;
-                            mma_f16_ss_elect(tm + kColS + x * kToks, a + off, b + off, idesc_s, k > 0);
-                        }
+                        for (int k = 0; k < D / 64; ++k)
+                            mma_f16_ss_elect4(tm + kColS + x * kToks, a + ((k * kToks * 128) >> 4), b + ((k * kToks * 128) >> 4), 2,
+                                              2, idesc_s, k);
                         mma_commit_elect(&s_full[x]);
                         if (x) mma_commit_elect(&empty[sk % L::kSlots]);
                         issued = true;

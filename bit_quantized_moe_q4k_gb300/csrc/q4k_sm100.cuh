@@ -198,6 +198,43 @@ __device__ __forceinline__ void mma_f16_ss_elect(uint32_t d_tmem, uint64_t a_des
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// Four products of consecutive k steps in one go, A and B `a_step` / `b_step` apart (descriptor units of 16
+// bytes, or tensor-memory columns for A from there): one election and no register traffic between them.
+// first_accumulates: whether the first adds to what D holds.
+__device__ __forceinline__ void mma_f16_ss_elect4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t a_step,
+                                                  uint32_t b_step, uint32_t idesc, uint32_t first_accumulates) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b64 a, b, sa, sb;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "cvt.u64.u32 sa, %4;\n\tcvt.u64.u32 sb, %5;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "add.u64 a, %1, sa;\n\tadd.u64 b, %2, sb;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, a, sa;\n\tadd.u64 b, b, sb;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, a, sa;\n\tadd.u64 b, b, sb;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_step), "r"(b_step), "r"(first_accumulates)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts_elect4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t a_step,
+                                                  uint32_t b_step, uint32_t idesc, uint32_t first_accumulates) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b64 b, sb;\n\t.reg .b32 a;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "cvt.u64.u32 sb, %5;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "add.u32 a, %1, %4;\n\tadd.u64 b, %2, sb;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+        "add.u32 a, a, %4;\n\tadd.u64 b, b, sb;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+        "add.u32 a, a, %4;\n\tadd.u64 b, b, sb;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(a_step), "r"(b_step), "r"(first_accumulates)
+        : "memory");
+}
 // A from tensor memory: the same issued by one lane that elect.sync picks among the warp's 32 lanes: the whole warp
 // runs the issuing loop, so its operands stay warp-uniform (no per-instruction transfer of a
 // lone thread's registers), and each instruction is issued once.
