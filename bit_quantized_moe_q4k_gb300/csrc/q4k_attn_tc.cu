@@ -5,23 +5,19 @@
 // sum 2^(-e_j) P_j, with the codes of both sides exact in fp16, bf16 queries in one fp16 term and fp32
 // queries (and their P) in two.
 //
-// A CTA takes 128 query rows of one kv head (row r: token r / group, head r % group, so the heads of a
-// group share each K and V tile) and walks over the tokens that some row sees, 128 at a time:
+// A CTA takes 128 (fp32) or 256 (bf16) query rows of one kv head (row r: token r / group, head r % group, so the
+// heads of a group share each K and V tile) and walks over the tokens that some row sees, 128 at a time:
 //   S = Q K^T   tcgen05.mma, Q and K from shared memory (K-major, 128-byte swizzle)
 //   P in place of S in tensor memory, the A operand of
 //   O = P V     V from shared memory as it lies in the cache, d contiguous (N-major)
-// S and O have two tiles each in tensor memory, so that S of the next tokens is multiplied while the
-// softmax of these is computed. O of each 128 tokens is a fresh accumulator that is added to fp32 sums in
-// registers: the tensor core's own accumulation does not round to nearest, and the running maximum's
-// correction costs nothing more there.
+// Roles by warp: softmax (thread = row), for fp32 the sums, expanding K, expanding V, issuing the products, and
+// looking pages and scales up. Every wait is bounded; an abort flag lets all roles leave together. The
+// loops are kept short: the roles share a scheduler and its instruction cache, and unrolled further they waited for
+// instructions (the bf16 prompt below took 1863 us with the first, fully unrolled ones).
 //
-// Roles: warps 0-3 softmax (thread = row), 4-7 the sums (thread = row) and the store, 8-11 read the
-// cache and write fp16 tiles, warp 12 issues the products, warp 13 looks the pages and scales up (14-15
-// idle). Every wait is bounded; an abort flag lets all roles leave together. The loops are kept
-// short: four roles share a scheduler, and unrolled further they waited for instructions.
-//
-// Bound by shared memory and the tensor core together: a tile of 128 x 128 x 128 takes 512 cycles for
-// each product, reads 96 KB of operands and writes 64 KB of converted K and V at 128 bytes a cycle.
+// Bound by the issue of instructions and the latency between S and P: a 128 x 128 x 128 product takes 512 cycles of the
+// tensor core, two a tile of fp32 rows' one. bf16, 8192 tokens, 32 / 8 heads, head_dim 128: 510 us, 1077
+// TFLOP/s of the pairs that are seen (56% of the card's measured dense rate).
 #include "q4k_paged.cuh"
 #include "q4k_sm100.cuh"
 #include "q4k_sync.cuh"
@@ -33,11 +29,6 @@ namespace {
 constexpr int kRows = 128;   // query rows of a CTA
 constexpr int kToks = 128;   // tokens of a tile
 constexpr int kGroups = kToks / 16;
-constexpr int kThreads = 512;
-constexpr int kLoadWarp = 8, kMmaWarp = 12, kPageWarp = 13;
-// Registers a thread of each warpgroup after the split; their sum is four times what the launch gives.
-constexpr int kRegsSoftmax = 152, kRegsSums = 184, kRegsLoad = 104, kRegsMma = 72;
-static_assert(kRegsSoftmax + kRegsSums + kRegsLoad + kRegsMma <= 4 * (65536 / kThreads), "register split");
 constexpr int kMetaRing = 4;
 
 struct PromptParams {
@@ -65,15 +56,6 @@ struct TileMeta {
 
 template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
-template <bool HL, int D>
-struct Layout {
-    static constexpr int kTerms = HL ? 2 : 1;
-    static constexpr int kTile = kToks * D * 2;            // a K or V tile (and one term of Q)
-    static constexpr int kSlots = HL ? 4 : 5;              // at most 6: kMetaRing holds what is in flight
-    static constexpr int kQ = kTerms * kTile;
-    static constexpr int kBytes = 1024 + kQ + kSlots * kTile;
-};
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -180,7 +162,7 @@ struct Loader {
         u1 = rs * 128 + (((2 * c + 1) ^ (rs & 7)) << 4);
     }
     // left: tokens of the tile that are there
-    __device__ __forceinline__ void fetch(const TileMeta& meta, int half, int left, uint4 (&r)[kLoads], int64_t side = 0) const {
+    __device__ __forceinline__ void fetch(const TileMeta& meta, int half, int left, uint4 (&r)[kLoads]) const {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int64_t at = meta.at[4 * half + 2 * x + (rs >> 4)];
@@ -188,12 +170,13 @@ struct Loader {
 #pragma unroll
             for (int p = 0; p < kPanels; ++p) {
                 r[x * kPanels + p] = make_uint4(0, 0, 0, 0);
-                if (there) r[x * kPanels + p] = __ldcg(reinterpret_cast<const uint4*>(cache + side + at + 64 * p));
+                if (there) r[x * kPanels + p] = __ldcg(reinterpret_cast<const uint4*>(cache + at + 64 * p));
             }
         }
     }
-    // NaN on V's side is written as 0 (0 * NaN would reach rows that do not see it) and reported.
-    __device__ __forceinline__ void put(uint8_t* base, bool v_side, const uint4 (&r)[kLoads], bool* nan) const {
+    // NaN on V's side is written as 0 (0 * NaN would reach rows that do not see it), and tile j noted among the first
+    // and last that hold any.
+    __device__ __forceinline__ void put(uint8_t* base, bool v_side, const uint4 (&r)[kLoads], int j, int* nan_tiles) const {
         __half2 acc[2] = {__float2half2_rn(0.0f), __float2half2_rn(0.0f)};
 #pragma unroll
         for (int x = 0; x < kLoads; ++x) {
@@ -210,7 +193,8 @@ struct Loader {
         }
         const __half2 a = __hadd2(acc[0], acc[1]);
         if (v_side && (__hisnan(__low2half(a)) || __hisnan(__high2half(a)))) {  // written again with 0 in NaN's place
-            *nan = true;
+            atomicMin(&nan_tiles[0], j);
+            atomicMax(&nan_tiles[1], j);
 #pragma unroll 1
             for (int x = 0; x < kLoads; ++x) {
                 const int off = (x % kPanels) * (kToks * 128) + (x / kPanels) * (32 * 128);
@@ -256,6 +240,38 @@ __device__ __forceinline__ bool page_ahead(const PromptParams& A, int seq, int h
         if (lane == 0) m.all_ok = all;
         __syncwarp();
         if (lane == 0) mbar_arrive(&meta_full[j % kMetaRing]);
+    }
+    return true;
+}
+
+// One side (K or V) of all tiles of an item, by a warpgroup: half a tile at a time, the other half's reads in flight.
+// entry(j): tile j's place in the order in which the products take the slots.
+template <int D, int kSlots, typename Entry>
+__device__ __forceinline__ bool expand_side(const PromptParams& A, bool v_side, int toks, int n, Entry entry, uint8_t* s_kv,
+                                            const TileMeta* metas, uint64_t* meta_full, uint64_t* meta_empty, uint64_t* full,
+                                            uint64_t* empty, int* nan_tiles, volatile int* abort) {
+    const int lane = threadIdx.x & 31;
+    Loader<D> ld(v_side ? A.v_cache : A.k_cache, threadIdx.x & 127);
+    uint4 ra[Loader<D>::kLoads], rb[Loader<D>::kLoads];
+    if (n > 0) {
+        if (!wait_all(&meta_full[0], 0, abort, A.wait_ns)) return false;
+        ld.fetch(metas[0], 0, toks, ra);
+    }
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+        const int e = entry(j), slot = e % kSlots, m = j % kMetaRing;
+        ld.fetch(metas[m], 1, toks - kToks * j, rb);
+        if (lane == 0) mbar_arrive(&meta_empty[m]);
+        if (!wait_all(&empty[slot], ((e / kSlots) & 1) ^ 1, abort, A.wait_ns)) return false;
+        uint8_t* base = s_kv + slot * (kToks * D * 2);
+        ld.put(base, v_side, ra, j, nan_tiles);
+        if (j + 1 < n) {
+            if (!wait_all(&meta_full[(j + 1) % kMetaRing], ((j + 1) / kMetaRing) & 1, abort, A.wait_ns)) return false;
+            ld.fetch(metas[(j + 1) % kMetaRing], 0, toks - kToks * (j + 1), ra);
+        }
+        ld.put(base + 64 * 128, v_side, rb, j, nan_tiles);
+        fence_proxy_async_smem();
+        mbar_arrive(&full[slot]);
     }
     return true;
 }
@@ -379,11 +395,17 @@ __device__ __forceinline__ float weights_and_max(uint32_t at, const TileMeta& me
     return l;
 }
 
-// Some V holds NaN (expanded as 0): dims [c0, c0 + N) of a row that sees tokens [lo, pos] are NaN where one is.
+// Some V of the tokens [from, to] holds NaN (expanded as 0): dims [c0, c0 + N) of a row that sees tokens [lo, pos]
+// are NaN where one of those is.
 template <int D, int N>
-__device__ __forceinline__ void mark_nan(const PromptParams& A, int seq, int head, int lo, int pos, int c0, float (&y)[N]) {
+__device__ __forceinline__ void mark_nan(const PromptParams& A, int seq, int head, int lo, int pos, int from, int to, int c0,
+                                         float (&y)[N]) {
+    lo = max(lo, from);
+    pos = min(pos, to);
+    int p = -1;
+#pragma unroll 1
     for (int tok = lo; tok <= pos; ++tok) {
-        const int p = page_id(A.B, seq, tok >> A.B.page_shift, nullptr);
+        if (tok == lo || (tok & 15) == 0) p = page_id(A.B, seq, tok >> A.B.page_shift, nullptr);
         if (p < 0) continue;
         const uint4* v = reinterpret_cast<const uint4*>(
             A.v_cache + ((((int64_t)p * A.kv_heads + head) << A.B.page_shift) + (tok & ((1 << A.B.page_shift) - 1))) * D + c0);
@@ -398,28 +420,47 @@ __device__ __forceinline__ void mark_nan(const PromptParams& A, int seq, int hea
     }
 }
 
-template <typename T, int D>
+// ---------------------------------------------------------------------------------------------------
+// Both kernels: warps 0-7 softmax or sums, 8-11 expand K, 12-15 V, warp 16 issues the products, warp 17 looks the
+// pages and scales up (18-19 idle).
+constexpr int kThreads = 640;
+constexpr int kKWarp = 8, kVWarp = 12, kMmaWarp = 16, kPageWarp = 17;
+constexpr int kRegsAll = 5 * (65536 / kThreads / 8 * 8);  // what a launch gives a thread, times the warpgroups
+
+// fp32 rows: 128 a CTA, queries and P in two fp16 terms. S and O have two tiles each in tensor memory, so that S of
+// the next tokens is multiplied while the softmax of these is computed. O of each 128 tokens is a fresh
+// accumulator that warps 4-7 add to fp32 sums in registers: the tensor core's own accumulation does not round to
+// nearest, and the running maximum's correction costs nothing more there. Order of the slots: K0, K1, V0, K2,
+// V1, ..., V(n-1).
+constexpr int kRegsSoftmax1 = 104, kRegsSums1 = 176, kRegsLoad1 = 72, kRegsCtrl1 = 56;
+static_assert(kRegsSoftmax1 + kRegsSums1 + 2 * kRegsLoad1 + kRegsCtrl1 <= kRegsAll, "register split");
+
+template <int D>
+struct Layout1 {
+    static constexpr int kTile = kToks * D * 2;  // a K or V tile, and one term of the queries
+    static constexpr int kSlots = 4;             // at most 6: kMetaRing holds what is in flight
+    static constexpr int kBytes = 1024 + 2 * kTile + kSlots * kTile;
+};
+
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_constant__ PromptParams A) {
-    constexpr bool HL = sizeof(T) == 4;
-    using L = Layout<HL, D>;
+    using L = Layout1<D>;
     constexpr uint32_t kColS = 0, kColO = 256;  // tensor memory: two S tiles, two O tiles
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* s_q = smem;
-    uint8_t* s_kv = smem + L::kQ;
+    uint8_t* s_kv = smem + 2 * L::kTile;
     __shared__ __align__(8) uint64_t full[L::kSlots], empty[L::kSlots], meta_full[kMetaRing], meta_empty[kMetaRing];
     __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], fin, drain;
     __shared__ TileMeta s_meta[kMetaRing];
     __shared__ float s_c[kRows], s_corr[2][kRows], s_inv[kRows];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_item[5];
+    __shared__ int s_item[5], s_nan[2];
     __shared__ volatile int s_abort;
-    __shared__ volatile int s_nan;
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-
     if (warp == 0) find_item(A, kRows, s_item);
     if (tid == 32) {
         for (int i = 0; i < L::kSlots; ++i) {
@@ -428,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         }
         for (int i = 0; i < kMetaRing; ++i) {
             mbar_init(&meta_full[i], 1);
-            mbar_init(&meta_empty[i], 8);  // the warps of the softmax and of the loaders
+            mbar_init(&meta_empty[i], 12);  // the warps of the softmax and of the loaders
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
@@ -440,7 +481,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         mbar_init(&drain, 1);
         fence_mbar_init();
         s_abort = 0;
-        s_nan = 0;
+        s_nan[0] = 0x7FFFFFFF;
+        s_nan[1] = -1;
     }
     __syncthreads();
     const int seq = s_item[0];
@@ -460,42 +502,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         tmem_alloc(&s_tmem, 512);
         tmem_relinquish();
     }
-    // queries: two threads a row, D/2 dims each, scaled by a power of two into fp16's range
-    if (tid < 256) {
-        const int row = tid >> 1, half = tid & 1, r = r0 + row;
+    // queries: four threads a row, D/4 dims each, scaled by a power of two into fp16's range
+    if (tid < 4 * kRows) {
+        const int row = tid >> 2, part = tid & 3, r = r0 + row;
         const bool valid = r < rows;
-        const T* p = static_cast<const T*>(A.q) + (int64_t)(start + (valid ? r / A.group : 0)) * A.q_stride +
-                     (int64_t)(head * A.group + (valid ? r % A.group : 0)) * D + half * (D / 2);
-        float x[D / 2];
-        Vec<T>::load(p, x);
+        const float* p = static_cast<const float*>(A.q) + (int64_t)(start + (valid ? r / A.group : 0)) * A.q_stride +
+                         (int64_t)(head * A.group + (valid ? r % A.group : 0)) * D + part * (D / 4);
+        float x[D / 4];
+        Vec<float>::load(p, x);
         float amax = 0.0f;
 #pragma unroll
-        for (int i = 0; i < D / 2; ++i) {
+        for (int i = 0; i < D / 4; ++i) {
             if (!valid) x[i] = 0.0f;
             const float a = fabsf(x[i]);
             if (a <= 3.402823466e38f) amax = fmaxf(amax, a);
         }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         const int e = amax > 0.0f ? min(max(134 - (int)(__float_as_uint(amax) >> 23), -120), 120) : 0;
         const float up = A.sign * exp2_int(e);
-        if (half == 0) s_c[row] = A.scale_log2 * exp2_int(-e);
+        if (part == 0) s_c[row] = A.scale_log2 * exp2_int(-e);
 #pragma unroll
-        for (int u = 0; u < D / 16; ++u) {  // 8 dims a unit
-            const int unit = half * (D / 16) + u;
+        for (int u = 0; u < D / 32; ++u) {  // 8 dims a unit
+            const int unit = part * (D / 32) + u;
             uint8_t* dst = s_q + (unit >> 3) * (kRows * 128) + row * 128 + (((unit & 7) ^ (row & 7)) << 4);
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float a = x[8 * u + 2 * i] * up, b = x[8 * u + 2 * i + 1] * up;
                 const __half2 h = __floats2half2_rn(a, b);
+                const float2 f = __half22float2(h);
                 hi[i] = h2_bits(h);
-                if (HL) {
-                    const float2 f = __half22float2(h);
-                    lo[i] = h2_bits(__floats2half2_rn(a - f.x, b - f.y));
-                }
+                lo[i] = h2_bits(__floats2half2_rn(a - f.x, b - f.y));
             }
             *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if (HL) *reinterpret_cast<uint4*>(dst + L::kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4*>(dst + L::kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         fence_proxy_async_smem();
     }
@@ -505,105 +546,74 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     const uint32_t tmem = s_tmem;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_all(bar, parity, &s_abort, A.wait_ns); };
+    // the place of tile j's K and V in the order of the slots
+    auto k_entry = [](int j) { return j == 0 ? 0 : 2 * j - 1; };
+    auto v_entry = [n](int j) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; };
 
-    if (warp >= kLoadWarp && warp < kMmaWarp) {
-        regs_dec<kRegsLoad>();
-        // ---------------- cache to fp16 tiles, half a tile at a time, the other half's reads in flight. Order of
-        // the slots: K0, K1, V0, K2, V1, ..., V(n-1)
-        Loader<D> ld(A.k_cache, tid - 32 * kLoadWarp);
-        const int64_t to_v = A.v_cache - A.k_cache;
-        // step s: half s & 1 of slot s >> 1, whose tile and side are
-        auto tile_of = [&](int s) { return s < 2 ? 0 : s >= 4 * n - 2 ? n - 1 : (s >> 1) & 1 ? (s + 2) >> 2 : (s >> 2) - 1; };
-        auto is_v = [&](int s) { return s >= 4 * n - 2 || (s >= 2 && !((s >> 1) & 1)); };
-        auto fetch = [&](int s, uint4 (&r)[Loader<D>::kLoads]) {
-            const int j = tile_of(s), half = s & 1;
-            const bool v_side = is_v(s);
-            if (half == 0 && !v_side && !wait(&meta_full[j % kMetaRing], (j / kMetaRing) & 1)) return false;
-            ld.fetch(s_meta[j % kMetaRing], half, kv_hi - kv0 - kToks * j, r, v_side ? to_v : 0);
-            if (half == 1 && v_side && lane == 0) mbar_arrive(&meta_empty[j % kMetaRing]);
-            return true;
-        };
-        int slot = 0, uses = 0;
-        bool nan = false;
-        uint4 ra[Loader<D>::kLoads], rb[Loader<D>::kLoads];
-        const int steps = 4 * n;
-        if (n > 0) ok = fetch(0, ra);
-#pragma unroll 1
-        for (int s = 0; s < steps && ok; s += 2) {
-            ok = fetch(s + 1, rb) && wait(&empty[slot], (uses & 1) ^ 1);
-            if (!ok) break;
-            const bool v_side = is_v(s);
-            uint8_t* base = s_kv + slot * L::kTile;
-            ld.put(base, v_side, ra, &nan);
-            if (s + 2 < steps && !(ok = fetch(s + 2, ra))) break;
-            ld.put(base + 64 * 128, v_side, rb, &nan);
-            fence_proxy_async_smem();
-            mbar_arrive(&full[slot]);
-            if (++slot == L::kSlots) { slot = 0; ++uses; }
-        }
-        if (nan) s_nan = 1;
-        mbar_arrive(&fin);
-    } else if (warp >= kMmaWarp) {
-        regs_dec<kRegsMma>();
+    if (warp >= kMmaWarp) {
+        regs_dec<kRegsCtrl1>();
         if (warp == kMmaWarp) {
-        // ---------------- products, issued by one elected lane of the warp
-        const uint32_t idesc_s = idesc_f16_f32(kRows, kToks);
-        const uint32_t idesc_o = idesc_f16_f32(kRows, D) | kIdescBMnMajor;
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const uint32_t q_at = __shfl_sync(0xffffffffu, smem_u32(s_q), 0), kv_at = q_at + L::kQ;
-        int slot = 0, uses = 0;
-        bool issued = false;
-        auto next_slot = [&]() { if (++slot == L::kSlots) { slot = 0; ++uses; } };
-        auto scores = [&](int j) {
-            if (!wait(&full[slot], uses & 1)) return false;
-            tc_fence_after();
-            const uint32_t d = tm + kColS + (j & 1) * kToks;
-            const uint64_t b = desc_sw128_kmajor(kv_at + slot * L::kTile);
-#pragma unroll
-            for (int t = 0; t < L::kTerms; ++t) {
-                const uint64_t a = desc_sw128_kmajor(q_at + t * L::kTile);
-#pragma unroll
-                for (int k = 0; k < D / 64; ++k)
-                    mma_f16_ss_elect4(d, a + ((k * kToks * 128) >> 4), b + ((k * kToks * 128) >> 4), 2, 2, idesc_s, t + k);
-            }
-            mma_commit_elect(&s_full[j & 1]);
-            mma_commit_elect(&empty[slot]);
-            issued = true;
-            next_slot();
-            return true;
-        };
+            // ---------------- products, issued by one elected lane of the warp
+            const uint32_t idesc_s = idesc_f16_f32(kRows, kToks);
+            const uint32_t idesc_o = idesc_f16_f32(kRows, D) | kIdescBMnMajor;
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t q_at = __shfl_sync(0xffffffffu, smem_u32(s_q), 0), kv_at = q_at + 2 * L::kTile;
+            bool issued = false;
 #pragma unroll 1
-        for (int j = -1; j < n && ok; ++j) {
-            if (j + 1 < n && !(ok = scores(j + 1))) break;
-            if (j < 0) continue;
-            // P of these tokens (o_empty of the tile two before is implied: the softmax waited for it)
-            ok = wait(&p_full[j & 1], (j >> 1) & 1) && wait(&full[slot], uses & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t p = tm + kColS + (j & 1) * kToks, d = tm + kColO + (j & 1) * D;
-            const uint64_t b = desc_sw128_mnmajor(kv_at + slot * L::kTile, kToks * 128);
-            // 32 tokens' P in the 32 columns of their S: 16 of the high term, 16 of the low
+            for (int j = -1; j < n && ok && n > 0; ++j) {
+                if (j + 1 < n) {
+                    const int e = k_entry(j + 1), slot = e % L::kSlots;
+                    ok = wait(&full[slot], (e / L::kSlots) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t b = desc_sw128_kmajor(kv_at + slot * L::kTile);
 #pragma unroll
-            for (int t = 0; t < L::kTerms; ++t)
+                    for (int t = 0; t < 2; ++t) {
+                        const uint64_t a = desc_sw128_kmajor(q_at + t * L::kTile);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)  // k steps 0, 2, 4, 6, then 1, 3, 5, 7: 32 columns apart
-                    mma_f16_ts_elect4(d, p + 8 * h + 16 * t, b + ((h * 16 * 128) >> 4), 32, (32 * 128) >> 4, idesc_o, t + h);
-            mma_commit_elect(&o_full[j & 1]);
-            mma_commit_elect(&empty[slot]);
-            next_slot();
-        }
-        if (!ok && issued) {  // outstanding products finish before tensor memory is freed
-            volatile int never = 0;
-            mma_commit_elect(&drain);
-            mbar_wait(&drain, 0, &never);
-        }
-        __syncwarp();
+                        for (int k = 0; k < D / 64; ++k)
+                            mma_f16_ss_elect4(tm + kColS + ((j + 1) & 1) * kToks, a + ((k * kToks * 128) >> 4),
+                                              b + ((k * kToks * 128) >> 4), 2, 2, idesc_s, t + k);
+                    }
+                    mma_commit_elect(&s_full[(j + 1) & 1]);
+                    mma_commit_elect(&empty[slot]);
+                    issued = true;
+                }
+                if (j < 0) continue;
+                // P of these tokens (o_empty of the tile two before is implied: the softmax waited for it)
+                const int e = v_entry(j), slot = e % L::kSlots;
+                ok = wait(&p_full[j & 1], (j >> 1) & 1) && wait(&full[slot], (e / L::kSlots) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t p = tm + kColS + (j & 1) * kToks, d = tm + kColO + (j & 1) * D;
+                const uint64_t b = desc_sw128_mnmajor(kv_at + slot * L::kTile, kToks * 128);
+                // 32 tokens' P in the 32 columns of their S: 16 of the high term, 16 of the low
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)  // k steps 0, 2, 4, 6, then 1, 3, 5, 7: 32 columns apart
+                        mma_f16_ts_elect4(d, p + 8 * h + 16 * t, b + ((h * 16 * 128) >> 4), 32, (32 * 128) >> 4, idesc_o, t + h);
+                mma_commit_elect(&o_full[j & 1]);
+                mma_commit_elect(&empty[slot]);
+            }
+            if (!ok && issued) {  // outstanding products finish before tensor memory is freed
+                volatile int never = 0;
+                mma_commit_elect(&drain);
+                mbar_wait(&drain, 0, &never);
+            }
+            __syncwarp();
         } else if (warp == kPageWarp) {
             ok = page_ahead<D>(A, seq, head, kv0, kv_hi, n, s_meta, meta_full, meta_empty, &s_abort);
         }
+    } else if (warp >= kKWarp) {
+        regs_dec<kRegsLoad1>();
+        const bool v_side = warp >= kVWarp;
+        ok = expand_side<D, L::kSlots>(A, v_side, kv_hi - kv0, n, [&](int j) { return v_side ? v_entry(j) : k_entry(j); }, s_kv,
+                                       s_meta, meta_full, meta_empty, full, empty, s_nan, &s_abort);
+        if (v_side) mbar_arrive(&fin);
     } else if (warp < 4) {
-        regs_inc<kRegsSoftmax>();
         // ---------------- softmax: thread = row = tensor memory lane
+        regs_inc<kRegsSoftmax1>();
         const int r = r0 + tid;
         const bool valid = r < rows;
         const int pos = first + (valid ? r / A.group : 0);
@@ -630,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             if (j >= 2) ok = wait(&o_empty[b], ((j >> 1) - 1) & 1);
             if (!ok) break;
             s_corr[b][tid] = corr;
-            l += weights<HL>(at, meta, crow, m_use, t0, lo, hi, whole);
+            l += weights<true>(at, meta, crow, m_use, t0, lo, hi, whole);
             if (lane == 0) mbar_arrive(&meta_empty[j % kMetaRing]);
             tmem_wait_st();
             tc_fence_before();
@@ -639,8 +649,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         s_inv[tid] = l == 0.0f ? 0.0f : 1.0f / l;  // 0: the row sees nothing
         mbar_arrive(&fin);
     } else {
-        regs_inc<kRegsSums>();
         // ---------------- sums: thread = row
+        regs_inc<kRegsSums1>();
         const int row = tid - 128, r = r0 + row;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         float2 acc[D / 2];
@@ -669,28 +679,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             mbar_arrive(&o_empty[b]);
         }
         ok = ok && wait(&fin, 0);  // the denominators, and the loaders' report of NaN
-        if (ok && s_nan && r < rows) {
-            const int pos = first + r / A.group;
-            float y[D];
-#pragma unroll
-            for (int c = 0; c < D; ++c) y[c] = c & 1 ? acc[c / 2].y : acc[c / 2].x;
-            mark_nan<D, D>(A, seq, head, A.window > 0 ? max(pos - A.window + 1, 0) : 0, pos, 0, y);
-#pragma unroll
-            for (int c = 0; c < D; c += 2) acc[c / 2] = make_float2(y[c], y[c + 1]);
-        }
         if (ok && r < rows) {
             const float inv = s_inv[row];
-            T* o = static_cast<T*>(A.out) + (int64_t)(start + r / A.group) * A.out_stride +
-                   (int64_t)(head * A.group + r % A.group) * D;
+            const int pos = first + r / A.group;
+            float* o = static_cast<float*>(A.out) + (int64_t)(start + r / A.group) * A.out_stride +
+                       (int64_t)(head * A.group + r % A.group) * D;
 #pragma unroll
-            for (int c = 0; c < D; c += 8) {
-                float y[8];
+            for (int c = 0; c < D; c += 16) {
+                float y[16];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float x = k & 1 ? acc[(c + k) / 2].y : acc[(c + k) / 2].x;
-                    y[k] = x * inv;  // a row that sees nothing: 0 * 0
-                }
-                Vec<T>::store(o + c, y);
+                for (int k = 0; k < 16; ++k) y[k] = (k & 1 ? acc[(c + k) / 2].y : acc[(c + k) / 2].x) * inv;  // sees nothing: 0 * 0
+                if (s_nan[1] >= 0)
+                    mark_nan<D, 16>(A, seq, head, A.window > 0 ? max(pos - A.window + 1, 0) : 0, pos, kv0 + kToks * s_nan[0],
+                                    kv0 + kToks * (s_nan[1] + 1) - 1, c, y);
+                Vec<float>::store(o + c, y);
             }
         }
     }
@@ -704,18 +706,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// ---------------------------------------------------------------------------------------------------
 // bf16 rows: 256 query rows a CTA, two tiles of 128 that share every K and V tile, so the cache is
 // expanded to fp16 half as often, and one tile's softmax runs while the other's products do. The sums stay
 // in tensor memory over all tokens (their rounding is far below a bf16 output's), scaled again only when a row's
 // maximum has grown by more than 2^8 since its reference was taken: P then stays within fp16.
 //
-// Roles: warps 0-3 and 4-7 the softmax of a tile each (thread = row) and its store, 8-11 expand K, 12-15 V,
-// warp 16 issues the products, warp 17 looks the pages and scales up (18-19 idle).
-constexpr int kThreads2 = 640;
-constexpr int kKWarp2 = 8, kVWarp2 = 12, kMmaWarp2 = 16, kPageWarp2 = 17;
+// Warps 0-3 and 4-7 are the softmax of a tile each (thread = row) and its store.
 constexpr int kRegsSoftmax2 = 136, kRegsLoad2 = 72, kRegsCtrl2 = 64;
-static_assert(2 * kRegsSoftmax2 + 2 * kRegsLoad2 + kRegsCtrl2 <= 5 * (65536 / kThreads2 / 8 * 8), "register split");
+static_assert(2 * kRegsSoftmax2 + 2 * kRegsLoad2 + kRegsCtrl2 <= kRegsAll, "register split");
 constexpr float kSlack = 8.0f;  // log2 growth of a row's maximum before its sums are scaled again
 
 template <int D>
@@ -726,7 +724,7 @@ struct Layout2 {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads2, 1) attn_prompt2_kernel(const __grid_constant__ PromptParams A) {
+__global__ void __launch_bounds__(kThreads, 1) attn_prompt2_kernel(const __grid_constant__ PromptParams A) {
     using L = Layout2<D>;
     constexpr uint32_t kColS = 0, kColO = 256;  // tensor memory: S (then P) and O of both row tiles
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -738,9 +736,8 @@ __global__ void __launch_bounds__(kThreads2, 1) attn_prompt2_kernel(const __grid
     __shared__ TileMeta s_meta[kMetaRing];
     __shared__ float s_c[2 * kRows];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_item[5];
+    __shared__ int s_item[5], s_nan[2];
     __shared__ volatile int s_abort;
-    __shared__ volatile int s_nan;
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -764,7 +761,8 @@ __global__ void __launch_bounds__(kThreads2, 1) attn_prompt2_kernel(const __grid
         mbar_init(&drain, 1);
         fence_mbar_init();
         s_abort = 0;
-        s_nan = 0;
+        s_nan[0] = 0x7FFFFFFF;
+        s_nan[1] = -1;
     }
     __syncthreads();
     const int seq = s_item[0];
@@ -778,7 +776,7 @@ __global__ void __launch_bounds__(kThreads2, 1) attn_prompt2_kernel(const __grid
     const int kv0 = kv_lo & ~15;
     const int n = (kv_hi - kv0 + kToks - 1) / kToks;  // tiles; 0: no row sees anything
 
-    if (warp == kMmaWarp2) {
+    if (warp == kMmaWarp) {
         tmem_alloc(&s_tmem, 512);
         tmem_relinquish();
     }
@@ -828,9 +826,9 @@ __global__ void __launch_bounds__(kThreads2, 1) attn_prompt2_kernel(const __grid
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_all(bar, parity, &s_abort, A.wait_ns); };
 
-    if (warp >= kMmaWarp2) {
+    if (warp >= kMmaWarp) {
         regs_dec<kRegsCtrl2>();
-        if (warp == kMmaWarp2) {
+        if (warp == kMmaWarp) {
             // ---------------- products, issued by one elected lane of the warp
             const uint32_t idesc_s = idesc_f16_f32(kRows, kToks);
             const uint32_t idesc_o = idesc_f16_f32(kRows, D) | kIdescBMnMajor;
@@ -876,38 +874,14 @@ __global__ void __launch_bounds__(kThreads2, 1) attn_prompt2_kernel(const __grid
                 mbar_wait(&drain, 0, &never);
             }
             __syncwarp();
-        } else if (warp == kPageWarp2) {
+        } else if (warp == kPageWarp) {
             ok = page_ahead<D>(A, seq, head, kv0, kv_hi, n, s_meta, meta_full, meta_empty, &s_abort);
         }
-    } else if (warp >= kKWarp2) {
+    } else if (warp >= kKWarp) {
         regs_dec<kRegsLoad2>();
-        // ---------------- cache to fp16 tiles: a warpgroup for K, one for V
-        const bool v_side = warp >= kVWarp2;
-        const int i = tid & 127;
-        Loader<D> ld(v_side ? A.v_cache : A.k_cache, i);
-        bool nan = false;
-        uint4 ra[Loader<D>::kLoads], rb[Loader<D>::kLoads];
-        ok = n == 0 || wait(&meta_full[0], 0);
-        if (n > 0 && ok) ld.fetch(s_meta[0], 0, kv_hi - kv0, ra);
-#pragma unroll 1
-        for (int j = 0; j < n && ok; ++j) {
-            const int slot = (2 * j + v_side) % L::kSlots, m = j % kMetaRing;
-            ld.fetch(s_meta[m], 1, kv_hi - kv0 - kToks * j, rb);
-            if (lane == 0) mbar_arrive(&meta_empty[m]);
-            ok = wait(&empty[slot], (((2 * j + v_side) / L::kSlots) & 1) ^ 1);
-            if (!ok) break;
-            uint8_t* base = s_kv + slot * L::kTile;
-            ld.put(base, v_side, ra, &nan);
-            if (j + 1 < n) {
-                ok = wait(&meta_full[(j + 1) % kMetaRing], ((j + 1) / kMetaRing) & 1);
-                if (!ok) break;
-                ld.fetch(s_meta[(j + 1) % kMetaRing], 0, kv_hi - kv0 - kToks * (j + 1), ra);
-            }
-            ld.put(base + 64 * 128, v_side, rb, &nan);
-            fence_proxy_async_smem();
-            mbar_arrive(&full[slot]);
-        }
-        if (nan) s_nan = 1;
+        const bool v_side = warp >= kVWarp;
+        ok = expand_side<D, L::kSlots>(A, v_side, kv_hi - kv0, n, [&](int j) { return 2 * j + v_side; }, s_kv, s_meta, meta_full,
+                                       meta_empty, full, empty, s_nan, &s_abort);
         if (v_side) mbar_arrive(&fin);
     } else {
         regs_inc<kRegsSoftmax2>();
@@ -991,7 +965,8 @@ __global__ void __launch_bounds__(kThreads2, 1) attn_prompt2_kernel(const __grid
                 }
 #pragma unroll
                 for (int c = 0; c < 32; ++c) y[c] = inv == 0.0f ? 0.0f : __uint_as_float(v[c]) * inv;
-                if (s_nan && valid) mark_nan<D, 32>(A, seq, head, lo, pos, 32 * q, y);
+                if (s_nan[1] >= 0 && valid)
+                    mark_nan<D, 32>(A, seq, head, lo, pos, kv0 + kToks * s_nan[0], kv0 + kToks * (s_nan[1] + 1) - 1, 32 * q, y);
                 if (valid) Vec<__nv_bfloat16>::store(o + 32 * q, y);
             }
         }
@@ -1003,24 +978,22 @@ __global__ void __launch_bounds__(kThreads2, 1) attn_prompt2_kernel(const __grid
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kMmaWarp2) tmem_dealloc(tmem, 512);
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 template <typename T, int D>
 cudaError_t launch_typed(const PromptParams& P, cudaStream_t stream) {
     constexpr bool HL = sizeof(T) == 4;
     void (*kern)(PromptParams);
-    int bytes, rows, threads;
+    int bytes, rows;
     if constexpr (HL) {
-        kern = attn_prompt_kernel<T, D>;
-        bytes = Layout<HL, D>::kBytes;
+        kern = attn_prompt_kernel<D>;
+        bytes = Layout1<D>::kBytes;
         rows = kRows;
-        threads = kThreads;
     } else {
         kern = attn_prompt2_kernel<D>;
         bytes = Layout2<D>::kBytes;
         rows = 2 * kRows;
-        threads = kThreads2;
     }
     // every CTA holds all of its SM's tensor memory: enough shared memory that one fits
     const int smem = bytes < 144 * 1024 ? 144 * 1024 : bytes;
@@ -1039,7 +1012,7 @@ cudaError_t launch_typed(const PromptParams& P, cudaStream_t stream) {
     if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)items);
-    cfg.blockDim = dim3((unsigned)threads);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
