@@ -354,8 +354,8 @@ __device__ __forceinline__ float weights(uint32_t at, const TileMeta& meta, floa
                 const __half2 hh = __floats2half2_rn(p[k].x, p[k].y);
                 pk[8 * h + k] = h2_bits(hh);
                 if constexpr (HL) {
-                    const float2 f = __half22float2(hh);
-                    pk[16 + 8 * h + k] = h2_bits(__floats2half2_rn(p[k].x - f.x, p[k].y - f.y));
+                    const float2 f = fma2(__half22float2(hh), make_float2(-1.0f, -1.0f), p[k]);
+                    pk[16 + 8 * h + k] = h2_bits(__floats2half2_rn(f.x, f.y));
                 }
             }
         }
@@ -430,7 +430,8 @@ constexpr int kRegsAll = 5 * (65536 / kThreads / 8 * 8);  // what a launch gives
 // fp32 rows: 128 a CTA, queries and P in two fp16 terms. S and O have two tiles each in tensor memory, so that S of
 // the next tokens is multiplied while the softmax of these is computed. O of each 128 tokens is a fresh
 // accumulator that warps 4-7 add to fp32 sums in registers: the tensor core's own accumulation does not round to
-// nearest, and the running maximum's correction costs nothing more there. Order of the slots: K0, K1, V0, K2,
+// nearest, and the running maximum's correction costs nothing more there. They also find the maximum of the next S, while
+// warps 0-3 make P of this one, the longest step. Order of the slots: K0, K1, V0, K2,
 // V1, ..., V(n-1).
 constexpr int kRegsSoftmax1 = 104, kRegsSums1 = 176, kRegsLoad1 = 72, kRegsCtrl1 = 56;
 static_assert(kRegsSoftmax1 + kRegsSums1 + 2 * kRegsLoad1 + kRegsCtrl1 <= kRegsAll, "register split");
@@ -451,9 +452,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     uint8_t* s_q = smem;
     uint8_t* s_kv = smem + 2 * L::kTile;
     __shared__ __align__(8) uint64_t full[L::kSlots], empty[L::kSlots], meta_full[kMetaRing], meta_empty[kMetaRing];
-    __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], fin, drain;
+    __shared__ __align__(8) uint64_t s_full[2], max_full[2], p_full[2], o_full[2], fin, drain;
     __shared__ TileMeta s_meta[kMetaRing];
-    __shared__ float s_c[kRows], s_corr[2][kRows], s_inv[kRows];
+    __shared__ float s_c[kRows], s_ref[2][kRows], s_inv[kRows];
     __shared__ uint32_t s_tmem;
     __shared__ int s_item[5], s_nan[2];
     __shared__ volatile int s_abort;
@@ -469,13 +470,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         }
         for (int i = 0; i < kMetaRing; ++i) {
             mbar_init(&meta_full[i], 1);
-            mbar_init(&meta_empty[i], 12);  // the warps of the softmax and of the loaders
+            mbar_init(&meta_empty[i], 16);  // the warps of the softmax, of the sums and of the loaders
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 128);
             mbar_init(&o_full[i], 1);
-            mbar_init(&o_empty[i], 128);
+            mbar_init(&max_full[i], 128);
         }
         mbar_init(&fin, 256);
         mbar_init(&drain, 1);
@@ -580,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     issued = true;
                 }
                 if (j < 0) continue;
-                // P of these tokens (o_empty of the tile two before is implied: the softmax waited for it)
+                // P of these tokens; O of the tile two before has been taken (its reader found this one's maximum after)
                 const int e = v_entry(j), slot = e % L::kSlots;
                 ok = wait(&p_full[j & 1], (j >> 1) & 1) && wait(&full[slot], (e / L::kSlots) & 1);
                 if (!ok) break;
@@ -620,27 +621,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         const int hi = valid ? pos + 1 : 0, lo = A.window > 0 ? max(pos - A.window + 1, 0) : 0;
         const float crow = s_c[tid];
         const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
-        float m = -INFINITY, l = 0.0f;
+        float ref = -INFINITY, l = 0.0f;
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
             const int b = j & 1;
-            ok = wait(&meta_full[j % kMetaRing], (j / kMetaRing) & 1) && wait(&s_full[b], (j >> 1) & 1);
+            ok = wait(&max_full[b], (j >> 1) & 1);  // S and its scales, too
             if (!ok) break;
             tc_fence_after();
             const TileMeta& meta = s_meta[j % kMetaRing];
             const int t0 = kv0 + kToks * j;
             const bool whole = meta.all_ok && t0 >= full_lo && t0 + kToks <= full_hi;
-            const uint32_t at = tmem + lane_base + kColS + b * kToks;
-            const float top = row_max(at, meta, crow, t0, lo, hi, whole);
-            const float m_new = fmaxf(m, top), m_use = m_new == -INFINITY ? 0.0f : m_new;
-            const float corr = ex2(m - m_use);
-            m = m_new;
-            l *= corr;
-            // the sums have taken the tile two before this one
-            if (j >= 2) ok = wait(&o_empty[b], ((j >> 1) - 1) & 1);
-            if (!ok) break;
-            s_corr[b][tid] = corr;
-            l += weights<true>(at, meta, crow, m_use, t0, lo, hi, whole);
+            const float r_new = s_ref[b][tid];  // -inf while the row has seen nothing
+            const float use = r_new == -INFINITY ? 0.0f : r_new;
+            l *= ex2(ref - use);
+            ref = r_new;
+            l += weights<true>(tmem + lane_base + kColS + b * kToks, meta, crow, use, t0, lo, hi, whole);
             if (lane == 0) mbar_arrive(&meta_empty[j % kMetaRing]);
             tmem_wait_st();
             tc_fence_before();
@@ -649,21 +644,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         s_inv[tid] = l == 0.0f ? 0.0f : 1.0f / l;  // 0: the row sees nothing
         mbar_arrive(&fin);
     } else {
-        // ---------------- sums: thread = row
+        // ---------------- maxima and sums: thread = row
         regs_inc<kRegsSums1>();
         const int row = tid - 128, r = r0 + row;
-        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+        const bool valid = r < rows;
+        const int pos = first + (valid ? r / A.group : 0);
+        const int hi = valid ? pos + 1 : 0, lo = A.window > 0 ? max(pos - A.window + 1, 0) : 0;
+        const float crow = s_c[row];
+        const uint32_t lane_at = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        float m = -INFINITY, corr = 0.0f, corr_last = 0.0f;
         float2 acc[D / 2];
 #pragma unroll
         for (int c = 0; c < D / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
 #pragma unroll 1
-        for (int j = 0; j < n; ++j) {
-            const int b = j & 1;
-            ok = wait(&p_full[b], (j >> 1) & 1) && wait(&o_full[b], (j >> 1) & 1);
+        for (int j = 0; j <= n && n > 0; ++j) {
+            if (j < n) {
+                const int b = j & 1;
+                ok = wait(&meta_full[j % kMetaRing], (j / kMetaRing) & 1) && wait(&s_full[b], (j >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const TileMeta& meta = s_meta[j % kMetaRing];
+                const int t0 = kv0 + kToks * j;
+                const bool whole = meta.all_ok && t0 >= full_lo && t0 + kToks <= full_hi;
+                const float m_new = fmaxf(m, row_max(lane_at + kColS + b * kToks, meta, crow, t0, lo, hi, whole));
+                corr_last = corr;
+                corr = ex2(m - (m_new == -INFINITY ? 0.0f : m_new));
+                m = m_new;
+                s_ref[b][row] = m_new;
+                if (lane == 0) mbar_arrive(&meta_empty[j % kMetaRing]);
+                tc_fence_before();
+                mbar_arrive(&max_full[b]);
+            } else {
+                corr_last = corr;
+            }
+            if (j == 0) continue;
+            ok = wait(&o_full[(j - 1) & 1], ((j - 1) >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            const float corr = s_corr[b][row];
-            const uint32_t at = tmem + lane_base + kColO + b * D;
+            const uint32_t at = lane_at + kColO + ((j - 1) & 1) * D;
             uint32_t v[2][16];
             tmem_ld16(at, v[0]);
 #pragma unroll
@@ -672,16 +690,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 if (q + 1 < D / 16) tmem_ld16(at + 16 * (q + 1), v[(q + 1) & 1]);
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
-                    acc[8 * q + c] = fma2(acc[8 * q + c], make_float2(corr, corr),
+                    acc[8 * q + c] = fma2(acc[8 * q + c], make_float2(corr_last, corr_last),
                                           make_float2(__uint_as_float(v[q & 1][2 * c]), __uint_as_float(v[q & 1][2 * c + 1])));
             }
             tc_fence_before();
-            mbar_arrive(&o_empty[b]);
         }
         ok = ok && wait(&fin, 0);  // the denominators, and the loaders' report of NaN
-        if (ok && r < rows) {
+        if (ok && valid) {
             const float inv = s_inv[row];
-            const int pos = first + r / A.group;
             float* o = static_cast<float*>(A.out) + (int64_t)(start + r / A.group) * A.out_stride +
                        (int64_t)(head * A.group + r % A.group) * D;
 #pragma unroll
@@ -690,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
 #pragma unroll
                 for (int k = 0; k < 16; ++k) y[k] = (k & 1 ? acc[(c + k) / 2].y : acc[(c + k) / 2].x) * inv;  // sees nothing: 0 * 0
                 if (s_nan[1] >= 0)
-                    mark_nan<D, 16>(A, seq, head, A.window > 0 ? max(pos - A.window + 1, 0) : 0, pos, kv0 + kToks * s_nan[0],
+                    mark_nan<D, 16>(A, seq, head, lo, pos, kv0 + kToks * s_nan[0],
                                     kv0 + kToks * (s_nan[1] + 1) - 1, c, y);
                 Vec<float>::store(o + c, y);
             }
