@@ -316,51 +316,81 @@ __device__ __forceinline__ float row_max(uint32_t at, const TileMeta& meta, floa
     return top;
 }
 
-// P = 2^(x - ref + 7) of a row in the place of its S, and the row's share of the denominator. 32 tokens' P
-// take 16 columns of one fp16 term, or the 32 of their S for two, hi then lo: columns of S that have been read.
-template <bool HL>
+// P of one group's 16 tokens, packed to fp16 (and what that leaves, packed to fp16: lo8, where wanted), and its sum.
+__device__ __forceinline__ float group_weights(const uint32_t* v, const TileMeta& meta, int g, float crow, float ref, int t0,
+                                               int lo, int hi, bool whole, uint32_t* hi8, uint32_t* lo8) {
+    const float c = crow * meta.ks[g], e = meta.ev[g] - (ref - 7.0f);
+    float2 p[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        p[k] = fma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), make_float2(c, c), make_float2(e, e));
+    if (!whole) {
+        const int tok = t0 + 16 * g, from = meta.at[g] >= 0 ? lo - tok : 16, to = hi - tok;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (2 * k < from || 2 * k >= to) p[k].x = -INFINITY;
+            if (2 * k + 1 < from || 2 * k + 1 >= to) p[k].y = -INFINITY;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) p[k] = make_float2(ex2(p[k].x), ex2(p[k].y));
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const __half2 h = __floats2half2_rn(p[k].x, p[k].y);
+        hi8[k] = h2_bits(h);
+        if (lo8) {
+            const float2 f = fma2(__half22float2(h), make_float2(-1.0f, -1.0f), p[k]);
+            lo8[k] = h2_bits(__floats2half2_rn(f.x, f.y));
+        }
+    }
+    const float2 sum = add2(add2(add2(p[0], p[1]), add2(p[2], p[3])), add2(add2(p[4], p[5]), add2(p[6], p[7])));
+    return sum.x + sum.y;
+}
+// P = 2^(x - ref + 7) of a row in the place of its S, and the row's share of the denominator: 32 tokens' P take 16
+// columns (one fp16 term), columns of S that have been read.
 __device__ __forceinline__ float weights(uint32_t at, const TileMeta& meta, float crow, float ref, int t0, int lo, int hi,
                                          bool whole) {
     float l = 0.0f;
 #pragma unroll 1
     for (int q = 0; q < kToks / 32; ++q) {
-        uint32_t v[32], pk[HL ? 32 : 16];
+        uint32_t v[32], pk[16];
         tmem_ld32(at + 32 * q, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int g = 2 * q + h;
-            const float c = crow * meta.ks[g], e = meta.ev[g] - (ref - 7.0f);
-            float2 p[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t* w = &v[16 * h + 2 * k];
-                p[k] = fma2(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), make_float2(c, c), make_float2(e, e));
-            }
-            if (!whole) {
-                const int tok = t0 + 16 * g, from = meta.at[g] >= 0 ? lo - tok : 16, to = hi - tok;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    if (2 * k < from || 2 * k >= to) p[k].x = -INFINITY;
-                    if (2 * k + 1 < from || 2 * k + 1 >= to) p[k].y = -INFINITY;
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) p[k] = make_float2(ex2(p[k].x), ex2(p[k].y));
-            const float2 sum = add2(add2(add2(p[0], p[1]), add2(p[2], p[3])), add2(add2(p[4], p[5]), add2(p[6], p[7])));
-            l = fmaf(sum.x + sum.y, meta.inv[g], l);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const __half2 hh = __floats2half2_rn(p[k].x, p[k].y);
-                pk[8 * h + k] = h2_bits(hh);
-                if constexpr (HL) {
-                    const float2 f = fma2(__half22float2(hh), make_float2(-1.0f, -1.0f), p[k]);
-                    pk[16 + 8 * h + k] = h2_bits(__floats2half2_rn(f.x, f.y));
-                }
-            }
+        for (int h = 0; h < 2; ++h) l = fmaf(group_weights(&v[16 * h], meta, 2 * q + h, crow, ref, t0, lo, hi, whole, &pk[8 * h], nullptr),
+                                             meta.inv[2 * q + h], l);
+        tmem_st16(at + 16 * q, pk);
+    }
+    return l;
+}
+// The same in two fp16 terms: 32 tokens' P take the 32 columns of their S, 16 high, then 16 low. The next group's S
+// is read before this one's P is written (over part of it).
+__device__ __forceinline__ float weights2(uint32_t at, const TileMeta& meta, float crow, float ref, int t0, int lo, int hi,
+                                          bool whole) {
+    float l = 0.0f;
+    uint32_t v[2][16];
+    tmem_ld16(at, v[0]);
+    tmem_wait_ld();
+    auto step = [&](int g, uint32_t (&now)[16], uint32_t (&next)[16], bool all) {
+        uint32_t hi8[8], lo8[8];
+        if (g + 1 < kGroups) tmem_ld16(at + 16 * (g + 1), next);
+        l = fmaf(group_weights(now, meta, g, crow, ref, t0, lo, hi, all, hi8, lo8), meta.inv[g], l);
+        tmem_wait_ld();
+        tmem_st8(at + 32 * (g >> 1) + 8 * (g & 1), hi8);
+        tmem_st8(at + 32 * (g >> 1) + 8 * (g & 1) + 16, lo8);
+    };
+    if (whole) {
+#pragma unroll 1
+        for (int g = 0; g < kGroups; g += 2) {
+            step(g, v[0], v[1], true);
+            step(g + 1, v[1], v[0], true);
         }
-        if constexpr (HL) tmem_st32(at + 32 * q, pk);
-        else tmem_st16(at + 16 * q, pk);
+    } else {
+#pragma unroll 1
+        for (int g = 0; g < kGroups; g += 2) {
+            step(g, v[0], v[1], false);
+            step(g + 1, v[1], v[0], false);
+        }
     }
     return l;
 }
@@ -635,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             const float use = r_new == -INFINITY ? 0.0f : r_new;
             l *= ex2(ref - use);
             ref = r_new;
-            l += weights<true>(tmem + lane_base + kColS + b * kToks, meta, crow, use, t0, lo, hi, whole);
+            l += weights2(tmem + lane_base + kColS + b * kToks, meta, crow, use, t0, lo, hi, whole);
             if (lane == 0) mbar_arrive(&meta_empty[j % kMetaRing]);
             tmem_wait_st();
             tc_fence_before();
@@ -956,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt2_kernel(const __grid_
                         }
                     }
                 }
-                l += weights<false>(at, meta, crow, ref == -INFINITY ? 0.0f : ref, t0, lo, hi, whole);
+                l += weights(at, meta, crow, ref == -INFINITY ? 0.0f : ref, t0, lo, hi, whole);
             }
             if (lane == 0) mbar_arrive(&meta_empty[j % kMetaRing]);
             tmem_wait_st();
