@@ -16,7 +16,12 @@
 // TB/s: the copy engine takes about 50 ns for one, whatever its size.) The copies place 16-byte units so
 // that the fragment reads meet different banks. The work
 // (sequence, kv head, row tile, 64 tokens) is laid out on one line and cut into equal pieces, one per
-// CTA, whatever the lengths; a second kernel joins the pieces of a tile.
+// CTA, whatever the lengths. The CTAs that share a tile leave partial results in the workspace; the last one to
+// arrive joins them, in two levels where there are many. (A second kernel for that found no room beside the first, so it
+// began to look for its tile only when the first had ended: 8 us of 49 for one sequence of 131071 tokens.)
+#include <atomic>
+#include <chrono>
+
 #include "q4k_paged.cuh"
 
 namespace q4k {
@@ -30,6 +35,9 @@ constexpr int kCtasPerSm = 3;
 // Up to this many query rows per kv head a sequence is worked on here, else by the prompt kernel.
 constexpr int kFewRows = 64;
 constexpr int kMaxParts = 512;                // CTAs that the workspace serves
+constexpr int kJoinCost = 8;                  // units that joining a tile is worth
+constexpr int kOneLevel = 16;                 // up to this many pieces of a tile are joined at once
+constexpr int kTickets = 2 * kMaxParts;       // arrival counters before the partial results: by group of pieces, by tile
 
 struct AttnParams {
     PagedBatch B;
@@ -43,6 +51,8 @@ struct AttnParams {
     int max_rows;       // sequences with more query rows per kv head are the prompt kernel's
     float scale_log2;   // softmax scale * log2(e)
     float* part;        // partial results: per CTA two slots of [rows][D] sums, rows M, rows l
+    unsigned long long* tickets;
+    unsigned long long tag;  // this launch's counters carry it in their high 48 bits: others count as 0
     int parts;          // CTAs the partial buffer holds
     int* err_flag;
 };
@@ -174,6 +184,18 @@ __device__ __forceinline__ int piece_of(int64_t total, int pieces, int64_t u) {
     return (int)(u < r * (q + 1) ? div_pos(u, q + 1) : r + div_pos(u - r * (q + 1), q));
 }
 
+// Arrive at a counter of this launch, whatever an earlier one or anything else left in its word; returns how many
+// had arrived before.
+__device__ __forceinline__ int arrive(unsigned long long* w, unsigned long long tag) {
+    unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(w);
+    for (;;) {
+        const int n = (old >> 16) == tag ? (int)(old & 0xFFFFu) : 0;
+        const unsigned long long seen = atomicCAS(w, old, (tag << 16) | (unsigned)(n + 1));
+        if (seen == old) return n;
+        old = seen;
+    }
+}
+
 // The ring of a warp: kRing stages of kPair chunks, and each chunk's page: K's scale, V's scale as
 // log2 and reciprocal, whether there is such a page.
 constexpr int kRing = 2, kPair = 2;
@@ -233,12 +255,20 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
     __shared__ SeqWork s_work[32];
     __shared__ uint4 s_q[D / 16][32];  // the tile's query fragments, a 16-dim step of a lane each
     __shared__ Cursor s_cur;
-    __shared__ int64_t s_u[2];
+    __shared__ int64_t s_u[2], s_total;
+    __shared__ int s_pieces;
+    __shared__ struct { int c0, slot0, size, groups, first, count, last; } s_join;
     if (warp == 0) {
         const SeqWork mine = seq_work<RT>(A, lane);
         s_work[lane] = mine;
         const int64_t total = total_work<RT>(A, mine);
-        const int pieces = (int)min((int64_t)min((int)gridDim.x, A.parts), total);
+        // Joining a tile costs about as much as eight of its units: where no tile is longer, pieces are not shorter
+        // than a whole one.
+        int longest = mine.units;
+        for (int i = 32 + lane; i < A.B.batch; i += 32) longest = max(longest, seq_work<RT>(A, i).units);
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        const int64_t least = longest <= kJoinCost ? kTileCost + longest : 1;
+        const int pieces = (int)min((int64_t)min((int)gridDim.x, A.parts), div_pos(total + least - 1, least));
         const bool any = (int)blockIdx.x < pieces;
         const int64_t u0 = any ? piece_begin(total, pieces, blockIdx.x) : 0;
         const int64_t u1 = any ? piece_begin(total, pieces, blockIdx.x + 1) : 0;
@@ -248,6 +278,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
             s_cur = c;
             s_u[0] = u0;
             s_u[1] = u1;
+            s_total = total;
+            s_pieces = pieces;
         }
     }
     __syncthreads();
@@ -272,6 +304,20 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
         }
         if (ub <= 0) break;
         const int rows = sp.n * A.group, first = sp.len - sp.n;
+        const bool whole = ua == 0 && ub == s_cur.w.units;
+        if (!whole && threadIdx.x == 32) {
+            // the tile's pieces c0 .. c1, in groups of about the root of their number where they are many
+            const int length = kTileCost + s_cur.w.units;
+            const int64_t begin = s_cur.begin + (int64_t)(tile * A.kv_heads + head) * length;
+            const int c0 = piece_of(s_total, s_pieces, begin + kTileCost), c1 = piece_of(s_total, s_pieces, begin + length - 1);
+            const int np = c1 - c0 + 1, size = np <= kOneLevel ? np : (int)ceilf(sqrtf((float)np)), of = ((int)blockIdx.x - c0) / size;
+            s_join.c0 = c0;
+            s_join.slot0 = piece_begin(s_total, s_pieces, c0) >= begin ? 0 : 1;
+            s_join.size = size;
+            s_join.groups = (np + size - 1) / size;
+            s_join.first = c0 + of * size;
+            s_join.count = min(size, c1 + 1 - s_join.first);
+        }
 
         // positions: some row of the tile sees tokens below tile_hi, all see those in [full_lo, full_hi)
         const int pf = first + tile * RT / A.group, pl = first + (min(rows, tile * RT + RT) - 1) / A.group;
@@ -618,18 +664,29 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                 s_m[warp * RT + g + 8 * j] = mx[j];
                 s_l[warp * RT + g + 8 * j] = l[j];
             }
-            // this lane's dims: D/8 (2 t) + n and D/8 (2 t + 1) + n, n = 0 .. NT - 1
-            float* d0 = s_o + (warp * RT + g + 8 * j) * D + D / 8 * 2 * t;
+            // this lane's dims: D/8 (2 t) + n and D/8 (2 t + 1) + n, n = 0 .. NT - 1; 16-byte units xored with the
+            // lane, or the eight lanes of a store would meet the same banks
+            float4* d0 = reinterpret_cast<float4*>(s_o + (warp * RT + g + 8 * j) * D);
 #pragma unroll
             for (int n = 0; n < NT; n += 4) {
-                *reinterpret_cast<float4*>(d0 + n) = make_float4(o[n][j].x, o[n + 1][j].x, o[n + 2][j].x, o[n + 3][j].x);
-                *reinterpret_cast<float4*>(d0 + D / 8 + n) = make_float4(o[n][j].y, o[n + 1][j].y, o[n + 2][j].y, o[n + 3][j].y);
+                const int u = D / 16 * t + n / 4, x = (2 * t + (g & 1)) & 7;
+                d0[u ^ x] = make_float4(o[n][j].x, o[n + 1][j].x, o[n + 2][j].x, o[n + 3][j].x);
+                d0[(u + D / 32) ^ x] = make_float4(o[n][j].y, o[n + 1][j].y, o[n + 2][j].y, o[n + 3][j].y);
             }
         }
         __syncthreads();
         // a tile that begins in this piece, but not at its start, goes to the second slot
-        const bool whole = ua == 0 && ub == s_cur.w.units;
-        float* part = A.part + ((int64_t)blockIdx.x * 2 + (not_first ? 1 : 0)) * (RT * (D + 2));
+        constexpr int kPart = RT * (D + 2);
+        float* part = A.part + ((int64_t)blockIdx.x * 2 + (not_first ? 1 : 0)) * kPart;
+        auto store_row = [&](int r, int c, const float4& acc, float den) {
+            const int row = tile * RT + r;
+            if (row >= rows) return;
+            const float iv = den == 0.0f ? 0.0f : 1.0f / den;  // 0: the row sees nothing
+            const float y[4] = {acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv};
+            Vec<T>::store(static_cast<T*>(A.out) + (int64_t)(sp.start + row / A.group) * A.out_stride +
+                              (int64_t)(head * A.group + row % A.group) * D + c,
+                          y);
+        };
         for (int i = threadIdx.x; i < RT * D / 4; i += 32 * kAttnWarps) {
             const int r = i / (D / 4), c = 4 * (i % (D / 4));
             float m = -INFINITY;
@@ -641,26 +698,78 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
 #pragma unroll
             for (int k = 0; k < kAttnWarps; ++k) {
                 const float wt = ex2(s_m[k * RT + r] - mu);
-                const float4 v = *reinterpret_cast<const float4*>(s_o + (k * RT + r) * D + c);
+                const int u = c / 4, x = (2 * (u / (D / 16)) + (r & 1)) & 7;
+                const float4 v = reinterpret_cast<const float4*>(s_o + (k * RT + r) * D)[u ^ x];
                 den = fmaf(wt, s_l[k * RT + r], den);
                 acc.x = fmaf(wt, v.x, acc.x); acc.y = fmaf(wt, v.y, acc.y);
                 acc.z = fmaf(wt, v.z, acc.z); acc.w = fmaf(wt, v.w, acc.w);
             }
             if (whole) {
-                const int row = tile * RT + r;
-                if (row < rows) {
-                    const float iv = den == 0.0f ? 0.0f : 1.0f / den;  // 0: the row sees nothing
-                    const float y[4] = {acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv};
-                    Vec<T>::store(static_cast<T*>(A.out) + (int64_t)(sp.start + row / A.group) * A.out_stride +
-                                      (int64_t)(head * A.group + row % A.group) * D + c,
-                                  y);
-                }
+                store_row(r, c, acc, den);
             } else {
                 *reinterpret_cast<float4*>(part + r * D + c) = acc;
                 if (c == 0) {
                     part[RT * D + r] = m;
                     part[RT * D + RT + r] = den;
                 }
+            }
+        }
+        if (!whole) {
+            auto last_to_arrive = [&](unsigned long long* w, int count) {  // every thread's results, then the counter
+                __syncthreads();
+                if (threadIdx.x == 0) {
+                    __threadfence();
+                    s_join.last = arrive(w, A.tag) == count - 1;
+                    if (s_join.last) {
+                        *reinterpret_cast<volatile unsigned long long*>(w) = A.tag << 16;  // for a replay of this launch
+                        __threadfence();
+                    }
+                }
+                __syncthreads();
+                return s_join.last != 0;
+            };
+            auto piece = [&](int i) { return A.part + ((int64_t)i * 2 + (i == s_join.c0 ? s_join.slot0 : 0)) * kPart; };
+            // pieces first, first + step, ..: their weighted sum to the first one's slot, or to the output
+            auto join = [&](int first, int step, int count, bool to_out) {
+                float* pm = reinterpret_cast<float*>(s_mem);  // maxima, then denominators, [count][RT]
+                float* pl = pm + count * RT;
+                for (int i = threadIdx.x; i < count * RT; i += 32 * kAttnWarps) {
+                    const float* x = piece(first + i / RT * step) + RT * D + i % RT;
+                    pm[i] = __ldcg(x);
+                    pl[i] = __ldcg(x + RT);
+                }
+                __syncthreads();
+#pragma unroll 1
+                for (int i = threadIdx.x; i < RT * D / 4; i += 32 * kAttnWarps) {
+                    const int r = i / (D / 4), c = 4 * (i % (D / 4));
+                    float m = -INFINITY, den = 0.0f;
+                    for (int k = 0; k < count; ++k) m = fmaxf(m, pm[k * RT + r]);
+                    const float mu = m == -INFINITY ? 0.0f : m;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                    for (int k = 0; k < count; ++k) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(piece(first + k * step) + r * D + c));
+                        const float wt = ex2(pm[k * RT + r] - mu);
+                        den = fmaf(wt, pl[k * RT + r], den);
+                        acc.x = fmaf(wt, v.x, acc.x); acc.y = fmaf(wt, v.y, acc.y);
+                        acc.z = fmaf(wt, v.z, acc.z); acc.w = fmaf(wt, v.w, acc.w);
+                    }
+                    if (to_out) {
+                        store_row(r, c, acc, den);
+                        continue;
+                    }
+                    float* x = piece(first);
+                    *reinterpret_cast<float4*>(x + r * D + c) = acc;
+                    if (c == 0) {
+                        x[RT * D + r] = m;
+                        x[RT * D + RT + r] = den;
+                    }
+                }
+            };
+            if (last_to_arrive(A.tickets + s_join.first, s_join.count)) {
+                join(s_join.first, 1, s_join.count, s_join.groups == 1);
+                if (s_join.groups > 1 && last_to_arrive(A.tickets + kMaxParts + s_join.c0, s_join.groups))
+                    join(s_join.c0, s_join.size, s_join.groups, true);
             }
         }
         not_first = true;
@@ -676,86 +785,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
             }
         }
         __syncthreads();
-    }
-}
-
-// Join the tiles that were cut. CTA i looks at the cut between pieces i and i + 1; the CTAs whose cuts
-// lie in one tile share its rows, so a tile of many pieces has many CTAs. The lengths were complete before
-// the kernel that this one follows, so the tile is found while that kernel still runs. Warps that
-// share a row take its pieces in turn.
-constexpr int kJoinWarps = 8;
-template <typename T, int D, int RT>
-__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ AttnParams A, int pieces_max) {
-    constexpr int kCols = D / 32, kPart = RT * (D + 2);
-    __shared__ float s_acc[kJoinWarps][D], s_den[kJoinWarps];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cut = blockIdx.x + 1;
-    const SeqWork mine = seq_work<RT>(A, lane);
-    const int64_t total = total_work<RT>(A, mine);
-    const int pieces = (int)min((int64_t)pieces_max, total);
-    int c0 = 0, c1 = 0, slot0 = 0, tile = 0, head = 0;
-    Cursor cur{};
-    if (cut < pieces && seek<RT>(A, piece_begin(total, pieces, cut), mine, &cur)) {
-        const int length = kTileCost + cur.w.units;
-        const int seg = (int)div_pos(piece_begin(total, pieces, cut) - cur.begin, length);
-        const int64_t begin = cur.begin + (int64_t)seg * length;
-        c0 = piece_of(total, pieces, begin + kTileCost);
-        c1 = piece_of(total, pieces, begin + length - 1);
-        slot0 = piece_begin(total, pieces, c0) >= begin ? 0 : 1;
-        tile = seg / A.kv_heads;
-        head = seg - tile * A.kv_heads;
-    }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (cut <= c0 || cut > c1) return;  // the cut lies before the tile's first unit, or no tile is cut here
-    const float* first = A.part + ((int64_t)c0 * 2 + slot0) * kPart;  // piece 0; piece i > 0 is slot 0 of CTA c0 + i
-    const float* rest = A.part + (int64_t)c0 * 2 * kPart;
-    const int np = c1 - c0 + 1, sharers = c1 - c0, mine_first = cut - c0 - 1;
-    auto part = [&](int i) { return i == 0 ? first : rest + (int64_t)i * 2 * kPart; };
-    const int rows = min(RT, cur.w.s.n * A.group - tile * RT);
-    const int here = (rows - mine_first + sharers - 1) / sharers;  // rows mine_first, mine_first + sharers, ...
-    if (here <= 0) return;
-    const int per_row = here >= kJoinWarps ? 1 : here > 4 ? 1 : here > 2 ? 2 : here > 1 ? 4 : 8;  // warps of a row
-    for (int k0 = 0; k0 < here; k0 += kJoinWarps / per_row) {
-        const int k = k0 + warp / per_row, r = mine_first + k * sharers;
-        float m = -INFINITY, acc[kCols] = {}, den = 0.0f;
-        if (k < here) {
-            for (int i = lane; i < np; i += 32) m = fmaxf(m, __ldcg(part(i) + RT * D + r));
-#pragma unroll
-            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float mu = m == -INFINITY ? 0.0f : m;
-#pragma unroll 4
-            for (int i = warp % per_row; i < np; i += per_row) {
-                const float* x = part(i);
-                const float wt = ex2(__ldcg(x + RT * D + r) - mu);
-#pragma unroll
-                for (int c = 0; c < kCols; ++c) acc[c] = fmaf(wt, __ldcg(x + r * D + 32 * c + lane), acc[c]);
-                den = fmaf(wt, __ldcg(x + RT * D + RT + r), den);
-            }
-        }
-        if (per_row > 1) {
-            if (lane == 0) s_den[warp] = den;
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) s_acc[warp][32 * c + lane] = acc[c];
-            __syncthreads();
-            if (warp % per_row == 0)
-                for (int i = 1; i < per_row; ++i) {
-                    den += s_den[warp + i];
-#pragma unroll
-                    for (int c = 0; c < kCols; ++c) acc[c] += s_acc[warp + i][32 * c + lane];
-                }
-            __syncthreads();
-        }
-        if (k < here && warp % per_row == 0) {
-            const int row = tile * RT + r;
-            T* out = static_cast<T*>(A.out) + (int64_t)(cur.w.s.start + row / A.group) * A.out_stride +
-                     (int64_t)(head * A.group + row % A.group) * D + lane;
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) {
-                const float y = den == 0.0f ? 0.0f : acc[c] / den;  // 0: the row sees nothing
-                if constexpr (sizeof(T) == 4) out[32 * c] = y;
-                else out[32 * c] = __float2bfloat16_rn(y);
-            }
-        }
     }
 }
 
@@ -787,19 +816,22 @@ cudaError_t launch_typed(const AttnParams& P, int64_t units, cudaStream_t stream
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attn_kernel<T, D, RT>, P);
-    if (e != cudaSuccess) return e;
-    if (grid == 1) return cudaSuccess;
-    cfg.gridDim = dim3((unsigned)(grid - 1));
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D, RT>, P, (int)grid);
+    return cudaLaunchKernelEx(&cfg, attn_kernel<T, D, RT>, P);
+}
+
+// A value that no other launch of the process has (and, from a start that differs, hardly any other process's).
+unsigned long long next_tag() {
+    static std::atomic<unsigned long long> n{0};
+    static const unsigned long long start =
+        (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count() * 0x9E3779B97F4A7C15ull ^
+        reinterpret_cast<uintptr_t>(&n);
+    return (start + n.fetch_add(1, std::memory_order_relaxed)) & 0xFFFFFFFFFFFFull;
 }
 
 }  // namespace
 
-size_t attn_workspace_bytes(int head_dim) {  // two slots of up to 16 rows per CTA
-    return (size_t)kMaxParts * 2 * 16 * (head_dim + 2) * sizeof(float);
+size_t attn_workspace_bytes(int head_dim) {  // the counters, then two slots of up to 16 rows per CTA
+    return kTickets * sizeof(unsigned long long) + (size_t)kMaxParts * 2 * 16 * (head_dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int64_t q_stride, int q_heads, int kv_heads,
@@ -821,7 +853,9 @@ cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int6
     P.k_cache = k_cache; P.v_cache = v_cache; P.k_scale = k_scale; P.v_scale = v_scale;
     P.q_heads = q_heads; P.kv_heads = kv_heads; P.group = q_heads / kv_heads; P.window = window;
     P.scale_log2 = scale * 1.44269504088896340736f;
-    P.part = static_cast<float*>(workspace);
+    P.tickets = static_cast<unsigned long long*>(workspace);
+    P.tag = next_tag();
+    P.part = reinterpret_cast<float*>(P.tickets + kTickets);
     P.parts = num_sms() * kCtasPerSm < kMaxParts ? num_sms() * kCtasPerSm : kMaxParts;
     P.err_flag = err_flag;
     P.max_rows = prompts ? kFewRows : 0x7FFFFFFF;
