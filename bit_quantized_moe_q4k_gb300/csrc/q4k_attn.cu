@@ -17,7 +17,9 @@
 // that the fragment reads meet different banks. The work
 // (sequence, kv head, row tile, 64 tokens) is laid out on one line and cut into equal pieces, one per
 // CTA, whatever the lengths. The CTAs that share a tile leave partial results in the workspace; the last one to
-// arrive joins them, in two levels where there are many. (A second kernel for that found no room beside the first, so it
+// arrive joins them, in two levels where there are many. Where there are few tiles (one sequence), clusters of
+// eight CTAs work as one, 512 tokens a unit, and join their tiles through distributed shared memory: an eighth of the
+// pieces, and reads of a few hundred cycles instead of the thousand and more through L2. (A second kernel for that found no room beside the first, so it
 // began to look for its tile only when the first had ended: 8 us of 49 for one sequence of 131071 tokens.)
 #include <atomic>
 #include <chrono>
@@ -34,6 +36,7 @@ constexpr int kTileCost = 4;                  // units that starting and ending 
 constexpr int kCtasPerSm = 3;
 // Up to this many query rows per kv head a sequence is worked on here, else by the prompt kernel.
 constexpr int kFewRows = 64;
+constexpr int kLeast = 4;                      // units of a cluster's part of a tile, at least
 constexpr int kMaxParts = 512;                // CTAs that the workspace serves
 constexpr int kJoinCost = 8;                  // units that joining a tile is worth
 constexpr int kOneLevel = 16;                 // up to this many pieces of a tile are joined at once
@@ -102,7 +105,7 @@ struct SeqWork {
     int lo, tiles, units;
     int64_t total;
 };
-template <int RT>
+template <int RT, int CL>
 __device__ __forceinline__ SeqWork seq_work(const AttnParams& A, int i) {
     SeqWork w{};
     if (i >= A.B.batch) return w;
@@ -113,7 +116,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& A, int i) {
     const int first = max(w.s.len - w.s.n, 0);
     w.lo = A.window > 0 ? (max(first - A.window + 1, 0) & ~(kChunk - 1)) : 0;
     w.tiles = (w.s.n * A.group + RT - 1) / RT;
-    w.units = max((w.s.len - w.lo + kUnit - 1) / kUnit, 1);  // an empty sequence: its rows are zeroed
+    w.units = max((w.s.len - w.lo + CL * kUnit - 1) / (CL * kUnit), 1);  // an empty sequence: its rows are zeroed
     w.total = (int64_t)w.tiles * A.kv_heads * (kTileCost + w.units);
     return w;
 }
@@ -141,7 +144,7 @@ __device__ __forceinline__ bool seek(const AttnParams& A, int64_t u, const SeqWo
     const int lane = threadIdx.x & 31;
     int64_t acc = c->begin;
     for (int base = c->seq & ~31; base < A.B.batch; base += 32) {
-        SeqWork w = base == 0 ? mine : seq_work<RT>(A, base + lane);
+        SeqWork w = base == 0 ? mine : seq_work<RT, 1>(A, base + lane);
         if (base + lane < c->seq) w.total = 0;
         const int64_t inc = warp_scan(w.total);
         const unsigned hit = __ballot_sync(0xffffffffu, u < acc + inc);
@@ -165,7 +168,7 @@ __device__ __forceinline__ bool seek(const AttnParams& A, int64_t u, const SeqWo
 template <int RT>
 __device__ __forceinline__ int64_t total_work(const AttnParams& A, const SeqWork& mine) {
     int64_t t = mine.total;
-    for (int i = 32 + (threadIdx.x & 31); i < A.B.batch; i += 32) t += seq_work<RT>(A, i).total;
+    for (int i = 32 + (threadIdx.x & 31); i < A.B.batch; i += 32) t += seq_work<RT, 1>(A, i).total;
 #pragma unroll
     for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     return t;
@@ -173,6 +176,53 @@ __device__ __forceinline__ int64_t total_work(const AttnParams& A, const SeqWork
 // 64-bit values that mostly fit 32: the short division where they do.
 __device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
     return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+// What cluster `c` of `clusters` works on: a tile's units are shared by k clusters, k in proportion to its length but
+// at least one, and at least kLeast units a cluster; no cluster takes a part of two tiles.
+struct TilePart {
+    int index, k;  // the tile among its sequence's (row tile, kv head), and its clusters
+    int first, j;  // its first cluster; this one's number among them
+};
+template <int RT, int CL>
+__device__ __forceinline__ bool tile_part(const AttnParams& A, int c, int clusters, Cursor* cur, TilePart* p) {
+    const int lane = threadIdx.x & 31;
+    const SeqWork mine = seq_work<RT, CL>(A, lane);
+    int64_t tiles = (int64_t)mine.tiles * A.kv_heads, units = tiles * mine.units;
+    for (int i = 32 + lane; i < A.B.batch; i += 32) {
+        const SeqWork w = seq_work<RT, CL>(A, i);
+        tiles += (int64_t)w.tiles * A.kv_heads;
+        units += (int64_t)w.tiles * A.kv_heads * w.units;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+        units += __shfl_xor_sync(0xffffffffu, units, o);
+    }
+    const int64_t spare = max(clusters - tiles, (int64_t)0);
+    int64_t acc = 0;
+    for (int base = 0; base < A.B.batch; base += 32) {
+        const SeqWork w = base == 0 ? mine : seq_work<RT, CL>(A, base + lane);
+        const int k = w.tiles ? min(1 + (int)div_pos(w.units * spare, units), max(w.units / kLeast, 1)) : 1;
+        const int64_t own = (int64_t)w.tiles * A.kv_heads * k, inc = warp_scan(own);
+        const unsigned hit = __ballot_sync(0xffffffffu, c < acc + inc);
+        if (hit) {
+            const int src = __ffs(hit) - 1, begin = (int)(acc + __shfl_sync(0xffffffffu, inc - own, src));
+            cur->seq = base + src;
+            cur->w.s.start = __shfl_sync(0xffffffffu, w.s.start, src);
+            cur->w.s.n = __shfl_sync(0xffffffffu, w.s.n, src);
+            cur->w.s.len = __shfl_sync(0xffffffffu, w.s.len, src);
+            cur->w.lo = __shfl_sync(0xffffffffu, w.lo, src);
+            cur->w.tiles = __shfl_sync(0xffffffffu, w.tiles, src);
+            cur->w.units = __shfl_sync(0xffffffffu, w.units, src);
+            p->k = __shfl_sync(0xffffffffu, k, src);
+            p->index = (c - begin) / p->k;
+            p->j = (c - begin) - p->index * p->k;
+            p->first = c - p->j;
+            return true;
+        }
+        acc += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    return false;
 }
 // First unit of piece c when `total` units are cut into `pieces`.
 __device__ __forceinline__ int64_t piece_begin(int64_t total, int pieces, int c) {
@@ -184,16 +234,41 @@ __device__ __forceinline__ int piece_of(int64_t total, int pieces, int64_t u) {
     return (int)(u < r * (q + 1) ? div_pos(u, q + 1) : r + div_pos(u - r * (q + 1), q));
 }
 
-// Arrive at a counter of this launch, whatever an earlier one or anything else left in its word; returns how many
-// had arrived before.
-__device__ __forceinline__ int arrive(unsigned long long* w, unsigned long long tag) {
-    unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(w);
-    for (;;) {
-        const int n = (old >> 16) == tag ? (int)(old & 0xFFFFu) : 0;
-        const unsigned long long seen = atomicCAS(w, old, (tag << 16) | (unsigned)(n + 1));
-        if (seen == old) return n;
-        old = seen;
+// A counter of this launch, whatever an earlier one or anything else left in its word (`seen`): 48 bits of the launch's
+// tag, 16 of count. Every CTA that will arrive sees to the tag before (only this launch's CTAs change the word, all to
+// the same, so the second look finds it), so that arriving is one addition.
+__device__ __forceinline__ void open_counter(unsigned long long* w, unsigned long long tag, unsigned long long seen) {
+    while ((seen >> 16) != tag) {
+        const unsigned long long was = atomicCAS(w, seen, tag << 16);
+        if (was == seen) return;
+        seen = was;
     }
+}
+__device__ __forceinline__ int arrive(unsigned long long* w) {  // how many had arrived before
+    return (int)(atomicAdd(w, 1ull) & 0xFFFFu);
+}
+
+// Clusters (CL CTAs that work as one).
+__device__ __forceinline__ int cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return (int)r;
+}
+template <int CL> __device__ __forceinline__ void sync_all() {  // the CTA, or the cluster's CTAs
+    if constexpr (CL == 1)
+        __syncthreads();
+    else
+        asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// A word of the shared memory of CTA `rank` of the cluster, at the place of `p` in this one's.
+__device__ __forceinline__ float peer_f32(const float* p, int rank) {
+    float v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+        : "=f"(v)
+        : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank)
+        : "memory");
+    return v;
 }
 
 // The ring of a warp: kRing stages of kPair chunks, and each chunk's page: K's scale, V's scale as
@@ -237,7 +312,7 @@ __device__ __forceinline__ float scale_log2_of(float s) {
 
 // RT: query rows of a tile. fp32: 8 (two fp16 terms fill the 16 rows); bf16: 8 where a tile has no
 // more rows, else 16.
-template <typename T, int D, int RT>
+template <typename T, int D, int RT, int CL>
 __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const __grid_constant__ AttnParams A) {
     constexpr bool HL = sizeof(T) == 4;           // two fp16 terms
     constexpr int NR = RT / 8;                    // rows of a thread: g, and g + 8
@@ -250,36 +325,52 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    // The first warp finds the CTA's piece and its segments; what the main loop does not need stays in
+    const int rank = CL > 1 ? cluster_rank() : 0, my_piece = CL > 1 ? (int)blockIdx.x / CL : (int)blockIdx.x;
+    __shared__ float s_xm[RT], s_xl[RT];  // the CTA's share of a tile, for its cluster: maxima, denominators, sums
+    float* s_x = s_o + kAttnWarps * RT * D;
+    // The first warp finds the piece and its segments; what the main loop does not need stays in
     // shared memory.
     __shared__ SeqWork s_work[32];
     __shared__ uint4 s_q[D / 16][32];  // the tile's query fragments, a 16-dim step of a lane each
     __shared__ Cursor s_cur;
     __shared__ int64_t s_u[2], s_total;
     __shared__ int s_pieces;
+    __shared__ TilePart s_tile;
     __shared__ struct { int c0, slot0, size, groups, first, count, last; } s_join;
     if (warp == 0) {
-        const SeqWork mine = seq_work<RT>(A, lane);
-        s_work[lane] = mine;
-        const int64_t total = total_work<RT>(A, mine);
-        // Joining a tile costs about as much as eight of its units: where no tile is longer, pieces are not shorter
-        // than a whole one.
-        int longest = mine.units;
-        for (int i = 32 + lane; i < A.B.batch; i += 32) longest = max(longest, seq_work<RT>(A, i).units);
-        longest = __reduce_max_sync(0xffffffffu, longest);
-        const int64_t least = longest <= kJoinCost ? kTileCost + longest : 1;
-        const int pieces = (int)min((int64_t)min((int)gridDim.x, A.parts), div_pos(total + least - 1, least));
-        const bool any = (int)blockIdx.x < pieces;
-        const int64_t u0 = any ? piece_begin(total, pieces, blockIdx.x) : 0;
-        const int64_t u1 = any ? piece_begin(total, pieces, blockIdx.x + 1) : 0;
-        Cursor c{};
-        if (any) seek<RT>(A, u0, mine, &c);
-        if (lane == 0) {
-            s_cur = c;
-            s_u[0] = u0;
-            s_u[1] = u1;
-            s_total = total;
-            s_pieces = pieces;
+        if constexpr (CL > 1) {
+            Cursor c{};
+            TilePart p{};
+            const bool any = tile_part<RT, CL>(A, my_piece, min((int)gridDim.x / CL, A.parts), &c, &p);
+            if (lane == 0) {
+                s_cur = c;
+                s_tile = p;
+                s_u[0] = 0;
+                s_u[1] = any;
+            }
+        } else {
+            const SeqWork mine = seq_work<RT, 1>(A, lane);
+            s_work[lane] = mine;
+            const int64_t total = total_work<RT>(A, mine);
+            // Joining a tile costs about as much as eight of its units: where no tile is longer, pieces are not shorter
+            // than a whole one.
+            int longest = mine.units;
+            for (int i = 32 + lane; i < A.B.batch; i += 32) longest = max(longest, seq_work<RT, 1>(A, i).units);
+            longest = __reduce_max_sync(0xffffffffu, longest);
+            const int64_t least = longest <= kJoinCost ? kTileCost + longest : 1;
+            const int pieces = (int)min((int64_t)min((int)gridDim.x, A.parts), div_pos(total + least - 1, least));
+            const bool any = my_piece < pieces;
+            const int64_t u0 = any ? piece_begin(total, pieces, my_piece) : 0;
+            const int64_t u1 = any ? piece_begin(total, pieces, my_piece + 1) : 0;
+            Cursor c{};
+            if (any) seek<RT>(A, u0, mine, &c);
+            if (lane == 0) {
+                s_cur = c;
+                s_u[0] = u0;
+                s_u[1] = u1;
+                s_total = total;
+                s_pieces = pieces;
+            }
         }
     }
     __syncthreads();
@@ -289,8 +380,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
     while (s_u[0] < s_u[1]) {
         const SeqSpan sp = s_cur.w.s;
         const int w_lo = s_cur.w.lo, seq = s_cur.seq;
-        int tile, head, ua, ub, step;
-        {
+        int tile, head, ua, ub, step = 0;
+        if constexpr (CL > 1) {
+            ua = (int)((int64_t)s_cur.w.units * s_tile.j / s_tile.k);
+            ub = (int)((int64_t)s_cur.w.units * (s_tile.j + 1) / s_tile.k);
+            tile = s_tile.index / A.kv_heads;
+            head = s_tile.index - tile * A.kv_heads;
+        } else {
             const int64_t at = s_u[0] - s_cur.begin;
             const int length = kTileCost + s_cur.w.units;
             const int seg = (int)div_pos(at, length);  // (row tile, kv head) of the sequence
@@ -307,12 +403,20 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
         const bool whole = ua == 0 && ub == s_cur.w.units;
         if (!whole && threadIdx.x == 32) {
             // the tile's pieces c0 .. c1, in groups of about the root of their number where they are many
-            const int length = kTileCost + s_cur.w.units;
-            const int64_t begin = s_cur.begin + (int64_t)(tile * A.kv_heads + head) * length;
-            const int c0 = piece_of(s_total, s_pieces, begin + kTileCost), c1 = piece_of(s_total, s_pieces, begin + length - 1);
-            const int np = c1 - c0 + 1, size = np <= kOneLevel ? np : (int)ceilf(sqrtf((float)np)), of = ((int)blockIdx.x - c0) / size;
+            int c0, c1, slot0 = 0;
+            if constexpr (CL > 1) {
+                c0 = s_tile.first;
+                c1 = c0 + s_tile.k - 1;
+            } else {
+                const int length = kTileCost + s_cur.w.units;
+                const int64_t begin = s_cur.begin + (int64_t)(tile * A.kv_heads + head) * length;
+                c0 = piece_of(s_total, s_pieces, begin + kTileCost);
+                c1 = piece_of(s_total, s_pieces, begin + length - 1);
+                slot0 = piece_begin(s_total, s_pieces, c0) >= begin ? 0 : 1;
+            }
+            const int np = c1 - c0 + 1, size = np <= kOneLevel ? np : (int)ceilf(sqrtf((float)np)), of = (my_piece - c0) / size;
             s_join.c0 = c0;
-            s_join.slot0 = piece_begin(s_total, s_pieces, c0) >= begin ? 0 : 1;
+            s_join.slot0 = slot0;
             s_join.size = size;
             s_join.groups = (np + size - 1) / size;
             s_join.first = c0 + of * size;
@@ -324,13 +428,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
         const int tile_hi = max(pl + 1, 0), full_hi = max(pf + 1, 0);
         const int full_lo = A.window > 0 ? max(pl - A.window + 1, 0) : 0;
 
-        // this warp's chunks: base0 + kUnit i, i < n
-        const int c_end = min(w_lo + ub * kUnit, tile_hi);
-        const int base0 = w_lo + ua * kUnit + warp * kChunk;
-        const int n = base0 < c_end ? (c_end - base0 + kUnit - 1) / kUnit : 0;
-        auto page_of = [&](int i) {
-            return i < n ? page_id(A.B, seq, (base0 + kUnit * i) >> A.B.page_shift, A.err_flag) : -1;
-        };
+        // this warp's chunks: base0 + kStep i, i < n
+        constexpr int kStep = CL * kUnit;
+        const int c_end = min(w_lo + ub * kStep, tile_hi);
+        const int base0 = w_lo + ua * kStep + rank * kUnit + warp * kChunk;
+        const int n = base0 < c_end ? (c_end - base0 + kStep - 1) / kStep : 0;
+        auto entry_of = [&](int i) { return i < n ? page_entry(A.B, seq, (base0 + kStep * i) >> A.B.page_shift) : -1; };
+        auto checked = [&](int i, int p) { return i < n ? page_checked(A.B, p, A.err_flag) : -1; };
         auto scales_of = [&](int pid, float& ks, float& vs) {
             ks = vs = 1.0f;
             if (pid >= 0) {
@@ -338,9 +442,28 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                 vs = __ldcg(A.v_scale + (int64_t)pid * A.kv_heads + head);
             }
         };
-        PageAhead ah{page_of(lane), page_of(32 + lane), page_of(64 + lane), 1.f, 1.f, 1.f, 1.f};
-        scales_of(ah.p0, ah.ks0, ah.vs0);
-        scales_of(ah.p1, ah.ks1, ah.vs1);
+        // What a segment begins with is a chain of reads through L2, so each is issued before an earlier one is
+        // looked at: page ids, the tile's queries, the counters, the first copies, scales.
+        PageAhead ah{entry_of(lane), entry_of(32 + lane), entry_of(64 + lane), 1.f, 1.f, 1.f, 1.f};
+        float x[NR][D / 64][16];
+        // a row's token, its dims 64 h + 16 t ..; rows past the last one read the first one's
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+            const int r = tile * RT + g + 8 * j < rows ? tile * RT + g + 8 * j : 0;
+            const T* p = static_cast<const T*>(A.q) + (int64_t)(sp.start + r / A.group) * A.q_stride +
+                         (int64_t)(head * A.group + r % A.group) * D + 16 * t;
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) Vec<T>::load(p + 64 * h, x[j][h]);
+        }
+        unsigned long long seen[2] = {};
+        const bool opens = !whole && threadIdx.x == 32 && rank == 0;
+        if (opens) {
+            seen[0] = *reinterpret_cast<volatile unsigned long long*>(A.tickets + s_join.first);
+            seen[1] = *reinterpret_cast<volatile unsigned long long*>(A.tickets + kMaxParts + s_join.c0);
+        }
+        ah.p0 = checked(lane, ah.p0);
+        ah.p1 = checked(32 + lane, ah.p1);
+        ah.p2 = checked(64 + lane, ah.p2);
         const int n_st = (n + kPair - 1) / kPair;
         auto issue = [&](int k) {  // the copies of stage k (a group of its own, empty past the last stage)
 #pragma unroll
@@ -350,11 +473,11 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                     ah.p0 = ah.p1; ah.ks0 = ah.ks1; ah.vs0 = ah.vs1;
                     ah.p1 = ah.p2;
                     scales_of(ah.p1, ah.ks1, ah.vs1);
-                    ah.p2 = page_of(i + 64 + lane);
+                    ah.p2 = checked(i + 64 + lane, entry_of(i + 64 + lane));
                 }
                 const int pid = __shfl_sync(0xffffffffu, ah.p0, i & 31);  // -1 past the last chunk
                 if (pid < 0) continue;
-                const int slot = (base0 + kUnit * i) & ((1 << A.B.page_shift) - 1);
+                const int slot = (base0 + kStep * i) & ((1 << A.B.page_shift) - 1);
                 const int64_t at = ((((int64_t)pid * A.kv_heads + head) << A.B.page_shift) + slot) * D + 16 * lane;
                 const uint32_t dst = ring_at + k % kRing * kStage<D> + c * kSlot<D>;
                 constexpr int kUnits = D / 16, kRows = 32 / kUnits;  // a row's units; rows of one copy instruction
@@ -373,7 +496,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                 s_meta[warp][k % kRing * kPair + c] = ChunkMeta{ah.ks0, scale_log2_of(ah.vs0), 1.0f / ah.vs0, ah.p0 >= 0};
         };
         for (int k = 0; k < kRing; ++k) issue(k);
-        for (int k = 0; k < kRing; ++k) note(k);
+        scales_of(ah.p0, ah.ks0, ah.vs0);
+        scales_of(ah.p1, ah.ks1, ah.vs1);
 
         // the thread's rows: position limits and query fragments
         int hi[NR], lo[NR];
@@ -386,20 +510,15 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
             const int pos = first + tok;
             hi[j] = valid ? pos + 1 : 0;
             lo[j] = A.window > 0 ? max(pos - A.window + 1, 0) : 0;
-            float x[D / 64][16];
             float amax = 0.0f;
-            const T* p = static_cast<const T*>(A.q) + (int64_t)(sp.start + tok) * A.q_stride +
-                         (int64_t)(head * A.group + (valid ? r % A.group : 0)) * D + 16 * t;
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h) {
-                Vec<T>::load(p + 64 * h, x[h]);
+            for (int h = 0; h < D / 64; ++h)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    if (!valid) x[h][i] = 0.0f;
-                    const float a = fabsf(x[h][i]);
+                    if (!valid) x[j][h][i] = 0.0f;
+                    const float a = fabsf(x[j][h][i]);
                     if (a <= 3.402823466e38f) amax = fmaxf(amax, a);
                 }
-            }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             // power of two that brings the row's largest magnitude to [2^7, 2^8)
@@ -412,8 +531,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (i != warp) continue;
-                    const float a0 = x[h][4 * i] * up, a1 = x[h][4 * i + 1] * up;
-                    const float a2 = x[h][4 * i + 2] * up, a3 = x[h][4 * i + 3] * up;
+                    const float a0 = x[j][h][4 * i] * up, a1 = x[j][h][4 * i + 1] * up;
+                    const float a2 = x[j][h][4 * i + 2] * up, a3 = x[j][h][4 * i + 3] * up;
                     uint4 f;
                     if constexpr (HL) {
                         const __half2 h01 = __floats2half2_rn(a0, a1), h23 = __floats2half2_rn(a2, a3);
@@ -435,6 +554,11 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                 }
         }
         static_assert(kAttnWarps == 4, "a step of each 64 dims a warp");
+        for (int k = 0; k < kRing; ++k) note(k);
+        if (opens) {
+            if (s_join.count > 1) open_counter(A.tickets + s_join.first, A.tag, seen[0]);
+            if (s_join.groups > 1) open_counter(A.tickets + kMaxParts + s_join.c0, A.tag, seen[1]);
+        }
         __syncthreads();
 
         float2 o[NT][NR];
@@ -485,7 +609,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
             }
 #pragma unroll
             for (int c = 0; c < S; ++c) {
-                const int base = base0 + kUnit * (i + c);
+                const int base = base0 + kStep * (i + c);
                 const ChunkMeta meta = s_meta[warp][stage * S + c];
                 // x = c * s + e, masked
                 inv[c] = meta.inv;
@@ -582,7 +706,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                     // tokens that no row of the tile sees hold anything: NaN codes too
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int tok = base0 + kUnit * (i + c) + 4 * t + k;
+                        const int tok = base0 + kStep * (i + c) + 4 * t + k;
                         if (!held[c] || tok >= tile_hi || tok < w_lo)
 #pragma unroll
                             for (int q = 0; q < D / 32; ++q) vf[c][k][q] = 0;
@@ -600,7 +724,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                         for (int j = 0; j < NR; ++j)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                const int tok = base0 + kUnit * (i + c) + 4 * t + k;
+                                const int tok = base0 + kStep * (i + c) + 4 * t + k;
                                 if (tok >= lo[j] && tok < hi[j]) see[2 * (k >> 1) + j] |= 0x3C00u << (16 * (k & 1));
                             }
 #pragma unroll
@@ -677,7 +801,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
         __syncthreads();
         // a tile that begins in this piece, but not at its start, goes to the second slot
         constexpr int kPart = RT * (D + 2);
-        float* part = A.part + ((int64_t)blockIdx.x * 2 + (not_first ? 1 : 0)) * kPart;
+        float* part = A.part + ((int64_t)my_piece * 2 + (not_first ? 1 : 0)) * kPart;
         auto store_row = [&](int r, int c, const float4& acc, float den) {
             const int row = tile * RT + r;
             if (row >= rows) return;
@@ -704,6 +828,14 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                 acc.x = fmaf(wt, v.x, acc.x); acc.y = fmaf(wt, v.y, acc.y);
                 acc.z = fmaf(wt, v.z, acc.z); acc.w = fmaf(wt, v.w, acc.w);
             }
+            if constexpr (CL > 1) {
+                *reinterpret_cast<float4*>(s_x + r * D + c) = acc;
+                if (c == 0) {
+                    s_xm[r] = m;
+                    s_xl[r] = den;
+                }
+                continue;
+            }
             if (whole) {
                 store_row(r, c, acc, den);
             } else {
@@ -714,19 +846,60 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                 }
             }
         }
+        auto peer_or_own = [&](const float* x) {  // the cluster's first CTA's
+            if constexpr (CL > 1) return peer_f32(x, 0);
+            else return *x;
+        };
+        if constexpr (CL > 1) {
+            // the cluster's shares: CTA `rank` joins rows rank, rank + CL, ...
+            sync_all<CL>();
+            for (int i = threadIdx.x; i < RT / CL * D; i += 32 * kAttnWarps) {
+                const int r = rank + CL * (i / D), c = i % D;
+                float xm[CL], xl[CL], xv[CL], m = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < CL; ++k) {
+                    xm[k] = peer_f32(s_xm + r, k);
+                    xl[k] = peer_f32(s_xl + r, k);
+                    xv[k] = peer_f32(s_x + r * D + c, k);
+                }
+#pragma unroll
+                for (int k = 0; k < CL; ++k) m = fmaxf(m, xm[k]);
+                const float mu = m == -INFINITY ? 0.0f : m;
+                float acc = 0.0f, den = 0.0f;
+#pragma unroll
+                for (int k = 0; k < CL; ++k) {
+                    const float wt = ex2(xm[k] - mu);
+                    den = fmaf(wt, xl[k], den);
+                    acc = fmaf(wt, xv[k], acc);
+                }
+                if (!whole) {
+                    part[r * D + c] = acc;
+                    if (c == 0) {
+                        part[RT * D + r] = m;
+                        part[RT * D + RT + r] = den;
+                    }
+                } else if (const int row = tile * RT + r; row < rows) {
+                    const float y = den == 0.0f ? 0.0f : acc / den;  // 0: the row sees nothing
+                    T* o = static_cast<T*>(A.out) + (int64_t)(sp.start + row / A.group) * A.out_stride +
+                           (int64_t)(head * A.group + row % A.group) * D + c;
+                    if constexpr (HL) *o = y;
+                    else *o = __float2bfloat16_rn(y);
+                }
+            }
+        }
         if (!whole) {
             auto last_to_arrive = [&](unsigned long long* w, int count) {  // every thread's results, then the counter
-                __syncthreads();
-                if (threadIdx.x == 0) {
+                sync_all<CL>();
+                if (threadIdx.x == 0 && rank == 0) {
                     __threadfence();
-                    s_join.last = arrive(w, A.tag) == count - 1;
+                    s_join.last = arrive(w) == count - 1;
                     if (s_join.last) {
                         *reinterpret_cast<volatile unsigned long long*>(w) = A.tag << 16;  // for a replay of this launch
                         __threadfence();
                     }
                 }
-                __syncthreads();
-                return s_join.last != 0;
+                sync_all<CL>();
+                return __float_as_int(peer_or_own(reinterpret_cast<const float*>(&s_join.last))) != 0;
             };
             auto piece = [&](int i) { return A.part + ((int64_t)i * 2 + (i == s_join.c0 ? s_join.slot0 : 0)) * kPart; };
             // pieces first, first + step, ..: their weighted sum to the first one's slot, or to the output
@@ -739,8 +912,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                     pl[i] = __ldcg(x + RT);
                 }
                 __syncthreads();
+                // a cluster's CTAs take the 16-byte units in turn
 #pragma unroll 1
-                for (int i = threadIdx.x; i < RT * D / 4; i += 32 * kAttnWarps) {
+                for (int i = threadIdx.x * CL + rank; i < RT * D / 4; i += 32 * kAttnWarps * CL) {
                     const int r = i / (D / 4), c = 4 * (i % (D / 4));
                     float m = -INFINITY, den = 0.0f;
                     for (int k = 0; k < count; ++k) m = fmaxf(m, pm[k * RT + r]);
@@ -766,14 +940,16 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                     }
                 }
             };
-            if (last_to_arrive(A.tickets + s_join.first, s_join.count)) {
-                join(s_join.first, 1, s_join.count, s_join.groups == 1);
+            // A group of one has no counter: its piece may be the next tile's first, whose counter is at the same place.
+            if (s_join.count == 1 || last_to_arrive(A.tickets + s_join.first, s_join.count)) {
+                if (s_join.count > 1) join(s_join.first, 1, s_join.count, s_join.groups == 1);
                 if (s_join.groups > 1 && last_to_arrive(A.tickets + kMaxParts + s_join.c0, s_join.groups))
                     join(s_join.c0, s_join.size, s_join.groups, true);
             }
         }
         not_first = true;
-        __syncthreads();  // what lies over the rings has been read
+        sync_all<CL>();  // what lies over the rings has been read, by the cluster too
+        if (CL > 1) break;
         if (warp == 0) {
             const int64_t u = s_u[0] + step;
             Cursor c = s_cur;
@@ -788,35 +964,66 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
     }
 }
 
-template <typename T, int D, int RT>
-cudaError_t launch_typed(const AttnParams& P, int64_t units, cudaStream_t stream) {
-    // an upper bound of the row tiles: a sequence's last one may be part filled
-    const int64_t segs = ((int64_t)P.B.m * P.group / RT + (P.B.m < P.B.batch ? P.B.m : P.B.batch)) * P.kv_heads;
-    const size_t rings = (size_t)kAttnWarps * kRing * kStage<D>, join = (size_t)kAttnWarps * RT * D * sizeof(float);
+constexpr int kCluster = 8;
+
+template <typename T, int D, int RT, int CL>
+cudaError_t launch_cluster(const AttnParams& P, int max_len, cudaStream_t stream, int64_t segs, bool* fits) {
+    const size_t rings = (size_t)kAttnWarps * kRing * kStage<D>, join = (size_t)(kAttnWarps + 1) * RT * D * sizeof(float);
     const size_t smem = rings > join ? rings : join;
-    static bool set[64] = {};
+    static std::atomic<int> clusters[64];  // what the device holds at once; 0: not asked yet
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!set[dev]) {
-        e = cudaFuncSetAttribute(attn_kernel<T, D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        set[dev] = true;
-    }
-    int64_t grid = segs * units;
-    if (grid > P.parts) grid = P.parts;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(32 * kAttnWarps);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CL;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_kernel<T, D, RT>, P);
+    cfg.numAttrs = CL > 1 ? 2 : 1;
+    int most = clusters[dev].load(std::memory_order_relaxed);
+    if (most == 0) {
+        e = cudaFuncSetAttribute(attn_kernel<T, D, RT, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        most = P.parts;
+        if (CL > 1) {
+            cfg.gridDim = dim3(CL);
+            int n = 0;
+            e = cudaOccupancyMaxActiveClusters(&n, attn_kernel<T, D, RT, CL>, &cfg);
+            if (e != cudaSuccess) return e;
+            most = n < 1 ? 1 : n < P.parts ? n : P.parts;
+        }
+        clusters[dev].store(most, std::memory_order_relaxed);
+    }
+    if (CL > 1 && segs > most) {
+        *fits = false;
+        return cudaSuccess;
+    }
+    int64_t grid = segs * (kTileCost + max_len / (CL * kUnit) + 1);
+    if (grid > most) grid = most;
+    cfg.gridDim = dim3((unsigned)(grid * CL));
+    return cudaLaunchKernelEx(&cfg, attn_kernel<T, D, RT, CL>, P);
+}
+
+template <typename T, int D, int RT>
+cudaError_t launch_typed(const AttnParams& P, int max_len, cudaStream_t stream) {
+    const int64_t held = (int64_t)P.B.max_pages << P.B.page_shift;  // no sequence is longer than its table's row
+    if (max_len > held) max_len = (int)held;
+    // an upper bound of the row tiles: a sequence's last one may be part filled
+    const int64_t segs = ((int64_t)P.B.m * P.group / RT + (P.B.m < P.B.batch ? P.B.m : P.B.batch)) * P.kv_heads;
+    // Clusters where each tile finds one and is longer than a few of a CTA's units.
+    if (max_len > 4 * kUnit) {
+        bool fits = true;
+        const cudaError_t e = launch_cluster<T, D, RT, kCluster>(P, max_len, stream, segs, &fits);
+        if (e != cudaSuccess || fits) return e;
+    }
+    return launch_cluster<T, D, RT, 1>(P, max_len, stream, segs, nullptr);
 }
 
 // A value that no other launch of the process has (and, from a start that differs, hardly any other process's).
@@ -859,16 +1066,15 @@ cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int6
     P.parts = num_sms() * kCtasPerSm < kMaxParts ? num_sms() * kCtasPerSm : kMaxParts;
     P.err_flag = err_flag;
     P.max_rows = prompts ? kFewRows : 0x7FFFFFFF;
-    const int64_t units = (max_len + kUnit - 1) / kUnit + 1 + kTileCost;
     if (dtype == Q4K_F32)
-        return head_dim == 64 ? launch_typed<float, 64, 8>(P, units, stream) : launch_typed<float, 128, 8>(P, units, stream);
+        return head_dim == 64 ? launch_typed<float, 64, 8>(P, max_len, stream) : launch_typed<float, 128, 8>(P, max_len, stream);
     // bf16: tiles of 8 rows where a sequence's rows fit one (half the softmax), else 16; next to prompts
     // the other sequences mostly decode
     if ((prompts ? P.group : most) <= 8)
-        return head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 8>(P, units, stream)
-                              : launch_typed<__nv_bfloat16, 128, 8>(P, units, stream);
-    return head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 16>(P, units, stream)
-                          : launch_typed<__nv_bfloat16, 128, 16>(P, units, stream);
+        return head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 8>(P, max_len, stream)
+                              : launch_typed<__nv_bfloat16, 128, 8>(P, max_len, stream);
+    return head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 16>(P, max_len, stream)
+                          : launch_typed<__nv_bfloat16, 128, 16>(P, max_len, stream);
 }
 
 }  // namespace q4k

@@ -39,12 +39,18 @@ __device__ __forceinline__ SeqSpan seq_span(const PagedBatch& B, int i, bool* ba
     return s;
 }
 
-// Page of the sequence, or -1 (flag raised) when the table holds an id outside [0, num_pages).
-__device__ __forceinline__ int page_id(const PagedBatch& B, int seq, int page, int* err_flag) {
-    const int p = __ldcg(B.table + (int64_t)seq * B.max_pages + page);
+// Page of the sequence, or -1 (flag raised) when the table holds an id outside [0, num_pages). The
+// read and the check apart, for callers with other reads to issue in between.
+__device__ __forceinline__ int page_entry(const PagedBatch& B, int seq, int page) {
+    return __ldcg(B.table + (int64_t)seq * B.max_pages + page);
+}
+__device__ __forceinline__ int page_checked(const PagedBatch& B, int p, int* err_flag) {
     if ((unsigned)p < (unsigned)B.num_pages) return p;
     raise_flag(err_flag, Q4K_ERR_PAGE);
     return -1;
+}
+__device__ __forceinline__ int page_id(const PagedBatch& B, int seq, int page, int* err_flag) {
+    return page_checked(B, page_entry(B, seq, page), err_flag);
 }
 
 // ---- element access -----------------------------------------------------------------------------

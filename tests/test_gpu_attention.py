@@ -499,6 +499,21 @@ def test_attention_long_axis_is_split(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("long", [9000, 24000, 33333, 60001])
+def test_attention_one_long_sequence_among_short_ones(long, dtype):
+    """The long one's axis is cut into many pieces, joined in two levels; the short ones share its last piece."""
+    run_attention(31, [1] * 40, [1 + i % 3 for i in range(20)] + [long] + [2] * 19, 8, 2, 64, 128, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new,lens,window", [
+    ([1, 1, 1], [300, 5000, 0], 0), ([1, 0, 3], [2100, 0, 2047], 0), ([2], [20000], 0), ([1, 4], [7000, 9001], 3000)])
+def test_attention_few_long_sequences(new, lens, window, dtype):
+    """Few tiles: each is shared by clusters of CTAs, in proportion to its length. (A length below its new rows is flagged.)"""
+    run_attention(32, new, lens, 8, 2, 128, 64, dtype, window=window, flagged=12 if any(l < n for n, l in zip(new, lens)) else 0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("gain", [0.0, 1e-30, 30.0, 1e20])
 def test_attention_query_magnitudes(gain, dtype):
     """Queries of any size; at 1e20 the softmax is a choice of one token."""
