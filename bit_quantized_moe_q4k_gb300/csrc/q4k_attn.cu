@@ -36,7 +36,7 @@ constexpr int kTileCost = 4;                  // units that starting and ending 
 constexpr int kCtasPerSm = 3;
 // Up to this many query rows per kv head a sequence is worked on here, else by the prompt kernel.
 constexpr int kFewRows = 64;
-constexpr int kLeast = 4;                      // units of a cluster's part of a tile, at least
+constexpr int kLeast = 4;                      // units of a cluster's part of a tile, at least (8: 8000 tokens 15.4 -> 16.5 us)
 constexpr int kMaxParts = 512;                // CTAs that the workspace serves
 constexpr int kJoinCost = 8;                  // units that joining a tile is worth
 constexpr int kOneLevel = 16;                 // up to this many pieces of a tile are joined at once
@@ -182,6 +182,7 @@ __device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
 struct TilePart {
     int index, k;  // the tile among its sequence's (row tile, kv head), and its clusters
     int first, j;  // its first cluster; this one's number among them
+    bool more;     // there are more tiles than clusters, which then walk over them, a whole one at a time
 };
 template <int RT, int CL>
 __device__ __forceinline__ bool tile_part(const AttnParams& A, int c, int clusters, Cursor* cur, TilePart* p) {
@@ -199,10 +200,11 @@ __device__ __forceinline__ bool tile_part(const AttnParams& A, int c, int cluste
         units += __shfl_xor_sync(0xffffffffu, units, o);
     }
     const int64_t spare = max(clusters - tiles, (int64_t)0);
+    p->more = tiles > clusters;
     int64_t acc = 0;
     for (int base = 0; base < A.B.batch; base += 32) {
         const SeqWork w = base == 0 ? mine : seq_work<RT, CL>(A, base + lane);
-        const int k = w.tiles ? min(1 + (int)div_pos(w.units * spare, units), max(w.units / kLeast, 1)) : 1;
+        const int k = w.tiles ? min(1 + (int)div_pos(w.units * spare, units), w.units <= kJoinCost ? 1 : w.units / kLeast) : 1;
         const int64_t own = (int64_t)w.tiles * A.kv_heads * k, inc = warp_scan(own);
         const unsigned hit = __ballot_sync(0xffffffffu, c < acc + inc);
         if (hit) {
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
         if constexpr (CL > 1) {
             Cursor c{};
             TilePart p{};
-            const bool any = tile_part<RT, CL>(A, my_piece, min((int)gridDim.x / CL, A.parts), &c, &p);
+            const bool any = tile_part<RT, CL>(A, my_piece, gridDim.x / CL, &c, &p);
             if (lane == 0) {
                 s_cur = c;
                 s_tile = p;
@@ -949,8 +951,20 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
         }
         not_first = true;
         sync_all<CL>();  // what lies over the rings has been read, by the cluster too
-        if (CL > 1) break;
-        if (warp == 0) {
+        if constexpr (CL > 1) {
+            if (!s_tile.more) break;
+            if (warp == 0) {
+                Cursor c{};
+                TilePart p{};
+                const int clusters = gridDim.x / CL, next = s_tile.first + clusters;
+                const bool any = tile_part<RT, CL>(A, next, clusters, &c, &p);
+                if (lane == 0) {
+                    s_cur = c;
+                    s_tile = p;
+                    s_u[1] = any;
+                }
+            }
+        } else if (warp == 0) {
             const int64_t u = s_u[0] + step;
             Cursor c = s_cur;
             __syncwarp();
@@ -1012,17 +1026,18 @@ cudaError_t launch_cluster(const AttnParams& P, int max_len, cudaStream_t stream
 }
 
 template <typename T, int D, int RT>
-cudaError_t launch_typed(const AttnParams& P, int max_len, cudaStream_t stream) {
+cudaError_t launch_typed(const AttnParams& P, int64_t max_rows, int max_len, cudaStream_t stream) {
     const int64_t held = (int64_t)P.B.max_pages << P.B.page_shift;  // no sequence is longer than its table's row
     if (max_len > held) max_len = (int)held;
-    // an upper bound of the row tiles: a sequence's last one may be part filled
-    const int64_t segs = ((int64_t)P.B.m * P.group / RT + (P.B.m < P.B.batch ? P.B.m : P.B.batch)) * P.kv_heads;
-    // Clusters where each tile finds one and is longer than a few of a CTA's units.
-    if (max_len > 4 * kUnit) {
-        bool fits = true;
-        const cudaError_t e = launch_cluster<T, D, RT, kCluster>(P, max_len, stream, segs, &fits);
-        if (e != cudaSuccess || fits) return e;
-    }
+    // An upper bound of the row tiles: each sequence's last one may be part filled, and none has more than max_rows.
+    const int64_t seqs = P.B.m < P.B.batch ? P.B.m : P.B.batch, full = (int64_t)P.B.m * P.group / RT;
+    const int64_t each = max_rows > RT ? (max_rows + RT - 1) / RT : 1;
+    const int64_t segs = (full + seqs < seqs * each ? full + seqs : seqs * each) * P.kv_heads;
+    // Clusters where each tile finds one (51 at once on a GB300). 4 kv heads of 8 rows of fp32: one sequence of 1000 tokens
+    // 8.5 us with, 12.9 without; of 16000 17.3 and 22.7; ten of 2000 13.0 and 17.6; 64 tiles of 1000 20.6 and 17.6.
+    bool fits = true;
+    const cudaError_t e = launch_cluster<T, D, RT, kCluster>(P, max_len, stream, segs, &fits);
+    if (e != cudaSuccess || fits) return e;
     return launch_cluster<T, D, RT, 1>(P, max_len, stream, segs, nullptr);
 }
 
@@ -1066,15 +1081,16 @@ cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int6
     P.parts = num_sms() * kCtasPerSm < kMaxParts ? num_sms() * kCtasPerSm : kMaxParts;
     P.err_flag = err_flag;
     P.max_rows = prompts ? kFewRows : 0x7FFFFFFF;
+    const int64_t rows = prompts ? kFewRows : most;  // of a sequence, per kv head
     if (dtype == Q4K_F32)
-        return head_dim == 64 ? launch_typed<float, 64, 8>(P, max_len, stream) : launch_typed<float, 128, 8>(P, max_len, stream);
+        return head_dim == 64 ? launch_typed<float, 64, 8>(P, rows, max_len, stream) : launch_typed<float, 128, 8>(P, rows, max_len, stream);
     // bf16: tiles of 8 rows where a sequence's rows fit one (half the softmax), else 16; next to prompts
     // the other sequences mostly decode
     if ((prompts ? P.group : most) <= 8)
-        return head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 8>(P, max_len, stream)
-                              : launch_typed<__nv_bfloat16, 128, 8>(P, max_len, stream);
-    return head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 16>(P, max_len, stream)
-                          : launch_typed<__nv_bfloat16, 128, 16>(P, max_len, stream);
+        return head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 8>(P, rows, max_len, stream)
+                              : launch_typed<__nv_bfloat16, 128, 8>(P, rows, max_len, stream);
+    return head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 16>(P, rows, max_len, stream)
+                          : launch_typed<__nv_bfloat16, 128, 16>(P, rows, max_len, stream);
 }
 
 }  // namespace q4k
