@@ -75,25 +75,19 @@ __device__ __forceinline__ void append_page(const AppendParams& A, int seq, int 
                                             int heads, bool keys, float* s_max) {
     using Lane = HeadLane<D>;
     constexpr int kSet = W * Lane::kHeads * HELD;
-    const int pid = page_id(A.B, seq, page, A.err_flag);
-    if (pid < 0) return;
+    const int entry = page_entry(A.B, seq, page);  // looked at once the rows are on their way
     const int lane = threadIdx.x & 31, warp = W == 1 ? 0 : threadIdx.x >> 5, sub = lane / Lane::kLanes;
     const int first = s.len - s.n;                          // position of the first new row
     const int lo = max(max(first, 0) - page * P, 0);        // slots [lo, hi) of the page are new
     const int hi = min(s.len - page * P, P);
     const Lane ln(keys ? A.rot_dim : 0, A.pairs_mode);
-    float* sp = (keys ? A.k_scale : A.v_scale) + (int64_t)pid * heads + head;
-    uint8_t* codes = (keys ? A.k_cache : A.v_cache) + ((int64_t)pid * heads + head) * (P * D);
-    const float old = lo > 0 ? __ldcg(sp) : 0.0f;
     const int64_t stride = keys ? A.k_stride : A.v_stride;
     const T* x = static_cast<const T*>(keys ? A.k : A.v) + (int64_t)(s.start + page * P - first) * stride + head * D;
     float w[8];
     uint64_t F[4];
     const bool norm = keys && A.w_k != nullptr, rot = keys && A.rot_dim;
-    if (norm) ln.load(reinterpret_cast<const __nv_bfloat16*>(A.w_k), w);
-    if (rot) ln.fractions(A.inv_freq, F);
     float v[HELD][8];
-    auto take = [&](int set) {
+    auto read = [&](int set) {
 #pragma unroll
         for (int i = 0; i < HELD; ++i) {
             const int slot = set * kSet + (i * W + warp) * Lane::kHeads + sub;
@@ -101,6 +95,8 @@ __device__ __forceinline__ void append_page(const AppendParams& A, int seq, int 
             for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
             if (slot >= lo && slot < hi) ln.load(x + slot * stride, v[i]);
         }
+    };
+    auto turn = [&](int set) {
 #pragma unroll
         for (int i = 0; i < HELD; ++i) {
             const int slot = set * kSet + (i * W + warp) * Lane::kHeads;
@@ -114,9 +110,18 @@ __device__ __forceinline__ void append_page(const AppendParams& A, int seq, int 
         }
     };
     const int set0 = lo / kSet, set1 = (hi - 1) / kSet;
+    read(set0);
+    if (norm) ln.load(reinterpret_cast<const __nv_bfloat16*>(A.w_k), w);
+    if (rot) ln.fractions(A.inv_freq, F);
+    const int pid = page_checked(A.B, entry, A.err_flag);
+    if (pid < 0) return;  // the same in all threads
+    float* sp = (keys ? A.k_scale : A.v_scale) + (int64_t)pid * heads + head;
+    uint8_t* codes = (keys ? A.k_cache : A.v_cache) + ((int64_t)pid * heads + head) * (P * D);
+    const float old = lo > 0 ? __ldcg(sp) : 0.0f;
     float amax = 0.0f;
     for (int set = set0; set <= set1; ++set) {
-        take(set);
+        if (set != set0) read(set);
+        turn(set);
 #pragma unroll
         for (int i = 0; i < HELD; ++i)
 #pragma unroll
@@ -137,7 +142,10 @@ __device__ __forceinline__ void append_page(const AppendParams& A, int seq, int 
     if (W == 1 ? lane == 0 : threadIdx.x == 0) *sp = scale;  // every thread has read the old one
     const float inv = 1.0f / scale;  // exact: a power of two
     for (int set = set0; set <= set1; ++set) {
-        if (set0 != set1) take(set);
+        if (set0 != set1) {
+            read(set);
+            turn(set);
+        }
 #pragma unroll
         for (int i = 0; i < HELD; ++i) {
             const int slot = set * kSet + (i * W + warp) * Lane::kHeads + sub;

@@ -136,9 +136,25 @@ __device__ __forceinline__ uint64_t turn_fraction(double f) {
     uint64_t F = sh >= 64 ? 0 : sh >= 0 ? hi >> sh : sh > -64 ? hi << -sh : 0;
     return (bits >> 63) ? 0 - F : F;
 }
+// Sine and cosine of pos * F turns. The top bits choose the quadrant and leave |x| <= pi/4, where the
+// Taylor polynomials to x^9 and x^10 are within 2^-28 and 2^-29 of the functions: rounding is all the error.
 __device__ __forceinline__ void turn_sincos(int pos, uint64_t F, float* s, float* c) {
-    const int t = (int)(((uint64_t)(int64_t)pos * F) >> 32);               // turn * 2^32, in [-1/2, 1/2)
-    sincospif((float)t * 4.656612873077393e-10f, s, c);                    // 2^-31: half turns
+    const uint32_t t = (uint32_t)(((uint64_t)(int64_t)pos * F) >> 32);     // turn * 2^32
+    const uint32_t q = (t + 0x20000000u) >> 30;                            // quarter turns, rounded
+    const float x = (float)(int)(t - (q << 30)) * 1.46291807926715968e-9f; // 2 pi / 2^32
+    const float z = x * x;
+    float a = fmaf(z, 1.0f / 362880.0f, -1.0f / 5040.0f);
+    a = fmaf(z, a, 1.0f / 120.0f);
+    a = fmaf(z, a, -1.0f / 6.0f);
+    a = fmaf(x * z, a, x);
+    float b = fmaf(z, -1.0f / 3628800.0f, 1.0f / 40320.0f);
+    b = fmaf(z, b, -1.0f / 720.0f);
+    b = fmaf(z, b, 1.0f / 24.0f);
+    b = fmaf(z, b, -0.5f);
+    b = fmaf(z, b, 1.0f);
+    const float u = (q & 1) ? b : a, v = (q & 1) ? a : b;
+    *s = __uint_as_float(__float_as_uint(u) ^ (q & 2) << 30);
+    *c = __uint_as_float(__float_as_uint(v) ^ ((q + 1) & 2) << 30);
 }
 
 // A head spread over D/8 lanes, 8 dims a lane in two runs of 4, so that a lane holds four whole
@@ -163,6 +179,10 @@ struct HeadLane {
             c1 = c0 + 4;
         }
     }
+    __device__ __forceinline__ void shared(const float* head, float (&v)[8]) const {  // of a head in shared memory
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { v[i] = head[c0 + i]; v[4 + i] = head[c1 + i]; }
+    }
     template <typename T> __device__ __forceinline__ void load(const T* head, float (&v)[8]) const {
         float a[4], b[4];
         Vec<T>::load(head + c0, a);
@@ -186,22 +206,33 @@ struct HeadLane {
     // (a, b) -> (a cos - b sin, b cos + a sin)
     __device__ __forceinline__ void rotate(const float (&sn)[4], const float (&cs)[4], float (&v)[8]) const {
         if (!turns) return;
+        if (pairs) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = pairs ? v[2 * i] : v[i], b = pairs ? v[2 * i + 1] : v[4 + i];
-            const float x = a * cs[i] - b * sn[i], y = b * cs[i] + a * sn[i];
-            if (pairs) { v[2 * i] = x; v[2 * i + 1] = y; }
-            else { v[i] = x; v[4 + i] = y; }
+            for (int i = 0; i < 4; ++i) turn(sn[i], cs[i], v[2 * i], v[2 * i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) turn(sn[i], cs[i], v[i], v[4 + i]);
         }
     }
-    // v * w / sqrt(mean v^2 + eps), the mean over the head's lanes (the whole warp calls it)
-    __device__ __forceinline__ static void norm(const float (&w)[8], float eps, float (&v)[8]) {
+    __device__ __forceinline__ static void turn(float sn, float cs, float& a, float& b) {
+        const float x = a * cs - b * sn;
+        b = b * cs + a * sn;
+        a = x;
+    }
+    // 1 / sqrt(mean v^2 + eps), the mean over the head's lanes (the whole warp calls it): the hardware's estimate and one
+    // Newton step, half the instructions of a root and a quotient. (0: infinite, as the quotient would be.)
+    __device__ __forceinline__ static float inv_rms(float eps, const float (&v)[8]) {
         float ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
 #pragma unroll
         for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float r = 1.0f / sqrtf(ss / (float)D + eps);
+        const float a = fmaf(ss, 1.0f / (float)D, eps), r = rsqrtf(a);
+        const float n = r * fmaf(-0.5f * a * r, r, 1.5f);
+        return a > 1e-37f && a < 1e37f ? n : r;
+    }
+    __device__ __forceinline__ static void norm(const float (&w)[8], float eps, float (&v)[8]) {
+        const float r = inv_rms(eps, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = v[i] * r * w[i];
     }
