@@ -59,34 +59,31 @@ __device__ __forceinline__ int page_id(const PagedBatch& B, int seq, int page, i
 // may hold lines from before the writes.
 template <typename T> struct Vec;  // N consecutive elements of an input row as fp32
 template <> struct Vec<float> {
+    using Four = float4;  // four elements as they are in memory
+    static __device__ __forceinline__ void unpack(const Four& f, float* v) {
+        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+    }
     template <int N> static __device__ __forceinline__ void load(const float* p, float (&v)[N]) {
-        if constexpr (N == 2) {
-            const float2 a = __ldcg(reinterpret_cast<const float2*>(p));
-            v[0] = a.x; v[1] = a.y;
-        } else {
 #pragma unroll
-            for (int i = 0; i < N; i += 4) {
-                const float4 a = __ldcg(reinterpret_cast<const float4*>(p + i));
-                v[i] = a.x; v[i + 1] = a.y; v[i + 2] = a.z; v[i + 3] = a.w;
-            }
+        for (int i = 0; i < N; i += 4) {
+            const float4 a = __ldcg(reinterpret_cast<const float4*>(p + i));
+            v[i] = a.x; v[i + 1] = a.y; v[i + 2] = a.z; v[i + 3] = a.w;
         }
     }
     template <int N> static __device__ __forceinline__ void store(float* p, const float (&v)[N]) {
-        if constexpr (N == 2) {
-            *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
-        } else {
 #pragma unroll
-            for (int i = 0; i < N; i += 4)
-                *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        }
+        for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
     }
 };
 template <> struct Vec<__nv_bfloat16> {
+    using Four = uint2;
+    static __device__ __forceinline__ void unpack(const Four& f, float* v) {
+        v[0] = __uint_as_float(f.x << 16); v[1] = __uint_as_float(f.x & 0xFFFF0000u);
+        v[2] = __uint_as_float(f.y << 16); v[3] = __uint_as_float(f.y & 0xFFFF0000u);
+    }
     template <int N> static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&v)[N]) {
         uint32_t w[N / 2];
-        if constexpr (N == 2) {
-            w[0] = __ldcg(reinterpret_cast<const unsigned*>(p));
-        } else if constexpr (N == 4) {
+        if constexpr (N == 4) {
             const uint2 a = __ldcg(reinterpret_cast<const uint2*>(p));
             w[0] = a.x; w[1] = a.y;
         } else {
@@ -109,9 +106,7 @@ template <> struct Vec<__nv_bfloat16> {
             const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
             w[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
-        if constexpr (N == 2) {
-            *reinterpret_cast<uint32_t*>(p) = w[0];
-        } else if constexpr (N == 4) {
+        if constexpr (N == 4) {
             *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
         } else {
 #pragma unroll
@@ -189,6 +184,18 @@ struct HeadLane {
         Vec<T>::load(head + c1, b);
 #pragma unroll
         for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
+    }
+    // The same in two steps, for loads that are to be in flight while other work goes on.
+    template <typename T> struct Raw {
+        typename Vec<T>::Four a{}, b{};
+    };
+    template <typename T> __device__ __forceinline__ void load(const T* head, Raw<T>& r) const {
+        r.a = __ldcg(reinterpret_cast<const typename Vec<T>::Four*>(head + c0));
+        r.b = __ldcg(reinterpret_cast<const typename Vec<T>::Four*>(head + c1));
+    }
+    template <typename T> __device__ __forceinline__ static void unpack(const Raw<T>& r, float (&v)[8]) {
+        Vec<T>::unpack(r.a, v);
+        Vec<T>::unpack(r.b, v + 4);
     }
     template <typename T> __device__ __forceinline__ void store(T* head, const float (&v)[8]) const {
         const float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
