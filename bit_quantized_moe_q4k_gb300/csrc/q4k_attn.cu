@@ -34,8 +34,11 @@ constexpr int kChunk = 16;                    // tokens a warp takes at a time
 constexpr int kUnit = kChunk * kAttnWarps;    // tokens of one unit of work
 constexpr int kTileCost = 4;                  // units that starting and ending a tile are worth
 constexpr int kCtasPerSm = 3;
-// Up to this many query rows per kv head a sequence is worked on here, else by the prompt kernel.
-constexpr int kFewRows = 64;
+// A sequence is worked on here up to kFewRows query rows per kv head, and a whole batch up to kFewTiles tiles of 8 rows,
+// else by the prompt kernel, whose tiles hold 128 or 256 rows and are not split along the axis. fp32, 4 kv heads, here
+// and there: 16 sequences of 2000 tokens with 48 rows 43 and 45 us, with 64 51 and 46 (bf16 42 and 43), with 96 71 and
+// 48 (bf16 49 and 44); one of 4000 with 64 rows 16 and 70, with 256 34 and 73.
+constexpr int kFewRows = 64, kFewTiles = 450;
 constexpr int kLeast = 4;                      // units of a cluster's part of a tile, at least (8: 8000 tokens 15.4 -> 16.5 us)
 constexpr int kMaxParts = 512;                // CTAs that the workspace serves
 constexpr int kJoinCost = 8;                  // units that joining a tile is worth
@@ -1063,7 +1066,8 @@ cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int6
     // Which kernel a sequence takes goes by its query rows per kv head; max_q_len says which kernels can
     // be needed, and a kernel that is launched alone takes every sequence.
     const int64_t most = (int64_t)max_q_len * (q_heads / kv_heads);
-    const bool prompts = most > kFewRows, few = !prompts || !(B.batch == 1 || B.m == (int64_t)B.batch * max_q_len);
+    const bool prompts = most > kFewRows && (int64_t)B.m * q_heads > 8 * kFewTiles;
+    const bool few = !prompts || !(B.batch == 1 || B.m == (int64_t)B.batch * max_q_len);
     if (prompts) {
         const cudaError_t e = launch_attention_prompt(B, q, dtype, q_stride, q_heads, kv_heads, head_dim, k_cache, v_cache,
                                                       k_scale, v_scale, few ? kFewRows + 1 : 1, scale, window, out,

@@ -360,7 +360,9 @@ cudaError_t launch_page(const AppendParams& A, int kv_heads, cudaStream_t stream
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    // Mostly single tokens: a warp an item; else the CTA that shares a page's rows.
+    // Mostly single tokens: a warp an item; else the CTA that shares a page's rows. 64 sequences of 1 token 3.8 us and
+    // 6.7, of 4 4.2 and 9.8; 8 of 16 tokens 9.7 and 4.2. The mean is all the host knows, and a prompt among single
+    // tokens costs a warp up to 64 rounds of reads a page, so the bound is low.
     if (A.B.m <= 2 * (int64_t)A.B.batch) {
         cfg.gridDim = dim3((unsigned)items, (unsigned)((2 * kv_heads + kTokenWarps - 1) / kTokenWarps));
         cfg.blockDim = dim3(32 * kTokenWarps);

@@ -493,6 +493,28 @@ def test_attention_prompts_short_heads(new, lens, hq, hk, page, window, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,lens,hq,hk,page,window", [
+    ([130], [200], 64, 8, 32, 0), ([130], [200], 64, 8, 32, 33), ([257, 129], [257, 700], 32, 8, 16, 0), ([300], [421], 32, 2, 64, 150),
+    ([70, 1, 40], [70, 300, 111], 64, 4, 32, 0), ([65, 66, 1, 200], [65, 400, 50, 201], 28, 2, 16, 0), ([500], [500], 8, 8, 128, 0),
+    ([0, 300, 2], [7, 1300, 2], 14, 1, 128, 1), ([128, 128], [128, 256], 16, 1, 64, 100),
+])
+def test_attention_prompts_of_many_rows(new, lens, hq, hk, page, window, d, dtype):
+    """Batches with enough rows that prompts go to the prompt kernels, alone or next to sequences that decode."""
+    run_attention(sum(lens) + 1, new, lens, hq, hk, d, page, dtype, window, pad=16)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attention_prompts_of_many_rows_scales_and_magnitudes(dtype):
+    def spread(c):
+        c.scale["v"][:] = (2.0 ** np.resize([-40.0, 0.0, 30.0, -64.0, -3.0], c.scale["v"].size)).reshape(c.scale["v"].shape)
+    run_attention(51, [1, 3, 100], [130, 90, 120], 64, 8, 128, 16, dtype, pow2=False)
+    run_attention(52, [1, 2, 90], [130, 90, 200], 64, 8, 128, 16, dtype, codes_after=spread)
+    for gain in (0.0, 1e-30, 30.0):
+        run_attention(53, [140], [180], 32, 4, 128, 16, dtype, q_gain=gain)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_attention_long_axis_is_split(dtype):
     run_attention(5, [1], [20011], 8, 1, 128, 64, dtype)
     run_attention(6, [1, 1, 1], [9000, 2, 4097], 4, 2, 64, 16, dtype)
@@ -538,8 +560,9 @@ def test_attention_value_scales_far_apart(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("new,lens", [([1, 1], [5, 33]), ([3], [40]), ([80], [100]), ([200, 2], [200, 18])])
-def test_attention_nan_in_slots_past_the_end(new, lens, dtype):
+@pytest.mark.parametrize("new,lens,hq", [([1, 1], [5, 33], 8), ([3], [40], 8), ([80], [100], 8), ([200, 2], [200, 18], 8),
+                                         ([80], [100], 64), ([200, 2], [200, 18], 64)])
+def test_attention_nan_in_slots_past_the_end(new, lens, hq, dtype):
     page = 16
 
     def spoil(c):
@@ -550,16 +573,17 @@ def test_attention_nan_in_slots_past_the_end(new, lens, dtype):
             at += k
             for s in "kv":
                 c.codes[s][last, :, n - (k - 1) * page:] = 0x7F
-    run_attention(sum(lens), new, lens, 8, 2, 128, page, dtype, codes_after=spoil)
+    run_attention(sum(lens), new, lens, hq, 2, 128, page, dtype, codes_after=spoil)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("n,length,window", [(4, 40, 0), (6, 200, 20), (150, 200, 0), (150, 300, 40)])
-def test_attention_nan_reaches_only_the_rows_that_see_it(n, length, window, d, dtype):
+@pytest.mark.parametrize("n,length,window,hq", [(4, 40, 0, 4), (6, 200, 20, 4), (150, 200, 0, 4), (150, 300, 40, 4),
+                                                (150, 200, 0, 32), (150, 300, 40, 32)])
+def test_attention_nan_reaches_only_the_rows_that_see_it(n, length, window, hq, d, dtype):
     """NaN in one value dim of one token: that dim of the rows that see the token, nothing else;
     NaN in a key: every dim of those rows."""
-    page, hq, hk, dim = 16, 4, 2, 5
+    page, hk, dim = 16, 2, 5
     lens = [length]
     clean = run_attention(n, [n], lens, hq, hk, d, page, dtype, window)
     for side in "vk":
@@ -579,10 +603,10 @@ def test_attention_nan_reaches_only_the_rows_that_see_it(n, length, window, d, d
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("n,length", [(1, 40), (1, 9000), (3, 40), (90, 120)])
-def test_attention_nan_query(n, length, dtype):
+@pytest.mark.parametrize("n,length,hq", [(1, 40, 4), (1, 9000, 4), (3, 40, 4), (90, 120, 4), (90, 120, 64)])
+def test_attention_nan_query(n, length, hq, dtype):
     """A NaN in a query makes its row NaN (not the zero of a row that sees nothing), and no other row."""
-    hq, hk, d, page = 4, 2, 64, 16
+    hk, d, page = 2, 64, 16
     c = Cache(1, -(-length // page), hk, page, d)
     c.upload()
     q = rows(np.random.default_rng(1).standard_normal((n, hq * d)), dtype)
@@ -605,6 +629,8 @@ def test_attention_results_do_not_depend_on_hints_or_neighbours():
     for hints in ((1, 1), (300, 100000), (0, 0)):
         run_attention(31, [1, 40, 2], [400, 90, 17], 8, 2, 128, 16, "f32", hints=hints)
         run_attention(32, [1, 140, 2], [400, 190, 17], 8, 2, 128, 16, "bf16", hints=hints)
+        run_attention(33, [1, 140, 2], [400, 190, 17], 64, 8, 128, 16, "f32", hints=hints)
+        run_attention(34, [1, 140, 2], [400, 190, 17], 64, 8, 128, 16, "bf16", hints=hints)
 
 
 def test_attention_rows_before_the_sequence_are_zero():
@@ -613,17 +639,17 @@ def test_attention_rows_before_the_sequence_are_zero():
     assert (got[:2] == 0).all() and (got[4:] == 0).all() and (got[2:4] != 0).any()
 
 
-@pytest.mark.parametrize("new", [[1, 1], [90, 1]])
-def test_attention_bad_page_ids(new):
+@pytest.mark.parametrize("new,hq", [([1, 1], 8), ([90, 1], 8), ([90, 1], 64)])
+def test_attention_bad_page_ids(new, hq):
     """A page id outside the cache: flagged, its tokens are not seen; the other sequence is right."""
     page, lens = 16, [100, 40]
     c = Cache(6, 12, 2, page, 128)
     table = tables(c, lens)
-    good = run_attention(6, new, lens, 8, 2, 128, page, "f32", cache=c, table=table)
+    good = run_attention(6, new, lens, hq, 2, 128, page, "f32", cache=c, table=table)
     for bad in (-1, 12, 0x7FFFFFFF):
         t = table.copy()
         t[0, 2] = bad
-        got = run_attention(6, new, lens, 8, 2, 128, page, "f32", cache=c, table=t, check=False, flagged=11)
+        got = run_attention(6, new, lens, hq, 2, 128, page, "f32", cache=c, table=t, check=False, flagged=11)
         assert np.isfinite(got).all() and np.array_equal(got[new[0]:], good[new[0]:])
         assert not np.array_equal(got[:new[0]], good[:new[0]])
 
