@@ -12,15 +12,19 @@
 //
 // Bound by the cache's bytes. Each warp owns a ring of stages in shared memory, a stage being two chunks
 // of 16 tokens (2 KB of K and 2 KB of V each at head_dim 128), which its lanes fill by 16-byte
-// asynchronous copies one stage ahead. (Bulk copies of these pieces, 5 a chunk, held the rate to 2.3
-// TB/s: the copy engine takes about 50 ns for one, whatever its size.) The copies place 16-byte units so
-// that the fragment reads meet different banks. The work
-// (sequence, kv head, row tile, 64 tokens) is laid out on one line and cut into equal pieces, one per
-// CTA, whatever the lengths. The CTAs that share a tile leave partial results in the workspace; the last one to
-// arrive joins them, in two levels where there are many. Where there are few tiles (one sequence), clusters of
-// eight CTAs work as one, 512 tokens a unit, and join their tiles through distributed shared memory: an eighth of the
-// pieces, and reads of a few hundred cycles instead of the thousand and more through L2. (A second kernel for that found no room beside the first, so it
-// began to look for its tile only when the first had ended: 8 us of 49 for one sequence of 131071 tokens.)
+// asynchronous copies one stage ahead (bulk copies, five a chunk, took 223 us for the batch below where these then
+// took 199). The copies place 16-byte units so that the fragment reads meet different banks.
+//
+// The work (sequence, kv head, row tile, 64 tokens) is laid out on one line and cut into equal pieces, one per CTA,
+// whatever the lengths. The CTAs that share a tile leave partial results in the workspace; the last one to arrive
+// joins them, in two levels where there are many. (A second kernel for that found no room beside the first, so it began
+// to look for its tile only when the first had ended: 8 us of 49 for the long sequence below.) Where there are few
+// tiles, clusters of eight CTAs work as one, 512 tokens a unit, and join their tiles through distributed shared
+// memory: an eighth of the pieces, and reads of a few hundred cycles instead of the thousand and more through L2.
+//
+// 64 ragged sequences of up to 8192 tokens, 8 kv heads of 128, 514 MB: 102 us, 5.0 TB/s. One of 131071, 4 kv heads,
+// 134 MB: 39 us; beyond about 20 us of latency (launch, lengths, pages, queries, first copies, two joins) it streams
+// at 6.7 TB/s. One of 509: 8.5 us, that latency without the join through L2.
 #include <atomic>
 #include <chrono>
 
@@ -52,7 +56,7 @@ struct AttnParams {
     int64_t q_stride, out_stride;
     const uint8_t *k_cache, *v_cache;
     const float *k_scale, *v_scale;
-    int q_heads, kv_heads, group;
+    int kv_heads, group;
     int window;
     int max_rows;       // sequences with more query rows per kv head are the prompt kernel's
     float scale_log2;   // softmax scale * log2(e)
@@ -1077,7 +1081,7 @@ cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int6
     AttnParams P{};
     P.B = B; P.q = q; P.out = out; P.q_stride = q_stride; P.out_stride = out_stride;
     P.k_cache = k_cache; P.v_cache = v_cache; P.k_scale = k_scale; P.v_scale = v_scale;
-    P.q_heads = q_heads; P.kv_heads = kv_heads; P.group = q_heads / kv_heads; P.window = window;
+    P.kv_heads = kv_heads; P.group = q_heads / kv_heads; P.window = window;
     P.scale_log2 = scale * 1.44269504088896340736f;
     P.tickets = static_cast<unsigned long long*>(workspace);
     P.tag = next_tag();

@@ -200,12 +200,15 @@ __device__ __forceinline__ void append_tokens(const AppendParams& A, int seq, in
     const int set0 = S.lo / kSet, set1 = (S.hi - 1) / kSet;
     read(set0);
     if (norm) ln.load(reinterpret_cast<const __nv_bfloat16*>(A.w_k), w);
-    if (rot) ln.fractions(A.inv_freq, F);
+    double f[4];
+    if (rot) ln.frequencies(A.inv_freq, f);
     const int pid = page_checked(A.B, entry, A.err_flag);
     if (pid < 0) return;  // the same in all lanes
     float* sp = S.scale(A, pid, head, heads);
     uint8_t* codes = S.codes(A, pid, head, heads);
     const float old = S.lo > 0 ? __ldcg(sp) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) F[i] = rot ? turn_fraction(f[i]) : 0;
     float amax = 0.0f;
     for (int set = set0; set <= set1; ++set) {
         if (set != set0) read(set);
@@ -262,7 +265,7 @@ __device__ __forceinline__ void append_page(const AppendParams& A, int seq, int 
     if (rot) {
         const int pair = threadIdx.x % (D / 2);
         if (2 * pair < A.rot_dim) {
-            const uint64_t F = turn_fraction(A.inv_freq[pair]);
+            const uint64_t F = turn_fraction(__ldcg(A.inv_freq + pair));
             for (int slot = S.lo + threadIdx.x / (D / 2); slot < S.hi; slot += 32 * W / (D / 2))
                 turn_sincos(page * P + slot, F, s_turn + slot * D + pair, s_turn + slot * D + D / 2 + pair);
         }

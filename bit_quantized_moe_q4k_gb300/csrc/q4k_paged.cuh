@@ -202,9 +202,9 @@ struct HeadLane {
         Vec<T>::store(head + c0, a);
         Vec<T>::store(head + c1, b);
     }
-    __device__ __forceinline__ void fractions(const double* inv_freq, uint64_t (&F)[4]) const {
+    __device__ __forceinline__ void frequencies(const double* inv_freq, double (&f)[4]) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) F[i] = turns ? turn_fraction(inv_freq[j0 + i]) : 0;
+        for (int i = 0; i < 4; ++i) f[i] = turns ? __ldcg(inv_freq + j0 + i) : 0.0;
     }
     __device__ __forceinline__ void angles(int pos, const uint64_t (&F)[4], float (&sn)[4], float (&cs)[4]) const {
 #pragma unroll

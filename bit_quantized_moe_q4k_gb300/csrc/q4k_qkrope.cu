@@ -8,7 +8,7 @@
 // prompt below), and a warp takes one step of heads after the other.
 //
 // Bound by bytes: 8192 tokens of 40 heads of 128 in bf16, 168 MB, 35 us, 4.8 TB/s. What hides the latency is
-// warps, 56 an SM at 36 registers: two to four steps in flight per warp, at 70 to 114 registers, took 50 to 78 us.
+// warps, 64 an SM at 32 registers: two to four steps in flight per warp, at 70 to 114 registers, took 50 to 78 us.
 #include "q4k_paged.cuh"
 
 namespace q4k {
@@ -26,7 +26,7 @@ struct NormRopeParams {
 };
 
 constexpr int kRopeWarps = 4;
-constexpr int kRopeCtas = 14;  // of an SM: as many as hold a step without spills
+constexpr int kRopeCtas = 16;  // of an SM: all its warps, at 32 registers
 
 template <typename TI, typename TO, int D>
 __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
@@ -49,14 +49,27 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) norm_rope_kernel(c
     };
     float v[8] = {};
     take(h0 + sub, v);
-    const int pos = P.rot_dim ? __ldcg(P.pos + t) : 0;
-    // a side without weights multiplies by ones: its norm is computed (the warp's lanes stay together) and dropped
-    for (int i = threadIdx.x; i < D; i += 32 * kRopeWarps) {
-        s_w[0][i] = P.w_q ? __uint_as_float((uint32_t)P.w_q[i] << 16) : 1.0f;
-        s_w[1][i] = P.w_k ? __uint_as_float((uint32_t)P.w_k[i] << 16) : 1.0f;
-    }
-    for (int i = threadIdx.x; 2 * i < P.rot_dim; i += 32 * kRopeWarps)
-        turn_sincos(pos, turn_fraction(P.inv_freq[i]), &s_sn[i], &s_cs[i]);
+    // every read is on its way before the first is looked at
+    static_assert(D / 2 <= 32 * kRopeWarps, "an angle a thread");
+    constexpr int kEach = D > 32 * kRopeWarps ? D / (32 * kRopeWarps) : 1;
+    const int i = threadIdx.x;
+    const bool turns = 2 * i < P.rot_dim;
+    const int pos = turns ? __ldcg(P.pos + t) : 0;
+    const double f = turns ? __ldcg(P.inv_freq + i) : 0.0;
+    uint16_t w[2][kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+        if (const int c = i + 32 * kRopeWarps * j; c < D) {
+            w[0][j] = P.w_q ? __ldcg(P.w_q + c) : 0x3F80;  // a side without weights multiplies by ones
+            w[1][j] = P.w_k ? __ldcg(P.w_k + c) : 0x3F80;
+        }
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+        if (const int c = i + 32 * kRopeWarps * j; c < D) {
+            s_w[0][c] = __uint_as_float((uint32_t)w[0][j] << 16);
+            s_w[1][c] = __uint_as_float((uint32_t)w[1][j] << 16);
+        }
+    if (turns) turn_sincos(pos, turn_fraction(f), &s_sn[i], &s_cs[i]);
     __syncthreads();
     float sn[4], cs[4];
     if (ln.turns) {
@@ -70,11 +83,12 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) norm_rope_kernel(c
     for (; h0 < P.heads; h0 += stride) {
         const int h = h0 + sub;
         const bool is_q = h < P.q_heads;
-        float r = Lane::inv_rms(P.eps, v), w[8];
+        // the norm is computed for a side without weights too (the warp's lanes stay together), and dropped
+        float r = Lane::inv_rms(P.eps, v), g[8];
         if (!(is_q ? P.w_q : P.w_k)) r = 1.0f;
-        ln.shared(is_q ? s_w[0] : s_w[1], w);
+        ln.shared(is_q ? s_w[0] : s_w[1], g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] * r * w[i];
+        for (int i = 0; i < 8; ++i) v[i] = v[i] * r * g[i];
         ln.rotate(sn, cs, v);
         if (is_q) ln.store(qo + h * D, v);
         else if (h < P.heads) ln.store(ko + (h - P.q_heads) * D, v);

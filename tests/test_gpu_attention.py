@@ -14,6 +14,7 @@ Tolerances are counted from the kernels' roundings, u = 2^-24 (half a step of fp
     add 2^-11 of it, and the store half a step of the output type.
 """
 import math
+from pathlib import Path
 
 import numpy as np
 import pytest
@@ -691,16 +692,16 @@ def test_attention_offsets_past_32_bits():
             full[int(ids[0, i])] = dev(small.codes[s][i])
         ks[int(ids[0, i])] = dev(small.scale["k"][i])
         vs[int(ids[0, i])] = dev(small.scale["v"][i])
-    for n in (1, 160):
-        q = rows(g.standard_normal((n, hk * d)), "f32")
+    for n, hq, dtype in ((1, hk, "f32"), (160, hk, "f32"), (240, 2 * hk, "f32"), (240, 2 * hk, "bf16")):
+        q = rows(g.standard_normal((n, hq * d)), dtype)
         out = torch.empty_like(q)
-        nbytes = q4k.q4k_paged_attention_workspace_size(1, n, hk, hk, d)
+        nbytes = q4k.q4k_paged_attention_workspace_size(1, n, hq, hk, d)
         ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
-        q4k.q4k_paged_attention(q, n, hk, hk, d, hk * d, k, v, ks, vs, dev(np.array([0, n], np.int32)),
+        q4k.q4k_paged_attention(q, n, hq, hk, d, hq * d, k, v, ks, vs, dev(np.array([0, n], np.int32)),
                                 dev(np.array([300], np.int32)), dev(ids), 1, 3, page, pages, n, 300, 0.09, 0, out,
-                                hk * d, ws, nbytes)
-        ref, tol = attention_ref(f64(q).reshape(n, hk, d), small, np.array([[0, 1, 2]]), [n], [300], 1, 0.09, 0, "f32")
-        assert (np.abs(f64(out).reshape(n, hk, d) - ref) <= tol).all()
+                                hq * d, ws, nbytes)
+        ref, tol = attention_ref(f64(q).reshape(n, hq, d), small, np.array([[0, 1, 2]]), [n], [300], hq // hk, 0.09, 0, dtype)
+        assert (np.abs(f64(out).reshape(n, hq, d) - ref) <= tol).all()
     # an append into the last page
     kv = rows(g.standard_normal((1, 2 * hk * d)), "f32")
     q4k.q4k_kv_append(kv, kv[:, hk * d:], 1, hk, d, 2 * hk * d, 2 * hk * d, None, EPS, None, 0, 0,
@@ -709,6 +710,26 @@ def test_attention_offsets_past_32_bits():
     got = E4M3[host(v[pages - 1, :, 0])] * host(vs[pages - 1]).astype(np.float64)[:, None]
     x = f64(kv)[0, hk * d:].reshape(hk, d)
     assert (np.abs(got - x) <= np.maximum(2.0 ** -4 * np.abs(x), 2.0 ** -10 * host(vs[pages - 1])[:, None])).all()
+
+
+def test_decoder_layer_example():
+    """Prompts and then single tokens give what the same tokens give in one call, up to the cache's rounding: a page whose
+    scale grows under later tokens has its codes rounded twice, by e4m3's 2^-4 at most each, in a sum of many."""
+    import sys
+    sys.path.insert(0, str(Path(__file__).resolve().parent.parent / "examples"))
+    import decoder_layer as ex
+    prompts, steps = (5, 33, 130), 4
+    xs, out, layer, _ = ex.run(prompts, steps, seed=3, hidden=512, inter=256, experts=4, top_k=4)
+    lens = [n + steps for n in prompts]
+    cache = ex.Cache(len(lens), max(lens), layer.hk, layer.d)
+    cache.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+    pos = torch.cat([torch.arange(n, dtype=torch.int32, device="cuda") for n in lens])
+    y = layer.forward(torch.cat(xs), pos, ex.starts(lens), cache, max(lens), max(lens), layer.buffers(sum(lens), len(lens)))
+    layer.check()
+    for a, b in zip(y.split(lens), out):
+        a, b = f64(a), f64(b)
+        assert np.isfinite(a).all()
+        assert (np.linalg.norm(a - b, axis=1) <= 2.0 ** -4 * np.linalg.norm(a, axis=1)).all()
 
 
 def test_the_three_calls_in_a_graph():
