@@ -92,10 +92,64 @@ __device__ __forceinline__ void expand16(const uint4& c, uint32_t (&h)[8]) {
     e4m3x4_to_f16x4(c.w, &h[6], &h[7]);
 }
 
+// The block's item among two to 32 sequences (lane i holds the i-th): the items in falling order of the tokens that
+// they walk over, in steps of 128, since the last ones to start decide when the kernel ends. A sequence's tiles
+// that walk over L tokens or more are its last ones, so their number is a quotient, and L is found by bisection.
+// (Sequence by sequence, six ragged chunks of fp32 took 178 us instead of 158.)
+__device__ __forceinline__ void find_by_length(const PromptParams& A, int tile_rows, const SeqSpan& s, int tiles, int* item) {
+    const int lane = threadIdx.x & 31, most = A.window > 0 ? A.window + tile_rows / A.group : 0x7FFFFFFF;
+    auto count = [&](int step) {  // this sequence's items of at least 128 * step tokens
+        const int tokens = 128 * step;
+        if (step == 0) return tiles * A.kv_heads;
+        if (tokens > s.len || tokens > most) return 0;
+        const int before = max(tokens - 1 - (s.len - s.n), 0) * A.group / tile_rows;
+        return max(tiles - before, 0) * A.kv_heads;
+    };
+    const int at = blockIdx.x;
+    int lo = 0, hi = (__reduce_max_sync(0xffffffffu, tiles ? s.len : 0) >> 7) + 1;  // count(lo) > at >= count(hi)
+    if ((int)__reduce_add_sync(0xffffffffu, count(0)) <= at) {
+        if (lane == 0) item[0] = -1;
+        return;
+    }
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((int)__reduce_add_sync(0xffffffffu, count(mid)) > at) lo = mid;
+        else hi = mid;
+    }
+    const int above = count(hi), own = count(lo) - above;
+    int inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    const int rest = at - (int)__reduce_add_sync(0xffffffffu, above) - (inc - own);
+    if (rest >= 0 && rest < own) {  // one lane
+        item[0] = lane;
+        item[1] = tiles * A.kv_heads - above - 1 - rest;
+        item[2] = s.start;
+        item[3] = s.n;
+        item[4] = s.len;
+    }
+}
+
 // The block's item: sequence, row tile * kv_heads + kv head, its first row, new tokens and length; -1 past
-// the last. Items are taken from the last row tile of the last sequence down, so the longest come first.
+// the last. Otherwise from the last row tile of the last sequence down.
 __device__ __forceinline__ void find_item(const PromptParams& A, int tile_rows, int* item) {
     const int lane = threadIdx.x & 31;
+    if (A.B.batch > 1 && A.B.batch <= 32) {
+        SeqSpan s{0, 0, 0};
+        int tiles = 0;
+        if (lane < A.B.batch) {
+            bool bad;
+            s = seq_span(A.B, lane, &bad);
+            if (bad) raise_flag(A.err_flag, Q4K_ERR_SEQ);
+            const int rows = s.n * A.group;
+            if (rows >= A.min_rows) tiles = (rows + tile_rows - 1) / tile_rows;
+        }
+        find_by_length(A, tile_rows, s, tiles, item);
+        return;
+    }
     int at = blockIdx.x;
     for (int top = A.B.batch; top > 0; top -= 32) {
         const int i = top - 1 - lane;  // lane 0: the last sequence
