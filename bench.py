@@ -573,6 +573,9 @@ def time_graph(step, K, Wm, stream, local_rank, soak_s=0.3):
     """Eager warm-up, W steps then K steps captured in CUDA graphs; clocks sampled over an
     untimed soak of the K-step graph and the timed replay. Returns (ms per step, clocks)."""
     import torch
+    # The inputs were written on the default stream, and buffers made last may lie where its queued work still writes
+    # tensors that are freed already: all of that has to end before another stream uses them.
+    torch.cuda.synchronize()
     for i in range(3):
         with torch.cuda.stream(stream):
             step(i)
