@@ -9,7 +9,7 @@
 // holds hardly depends on how many calls filled it.
 //
 // Single tokens (up to two a sequence): a warp per item, bound by latency, a chain of lengths, page and row, scale:
-// 3.0 us for one sequence, 6.2 for 256 of 8 heads. Item i < batch is sequence i's first page, so a decode batch
+// 2.6 us for one sequence, 6.7 for 256 of 8 heads. Item i < batch is sequence i's first page, so a decode batch
 // finds its work without a search; further pages are found by a scan over the sequences. Prompts: a CTA per
 // (page, side) that takes heads one after the other, the next one's rows on their way, so that the chain and the
 // sines are paid once: 8191 tokens of 8 heads of 128 in bf16, 50 MB, 23 us, 2.2 TB/s (a CTA per head: 28). Each

@@ -4,7 +4,7 @@ plain fp64 implementations written here, through the C ABI.
 Tolerances are counted from the kernels' roundings, u = 2^-24 (half a step of fp32):
   * norm and rotation: the sum of squares has at most 13 additions, all terms positive (13 u,
     halved by the root), mean, eps, root and reciprocal 3.5 u, two products 2 u: 12 u of the normed
-    value; sine and cosine are within 5.4 u (pi u from rounding the turn to fp32, 2 u of sincospi,
+    value; sine and cosine are within 5.4 u (3 u pi/4 from the reduced angle in fp32, 2 u of the polynomials,
     0.3 u of the 32-bit turn); two products and a sum: 2 u. Together below 24 u (|a| + |b|).
   * the append adds half a step of e4m3: 2^-4 |x|, or 2^-10 of the scale where that is larger.
   * attention, per row: |ds| <= S (2^-22 + (d/16 + 8) 2^-23) with S the largest sum_c |q_c k_c| *
