@@ -22,7 +22,7 @@
 // tiles, clusters of eight CTAs work as one, 512 tokens a unit, and join their tiles through distributed shared
 // memory: an eighth of the pieces, and reads of a few hundred cycles instead of the thousand and more through L2.
 //
-// 64 ragged sequences of up to 8192 tokens, 8 kv heads of 128, 514 MB: 102 us, 5.0 TB/s. One of 131071, 4 kv heads,
+// 64 ragged sequences of up to 8192 tokens, 8 kv heads of 128, 514 MB: 96 us, 5.3 TB/s. One of 131071, 4 kv heads,
 // 134 MB: 39 us; beyond about 20 us of latency (launch, lengths, pages, queries, first copies, two joins) it streams
 // at 6.7 TB/s. One of 509: 8.5 us, that latency without the join through L2.
 #include <atomic>
@@ -36,7 +36,9 @@ namespace {
 constexpr int kAttnWarps = 4;
 constexpr int kChunk = 16;                    // tokens a warp takes at a time
 constexpr int kUnit = kChunk * kAttnWarps;    // tokens of one unit of work
-constexpr int kTileCost = 4;                  // units that starting and ending a tile are worth
+// Units that starting and ending a tile are worth. Ragged batches of 64 up to 8192 tokens, 256 up to 2000, 40 up to
+// 30000: 102, 87, 184 us with 4; 96, 76, 174 with 10; 97, 79, 173 with 16.
+constexpr int kTileCost = 10;
 constexpr int kCtasPerSm = 3;
 // A sequence is worked on here up to kFewRows query rows per kv head, and a whole batch up to kFewTiles tiles of 8 rows,
 // else by the prompt kernel, whose tiles hold 128 or 256 rows and are not split along the axis. fp32, 4 kv heads, here
@@ -45,8 +47,9 @@ constexpr int kCtasPerSm = 3;
 constexpr int kFewRows = 64, kFewTiles = 450;
 constexpr int kLeast = 4;                      // units of a cluster's part of a tile, at least (8: 8000 tokens 15.4 -> 16.5 us)
 constexpr int kMaxParts = 512;                // CTAs that the workspace serves
-constexpr int kJoinCost = 8;                  // units that joining a tile is worth
-constexpr int kOneLevel = 16;                 // up to this many pieces of a tile are joined at once
+constexpr int kJoinCost = 8;                  // units that joining a tile is worth (16: 8000 tokens 15.4 -> 17.5 us)
+static_assert(kJoinCost >= kLeast, "a tile that is shared has a unit for each cluster");
+constexpr int kOneLevel = 16;                 // up to this many pieces of a tile are joined at once (4: 16000 tokens 17 -> 21 us)
 constexpr int kTickets = 2 * kMaxParts;       // arrival counters before the partial results: by group of pieces, by tile
 
 struct AttnParams {
