@@ -1070,6 +1070,7 @@ cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int6
                              int head_dim, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
                              const float* v_scale, int max_q_len, int max_len, float scale, int window, void* out,
                              int64_t out_stride, void* workspace, int* err_flag, cudaStream_t stream) {
+    if (window >= 1 << 30) window = 0;  // no sequence is longer: every row sees all before it
     // Which kernel a sequence takes goes by its query rows per kv head; max_q_len says which kernels can
     // be needed, and a kernel that is launched alone takes every sequence.
     const int64_t most = (int64_t)max_q_len * (q_heads / kv_heads);

@@ -102,7 +102,7 @@ cudaError_t launch_dim(const NormRopeParams& P, cudaStream_t stream) {
     // token wants every head at once, a prompt the angles computed once.
     const int steps = (P.heads + HeadLane<D>::kHeads - 1) / HeadLane<D>::kHeads;
     const int most = (steps + kRopeWarps - 1) / kRopeWarps;
-    const int want = (16 * num_sms() + kRopeWarps * P.m - 1) / (kRopeWarps * P.m);
+    const int64_t want = (16 * num_sms() + kRopeWarps * (int64_t)P.m - 1) / (kRopeWarps * (int64_t)P.m);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)P.m, (unsigned)(want < most ? want : most));
     cfg.blockDim = dim3(32 * kRopeWarps);

@@ -506,6 +506,13 @@ def test_attention_prompts_of_many_rows(new, lens, hq, hk, page, window, d, dtyp
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new,lens,hq", [([1, 2], [70, 300], 8), ([150, 1], [150, 300], 64)])
+def test_attention_largest_window(new, lens, hq, dtype):
+    wide = run_attention(54, new, lens, hq, 2, 128, 16, dtype, window=0x7FFFFFFF)
+    assert np.array_equal(wide, run_attention(54, new, lens, hq, 2, 128, 16, dtype, window=0))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_attention_prompts_of_many_rows_scales_and_magnitudes(dtype):
     def spread(c):
         c.scale["v"][:] = (2.0 ** np.resize([-40.0, 0.0, 30.0, -64.0, -3.0], c.scale["v"].size)).reshape(c.scale["v"].shape)
