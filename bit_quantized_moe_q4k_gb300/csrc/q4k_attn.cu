@@ -1029,7 +1029,9 @@ cudaError_t launch_cluster(const AttnParams& P, int max_len, cudaStream_t stream
         *fits = false;
         return cudaSuccess;
     }
-    int64_t grid = segs * (kTileCost + max_len / (CL * kUnit) + 1);
+    // no more CTAs or clusters than can share the tiles: the others would only look for work
+    const int units = max_len / (CL * kUnit) + 1;
+    int64_t grid = segs * (units <= kJoinCost ? 1 : CL > 1 ? units / kLeast : kTileCost + units);
     if (grid > most) grid = most;
     cfg.gridDim = dim3((unsigned)(grid * CL));
     return cudaLaunchKernelEx(&cfg, attn_kernel<T, D, RT, CL>, P);
