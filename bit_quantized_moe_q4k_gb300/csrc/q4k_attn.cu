@@ -187,7 +187,7 @@ __device__ __forceinline__ int64_t total_work(const AttnParams& A, const SeqWork
 __device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
     return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
-// What cluster `c` of `clusters` works on: a tile's units are shared by k clusters, k in proportion to its length but
+// What cluster (or CTA) `c` of `clusters` works on, `mine` being the work of sequence `lane`: a tile's units are shared by k clusters, k in proportion to its length but
 // at least one, and at least kLeast units a cluster; no cluster takes a part of two tiles.
 struct TilePart {
     int index, k;  // the tile among its sequence's (row tile, kv head), and its clusters
@@ -195,9 +195,8 @@ struct TilePart {
     bool more;     // there are more tiles than clusters, which then walk over them, a whole one at a time
 };
 template <int RT, int CL>
-__device__ __forceinline__ bool tile_part(const AttnParams& A, int c, int clusters, Cursor* cur, TilePart* p) {
+__device__ __forceinline__ bool tile_part(const AttnParams& A, const SeqWork& mine, int c, int clusters, Cursor* cur, TilePart* p) {
     const int lane = threadIdx.x & 31;
-    const SeqWork mine = seq_work<RT, CL>(A, lane);
     int64_t tiles = (int64_t)mine.tiles * A.kv_heads, units = tiles * mine.units;
     for (int i = 32 + lane; i < A.B.batch; i += 32) {
         const SeqWork w = seq_work<RT, CL>(A, i);
@@ -348,12 +347,28 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
     __shared__ int64_t s_u[2], s_total;
     __shared__ int s_pieces;
     __shared__ TilePart s_tile;
+    __shared__ bool s_by_tile;
     __shared__ struct { int c0, slot0, size, groups, first, count, last; } s_join;
     if (warp == 0) {
-        if constexpr (CL > 1) {
+        const SeqWork mine = seq_work<RT, CL>(A, lane);
+        int longest = mine.units;
+        int64_t tiles = (int64_t)mine.tiles * A.kv_heads;
+        for (int i = 32 + lane; CL == 1 && i < A.B.batch; i += 32) {
+            const SeqWork w = seq_work<RT, CL>(A, i);
+            longest = max(longest, w.units);
+            tiles += (int64_t)w.tiles * A.kv_heads;
+        }
+        longest = __reduce_max_sync(0xffffffffu, longest);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+        // Joining a tile costs about as much as eight of its units: where no tile is longer, a CTA takes a whole one if
+        // there are enough (128 tiles of up to 400 tokens: 13 us, cut into equal pieces 24).
+        const bool by_tile = CL > 1 || (longest <= kJoinCost && tiles <= gridDim.x);
+        if (lane == 0) s_by_tile = by_tile;
+        if (by_tile) {
             Cursor c{};
             TilePart p{};
-            const bool any = tile_part<RT, CL>(A, my_piece, gridDim.x / CL, &c, &p);
+            const bool any = tile_part<RT, CL>(A, mine, my_piece, gridDim.x / CL, &c, &p);
             if (lane == 0) {
                 s_cur = c;
                 s_tile = p;
@@ -361,14 +376,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                 s_u[1] = any;
             }
         } else {
-            const SeqWork mine = seq_work<RT, 1>(A, lane);
             s_work[lane] = mine;
             const int64_t total = total_work<RT>(A, mine);
-            // Joining a tile costs about as much as eight of its units: where no tile is longer, pieces are not shorter
-            // than a whole one.
-            int longest = mine.units;
-            for (int i = 32 + lane; i < A.B.batch; i += 32) longest = max(longest, seq_work<RT, 1>(A, i).units);
-            longest = __reduce_max_sync(0xffffffffu, longest);
+            // more such tiles than CTAs: pieces are not shorter than a whole one
             const int64_t least = longest <= kJoinCost ? kTileCost + longest : 1;
             const int pieces = (int)min((int64_t)min((int)gridDim.x, A.parts), div_pos(total + least - 1, least));
             const bool any = my_piece < pieces;
@@ -393,7 +403,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
         const SeqSpan sp = s_cur.w.s;
         const int w_lo = s_cur.w.lo, seq = s_cur.seq;
         int tile, head, ua, ub, step = 0;
-        if constexpr (CL > 1) {
+        const bool by_tile = CL > 1 || s_by_tile;
+        if (by_tile) {
             ua = (int)((int64_t)s_cur.w.units * s_tile.j / s_tile.k);
             ub = (int)((int64_t)s_cur.w.units * (s_tile.j + 1) / s_tile.k);
             tile = s_tile.index / A.kv_heads;
@@ -416,7 +427,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
         if (!whole && threadIdx.x == 32) {
             // the tile's pieces c0 .. c1, in groups of about the root of their number where they are many
             int c0, c1, slot0 = 0;
-            if constexpr (CL > 1) {
+            if (by_tile) {
                 c0 = s_tile.first;
                 c1 = c0 + s_tile.k - 1;
             } else {
@@ -961,13 +972,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
         }
         not_first = true;
         sync_all<CL>();  // what lies over the rings has been read, by the cluster too
-        if constexpr (CL > 1) {
+        if (by_tile) {
             if (!s_tile.more) break;
             if (warp == 0) {
                 Cursor c{};
                 TilePart p{};
                 const int clusters = gridDim.x / CL, next = s_tile.first + clusters;
-                const bool any = tile_part<RT, CL>(A, next, clusters, &c, &p);
+                const bool any = tile_part<RT, CL>(A, seq_work<RT, CL>(A, lane), next, clusters, &c, &p);
                 if (lane == 0) {
                     s_cur = c;
                     s_tile = p;

@@ -536,6 +536,13 @@ def test_attention_one_long_sequence_among_short_ones(long, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("batch,longest", [(20, 200), (40, 511), (70, 200), (70, 700), (200, 60)])
+def test_attention_many_short_sequences(batch, longest, dtype):
+    """A CTA per tile, more tiles than CTAs, and tiles that are cut although they are many."""
+    run_attention(55, [1] * batch, [1 + 37 * i % longest for i in range(batch - 1)] + [longest], 8, 8, 64, 32, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("new,lens,window", [
     ([1, 1, 1], [300, 5000, 0], 0), ([1, 0, 3], [2100, 0, 2047], 0), ([2], [20000], 0), ([1, 4], [7000, 9001], 3000)])
 def test_attention_few_long_sequences(new, lens, window, dtype):
