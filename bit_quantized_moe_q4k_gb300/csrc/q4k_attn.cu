@@ -934,7 +934,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                     pm[i] = __ldcg(x);
                     pl[i] = __ldcg(x + RT);
                 }
-                __syncthreads();
+                sync_all<CL>();  // the first piece's maxima and denominators are written over below: the whole cluster has them
                 // a cluster's CTAs take the 16-byte units in turn
 #pragma unroll 1
                 for (int i = threadIdx.x * CL + rank; i < RT * D / 4; i += 32 * kAttnWarps * CL) {

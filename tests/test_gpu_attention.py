@@ -784,3 +784,73 @@ def test_the_three_calls_in_a_graph():
             t.copy_(k)
         step()
         assert torch.equal(got, out)
+
+
+# ---- one sequence over a long cache --------------------------------------------------------------
+
+class LongCache:
+    """One sequence's pages in a cache made on the device: random codes (no NaN) and power-of-two scales."""
+
+    def __init__(self, seed, length, heads, page, d):
+        g = torch.Generator("cuda").manual_seed(seed)
+        self.heads, self.page, self.d, self.length = heads, page, d, length
+        self.pages = -(-length // page) + 1
+        shape = (self.pages, heads, page, d)
+        self.codes = {s: (torch.randn(shape, generator=g, device="cuda") * 60).clamp(-440, 440).to(torch.float8_e4m3fn)
+                      for s in "kv"}
+        self.scale = {s: torch.ldexp(torch.ones((), device="cuda"), torch.randint(lo, lo + 4, shape[:2], generator=g, device="cuda"))
+                      for s, lo in (("k", -9), ("v", -10))}
+        self.table = torch.randperm(self.pages, generator=g, device="cuda").to(torch.int32)[None, :-1].contiguous()
+
+    def values(self, side):
+        """[heads, length, d] in fp64, on the device."""
+        ids = self.table[0].long()
+        v = self.codes[side].view(torch.uint8)[ids].view(torch.float8_e4m3fn).double() * self.scale[side][ids].double()[..., None, None]
+        return v.transpose(0, 1).reshape(self.heads, -1, self.d)[:, :self.length]
+
+
+def long_attention_ref(q, cache, n, group, scale, dtype):
+    """attention_ref for one sequence's last n tokens, on the device: (result, bound), [n, q_heads, d]."""
+    d, length = cache.d, cache.length
+    q = q.double().view(n, -1, d)
+    out, tol = torch.zeros_like(q), torch.zeros_like(q)
+    k, v = cache.values("k"), cache.values("v")
+    for r in range(n):
+        seen = length - n + r + 1
+        for h in range(q.shape[1]):
+            kk, vv = k[h // group, :seen], v[h // group, :seen]
+            s = kk @ q[r, h] * scale
+            p = torch.softmax(s, 0)
+            ds = scale * (kk.abs() @ q[r, h].abs()).max() * (2.0 ** -22 + (d / 16 + 8) * 2.0 ** -23)
+            x = (s.abs().max() * 1.45 + 64 + 14) * 2.0 ** -23 + 2.0 ** -22
+            rel = 2 * (ds + x) + (seen / 64 + 40) * U + (2.0 ** -11 * 1.01 if dtype == "bf16" else 0.0)
+            out[r, h] = p @ vv
+            tol[r, h] = rel * (p @ vv.abs()) + STEP[dtype] * out[r, h].abs() * 1.01
+    return out, tol
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hk", [1, 2, 3])
+@pytest.mark.parametrize("n,length", [(1, 34816), (1, 40000), (2, 131071)])
+def test_attention_one_sequence_over_a_long_cache(n, length, hk, d, dtype):
+    """Few tiles and a long axis: more than sixteen clusters share a tile and join it in two levels. The same bits each time."""
+    group, page = 4, 64
+    c = LongCache(length + hk, length, hk, page, d)
+    q = rows(np.random.default_rng(length + d).standard_normal((n, group * hk * d)), dtype)
+    scale, nbytes = 1 / math.sqrt(d), q4k.q4k_paged_attention_workspace_size(1, n, group * hk, hk, d)
+    start, lens = dev(np.array([0, n], np.int32)), dev(np.array([length], np.int32))
+    flag, got = err_flag(), []
+    for fill in (0xFF, 0, 0x55):
+        ws = torch.full((nbytes,), fill, dtype=torch.uint8, device="cuda")
+        for _ in range(20):
+            out = torch.full_like(q, 7.0)
+            q4k.q4k_paged_attention(q, n, group * hk, hk, d, group * hk * d, c.codes["k"], c.codes["v"], c.scale["k"], c.scale["v"],
+                                    start, lens, c.table, 1, c.table.shape[1], page, c.pages, n, length, scale, 0, out,
+                                    group * hk * d, ws, nbytes, flag)
+            got.append(out)
+    assert int(host(flag)[0]) == 0
+    assert all(torch.equal(got[0], x) for x in got[1:])
+    ref, tol = long_attention_ref(q, c, n, group, scale, dtype)
+    worst = float(((got[0].double().view_as(ref) - ref).abs() / tol).max())
+    assert worst <= 1, f"{worst} of the bound"
