@@ -200,6 +200,12 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatil
     return __all_sync(0xffffffffu, done) != 0;
 }
 
+// A warp's one arrival, once each of its lanes has read what the barrier gives back.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // Expands half tiles (64 rows) of the cache. A thread reads 16 codes of rows 32 x + rs, in each 64-dim panel,
 // and writes them as two 16-byte units of the panel's 128-byte rows; the eight threads of a store's phase
 // hold two rows of different parity, so their units lie on different banks.
@@ -292,8 +298,7 @@ __device__ __forceinline__ bool page_ahead(const PromptParams& A, int seq, int h
             m.inv[lane] = 1.0f / vs;
         }
         if (lane == 0) m.all_ok = all;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&meta_full[j % kMetaRing]);
+        warp_arrive(&meta_full[j % kMetaRing]);
     }
     return true;
 }
@@ -315,7 +320,7 @@ __device__ __forceinline__ bool expand_side(const PromptParams& A, bool v_side, 
     for (int j = 0; j < n; ++j) {
         const int e = entry(j), slot = e % kSlots, m = j % kMetaRing;
         ld.fetch(metas[m], 1, toks - kToks * j, rb);
-        if (lane == 0) mbar_arrive(&meta_empty[m]);
+        warp_arrive(&meta_empty[m]);
         if (!wait_all(&empty[slot], ((e / kSlots) & 1) ^ 1, abort, A.wait_ns)) return false;
         uint8_t* base = s_kv + slot * (kToks * D * 2);
         ld.put(base, v_side, ra, j, nan_tiles);
@@ -720,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             l *= ex2(ref - use);
             ref = r_new;
             l += weights2(tmem + lane_base + kColS + b * kToks, meta, crow, use, t0, lo, hi, whole);
-            if (lane == 0) mbar_arrive(&meta_empty[j % kMetaRing]);
+            warp_arrive(&meta_empty[j % kMetaRing]);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&p_full[b]);
@@ -755,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 corr = ex2(m - (m_new == -INFINITY ? 0.0f : m_new));
                 m = m_new;
                 s_ref[b][row] = m_new;
-                if (lane == 0) mbar_arrive(&meta_empty[j % kMetaRing]);
+                warp_arrive(&meta_empty[j % kMetaRing]);
                 tc_fence_before();
                 mbar_arrive(&max_full[b]);
             } else {
@@ -1042,7 +1047,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt2_kernel(const __grid_
                 }
                 l += weights(at, meta, crow, ref == -INFINITY ? 0.0f : ref, t0, lo, hi, whole);
             }
-            if (lane == 0) mbar_arrive(&meta_empty[j % kMetaRing]);
+            warp_arrive(&meta_empty[j % kMetaRing]);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&p_full[x]);

@@ -854,3 +854,26 @@ def test_attention_one_sequence_over_a_long_cache(n, length, hk, d, dtype):
     ref, tol = long_attention_ref(q, c, n, group, scale, dtype)
     worst = float(((got[0].double().view_as(ref) - ref).abs() / tol).max())
     assert worst <= 1, f"{worst} of the bound"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,page,n,length", [(64, 16, 60, 4003), (128, 16, 61, 4003), (128, 128, 63, 9001)])
+def test_attention_prompt_over_many_tiles(d, page, n, length, dtype):
+    """The prompt kernels' rings of pages and slots turn over many times. The same bits each time."""
+    group, hk = 8, 8
+    c = LongCache(length + d, length, hk, page, d)
+    q = rows(np.random.default_rng(length + d).standard_normal((n, group * hk * d)), dtype)
+    scale, nbytes = 1 / math.sqrt(d), q4k.q4k_paged_attention_workspace_size(1, n, group * hk, hk, d)
+    ws, flag, got = torch.empty(nbytes, dtype=torch.uint8, device="cuda"), err_flag(), []
+    start, lens = dev(np.array([0, n], np.int32)), dev(np.array([length], np.int32))
+    for _ in range(10):
+        out = torch.full_like(q, 7.0)
+        q4k.q4k_paged_attention(q, n, group * hk, hk, d, group * hk * d, c.codes["k"], c.codes["v"], c.scale["k"], c.scale["v"],
+                                start, lens, c.table, 1, c.table.shape[1], page, c.pages, n, length, scale, 0, out,
+                                group * hk * d, ws, nbytes, flag)
+        got.append(out)
+    assert int(host(flag)[0]) == 0
+    assert all(torch.equal(got[0], x) for x in got[1:])
+    ref, tol = long_attention_ref(q, c, n, group, scale, dtype)
+    worst = float(((got[0].double().view_as(ref) - ref).abs() / tol).max())
+    assert worst <= 1, f"{worst} of the bound"
