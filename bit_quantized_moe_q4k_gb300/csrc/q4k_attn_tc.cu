@@ -18,6 +18,8 @@
 // Bound by the issue of instructions and the latency between S and P: a 128 x 128 x 128 product takes 512 cycles of the
 // tensor core, two a tile of fp32 rows' one. bf16, 8192 tokens, 32 / 8 heads, head_dim 128: 510 us, 1077
 // TFLOP/s of the pairs that are seen (56% of the card's measured dense rate).
+#include <atomic>
+
 #include "q4k_paged.cuh"
 #include "q4k_sm100.cuh"
 #include "q4k_sync.cuh"
@@ -1102,15 +1104,15 @@ cudaError_t launch_typed(const PromptParams& P, cudaStream_t stream) {
     }
     // every CTA holds all of its SM's tensor memory: enough shared memory that one fits
     const int smem = bytes < 144 * 1024 ? 144 * 1024 : bytes;
-    static bool set[64] = {};
+    static std::atomic<bool> allowed[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!set[dev]) {
+    if (!allowed[dev].load(std::memory_order_relaxed)) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        set[dev] = true;
+        allowed[dev].store(true, std::memory_order_relaxed);
     }
     // an upper bound of the row tiles: a sequence's last one may be part filled
     const int64_t items = ((int64_t)P.B.m * P.group / rows + (P.B.m < P.B.batch ? P.B.m : P.B.batch)) * P.kv_heads;
