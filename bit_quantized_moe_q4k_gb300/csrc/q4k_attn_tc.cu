@@ -186,18 +186,20 @@ __device__ __forceinline__ void find_item(const PromptParams& A, int tile_rows, 
     if (lane == 0) item[0] = -1;
 }
 
-// A wait of a whole warp, bounded in time: its lanes go on, or give up, together.
+// A wait of a whole warp, bounded in time: its lanes go on, or give up, together. The clock is looked at every 64 tries;
+// below a millisecond, which a try that suspends the thread may outlast, the tries do not suspend it and each looks.
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
-    bool done = mbar_try_wait(bar, parity);
+    const bool short_limit = limit_ns < 1000000;
+    bool done = short_limit ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
     uint64_t t0 = 0;
     for (uint32_t i = 1; !done; ++i) {
         if (*abort) break;
-        if ((i & 63) == 0) {  // the limit is looked at every 64 tries
+        if (short_limit || (i & 63) == 0) {
             const uint64_t t = global_timer_ns();
             if (t0 == 0) t0 = t;
             else if (t - t0 > limit_ns) break;
         }
-        done = mbar_try_wait(bar, parity);
+        done = short_limit ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
     }
     return __all_sync(0xffffffffu, done) != 0;
 }
@@ -688,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 mma_commit_elect(&o_full[j & 1]);
                 mma_commit_elect(&empty[slot]);
             }
-            if (!ok && issued) {  // outstanding products finish before tensor memory is freed
+            if (issued) {  // whichever role gave up: outstanding products finish before tensor memory is freed
                 volatile int never = 0;
                 mma_commit_elect(&drain);
                 mbar_wait(&drain, 0, &never);
@@ -975,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt2_kernel(const __grid_
                     }
                 }
             }
-            if (!ok && issued) {  // outstanding products finish before tensor memory is freed
+            if (issued) {  // whichever role gave up: outstanding products finish before tensor memory is freed
                 volatile int never = 0;
                 mma_commit_elect(&drain);
                 mbar_wait(&drain, 0, &never);

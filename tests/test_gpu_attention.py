@@ -877,3 +877,33 @@ def test_attention_prompt_over_many_tiles(d, page, n, length, dtype):
     ref, tol = long_attention_ref(q, c, n, group, scale, dtype)
     worst = float(((got[0].double().view_as(ref) - ref).abs() / tol).max())
     assert worst <= 1, f"{worst} of the bound"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_prompt_wait_limit_runs_out(d, dtype, monkeypatch):
+    """Short wait limits (Q4K_WAIT_NS) make the prompt kernels' roles give up at different places: they leave together, the
+    products under way finish before tensor memory is freed, Q4K_ERR_TIMEOUT is in the device flag, and the next call
+    with the default limit is right. A call that no wait of ran out is right too."""
+    n, length, hq, hk, page = 300, 1500, 32, 4, 32
+    c = LongCache(d, length, hk, page, d)
+    q = rows(np.random.default_rng(d).standard_normal((n, hq * d)), dtype)
+    nbytes = q4k.q4k_paged_attention_workspace_size(1, n, hq, hk, d)
+    ws, start, lens = torch.empty(nbytes, dtype=torch.uint8, device="cuda"), dev(np.array([0, n], np.int32)), dev(np.array([length], np.int32))
+
+    def call():
+        out, flag = torch.full_like(q, 7.0), err_flag()
+        q4k.q4k_paged_attention(q, n, hq, hk, d, hq * d, c.codes["k"], c.codes["v"], c.scale["k"], c.scale["v"], start, lens,
+                                c.table, 1, c.table.shape[1], page, c.pages, n, length, 0.1, 0, out, hq * d, ws, nbytes, flag)
+        return out, int(host(flag)[0])
+
+    good, status = call()
+    assert status == 0
+    for limit in (1, 200, 500, 1000, 2000, 4000, 8000, 20000, 100000):
+        monkeypatch.setenv("Q4K_WAIT_NS", str(limit))
+        for _ in range(3):
+            out, status = call()
+            assert status == 10 or (status == 0 and limit > 1 and torch.equal(out, good)), limit
+        monkeypatch.delenv("Q4K_WAIT_NS")
+        out, status = call()
+        assert status == 0 and torch.equal(out, good)
