@@ -186,20 +186,22 @@ __device__ __forceinline__ void find_item(const PromptParams& A, int tile_rows, 
     if (lane == 0) item[0] = -1;
 }
 
-// A wait of a whole warp, bounded in time: its lanes go on, or give up, together. The clock is looked at every 64 tries;
-// below a millisecond, which a try that suspends the thread may outlast, the tries do not suspend it and each looks.
+// A wait of a whole warp, bounded in time: its lanes go on, or give up, together. The clock is looked at every 64 tries.
+// A try suspends the thread, maybe for longer than a limit below a millisecond, so with SHORT such a limit is polled
+// for; the page warp does, whose abort ends the others' waits (in all roles it took 515 us for the prompt below, not 508).
+template <bool SHORT = false>
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
-    const bool short_limit = limit_ns < 1000000;
-    bool done = short_limit ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+    const bool poll = SHORT && limit_ns < 1000000;
+    bool done = poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
     uint64_t t0 = 0;
     for (uint32_t i = 1; !done; ++i) {
         if (*abort) break;
-        if (short_limit || (i & 63) == 0) {
+        if (poll || (i & 63) == 0) {
             const uint64_t t = global_timer_ns();
             if (t0 == 0) t0 = t;
             else if (t - t0 > limit_ns) break;
         }
-        done = short_limit ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+        done = poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
     }
     return __all_sync(0xffffffffu, done) != 0;
 }
@@ -293,7 +295,7 @@ __device__ __forceinline__ bool page_ahead(const PromptParams& A, int seq, int h
             vs = __ldcg(A.v_scale + ph);
         }
         const bool all = __all_sync(0xffffffffu, lane >= kGroups || pid >= 0 || tok >= kv_hi);
-        if (!wait_all(&meta_empty[j % kMetaRing], ((j / kMetaRing) & 1) ^ 1, abort, A.wait_ns)) return false;
+        if (!wait_all<true>(&meta_empty[j % kMetaRing], ((j / kMetaRing) & 1) ^ 1, abort, A.wait_ns)) return false;
         TileMeta& m = metas[j % kMetaRing];
         if (lane < kGroups) {
             m.at[lane] = pid < 0 ? (int64_t)-1 : ((ph << A.B.page_shift) + (tok & ((1 << A.B.page_shift) - 1))) * D;
