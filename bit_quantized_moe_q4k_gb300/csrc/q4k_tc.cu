@@ -396,8 +396,8 @@ tc_gemm_kernel(const __grid_constant__ TcParams P) {
             }
         }
         }
-        if (!ok && lane == 0) {
-            // let the copies already issued land before the CTA leaves (bounded)
+        if (lane == 0) {
+            // whichever role gave up: the copies already issued land before the CTA leaves (bounded)
             volatile int never = 0;
             for (int g = max(0, raw_issued - kNRaw); g < raw_issued; ++g)
                 mbar_wait(&bar_raw_full[g % kNRaw], (g / kNRaw) & 1, &never);
@@ -498,11 +498,11 @@ tc_gemm_kernel(const __grid_constant__ TcParams P) {
                 s_abort = 1;
                 raise_flag(P.err_flag, Q4K_ERR_TIMEOUT);
             }
-            if (issued > 0) {  // outstanding MMAs finish before tensor memory is freed
-                volatile int never = 0;
-                mma_commit_elect(&bar_drain);
-                mbar_wait(&bar_drain, 0, &never);
-            }
+        }
+        if (issued > 0) {  // whichever role gave up: outstanding MMAs finish before tensor memory is freed
+            volatile int never = 0;
+            mma_commit_elect(&bar_drain);
+            mbar_wait(&bar_drain, 0, &never);
         }
         __syncwarp();
     } else {
