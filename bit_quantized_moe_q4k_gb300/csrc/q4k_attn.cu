@@ -3,12 +3,15 @@
 //   out[r] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q_r . k_j)  over the tokens j that row r sees
 //
 // With everything in powers of two and V's page scale 2^e_j inside the exponent,
-//   x_j = c * (code_k . q) * ks_j + e_j,   P_j = 2^(x_j - M),  M the running maximum of x,
+//   x_j = c * (code_k . q) * ks_j + e_j,   P_j = 2^(x_j - M + 15),  M the running maximum of x,
 //   l = sum_j 2^(-e_j) P_j,   out = sum_j P_j code_v,j / l,
 // so the codes of both sides enter the matrix products as they are: e4m3 is exact in fp16. Query
 // rows are the M side of mma.m16n8k16: fp32 queries are split into two fp16 halves (hi in rows 0-7,
 // lo in rows 8-15, scaled by a power of two so that 22 bits survive) and so are their P; bf16
-// queries are exact in one half and P is rounded to fp16 (2^-12), so 16 rows fill the tile.
+// queries are exact in one half and P is rounded to fp16 (2^-11), so 16 rows fill the tile. 2^15 is
+// the largest power of two in fp16, and the low half of P is held times 2^11, so that small weights (all of them where
+// one token without value dominates) stay normal numbers: P_j keeps its 11 or 22 bits down to 2^-29 of the
+// largest, below that 2^-40 or 2^-51 of it.
 //
 // Bound by the cache's bytes. Each warp owns a ring of stages in shared memory, a stage being two chunks
 // of 16 tokens (2 KB of K and 2 KB of V each at head_dim 128), which its lanes fill by 16-byte
@@ -89,10 +92,16 @@ __device__ __forceinline__ void mma_16816_zero(float (&c)[4], const uint32_t (&a
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
-// Two fp32 additions or products in one instruction, each rounded to nearest.
+// Two fp32 operations in one instruction, each rounded to nearest.
 __device__ __forceinline__ void add2(float2& a, float x, float y) {
     float2 b = make_float2(x, y);
     asm("add.rn.f32x2 %0, %0, %1;" : "+l"(reinterpret_cast<uint64_t&>(a)) : "l"(reinterpret_cast<uint64_t&>(b)));
+}
+__device__ __forceinline__ void fma2(float2& a, float x, float y, float scale) {  // a += (x, y) * scale
+    float2 b = make_float2(x, y), c = make_float2(scale, scale);
+    asm("fma.rn.f32x2 %0, %1, %2, %0;"
+        : "+l"(reinterpret_cast<uint64_t&>(a))
+        : "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
 }
 __device__ __forceinline__ void mul2(float2& a, float x) {
     float2 b = make_float2(x, x);
@@ -672,6 +681,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                 const float m_new = fmaxf(mx[j], top);
                 grew = grew || m_new > mx[j];
                 const float m_use = m_new == -INFINITY ? 0.0f : m_new;
+                const float base = __fadd_ru(m_use, -15.0f);  // rounded up: x - base is 15 at most
                 corr[j] = ex2(mx[j] - m_use);
                 mx[j] = m_new;
                 l[j] *= corr[j];
@@ -680,7 +690,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                     float sum = 0.0f;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        x[c][j][k] = ex2(x[c][j][k] - (m_use - 7.0f));  // P * 2^7: fp16 keeps more of the small ones
+                        x[c][j][k] = ex2(x[c][j][k] - base);
                         sum += x[c][j][k];
                     }
                     l[j] = fmaf(sum, inv[c], l[j]);
@@ -717,8 +727,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                     const float2 b0 = __half22float2(h0), b1 = __half22float2(h1);
                     pa[c][0] = *reinterpret_cast<const uint32_t*>(&h0);
                     pa[c][2] = *reinterpret_cast<const uint32_t*>(&h1);
-                    pa[c][1] = pack_f16(x[c][0][0] - b0.x, x[c][0][1] - b0.y);
-                    pa[c][3] = pack_f16(x[c][0][2] - b1.x, x[c][0][3] - b1.y);
+                    float2 r0 = make_float2(x[c][0][0], x[c][0][1]), r1 = make_float2(x[c][0][2], x[c][0][3]);
+                    mul2(r0, 2048.0f);
+                    mul2(r1, 2048.0f);
+                    fma2(r0, b0.x, b0.y, -2048.0f);
+                    fma2(r1, b1.x, b1.y, -2048.0f);
+                    pa[c][1] = pack_f16(r0.x, r0.y);
+                    pa[c][3] = pack_f16(r1.x, r1.y);
                 } else {
                     pa[c][0] = pack_f16(x[c][0][0], x[c][0][1]);
                     pa[c][2] = pack_f16(x[c][0][2], x[c][0][3]);
@@ -795,7 +810,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
 #pragma unroll
                     for (int c = 1; c < S; ++c) mma_16816(acc, pa[c], b0[c][k], b1[c][k]);
                     add2(o[4 * q + k][0], acc[0], acc[1]);
-                    if (HL) add2(o[4 * q + k][0], acc[2], acc[3]);
+                    if (HL) fma2(o[4 * q + k][0], acc[2], acc[3], 1.0f / 2048.0f);
                     if (RT == 16) add2(o[4 * q + k][NR - 1], acc[2], acc[3]);
                 }
             }

@@ -1,9 +1,11 @@
 // q4k_attn_tc.cu -- attention over the paged 8-bit cache for many query rows per kv head (prompts), on the
 // tensor cores.
 //
-// The mathematics of q4k_attn.cu: x_j = c (code_k . q) + e_j, P_j = 2^(x_j - M + 7), out = sum P_j code_v,j /
+// The mathematics of q4k_attn.cu: x_j = c (code_k . q) + e_j, P_j = 2^(x_j - M + B), out = sum P_j code_v,j /
 // sum 2^(-e_j) P_j, with the codes of both sides exact in fp16, bf16 queries in one fp16 term and fp32
-// queries (and their P) in two.
+// queries (and their P) in two. P is 2^15 at most, fp16's largest power of two: B is 15, or 9 where M may be behind by
+// 2^6 (bf16). So P_j keeps its 11 bits down to 2^-23 of the largest and 2^-34 of it below (bf16), its 22 bits down to
+// 2^-29 and 2^-51 of it below (fp32, whose low term is held times 2^11).
 //
 // A CTA takes 128 (fp32) or 256 (bf16) query rows of one kv head (row r: token r / group, head r % group, so the
 // heads of a group share each K and V tile) and walks over the tokens that some row sees, 128 at a time:
@@ -16,8 +18,8 @@
 // instructions (the bf16 prompt below took 1863 us with the first, fully unrolled ones).
 //
 // Bound by the issue of instructions and the latency between S and P: a 128 x 128 x 128 product takes 512 cycles of the
-// tensor core, two a tile of fp32 rows' one. bf16, 8192 tokens, 32 / 8 heads, head_dim 128: 510 us, 1077
-// TFLOP/s of the pairs that are seen (56% of the card's measured dense rate).
+// tensor core, two a tile of fp32 rows' one. bf16, 8192 tokens, 32 / 8 heads, head_dim 128: 517 us, 1064
+// TFLOP/s of the pairs that are seen (55% of the card's measured dense rate).
 #include <atomic>
 
 #include "q4k_paged.cuh"
@@ -80,6 +82,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     float2 d;
     asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
         : "=l"(reinterpret_cast<uint64_t&>(d))
         : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
     return d;
@@ -315,7 +324,6 @@ template <int D, int kSlots, typename Entry>
 __device__ __forceinline__ bool expand_side(const PromptParams& A, bool v_side, int toks, int n, Entry entry, uint8_t* s_kv,
                                             const TileMeta* metas, uint64_t* meta_full, uint64_t* meta_empty, uint64_t* full,
                                             uint64_t* empty, int* nan_tiles, volatile int* abort) {
-    const int lane = threadIdx.x & 31;
     Loader<D> ld(v_side ? A.v_cache : A.k_cache, threadIdx.x & 127);
     uint4 ra[Loader<D>::kLoads], rb[Loader<D>::kLoads];
     if (n > 0) {
@@ -381,18 +389,28 @@ __device__ __forceinline__ float row_max(uint32_t at, const TileMeta& meta, floa
     return top;
 }
 
-// P of one group's 16 tokens, packed to fp16 (and what that leaves, packed to fp16: lo8, where wanted), and its sum.
-__device__ __forceinline__ float group_weights(const uint32_t* v, const TileMeta& meta, int g, float crow, float ref, int t0,
-                                               int lo, int hi, bool whole, uint32_t* hi8, uint32_t* lo8) {
-    const float c = crow * meta.ks[g], e = meta.ev[g] - (ref - 7.0f);
+constexpr float kTop = 15.0f;  // log2 of the largest P
+
+// What x is taken from in the exponent of P, with references up to kNear and so with x - base in one rounding; further off
+// than that x is rounded first, as its maximum was (x <= M, and base is rounded up), so that P stays below 2^16 still.
+constexpr float kNear = 1048576.0f;
+__device__ __forceinline__ float weight_base(float ref, float bits) { return __fadd_ru(ref, -bits); }
+__device__ __forceinline__ bool all_near(float ref) { return __all_sync(0xffffffffu, fabsf(ref) < kNear) != 0; }
+
+// P of one group's 16 tokens, packed to fp16 (and what that leaves times 2^11, packed to fp16: lo8, where wanted), and its
+// sum. plain: the row sees them all, and its reference is near.
+__device__ __forceinline__ float group_weights(const uint32_t* v, const TileMeta& meta, int g, float crow, float base, int t0,
+                                               int lo, int hi, bool plain, uint32_t* hi8, uint32_t* lo8) {
+    const float c = crow * meta.ks[g], e = plain ? meta.ev[g] - base : meta.ev[g];
     float2 p[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         p[k] = fma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), make_float2(c, c), make_float2(e, e));
-    if (!whole) {
+    if (!plain) {
         const int tok = t0 + 16 * g, from = meta.at[g] >= 0 ? lo - tok : 16, to = hi - tok;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
+            p[k] = add2(p[k], make_float2(-base, -base));
             if (2 * k < from || 2 * k >= to) p[k].x = -INFINITY;
             if (2 * k + 1 < from || 2 * k + 1 >= to) p[k].y = -INFINITY;
         }
@@ -404,17 +422,16 @@ __device__ __forceinline__ float group_weights(const uint32_t* v, const TileMeta
         const __half2 h = __floats2half2_rn(p[k].x, p[k].y);
         hi8[k] = h2_bits(h);
         if (lo8) {
-            const float2 f = fma2(__half22float2(h), make_float2(-1.0f, -1.0f), p[k]);
+            const float2 f = fma2(__half22float2(h), make_float2(-2048.0f, -2048.0f), mul2(p[k], make_float2(2048.0f, 2048.0f)));
             lo8[k] = h2_bits(__floats2half2_rn(f.x, f.y));
         }
     }
     const float2 sum = add2(add2(add2(p[0], p[1]), add2(p[2], p[3])), add2(add2(p[4], p[5]), add2(p[6], p[7])));
     return sum.x + sum.y;
 }
-// P = 2^(x - ref + 7) of a row in the place of its S, and the row's share of the denominator: 32 tokens' P take 16
+// P = 2^(x - base) of a row in the place of its S, and the row's share of the denominator: 32 tokens' P take 16
 // columns (one fp16 term), columns of S that have been read.
-__device__ __forceinline__ float weights(uint32_t at, const TileMeta& meta, float crow, float ref, int t0, int lo, int hi,
-                                         bool whole) {
+__device__ __forceinline__ float weights(uint32_t at, const TileMeta& meta, float crow, float base, int t0, int lo, int hi) {
     float l = 0.0f;
 #pragma unroll 1
     for (int q = 0; q < kToks / 32; ++q) {
@@ -422,7 +439,7 @@ __device__ __forceinline__ float weights(uint32_t at, const TileMeta& meta, floa
         tmem_ld32(at + 32 * q, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) l = fmaf(group_weights(&v[16 * h], meta, 2 * q + h, crow, ref, t0, lo, hi, whole, &pk[8 * h], nullptr),
+        for (int h = 0; h < 2; ++h) l = fmaf(group_weights(&v[16 * h], meta, 2 * q + h, crow, base, t0, lo, hi, false, &pk[8 * h], nullptr),
                                              meta.inv[2 * q + h], l);
         tmem_st16(at + 16 * q, pk);
     }
@@ -430,8 +447,8 @@ __device__ __forceinline__ float weights(uint32_t at, const TileMeta& meta, floa
 }
 // The same in two fp16 terms: 32 tokens' P take the 32 columns of their S, 16 high, then 16 low. The next group's S
 // is read before this one's P is written (over part of it).
-__device__ __forceinline__ float weights2(uint32_t at, const TileMeta& meta, float crow, float ref, int t0, int lo, int hi,
-                                          bool whole) {
+__device__ __forceinline__ float weights2(uint32_t at, const TileMeta& meta, float crow, float base, int t0, int lo, int hi,
+                                          bool plain) {
     float l = 0.0f;
     uint32_t v[2][16];
     tmem_ld16(at, v[0]);
@@ -439,12 +456,12 @@ __device__ __forceinline__ float weights2(uint32_t at, const TileMeta& meta, flo
     auto step = [&](int g, uint32_t (&now)[16], uint32_t (&next)[16], bool all) {
         uint32_t hi8[8], lo8[8];
         if (g + 1 < kGroups) tmem_ld16(at + 16 * (g + 1), next);
-        l = fmaf(group_weights(now, meta, g, crow, ref, t0, lo, hi, all, hi8, lo8), meta.inv[g], l);
+        l = fmaf(group_weights(now, meta, g, crow, base, t0, lo, hi, all, hi8, lo8), meta.inv[g], l);
         tmem_wait_ld();
         tmem_st8(at + 32 * (g >> 1) + 8 * (g & 1), hi8);
         tmem_st8(at + 32 * (g >> 1) + 8 * (g & 1) + 16, lo8);
     };
-    if (whole) {
+    if (plain) {
 #pragma unroll 1
         for (int g = 0; g < kGroups; g += 2) {
             step(g, v[0], v[1], true);
@@ -460,9 +477,9 @@ __device__ __forceinline__ float weights2(uint32_t at, const TileMeta& meta, flo
     return l;
 }
 
-// The same in one pass with the largest x, for a tile that the row sees whole, P left in registers (one
+// The same in one pass with the largest x - base, for a tile that the row sees whole, P left in registers (one
 // term): S stays as it is until the caller knows that the reference held.
-__device__ __forceinline__ float weights_and_max(uint32_t at, const TileMeta& meta, float crow, float ref,
+__device__ __forceinline__ float weights_and_max(uint32_t at, const TileMeta& meta, float crow, float base,
                                                  uint32_t (&pk)[2][32], float* top_out) {
     float l = 0.0f, top[2] = {-INFINITY, -INFINITY};
     uint32_t v[2][16];
@@ -471,7 +488,7 @@ __device__ __forceinline__ float weights_and_max(uint32_t at, const TileMeta& me
     for (int g = 0; g < kGroups; ++g) {
         tmem_wait_ld();
         if (g + 1 < kGroups) tmem_ld16(at + 16 * (g + 1), v[(g + 1) & 1]);
-        const float c = crow * meta.ks[g], e = meta.ev[g] - (ref - 7.0f);
+        const float c = crow * meta.ks[g], e = meta.ev[g] - base;
         float2 p[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
@@ -486,7 +503,7 @@ __device__ __forceinline__ float weights_and_max(uint32_t at, const TileMeta& me
         const float2 sum = add2(add2(add2(p[0], p[1]), add2(p[2], p[3])), add2(add2(p[4], p[5]), add2(p[6], p[7])));
         l = fmaf(sum.x + sum.y, meta.inv[g], l);
     }
-    *top_out = fmaxf(top[0], top[1]) + (ref - 7.0f);
+    *top_out = fmaxf(top[0], top[1]);
     return l;
 }
 
@@ -556,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, warp = tid >> 5;
     if (warp == 0) find_item(A, kRows, s_item);
     if (tid == 32) {
         for (int i = 0; i < L::kSlots; ++i) {
@@ -663,13 +680,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t b = desc_sw128_kmajor(kv_at + slot * L::kTile);
+                    // the low term first, into small sums: the tensor core's additions truncate
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
+                    for (int t = 1; t >= 0; --t) {
                         const uint64_t a = desc_sw128_kmajor(q_at + t * L::kTile);
 #pragma unroll
                         for (int k = 0; k < D / 64; ++k)
                             mma_f16_ss_elect4(tm + kColS + ((j + 1) & 1) * kToks, a + ((k * kToks * 128) >> 4),
-                                              b + ((k * kToks * 128) >> 4), 2, 2, idesc_s, t + k);
+                                              b + ((k * kToks * 128) >> 4), 2, 2, idesc_s, 1 - t + k);
                     }
                     mma_commit_elect(&s_full[(j + 1) & 1]);
                     mma_commit_elect(&empty[slot]);
@@ -683,12 +701,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 tc_fence_after();
                 const uint32_t p = tm + kColS + (j & 1) * kToks, d = tm + kColO + (j & 1) * D;
                 const uint64_t b = desc_sw128_mnmajor(kv_at + slot * L::kTile, kToks * 128);
-                // 32 tokens' P in the 32 columns of their S: 16 of the high term, 16 of the low
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)  // k steps 0, 2, 4, 6, then 1, 3, 5, 7: 32 columns apart
-                        mma_f16_ts_elect4(d, p + 8 * h + 16 * t, b + ((h * 16 * 128) >> 4), 32, (32 * 128) >> 4, idesc_o, t + h);
+                // 32 tokens' P in the 32 columns of their S: 16 of the high term, 16 of the low. The low one first; its
+                // sums lose their 2^11 with the high term's first product. k steps 0, 2, 4, 6, then 1, 3, 5, 7: 32 columns apart.
+                const uint64_t b1 = b + ((16 * 128) >> 4);
+                mma_f16_ts_elect4(d, p + 16, b, 32, (32 * 128) >> 4, idesc_o, 0);
+                mma_f16_ts_elect4(d, p + 24, b1, 32, (32 * 128) >> 4, idesc_o, 1);
+                mma_f16_ts_elect4<11>(d, p, b, 32, (32 * 128) >> 4, idesc_o, 1);
+                mma_f16_ts_elect4(d, p + 8, b1, 32, (32 * 128) >> 4, idesc_o, 1);
                 mma_commit_elect(&o_full[j & 1]);
                 mma_commit_elect(&empty[slot]);
             }
@@ -730,7 +749,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             const float use = r_new == -INFINITY ? 0.0f : r_new;
             l *= ex2(ref - use);
             ref = r_new;
-            l += weights2(tmem + lane_base + kColS + b * kToks, meta, crow, use, t0, lo, hi, whole);
+            const bool plain = all_near(use) && whole;
+            l += weights2(tmem + lane_base + kColS + b * kToks, meta, crow, weight_base(use, kTop), t0, lo, hi, plain);
             warp_arrive(&meta_empty[j % kMetaRing]);
             tmem_wait_st();
             tc_fence_before();
@@ -820,12 +840,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
 // bf16 rows: 256 query rows a CTA, two tiles of 128 that share every K and V tile, so the cache is
 // expanded to fp16 half as often, and one tile's softmax runs while the other's products do. The sums stay
 // in tensor memory over all tokens (their rounding is far below a bf16 output's), scaled again only when a row's
-// maximum has grown by more than 2^8 since its reference was taken: P then stays within fp16.
+// maximum has grown by more than 2^6 since its reference was taken: P then stays within fp16.
 //
 // Warps 0-3 and 4-7 are the softmax of a tile each (thread = row) and its store.
 constexpr int kRegsSoftmax2 = 136, kRegsLoad2 = 72, kRegsCtrl2 = 64;
 static_assert(2 * kRegsSoftmax2 + 2 * kRegsLoad2 + kRegsCtrl2 <= kRegsAll, "register split");
-constexpr float kSlack = 8.0f;  // log2 growth of a row's maximum before its sums are scaled again
+// log2 growth of a row's maximum before its sums are scaled again. What it grows by is taken from the bits of small weights;
+// the bf16 prompt below takes 579 us with 4, 537 with 5, 517 with 6, 510 with 8.
+constexpr float kSlack = 6.0f;
 
 template <int D>
 struct Layout2 {
@@ -852,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt2_kernel(const __grid_
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, warp = tid >> 5;
     if (warp == 0) find_item(A, 2 * kRows, s_item);
     if (tid == 32) {
         for (int i = 0; i < L::kSlots; ++i) {
@@ -1009,6 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt2_kernel(const __grid_
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t at = tmem + lane_base + kColS + x * kToks, o_at = tmem + lane_base + kColO + x * D;
         float ref = -INFINITY, l = 0.0f;  // the reference of P and of the sums
+        bool near = false;                // all rows of the warp have one, and near
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
             ok = wait(&meta_full[j % kMetaRing], (j / kMetaRing) & 1) && wait(&s_full[x], j & 1);
@@ -1021,11 +1044,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt2_kernel(const __grid_
             // its reference; else the maximum first, a new reference, and the sums so far (all products
             // before this S are complete) scaled to it.
             bool done = false;
-            if (whole && !__any_sync(0xffffffffu, ref == -INFINITY)) {
+            if (whole && near) {
                 uint32_t pk[2][32];
                 float top;
-                const float sum = weights_and_max(at, meta, crow, ref, pk, &top);
-                if (!__any_sync(0xffffffffu, top > ref + kSlack)) {
+                const float sum = weights_and_max(at, meta, crow, weight_base(ref, kTop - kSlack), pk, &top);
+                if (!__any_sync(0xffffffffu, top > kTop)) {
                     l += sum;
                     tmem_st32(at, pk[0]);
                     tmem_st32(at + 32, pk[1]);
@@ -1034,10 +1057,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt2_kernel(const __grid_
             }
             if (!done) {
                 const float top = row_max(at, meta, crow, t0, lo, hi, whole);
-                if (__any_sync(0xffffffffu, top > ref + kSlack)) {
+                if (__any_sync(0xffffffffu, top - ref > kSlack)) {
                     const float m_new = fmaxf(ref, top);
                     const float corr = ex2(ref - (m_new == -INFINITY ? 0.0f : m_new));
                     ref = m_new;
+                    near = all_near(ref);
                     l *= corr;
                     if (j > 0) {
 #pragma unroll 1
@@ -1051,7 +1075,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt2_kernel(const __grid_
                         }
                     }
                 }
-                l += weights(at, meta, crow, ref == -INFINITY ? 0.0f : ref, t0, lo, hi, whole);
+                l += weights(at, meta, crow, weight_base(ref == -INFINITY ? 0.0f : ref, kTop - kSlack), t0, lo, hi);
             }
             warp_arrive(&meta_empty[j % kMetaRing]);
             tmem_wait_st();

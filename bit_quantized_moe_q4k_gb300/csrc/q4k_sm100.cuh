@@ -207,6 +207,8 @@ __device__ __forceinline__ void mma_f16_ss_elect4(uint32_t d_tmem, uint64_t a_de
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_step), "r"(b_step), "r"(first_accumulates)
         : "memory");
 }
+// DOWN: what D holds is taken times 2^-DOWN by the first.
+template <int DOWN = 0>
 __device__ __forceinline__ void mma_f16_ts_elect4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t a_step,
                                                   uint32_t b_step, uint32_t idesc, uint32_t first_accumulates) {
     asm volatile(
@@ -214,14 +216,14 @@ __device__ __forceinline__ void mma_f16_ts_elect4(uint32_t d_tmem, uint32_t a_tm
         "elect.sync _|e, 0xffffffff;\n\t"
         "setp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
         "cvt.u64.u32 sb, %5;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p, %7;\n\t"
         "add.u32 a, %1, %4;\n\tadd.u64 b, %2, sb;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
         "add.u32 a, a, %4;\n\tadd.u64 b, b, sb;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
         "add.u32 a, a, %4;\n\tadd.u64 b, b, sb;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(a_step), "r"(b_step), "r"(first_accumulates)
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(a_step), "r"(b_step), "r"(first_accumulates), "n"(DOWN)
         : "memory");
 }
 // A from tensor memory: the same issued by one lane that elect.sync picks among the warp's 32 lanes: the whole warp

@@ -469,7 +469,12 @@ int q4k_kv_append(const void* d_k, const void* d_v, int dtype, int m, int kv_hea
  *   d_q [m, q_heads*head_dim], d_out the same type; d_out must not overlap d_q.
  *   max_q_len, max_len: upper bounds on a sequence's new and cached tokens that choose the
  *     kernels and their grids; results do not depend on their being tight or right.
- *   fp32 queries keep 22 bits of q and of the softmax weights; bf16 ones are exact.
+ *   Scores, maxima, denominators and sums are fp32. The matrix products take fp16: a query element is off by
+ *     2^-32 of its row's largest, and an fp32 one by 2^-22 of itself. A softmax weight p_j enters the product with
+ *     V times its page's V scale, relative to the row's largest such product W: for bf16 queries it is off by 2^-11
+ *     of itself or, where that is more, by 2^-40 W (2^-34 W in prompts); for fp32 ones by 2^-22 of itself or 2^-51 W.
+ *     The denominator has the weights in fp32. So where one token of small values has almost all the weight, a
+ *     bf16 result keeps 11 bits of the others' weights down to 2^-29 (2^-23 in prompts) of its own.
  * kv_heads divides q_heads. Workspace: q4k_paged_attention_workspace_size bytes, any contents. */
 size_t q4k_paged_attention_workspace_size(int batch, int m, int q_heads, int kv_heads, int head_dim);
 int q4k_paged_attention(const void* d_q, int dtype, int m, int q_heads, int kv_heads, int head_dim, int64_t q_stride,

@@ -907,3 +907,56 @@ def test_attention_prompt_wait_limit_runs_out(d, dtype, monkeypatch):
         monkeypatch.delenv("Q4K_WAIT_NS")
         out, status = call()
         assert status == 0 and torch.equal(out, good)
+
+
+# ---- a dominant token whose value is zero ---------------------------------------------------------
+# The weights p_j enter the product with V as P_j = 2^B p_j s_j / W, s_j the V scale of j's page, W the largest p_j s_j. An
+# fp16 term is off by 2^-11 P_j, or 2^-25 below fp16's normal numbers; the second term of fp32 rows is held times 2^11, so
+# both together are off by 2^-22 P_j or 2^-36. B is 15; 9 in the prompt kernel for bf16. So sum_j |dp_j| |v_j| is at most
+# 2^-22 or 2^-11 of sum_j p_j |v_j|, plus 2^-36 or 2^-25 times 2^-B W sum_j |code_j|.
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,length,hq,hk,d", [(1, 300, 8, 2, 128), (2, 9000, 4, 1, 64), (60, 400, 64, 8, 128), (65, 333, 64, 8, 64)])
+@pytest.mark.parametrize("nats", [12.0, 16.0, 20.0])
+@pytest.mark.parametrize("up", [0, 6])
+def test_attention_dominant_token_without_value(up, nats, n, length, hq, hk, d, dtype):
+    """A sink: the first token's score is `nats` above the others' and its values are zero, so the result is made of weights
+    of e^-nats; its page's V scale is 2^up times the others'."""
+    g = np.random.default_rng(int(nats) + length)
+    page, scale = 16, 1 / math.sqrt(d)
+    c = Cache(length + d, -(-length // page), hk, page, d)
+    c.scale["k"][:], c.scale["v"][:] = 2.0 ** -7, 2.0 ** -6
+    table = c.order[None, :].copy()
+    u = g.choice([-1.0, 1.0], (hk, d))
+    c.codes["k"][table[0, 0], :, 0] = e4m3_round(u * 128)  # K of the first token: u
+    c.codes["v"][table[0, 0], :, 0] = 0
+    c.scale["v"][table[0, 0]] *= 2.0 ** up
+    c.upload()
+    q = np.repeat(u, hq // hk, 0) * nats / math.sqrt(d) + 0.5 * g.standard_normal((n, hq, d))
+    q = rows(q.reshape(n, hq * d), dtype)
+    out, flag = torch.empty_like(q), err_flag()
+    nbytes = q4k.q4k_paged_attention_workspace_size(1, n, hq, hk, d)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    q4k.q4k_paged_attention(q, n, hq, hk, d, hq * d, c.dev["k"], c.dev["v"], c.dev_scale["k"], c.dev_scale["v"],
+                            dev(np.array([0, n], np.int32)), dev(np.array([length], np.int32)), dev(table), 1, table.shape[1],
+                            page, c.pages, n, length, scale, 0, out, hq * d, ws, nbytes, flag)
+    assert int(host(flag)[0]) == 0
+    qs = f64(q).reshape(n, hq, d)
+    ref, tol = attention_ref(qs, c, table, [n], [length], hq // hk, scale, 0, dtype)
+    k, codes = c.values("k", table[0], length), np.abs(E4M3[c.codes["v"][table[0]]]).transpose(1, 0, 2, 3).reshape(hk, -1, d)
+    s_v = np.repeat(c.scale["v"][table[0]].T.astype(np.float64), page, 1)  # [hk, tokens]
+    bits = 36 + 15 if dtype == "f32" else 25 + (9 if n > 8 else 15)
+    least = 1.0
+    for r in range(n):
+        seen = length - n + r + 1
+        for h in range(hq):
+            x = k[h // (hq // hk), :seen] @ qs[r, h] * scale
+            p = np.exp(x - x.max())
+            p /= p.sum()
+            least = min(least, p[0])
+            floor = 2.0 ** -bits * (p * s_v[h // (hq // hk), :seen]).max() * codes[h // (hq // hk), :seen].sum(0)
+            weight = 2.0 ** -22 * (p @ (codes[h // (hq // hk), :seen] * s_v[h // (hq // hk), :seen, None])) if dtype == "f32" else 0.0
+            tol[r, h] += floor + weight
+    assert least > 0.5  # the sink dominates every row
+    worst = np.max(np.abs(f64(out).reshape(n, hq, d) - ref) / np.maximum(tol, 1e-300))
+    assert worst <= 1, f"{worst} of the bound"
