@@ -909,6 +909,31 @@ def test_attention_prompt_wait_limit_runs_out(d, dtype, monkeypatch):
         assert status == 0 and torch.equal(out, good)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("gain", [1e5, 1e7, 1e9, 1e20])
+def test_attention_prompt_query_magnitudes(gain, d, dtype):
+    """Scores so large that the softmax is a choice of one token: its values, no NaN."""
+    new, lens, hq, hk, page = [60], [200], 64, 8, 16
+    c = Cache(77, 14, hk, page, d)
+    table = tables(c, lens)
+    got = run_attention(77, new, lens, hq, hk, d, page, dtype, q_gain=gain, check=False, cache=c, table=table)
+    q = f64(rows(np.random.default_rng(77).standard_normal((60, hq * d)) * gain, dtype)).reshape(60, hq, d)
+    k, v = (c.values(s, table[0, :13], 200) for s in "kv")
+    apart = 0
+    for r in range(60):
+        for h in range(hq):
+            s = np.sort(np.stack([k[h // 8, :141 + r] @ q[r, h], np.arange(141 + r)], 1).view("f8,f8"), axis=0, order="f0")
+            top, second = s["f0"][-1, 0], s["f0"][-2, 0]
+            off = (d / 16 + 8) * 2.0 ** -22 * (np.abs(k[h // 8, :141 + r]) @ np.abs(q[r, h])).max()
+            if (top - second - 2 * off) / math.sqrt(d) < 40:  # e^-40 of the others' values is below a rounding
+                continue
+            apart += 1
+            want = v[h // 8, int(s["f1"][-1, 0])]
+            assert (np.abs(got[r, h] - want) <= (STEP[dtype] + 2.0 ** -11) * np.abs(want) + 2.0 ** -40).all()
+    assert apart > 1000 and np.isfinite(got).all()
+
+
 # ---- a dominant token whose value is zero ---------------------------------------------------------
 # The weights p_j enter the product with V as P_j = 2^B p_j s_j / W, s_j the V scale of j's page, W the largest p_j s_j. An
 # fp16 term is off by 2^-11 P_j, or 2^-25 below fp16's normal numbers; the second term of fp32 rows is held times 2^11, so
