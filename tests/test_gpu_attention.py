@@ -985,3 +985,17 @@ def test_attention_dominant_token_without_value(up, nats, n, length, hq, hk, d, 
     assert least > 0.5  # the sink dominates every row
     worst = np.max(np.abs(f64(out).reshape(n, hq, d) - ref) / np.maximum(tol, 1e-300))
     assert worst <= 1, f"{worst} of the bound"
+
+
+# ---- append: several heads a CTA -----------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new,ctx,heads,d,page,kw", [
+    ([4003], [37], 8, 128, 16, {}), ([1800, 3], [5, 0], 5, 64, 16, dict(mode="pairs")), ([2500, 0, 1400], [9, 3, 31], 8, 64, 32, {}),
+    ([8191], [37], 8, 128, 64, {}), ([8000], [63], 5, 128, 64, dict(rot=64)), ([14001], [100], 3, 128, 128, dict(gain=30.0, norm=False)),
+    ([2600], [11], 8, 64, 16, dict(rot=0, norm=False)),
+])
+def test_append_prompts_of_several_heads(new, ctx, heads, d, page, kw, dtype):
+    """Prompts of so many pages that a CTA takes a page's heads one after the other, all of them or a share that may be the
+    smaller one, behind a prefix that ends inside a page, whose codes are rounded again for every head."""
+    run_append(sum(new) + heads, new, ctx, heads, d, page, dtype, **kw)
