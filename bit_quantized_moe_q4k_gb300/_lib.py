@@ -166,11 +166,13 @@ def _dev(t, kinds) -> int | None:
 
 
 def _row_type(kinds, a, b) -> int:
-    """The library's element type of one or two row tensors."""
-    t = a if b is None else b
-    if t is None or t.dtype not in kinds.rows or (a is not None and a.dtype is not t.dtype):
+    """The library's element type of one or two row tensors; a raw address has the type of the other one."""
+    types = {t.dtype for t in (a, b) if t is not None and t.__class__ is not int}
+    if not types:
+        raise ValueError("the rows' element type is a tensor's: one tensor expected besides raw addresses")
+    if len(types) > 1 or not types <= kinds.rows.keys():
         raise ValueError("float32 or bfloat16 tensors of one type expected")
-    return kinds.rows[t.dtype]
+    return kinds.rows[types.pop()]
 
 
 # ---- sizes -------------------------------------------------------------------------------------

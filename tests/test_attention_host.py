@@ -150,3 +150,33 @@ def test_host_tensors_are_refused():
     x = torch.zeros(8)
     with pytest.raises(ValueError):
         q4k.q4k_qk_norm_rope(x, None, 1, 1, 0, 64, 64, 64, None, None, 1e-6, None, None, 0, 0, x, None, 64, 64, stream=0)
+
+
+def test_bindings_take_raw_addresses_for_rows():
+    """Addresses pass where tensors do; the rows' element type is the other tensor's, and one tensor is asked for."""
+    f32, bf, i32, f64, u8 = (FakeCuda(t) for t in (torch.float32, torch.bfloat16, torch.int32, torch.float64, torch.uint8))
+
+    def nr(q, k, qo, ko):
+        q4k.q4k_qk_norm_rope(q, k, 0, 8, 2, 128, 1024, 256, bf, bf, 1e-6, i32, f64, 128, 0, qo, ko, 1024, 256, stream=0)
+
+    def ap(k, v):
+        q4k.q4k_kv_append(k, v, 0, 2, 128, 256, 256, bf, 1e-6, f64, 128, 0, i32, i32, i32, 1, 4, 16, 8, u8, u8, f32, f32, stream=0)
+
+    def at(q, out):
+        q4k.q4k_paged_attention(q, 0, 8, 2, 128, 1024, A16, u8, f32, f32, i32, i32, A16, 1, 4, 16, 8, 1, 64, 0.1, 0, out, 1024,
+                                A16, 0, stream=0)
+
+    nr(A16, f32, f32, A16)
+    nr(bf, A16, A16, f32)
+    nr(f32, None, None, f32)
+    ap(A16, bf)
+    ap(f32, A16)
+    at(A16, bf)
+    at(f32, A16)
+    for call in (lambda: nr(A16, A16, f32, f32), lambda: nr(f32, f32, A16, None), lambda: ap(A16, A16), lambda: at(A16, A16),
+                 lambda: at(None, A16)):
+        with pytest.raises(ValueError, match="element type"):
+            call()
+    for call in (lambda: at(f32, bf), lambda: ap(bf, f32), lambda: ap(A16, i32)):
+        with pytest.raises(ValueError):
+            call()
