@@ -180,3 +180,19 @@ def test_bindings_take_raw_addresses_for_rows():
     for call in (lambda: at(f32, bf), lambda: ap(bf, f32), lambda: ap(A16, i32)):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("raw", [True, False])
+def test_the_current_stream_with_and_without_torchs_raw_getter(raw, monkeypatch):
+    """The raw getter is not part of torch's public interface: without it the public one is asked."""
+    from types import SimpleNamespace
+
+    from bit_quantized_moe_q4k_gb300 import _lib
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: SimpleNamespace(cuda_stream=77))
+    if raw:
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 78 + device, raising=False)
+    else:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    assert _lib._stream(None) == (78 if raw else 77)
+    assert _lib._stream(5) == 5 and _lib._stream(SimpleNamespace(cuda_stream=6)) == 6
