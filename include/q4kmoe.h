@@ -406,7 +406,9 @@ int q4k_rms_norm(const float* d_x, const uint16_t* d_w, int m, int hidden, float
  * The paged cache (caller-owned device memory):
  *   k_cache, v_cache: e4m3 codes [num_pages][kv_heads][page_size][head_dim], 16-byte aligned
  *   k_scale, v_scale: fp32 [num_pages][kv_heads]; value = code * scale. q4k_kv_append writes
- *     powers of two; q4k_paged_attention takes any positive normal scale up to 2^120.
+ *     powers of two from 2^-64 to 2^120. q4k_paged_attention takes any positive normal K scale up to
+ *     2^120, and V scales from 2^-80 to 2^120 that lie within a factor of 2^96 of one another in
+ *     a sequence (they are exponents of the softmax weights, whose denominator is one fp32).
  *   page_size 16, 32, 64 or 128; head_dim 64 or 128.
  * A batch of sequences (device memory, read on the device only):
  *   q_start   [batch + 1]: sequence i's new tokens are rows q_start[i] .. q_start[i+1] - 1 of the
@@ -422,7 +424,8 @@ int q4k_rms_norm(const float* d_x, const uint16_t* d_w, int m, int hidden, float
  * access leaves its buffer. Two sequences may share pages they only read; a page that receives
  * tokens belongs to one sequence.
  * Launches are programmatic dependents that wait for the previous kernel before reading.
- * Limits: max_pages*page_size <= 2^30, kv_heads <= 65535.
+ * Limits (Q4K_ERR_LIMIT): max_pages*page_size <= 2^30, q_heads and kv_heads <= 65535; where
+ * there is a cache, m and batch <= 2^24, and m*q_heads/kv_heads <= 2^30.
  */
 #define Q4K_F32 0
 #define Q4K_BF16 1

@@ -999,3 +999,15 @@ def test_append_prompts_of_several_heads(new, ctx, heads, d, page, kw, dtype):
     """Prompts of so many pages that a CTA takes a page's heads one after the other, all of them or a share that may be the
     smaller one, behind a prefix that ends inside a page, whose codes are rounded again for every head."""
     run_append(sum(new) + heads, new, ctx, heads, d, page, dtype, **kw)
+
+
+# ---- V scales at the ends of their range ----------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new,lens,hq,hk,d", [([1, 2], [130, 90], 8, 2, 128), ([1], [5000], 8, 1, 64), ([60], [200], 64, 8, 128), ([60], [200], 64, 8, 64)])
+@pytest.mark.parametrize("exps", [[-80], [-80, 16], [16, -80, -30]])
+def test_attention_value_scales_at_the_ends(exps, new, lens, hq, hk, d, dtype):
+    """(attention_ref's bound for x allows two roundings of values below 128 in log2 units.)"""
+    def ends(c):
+        c.scale["v"][:] = (2.0 ** np.resize(np.array(exps, float), c.scale["v"].size)).reshape(c.scale["v"].shape)
+    run_attention(60 + len(exps), new, lens, hq, hk, d, 16, dtype, codes_after=ends)
