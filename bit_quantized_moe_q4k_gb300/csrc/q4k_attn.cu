@@ -26,8 +26,8 @@
 // memory: an eighth of the pieces, and reads of a few hundred cycles instead of the thousand and more through L2.
 //
 // 64 ragged sequences of up to 8192 tokens, 8 kv heads of 128, 514 MB: 96 us, 5.3 TB/s. One of 131071, 4 kv heads,
-// 134 MB: 39 us; beyond about 20 us of latency (launch, lengths, pages, queries, first copies, two joins) it streams
-// at 6.7 TB/s. One of 509: 8.5 us, that latency without the join through L2.
+// 134 MB: 39 us, 20 of them bytes at the copy rate. One of 509: 8.4 us, the chain of launch, lengths, pages, queries, first copies and
+// the joins of warps and cluster; what the long one takes beyond both is not broken down.
 #include <atomic>
 #include <chrono>
 

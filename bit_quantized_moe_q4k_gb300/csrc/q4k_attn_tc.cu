@@ -17,9 +17,12 @@
 // loops are kept short: the roles share a scheduler and its instruction cache, and unrolled further they waited for
 // instructions (the bf16 prompt below took 1863 us with the first, fully unrolled ones).
 //
-// Bound by the issue of instructions and the latency between S and P: a 128 x 128 x 128 product takes 512 cycles of the
-// tensor core, two a tile of fp32 rows' one. bf16, 8192 tokens, 32 / 8 heads, head_dim 128: 517 us, 1064
-// TFLOP/s of the pairs that are seen (55% of the card's measured dense rate).
+// Bound by the chain S, largest value, exponentials, P, product, which is serial within a row tile and which the two row
+// tiles of a CTA do not cover: the tensor pipe is active 45% of the time and issue 49%. A 128 x 128 x 128 product
+// takes 512 cycles of the tensor core, four a tile of fp32 rows. 8192 tokens, 32 / 8 heads, head_dim 128: bf16 518 us,
+// 1061 TFLOP/s of the pairs that are seen (55% of the card's measured dense rate); fp32 1039 us, 529 TFLOP/s, with twice
+// the products. Items are not cut along the tokens, so few of them leave SMs idle: 256 new tokens behind 131000 are 32 items
+// (bf16) and take 1.9 ms.
 #include <atomic>
 
 #include "q4k_paged.cuh"
@@ -197,7 +200,7 @@ __device__ __forceinline__ void find_item(const PromptParams& A, int tile_rows, 
 
 // A wait of a whole warp, bounded in time: its lanes go on, or give up, together. The clock is looked at every 64 tries.
 // A try suspends the thread, maybe for longer than a limit below a millisecond, so with SHORT such a limit is polled
-// for; the page warp does, whose abort ends the others' waits (in all roles it took 515 us for the prompt below, not 508).
+// for; the page warp does, whose abort ends the others' waits (in all roles it took the bf16 prompt above 7 us more).
 template <bool SHORT = false>
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
     const bool poll = SHORT && limit_ns < 1000000;
@@ -839,14 +842,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
 
 // bf16 rows: 256 query rows a CTA, two tiles of 128 that share every K and V tile, so the cache is
 // expanded to fp16 half as often, and one tile's softmax runs while the other's products do. The sums stay
-// in tensor memory over all tokens (their rounding is far below a bf16 output's), scaled again only when a row's
+// in tensor memory over all tokens (the tensor core adds each 16 tokens' product truncated, 2^-23 of the sum at most: 2^-10
+// of it over 131072 tokens, a quarter of a bf16 step), scaled again only when a row's
 // maximum has grown by more than 2^6 since its reference was taken: P then stays within fp16.
 //
 // Warps 0-3 and 4-7 are the softmax of a tile each (thread = row) and its store.
 constexpr int kRegsSoftmax2 = 136, kRegsLoad2 = 72, kRegsCtrl2 = 64;
 static_assert(2 * kRegsSoftmax2 + 2 * kRegsLoad2 + kRegsCtrl2 <= kRegsAll, "register split");
 // log2 growth of a row's maximum before its sums are scaled again. What it grows by is taken from the bits of small weights;
-// the bf16 prompt below takes 579 us with 4, 537 with 5, 517 with 6, 510 with 8.
+// the bf16 prompt above takes 579 us with 4, 537 with 5, 517 with 6, 510 with 8.
 constexpr float kSlack = 6.0f;
 
 template <int D>

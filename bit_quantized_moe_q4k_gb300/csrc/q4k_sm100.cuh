@@ -226,7 +226,7 @@ __device__ __forceinline__ void mma_f16_ts_elect4(uint32_t d_tmem, uint32_t a_tm
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(a_step), "r"(b_step), "r"(first_accumulates), "n"(DOWN)
         : "memory");
 }
-// A from tensor memory: the same issued by one lane that elect.sync picks among the warp's 32 lanes: the whole warp
+// mma_f16_ts issued by one lane that elect.sync picks among the warp's 32 lanes: the whole warp
 // runs the issuing loop, so its operands stay warp-uniform (no per-instruction transfer of a
 // lone thread's registers), and each instruction is issued once.
 __device__ __forceinline__ void mma_f16_ts_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
