@@ -21,6 +21,7 @@ STATUS_NAMES = {
     0: "Q4K_OK", 1: "Q4K_ERR_NULL", 2: "Q4K_ERR_SHAPE", 3: "Q4K_ERR_TOPK", 4: "Q4K_ERR_WORKSPACE",
     5: "Q4K_ERR_CUDA", 6: "Q4K_ERR_EXPERT_ID", 7: "Q4K_ERR_ALIGN", 8: "Q4K_ERR_MODE", 9: "Q4K_ERR_LIMIT",
     10: "Q4K_ERR_TIMEOUT", 11: "Q4K_ERR_PAGE", 12: "Q4K_ERR_SEQ", 13: "Q4K_ERR_DTYPE",
+    14: "Q4K_ERR_TOKEN",
 }
 SHARED_NONE, SHARED_SIGMOID, SHARED_UNSCALED = 0, 1, 2
 PATH_TWO_LAUNCH, PATH_PERSISTENT, PATH_PERSISTENT_WIDE = 0, 1, 2
@@ -67,6 +68,9 @@ SIGNATURES = {
     "q4k_paged_attention_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "q4k_paged_attention": (_I, [_P, _I, _I, _I, _I, _I, _I64, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I,
                                  ctypes.c_float, _I, _P, _I64, _P, _SZ, _P, _P]),
+    "q4k_page_tables": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "q4k_verify_drafts_workspace_size": (_SZ, [_I, _I, _I]),
+    "q4k_verify_drafts": (_I, [_P, _I, _I, _I, _I64, _P, _I64, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P]),
     "q4k_quantize_rows": (_I, [_P, _I64, _I, _P, _P]),
     "q4k_stream_ceiling_sink_words": (_I, []),
     "q4k_stream_ceiling": (_I, [_P, _U64, _P, _P]),
@@ -141,6 +145,7 @@ class _Kinds:
         self.bf16 = frozenset((torch.bfloat16, torch.uint16, torch.int16))
         self.e4m3 = frozenset((torch.float8_e4m3fn, torch.uint8, torch.int8))
         self.i32, self.f32, self.f64 = (frozenset((t,)) for t in (torch.int32, torch.float32, torch.float64))
+        self.i64 = frozenset((torch.int64,))
         self.u8 = frozenset((torch.uint8,))
 
 
@@ -375,6 +380,34 @@ def q4k_paged_attention(q, m, q_heads, kv_heads, head_dim, q_stride, k_cache, v_
         _dev(v_cache, K.e4m3), _dev(k_scale, K.f32), _dev(v_scale, K.f32), _dev(q_start, K.i32), _dev(seq_lens, K.i32),
         _dev(page_table, K.i32), batch, max_pages, page_size, num_pages, max_q_len, max_len, scale, window,
         _dev(out, K.rows), out_stride, _dev(workspace, K.u8), ws_bytes, _dev(err_flag, K.i32), _stream(stream)))
+
+
+def q4k_page_tables(kept, new, fixed, batch, m, max_pages, page_size, num_pages, held, free_pages, free_count, page_table,
+                    held_out, free_count_out, q_start, seq_lens, pos, slots, err_flag=None, stream=None):
+    """A step's page table, starts, lengths, positions and slots (int64) on the device from the tokens each sequence keeps
+    and brings; fixed, pos and slots may be None; held, free_count and kept may take held_out, free_count_out and seq_lens."""
+    K = _kinds()
+    _check((_lib or load()).q4k_page_tables(
+        _dev(kept, K.i32), _dev(new, K.i32), _dev(fixed, K.i32), batch, m, max_pages, page_size, num_pages, _dev(held, K.i32),
+        _dev(free_pages, K.i32), _dev(free_count, K.i32), _dev(page_table, K.i32), _dev(held_out, K.i32),
+        _dev(free_count_out, K.i32), _dev(q_start, K.i32), _dev(seq_lens, K.i32), _dev(pos, K.i32), _dev(slots, K.i64),
+        _dev(err_flag, K.i32), _stream(stream)))
+
+
+def q4k_verify_drafts_workspace_size(batch, m, vocab) -> int:
+    return int(load().q4k_verify_drafts_workspace_size(batch, m, vocab))
+
+
+def q4k_verify_drafts(logits, m, vocab, logits_stride, draft_probs, draft_stride, tokens, q_start, batch, temperature, u_accept,
+                      u_sample, seq_lens, accepted, next_token, kept, workspace, ws_bytes, err_flag=None, stream=None):
+    """Accepted drafts, the token after them and the cached tokens that remain, from given random numbers (draft_probs
+    None: drafts without probabilities; temperature None: 1; seq_lens and kept may be None)."""
+    K = _kinds()
+    _check((_lib or load()).q4k_verify_drafts(
+        _dev(logits, K.rows), _row_type(K, logits, None), m, vocab, logits_stride, _dev(draft_probs, K.f32), draft_stride,
+        _dev(tokens, K.i32), _dev(q_start, K.i32), batch, _dev(temperature, K.f32), _dev(u_accept, K.f32), _dev(u_sample, K.f32),
+        _dev(seq_lens, K.i32), _dev(accepted, K.i32), _dev(next_token, K.i32), _dev(kept, K.i32), _dev(workspace, K.u8), ws_bytes,
+        _dev(err_flag, K.i32), _stream(stream)))
 
 
 def q4k_quantize_rows(x, rows, k, out, stream=None):

@@ -375,6 +375,10 @@ int check_norm_weight(const uint16_t* w) {
     return Q4K_OK;
 }
 
+int page_shift_of(int page_size) {  // -1: not a page size
+    return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : page_size == 128 ? 7 : -1;
+}
+
 // The sizes and pointers of a paged cache and the batch that reads or fills it.
 int check_paged(int m, int batch, int kv_heads, int head_dim, int max_pages, int page_size, int num_pages,
                 const void* q_start, const void* seq_lens, const void* table, const void* k_cache, const void* v_cache,
@@ -383,7 +387,7 @@ int check_paged(int m, int batch, int kv_heads, int head_dim, int max_pages, int
     if (head_dim != 64 && head_dim != 128) return fail(Q4K_ERR_SHAPE, "head_dim must be 64 or 128 (got %d)", head_dim);
     if (kv_heads < 1) return fail(Q4K_ERR_SHAPE, "kv_heads must be >= 1 (got %d)", kv_heads);
     if (kv_heads > 65535) return fail(Q4K_ERR_LIMIT, "kv_heads must be <= 65535 (got %d)", kv_heads);
-    if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
+    if (page_shift_of(page_size) < 0)
         return fail(Q4K_ERR_SHAPE, "page_size must be 16, 32, 64 or 128 (got %d)", page_size);
     if (num_pages < 1 || max_pages < 1) return fail(Q4K_ERR_SHAPE, "num_pages and max_pages must be >= 1 (got %d, %d)", num_pages, max_pages);
     if ((int64_t)max_pages * page_size > (int64_t)1 << 30) return fail(Q4K_ERR_LIMIT, "max_pages*page_size must be <= 2^30");
@@ -398,7 +402,7 @@ int check_paged(int m, int batch, int kv_heads, int head_dim, int max_pages, int
     B->seq_lens = static_cast<const int32_t*>(seq_lens);
     B->table = static_cast<const int32_t*>(table);
     B->batch = batch; B->m = m; B->max_pages = max_pages; B->num_pages = num_pages;
-    B->page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+    B->page_shift = page_shift_of(page_size);
     return Q4K_OK;
 }
 
@@ -893,6 +897,67 @@ int q4k_paged_attention(const void* d_q, int dtype, int m, int q_heads, int kv_h
                                         d_k_scale, d_v_scale, max_q_len, max_len, scale, window, d_out, out_stride, d_workspace,
                                         d_err_flag, stream),
                        "attention launch");
+}
+
+int q4k_page_tables(const int32_t* d_kept, const int32_t* d_new, const int32_t* d_fixed, int batch, int m, int max_pages,
+                    int page_size, int num_pages, const int32_t* d_held, int32_t* d_free_pages,
+                    const int32_t* d_free_count, int32_t* d_page_table, int32_t* d_held_out, int32_t* d_free_count_out,
+                    int32_t* d_q_start, int32_t* d_seq_lens, int32_t* d_pos, int64_t* d_slots, int* d_err_flag,
+                    cudaStream_t stream) {
+    if (m < 0 || batch < 0) return fail(Q4K_ERR_SHAPE, "m and batch must be >= 0 (got %d, %d)", m, batch);
+    if (page_shift_of(page_size) < 0) return fail(Q4K_ERR_SHAPE, "page_size must be 16, 32, 64 or 128 (got %d)", page_size);
+    if (num_pages < 1 || max_pages < 1) return fail(Q4K_ERR_SHAPE, "num_pages and max_pages must be >= 1 (got %d, %d)", num_pages, max_pages);
+    if ((int64_t)max_pages * page_size > (int64_t)1 << 30) return fail(Q4K_ERR_LIMIT, "max_pages*page_size must be <= 2^30");
+    if (m > 1 << 24) return fail(Q4K_ERR_LIMIT, "m must be <= 2^24 (got %d)", m);
+    if (batch > kTablesMaxBatch) return fail(Q4K_ERR_LIMIT, "batch must be <= %d (got %d)", kTablesMaxBatch, batch);
+    if (!d_free_pages || !d_free_count || !d_free_count_out || !d_q_start)
+        return fail(Q4K_ERR_NULL, "free_pages, free_count, free_count_out and q_start are required");
+    if (batch > 0 && (!d_kept || !d_new || !d_held || !d_page_table || !d_held_out || !d_seq_lens))
+        return fail(Q4K_ERR_NULL, "kept, new, held, page_table, held_out and seq_lens are required");
+    for (const void* p : {(const void*)d_kept, (const void*)d_new, (const void*)d_fixed, (const void*)d_held, (const void*)d_free_pages,
+                          (const void*)d_free_count, (const void*)d_page_table, (const void*)d_held_out, (const void*)d_free_count_out,
+                          (const void*)d_q_start, (const void*)d_seq_lens, (const void*)d_pos})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return fail(Q4K_ERR_ALIGN, "int32 arrays must be 4-byte aligned");
+    if (reinterpret_cast<uintptr_t>(d_slots) & 7u) return fail(Q4K_ERR_ALIGN, "slots must be 8-byte aligned");
+    return cuda_status(launch_page_tables(d_kept, d_new, d_fixed, batch, m, max_pages, page_shift_of(page_size), num_pages,
+                                          d_held, d_free_pages, d_free_count, d_page_table, d_held_out, d_free_count_out,
+                                          d_q_start, d_seq_lens, d_pos, d_slots, d_err_flag, stream),
+                       "page tables launch");
+}
+
+size_t q4k_verify_drafts_workspace_size(int batch, int m, int vocab) {
+    if (batch < 0 || m < 0 || vocab < 1 || m > 1 << 24 || vocab > kVerifyMaxVocab) return 0;
+    return align_up(verify_workspace_bytes(m, vocab));
+}
+
+int q4k_verify_drafts(const void* d_logits, int dtype, int m, int vocab, int64_t logits_stride, const float* d_draft_probs,
+                      int64_t draft_stride, const int32_t* d_tokens, const int32_t* d_q_start, int batch,
+                      const float* d_temperature, const float* d_u_accept, const float* d_u_sample,
+                      const int32_t* d_seq_lens, int32_t* d_accepted, int32_t* d_next, int32_t* d_kept, void* d_workspace,
+                      size_t ws_bytes, int* d_err_flag, cudaStream_t stream) {
+    int st = check_dtype(dtype);
+    if (st) return st;
+    if (m < 0 || batch < 0) return fail(Q4K_ERR_SHAPE, "m and batch must be >= 0 (got %d, %d)", m, batch);
+    if (vocab < 1) return fail(Q4K_ERR_SHAPE, "vocab must be >= 1 (got %d)", vocab);
+    if (m > 1 << 24 || batch > 1 << 24) return fail(Q4K_ERR_LIMIT, "m and batch must be <= 2^24 (got %d, %d)", m, batch);
+    if (vocab > kVerifyMaxVocab) return fail(Q4K_ERR_LIMIT, "vocab must be <= 2^20 (got %d)", vocab);
+    if (batch == 0) return Q4K_OK;
+    if (!d_q_start || !d_u_sample || !d_accepted || !d_next) return fail(Q4K_ERR_NULL, "q_start, u_sample, accepted and next are required");
+    if (m > 0 && (!d_logits || !d_tokens || !d_u_accept)) return fail(Q4K_ERR_NULL, "logits, tokens and u_accept are required");
+    if (d_kept && !d_seq_lens) return fail(Q4K_ERR_NULL, "kept without seq_lens");
+    if (m > 0 && (logits_stride < vocab || (d_draft_probs && draft_stride < vocab)))
+        return fail(Q4K_ERR_SHAPE, "rows of %d tokens overlap at strides %lld, %lld", vocab, (long long)logits_stride, (long long)draft_stride);
+    if (reinterpret_cast<uintptr_t>(d_logits) % elem_bytes(dtype)) return fail(Q4K_ERR_ALIGN, "logits must be aligned to their elements");
+    for (const void* p : {(const void*)d_draft_probs, (const void*)d_tokens, (const void*)d_q_start, (const void*)d_temperature,
+                          (const void*)d_u_accept, (const void*)d_u_sample, (const void*)d_seq_lens, (const void*)d_accepted,
+                          (const void*)d_next, (const void*)d_kept})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return fail(Q4K_ERR_ALIGN, "arrays of int32 and fp32 must be 4-byte aligned");
+    if (m > 0) st = check_workspace(d_workspace, ws_bytes, q4k_verify_drafts_workspace_size(batch, m, vocab));
+    if (st) return st;
+    return cuda_status(launch_verify(d_logits, dtype, m, vocab, logits_stride, d_draft_probs, draft_stride, d_tokens, d_q_start,
+                                     batch, d_temperature, d_u_accept, d_u_sample, d_seq_lens, d_accepted, d_next, d_kept,
+                                     d_workspace, d_err_flag, stream),
+                       "draft verification launch");
 }
 
 int q4k_quantize_rows(const float* d_x, int64_t rows, int k, void* d_out, cudaStream_t stream) {

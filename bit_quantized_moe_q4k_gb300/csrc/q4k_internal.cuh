@@ -67,6 +67,21 @@ cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int6
                              int head_dim, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
                              const float* v_scale, int max_q_len, int max_len, float scale, int window, void* out,
                              int64_t out_stride, void* workspace, int* err_flag, cudaStream_t stream);
+// A step's page tables (q4k_tables.cu).
+constexpr int kTablesMaxBatch = 8192;  // its lengths and sums lie in shared memory
+cudaError_t launch_page_tables(const int32_t* kept, const int32_t* fresh, const int32_t* fixed, int batch, int m,
+                               int max_pages, int page_shift, int num_pages, const int32_t* held, int32_t* free_pages,
+                               const int32_t* count, int32_t* table, int32_t* held_out, int32_t* count_out,
+                               int32_t* q_start, int32_t* seq_lens, int32_t* pos, int64_t* slots, int* err_flag,
+                               cudaStream_t stream);
+// Drafted tokens against the target's distribution (q4k_verify.cu).
+constexpr int kVerifyMaxVocab = 1 << 20;  // weights keep 43 bits in sums of 64
+size_t verify_workspace_bytes(int m, int vocab);
+cudaError_t launch_verify(const void* logits, int dtype, int m, int vocab, int64_t logits_stride, const float* probs,
+                          int64_t probs_stride, const int32_t* tokens, const int32_t* q_start, int batch,
+                          const float* temperature, const float* u_accept, const float* u_sample, const int32_t* seq_lens,
+                          int32_t* accepted, int32_t* next, int32_t* kept, void* workspace, int* err_flag,
+                          cudaStream_t stream);
 cudaError_t launch_quantize(const float* x, int64_t rows, int k, uint8_t* out, cudaStream_t stream);
 cudaError_t launch_stream_ceiling(const void* src, uint64_t bytes, uint32_t* sink, cudaStream_t stream);
 // Up to 5 small copies (sizes multiples of 4 bytes) in one launch; sources may be host memory

@@ -78,7 +78,8 @@ typedef enum {
     Q4K_ERR_TIMEOUT = 10,  /* device flag value: a pipeline wait in a kernel gave up (bounded) */
     Q4K_ERR_PAGE = 11,     /* device flag value: a page id was outside [0, num_pages)          */
     Q4K_ERR_SEQ = 12,      /* device flag value: q_start or seq_lens do not fit together       */
-    Q4K_ERR_DTYPE = 13     /* dtype not Q4K_F32 or Q4K_BF16                                    */
+    Q4K_ERR_DTYPE = 13,    /* dtype not Q4K_F32 or Q4K_BF16                                    */
+    Q4K_ERR_TOKEN = 14     /* device flag value: a draft outside the vocabulary, or a row of logits without a token to choose */
 } q4k_status;
 
 #define Q4K_MAX_TOP_K 16
@@ -486,6 +487,69 @@ int q4k_paged_attention(const void* d_q, int dtype, int m, int q_heads, int kv_h
                         int max_pages, int page_size, int num_pages, int max_q_len, int max_len, float scale,
                         int window, void* d_out, int64_t out_stride, void* d_workspace, size_t ws_bytes,
                         int* d_err_flag, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * q4k_page_tables -- a serving step's batch, built on the device from its sequences' lengths: page
+ * table, starts, lengths, positions and slots as the three calls above read them (no counterpart in
+ * the studied pages; an addition of this library). Sequence i keeps kept[i] cached tokens (less than
+ * it had: drafts were rejected; 0 with new[i] = 0: it has ended) and brings new[i] more.
+ *   need_i = max(ceil((kept[i] + new[i]) / page_size) - fixed[i], 0) pages are to be its own. It holds
+ *   held[i], in entries fixed[i] .. fixed[i] + held[i] - 1 of its row of the table; the first fixed[i]
+ *   entries are another's (a shared prefix; the caller writes them) and are neither taken nor given
+ *   back. fixed[i] may change while held[i] is 0. d_fixed NULL: none.
+ *   The free pages are the first *free_count entries of free_pages, a stack. Pages beyond need_i are given back:
+ *   put on top in the order of sequences and entries. Then pages that are lacking are taken from the top, in the
+ *   same order. Table entries given back, and stack entries above the top, are left as they were.
+ * Results: page_table and free_pages in place; held_out[i] = need_i; free_count_out; q_start [batch + 1], the
+ *   exclusive sum of new; seq_lens[i] = kept[i] + new[i]; for row r of sequence i, pos[r] = kept[i] + r - q_start[i]
+ *   and slots[r] = page * page_size + pos[r] % page_size (int64), for rows from q_start[batch] to m pos 0 and slot -1.
+ *   d_pos and d_slots may be NULL. d_held_out, d_free_count_out and d_seq_lens may be d_held, d_free_count and
+ *   d_kept themselves (a captured step then goes on from its own results); else a call may be repeated with the
+ *   same result. No other buffers overlap.
+ * Device flags: a sequence that is lacking a page, and each after it that needs one, gets no new tokens and keeps what it
+ *   holds (Q4K_ERR_PAGE); tokens that exceed m rows, in the order of sequences, or a row of the table, or are negative, are
+ *   not brought (their sequence gets no new ones; Q4K_ERR_SEQ). q_start and seq_lens tell what each got. kept, held, fixed and
+ *   free_count outside what fits are clamped (Q4K_ERR_SEQ, Q4K_ERR_PAGE); a page id outside [0, num_pages) that is taken, or in
+ *   whose page a new token lies, raises Q4K_ERR_PAGE. No access leaves its buffer: page_table [batch][max_pages], free_pages
+ *   [num_pages].
+ * batch 0 or m 0 are calls like others. Limits (Q4K_ERR_LIMIT): batch <= 8192, m <= 2^24,
+ * max_pages*page_size <= 2^30. One launch. */
+int q4k_page_tables(const int32_t* d_kept, const int32_t* d_new, const int32_t* d_fixed, int batch, int m, int max_pages,
+                    int page_size, int num_pages, const int32_t* d_held, int32_t* d_free_pages,
+                    const int32_t* d_free_count, int32_t* d_page_table, int32_t* d_held_out, int32_t* d_free_count_out,
+                    int32_t* d_q_start, int32_t* d_seq_lens, int32_t* d_pos, int64_t* d_slots, int* d_err_flag,
+                    cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * q4k_verify_drafts -- drafted tokens against the target's distribution, from given random numbers
+ * (no counterpart in the studied pages; an addition of this library).
+ *   Sequence i's rows are q_start[i] .. q_start[i+1] - 1, as of q4k_paged_attention: tokens[r] is the row's token, the
+ *   first one a token of the sequence, the others drafts; logits[r] the target's logits after it. With
+ *   p_r = softmax(logits[r] / T), T = temperature[i], and q_r the distribution that the draft tokens[r+1] was drawn from:
+ *     the draft d = tokens[r+1] is accepted while u_accept[r] * q_r(d) < p_r(d), in order;
+ *     next[i] is drawn at the row after the last accepted one, r = q_start[i] + accepted[i]: from max(p_r - q_r, 0) if a draft
+ *     was rejected there (from p_r should nothing be left), else from p_r: the first token whose cumulative sum exceeds
+ *     u_sample[i] times the whole sum.
+ *     kept[i] = seq_lens[i] - (rows of i) + 1 + accepted[i]: the cached tokens that remain, q4k_page_tables' kept of the next step.
+ *   A sequence without rows: accepted 0, next -1, kept seq_lens[i].
+ *   d_logits: [m, vocab] in dtype, rows logits_stride apart; d_draft_probs: q_r in fp32 [m, vocab], rows draft_stride apart (each
+ *   sequence's last row is not read), NULL: drafts without probabilities, q_r(d) = 1 (rejected: from p_r without d). Any
+ *   alignment of the rows; 16-byte aligned ones are read faster. d_temperature fp32 [batch], NULL: all 1. Temperatures not above 2^-64 (0, negative, NaN) choose
+ *   the largest logit, the lowest index of equal ones (p_r is 1 there). d_seq_lens and d_kept may be NULL; d_kept may be d_seq_lens.
+ *   A logit of -inf or NaN has no probability, +inf counts as the largest finite number. Random numbers are meant from [0, 1):
+ *   outside it u_sample counts as the nearer end, u_accept as it stands, below 0 (or NaN) as 0; negative or NaN probabilities count as 0.
+ *   Decisions are those of exact arithmetic but where a random number comes next to a border: weights are good to 2^-41 of
+ *   themselves and, in the sums, rounded to 2^-(63 - ceil(log2(vocab))) of the row's largest weight.
+ * Device flags: a draft outside [0, vocab) is rejected, a row of logits without any probability gives next -1 (Q4K_ERR_TOKEN);
+ * q_start falling or outside [0, m] is clamped (Q4K_ERR_SEQ).
+ * Limits (Q4K_ERR_LIMIT): vocab <= 2^20, m and batch <= 2^24. Two launches.
+ * Workspace: q4k_verify_drafts_workspace_size bytes, any contents. */
+size_t q4k_verify_drafts_workspace_size(int batch, int m, int vocab);
+int q4k_verify_drafts(const void* d_logits, int dtype, int m, int vocab, int64_t logits_stride, const float* d_draft_probs,
+                      int64_t draft_stride, const int32_t* d_tokens, const int32_t* d_q_start, int batch,
+                      const float* d_temperature, const float* d_u_accept, const float* d_u_sample,
+                      const int32_t* d_seq_lens, int32_t* d_accepted, int32_t* d_next, int32_t* d_kept, void* d_workspace,
+                      size_t ws_bytes, int* d_err_flag, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------------
  * q4k_quantize_rows -- fp32 [rows, k] -> Q4_K bytes [rows, k/256*144] on the device

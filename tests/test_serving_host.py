@@ -1,0 +1,102 @@
+"""Host-side checks (no GPU) of the calls around the paged cache in a serving step: invalid arguments are refused
+with the documented status before anything is enqueued, and the bindings refuse tensors of other element types."""
+import pytest
+
+import bit_quantized_moe_q4k_gb300 as q4k
+
+torch = pytest.importorskip("torch")
+
+A16 = 1 << 20          # a fake 16-byte-aligned address; never dereferenced by these calls
+
+
+class FakeCuda:
+    """What a binding reads of a device tensor before it calls the library."""
+    is_cuda = True
+
+    def __init__(self, dtype):
+        self.dtype = dtype
+
+    def data_ptr(self):
+        return A16
+
+
+def tables(**kw):
+    a = dict(kept=A16, new=A16, fixed=A16, batch=3, m=7, mp=4, page=16, np=8, held=A16, free=A16, count=A16, table=A16, ho=A16, co=A16,
+             qs=A16, lens=A16, pos=A16, slots=A16)
+    a.update(kw)
+    return q4k.load().q4k_page_tables(a["kept"], a["new"], a["fixed"], a["batch"], a["m"], a["mp"], a["page"], a["np"], a["held"],
+                                      a["free"], a["count"], a["table"], a["ho"], a["co"], a["qs"], a["lens"], a["pos"], a["slots"],
+                                      None, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(batch=-1), 2), (dict(m=-1), 2), (dict(page=8), 2), (dict(page=48), 2), (dict(page=256), 2), (dict(np=0), 2), (dict(mp=0), 2),
+    (dict(mp=1 << 27), 9), (dict(m=(1 << 24) + 1), 9), (dict(batch=8193), 9),
+    (dict(kept=None), 1), (dict(new=None), 1), (dict(held=None), 1), (dict(free=None), 1), (dict(count=None), 1), (dict(table=None), 1),
+    (dict(ho=None), 1), (dict(co=None), 1), (dict(qs=None), 1), (dict(lens=None), 1), (dict(batch=0, qs=None), 1),
+    (dict(kept=A16 + 2), 7), (dict(fixed=A16 + 1), 7), (dict(table=A16 + 2), 7), (dict(pos=A16 + 2), 7), (dict(slots=A16 + 4), 7),
+])
+def test_tables_rejects(kw, status):
+    assert tables(**kw) == status
+    assert q4k.load().q4k_last_error_string()
+
+
+def test_tables_binding_refuses_other_element_types():
+    i32, i64, f32 = (FakeCuda(t) for t in (torch.int32, torch.int64, torch.float32))
+    good = [i32, i32, i32, 3, 7, 4, 16, 8, i32, i32, i32, i32, i32, i32, i32, i32, i32, i64, i32]
+    for at, x in enumerate(good):
+        if isinstance(x, int):
+            continue
+        for other in (i32, i64, f32):
+            if other.dtype == x.dtype:
+                continue
+            args = list(good)
+            args[at] = other
+            with pytest.raises(ValueError):
+                q4k.q4k_page_tables(*args, stream=0)
+
+
+def verify(**kw):
+    a = dict(x=A16, dtype=0, m=7, v=100, xs=100, q=A16, qs=100, tok=A16, st=A16, batch=3, t=A16, ua=A16, us=A16, lens=A16, acc=A16,
+             nxt=A16, kept=A16, ws=A16, wsb=None)
+    a.update(kw)
+    lib = q4k.load()
+    if a["wsb"] is None:
+        a["wsb"] = lib.q4k_verify_drafts_workspace_size(3, 7, 100)
+    return lib.q4k_verify_drafts(a["x"], a["dtype"], a["m"], a["v"], a["xs"], a["q"], a["qs"], a["tok"], a["st"], a["batch"], a["t"],
+                                 a["ua"], a["us"], a["lens"], a["acc"], a["nxt"], a["kept"], a["ws"], a["wsb"], None, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=2), 13), (dict(m=-1), 2), (dict(batch=-1), 2), (dict(v=0), 2), (dict(xs=99), 2), (dict(qs=99), 2),
+    (dict(m=(1 << 24) + 1), 9), (dict(batch=(1 << 24) + 1), 9), (dict(v=(1 << 20) + 1, xs=1 << 21, qs=1 << 21), 9),
+    (dict(x=None), 1), (dict(tok=None), 1), (dict(st=None), 1), (dict(ua=None), 1), (dict(us=None), 1), (dict(acc=None), 1),
+    (dict(nxt=None), 1), (dict(lens=None), 1), (dict(x=A16 + 2), 7), (dict(dtype=1, x=A16 + 1), 7), (dict(q=A16 + 2), 7),
+    (dict(tok=A16 + 1), 7), (dict(kept=A16 + 2), 7), (dict(ws=None), 4), (dict(wsb=16), 4), (dict(ws=A16 + 16), 4),
+])
+def test_verify_rejects(kw, status):
+    assert verify(**kw) == status
+    assert q4k.load().q4k_last_error_string()
+
+
+def test_verify_empty_and_workspace():
+    assert verify(batch=0) == 0
+    lib = q4k.load()
+    assert lib.q4k_verify_drafts_workspace_size(3, 7, 50001) % 256 == 0
+    for bad in ((-1, 1, 100), (1, -1, 100), (1, 1, 0), (1, 1, (1 << 20) + 1), (1, (1 << 24) + 1, 100)):
+        assert lib.q4k_verify_drafts_workspace_size(*bad) == 0
+
+
+def test_verify_binding_refuses_other_element_types():
+    i32, i64, f32, f16, u8 = (FakeCuda(t) for t in (torch.int32, torch.int64, torch.float32, torch.float16, torch.uint8))
+    good = [f32, 7, 100, 100, f32, 100, i32, i32, 3, f32, f32, f32, i32, i32, i32, i32, u8, 1 << 20, i32]
+    for at, x in enumerate(good):
+        if isinstance(x, int):
+            continue
+        for other in (i32, i64, f32, f16, u8):
+            if other.dtype == x.dtype:
+                continue
+            args = list(good)
+            args[at] = other
+            with pytest.raises(ValueError):
+                q4k.q4k_verify_drafts(*args, stream=0)
