@@ -71,6 +71,9 @@ SIGNATURES = {
     "q4k_page_tables": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "q4k_verify_drafts_workspace_size": (_SZ, [_I, _I, _I]),
     "q4k_verify_drafts": (_I, [_P, _I, _I, _I, _I64, _P, _I64, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P]),
+    "q4k_shared_prefix_attention_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "q4k_shared_prefix_attention": (_I, [_P, _I, _I, _I, _I, _I, _I64, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _I, _I, _I,
+                                         _I, ctypes.c_float, _I, _P, _I64, _P, _SZ, _P, _P]),
     "q4k_quantize_rows": (_I, [_P, _I64, _I, _P, _P]),
     "q4k_stream_ceiling_sink_words": (_I, []),
     "q4k_stream_ceiling": (_I, [_P, _U64, _P, _P]),
@@ -380,6 +383,24 @@ def q4k_paged_attention(q, m, q_heads, kv_heads, head_dim, q_stride, k_cache, v_
         _dev(v_cache, K.e4m3), _dev(k_scale, K.f32), _dev(v_scale, K.f32), _dev(q_start, K.i32), _dev(seq_lens, K.i32),
         _dev(page_table, K.i32), batch, max_pages, page_size, num_pages, max_q_len, max_len, scale, window,
         _dev(out, K.rows), out_stride, _dev(workspace, K.u8), ws_bytes, _dev(err_flag, K.i32), _stream(stream)))
+
+
+def q4k_shared_prefix_attention_workspace_size(batch, groups, m, q_heads, kv_heads, head_dim) -> int:
+    return int(load().q4k_shared_prefix_attention_workspace_size(batch, groups, m, q_heads, kv_heads, head_dim))
+
+
+def q4k_shared_prefix_attention(q, m, q_heads, kv_heads, head_dim, q_stride, k_cache, v_cache, k_scale, v_scale, q_start,
+                                seq_lens, page_table, batch, max_pages, page_size, num_pages, group_start, prefix_lens, groups,
+                                max_q_len, max_len, max_prefix, scale, window, out, out_stride, workspace, ws_bytes,
+                                err_flag=None, stream=None):
+    """q4k_paged_attention where the sequences of a group share a prefix, which is computed once for all of them."""
+    K = _kinds()
+    _check((_lib or load()).q4k_shared_prefix_attention(
+        _dev(q, K.rows), _row_type(K, q, out), m, q_heads, kv_heads, head_dim, q_stride, _dev(k_cache, K.e4m3),
+        _dev(v_cache, K.e4m3), _dev(k_scale, K.f32), _dev(v_scale, K.f32), _dev(q_start, K.i32), _dev(seq_lens, K.i32),
+        _dev(page_table, K.i32), batch, max_pages, page_size, num_pages, _dev(group_start, K.i32), _dev(prefix_lens, K.i32),
+        groups, max_q_len, max_len, max_prefix, scale, window, _dev(out, K.rows), out_stride, _dev(workspace, K.u8), ws_bytes,
+        _dev(err_flag, K.i32), _stream(stream)))
 
 
 def q4k_page_tables(kept, new, fixed, batch, m, max_pages, page_size, num_pages, held, free_pages, free_count, page_table,

@@ -8,6 +8,7 @@
 
 #include "q4k_internal.cuh"
 #include "q4k_paged.cuh"
+#include "q4k_prefix.cuh"
 
 using namespace q4k;
 
@@ -404,6 +405,26 @@ int check_paged(int m, int batch, int kv_heads, int head_dim, int max_pages, int
     B->batch = batch; B->m = m; B->max_pages = max_pages; B->num_pages = num_pages;
     B->page_shift = page_shift_of(page_size);
     return Q4K_OK;
+}
+
+// What attention over the cache asks of its arguments, with or without shared prefixes.
+int check_attention(const void* d_q, int dtype, int m, int q_heads, int kv_heads, int head_dim, int64_t q_stride,
+                           const void* d_k_cache, const void* d_v_cache, const float* d_k_scale, const float* d_v_scale,
+                           const int32_t* d_q_start, const int32_t* d_seq_lens, const int32_t* d_page_table, int batch,
+                           int max_pages, int page_size, int num_pages, int max_q_len, int max_len, int window,
+                           const void* d_out, int64_t out_stride, PagedBatch* B) {
+    int st = check_dtype(dtype);
+    if (!st) st = check_paged(m, batch, kv_heads, head_dim, max_pages, page_size, num_pages, d_q_start, d_seq_lens,
+                              d_page_table, d_k_cache, d_v_cache, d_k_scale, d_v_scale, B);
+    if (st) return st;
+    if (q_heads < kv_heads || q_heads % kv_heads != 0) return fail(Q4K_ERR_SHAPE, "kv_heads must divide q_heads (got %d, %d)", q_heads, kv_heads);
+    if (q_heads > 65535) return fail(Q4K_ERR_LIMIT, "q_heads must be <= 65535 (got %d)", q_heads);
+    if ((int64_t)m * (q_heads / kv_heads) > (int64_t)1 << 30) return fail(Q4K_ERR_LIMIT, "m*q_heads/kv_heads must be <= 2^30");
+    if (max_q_len < 0 || max_len < 0 || window < 0) return fail(Q4K_ERR_SHAPE, "max_q_len, max_len and window must be >= 0");
+    if (m == 0 || batch == 0) return Q4K_OK;
+    st = check_rows("q", d_q, q_stride, (int64_t)q_heads * head_dim, dtype);
+    if (!st) st = check_rows("out", d_out, out_stride, (int64_t)q_heads * head_dim, dtype);
+    return st;
 }
 
 }  // namespace
@@ -879,23 +900,52 @@ int q4k_paged_attention(const void* d_q, int dtype, int m, int q_heads, int kv_h
                         int window, void* d_out, int64_t out_stride, void* d_workspace, size_t ws_bytes,
                         int* d_err_flag, cudaStream_t stream) {
     PagedBatch B{};
-    int st = check_dtype(dtype);
-    if (!st) st = check_paged(m, batch, kv_heads, head_dim, max_pages, page_size, num_pages, d_q_start, d_seq_lens,
-                              d_page_table, d_k_cache, d_v_cache, d_k_scale, d_v_scale, &B);
-    if (st) return st;
-    if (q_heads < kv_heads || q_heads % kv_heads != 0) return fail(Q4K_ERR_SHAPE, "kv_heads must divide q_heads (got %d, %d)", q_heads, kv_heads);
-    if (q_heads > 65535) return fail(Q4K_ERR_LIMIT, "q_heads must be <= 65535 (got %d)", q_heads);
-    if ((int64_t)m * (q_heads / kv_heads) > (int64_t)1 << 30) return fail(Q4K_ERR_LIMIT, "m*q_heads/kv_heads must be <= 2^30");
-    if (max_q_len < 0 || max_len < 0 || window < 0) return fail(Q4K_ERR_SHAPE, "max_q_len, max_len and window must be >= 0");
-    if (m == 0 || batch == 0) return Q4K_OK;
-    st = check_rows("q", d_q, q_stride, (int64_t)q_heads * head_dim, dtype);
-    if (!st) st = check_rows("out", d_out, out_stride, (int64_t)q_heads * head_dim, dtype);
-    if (!st) st = check_workspace(d_workspace, ws_bytes, q4k_paged_attention_workspace_size(batch, m, q_heads, kv_heads, head_dim));
+    int st = check_attention(d_q, dtype, m, q_heads, kv_heads, head_dim, q_stride, d_k_cache, d_v_cache, d_k_scale, d_v_scale,
+                             d_q_start, d_seq_lens, d_page_table, batch, max_pages, page_size, num_pages, max_q_len, max_len,
+                             window, d_out, out_stride, &B);
+    if (st || m == 0 || batch == 0) return st;
+    st = check_workspace(d_workspace, ws_bytes, q4k_paged_attention_workspace_size(batch, m, q_heads, kv_heads, head_dim));
     if (st) return st;
     return cuda_status(launch_attention(B, d_q, dtype, q_stride, q_heads, kv_heads, head_dim,
                                         static_cast<const uint8_t*>(d_k_cache), static_cast<const uint8_t*>(d_v_cache),
                                         d_k_scale, d_v_scale, max_q_len, max_len, scale, window, d_out, out_stride, d_workspace,
                                         d_err_flag, stream),
+                       "attention launch");
+}
+
+size_t q4k_shared_prefix_attention_workspace_size(int batch, int groups, int m, int q_heads, int kv_heads, int head_dim) {
+    const size_t own = q4k_paged_attention_workspace_size(batch, m, q_heads, kv_heads, head_dim);
+    if (own == 0 || groups < 0 || groups > 1 << 24) return 0;
+    return own + align_up(prefix_workspace_bytes(batch, groups, m, q_heads, kv_heads, head_dim));
+}
+
+int q4k_shared_prefix_attention(const void* d_q, int dtype, int m, int q_heads, int kv_heads, int head_dim, int64_t q_stride,
+                                const void* d_k_cache, const void* d_v_cache, const float* d_k_scale,
+                                const float* d_v_scale, const int32_t* d_q_start, const int32_t* d_seq_lens,
+                                const int32_t* d_page_table, int batch, int max_pages, int page_size, int num_pages,
+                                const int32_t* d_group_start, const int32_t* d_prefix_lens, int groups, int max_q_len,
+                                int max_len, int max_prefix, float scale, int window, void* d_out, int64_t out_stride,
+                                void* d_workspace, size_t ws_bytes, int* d_err_flag, cudaStream_t stream) {
+    PagedBatch B{};
+    int st = check_attention(d_q, dtype, m, q_heads, kv_heads, head_dim, q_stride, d_k_cache, d_v_cache, d_k_scale, d_v_scale,
+                             d_q_start, d_seq_lens, d_page_table, batch, max_pages, page_size, num_pages, max_q_len, max_len,
+                             window, d_out, out_stride, &B);
+    if (st) return st;
+    if (groups < 0 || max_prefix < 0) return fail(Q4K_ERR_SHAPE, "groups and max_prefix must be >= 0 (got %d, %d)", groups, max_prefix);
+    if (groups > 1 << 24) return fail(Q4K_ERR_LIMIT, "groups must be <= 2^24 (got %d)", groups);
+    if (m == 0 || batch == 0) return Q4K_OK;
+    if (groups > 0 && (!d_group_start || !d_prefix_lens)) return fail(Q4K_ERR_NULL, "group_start and prefix_lens are required");
+    for (const void* p : {(const void*)d_group_start, (const void*)d_prefix_lens})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return fail(Q4K_ERR_ALIGN, "group_start and prefix_lens must be 4-byte aligned");
+    const size_t own = q4k_paged_attention_workspace_size(batch, m, q_heads, kv_heads, head_dim);
+    const size_t more = prefix_workspace_bytes(batch, groups, m, q_heads, kv_heads, head_dim);
+    st = check_workspace(d_workspace, ws_bytes, own + align_up(more));
+    if (st) return st;
+    SharedPrefix S{d_group_start, d_prefix_lens, groups, max_prefix, static_cast<uint8_t*>(d_workspace) + own};
+    return cuda_status(launch_attention(B, d_q, dtype, q_stride, q_heads, kv_heads, head_dim,
+                                        static_cast<const uint8_t*>(d_k_cache), static_cast<const uint8_t*>(d_v_cache),
+                                        d_k_scale, d_v_scale, max_q_len, max_len, scale, window, d_out, out_stride, d_workspace,
+                                        d_err_flag, stream, more > 0 && max_prefix >= page_size ? &S : nullptr),
                        "attention launch");
 }
 

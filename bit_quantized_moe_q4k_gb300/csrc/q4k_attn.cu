@@ -32,6 +32,7 @@
 #include <chrono>
 
 #include "q4k_paged.cuh"
+#include "q4k_prefix.cuh"
 
 namespace q4k {
 namespace {
@@ -71,6 +72,7 @@ struct AttnParams {
     unsigned long long tag;  // this launch's counters carry it in their high 48 bits: others count as 0
     int parts;          // CTAs the partial buffer holds
     int* err_flag;
+    PrefixPlan pre;     // with SH: what the tokens that sequences share gave (q4k_prefix.cu)
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -124,7 +126,8 @@ struct SeqWork {
     int lo, tiles, units;
     int64_t total;
 };
-template <int RT, int CL>
+// SH: a sequence's work begins behind the tokens that it shares, whose part is computed elsewhere.
+template <int RT, int CL, bool SH>
 __device__ __forceinline__ SeqWork seq_work(const AttnParams& A, int i) {
     SeqWork w{};
     if (i >= A.B.batch) return w;
@@ -134,6 +137,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& A, int i) {
     if (w.s.n == 0 || (int64_t)w.s.n * A.group > A.max_rows) return w;
     const int first = max(w.s.len - w.s.n, 0);
     w.lo = A.window > 0 ? (max(first - A.window + 1, 0) & ~(kChunk - 1)) : 0;
+    if constexpr (SH) w.lo = max(w.lo, min(__ldcg(A.pre.seq + i).y, max(first, 0)) & ~(kChunk - 1));
     w.tiles = (w.s.n * A.group + RT - 1) / RT;
     w.units = max((w.s.len - w.lo + CL * kUnit - 1) / (CL * kUnit), 1);  // an empty sequence: its rows are zeroed
     w.total = (int64_t)w.tiles * A.kv_heads * (kTileCost + w.units);
@@ -158,12 +162,12 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v) {  // inclusive
 }
 // Move the cursor to the sequence that holds u (u >= c.begin; false past the end). `mine`: the work
 // of sequence `lane`, read once (it is all there is up to 32 sequences).
-template <int RT>
+template <int RT, bool SH>
 __device__ __forceinline__ bool seek(const AttnParams& A, int64_t u, const SeqWork& mine, Cursor* c) {
     const int lane = threadIdx.x & 31;
     int64_t acc = c->begin;
     for (int base = c->seq & ~31; base < A.B.batch; base += 32) {
-        SeqWork w = base == 0 ? mine : seq_work<RT, 1>(A, base + lane);
+        SeqWork w = base == 0 ? mine : seq_work<RT, 1, SH>(A, base + lane);
         if (base + lane < c->seq) w.total = 0;
         const int64_t inc = warp_scan(w.total);
         const unsigned hit = __ballot_sync(0xffffffffu, u < acc + inc);
@@ -184,10 +188,10 @@ __device__ __forceinline__ bool seek(const AttnParams& A, int64_t u, const SeqWo
     }
     return false;
 }
-template <int RT>
+template <int RT, bool SH>
 __device__ __forceinline__ int64_t total_work(const AttnParams& A, const SeqWork& mine) {
     int64_t t = mine.total;
-    for (int i = 32 + (threadIdx.x & 31); i < A.B.batch; i += 32) t += seq_work<RT, 1>(A, i).total;
+    for (int i = 32 + (threadIdx.x & 31); i < A.B.batch; i += 32) t += seq_work<RT, 1, SH>(A, i).total;
 #pragma unroll
     for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     return t;
@@ -203,12 +207,12 @@ struct TilePart {
     int first, j;  // its first cluster; this one's number among them
     bool more;     // there are more tiles than clusters, which then walk over them, a whole one at a time
 };
-template <int RT, int CL>
+template <int RT, int CL, bool SH>
 __device__ __forceinline__ bool tile_part(const AttnParams& A, const SeqWork& mine, int c, int clusters, Cursor* cur, TilePart* p) {
     const int lane = threadIdx.x & 31;
     int64_t tiles = (int64_t)mine.tiles * A.kv_heads, units = tiles * mine.units;
     for (int i = 32 + lane; i < A.B.batch; i += 32) {
-        const SeqWork w = seq_work<RT, CL>(A, i);
+        const SeqWork w = seq_work<RT, CL, SH>(A, i);
         tiles += (int64_t)w.tiles * A.kv_heads;
         units += (int64_t)w.tiles * A.kv_heads * w.units;
     }
@@ -221,7 +225,7 @@ __device__ __forceinline__ bool tile_part(const AttnParams& A, const SeqWork& mi
     p->more = tiles > clusters;
     int64_t acc = 0;
     for (int base = 0; base < A.B.batch; base += 32) {
-        const SeqWork w = base == 0 ? mine : seq_work<RT, CL>(A, base + lane);
+        const SeqWork w = base == 0 ? mine : seq_work<RT, CL, SH>(A, base + lane);
         const int k = w.tiles ? min(1 + (int)div_pos(w.units * spare, units), w.units <= kJoinCost ? 1 : w.units / kLeast) : 1;
         const int64_t own = (int64_t)w.tiles * A.kv_heads * k, inc = warp_scan(own);
         const unsigned hit = __ballot_sync(0xffffffffu, c < acc + inc);
@@ -330,9 +334,49 @@ __device__ __forceinline__ float scale_log2_of(float s) {
     return (b & 0x7FFFFFu) ? e + log2f(__uint_as_float((b & 0x7FFFFFu) | 0x3F800000u)) : e;
 }
 
+// The shared part of a query row, joined to its own one (sums acc and denominator den, relative to 2^ref): `place` holds its first
+// slot, how many there are, and its row in them. V: the dims of a thread, from dim c.
+__device__ __forceinline__ void scale_by(float& a, float w) { a *= w; }
+__device__ __forceinline__ void scale_by(float4& a, float w) { a.x *= w; a.y *= w; a.z *= w; a.w *= w; }
+__device__ __forceinline__ void add_times(float& a, float w, float x) { a = fmaf(w, x, a); }
+__device__ __forceinline__ void add_times(float4& a, float w, const float4& x) {
+    a.x = fmaf(w, x.x, a.x); a.y = fmaf(w, x.y, a.y); a.z = fmaf(w, x.z, a.z); a.w = fmaf(w, x.w, a.w);
+}
+template <int D, typename V>
+__device__ __forceinline__ void join_shared(const PrefixPlan& P, const int4& place, int c, V& acc, float& den, float ref) {
+    constexpr int kAtOnce = 4;
+#pragma unroll 1
+    for (int k0 = 0; k0 < place.y; k0 += kAtOnce) {
+        float2 f[kAtOnce];
+        V x[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int64_t at = (int64_t)(place.x + min(k0 + k, place.y - 1)) * P.tile_rows + place.z;
+            f[k] = __ldcg(P.refs + at);
+            x[k] = __ldcg(reinterpret_cast<const V*>(P.sums + at * D + c));
+        }
+        float top = ref;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, f[k].x);
+        const float use = top == -INFINITY ? 0.0f : top, keep = ex2(ref - use);
+        scale_by(acc, keep);
+        den *= keep;
+        ref = top;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            if (k0 + k >= place.y) continue;
+            const float w = ex2(f[k].x - use);
+            den = fmaf(w, f[k].y, den);
+            add_times(acc, w, x[k]);
+        }
+    }
+}
+// What P and so the sums of a tile are relative to, for the running maximum m (x - reference is 15 at most).
+__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? m : __fadd_ru(m, -15.0f); }
+
 // RT: query rows of a tile. fp32: 8 (two fp16 terms fill the 16 rows); bf16: 8 where a tile has no
 // more rows, else 16.
-template <typename T, int D, int RT, int CL>
+template <typename T, int D, int RT, int CL, bool SH>
 __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const __grid_constant__ AttnParams A) {
     constexpr bool HL = sizeof(T) == 4;           // two fp16 terms
     constexpr int NR = RT / 8;                    // rows of a thread: g, and g + 8
@@ -342,7 +386,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
     float* s_o = reinterpret_cast<float*>(s_mem); // [warps][RT][D], over the rings once they are read
     __shared__ float s_m[kAttnWarps * RT], s_l[kAttnWarps * RT];
     __shared__ ChunkMeta s_meta[kAttnWarps][kRing * kPair];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // With SH the kernel before computes the shared part and began when all before it had ended (it waited for the plan's
+    // kernel): only its results have to be waited for, when they are joined.
+    if constexpr (!SH) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int rank = CL > 1 ? cluster_rank() : 0, my_piece = CL > 1 ? (int)blockIdx.x / CL : (int)blockIdx.x;
@@ -357,13 +403,14 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
     __shared__ int s_pieces;
     __shared__ TilePart s_tile;
     __shared__ bool s_by_tile;
+    __shared__ int4 s_pre[SH ? RT : 1];  // where the shared part of each row is
     __shared__ struct { int c0, slot0, size, groups, first, count, last; } s_join;
     if (warp == 0) {
-        const SeqWork mine = seq_work<RT, CL>(A, lane);
+        const SeqWork mine = seq_work<RT, CL, SH>(A, lane);
         int longest = mine.units;
         int64_t tiles = (int64_t)mine.tiles * A.kv_heads;
         for (int i = 32 + lane; CL == 1 && i < A.B.batch; i += 32) {
-            const SeqWork w = seq_work<RT, CL>(A, i);
+            const SeqWork w = seq_work<RT, CL, SH>(A, i);
             longest = max(longest, w.units);
             tiles += (int64_t)w.tiles * A.kv_heads;
         }
@@ -377,7 +424,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
         if (by_tile) {
             Cursor c{};
             TilePart p{};
-            const bool any = tile_part<RT, CL>(A, mine, my_piece, gridDim.x / CL, &c, &p);
+            const bool any = tile_part<RT, CL, SH>(A, mine, my_piece, gridDim.x / CL, &c, &p);
             if (lane == 0) {
                 s_cur = c;
                 s_tile = p;
@@ -386,7 +433,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
             }
         } else {
             s_work[lane] = mine;
-            const int64_t total = total_work<RT>(A, mine);
+            const int64_t total = total_work<RT, SH>(A, mine);
             // more such tiles than CTAs: pieces are not shorter than a whole one
             const int64_t least = longest <= kJoinCost ? kTileCost + longest : 1;
             const int pieces = (int)min((int64_t)min((int)gridDim.x, A.parts), div_pos(total + least - 1, least));
@@ -394,7 +441,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
             const int64_t u0 = any ? piece_begin(total, pieces, my_piece) : 0;
             const int64_t u1 = any ? piece_begin(total, pieces, my_piece + 1) : 0;
             Cursor c{};
-            if (any) seek<RT>(A, u0, mine, &c);
+            if (any) seek<RT, SH>(A, u0, mine, &c);
             if (lane == 0) {
                 s_cur = c;
                 s_u[0] = u0;
@@ -528,6 +575,20 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                 s_meta[warp][k % kRing * kPair + c] = ChunkMeta{ah.ks0, scale_log2_of(ah.vs0), 1.0f / ah.vs0, ah.p0 >= 0};
         };
         for (int k = 0; k < kRing; ++k) issue(k);
+        if (SH && warp == 2 && lane < RT) {
+            const int row = tile * RT + lane, group = __ldcg(A.pre.seq + seq).x;
+            int4 place = make_int4(0, 0, 0, 0);
+            if (row < rows && group >= 0 && group < A.pre.groups) {
+                const PrefixGroup* G = A.pre.group + group;
+                const int r = max(sp.start - __ldcg(&G->row0), 0) * A.group + row, row_tile = r / A.pre.tile_rows;
+                const int64_t item = __ldcg(&G->item0) + (int64_t)row_tile * A.kv_heads + head;
+                // (a plan that another call on this workspace has written over leads to no place outside it)
+                const int2 p = item >= 0 && item < A.pre.items ? __ldcg(A.pre.piece + item) : make_int2(0, 0);
+                if (p.x >= 0 && p.y > 0 && p.y <= kPrefixCtas && p.x + p.y <= A.pre.slots)
+                    place = make_int4(p.x, p.y, r - row_tile * A.pre.tile_rows, 0);
+            }
+            s_pre[lane] = place;
+        }
         scales_of(ah.p0, ah.ks0, ah.vs0);
         scales_of(ah.p1, ah.ks1, ah.vs1);
 
@@ -815,6 +876,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                 }
             }
         }
+        if constexpr (SH) asm volatile("griddepcontrol.wait;" ::: "memory");
         // join the warps: each row's maximum, then the weighted sums
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
@@ -840,9 +902,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
         // a tile that begins in this piece, but not at its start, goes to the second slot
         constexpr int kPart = RT * (D + 2);
         float* part = A.part + ((int64_t)my_piece * 2 + (not_first ? 1 : 0)) * kPart;
-        auto store_row = [&](int r, int c, const float4& acc, float den) {
+        auto store_row = [&](int r, int c, float4 acc, float den, float m) {
             const int row = tile * RT + r;
             if (row >= rows) return;
+            if constexpr (SH) join_shared<D>(A.pre, s_pre[r], c, acc, den, reference(m));
             const float iv = den == 0.0f ? 0.0f : 1.0f / den;  // 0: the row sees nothing
             const float y[4] = {acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv};
             Vec<T>::store(static_cast<T*>(A.out) + (int64_t)(sp.start + row / A.group) * A.out_stride +
@@ -875,7 +938,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                 continue;
             }
             if (whole) {
-                store_row(r, c, acc, den);
+                store_row(r, c, acc, den, m);
             } else {
                 *reinterpret_cast<float4*>(part + r * D + c) = acc;
                 if (c == 0) {
@@ -917,6 +980,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                         part[RT * D + RT + r] = den;
                     }
                 } else if (const int row = tile * RT + r; row < rows) {
+                    if constexpr (SH) join_shared<D>(A.pre, s_pre[r], c, acc, den, reference(m));
                     const float y = den == 0.0f ? 0.0f : acc / den;  // 0: the row sees nothing
                     T* o = static_cast<T*>(A.out) + (int64_t)(sp.start + row / A.group) * A.out_stride +
                            (int64_t)(head * A.group + row % A.group) * D + c;
@@ -967,7 +1031,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                         acc.z = fmaf(wt, v.z, acc.z); acc.w = fmaf(wt, v.w, acc.w);
                     }
                     if (to_out) {
-                        store_row(r, c, acc, den);
+                        store_row(r, c, acc, den, m);
                         continue;
                     }
                     float* x = piece(first);
@@ -993,7 +1057,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                 Cursor c{};
                 TilePart p{};
                 const int clusters = gridDim.x / CL, next = s_tile.first + clusters;
-                const bool any = tile_part<RT, CL>(A, seq_work<RT, CL>(A, lane), next, clusters, &c, &p);
+                const bool any = tile_part<RT, CL, SH>(A, seq_work<RT, CL, SH>(A, lane), next, clusters, &c, &p);
                 if (lane == 0) {
                     s_cur = c;
                     s_tile = p;
@@ -1004,7 +1068,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
             const int64_t u = s_u[0] + step;
             Cursor c = s_cur;
             __syncwarp();
-            const bool more = u < s_u[1] && (u < c.begin + c.w.total || seek<RT>(A, u, s_work[lane], &c));
+            const bool more = u < s_u[1] && (u < c.begin + c.w.total || seek<RT, SH>(A, u, s_work[lane], &c));
             if (lane == 0) {
                 s_cur = c;
                 s_u[0] = more ? u : s_u[1];
@@ -1012,11 +1076,12 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
         }
         __syncthreads();
     }
+    if constexpr (SH) asm volatile("griddepcontrol.wait;" ::: "memory");  // what comes after this kernel comes after that one, too
 }
 
 constexpr int kCluster = 8;
 
-template <typename T, int D, int RT, int CL>
+template <typename T, int D, int RT, int CL, bool SH>
 cudaError_t launch_cluster(const AttnParams& P, int max_len, cudaStream_t stream, int64_t segs, bool* fits) {
     const size_t rings = (size_t)kAttnWarps * kRing * kStage<D>, join = (size_t)(kAttnWarps + 1) * RT * D * sizeof(float);
     const size_t smem = rings > join ? rings : join;
@@ -1039,13 +1104,13 @@ cudaError_t launch_cluster(const AttnParams& P, int max_len, cudaStream_t stream
     cfg.numAttrs = CL > 1 ? 2 : 1;
     int most = clusters[dev].load(std::memory_order_relaxed);
     if (most == 0) {
-        e = cudaFuncSetAttribute(attn_kernel<T, D, RT, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = cudaFuncSetAttribute(attn_kernel<T, D, RT, CL, SH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         most = P.parts;
         if (CL > 1) {
             cfg.gridDim = dim3(CL);
             int n = 0;
-            e = cudaOccupancyMaxActiveClusters(&n, attn_kernel<T, D, RT, CL>, &cfg);
+            e = cudaOccupancyMaxActiveClusters(&n, attn_kernel<T, D, RT, CL, SH>, &cfg);
             if (e != cudaSuccess) return e;
             most = n < 1 ? 1 : n < P.parts ? n : P.parts;
         }
@@ -1060,11 +1125,11 @@ cudaError_t launch_cluster(const AttnParams& P, int max_len, cudaStream_t stream
     int64_t grid = segs * (units <= kJoinCost ? 1 : CL > 1 ? units / kLeast : kTileCost + units);
     if (grid > most) grid = most;
     cfg.gridDim = dim3((unsigned)(grid * CL));
-    return cudaLaunchKernelEx(&cfg, attn_kernel<T, D, RT, CL>, P);
+    return cudaLaunchKernelEx(&cfg, attn_kernel<T, D, RT, CL, SH>, P);
 }
 
-template <typename T, int D, int RT>
-cudaError_t launch_typed(const AttnParams& P, int64_t max_rows, int max_len, cudaStream_t stream) {
+template <typename T, int D, int RT, bool SH>
+cudaError_t launch_rows(const AttnParams& P, int64_t max_rows, int max_len, cudaStream_t stream) {
     const int64_t held = (int64_t)P.B.max_pages << P.B.page_shift;  // no sequence is longer than its table's row
     if (max_len > held) max_len = (int)held;
     // An upper bound of the row tiles: each sequence's last one may be part filled, and none has more than max_rows.
@@ -1074,9 +1139,14 @@ cudaError_t launch_typed(const AttnParams& P, int64_t max_rows, int max_len, cud
     // Clusters where each tile finds one (51 at once on a GB300). 4 kv heads of 8 rows of fp32: one sequence of 1000 tokens
     // 8.5 us with, 12.9 without; of 16000 17.3 and 22.7; ten of 2000 13.0 and 17.6; 64 tiles of 1000 20.6 and 17.6.
     bool fits = true;
-    const cudaError_t e = launch_cluster<T, D, RT, kCluster>(P, max_len, stream, segs, &fits);
+    const cudaError_t e = launch_cluster<T, D, RT, kCluster, SH>(P, max_len, stream, segs, &fits);
     if (e != cudaSuccess || fits) return e;
-    return launch_cluster<T, D, RT, 1>(P, max_len, stream, segs, nullptr);
+    return launch_cluster<T, D, RT, 1, SH>(P, max_len, stream, segs, nullptr);
+}
+
+template <typename T, int D, int RT>
+cudaError_t launch_typed(const AttnParams& P, int64_t max_rows, int max_len, cudaStream_t stream) {
+    return P.pre.seq ? launch_rows<T, D, RT, true>(P, max_rows, max_len, stream) : launch_rows<T, D, RT, false>(P, max_rows, max_len, stream);
 }
 
 // A value that no other launch of the process has (and, from a start that differs, hardly any other process's).
@@ -1097,7 +1167,7 @@ size_t attn_workspace_bytes(int head_dim) {  // the counters, then two slots of 
 cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int64_t q_stride, int q_heads, int kv_heads,
                              int head_dim, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
                              const float* v_scale, int max_q_len, int max_len, float scale, int window, void* out,
-                             int64_t out_stride, void* workspace, int* err_flag, cudaStream_t stream) {
+                             int64_t out_stride, void* workspace, int* err_flag, cudaStream_t stream, const SharedPrefix* shared) {
     if (window >= 1 << 30) window = 0;  // no sequence is longer: every row sees all before it
     // Which kernel a sequence takes goes by its query rows per kv head; max_q_len says which kernels can
     // be needed, and a kernel that is launched alone takes every sequence.
@@ -1111,6 +1181,13 @@ cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int6
         if (e != cudaSuccess || !few) return e;
     }
     AttnParams P{};
+    if (shared) {
+        const cudaError_t e = launch_prefix(B, q, dtype, q_stride, q_heads, kv_heads, head_dim, k_cache, v_cache, k_scale, v_scale,
+                                            shared->group_start, shared->prefix_lens, shared->groups, shared->max_prefix,
+                                            prompts ? kFewRows : 0x7FFFFFFF, scale, window, shared->workspace, err_flag, &P.pre,
+                                            stream);
+        if (e != cudaSuccess) return e;
+    }
     P.B = B; P.q = q; P.out = out; P.q_stride = q_stride; P.out_stride = out_stride;
     P.k_cache = k_cache; P.v_cache = v_cache; P.k_scale = k_scale; P.v_scale = v_scale;
     P.kv_heads = kv_heads; P.group = q_heads / kv_heads; P.window = window;

@@ -489,8 +489,35 @@ int q4k_paged_attention(const void* d_q, int dtype, int m, int q_heads, int kv_h
                         int* d_err_flag, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------------
+ * q4k_shared_prefix_attention -- q4k_paged_attention for batches in which groups of sequences share a prefix, whose
+ * tokens are read and multiplied once for the whole group (no counterpart in the studied pages; an addition of this
+ * library). The result is q4k_paged_attention's, within the same bounds.
+ *   d_group_start [groups + 1], d_prefix_lens [groups] (device memory, int32): sequences group_start[g] ..
+ *   group_start[g+1] - 1 have their first prefix_lens[g] tokens in common, and those of their pages that lie wholly in the prefix: the
+ *   first prefix_lens[g] / page_size entries of their rows of the page table are the same (which of the rows is read is not
+ *   specified). Rising, within [0, batch]; sequences before the first group or after the last share nothing.
+ *   What is shared is the whole pages of the prefix that lie before every new token of the group's sequences; the sequences read all else,
+ *   and groups with new tokens in fewer than two sequences, as in q4k_paged_attention.
+ *   max_prefix: an upper bound of prefix_lens that chooses the kernels (below page_size: nothing is shared).
+ *   The rest: as in q4k_paged_attention. Sequences of more than 64 query rows per kv head in calls that it gives to its prompt
+ *   kernels, and calls of more than 2^20 query rows (m*q_heads), read their prefixes themselves.
+ * Device flags: as in q4k_paged_attention; group_start falling or outside [0, batch] (or q_start outside its rules): nothing is shared,
+ * prefix_lens outside [0, max_pages*page_size] are clamped (Q4K_ERR_SEQ).
+ * Limits (Q4K_ERR_LIMIT): q4k_paged_attention's, groups <= 2^24. Three launches (one more beside prompts). Within one softmax row the
+ * fp32 sums of the two parts are joined once more: 2^-23 of the result.
+ * Workspace: q4k_shared_prefix_attention_workspace_size bytes, any contents. */
+size_t q4k_shared_prefix_attention_workspace_size(int batch, int groups, int m, int q_heads, int kv_heads, int head_dim);
+int q4k_shared_prefix_attention(const void* d_q, int dtype, int m, int q_heads, int kv_heads, int head_dim, int64_t q_stride,
+                                const void* d_k_cache, const void* d_v_cache, const float* d_k_scale,
+                                const float* d_v_scale, const int32_t* d_q_start, const int32_t* d_seq_lens,
+                                const int32_t* d_page_table, int batch, int max_pages, int page_size, int num_pages,
+                                const int32_t* d_group_start, const int32_t* d_prefix_lens, int groups, int max_q_len,
+                                int max_len, int max_prefix, float scale, int window, void* d_out, int64_t out_stride,
+                                void* d_workspace, size_t ws_bytes, int* d_err_flag, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------
  * q4k_page_tables -- a serving step's batch, built on the device from its sequences' lengths: page
- * table, starts, lengths, positions and slots as the three calls above read them (no counterpart in
+ * table, starts, lengths, positions and slots as the calls above read them (no counterpart in
  * the studied pages; an addition of this library). Sequence i keeps kept[i] cached tokens (less than
  * it had: drafts were rejected; 0 with new[i] = 0: it has ended) and brings new[i] more.
  *   need_i = max(ceil((kept[i] + new[i]) / page_size) - fixed[i], 0) pages are to be its own. It holds

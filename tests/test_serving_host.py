@@ -4,6 +4,8 @@ import pytest
 
 import bit_quantized_moe_q4k_gb300 as q4k
 
+from test_attention_host import PAGED_REFUSALS
+
 torch = pytest.importorskip("torch")
 
 A16 = 1 << 20          # a fake 16-byte-aligned address; never dereferenced by these calls
@@ -100,3 +102,57 @@ def test_verify_binding_refuses_other_element_types():
             args[at] = other
             with pytest.raises(ValueError):
                 q4k.q4k_verify_drafts(*args, stream=0)
+
+
+def prefix(**kw):
+    a = dict(q=A16, dtype=0, m=3, hq=8, hk=2, d=128, qs=1024, kc=A16, vc=A16, ksc=A16, vsc=A16, qst=A16, lens=A16, table=A16, batch=2,
+             mp=4, page=16, np=8, gs=A16, pl=A16, groups=1, maxq=2, maxl=64, maxp=32, scale=0.1, window=0, out=A16, os=1024, ws=A16,
+             wsb=None)
+    a.update(kw)
+    lib = q4k.load()
+    if a["wsb"] is None:
+        a["wsb"] = lib.q4k_shared_prefix_attention_workspace_size(2, 1, 3, 8, 2, 128)
+    return lib.q4k_shared_prefix_attention(
+        a["q"], a["dtype"], a["m"], a["hq"], a["hk"], a["d"], a["qs"], a["kc"], a["vc"], a["ksc"], a["vsc"], a["qst"], a["lens"],
+        a["table"], a["batch"], a["mp"], a["page"], a["np"], a["gs"], a["pl"], a["groups"], a["maxq"], a["maxl"], a["maxp"], a["scale"],
+        a["window"], a["out"], a["os"], a["ws"], a["wsb"], None, None)
+
+
+@pytest.mark.parametrize("kw,status", PAGED_REFUSALS + [
+    (dict(hq=7), 2), (dict(hq=1), 2), (dict(maxq=-1), 2), (dict(maxl=-1), 2), (dict(window=-1), 2), (dict(qs=1022), 2),
+    (dict(qs=1026), 7), (dict(os=1020), 2), (dict(q=None), 1), (dict(out=None), 1), (dict(q=A16 + 4), 7), (dict(out=A16 + 8), 7),
+    (dict(ws=None), 4), (dict(wsb=1024), 4), (dict(ws=A16 + 16), 4), (dict(hq=65538, qs=1 << 24, os=1 << 24), 9),
+    (dict(groups=-1), 2), (dict(maxp=-1), 2), (dict(groups=(1 << 24) + 1), 9), (dict(gs=None), 1), (dict(pl=None), 1),
+    (dict(gs=A16 + 2), 7), (dict(pl=A16 + 1), 7),
+])
+def test_prefix_rejects(kw, status):
+    assert prefix(**kw) == status
+    assert q4k.load().q4k_last_error_string()
+
+
+def test_prefix_empty_and_workspace():
+    assert prefix(m=0) == 0
+    assert prefix(batch=0) == 0
+    lib = q4k.load()
+    own = lib.q4k_paged_attention_workspace_size(64, 64, 32, 8, 128)
+    assert lib.q4k_shared_prefix_attention_workspace_size(64, 0, 64, 32, 8, 128) == own
+    some = lib.q4k_shared_prefix_attention_workspace_size(64, 1, 64, 32, 8, 128)
+    assert some > own and some % 256 == 0
+    # beyond 2^20 query rows nothing is shared, and no place for it is asked for
+    assert lib.q4k_shared_prefix_attention_workspace_size(64, 1, (1 << 20) // 32 + 1, 32, 8, 128) == own
+    for bad in ((1, 1, 1, 32, 4, 96), (1, 1, 1, 30, 4, 128), (-1, 1, 1, 32, 4, 128), (1, -1, 1, 32, 4, 128)):
+        assert lib.q4k_shared_prefix_attention_workspace_size(*bad) == 0
+
+
+def test_prefix_binding_refuses_other_element_types():
+    f32, f8, i32, u8, f16 = (FakeCuda(t) for t in (torch.float32, torch.float8_e4m3fn, torch.int32, torch.uint8, torch.float16))
+    good = [f32, 3, 8, 2, 128, 1024, f8, f8, f32, f32, i32, i32, i32, 2, 4, 16, 8, i32, i32, 1, 2, 64, 32, 0.1, 0, f32, 1024, u8, 1 << 30,
+            i32]
+    for at, x in enumerate(good):
+        if isinstance(x, (int, float)):
+            continue
+        for other in (f16, f32 if x is not f32 else i32):
+            args = list(good)
+            args[at] = other
+            with pytest.raises(ValueError):
+                q4k.q4k_shared_prefix_attention(*args, stream=0)
