@@ -10,9 +10,8 @@
 //   1. verify_stats_kernel: each row's largest logit and its sum of 2^(c (x - max)), c = log2(e) / T, in fp32, by chunks of
 //      rows over all SMs. Bound by the logits' bytes.
 //   2. verify_pick_kernel: a cluster of eight CTAs a sequence. An acceptance whose two sides differ by more than 2^-14 stands;
-//      another is computed again from weights good to 2^-41. The token is drawn in such weights, as 64-bit integers in units of
-//      2^-b of the row's largest, b = 63 - log2(vocabulary): their sums are exact in any order. One row of logits, and of the drafts' probabilities, is read up to three times, the
-//      second and third time from L2.
+//      another is computed again from weights good to 2^-41. The token is drawn in weights good to 2^-31, as 64-bit integers in units of
+//      2^-b of the row's largest, b = 62 - log2(vocabulary): their sums are exact in any order. One row of logits, and of the drafts' probabilities, is read once.
 #include <atomic>
 
 #include "q4k_paged.cuh"
@@ -20,13 +19,17 @@
 namespace q4k {
 namespace {
 
-constexpr int kStatThreads = 256, kStatUnits = 4;   // 16-byte units of a thread in flight
-constexpr int kPickThreads = 512, kPickWarps = kPickThreads / 32, kPickCluster = 8, kAllWarps = kPickWarps * kPickCluster;
+constexpr int kStatThreads = 256;
+constexpr int kPickThreads = 256, kPickWarps = kPickThreads / 32, kMostCluster = 8;
+constexpr int kSeg = 512;                           // tokens of a segment, whose sum is kept
 constexpr float kGreedy = 5.421010862427522e-20f;   // 2^-64: temperatures not above choose the largest logit
 constexpr float kLargest = 3.402823466e38f;
-// Above the relative error of a decision's two sides in fp32: exponents of up to 100 rounded three times (1.3e-5), ex2, a
-// few hundred additions a thread (1.2e-5).
-constexpr double kClose = 1.0 / 16384.0;
+// The relative error of a decision's two sides in fp32 is below (1.4 |y| + 86) 2^-23, y the draft's exponent: four roundings of y
+// (4 ln 2 2^-24 |y|), the same in the sum, where the mean of |y| is the distribution's entropy at most (20 bits), ex2 (2 2^-23), up to
+// nine changes of a thread's largest (18 2^-23), and some sixty additions one after another (30 2^-23).
+__device__ __forceinline__ float closeness(float y) { return fmaf(fabsf(y), 1.5f, 96.0f) * 1.1920929e-7f; }
+// And where it is computed from the draw's weights, 2^-31 each and cut at 2^-45 of 2^17 tokens.
+constexpr double kCloseFine = 1.0 / 67108864.0;
 
 struct VerifyParams {
     const void* logits;
@@ -37,7 +40,7 @@ struct VerifyParams {
     int32_t *accepted, *next, *kept;
     float4* stats;   // [m][chunks]: largest, sum, its index (bits)
     int batch, m, vocab, chunks;
-    int bits;        // weights are integers in units of 2^-bits: 2^(63 - bits) of them add up to less than 2^64
+    int bits;        // weights are integers in units of 2^-bits: the row's add up to 2^62 at most
     int* err_flag;
 };
 
@@ -47,6 +50,26 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Two fp32 operations in one instruction, each rounded to nearest.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return d;
 }
 __device__ __forceinline__ float one(const float* p) { return __ldcg(p); }
 __device__ __forceinline__ float one(const __nv_bfloat16* p) {
@@ -79,34 +102,30 @@ __device__ __forceinline__ int sequence_of(const VerifyParams& A, int r) {
 
 // ---- the rows in fp32 ---------------------------------------------------------------------------------------------
 template <typename T>
-__global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const __grid_constant__ VerifyParams A) {
+__global__ void __launch_bounds__(kStatThreads, 4) verify_stats_kernel(const __grid_constant__ VerifyParams A) {
     constexpr int V = 16 / (int)sizeof(T), W = kStatThreads / 32;
+    constexpr int kUnits = 4;  // 16-byte units a thread and batch
     __shared__ float s_m[W], s_s[W], s_t;
     __shared__ int s_i[W], s_seq;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x / A.chunks, chunk = blockIdx.x - row * A.chunks;
     const T* x = static_cast<const T*>(A.logits) + (int64_t)row * A.logits_stride;
-    // 16-byte units from the aligned address at or below the row; only units that lie inside the row are read whole
+    // 16-byte units from the aligned address at or below the row. Whole ones lie inside it; the two ends are read by element.
     const int shift = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
     const int units = (A.vocab + shift + V - 1) / V;
     const int u0 = (int)((int64_t)units * chunk / A.chunks), u1 = (int)((int64_t)units * (chunk + 1) / A.chunks);
-    auto load = [&](int u, float (&v)[V]) {
-        const int e = u * V - shift;
-        if (u < u1 && e >= 0 && e + V <= A.vocab) {
-            unpack<T, V>(__ldcg(reinterpret_cast<const uint4*>(x + e)), v);
-        } else {
+    const int w0 = max(u0, shift ? 1 : 0), w1 = min(u1, (A.vocab + shift) / V);   // the chunk's whole units
+    const uint4* const xu = reinterpret_cast<const uint4*>(x - shift);
+    constexpr int kStep = kUnits * kStatThreads;
+    uint4 raw[2][kUnits];  // two batches, one under way while another is worked on
+    auto fetch = [&](int u, uint4 (&to)[kUnits]) {
+        if (u + kStep <= w1) {
 #pragma unroll
-            for (int k = 0; k < V; ++k) v[k] = u < u1 && e + k >= 0 && e + k < A.vocab ? one(x + e + k) : -INFINITY;
+            for (int j = 0; j < kUnits; ++j) to[j] = __ldcg(xu + u + j * kStatThreads + tid);
         }
     };
-    float v[kStatUnits][V];
-    auto fetch = [&](int u) {
-#pragma unroll
-        for (int j = 0; j < kStatUnits; ++j) load(u + j * kStatThreads + tid, v[j]);
-    };
-    fetch(u0);
+    fetch(w0, raw[0]);
     if (warp == 0) {
         const int seq = sequence_of(A, row);
         if (lane == 0) {
@@ -120,55 +139,117 @@ __global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const __grid
     const float c = 1.44269504088896340736f / s_t;
     float m = -INFINITY, s = 0.0f;
     int best = 0x7FFFFFFF;
-    bool tamed = false;
-    for (int u = u0;;) {
-        if (greedy) {
+    // One unit: its elements begin at token e.
+    auto choose = [&](int e, const float (&v)[V]) {
 #pragma unroll
-            for (int j = 0; j < kStatUnits; ++j)
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const float y = tame(v[j][k]);
-                    if (y > m) {
-                        m = y;
-                        best = (u + j * kStatThreads + tid) * V - shift + k;
-                    }
-                }
-        } else {
-            float top = m;
-#pragma unroll
-            for (int j = 0; j < kStatUnits; ++j)
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    if (tamed) v[j][k] = tame(v[j][k]);
-                    top = fmaxf(top, v[j][k]);
-                }
-            if (top > -INFINITY) {
-                s *= ex2((m - top) * c);
-                if (m == -INFINITY) s = 0.0f;
-                m = top;
-#pragma unroll
-                for (int j = 0; j < kStatUnits; ++j) {
-                    float part = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        const float w = ex2((v[j][k] - m) * c);
-                        part += tamed && v[j][k] == -INFINITY ? 0.0f : w;
-                    }
-                    s += part;
-                }
+        for (int k = 0; k < V; ++k) {
+            const float y = tame(v[k]);
+            if (y > m || (y == m && e + k < best && y > -INFINITY)) {
+                m = y;
+                best = e + k;
             }
         }
-        u += kStatUnits * kStatThreads;
-        if (u >= u1) {
-            // NaN, +inf or a c of 0 among them: once more with every logit tamed
-            if (tamed || greedy || (s < INFINITY && m < INFINITY)) break;
-            tamed = true;
-            m = -INFINITY;
-            s = 0.0f;
-            u = u0;
+    };
+    auto rise = [&](float top) {  // the sum's reference
+        s = m > -INFINITY ? s * ex2((m - top) * c) : 0.0f;
+        m = top;
+    };
+    auto add = [&](const float (&v)[V]) {
+        float2 part = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+            float2 y = add2(make_float2(v[k], v[k + 1]), make_float2(-m, -m));
+            y = mul2(y, make_float2(c, c));
+            part = add2(part, make_float2(ex2(y.x), ex2(y.y)));
         }
-        fetch(u);
+        s += part.x + part.y;
+    };
+    auto take = [&](int u, const uint4 (&from)[kUnits]) {
+        if (greedy) {
+#pragma unroll
+            for (int j = 0; j < kUnits; ++j) {
+                float v[V];
+                unpack<T, V>(from[j], v);
+                choose((u + j * kStatThreads + tid) * V - shift, v);
+            }
+            return;
+        }
+        float top = m;
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j) {
+            float v[V];
+            unpack<T, V>(from[j], v);
+#pragma unroll
+            for (int k = 0; k < V; k += 2) top = max3(top, v[k], v[k + 1]);
+        }
+        if (top > m) rise(top);
+        if (m == -INFINITY) return;
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j) {
+            float v[V];
+            unpack<T, V>(from[j], v);
+            add(v);
+        }
+    };
+    int u = w0;
+    for (; u + 2 * kStep <= w1; u += 2 * kStep) {
+        fetch(u + kStep, raw[1]);
+        take(u, raw[0]);
+        fetch(u + 2 * kStep, raw[0]);
+        take(u + kStep, raw[1]);
     }
+    if (u + kStep <= w1) {
+        take(u, raw[0]);
+        u += kStep;
+    }
+    // what is left of the whole units, then the ends
+    auto few = [&](int e, const float (&v)[V]) {
+        if (greedy) return choose(e, v);
+        float top = m;
+#pragma unroll
+        for (int k = 0; k < V; ++k) top = fmaxf(top, v[k]);
+        if (top > m) rise(top);
+        if (m > -INFINITY) add(v);
+    };
+    auto at_end = [&](int un, float (&v)[V]) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int e = un * V - shift + k;
+            v[k] = e >= 0 && e < A.vocab ? one(x + e) : -INFINITY;
+        }
+    };
+    for (int v0 = u + tid; v0 < w1; v0 += kStatThreads) {
+        float v[V];
+        unpack<T, V>(__ldcg(xu + v0), v);
+        few(v0 * V - shift, v);
+    }
+    if (tid < 2) {
+        const int un = tid ? u1 - 1 : u0;   // an end of the chunk that is no whole unit
+        if (un >= u0 && un < u1 && (un < w0 || un >= w1) && (tid == 0 || u1 - 1 != u0)) {
+            float v[V];
+            at_end(un, v);
+            few(un * V - shift, v);
+        }
+    }
+    if (!greedy && !(s < INFINITY && m < INFINITY)) {  // NaN, +inf or a c of 0 among them: once more, with every logit tamed
+        m = -INFINITY;
+        s = 0.0f;
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass)
+#pragma unroll 1
+            for (int un = u0 + tid; un < u1; un += kStatThreads) {
+                float v[V];
+                at_end(un, v);
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const float y = tame(v[k]);
+                    if (pass == 0) m = fmaxf(m, y);
+                    else s += y > -INFINITY ? ex2((y - m) * c) : 0.0f;
+                }
+            }
+    }
+    // The next kernel's large CTAs are let in only now: they would take the place of this one's.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // the block's
     float top = m;
 #pragma unroll
@@ -201,20 +282,32 @@ __global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const __grid
     A.stats[blockIdx.x] = make_float4(all, sum, __int_as_float(at), 0.0f);
 }
 
-// ---- precise weights ----------------------------------------------------------------------------------------------
-// 2^(i/256), i < 256, as two floats: products of the square roots of square roots of 2.
+// ---- weights of more than 24 bits ---------------------------------------------------------------------------------
+// The weight 2^y of a logit, y = c (x - top), relative to the row's largest: y in two floats (2^-46 of itself), cut into
+// multiples of a table's step and a rest r; 2^r = 1 + a + a^2/2 + .., a = r ln 2.
+//   Weigher: 1024 steps, 32 bits of the power in an integer, a^2/2 the last term: off by 2^-31 of itself at most
+//            (half a unit of 2^-31 in the table, half in the product, 2^-37 from the next term), 34 instructions. For the draw.
+//   precise: 256 steps, two floats, a^3/6: 2^-41. For an acceptance too close to call in fp32.
+constexpr double kRoots[10] = {  // 2^(1/2), 2^(1/4), ..
+    1.414213562373095048801689, 1.189207115002721066717500, 1.090507732665257659207010, 1.044273782427413840321966,
+    1.021897148654116678234480, 1.010889286051700460020410, 1.005429901112802821351384, 1.002711275050202485430746,
+    1.001354719892108205880882, 1.000677130693066356678173};
+constexpr double power_of_two(int i, int bits) {  // 2^(i / 2^bits)
+    double x = 1.0;
+    for (int k = 0; k < bits; ++k)
+        if (i >> (bits - 1 - k) & 1) x *= kRoots[k];
+    return x;
+}
+constexpr int kTable = 1024;
 struct Powers {
+    uint32_t fix[kTable];  // 2^(i/1024) 2^31
     float hi[256], lo[256];
 };
 constexpr Powers make_powers() {
-    constexpr double root[8] = {1.414213562373095048801689, 1.189207115002721066717500, 1.090507732665257659207010,
-                                1.044273782427413840321966, 1.021897148654116678234480, 1.010889286051700460020410,
-                                1.005429901112802821351384, 1.002711275050202485430746};
     Powers p{};
+    for (int i = 0; i < kTable; ++i) p.fix[i] = (uint32_t)(power_of_two(i, 10) * 2147483648.0 + 0.5);
     for (int i = 0; i < 256; ++i) {
-        double x = 1.0;
-        for (int k = 0; k < 8; ++k)
-            if (i >> (7 - k) & 1) x *= root[k];
+        const double x = power_of_two(i, 8);
         p.hi[i] = (float)x;
         p.lo[i] = (float)(x - (double)p.hi[i]);
     }
@@ -222,55 +315,79 @@ constexpr Powers make_powers() {
 }
 __device__ const Powers kPowers = make_powers();
 
-// The weight 2^(c (x - top)) of a logit, relative error 2^-41: the exponent in two floats (2^-46 of itself), cut
-// into 256ths and a rest r of at most 2^-9; 2^r = 1 + a + a^2/2 + a^3/6, a = r ln 2, whose next term is below 2^-42.
 struct Weigher {
-    const float2* pow;   // in shared memory
+    const uint2* table;   // in shared memory: the integer, and the same as a float
     float top, c_hi, c_lo;
-    int bits;
-    __device__ __forceinline__ Weigher(const float2* p, float t, float temperature, int b) : pow(p), top(t), bits(b) {
-        const double c = 1.4426950408889634074 / (double)temperature;
-        c_hi = (float)c;
-        c_lo = (float)(c - (double)c_hi);
+    int down;             // 63 - bits: the sums' unit is 2^-bits
+    __device__ __forceinline__ Weigher(const uint2* t, float largest, float temperature, int bits) : table(t), top(largest), down(63 - bits) {
+        // log2(e) / T in two floats (fp64 has no rate worth the name here: one quotient a thread took 8 us a CTA)
+        constexpr float l_hi = 1.442695040888963407f, l_lo = (float)(1.4426950408889634074 - (double)l_hi);
+        c_hi = l_hi / temperature;
+        c_lo = (fmaf(-c_hi, temperature, l_hi) + l_lo) / temperature;
+    }
+    __device__ __forceinline__ void exponent(float x, float* y, float* yl) const {
+        const float d = x - top, b = d - x, dl = (x - (d - b)) + (-top - b);  // x - top in two floats
+        *y = d * c_hi;
+        *yl = fmaf(d, c_lo, fmaf(dl, c_hi, fmaf(d, c_hi, -*y)));
+    }
+    // Mantissa in [2^31, 2^32) and exponent: weight = mant 2^(e - 31), off by 2^-31 of itself. No probability, or below 2^-200: e < -190.
+    __device__ __forceinline__ void parts(float x, uint32_t* mant, int* e) const {
+        constexpr float kRound = 12582912.0f;  // 1.5 2^23: adding it rounds to an integer, which the low bits hold
+        constexpr int kRoundBits = 0x4B400000;
+        float y, yl;
+        exponent(x, &y, &yl);
+        y = fmaxf(y, -200.0f);   // -inf and NaN (no probability), too: far below the unit
+        const float kf = fmaf(y, (float)kTable, kRound);
+        const int n = __float_as_int(kf) - kRoundBits;
+        const float r = fmaf(kf - kRound, -1.0f / kTable, y) + yl;
+        const float p = r * fmaf(r, 0.240226506959100712f, 0.693147180559945309f);  // (ln 2)^2 / 2, ln 2
+        const uint2 t = table[n & (kTable - 1)];
+        *mant = t.x + (uint32_t)(__float_as_int(fmaf(__uint_as_float(t.y), p, kRound)) - kRoundBits);
+        *e = n >> 10;
+    }
+    // In units of 2^-bits, cut off; 0 for tokens without probability.
+    __device__ __forceinline__ uint64_t operator()(float x) const {
+        uint32_t w;
+        int e;
+        parts(x, &w, &e);
+        const int shift = down - e;   // w 2^-31 2^e in that unit: w 2^32 to the right
+        return shift > 63 ? 0 : ((uint64_t)w << 32) >> shift;
     }
     // mantissa in [2^43, 2^44) and exponent: weight = mant 2^(e - 43). False: below 2^-1000, or no probability.
-    __device__ __forceinline__ bool parts(float x, uint64_t* mant, int* e) const {
-        // x - top in two floats, then times c
-        const float d = x - top, b = d - x, dl = (x - (d - b)) + (-top - b);
-        const float y = d * c_hi;
+    __device__ __noinline__ bool precise(float x, uint64_t* mant, int* e) const {
+        float y, yl;
+        exponent(x, &y, &yl);
         if (!(y > -1000.0f)) return false;
-        const float yl = fmaf(d, c_hi, -y) + fmaf(d, c_lo, dl * c_hi);
         const float k = rintf(y * 256.0f);
         const int n = (int)k;
         const float r = fmaf(k, -1.0f / 256.0f, y);   // exact
         const float a = r * 0.693147180559945309417f;  // ln 2 = this float and the one below
         const float al = fmaf(r, 0.693147180559945309417f, -a) + fmaf(r, -1.904654299957768e-9f, yl * 0.693147180559945309417f);
         const float z = a + al, s = fmaf(z * z, fmaf(z, 1.0f / 6.0f, 0.5f), al);   // al has the exponent's second float, too: up to 2^-19
-        const float2 t = pow[n & 255];
-        const float b1 = t.x * a;
-        const float b2 = fmaf(t.x, s, fmaf(t.y, a, t.y + fmaf(t.x, a, -b1)));
-        // t.x + b1 + b2 in units of 2^-43: |b1| below 2^-8, |b2| below 2^-18
-        *mant = ((uint64_t)((__float_as_uint(t.x) & 0x7FFFFFu) | 0x800000u) << 20) + __float2ll_rn(b1 * 8796093022208.0f) +
+        const float hi = kPowers.hi[n & 255], lo = kPowers.lo[n & 255];
+        const float b1 = hi * a;
+        const float b2 = fmaf(hi, s, fmaf(lo, a, lo + fmaf(hi, a, -b1)));
+        // hi + b1 + b2 in units of 2^-43: |b1| below 2^-8, |b2| below 2^-18
+        *mant = ((uint64_t)((__float_as_uint(hi) & 0x7FFFFFu) | 0x800000u) << 20) + __float2ll_rn(b1 * 8796093022208.0f) +
                 __float2int_rn(b2 * 8796093022208.0f);
         *e = n >> 8;
         return true;
     }
-    __device__ __forceinline__ uint64_t operator()(float x) const {  // in units of 2^-bits, rounded; 0 for tokens without probability
+    __device__ __forceinline__ uint64_t precise_weight(float x) const {  // in units of 2^-bits, rounded
         uint64_t mant;
         int e;
-        if (!parts(x, &mant, &e)) return 0;
-        const int up = e + bits - 43;
+        if (!precise(x, &mant, &e)) return 0;
+        const int up = e + 20 - down;
         return up >= 0 ? mant << up : up < -45 ? 0 : ((mant >> (-up - 1)) + 1) >> 1;
     }
 };
 // floor(f * s) for f in [0, 1] (above: s, below or NaN: 0), s < 2^63.
 __device__ __forceinline__ uint64_t portion(float f, uint64_t s) {
-    if (!(f > 0.0f)) return 0;
-    if (f >= 1.0f) return s;
-    const uint32_t b = __float_as_uint(f), e = b >> 23;
-    const uint64_t m = e ? (b & 0x7FFFFFu) | 0x800000u : (uint64_t)(b & 0x7FFFFFu) << 1;  // f = m 2^(e - 150)
-    const int down = 126 - (int)e;
-    return down >= 64 ? 0 : __umul64hi(m << 40, s) >> down;
+    const uint32_t b = __float_as_uint(fminf(fmaxf(f, 0.0f), 1.0f));
+    const uint32_t m8 = b << 8 | 0x80000000u;   // f = m8 2^(e - 158), but for zero and denormal numbers, whose product is below 1
+    const uint64_t hi = (uint64_t)m8 * (uint32_t)(s >> 32) + (((uint64_t)m8 * (uint32_t)s) >> 32);  // m8 s / 2^32
+    const int down = 126 - (int)(b >> 23);
+    return down > 63 ? 0 : down >= 0 ? hi >> down : s;   // down is -1 for f = 1 alone
 }
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 #pragma unroll
@@ -289,23 +406,34 @@ __device__ __forceinline__ void sync_cluster() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
+// A cluster of one to eight CTAs a sequence; a CTA's part of the vocabulary is cut into segments of kSeg tokens.
 // VEC: the rows of logits and probabilities are 16-byte aligned, so a lane takes 16 bytes of logits at a time, else one element.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kPickThreads) verify_pick_kernel(const __grid_constant__ VerifyParams A) {
-    constexpr int V = VEC ? 16 / (int)sizeof(T) : 1;
-    __shared__ float2 s_pow[256];
-    __shared__ uint64_t s_part[2][kPickWarps], s_all[kAllWarps];
+__global__ void __launch_bounds__(kPickThreads, 4) verify_pick_kernel(const __grid_constant__ VerifyParams A) {
+    constexpr int V = VEC ? 16 / (int)sizeof(T) : 1, kSteps = kSeg / (32 * V), kAhead = kSteps < 4 ? kSteps : 4;
+    extern __shared__ __align__(16) uint64_t s_sum[];   // [segments of the CTA]: what is left of their weights, then ..
+    __shared__ uint2 s_pow[kTable];
+    __shared__ uint64_t s_part[2][3], s_warp[kPickWarps];
     __shared__ int s_stop, s_close;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, seq = blockIdx.x / kPickCluster;
-    const int rank = blockIdx.x - seq * kPickCluster;
-    if (tid < 256) s_pow[tid] = make_float2(kPowers.hi[tid], kPowers.lo[tid]);
+    __shared__ float s_top[kPickWarps], s_row_sum[kPickWarps];  // of the row at which a warp stopped
+    __shared__ int s_best[kPickWarps];
+    uint32_t rank, ranks;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, seq = blockIdx.x / ranks;
+    const int segs = (A.vocab + kSeg - 1) / kSeg, per = (segs + ranks - 1) / ranks;
+    const int seg0 = min((int)rank * per, segs), seg1 = min(seg0 + per, segs);
+    float* s_share = reinterpret_cast<float*>(s_sum + per);  // .. the drafts' probability among those that are left something
+    for (int i = tid; i < kTable; i += kPickThreads) s_pow[i] = make_uint2(kPowers.fix[i], __float_as_uint((float)kPowers.fix[i]));
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int a = __ldcg(A.q_start + seq), b = __ldcg(A.q_start + seq + 1);
     const int start = min(max(a, 0), A.m), n = min(max(b, start), A.m) - start;
+    const float temperature = A.temperature ? __ldcg(A.temperature + seq) : 1.0f;
+    const float u_sample = __ldcg(A.u_sample + seq);
+    const int len = A.seq_lens ? __ldcg(A.seq_lens + seq) : 0;
     const bool writes = rank == 0 && tid == 0;
     if (writes && (start != a || start + n != b)) raise_flag(A.err_flag, Q4K_ERR_SEQ);
-    const int len = A.seq_lens ? __ldcg(A.seq_lens + seq) : 0;
     if (n == 0) {
         if (writes) {
             A.accepted[seq] = 0;
@@ -314,7 +442,6 @@ __global__ void __launch_bounds__(kPickThreads) verify_pick_kernel(const __grid_
         }
         return;
     }
-    const float temperature = A.temperature ? __ldcg(A.temperature + seq) : 1.0f;
     const bool greedy = !(temperature > kGreedy);
     const float c = 1.44269504088896340736f / temperature;
 
@@ -346,34 +473,38 @@ __global__ void __launch_bounds__(kPickThreads) verify_pick_kernel(const __grid_
         return R;
     };
     auto logit = [&](int r, int d) { return tame(one(static_cast<const T*>(A.logits) + (int64_t)r * A.logits_stride + d)); };
-    // u q(d): what p(d) has to exceed
-    auto bar = [&](int r, int d) {
-        const double u = fmaxf(__ldcg(A.u_accept + r), 0.0f);
-        return A.probs ? u * (double)fmaxf(__ldcg(A.probs + (int64_t)r * A.probs_stride + d), 0.0f) : u;
-    };
+    auto chance = [&](int r) { return fmaxf(__ldcg(A.u_accept + r), 0.0f); };
+    auto drafts = [&](int r, int d) { return A.probs ? fmaxf(__ldcg(A.probs + (int64_t)r * A.probs_stride + d), 0.0f) : 1.0f; };
     enum { kYes, kNo, kAsk };
     auto decide = [&](int r) {
-        const Row R = row_of(r);
-        const int d = __ldcg(A.tokens + r + 1);
-        if ((unsigned)d >= (unsigned)A.vocab) {
-            if (rank == 0 && lane == 0) raise_flag(A.err_flag, Q4K_ERR_TOKEN);
+        if (r == start + n - 1) {  // no draft behind it
+            const Row R = row_of(r);
+            if (lane == 0) {
+                s_top[warp] = R.top;
+                s_row_sum[warp] = R.sum;
+                s_best[warp] = R.best;
+            }
             return (int)kNo;
         }
-        const float x = logit(r, d);
-        const double need = bar(r, d);
+        const int d = __ldcg(A.tokens + r + 1);
+        const bool there = (unsigned)d < (unsigned)A.vocab;
+        const float x = there ? logit(r, d) : -INFINITY, u = chance(r), q = there ? drafts(r, d) : 0.0f;
+        const Row R = row_of(r);
+        if (lane == 0) {
+            s_top[warp] = R.top;
+            s_row_sum[warp] = R.sum;
+            s_best[warp] = R.best;
+        }
+        if (!there && rank == 0 && lane == 0) raise_flag(A.err_flag, Q4K_ERR_TOKEN);
         if (x == -INFINITY) return (int)kNo;
-        if (greedy) return (int)(d == R.best && need < 1.0 ? kYes : kNo);
-        if (need == 0.0) return (int)kYes;
-        const float w = ex2((x - R.top) * c);
-        const double l = need * (double)R.sum;
-        if (w < 1e-30f) return (int)kAsk;
-        return (int)(l * (1.0 + kClose) < (double)w ? kYes : l * (1.0 - kClose) >= (double)w ? kNo : kAsk);
+        if (u == 0.0f || q == 0.0f) return (int)(!greedy || d == R.best ? kYes : kNo);
+        const float need = u * q;
+        if (greedy) return (int)(d == R.best && need < 1.0f ? kYes : kNo);
+        const float y = (x - R.top) * c, w = ex2(y), l = need * R.sum, band = closeness(y);
+        if (w < 1e-30f || need < 1e-30f) return (int)kAsk;
+        return (int)(l * (1.0f + band) < w ? kYes : l * (1.0f - band) >= w ? kNo : kAsk);
     };
 
-    // this warp's part of a row, in the order of the tokens: 32 lanes of V at a time
-    const int all_warp = rank * kPickWarps + warp;
-    const int seg = ((A.vocab + kAllWarps - 1) / kAllWarps + 32 * V - 1) / (32 * V) * (32 * V);
-    const int e0 = min(all_warp * seg, A.vocab), e1 = min(e0 + seg, A.vocab);
     auto logits_at = [&](const T* x, int e, float (&v)[V]) {
         if (VEC && e + V <= A.vocab) {
             if constexpr (VEC) unpack<T, V>(__ldcg(reinterpret_cast<const uint4*>(x + e)), v);
@@ -396,40 +527,41 @@ __global__ void __launch_bounds__(kPickThreads) verify_pick_kernel(const __grid_
             for (int k = 0; k < V; ++k) v[k] = e + k < A.vocab ? __ldcg(q + e + k) : 0.0f;
         }
     };
-    // every warp's sum of the cluster's 128, in s_all, and their total
+    // A value of every warp: the CTA's sum, in every thread.
+    auto block_sum = [&](uint64_t v) {
+        v = warp_sum(v);
+        __syncthreads();
+        if (lane == 0) s_warp[warp] = v;
+        __syncthreads();
+        return warp_sum(lane < kPickWarps ? s_warp[lane] : 0);
+    };
+    // Values of every CTA, lane k's those of CTA k.
     int turn = 0;
     bool gathered = false;
-    auto gather = [&](uint64_t mine) {
+    struct Values { uint64_t a, b, c; };
+    auto gather = [&](uint64_t a, uint64_t b, uint64_t c) {
         gathered = true;
-        if (lane == 0) s_part[turn][warp] = mine;
-        sync_cluster();
-        if (tid < kAllWarps) s_all[tid] = peer_u64(&s_part[turn][tid % kPickWarps], tid / kPickWarps);
-        __syncthreads();
-        turn ^= 1;   // written again only after the next gather's barrier
-        uint64_t t = 0;
-        for (int k = lane; k < kAllWarps; k += 32) t += s_all[k];
-        return warp_sum(t);
-    };
-    auto weights_of = [&](const Weigher& W, int r) {
-        const T* x = static_cast<const T*>(A.logits) + (int64_t)r * A.logits_stride;
-        uint64_t t = 0;
-        for (int e = e0 + lane * V; e < e1; e += 32 * V) {
-            float v[V];
-            logits_at(x, e, v);
-#pragma unroll
-            for (int k = 0; k < V; ++k) t += W(tame(v[k]));
+        if (tid == 0) {
+            s_part[turn][0] = a;
+            s_part[turn][1] = b;
+            s_part[turn][2] = c;
         }
-        return warp_sum(t);
+        sync_cluster();
+        Values v{};
+        if (lane < (int)ranks) v = Values{peer_u64(&s_part[turn][0], lane), peer_u64(&s_part[turn][1], lane), peer_u64(&s_part[turn][2], lane)};
+        turn ^= 1;   // written again only after the next gather's barrier
+        return v;
     };
 
-    // how many drafts are accepted
+    // How many drafts are accepted. A decision too close to call in fp32 counts as a rejection until the draw's first pass has
+    // given the row's sum; should the draft pass after all, the search goes on behind it.
     int at = 0;
-    uint64_t whole = 0;      // the row's sum, once it is known
-    bool rejected = false;
-    while (at < n - 1) {
+    bool rejected, asked;
+    Row R;
+    auto search = [&]() {
         if (tid == 0) s_stop = s_close = 0x7FFFFFFF;
         __syncthreads();
-        for (int j = at + warp; j < n - 1; j += kPickWarps) {
+        for (int j = at + warp; j < n; j += kPickWarps) {
             const int said = decide(start + j);
             if (said == kYes) continue;
             if (lane == 0) {
@@ -439,111 +571,213 @@ __global__ void __launch_bounds__(kPickThreads) verify_pick_kernel(const __grid_
             break;
         }
         __syncthreads();
-        const int stop = s_stop, close = s_close;
+        const int by = (s_stop - at) % kPickWarps;
+        R = Row{s_top[by], s_row_sum[by], s_best[by]};
+        at = s_stop;
+        rejected = at < n - 1;
+        asked = rejected && s_close == at;
         __syncthreads();
-        whole = 0;
-        if (stop == 0x7FFFFFFF) {
-            at = n - 1;
-            break;
+    };
+    // The row behind them: a pass over it, which gives every segment's sum and the row's.
+    int r;
+    const T* x;
+    const float* q;
+    int drafted;
+    uint64_t whole, about, left_of, share_of;   // left_of, share_of: of CTA `lane`
+    for (;;) {
+        search();
+        r = start + at;
+        if (R.top == -INFINITY || greedy) {
+            if (writes) {
+                A.accepted[seq] = at;
+                if (A.kept) A.kept[seq] = len - n + 1 + at;
+                A.next[seq] = R.top == -INFINITY ? -1 : R.best;
+                if (R.top == -INFINITY) raise_flag(A.err_flag, Q4K_ERR_TOKEN);
+            }
+            if (gathered) sync_cluster();   // no CTA leaves while another reads its sums
+            return;
         }
-        at = stop;
-        rejected = true;
-        if (close != stop) break;
-        const int r = start + stop, d = __ldcg(A.tokens + r + 1);
-        const Weigher W(s_pow, row_of(r).top, temperature, A.bits);
-        whole = gather(weights_of(W, r));
-        uint64_t mant;
+        const Weigher W(s_pow, R.top, temperature, A.bits);
+        x = static_cast<const T*>(A.logits) + (int64_t)r * A.logits_stride;
+        q = rejected && A.probs ? A.probs + (int64_t)r * A.probs_stride : nullptr;
+        drafted = rejected && !A.probs ? __ldcg(A.tokens + r + 1) : -1;  // only it has nothing left
+        // One pass with the sum S that fp32 gave: what is left is max(w - q S, 0), and where S is off by s, the sum of that over a
+        // segment is off by s times the q of the tokens that are left something (which those are, S decides well enough: a token that
+        // changes sides has next to nothing left). So each segment keeps both sums, and the precise S comes in afterwards.
+        about = __float2ull_rn(R.sum * __int_as_float((127 + A.bits) << 23));
+        uint64_t cta_whole = 0, cta_left = 0, cta_share = 0;   // shares in units of 2^-40
+        for (int sg = seg0 + warp; sg < seg1; sg += kPickWarps) {
+            uint64_t all = 0, left = 0;
+            float share = 0.0f;
+#pragma unroll
+            for (int i0 = 0; i0 < kSteps; i0 += kAhead) {
+                float v[kAhead][V], p[kAhead][V];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const int e = sg * kSeg + (i0 + i) * 32 * V + lane * V;
+                    logits_at(x, e, v[i]);
+                    if (q) probs_at(q, e, p[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                    for (int k = 0; k < V; ++k) {
+                        const uint64_t w = W(fminf(v[i][k], kLargest));   // (-inf and NaN it takes as they are)
+                        all += w;
+                        if (q) {
+                            const uint64_t away = portion(p[i][k], about);
+                            if (w > away) {
+                                left += w - away;
+                                share += fmaxf(p[i][k], 0.0f);
+                            }
+                        } else if (sg * kSeg + (i0 + i) * 32 * V + lane * V + k != drafted) {
+                            left += w;
+                        }
+                    }
+            }
+            all = warp_sum(all);
+            left = warp_sum(left);
+            if (q) {
+#pragma unroll
+                for (int o = 16; o; o >>= 1) share += __shfl_xor_sync(0xffffffffu, share, o);
+            }
+            if (lane == 0) {
+                s_sum[sg - seg0] = left;
+                s_share[sg - seg0] = share;
+                cta_whole += all;
+                cta_left += left;
+                cta_share += __float2ull_rn(share * 1099511627776.0f);
+            }
+        }
+        const uint64_t a0 = block_sum(cta_whole), b0 = block_sum(cta_left), c0 = block_sum(cta_share);
+        const Values sums = gather(a0, b0, c0);
+        whole = warp_sum(sums.a);
+        left_of = sums.b;
+        share_of = sums.c;
+        if (!asked) break;
+        // u q(d) S against w(d)
+        const int d = __ldcg(A.tokens + r + 1);
+        uint32_t m32;
         int e;
-        const bool some = W.parts(logit(r, d), &mant, &e);
-        if (!some || !(bar(r, d) * (double)whole < scalbn((double)mant, e + A.bits - 43))) break;
-        rejected = false;
-        whole = 0;
+        W.parts(logit(r, d), &m32, &e);
+        const double need = (double)chance(r) * (double)drafts(r, d), l = need * (double)whole, w = scalbn((double)m32, e + A.bits - 31);
+        bool passes = l < w;
+        if (!(fabs(l - w) > kCloseFine * w) || e < -190) {  // closer still (or a draft below 2^-190): all to 2^-41
+            uint64_t sum = 0, mant;
+#pragma unroll 1
+            for (int i = seg0 * kSeg + tid; i < min(seg1 * kSeg, A.vocab); i += kPickThreads) sum += W.precise_weight(tame(one(x + i)));
+            const uint64_t fine = warp_sum(gather(block_sum(sum), 0, 0).a);
+            passes = W.precise(logit(r, d), &mant, &e) && need * (double)fine < scalbn((double)mant, e + A.bits - 43);
+        }
+        if (!passes) break;
         ++at;
+        __syncthreads();
     }
-    // the token after them
-    const int r = start + at;
-    const Row R = row_of(r);
+    const Weigher W(s_pow, R.top, temperature, A.bits);
     if (writes) {
         A.accepted[seq] = at;
         if (A.kept) A.kept[seq] = len - n + 1 + at;
     }
-    if (greedy || R.top == -INFINITY) {
-        if (writes) {
-            A.next[seq] = R.top == -INFINITY ? -1 : R.best;
-            if (R.top == -INFINITY) raise_flag(A.err_flag, Q4K_ERR_TOKEN);
-        }
-        if (gathered) sync_cluster();   // no CTA leaves while another reads its sums
-        return;
-    }
-    const Weigher W(s_pow, R.top, temperature, A.bits);
-    __syncthreads();   // s_pow, where no draft was looked at
-    if (!whole) whole = gather(weights_of(W, r));
-    const T* x = static_cast<const T*>(A.logits) + (int64_t)r * A.logits_stride;
-    const float* q = A.probs ? A.probs + (int64_t)r * A.probs_stride : nullptr;
-    const int drafted = rejected ? __ldcg(A.tokens + r + 1) : -1;
-    // what is left of a token's weight
-    bool minus = rejected;
-    auto left = [&](int e, float y, float qe) {
-        const uint64_t w = W(tame(y));
-        if (!minus) return w;
-        if (!q) return e == drafted ? (uint64_t)0 : w;
-        const uint64_t away = portion(qe, whole);
-        return w > away ? w - away : (uint64_t)0;
+    // what is left, with the precise S: of the CTAs, and of this one's segments as they are looked at
+    const float off = q ? (float)(int64_t)(whole - about) : 0.0f;
+    auto corrected = [&](uint64_t left, float share) {
+        const int64_t v = (int64_t)left - __float2ll_rn(off * share);
+        return v > 0 ? (uint64_t)v : 0;
     };
-    uint64_t rest = whole;
-    if (rejected) {
-        uint64_t t = 0;
-        for (int e = e0 + lane * V; e < e1; e += 32 * V) {
-            float v[V], p[V];
-            logits_at(x, e, v);
-            if (q) probs_at(q, e, p);
-#pragma unroll
-            for (int k = 0; k < V; ++k) t += left(e + k, v[k], q ? p[k] : 0.0f);
-        }
-        rest = gather(warp_sum(t));
-        if (rest == 0) {   // nothing is left: from the distribution itself
-            minus = false;
-            rest = gather(weights_of(W, r));
-        }
-    }
-    // the first token whose cumulative sum exceeds u * rest: the warp that holds it, then its place there
-    const uint64_t goal = min(portion(__ldcg(A.u_sample + seq), rest), rest - 1);
-    uint64_t before = 0;
-    for (int k = lane; k < all_warp; k += 32) before += s_all[k];
-    before = warp_sum(before);
-    if (goal >= before && goal - before < s_all[all_warp]) {
-        for (int base = e0; base < e1; base += 32 * V) {
-            const int e = base + lane * V;
-            float v[V], p[V];
-            uint64_t w[V], own = 0;
-            logits_at(x, e, v);
-            if (q) probs_at(q, e, p);
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                w[k] = e + k < e1 ? left(e + k, v[k], q ? p[k] : 0.0f) : 0;
-                own += w[k];
+    left_of = corrected(left_of, (float)share_of * 9.094947e-13f);
+    bool minus = rejected;
+    if (!__any_sync(0xffffffffu, left_of != 0)) {
+        // nothing is left: from the distribution itself
+        minus = false;
+        uint64_t cta_left = 0;
+        for (int sg = seg0 + warp; sg < seg1; sg += kPickWarps) {
+            uint64_t t = 0;
+#pragma unroll 1
+            for (int e = sg * kSeg + lane; e < min((sg + 1) * kSeg, A.vocab); e += 32) t += W(tame(one(x + e)));
+            t = warp_sum(t);
+            if (lane == 0) {
+                s_sum[sg - seg0] = t;
+                cta_left += t;
             }
-            uint64_t inc = own;
+        }
+        left_of = gather(block_sum(cta_left), 0, 0).a;
+    }
+    const uint64_t rest = warp_sum(left_of), cta_before = warp_sum(lane < (int)rank ? left_of : 0);
+    const uint64_t cta_rest = __shfl_sync(0xffffffffu, left_of, (int)rank);
+    // the first token whose cumulative sum exceeds u * rest: the CTA's segment that holds it, then its place there
+    const uint64_t goal = min(portion(u_sample, rest), rest - 1);
+    if (goal >= cta_before && goal - cta_before < cta_rest) {
+        // every warp finds the segment, then takes a part of it: its tokens' sums, then the place in the part that holds the goal
+        uint64_t before = cta_before;
+        int sg = -1, last_sg = 0;   // last_sg: the last with something left, should rounding leave the goal behind all of them
+        for (int base = 0; base < seg1 - seg0 && sg < 0; base += 32) {
+            const uint64_t v = base + lane >= seg1 - seg0 ? 0
+                               : minus && q              ? corrected(s_sum[base + lane], s_share[base + lane])
+                                                         : s_sum[base + lane];
+            uint64_t inc = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o) inc += y;
             }
-            const unsigned hit = __ballot_sync(0xffffffffu, before + inc > goal);
+            const unsigned hit = __ballot_sync(0xffffffffu, before + inc > goal), some = __ballot_sync(0xffffffffu, v != 0);
+            if (some) last_sg = base + 31 - __clz(some);
             if (hit) {
-                if (lane == __ffs(hit) - 1) {
-                    uint64_t cum = before + inc - own;
-                    int found = -1;
-#pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        cum += w[k];
-                        if (found < 0 && cum > goal) found = e + k;
-                    }
-                    A.next[seq] = found;
-                }
-                break;
+                const int src = __ffs(hit) - 1;
+                sg = base + src;
+                before += __shfl_sync(0xffffffffu, inc - v, src);
+            } else {
+                before += __shfl_sync(0xffffffffu, inc, 31);
             }
-            before += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        const bool past = sg < 0;
+        sg = seg0 + (past ? last_sg : sg);
+        constexpr int kMine = kSeg / kPickThreads;   // tokens of a lane, one after another
+        const int e = sg * kSeg + (warp * 32 + lane) * kMine;
+        uint64_t w[kMine], own = 0;
+        int mine = -1;
+#pragma unroll
+        for (int k = 0; k < kMine; ++k) {
+            w[k] = e + k < A.vocab ? W(tame(one(x + e + k))) : 0;
+            if (minus && q) {
+                const uint64_t away = e + k < A.vocab ? portion(__ldcg(q + e + k), whole) : 0;
+                w[k] = w[k] > away ? w[k] - away : 0;
+            } else if (minus && e + k == drafted) {
+                w[k] = 0;
+            }
+            if (w[k]) mine = e + k;
+            own += w[k];
+        }
+        uint64_t inc = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) s_warp[warp] = inc;
+        mine = __reduce_max_sync(0xffffffffu, mine);
+        if (lane == 0) s_best[warp] = mine;
+        __syncthreads();
+        const uint64_t part = lane < kPickWarps ? s_warp[lane] : 0;
+        before += warp_sum(lane < warp ? part : 0);
+        const unsigned hit = __ballot_sync(0xffffffffu, !past && before + inc > goal);
+        const uint64_t end = before + __shfl_sync(0xffffffffu, inc, 31);
+        if (hit && before <= goal) {
+            if (lane == __ffs(hit) - 1) {
+                uint64_t cum = before + inc - own;
+                int found = -1;
+#pragma unroll
+                for (int k = 0; k < kMine; ++k) {
+                    cum += w[k];
+                    if (found < 0 && cum > goal) found = e + k;
+                }
+                A.next[seq] = found;
+            }
+        } else if (warp == kPickWarps - 1 && lane == 0 && (past || end <= goal)) {
+            int last = -1;
+#pragma unroll
+            for (int k = 0; k < kPickWarps; ++k) last = max(last, s_best[k]);
+            A.next[seq] = last >= 0 ? last : R.best;
         }
     }
     sync_cluster();
@@ -566,7 +800,6 @@ cudaError_t launch_typed(const VerifyParams& P, cudaStream_t stream) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kPickCluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -574,8 +807,15 @@ cudaError_t launch_typed(const VerifyParams& P, cudaStream_t stream) {
         const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_stats_kernel<T>, P);
         if (e != cudaSuccess) return e;
     }
-    cfg.gridDim = dim3((unsigned)P.batch * kPickCluster);
+    // Up to eight CTAs a sequence, four an SM at once, and not many more than twice that in all: a CTA's chain of reads and barriers is
+    // some microseconds long, whatever its part of the vocabulary.
+    int ranks = kMostCluster;
+    while (ranks > 1 && (int64_t)P.batch * ranks > 8 * 152) ranks /= 2;
+    attr[1].val.clusterDim.x = ranks;
+    const int segs = (P.vocab + kSeg - 1) / kSeg, per = (segs + ranks - 1) / ranks;
+    cfg.gridDim = dim3((unsigned)P.batch * ranks);
     cfg.blockDim = dim3(kPickThreads);
+    cfg.dynamicSmemBytes = (size_t)per * (sizeof(uint64_t) + sizeof(float));  // 24 KB at most
     cfg.numAttrs = 2;
     const auto even = [](const void* p, int64_t stride, int size) {
         return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride * size % 16 == 0;
@@ -598,8 +838,8 @@ cudaError_t launch_verify(const void* logits, int dtype, int m, int vocab, int64
     P.u_accept = u_accept; P.u_sample = u_sample; P.accepted = accepted; P.next = next; P.kept = kept;
     P.stats = static_cast<float4*>(workspace);
     P.batch = batch; P.m = m; P.vocab = vocab; P.chunks = chunks_of(m, vocab); P.err_flag = err_flag;
-    P.bits = 63;
-    while ((int64_t)1 << (63 - P.bits) < vocab) --P.bits;
+    P.bits = 62;
+    while ((int64_t)1 << (62 - P.bits) < vocab) --P.bits;
     return dtype == Q4K_F32 ? launch_typed<float>(P, stream) : launch_typed<__nv_bfloat16>(P, stream);
 }
 

@@ -1,9 +1,9 @@
 """GPU tests of q4k_verify_drafts against a walk over the sequences in extended precision (numpy's long double). The
-results are whole numbers: equal or wrong, but for a draw next to a border between tokens. A weight is off by 2^-41 of itself
-(its exponent, up to 64, by 2^-46 of itself, the fourth term of the exponential below 2^-42, three roundings of 2^-44), and its rounding
-to the sums' unit of 2^-b of the largest weight, b = 63 - ceil(log2 n), by half of that. So a cumulative sum of n weights is off by at
-most E = 2^-41 + n 2^-(b + 1) of the whole, which is not less than the largest weight; what is taken away for a draft,
-another sum's share, brings it to 2 E, and the goal, a share of the whole, to 4 E. In acceptances a random number within 2^-36 of the
+results are whole numbers: equal or wrong, but for a draw next to a border between tokens. A weight is off by 2^-31 of itself
+(half a unit of 2^-31 in a table of powers and half in the product with the rest of the exponent), and, cut to the sums' unit of 2^-b
+of the largest weight, b = 62 - ceil(log2 n), by that. So a cumulative sum of n weights is off by at
+most E = 2^-31 + n 2^-b of the whole, which is not less than the largest weight; what is taken away for a draft,
+another sum's share, brings it to 2 E, and the goal, a share of the whole, to 4 E. (Acceptances are decided to 2^-41.) In acceptances a random number within 2^-36 of the
 border is not expected from the seeds here; the reference says so if one comes."""
 import math
 
@@ -86,7 +86,7 @@ def plain(x, probs, tokens, start, temperature, u_accept, u_sample, lens, strict
         at = min(int(np.searchsorted(cum, goal, side="right")), int(np.nonzero(rest)[0][-1]))
         if drawn is not None and drawn[i] != at:   # next to a border?
             j, n = drawn[i], len(p)
-            e = 4 * (2.0 ** -41 + n * 2.0 ** -(64 - math.ceil(math.log2(n))))   # p sums to 1
+            e = 4 * (2.0 ** -31 + n * 2.0 ** -(62 - math.ceil(math.log2(n))))   # p sums to 1
             if 0 <= j < n and rest[j] > 0 and cum[j] - rest[j] - e <= goal <= cum[j] + e:
                 at = j
         nxt.append(at)
