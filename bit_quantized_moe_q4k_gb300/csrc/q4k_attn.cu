@@ -53,6 +53,7 @@ constexpr int kLeast = 4;                      // units of a cluster's part of a
 constexpr int kMaxParts = 512;                // CTAs that the workspace serves
 constexpr int kJoinCost = 8;                  // units that joining a tile is worth (16: 8000 tokens 15.4 -> 17.5 us)
 static_assert(kJoinCost >= kLeast, "a tile that is shared has a unit for each cluster");
+constexpr int kListed = 16;                   // units up to which a tile is taken whole from the plan's list, whatever a CTA's share
 constexpr int kOneLevel = 16;                 // up to this many pieces of a tile are joined at once (4: 16000 tokens 17 -> 21 us)
 constexpr int kTickets = 2 * kMaxParts;       // arrival counters before the partial results: by group of pieces, by tile
 
@@ -334,45 +335,26 @@ __device__ __forceinline__ float scale_log2_of(float s) {
     return (b & 0x7FFFFFu) ? e + log2f(__uint_as_float((b & 0x7FFFFFu) | 0x3F800000u)) : e;
 }
 
-// The shared part of a query row, joined to its own one (sums acc and denominator den, relative to 2^ref): `place` holds its first
-// slot, how many there are, and its row in them. V: the dims of a thread, from dim c.
-__device__ __forceinline__ void scale_by(float& a, float w) { a *= w; }
-__device__ __forceinline__ void scale_by(float4& a, float w) { a.x *= w; a.y *= w; a.z *= w; a.w *= w; }
-__device__ __forceinline__ void add_times(float& a, float w, float x) { a = fmaf(w, x, a); }
-__device__ __forceinline__ void add_times(float4& a, float w, const float4& x) {
-    a.x = fmaf(w, x.x, a.x); a.y = fmaf(w, x.y, a.y); a.z = fmaf(w, x.z, a.z); a.w = fmaf(w, x.w, a.w);
-}
-template <int D, typename V>
-__device__ __forceinline__ void join_shared(const PrefixPlan& P, const int4& place, int c, V& acc, float& den, float ref) {
-    constexpr int kAtOnce = 4;
-#pragma unroll 1
-    for (int k0 = 0; k0 < place.y; k0 += kAtOnce) {
-        float2 f[kAtOnce];
-        V x[kAtOnce];
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-            const int64_t at = (int64_t)(place.x + min(k0 + k, place.y - 1)) * P.tile_rows + place.z;
-            f[k] = __ldcg(P.refs + at);
-            x[k] = __ldcg(reinterpret_cast<const V*>(P.sums + at * D + c));
-        }
-        float top = ref;
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, f[k].x);
-        const float use = top == -INFINITY ? 0.0f : top, keep = ex2(ref - use);
-        scale_by(acc, keep);
-        den *= keep;
-        ref = top;
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-            if (k0 + k >= place.y) continue;
-            const float w = ex2(f[k].x - use);
-            den = fmaf(w, f[k].y, den);
-            add_times(acc, w, x[k]);
-        }
-    }
-}
 // What P and so the sums of a tile are relative to, for the running maximum m (x - reference is 15 at most).
 __device__ __forceinline__ float reference(float m) { return m == -INFINITY ? m : __fadd_ru(m, -15.0f); }
+
+// The (row tile, kv head) `t` of the plan's list: false past the last.
+__device__ __forceinline__ bool listed_tile(const AttnParams& A, int64_t t, int tiles, Cursor* c, TilePart* p) {
+    const int64_t i = t / A.kv_heads;
+    if (i >= tiles) return false;
+    const int4* at = reinterpret_cast<const int4*>(A.pre.own + i);
+    const int4 a = __ldcg(at), b = __ldcg(at + 1);
+    c->seq = min(max(a.x, 0), A.B.batch - 1);   // (not believed as far as addresses go: the workspace may be written over)
+    c->w.s.start = min(max(a.y, 0), A.B.m);
+    c->w.s.n = min(max(a.z, 0), A.B.m - c->w.s.start);
+    c->w.s.len = min(max(a.w, 0), A.B.max_pages << A.B.page_shift);
+    c->w.lo = max(b.x, 0) & ~(kChunk - 1);
+    c->w.units = b.y;
+    p->index = b.z * A.kv_heads + (int)(t - i * A.kv_heads);
+    p->k = 1;
+    p->j = 0;
+    return true;
+}
 
 // RT: query rows of a tile. fp32: 8 (two fp16 terms fill the 16 rows); bf16: 8 where a tile has no
 // more rows, else 16.
@@ -387,7 +369,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
     __shared__ float s_m[kAttnWarps * RT], s_l[kAttnWarps * RT];
     __shared__ ChunkMeta s_meta[kAttnWarps][kRing * kPair];
     // With SH the kernel before computes the shared part and began when all before it had ended (it waited for the plan's
-    // kernel): only its results have to be waited for, when they are joined.
+    // kernel). This one reads nothing of it and runs beside it.
     if constexpr (!SH) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -403,9 +385,27 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
     __shared__ int s_pieces;
     __shared__ TilePart s_tile;
     __shared__ bool s_by_tile;
-    __shared__ int4 s_pre[SH ? RT : 1];  // where the shared part of each row is
+    __shared__ bool s_shares;            // the tile's sequence shares a part, which is joined to these sums afterwards
     __shared__ struct { int c0, slot0, size, groups, first, count, last; } s_join;
-    if (warp == 0) {
+    // Behind shared prefixes the plan has a list of the row tiles. While no tile is much longer than a CTA's share of the work, the CTAs
+    // take whole ones from it, each the next that is left as it has done with one.
+    int list = 0;
+    if constexpr (SH && CL == 1) {
+        const int4 h = __ldcg(reinterpret_cast<const int4*>(&A.pre.head->ctas));
+        const int64_t load = __ldcg(&A.pre.head->own_units) / gridDim.x;
+        list = h.z <= max((int64_t)kListed, load) ? min(max(h.y, 0), (int)min(A.pre.owns, (int64_t)0x7FFFFFFF)) : 0;
+    }
+    if (SH && CL == 1 && list > 0) {
+        if (threadIdx.x == 0) {
+            Cursor c{};
+            TilePart p{};
+            s_u[0] = 0;
+            s_u[1] = listed_tile(A, blockIdx.x, list, &c, &p);
+            s_cur = c;
+            s_tile = p;
+            s_by_tile = true;
+        }
+    } else if (warp == 0) {
         const SeqWork mine = seq_work<RT, CL, SH>(A, lane);
         int longest = mine.units;
         int64_t tiles = (int64_t)mine.tiles * A.kv_heads;
@@ -458,6 +458,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
     while (s_u[0] < s_u[1]) {
         const SeqSpan sp = s_cur.w.s;
         const int w_lo = s_cur.w.lo, seq = s_cur.seq;
+        unsigned taken = 0;  // the tile after this one: asked for now, looked at when this one is done
+        if (SH && CL == 1 && list > 0 && threadIdx.x == 0) taken = atomicAdd(&A.pre.head->next, 1u);
         int tile, head, ua, ub, step = 0;
         const bool by_tile = CL > 1 || s_by_tile;
         if (by_tile) {
@@ -575,20 +577,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                 s_meta[warp][k % kRing * kPair + c] = ChunkMeta{ah.ks0, scale_log2_of(ah.vs0), 1.0f / ah.vs0, ah.p0 >= 0};
         };
         for (int k = 0; k < kRing; ++k) issue(k);
-        if (SH && warp == 2 && lane < RT) {
-            const int row = tile * RT + lane, group = __ldcg(A.pre.seq + seq).x;
-            int4 place = make_int4(0, 0, 0, 0);
-            if (row < rows && group >= 0 && group < A.pre.groups) {
-                const PrefixGroup* G = A.pre.group + group;
-                const int r = max(sp.start - __ldcg(&G->row0), 0) * A.group + row, row_tile = r / A.pre.tile_rows;
-                const int64_t item = __ldcg(&G->item0) + (int64_t)row_tile * A.kv_heads + head;
-                // (a plan that another call on this workspace has written over leads to no place outside it)
-                const int2 p = item >= 0 && item < A.pre.items ? __ldcg(A.pre.piece + item) : make_int2(0, 0);
-                if (p.x >= 0 && p.y > 0 && p.y <= kPrefixCtas && p.x + p.y <= A.pre.slots)
-                    place = make_int4(p.x, p.y, r - row_tile * A.pre.tile_rows, 0);
-            }
-            s_pre[lane] = place;
-        }
+        if (SH && threadIdx.x == 64) s_shares = __ldcg(A.pre.seq + seq).x >= 0;
         scales_of(ah.p0, ah.ks0, ah.vs0);
         scales_of(ah.p1, ah.ks1, ah.vs1);
 
@@ -876,7 +865,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                 }
             }
         }
-        if constexpr (SH) asm volatile("griddepcontrol.wait;" ::: "memory");
         // join the warps: each row's maximum, then the weighted sums
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
@@ -902,10 +890,19 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
         // a tile that begins in this piece, but not at its start, goes to the second slot
         constexpr int kPart = RT * (D + 2);
         float* part = A.part + ((int64_t)my_piece * 2 + (not_first ? 1 : 0)) * kPart;
-        auto store_row = [&](int r, int c, float4 acc, float den, float m) {
+        // The row's place among all query rows, for sums that are joined to the shared part's.
+        auto leave = [&](int row, int c, float den, float m) {
+            const int64_t at = (int64_t)(sp.start + row / A.group) * A.kv_heads * A.group + head * A.group + row % A.group;
+            if (c == 0) A.pre.own_refs[at] = make_float2(reference(m), den);
+            return A.pre.own_sums + at * D + c;
+        };
+        auto store_row = [&](int r, int c, const float4& acc, float den, float m) {
             const int row = tile * RT + r;
             if (row >= rows) return;
-            if constexpr (SH) join_shared<D>(A.pre, s_pre[r], c, acc, den, reference(m));
+            if (SH && s_shares) {
+                *reinterpret_cast<float4*>(leave(row, c, den, m)) = acc;
+                return;
+            }
             const float iv = den == 0.0f ? 0.0f : 1.0f / den;  // 0: the row sees nothing
             const float y[4] = {acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv};
             Vec<T>::store(static_cast<T*>(A.out) + (int64_t)(sp.start + row / A.group) * A.out_stride +
@@ -980,7 +977,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                         part[RT * D + RT + r] = den;
                     }
                 } else if (const int row = tile * RT + r; row < rows) {
-                    if constexpr (SH) join_shared<D>(A.pre, s_pre[r], c, acc, den, reference(m));
+                    if (SH && s_shares) {
+                        *leave(row, c, den, m) = acc;
+                        continue;
+                    }
                     const float y = den == 0.0f ? 0.0f : acc / den;  // 0: the row sees nothing
                     T* o = static_cast<T*>(A.out) + (int64_t)(sp.start + row / A.group) * A.out_stride +
                            (int64_t)(head * A.group + row % A.group) * D + c;
@@ -1051,7 +1051,15 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
         }
         not_first = true;
         sync_all<CL>();  // what lies over the rings has been read, by the cluster too
-        if (by_tile) {
+        if (SH && CL == 1 && list > 0) {
+            if (threadIdx.x == 0) {
+                Cursor c{};
+                TilePart p{};
+                s_u[1] = listed_tile(A, (int64_t)gridDim.x + taken, list, &c, &p);
+                s_cur = c;
+                s_tile = p;
+            }
+        } else if (by_tile) {
             if (!s_tile.more) break;
             if (warp == 0) {
                 Cursor c{};
@@ -1180,12 +1188,15 @@ cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int6
                                                       out_stride, err_flag, stream);
         if (e != cudaSuccess || !few) return e;
     }
+    // bf16: tiles of 8 rows where a sequence's rows fit one (half the softmax), else 16; next to prompts
+    // the other sequences mostly decode
+    const int own_rows = dtype == Q4K_F32 || (prompts ? q_heads / kv_heads : most) <= 8 ? 8 : 16;
     AttnParams P{};
     if (shared) {
         const cudaError_t e = launch_prefix(B, q, dtype, q_stride, q_heads, kv_heads, head_dim, k_cache, v_cache, k_scale, v_scale,
                                             shared->group_start, shared->prefix_lens, shared->groups, shared->max_prefix,
-                                            prompts ? kFewRows : 0x7FFFFFFF, scale, window, shared->workspace, err_flag, &P.pre,
-                                            stream);
+                                            prompts ? kFewRows : 0x7FFFFFFF, own_rows, scale, window, shared->workspace, err_flag,
+                                            &P.pre, stream);
         if (e != cudaSuccess) return e;
     }
     P.B = B; P.q = q; P.out = out; P.q_stride = q_stride; P.out_stride = out_stride;
@@ -1198,16 +1209,17 @@ cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int6
     P.parts = num_sms() * kCtasPerSm < kMaxParts ? num_sms() * kCtasPerSm : kMaxParts;
     P.err_flag = err_flag;
     P.max_rows = prompts ? kFewRows : 0x7FFFFFFF;
+    auto own = [&](cudaError_t e) {  // joined to what is shared
+        return e != cudaSuccess || !shared ? e : launch_prefix_join(B, dtype, q_heads, kv_heads, head_dim, P.pre, out, out_stride, stream);
+    };
     const int64_t rows = prompts ? kFewRows : most;  // of a sequence, per kv head
     if (dtype == Q4K_F32)
-        return head_dim == 64 ? launch_typed<float, 64, 8>(P, rows, max_len, stream) : launch_typed<float, 128, 8>(P, rows, max_len, stream);
-    // bf16: tiles of 8 rows where a sequence's rows fit one (half the softmax), else 16; next to prompts
-    // the other sequences mostly decode
-    if ((prompts ? P.group : most) <= 8)
-        return head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 8>(P, rows, max_len, stream)
-                              : launch_typed<__nv_bfloat16, 128, 8>(P, rows, max_len, stream);
-    return head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 16>(P, rows, max_len, stream)
-                          : launch_typed<__nv_bfloat16, 128, 16>(P, rows, max_len, stream);
+        return own(head_dim == 64 ? launch_typed<float, 64, 8>(P, rows, max_len, stream) : launch_typed<float, 128, 8>(P, rows, max_len, stream));
+    if (own_rows == 8)
+        return own(head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 8>(P, rows, max_len, stream)
+                                  : launch_typed<__nv_bfloat16, 128, 8>(P, rows, max_len, stream));
+    return own(head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 16>(P, rows, max_len, stream)
+                              : launch_typed<__nv_bfloat16, 128, 16>(P, rows, max_len, stream));
 }
 
 }  // namespace q4k

@@ -69,8 +69,10 @@ size_t prefix_workspace_bytes(int batch, int groups, int m, int q_heads, int kv_
 cudaError_t launch_prefix(const PagedBatch& B, const void* q, int dtype, int64_t q_stride, int q_heads, int kv_heads,
                           int head_dim, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
                           const float* v_scale, const int32_t* group_start, const int32_t* prefix_lens, int groups,
-                          int max_prefix, int max_rows, float scale, int window, void* workspace, int* err_flag,
-                          PrefixPlan* plan, cudaStream_t stream);
+                          int max_prefix, int max_rows, int own_rows, float scale, int window, void* workspace,
+                          int* err_flag, PrefixPlan* plan, cudaStream_t stream);
+cudaError_t launch_prefix_join(const PagedBatch& B, int dtype, int q_heads, int kv_heads, int head_dim, const PrefixPlan& plan,
+                               void* out, int64_t out_stride, cudaStream_t stream);
 struct SharedPrefix {  // what launch_attention needs of it besides the batch
     const int32_t *group_start, *prefix_lens;
     int groups, max_prefix;

@@ -3,7 +3,8 @@
 //
 //   out_r = (sum over shared j + sum over own j) P_j v_j / (the same of P_j),
 // a sum of two parts that are each relative to a reference of their own, 2^(x - M), and joined by 2^(M_part - M).
-// The shared part is made here, the sequences' own one by q4k_attn.cu, which joins them as it stores.
+// The shared part is made here, the sequences' own one by q4k_attn.cu, which runs beside it where SMs are free; prefix_join_kernel joins
+// them. (Joined by the own part's kernel as it stored, each tile waited for the shared part and then took 7 us more.)
 //
 // prefix_plan_kernel lays the work out (q4k_prefix.cuh): one CTA, since it has to see every group before it can cut the line.
 // prefix_kernel<D> (fp32 rows, 128 a row tile) and prefix2_kernel<D> (bf16, 256) then are the prompt kernels of
@@ -20,74 +21,94 @@ using namespace tc;
 namespace {
 
 // ---- the plan -----------------------------------------------------------------------------------------------------
-constexpr int kPlanThreads = 512;
+constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanSeqs = 2048, kPlanGroups = 128;  // whose lengths, and plans, are looked up in shared memory
+// Units that a piece's start and end are worth, and a CTA's second piece costs it.
+constexpr int kPieceCost = 8;
 
 struct PlanParams {
     PagedBatch B;
     const int32_t *group_start, *prefix_lens;
     PrefixPlan plan;
     int kv_heads, rep, window, max_rows;
+    int own_rows;   // of the sequences' row tiles
     int* err_flag;
 };
 
-__device__ __forceinline__ int64_t block_exclusive(int64_t v, int64_t* total, int64_t* s_warp) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ int64_t warp_exclusive(int64_t v, int64_t* total) {
+    const int lane = threadIdx.x & 31;
     int64_t inc = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += x;
     }
-    if (lane == 31) s_warp[warp] = inc;
-    __syncthreads();
-    const int64_t x = lane < kPlanThreads / 32 ? s_warp[lane] : 0;
-    int64_t before = lane < warp ? x : 0, all = x;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        before += __shfl_xor_sync(0xffffffffu, before, o);
-        all += __shfl_xor_sync(0xffffffffu, all, o);
-    }
-    __syncthreads();
-    *total = all;
-    return before + inc - v;
+    *total = __shfl_sync(0xffffffffu, inc, 31);
+    return inc - v;
 }
 
-// Piece c of `ctas` begins at unit c * units / ctas.
+// Piece c of `ctas` of the line begins at unit c * units / ctas.
 __device__ __forceinline__ int64_t cut(int64_t units, int ctas, int64_t c) { return units * c / ctas; }
 __device__ __forceinline__ int piece_of(int64_t units, int ctas, int64_t u) {  // the last c with cut(c) <= u
     return (int)(((u + 1) * ctas - 1) / units);
 }
 
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ PlanParams A) {
-    __shared__ int64_t s_warp[32];
+    __shared__ int64_t s_own_units[kPlanWarps];
+    __shared__ int s_own[kPlanWarps], s_own_longest[kPlanWarps];
+    __shared__ PrefixHead s_head;
+    __shared__ int s_start[kPlanSeqs + 1], s_len[kPlanSeqs], s_from[kPlanSeqs];
+    __shared__ PrefixGroup s_group[kPlanGroups];
+    __shared__ int s_each;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int groups = A.plan.groups, batch = A.B.batch, shift = A.B.page_shift;
+    const int groups = A.plan.groups, batch = A.B.batch, shift = A.B.page_shift, cap = A.B.max_pages << shift;
+    const bool near = batch <= kPlanSeqs;
+    PrefixGroup* const plan = groups <= kPlanGroups ? s_group : A.plan.group;  // while it is made
     // Starts that do not rise would let groups share rows: then nothing is shared.
     bool bad = false;
     for (int i = tid; i < batch; i += kPlanThreads) {
-        const int a = __ldcg(A.B.q_start + i), b = __ldcg(A.B.q_start + i + 1);
+        const int a = __ldcg(A.B.q_start + i), b = __ldcg(A.B.q_start + i + 1), l = __ldcg(A.B.seq_lens + i);
         if (a < 0 || b < a || b > A.B.m) bad = true;
+        if (near) {
+            s_start[i] = a;
+            if (i == batch - 1) s_start[batch] = b;
+            s_len[i] = l;
+            s_from[i] = 0;
+        }
         A.plan.seq[i] = make_int2(-1, 0);
     }
     for (int g = tid; g < groups; g += kPlanThreads) {
         const int a = __ldcg(A.group_start + g), b = __ldcg(A.group_start + g + 1), p = __ldcg(A.prefix_lens + g);
         if (a < 0 || b < a || b > batch) bad = true;
-        if (p < 0 || p > (A.B.max_pages << shift)) raise_flag(A.err_flag, Q4K_ERR_SEQ);
+        if (p < 0 || p > cap) raise_flag(A.err_flag, Q4K_ERR_SEQ);
+        plan[g].leader = a;
+        plan[g].n = b;
+        plan[g].from = min(max(p, 0), cap);
     }
     if (bad) raise_flag(A.err_flag, Q4K_ERR_SEQ);
-    const bool none = __syncthreads_or(bad) != 0;  // the sequences' entries are written, too
+    const bool none = __syncthreads_or(bad) != 0;  // what the threads wrote is seen by all, too
+    auto span = [&](int i) {  // seq_span of the batch
+        if (!near) {
+            bool odd;
+            return seq_span(A.B, i, &odd);
+        }
+        SeqSpan s;
+        s.start = min(max(s_start[i], 0), A.B.m);
+        s.n = min(max(s_start[i + 1], s.start), A.B.m) - s.start;
+        s.len = min(max(s_len[i], 0), cap);
+        return s;
+    };
 
-    for (int g = warp; g < groups; g += kPlanThreads / 32) {
+    for (int g = warp; g < groups; g += kPlanWarps) {
+        const int a = plan[g].leader, b = plan[g].n, prefix = plan[g].from;
+        __syncwarp();
         PrefixGroup G{};
         if (!none) {
-            const int a = __ldcg(A.group_start + g), b = __ldcg(A.group_start + g + 1);
-            const int prefix = min(max(__ldcg(A.prefix_lens + g), 0), A.B.max_pages << shift);
             int least = 0x7FFFFFFF, most = -1, live = 0, rows = 0;
             for (int i = a + lane; i < b; i += 32) {
-                bool odd;
-                const SeqSpan s = seq_span(A.B, i, &odd);
+                const SeqSpan s = span(i);
                 if (s.n == 0) continue;
                 least = min(least, s.len - s.n);
                 most = max(most, s.len - 1);
@@ -100,8 +121,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
             live = __reduce_add_sync(0xffffffffu, live);
             G.leader = a;
             if (live > 1 && (int64_t)rows * A.rep <= A.max_rows) {
-                G.row0 = __ldcg(A.B.q_start + a);
-                G.n = __ldcg(A.B.q_start + b) - G.row0;
+                G.row0 = span(a).start;
+                G.n = span(b - 1).start + span(b - 1).n - G.row0;
                 G.from = min(prefix, max(least, 0)) >> shift << shift;
                 G.lo = A.window > 0 ? max(least - A.window + 1, 0) & ~15 : 0;
                 G.full_lo = A.window > 0 ? max(most - A.window + 1, 0) : 0;
@@ -110,51 +131,184 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
                     G.rows = (int)(((int64_t)G.n * A.rep + A.plan.tile_rows - 1) / A.plan.tile_rows);
                     for (int i = a + lane; i < b; i += 32) {
                         A.plan.seq[i] = make_int2(g, G.from);
+                        if (near) s_from[i] = G.from;
                         if (A.window > 0) {
-                            bool odd;
-                            const SeqSpan s = seq_span(A.B, i, &odd);
+                            const SeqSpan s = span(i);
                             for (int t = 0; t < s.n; ++t) A.plan.pos[s.start + t] = s.len - s.n + t;
                         }
                     }
                 }
             }
         }
-        if (lane == 0) A.plan.group[g] = G;
+        if (lane == 0) plan[g] = G;
     }
     __syncthreads();
-    // places on the line of work, of each thread's run of groups
-    const int per = (groups + kPlanThreads - 1) / kPlanThreads, lo = min(tid * per, groups), hi = min(lo + per, groups);
-    int64_t items = 0, units = 0, all_items, all_units;
-    for (int g = lo; g < hi; ++g) {
-        const int64_t n = (int64_t)A.plan.group[g].rows * A.kv_heads;
-        items += n;
-        units += n * A.plan.group[g].tiles;
+    // Warp 0: the groups' places. The other warps meanwhile count the sequences' own row tiles.
+    struct Own { SeqSpan s; int lo, tiles, units; };
+    auto own_of = [&](int i) {
+        Own w{};
+        w.s = span(i);
+        if (w.s.n == 0 || (int64_t)w.s.n * A.rep > A.max_rows) return w;
+        const int first = max(w.s.len - w.s.n, 0);
+        w.lo = max(A.window > 0 ? max(first - A.window + 1, 0) & ~15 : 0, near ? s_from[i] : A.plan.seq[i].y);
+        w.tiles = (w.s.n * A.rep + A.own_rows - 1) / A.own_rows;
+        w.units = max((w.s.len - w.lo + 63) / 64, 1);
+        return w;
+    };
+    constexpr int kOwnThreads = kPlanThreads - 32;
+    const int runs = (batch + kOwnThreads - 1) / kOwnThreads, s0 = min(max(tid - 32, 0) * runs, batch), s1 = warp ? min(s0 + runs, batch) : s0;
+    int own_before = 0;   // of this thread's run of sequences, within its warp
+    if (warp == 0) {
+        int64_t items = 0, units = 0;
+        int most = 1;
+        for (int g0 = 0; g0 < groups; g0 += 32) {
+            const int g = g0 + lane;
+            const int64_t n = g < groups ? (int64_t)plan[g].rows * A.kv_heads : 0, t = g < groups ? plan[g].tiles : 0;
+            int64_t ti, tu;
+            const int64_t i0 = warp_exclusive(n, &ti), v0 = warp_exclusive(n * t, &tu);
+            if (g < groups) {
+                plan[g].item0 = items + i0;
+                plan[g].unit0 = units + v0;
+            }
+            most = max(most, (int)t);
+            items += ti;
+            units += tu;
+        }
+        items = min(items, A.plan.items);
+        // Pieces of `each` units at most, none of two items, where that takes not much longer than equal pieces of the line of all
+        // units, of which many consist of two parts: the least such length that needs no more CTAs than there are.
+        int each = 0;
+        int64_t ctas = min(units, (int64_t)kPrefixCtas);
+        auto pieces_of = [&](int g, int length) { return plan[g].rows * A.kv_heads * ((plan[g].tiles + length - 1) / length); };
+        if (items > 0 && items <= kPrefixCtas) {
+            int b = __reduce_max_sync(0xffffffffu, most), a = 0;  // more than kPrefixCtas pieces of a, no more of b
+            while (b - a > 1) {
+                const int mid = (a + b) >> 1;
+                int pieces = 0;
+                for (int g = lane; g < groups; g += 32) pieces += pieces_of(g, mid);
+                if (__reduce_add_sync(0xffffffffu, pieces) <= kPrefixCtas) b = mid;
+                else a = mid;
+            }
+            if (b <= (units + kPrefixCtas - 1) / kPrefixCtas + kPieceCost) {
+                each = b;
+                ctas = 0;
+                for (int g0 = 0; g0 < groups; g0 += 32) {
+                    const int g = g0 + lane;
+                    int64_t tc;
+                    const int64_t c0 = warp_exclusive(g < groups ? pieces_of(g, each) : 0, &tc);
+                    if (g < groups) plan[g].unit0 = ctas + c0;
+                    ctas += tc;
+                }
+            }
+        }
+        if (lane == 0) {
+            s_each = each;
+            s_head = PrefixHead{units, items, (int)ctas, 0, 0, 0, 0};
+        }
+    } else {
+        int tiles = 0, longest = 0;
+        int64_t units = 0;
+        for (int i = s0; i < s1; ++i) {
+            const Own w = own_of(i);
+            tiles += w.tiles;
+            units += (int64_t)w.tiles * w.units;
+            longest = max(longest, w.units);
+        }
+        int inc = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += x;
+        }
+        own_before = inc - tiles;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        if (lane == 31) s_own[warp] = inc;
+        if (lane == 0) {
+            s_own_units[warp] = units;
+            s_own_longest[warp] = longest;
+        }
     }
-    items = block_exclusive(items, &all_items, s_warp);
-    units = block_exclusive(units, &all_units, s_warp);
-    for (int g = lo; g < hi; ++g) {
-        PrefixGroup* G = A.plan.group + g;
-        const int64_t n = (int64_t)G->rows * A.kv_heads;
-        G->item0 = items;
-        G->unit0 = units;
-        items += n;
-        units += n * G->tiles;
-    }
-    all_items = min(all_items, A.plan.items);
-    const int ctas = (int)min(all_units, (int64_t)kPrefixCtas);
-    if (tid == 0) *A.plan.head = PrefixHead{all_units, all_items, ctas, 0};
     __syncthreads();
-    for (int64_t i = tid; i < all_items; i += kPlanThreads) {
-        int a = 0, b = groups;  // the last group that begins at or before item i
+    const int each = s_each, ctas = s_head.ctas;
+    const int64_t all_items = s_head.items, all_units = s_head.units;
+    if (plan == s_group)
+        for (int g = tid; g < groups; g += kPlanThreads) A.plan.group[g] = plan[g];
+    auto group_of = [&](int64_t item) {  // the last group that begins at or before it
+        int a = 0, b = groups;
         while (b - a > 1) {
             const int mid = (a + b) >> 1;
-            if (A.plan.group[mid].item0 <= i) a = mid;
+            if (plan[mid].item0 <= item) a = mid;
             else b = mid;
         }
-        const PrefixGroup& G = A.plan.group[a];
-        const int64_t u = G.unit0 + (i - G.item0) * G.tiles;
-        const int c0 = piece_of(all_units, ctas, u), c1 = piece_of(all_units, ctas, u + G.tiles - 1);
-        A.plan.piece[i] = make_int2((int)(c0 + i), c1 - c0 + 1);
+        return a;
+    };
+    auto piece_at = [&](const PrefixGroup& G, int64_t item, int t, int n, int slot, int next) {
+        const int rel = (int)(item - G.item0), tile = rel / A.kv_heads;
+        PrefixPiece p;
+        p.n = n;
+        p.leader = G.leader;
+        p.head = rel - tile * A.kv_heads;
+        p.row0 = G.row0;
+        p.r0 = tile * A.plan.tile_rows;
+        p.rows = G.n * A.rep;
+        p.kv0 = G.lo + kToks * t;
+        p.kv_hi = min(G.from, p.kv0 + kToks * n);
+        p.full_lo = G.full_lo;
+        p.slot = slot;
+        p.next = next;
+        p.pad = 0;
+        return p;
+    };
+    for (int64_t i = tid; i < all_items; i += kPlanThreads) {
+        const PrefixGroup& G = plan[group_of(i)];
+        if (each > 0) {  // the item's pieces, a CTA each
+            const int k = (G.tiles + each - 1) / each;
+            A.plan.places[i] = make_int2((int)G.unit0 + (int)(i - G.item0) * k, k);
+        } else {
+            // the CTAs that share it: one that begins within it (or at its start) has it as its first piece, the one before it as a later one
+            const int64_t u = G.unit0 + (i - G.item0) * G.tiles, end = u + G.tiles;
+            const int c0 = piece_of(all_units, ctas, u), c1 = piece_of(all_units, ctas, end - 1);
+            A.plan.places[i] = make_int2((int)(c0 + i), c1 - c0 + 1);
+            for (int c = c0; c <= c1; ++c) {
+                const int64_t a = cut(all_units, ctas, c), b = cut(all_units, ctas, c + 1), from = max(a, u);
+                const int next = b > end ? (int)(kPrefixCtas + i + 1) : -1;
+                A.plan.piece[a >= u ? c : (int)(kPrefixCtas + i)] =
+                    piece_at(G, i, (int)(from - u), (int)(min(b, end) - from), (int)(c + i), next);
+            }
+        }
+    }
+    if (each > 0 && tid < ctas) {
+        int a = 0, b = groups;  // the last group whose pieces begin at or before CTA tid
+        while (b - a > 1) {
+            const int mid = (a + b) >> 1;
+            if (plan[mid].unit0 <= tid) a = mid;
+            else b = mid;
+        }
+        const PrefixGroup& G = plan[a];
+        const int k = (G.tiles + each - 1) / each, rel = tid - (int)G.unit0, item = rel / k, j = rel - item * k;
+        const int t = G.tiles * j / k;
+        A.plan.piece[tid] = piece_at(G, G.item0 + item, t, G.tiles * (j + 1) / k - t, tid, -1);
+    }
+    // the sequences' own row tiles
+    const int counted = lane > 0 && lane < kPlanWarps ? s_own[lane] : 0;
+    int at = own_before + __reduce_add_sync(0xffffffffu, lane < warp ? counted : 0);
+    const int all_tiles = __reduce_add_sync(0xffffffffu, counted);
+    for (int i = s0; i < s1; ++i) {
+        const Own w = own_of(i);
+        for (int t = 0; t < w.tiles; ++t, ++at)
+            if (at < A.plan.owns) A.plan.own[at] = OwnTile{i, w.s.start, w.s.n, w.s.len, w.lo, w.units, t, 0};
+    }
+    if (tid == 0) {
+        PrefixHead H = s_head;
+        H.own_tiles = all_tiles <= A.plan.owns ? all_tiles : 0;
+        for (int w = 1; w < kPlanWarps; ++w) {
+            H.own_longest = max(H.own_longest, s_own_longest[w]);
+            H.own_units += s_own_units[w];
+        }
+        H.own_units *= A.kv_heads;
+        *A.plan.head = H;
     }
 }
 
@@ -163,64 +317,51 @@ struct PrefixParams : PromptParams {  // window: the attention's; out, out_strid
     PrefixPlan plan;
 };
 
-// What a CTA does next: an item's units, or nothing (n 0).
-struct Segment {
-    int n;                    // units (tiles of 128 tokens)
-    int leader, head;         // whose pages, which kv head
-    int row0, r0, rows;       // the group's first row of the inputs; the row tile's first query row; the group's query rows
-    int kv0, kv_hi, full_lo;  // tokens
-    int slot;
-};
-// The warp finds the segment at unit s_u[0] of piece c, which ends at s_u[1], and goes past it. None once a role has given up.
-__device__ __forceinline__ void find_segment(const PrefixParams& A, int c, int64_t* s_u, volatile int* abort, Segment* out) {
+// The CTA's next piece, by a warp: number `at` of the list. None once a role has given up. Two calls at once on one workspace write over
+// each other's plans: nothing of one is believed as far as addresses go.
+__device__ __forceinline__ void read_piece(const PrefixParams& A, int at, volatile int* abort, PrefixPiece* out) {
     const int lane = threadIdx.x & 31;
-    const int64_t u = s_u[0], end = s_u[1];
-    __syncwarp();
-    if (u >= end || *abort) {
+    __syncwarp();  // `at` may come from where the piece goes
+    if (at < 0 || at >= kPrefixCtas + A.plan.items || (abort && *abort)) {
         if (lane == 0) out->n = 0;
         return;
     }
-    int lo = 0, hi = A.plan.groups - 1;  // the last group that begins at or before u (one without units begins where the next does)
-    while (hi - lo >= 32) {
-        const int step = (hi - lo) / 32 + 1, i = lo + lane * step;
-        const unsigned hit = __ballot_sync(0xffffffffu, i <= hi && __ldcg(&A.plan.group[i].unit0) <= u);
-        lo += (31 - __clz(hit)) * step;
-        hi = min(hi, lo + step - 1);
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, lo + lane <= hi && __ldcg(&A.plan.group[lo + lane].unit0) <= u);
-    lo += 31 - __clz(hit);
+    if (lane < 3) reinterpret_cast<int4*>(out)[lane] = __ldcg(reinterpret_cast<const int4*>(A.plan.piece + at) + lane);
+    __syncwarp();
     if (lane) return;
-    const int4* p = reinterpret_cast<const int4*>(A.plan.group + lo);
-    const int4 f[3] = {__ldcg(p), __ldcg(p + 1), __ldcg(p + 2)};
-    PrefixGroup G;
-    memcpy(&G, f, sizeof G);
-    // Two calls at once on one workspace write over each other's plans. Nothing of one is believed as far as addresses go.
-    G.tiles = min(max(G.tiles, 1), (A.B.max_pages << A.B.page_shift) / kToks + 1);
-    G.leader = min(max(G.leader, 0), A.B.batch - 1);
-    G.from = min(max(G.from, 0), A.B.max_pages << A.B.page_shift);
-    G.lo = min(max(G.lo, 0), G.from) & ~15;
-    G.row0 = min(max(G.row0, 0), A.B.m);
-    G.n = min(max(G.n, 0), A.B.m - G.row0);
-    const int64_t rel = max(u - G.unit0, (int64_t)0);
-    const int64_t item = min(rel / G.tiles, A.plan.items - 1);
-    const int t = (int)(rel % G.tiles), tile = (int)(item / A.kv_heads);
-    out->n = (int)min((int64_t)(G.tiles - t), end - u);
-    s_u[0] = u + out->n;
-    out->leader = G.leader;
-    out->head = (int)(item - (int64_t)tile * A.kv_heads);
-    out->row0 = G.row0;
-    out->r0 = tile * A.plan.tile_rows;
-    out->rows = G.n * A.group;
-    out->kv0 = G.lo + kToks * t;
-    out->kv_hi = min(G.from, out->kv0 + kToks * out->n);
-    out->full_lo = G.full_lo;
-    out->slot = (int)min(max(c + G.item0 + item, (int64_t)0), A.plan.slots - 1);
+    PrefixPiece p = *out;
+    p.leader = min(max(p.leader, 0), A.B.batch - 1);
+    p.head = min(max(p.head, 0), A.kv_heads - 1);
+    p.row0 = min(max(p.row0, 0), A.B.m - 1);
+    p.rows = (int)min((int64_t)max(p.rows, 1), (int64_t)(A.B.m - p.row0) * A.group);
+    p.r0 = min(max(p.r0, 0), p.rows - 1);
+    p.kv0 = max(p.kv0, 0) & ~15;
+    p.kv_hi = min(p.kv_hi, A.B.max_pages << A.B.page_shift) & ~15;
+    p.n = p.kv_hi > p.kv0 ? (p.kv_hi - p.kv0 + kToks - 1) / kToks : 0;
+    p.slot = (int)min((int64_t)max(p.slot, 0), A.plan.slots - 1);
+    p.next = p.next > at ? p.next : -1;
+    *out = p;
 }
-static_assert(sizeof(PrefixGroup) == 48, "read as three 16-byte words");
+static_assert(sizeof(PrefixPiece) == 48, "read as three 16-byte words");
 
 constexpr int kThreads = 640;
 constexpr int kKWarp = 8, kVWarp = 12, kMmaWarp = 16, kPageWarp = 17;  // as in the prompt kernels
 constexpr int kRegsAll = 5 * (65536 / kThreads / 8 * 8);
+
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// A row of partial sums, which the thread has put into shared memory, to global memory: a copy that runs by itself. The rows lie kRowBytes
+// apart there, so that a warp's writes meet all banks.
+template <int D> constexpr int kRowBytes = D * 4 + 16;
+template <int D>
+__device__ __forceinline__ void store_row_async(float* dst, const uint8_t* src) {
+    fence_proxy_async_smem();
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "n"(D * 4) : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// .. until shared memory may be written again
+__device__ __forceinline__ void stored() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 __device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }  // warps 0-7
 
@@ -248,18 +389,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     __shared__ TileMeta s_meta[kMetaRing];
     __shared__ float s_c[kRows], s_ref[2][kRows], s_l[kRows];
     __shared__ uint32_t s_tmem;
-    __shared__ Segment s_seg;
-    __shared__ int64_t s_u[2];
+    __shared__ PrefixPiece s_seg;
     __shared__ int s_nan[2];
     __shared__ volatile int s_abort;
-
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5;
-    const int64_t units = __ldcg(&A.plan.head->units);
-    const int ctas = __ldcg(&A.plan.head->ctas), cta = blockIdx.x;
-    if (cta >= ctas || ctas > kPrefixCtas || units < ctas || units > A.plan.units) return;  // the whole CTA, before any allocation
-    if (tid < 2) s_u[tid] = cut(units, ctas, cta + tid);
+    // what needs no results of the plan goes before the wait for it
     if (tid == 32) {
         for (int i = 0; i < L::kSlots; ++i) {
             mbar_init(&full[i], 128);
@@ -280,11 +414,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         mbar_init(&drain, 1);
         fence_mbar_init();
         s_abort = 0;
+        s_nan[0] = 0x7FFFFFFF;
+        s_nan[1] = -1;
     }
     if (warp == kMmaWarp) {
         tmem_alloc(&s_tmem, 512);
         tmem_relinquish();
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 0) read_piece(A, (int)blockIdx.x < __ldcg(&A.plan.head->ctas) ? (int)blockIdx.x : -1, nullptr, &s_seg);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -294,15 +433,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     bool issued = false;
     // Every role's loop: the segment before is done with by all, the next one is known to all (false: there is none).
     auto next = [&]() {
-        tc_fence_before();
-        __syncthreads();
-        if (warp == 0) find_segment(A, cta, s_u, &s_abort, &s_seg);
-        if (tid == 32) {
-            s_nan[0] = 0x7FFFFFFF;
-            s_nan[1] = -1;
+        if (seg > 0) {
+            tc_fence_before();
+            __syncthreads();
+            if (warp == 0) read_piece(A, s_seg.next, &s_abort, &s_seg);
+            if (tid == 32) {
+                s_nan[0] = 0x7FFFFFFF;
+                s_nan[1] = -1;
+            }
+            __syncthreads();
+            tc_fence_after();
         }
-        __syncthreads();
-        tc_fence_after();
         return s_seg.n > 0;  // not s_abort: a role that is already ahead may set it while others look
     };
     auto done = [&](bool ok) {
@@ -319,44 +460,61 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         const int r = valid ? s_seg.r0 + (tid & 127) : 0;
         return max(__ldcg(A.plan.pos + s_seg.row0 + r / A.group) - A.window + 1, 0);
     };
-    // Queries, by warps 0-7: four threads a row, D/4 dims each, 64 rows at a time, scaled by a power of two into fp16's range.
+    // Queries, by warps 0-7: sixteen (or eight) lanes a row of D dims, eight dims a lane. The rows are copied to where their two terms will lie, all
+    // at once, and turned into them there, scaled by a power of two into fp16's range.
     auto load_queries = [&]() {
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-            const int qrow = 64 * half + (tid >> 2), part = tid & 3, qr = s_seg.r0 + qrow;
-            const bool there = qr < s_seg.rows;
-            const float* p = static_cast<const float*>(A.q) + (int64_t)(s_seg.row0 + (there ? qr / A.group : 0)) * A.q_stride +
-                             (int64_t)(s_seg.head * A.group + (there ? qr % A.group : 0)) * D + part * (D / 4);
-            float x[D / 4];
-            Vec<float>::load(p, x);
+        constexpr int kLanes = D / 8, kStep = 256 / kLanes;   // lanes of a row, rows at a time
+        const int u = tid % kLanes;
+        int tok = (s_seg.r0 + tid / kLanes) / A.group, h = (s_seg.r0 + tid / kLanes) % A.group;
+        const int tok_step = kStep / A.group, h_step = kStep % A.group;
+        uint8_t* const at = s_q + (u >> 3) * (kRows * 128);
+#pragma unroll 4
+        for (int row = tid / kLanes; row < kRows; row += kStep) {
+            uint8_t* dst = at + row * 128 + (((u & 7) ^ (row & 7)) << 4);
+            if (s_seg.r0 + row < s_seg.rows) {
+                const float* p = static_cast<const float*>(A.q) + (int64_t)(s_seg.row0 + tok) * A.q_stride +
+                                 (int64_t)(s_seg.head * A.group + h) * D + 8 * u;
+                copy16(dst, p);
+                copy16(dst + L::kTile, p + 4);
+            } else {
+                *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<uint4*>(dst + L::kTile) = make_uint4(0, 0, 0, 0);
+            }
+            tok += tok_step;
+            h += h_step;
+            if (h >= A.group) {
+                h -= A.group;
+                ++tok;
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 4
+        for (int row = tid / kLanes; row < kRows; row += kStep) {
+            uint8_t* dst = at + row * 128 + (((u & 7) ^ (row & 7)) << 4);
+            float x[8];
+            *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(dst);
+            *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(dst + L::kTile);
             float amax = 0.0f;
 #pragma unroll
-            for (int i = 0; i < D / 4; ++i) {
-                if (!there) x[i] = 0.0f;
+            for (int i = 0; i < 8; ++i) {
                 const float a = fabsf(x[i]);
                 if (a <= 3.402823466e38f) amax = fmaxf(amax, a);
             }
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+#pragma unroll
+            for (int o = kLanes / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
             const int e = amax > 0.0f ? min(max(134 - (int)(__float_as_uint(amax) >> 23), -120), 120) : 0;
             const float up = A.sign * exp2_int(e);
-            if (part == 0) s_c[qrow] = A.scale_log2 * exp2_int(-e);
+            if (u == 0) s_c[row] = A.scale_log2 * exp2_int(-e);
+            uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k) {  // 8 dims a unit
-                const int unit = part * (D / 32) + k;
-                uint8_t* dst = s_q + (unit >> 3) * (kRows * 128) + qrow * 128 + (((unit & 7) ^ (qrow & 7)) << 4);
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a = x[8 * k + 2 * i] * up, b = x[8 * k + 2 * i + 1] * up;
-                    const __half2 h = __floats2half2_rn(a, b);
-                    const float2 f = __half22float2(h);
-                    hi[i] = h2_bits(h);
-                    lo[i] = h2_bits(__floats2half2_rn(a - f.x, b - f.y));
-                }
-                *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(dst + L::kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            for (int i = 0; i < 4; ++i) {
+                const float a = x[2 * i] * up, b = x[2 * i + 1] * up;
+                const __half2 t = __floats2half2_rn(a, b);
+                const float2 f = __half22float2(t);
+                hi[i] = h2_bits(t);
+                lo[i] = h2_bits(__floats2half2_rn(a - f.x, b - f.y));
             }
+            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(dst + L::kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         fence_proxy_async_smem();
         mbar_arrive(&q_full);
@@ -524,7 +682,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             ok = ok && wait(&fin, seg & 1);  // the denominators, and the loaders' report of NaN
             if (ok && valid) {
                 const int64_t place = (int64_t)s_seg.slot * kRows + row;
-                float* o = A.plan.sums + place * D;
+                // all products are done: the queries' and the tiles' place is free
+                uint8_t* const mine = s_q + row * kRowBytes<D>;
 #pragma unroll
                 for (int c = 0; c < D; c += 16) {
                     float y[16];
@@ -533,9 +692,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     if (s_nan[1] >= 0)
                         mark_nan<D, 16>(A, s_seg.leader, s_seg.head, lo, kv_hi - 1, kv0 + kToks * s_nan[0],
                                         kv0 + kToks * (s_nan[1] + 1) - 1, c, y);
-                    Vec<float>::store(o + c, y);
+                    Vec<float>::store(reinterpret_cast<float*>(mine) + c, y);
                 }
+                store_row_async<D>(A.plan.sums + place * D, mine);
                 A.plan.refs[place] = make_float2(m == -INFINITY ? m : weight_base(m, kTop), s_l[row]);
+                stored();
             }
             done(ok);
         }
@@ -570,18 +731,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix2_kernel(const __grid_const
     __shared__ TileMeta s_meta[kMetaRing];
     __shared__ float s_c[2 * kRows];
     __shared__ uint32_t s_tmem;
-    __shared__ Segment s_seg;
-    __shared__ int64_t s_u[2];
+    __shared__ PrefixPiece s_seg;
     __shared__ int s_nan[2];
     __shared__ volatile int s_abort;
-
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5;
-    const int64_t units = __ldcg(&A.plan.head->units);
-    const int ctas = __ldcg(&A.plan.head->ctas), cta = blockIdx.x;
-    if (cta >= ctas || ctas > kPrefixCtas || units < ctas || units > A.plan.units) return;  // the whole CTA, before any allocation
-    if (tid < 2) s_u[tid] = cut(units, ctas, cta + tid);
+    // what needs no results of the plan goes before the wait for it
     if (tid == 32) {
         for (int i = 0; i < L::kSlots; ++i) {
             mbar_init(&full[i], 128);
@@ -601,11 +755,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix2_kernel(const __grid_const
         mbar_init(&drain, 1);
         fence_mbar_init();
         s_abort = 0;
+        s_nan[0] = 0x7FFFFFFF;
+        s_nan[1] = -1;
     }
     if (warp == kMmaWarp) {
         tmem_alloc(&s_tmem, 512);
         tmem_relinquish();
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 0) read_piece(A, (int)blockIdx.x < __ldcg(&A.plan.head->ctas) ? (int)blockIdx.x : -1, nullptr, &s_seg);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -615,15 +774,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefix2_kernel(const __grid_const
     bool issued = false;
     // Every role's loop: the segment before is done with by all, the next one is known to all (false: there is none).
     auto next = [&]() {
-        tc_fence_before();
-        __syncthreads();
-        if (warp == 0) find_segment(A, cta, s_u, &s_abort, &s_seg);
-        if (tid == 32) {
-            s_nan[0] = 0x7FFFFFFF;
-            s_nan[1] = -1;
+        if (seg > 0) {
+            tc_fence_before();
+            __syncthreads();
+            if (warp == 0) read_piece(A, s_seg.next, &s_abort, &s_seg);
+            if (tid == 32) {
+                s_nan[0] = 0x7FFFFFFF;
+                s_nan[1] = -1;
+            }
+            __syncthreads();
+            tc_fence_after();
         }
-        __syncthreads();
-        tc_fence_after();
         return s_seg.n > 0;  // not s_abort: a role that is already ahead may set it while others look
     };
     auto done = [&](bool ok) {
@@ -704,43 +865,50 @@ __global__ void __launch_bounds__(kThreads, 1) prefix2_kernel(const __grid_const
         while (next()) {
             bool ok = true;
             const int n = s_seg.n, kv0 = s_seg.kv0, kv_hi = s_seg.kv_hi, r0 = s_seg.r0, rows = s_seg.rows, full_lo = s_seg.full_lo;
-            // queries: two threads a row, D/2 dims each, 128 rows at a time, scaled by a power of two into fp16's range (exact there)
-#pragma unroll 1
-            for (int y = 0; y < 2; ++y) {
-                const int qrow = tid >> 1, half = tid & 1, qr = r0 + y * kRows + qrow;
-                const bool there = qr < rows;
-                const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(A.q) +
-                                         (int64_t)(s_seg.row0 + (there ? qr / A.group : 0)) * A.q_stride +
-                                         (int64_t)(s_seg.head * A.group + (there ? qr % A.group : 0)) * D + half * (D / 2);
-                uint4 w4[D / 16];
-                uint32_t top = 0;  // largest finite magnitude's bits
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) w4[i] = there ? __ldcg(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint32_t w[4] = {w4[i].x, w4[i].y, w4[i].z, w4[i].w};
+            // queries: sixteen (or eight) lanes a row, eight dims a lane, as in prefix_kernel; exact in one fp16 term
+            {
+                constexpr int kLanes = D / 8, kStep = 256 / kLanes;
+                const int u = tid % kLanes;
+                int tok = (r0 + tid / kLanes) / A.group, h = (r0 + tid / kLanes) % A.group;
+                const int tok_step = kStep / A.group, h_step = kStep % A.group;
+                auto place_of = [&](int row) {
+                    return s_q + (row >> 7) * L::kTile + (u >> 3) * (kRows * 128) + (row & 127) * 128 + (((u & 7) ^ (row & 7)) << 4);
+                };
+#pragma unroll 4
+                for (int qrow = tid / kLanes; qrow < 2 * kRows; qrow += kStep) {
+                    if (r0 + qrow < rows)
+                        copy16(place_of(qrow), static_cast<const __nv_bfloat16*>(A.q) + (int64_t)(s_seg.row0 + tok) * A.q_stride +
+                                                   (int64_t)(s_seg.head * A.group + h) * D + 8 * u);
+                    else
+                        *reinterpret_cast<uint4*>(place_of(qrow)) = make_uint4(0, 0, 0, 0);
+                    tok += tok_step;
+                    h += h_step;
+                    if (h >= A.group) {
+                        h -= A.group;
+                        ++tok;
+                    }
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 4
+                for (int qrow = tid / kLanes; qrow < 2 * kRows; qrow += kStep) {
+                    uint4* const at = reinterpret_cast<uint4*>(place_of(qrow));
+                    const uint4 v = *at;
+                    uint32_t w[4] = {v.x, v.y, v.z, v.w}, top = 0;  // largest finite magnitude's bits
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const uint32_t a = w[k] & 0x7FFFu, b = (w[k] >> 16) & 0x7FFFu;
                         if (a < 0x7F80u) top = max(top, a);
                         if (b < 0x7F80u) top = max(top, b);
                     }
-                }
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                const int e = top > 0 ? min(max(134 - (int)(top >> 7), -120), 120) : 0;
-                const float up = A.sign * exp2_int(e);
-                if (half == 0) s_c[y * kRows + qrow] = A.scale_log2 * exp2_int(-e);
-                uint8_t* base = s_q + y * L::kTile + qrow * 128;
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {  // 8 dims a unit
-                    const int unit = half * (D / 16) + i;
-                    const uint32_t w[4] = {w4[i].x, w4[i].y, w4[i].z, w4[i].w};
-                    uint32_t h[4];
+                    for (int o = kLanes / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const int e = top > 0 ? min(max(134 - (int)(top >> 7), -120), 120) : 0;
+                    const float up = A.sign * exp2_int(e);
+                    if (u == 0) s_c[qrow] = A.scale_log2 * exp2_int(-e);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        h[k] = h2_bits(__floats2half2_rn(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up));
-                    *reinterpret_cast<uint4*>(base + (unit >> 3) * (kRows * 128) + (((unit & 7) ^ (qrow & 7)) << 4)) =
-                        make_uint4(h[0], h[1], h[2], h[3]);
+                        w[k] = h2_bits(__floats2half2_rn(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up));
+                    *at = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
             fence_proxy_async_smem();
@@ -802,11 +970,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix2_kernel(const __grid_const
                 tc_fence_before();
                 mbar_arrive(&p_full[x]);
             }
-            ok = ok && wait(&fin, seg & 1) && wait(&o_full[x], seg & 1);
+            ok = ok && wait(&fin, seg & 1) && wait(&o_full[x], seg & 1) && wait(&o_full[x ^ 1], seg & 1);
             if (ok) {
                 tc_fence_after();
                 const int64_t place = (int64_t)s_seg.slot * (2 * kRows) + x * kRows + row;
-                float* o = A.plan.sums + place * D;
+                // all products of both row tiles are done: the queries' and the tiles' place is free
+                uint8_t* const mine = s_q + (x * kRows + row) * kRowBytes<D>;
 #pragma unroll 1
                 for (int q = 0; q < D / 32; ++q) {
                     uint32_t v[32];
@@ -818,9 +987,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix2_kernel(const __grid_const
                     if (s_nan[1] >= 0 && valid)
                         mark_nan<D, 32>(A, s_seg.leader, s_seg.head, lo, kv_hi - 1, kv0 + kToks * s_nan[0],
                                         kv0 + kToks * (s_nan[1] + 1) - 1, 32 * q, y);
-                    if (valid) Vec<float>::store(o + 32 * q, y);
+                    if (valid) Vec<float>::store(reinterpret_cast<float*>(mine) + 32 * q, y);
                 }
-                if (valid) A.plan.refs[place] = make_float2(ref == -INFINITY ? ref : weight_base(ref, kTop - kSlack), l);
+                if (valid) {
+                    store_row_async<D>(A.plan.sums + place * D, mine);
+                    A.plan.refs[place] = make_float2(ref == -INFINITY ? ref : weight_base(ref, kTop - kSlack), l);
+                    stored();
+                }
             }
             done(ok);
         }
@@ -867,6 +1040,107 @@ cudaError_t launch_typed(const PrefixParams& P, int ctas, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, kern, P);
 }
 
+// ---- both parts ---------------------------------------------------------------------------------------------------
+// Each row's sums of its own tokens and of the pieces of the shared ones, to the largest of their references; 16 or 32 lanes a row of a
+// row tile, four dims a lane. Bound by reading the pieces, from L2.
+constexpr int kJoinRows = 16;
+
+struct JoinParams {
+    PrefixPlan plan;
+    void* out;
+    int64_t out_stride;
+    int kv_heads, group, m;
+};
+__device__ __forceinline__ float group_max(float x, int lanes) {
+    for (int o = lanes / 2; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinRows * D / 4) prefix_join_kernel(const __grid_constant__ JoinParams A) {
+    constexpr int kLanes = D / 4;
+    __shared__ PrefixGroup s_group;
+    __shared__ float s_w[kJoinRows][kPrefixCtas];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, lane = tid & 31, parts = A.plan.tile_rows / kJoinRows;
+    const int64_t item = blockIdx.x / parts;
+    const int2 place = item < A.plan.items ? __ldcg(A.plan.places + item) : make_int2(0, 0);
+    if (item >= __ldcg(&A.plan.head->items)) return;
+    if (tid < 32) {
+        int lo = 0, hi = A.plan.groups - 1;  // the last group that begins at or before the item (one without items begins where the next does)
+        while (hi - lo >= 32) {
+            const int step = (hi - lo) / 32 + 1, i = lo + lane * step;
+            const unsigned hit = __ballot_sync(0xffffffffu, i <= hi && __ldcg(&A.plan.group[i].item0) <= item);
+            lo += max(31 - __clz(hit), 0) * step;
+            hi = min(hi, lo + step - 1);
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, lo + lane <= hi && __ldcg(&A.plan.group[lo + lane].item0) <= item);
+        lo += max(31 - __clz(hit), 0);
+        if (lane < 3) reinterpret_cast<int4*>(&s_group)[lane] = __ldcg(reinterpret_cast<const int4*>(A.plan.group + lo) + lane);
+    }
+    __syncthreads();
+    const int rel = (int)(item - s_group.item0), tile = rel / A.kv_heads, head = rel - tile * A.kv_heads;
+    const int local = (int)(blockIdx.x - item * parts) * kJoinRows + tid / kLanes, r = tile * A.plan.tile_rows + local;
+    const int c = 4 * (tid % kLanes);
+    const int tok = s_group.row0 + r / A.group, h = head * A.group + r % A.group;
+    // (a plan that another call on this workspace has written over leads to no place outside it)
+    const bool there = r >= 0 && r < s_group.n * A.group && tok >= 0 && tok < A.m && head >= 0 && place.x >= 0 && place.y > 0 &&
+                       place.y <= kPrefixCtas && place.x + place.y <= A.plan.slots;
+    const int64_t row = (int64_t)tok * A.kv_heads * A.group + h, at = (int64_t)place.x * A.plan.tile_rows + local;
+    float2 own = make_float2(-INFINITY, 0.0f);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (there) {
+        own = __ldcg(A.plan.own_refs + row);
+        acc = __ldcg(reinterpret_cast<const float4*>(A.plan.own_sums + row * D + c));
+    }
+    // the pieces' weights, a lane each at a time
+    float top = own.x, den = 0.0f;
+    for (int k = tid % kLanes; there && k < place.y; k += kLanes) {
+        const float2 f = __ldcg(A.plan.refs + at + (int64_t)k * A.plan.tile_rows);
+        const float was = top;
+        top = fmaxf(top, f.x);
+        const float use = top == -INFINITY ? 0.0f : top;
+        den = fmaf(ex2(f.x - use), f.y, den * ex2(was - use));
+        s_w[tid / kLanes][k] = f.x;
+    }
+    const float mine = top;
+    top = group_max(top, kLanes);
+    const float use = top == -INFINITY ? 0.0f : top;
+    den *= ex2(mine - use);
+    for (int o = kLanes / 2; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    const float keep = ex2(own.x - use);
+    den = fmaf(keep, own.y, den);
+    __syncwarp();
+    if (!there) return;
+    float4 sum = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+    const float* x = A.plan.sums + at * D + c;
+    const int64_t step = (int64_t)A.plan.tile_rows * D;
+#pragma unroll 8
+    for (int k = 0; k < place.y; ++k) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(x + k * step));
+        const float w = ex2(s_w[tid / kLanes][k] - use);
+        sum.x = fmaf(w, v.x, sum.x); sum.y = fmaf(w, v.y, sum.y);
+        sum.z = fmaf(w, v.z, sum.z); sum.w = fmaf(w, v.w, sum.w);
+    }
+    const float iv = den == 0.0f ? 0.0f : 1.0f / den;
+    const float y[4] = {sum.x * iv, sum.y * iv, sum.z * iv, sum.w * iv};
+    Vec<T>::store(static_cast<T*>(A.out) + (int64_t)tok * A.out_stride + (int64_t)h * D + c, y);
+}
+
+template <typename T, int D>
+cudaError_t launch_join(const JoinParams& P, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(P.plan.items * (P.plan.tile_rows / kJoinRows)));
+    cfg.blockDim = dim3(kJoinRows * D / 4);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, prefix_join_kernel<T, D>, P);
+}
+
 // Row tiles of all groups at most: a group's last one may be part filled.
 int64_t most_items(int batch, int groups, int m, int rep, int kv_heads, int tile_rows) {
     const int some = groups < batch ? groups : batch;
@@ -882,17 +1156,23 @@ size_t layout(int batch, int groups, int m, int rep, int kv_heads, int head_dim,
         return p;
     };
     const int64_t items = most_items(batch, groups, m, rep, kv_heads, tile_rows), slots = items + kPrefixCtas;
+    const int64_t owns = (int64_t)m * rep / 8 + (m < batch ? m : batch);  // row tiles of eight rows and more, the last of a sequence part filled
     plan->head = reinterpret_cast<PrefixHead*>(part(sizeof(PrefixHead)));
     plan->group = reinterpret_cast<PrefixGroup*>(part(sizeof(PrefixGroup) * (size_t)groups));
     plan->seq = reinterpret_cast<int2*>(part(sizeof(int2) * (size_t)batch));
-    plan->piece = reinterpret_cast<int2*>(part(sizeof(int2) * (size_t)items));
+    plan->piece = reinterpret_cast<PrefixPiece*>(part(sizeof(PrefixPiece) * (size_t)slots));
+    plan->places = reinterpret_cast<int2*>(part(sizeof(int2) * (size_t)items));
+    plan->own = reinterpret_cast<OwnTile*>(part(sizeof(OwnTile) * (size_t)owns));
     plan->pos = reinterpret_cast<int*>(part(sizeof(int) * (size_t)m));
     plan->refs = reinterpret_cast<float2*>(part(sizeof(float2) * (size_t)slots * tile_rows));
     plan->sums = reinterpret_cast<float*>(part(sizeof(float) * (size_t)slots * tile_rows * head_dim));
+    plan->own_refs = reinterpret_cast<float2*>(part(sizeof(float2) * (size_t)m * rep * kv_heads));
+    plan->own_sums = reinterpret_cast<float*>(part(sizeof(float) * (size_t)m * rep * kv_heads * head_dim));
     plan->tile_rows = tile_rows;
     plan->groups = groups;
     plan->items = items;
     plan->slots = slots;
+    plan->owns = owns;
     return at;
 }
 
@@ -909,14 +1189,13 @@ size_t prefix_workspace_bytes(int batch, int groups, int m, int q_heads, int kv_
 cudaError_t launch_prefix(const PagedBatch& B, const void* q, int dtype, int64_t q_stride, int q_heads, int kv_heads,
                           int head_dim, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
                           const float* v_scale, const int32_t* group_start, const int32_t* prefix_lens, int groups,
-                          int max_prefix, int max_rows, float scale, int window, void* workspace, int* err_flag,
+                          int max_prefix, int max_rows, int own_rows, float scale, int window, void* workspace, int* err_flag,
                           PrefixPlan* plan, cudaStream_t stream) {
     const int rep = q_heads / kv_heads, tile_rows = dtype == Q4K_F32 ? kRows : 2 * kRows;
     layout(B.batch, groups, B.m, rep, kv_heads, head_dim, tile_rows, static_cast<uint8_t*>(workspace), plan);
-    plan->units = plan->items * (((int64_t)B.max_pages << B.page_shift) / kToks + 1);
     PlanParams L{};
     L.B = B; L.group_start = group_start; L.prefix_lens = prefix_lens; L.plan = *plan;
-    L.kv_heads = kv_heads; L.rep = rep; L.window = window; L.max_rows = max_rows; L.err_flag = err_flag;
+    L.kv_heads = kv_heads; L.rep = rep; L.window = window; L.max_rows = max_rows; L.own_rows = own_rows; L.err_flag = err_flag;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(kPlanThreads);
@@ -939,6 +1218,13 @@ cudaError_t launch_prefix(const PagedBatch& B, const void* q, int dtype, int64_t
     const int ctas = kPrefixCtas;
     if (dtype == Q4K_F32) return head_dim == 64 ? launch_typed<float, 64>(P, ctas, stream) : launch_typed<float, 128>(P, ctas, stream);
     return head_dim == 64 ? launch_typed<__nv_bfloat16, 64>(P, ctas, stream) : launch_typed<__nv_bfloat16, 128>(P, ctas, stream);
+}
+
+cudaError_t launch_prefix_join(const PagedBatch& B, int dtype, int q_heads, int kv_heads, int head_dim, const PrefixPlan& plan,
+                               void* out, int64_t out_stride, cudaStream_t stream) {
+    JoinParams P{plan, out, out_stride, kv_heads, q_heads / kv_heads, B.m};
+    if (dtype == Q4K_F32) return head_dim == 64 ? launch_join<float, 64>(P, stream) : launch_join<float, 128>(P, stream);
+    return head_dim == 64 ? launch_join<__nv_bfloat16, 64>(P, stream) : launch_join<__nv_bfloat16, 128>(P, stream);
 }
 
 }  // namespace q4k

@@ -1,10 +1,10 @@
-// q4k_prefix.cuh -- the plan of attention behind shared prefixes (q4k_prefix.cu makes it and computes the shared part; q4k_attn.cu
-// computes each sequence's own part and joins both).
+// q4k_prefix.cuh -- the plan of attention behind shared prefixes (q4k_prefix.cu makes it and computes the shared part and joins it to
+// the sequences' own parts, which q4k_attn.cu computes).
 //
 // A group's shared part is the whole pages of its prefix that lie before every new token of its sequences. Its query rows
 // (row r: new token r / rep of the group, query head r % rep of the kv head) are cut into row tiles; an item is a
-// (group, row tile, kv head), and the line of all items' 128-token units is cut into equal pieces, one a CTA. What a CTA
-// computes of an item goes to slot (CTA + item) of the partial results, a place of its own: along the line one or the other grows.
+// (group, row tile, kv head), and its units are the shared tokens, 128 at a time. Items are cut along the tokens into pieces for
+// one CTA each; what a piece gives goes to a slot of the partial results of its own.
 #pragma once
 
 #include "q4k_paged.cuh"
@@ -17,23 +17,48 @@ struct PrefixGroup {
     int full_lo;        // from here on every row sees them
     int leader;         // the sequence whose row of the page table is read
     int tiles, rows;    // units of 128 tokens, row tiles (0: nothing is shared)
-    int64_t unit0;      // its place on the line of work
+    int64_t unit0;      // its units' place on the line of all units, or its first CTA
     int64_t item0;      // its first item
+};
+// What a CTA computes of an item.
+struct alignas(16) PrefixPiece {
+    int n;                    // units (0: none)
+    int leader, head;         // whose pages, which kv head
+    int row0;                 // the group's first row of the inputs
+    int r0, rows;             // the row tile's first query row; the group's query rows
+    int kv0, kv_hi, full_lo;  // tokens; from full_lo on every row sees them
+    int slot;
+    int next;                 // the CTA's next piece (an index above this one's), or -1
+    int pad;
+};
+// A row tile of a sequence and what it sees of the sequence's own tokens.
+struct alignas(16) OwnTile {
+    int seq, start, n, len;   // as SeqSpan
+    int lo, units;            // from token lo (a multiple of 16), in units of 64 tokens
+    int tile, pad;
 };
 struct PrefixHead {
     int64_t units, items;
-    int ctas, pad;
+    int ctas;            // that compute the shared part
+    int own_tiles;       // row tiles of the sequences
+    int own_longest;     // units of the longest
+    unsigned next;       // the next (row tile, kv head) to be taken, beyond one for each CTA
+    int64_t own_units;   // of all (row tile, kv head)
 };
 struct PrefixPlan {
     PrefixHead* head;
     PrefixGroup* group;   // [groups]
     int2* seq;            // [batch]: group (-1: none), tokens taken from its shared part
-    int2* piece;          // [items]: first slot, slots
+    PrefixPiece* piece;   // [kPrefixCtas + items]: a CTA's first piece, then the pieces that begin an item after another's in a CTA
+    int2* places;         // [items]: first slot, slots
+    OwnTile* own;         // [own]
     int* pos;             // [m]: positions of the groups' rows, where there is a window
     float* sums;          // [slots][tile_rows][head_dim]
     float2* refs;         // [slots][tile_rows]: exponent that the sums and the denominator are relative to (-inf: nothing seen), denominator
+    float* own_sums;      // [m * q_heads][head_dim]: the same of the sequences' own parts, where they share another
+    float2* own_refs;     // [m * q_heads]
     int tile_rows, groups;
-    int64_t items, slots, units;  // what the workspace has room for, and the units there can be at most
+    int64_t items, slots, owns;   // what the workspace has room for
 };
 
 // Rows up to here have partial results of at most half a gigabyte; beyond (hundreds of rows a kv head for each of thousands of
