@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
             Cursor c{};
             TilePart p{};
             s_u[0] = 0;
-            s_u[1] = listed_tile(A, blockIdx.x, list, &c, &p);
+            s_u[1] = listed_tile(A, atomicAdd(&A.pre.head->next, 1u), list, &c, &p);
             s_cur = c;
             s_tile = p;
             s_by_tile = true;
@@ -1055,7 +1055,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
             if (threadIdx.x == 0) {
                 Cursor c{};
                 TilePart p{};
-                s_u[1] = listed_tile(A, (int64_t)gridDim.x + taken, list, &c, &p);
+                s_u[1] = listed_tile(A, taken, list, &c, &p);
                 s_cur = c;
                 s_tile = p;
             }

@@ -23,8 +23,8 @@ namespace {
 // ---- the plan -----------------------------------------------------------------------------------------------------
 constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanSeqs = 2048, kPlanGroups = 128;  // whose lengths, and plans, are looked up in shared memory
-// Units that a piece's start and end are worth, and a CTA's second piece costs it.
-constexpr int kPieceCost = 8;
+// Units (1.9 us each, 128 tokens of a row tile) that a piece's start and end are worth, and that an own tile takes of an SM.
+constexpr float kPieceCost = 6.0f, kOwnCost = 1.0f, kOwnUnitCost = 0.09f;
 
 struct PlanParams {
     PagedBatch B;
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
         if (lane == 0) plan[g] = G;
     }
     __syncthreads();
-    // Warp 0: the groups' places. The other warps meanwhile count the sequences' own row tiles.
+    // The sequences' own row tiles, counted by all warps but the first; it meanwhile finds the groups' places.
     struct Own { SeqSpan s; int lo, tiles, units; };
     auto own_of = [&](int i) {
         Own w{};
@@ -175,31 +175,40 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
             units += tu;
         }
         items = min(items, A.plan.items);
+        asm volatile("bar.sync 1, %0;" ::"n"(kPlanThreads) : "memory");
+        const int own_tiles = __reduce_add_sync(0xffffffffu, lane > 0 && lane < kPlanWarps ? s_own[lane] : 0);
+        float own_units = lane > 0 && lane < kPlanWarps ? (float)s_own_units[lane] : 0.0f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) own_units += __shfl_xor_sync(0xffffffffu, own_units, o);
+        // How many CTAs: the sequences' own tiles run on the SMs that these leave free, and on all when they are done. Candidates in steps
+        // of a sixteenth, the cheapest by estimate.
+        const float own_work = (float)A.kv_heads * (kOwnCost * (float)own_tiles + kOwnUnitCost * own_units);
+        const int candidate = max(kPrefixCtas * (lane < 16 ? lane + 1 : 16) / 16, 1);
+        const float shared_time = kPieceCost + ceilf((float)units / (float)candidate);
+        const float left = fmaxf(own_work - (float)(kPrefixCtas - candidate) * shared_time, 0.0f) / (float)kPrefixCtas;
+        // (the estimate's bits order as it does; the least by the lowest lane)
+        const unsigned best = __reduce_min_sync(0xffffffffu, (__float_as_uint(shared_time + left) & ~31u) | (unsigned)lane) & 31u;
+        const int most_ctas = __shfl_sync(0xffffffffu, candidate, (int)best);
         // Pieces of `each` units at most, none of two items, where that takes not much longer than equal pieces of the line of all
-        // units, of which many consist of two parts: the least such length that needs no more CTAs than there are.
+        // units, of which many consist of two parts.
         int each = 0;
-        int64_t ctas = min(units, (int64_t)kPrefixCtas);
-        auto pieces_of = [&](int g, int length) { return plan[g].rows * A.kv_heads * ((plan[g].tiles + length - 1) / length); };
+        const int equal = (int)((units + most_ctas - 1) / most_ctas);
+        int64_t ctas = min(units, (int64_t)most_ctas);
         if (items > 0 && items <= kPrefixCtas) {
-            int b = __reduce_max_sync(0xffffffffu, most), a = 0;  // more than kPrefixCtas pieces of a, no more of b
-            while (b - a > 1) {
-                const int mid = (a + b) >> 1;
-                int pieces = 0;
-                for (int g = lane; g < groups; g += 32) pieces += pieces_of(g, mid);
-                if (__reduce_add_sync(0xffffffffu, pieces) <= kPrefixCtas) b = mid;
-                else a = mid;
-            }
-            if (b <= (units + kPrefixCtas - 1) / kPrefixCtas + kPieceCost) {
-                each = b;
-                ctas = 0;
+            int64_t pieces = 0;
+            for (each = max(equal, 1); each <= equal + (int)kPieceCost; each += 1 + each / 16) {
+                pieces = 0;
                 for (int g0 = 0; g0 < groups; g0 += 32) {
                     const int g = g0 + lane;
-                    int64_t tc;
-                    const int64_t c0 = warp_exclusive(g < groups ? pieces_of(g, each) : 0, &tc);
-                    if (g < groups) plan[g].unit0 = ctas + c0;
-                    ctas += tc;
+                    int64_t more;
+                    const int64_t before = warp_exclusive(g < groups ? plan[g].rows * A.kv_heads * ((plan[g].tiles + each - 1) / each) : 0, &more);
+                    if (g < groups) plan[g].cta0 = (int)min(pieces + before, (int64_t)0x7FFFFFFF);
+                    pieces += more;
                 }
+                if (pieces <= most_ctas || pieces <= items) break;   // (an item is a piece at least)
             }
+            if (pieces <= max((int64_t)most_ctas, items) && pieces <= kPrefixCtas) ctas = pieces;
+            else each = 0;
         }
         if (lane == 0) {
             s_each = each;
@@ -229,6 +238,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
             s_own_units[warp] = units;
             s_own_longest[warp] = longest;
         }
+        asm volatile("bar.arrive 1, %0;" ::"n"(kPlanThreads) : "memory");
     }
     __syncthreads();
     const int each = s_each, ctas = s_head.ctas;
@@ -243,6 +253,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
             else b = mid;
         }
         return a;
+    };
+    auto item_at = [&](const PrefixGroup& G, int64_t item, int slot, int slots) {
+        const int rel = (int)(item - G.item0), tile = rel / A.kv_heads;
+        return PrefixItem{slot, slots, G.row0, tile * A.plan.tile_rows, G.n * A.rep, rel - tile * A.kv_heads, {0, 0}};
     };
     auto piece_at = [&](const PrefixGroup& G, int64_t item, int t, int n, int slot, int next) {
         const int rel = (int)(item - G.item0), tile = rel / A.kv_heads;
@@ -265,12 +279,12 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
         const PrefixGroup& G = plan[group_of(i)];
         if (each > 0) {  // the item's pieces, a CTA each
             const int k = (G.tiles + each - 1) / each;
-            A.plan.places[i] = make_int2((int)G.unit0 + (int)(i - G.item0) * k, k);
+            A.plan.item[i] = item_at(G, i, G.cta0 + (int)(i - G.item0) * k, k);
         } else {
             // the CTAs that share it: one that begins within it (or at its start) has it as its first piece, the one before it as a later one
             const int64_t u = G.unit0 + (i - G.item0) * G.tiles, end = u + G.tiles;
             const int c0 = piece_of(all_units, ctas, u), c1 = piece_of(all_units, ctas, end - 1);
-            A.plan.places[i] = make_int2((int)(c0 + i), c1 - c0 + 1);
+            A.plan.item[i] = item_at(G, i, (int)(c0 + i), c1 - c0 + 1);
             for (int c = c0; c <= c1; ++c) {
                 const int64_t a = cut(all_units, ctas, c), b = cut(all_units, ctas, c + 1), from = max(a, u);
                 const int next = b > end ? (int)(kPrefixCtas + i + 1) : -1;
@@ -283,11 +297,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
         int a = 0, b = groups;  // the last group whose pieces begin at or before CTA tid
         while (b - a > 1) {
             const int mid = (a + b) >> 1;
-            if (plan[mid].unit0 <= tid) a = mid;
+            if (plan[mid].cta0 <= tid) a = mid;
             else b = mid;
         }
         const PrefixGroup& G = plan[a];
-        const int k = (G.tiles + each - 1) / each, rel = tid - (int)G.unit0, item = rel / k, j = rel - item * k;
+        const int k = (G.tiles + each - 1) / each, rel = tid - G.cta0, item = rel / k, j = rel - item * k;
         const int t = G.tiles * j / k;
         A.plan.piece[tid] = piece_at(G, G.item0 + item, t, G.tiles * (j + 1) / k - t, tid, -1);
     }
@@ -351,6 +365,27 @@ constexpr int kRegsAll = 5 * (65536 / kThreads / 8 * 8);
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
+// The rows first, first + step, .. below `count` of a piece's row tile, a thread's part of each at `q` + its place: take(row, where, or null
+// past the group's last).
+template <typename T, typename F>
+__device__ __forceinline__ void copy_rows(const T* q, const PrefixParams& A, const PrefixPiece& seg, int d, int first, int step, int count,
+                                          F take) {
+    const int group = A.group, rows = seg.rows - seg.r0, r = seg.r0 + first;
+    int h = r % group;
+    const T* p = q + (int64_t)(seg.row0 + r / group) * A.q_stride + (int64_t)(seg.head * group + h) * d;
+    const int64_t move = (int64_t)(step / group) * A.q_stride + (step % group) * d, wrap = A.q_stride - (int64_t)group * d;
+    const int h_step = step % group;
+#pragma unroll 4
+    for (int row = first; row < count; row += step) {
+        take(row, row < rows ? p : nullptr);
+        p += move;
+        h += h_step;
+        if (h >= group) {
+            h -= group;
+            p += wrap;
+        }
+    }
+}
 // A row of partial sums, which the thread has put into shared memory, to global memory: a copy that runs by itself. The rows lie kRowBytes
 // apart there, so that a warp's writes meet all banks.
 template <int D> constexpr int kRowBytes = D * 4 + 16;
@@ -362,6 +397,20 @@ __device__ __forceinline__ void store_row_async(float* dst, const uint8_t* src) 
 }
 // .. until shared memory may be written again
 __device__ __forceinline__ void stored() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+// NaN where the row's tokens hold it, in a row of sums in shared memory. Rare, and kept out of the code that runs.
+template <int D>
+__device__ __noinline__ void mark_row(const PromptParams& A, int seq, int head, int lo, int hi, int from, int to, float* row) {
+#pragma unroll 1
+    for (int c = 0; c < D; c += 16) {
+        float y[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) y[k] = row[c + k];
+        mark_nan<D, 16>(A, seq, head, lo, hi, from, to, c, y);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) row[c + k] = y[k];
+    }
+}
 
 __device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }  // warps 0-7
 
@@ -381,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     using L = Layout<D>;
     constexpr uint32_t kColS = 0, kColO = 256;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (an offset, so that accesses are known to be to shared memory)
     uint8_t* s_q = smem;
     uint8_t* s_kv = smem + 2 * L::kTile;
     __shared__ __align__(8) uint64_t full[L::kSlots], empty[L::kSlots], meta_full[kMetaRing], meta_empty[kMetaRing];
@@ -460,61 +509,63 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         const int r = valid ? s_seg.r0 + (tid & 127) : 0;
         return max(__ldcg(A.plan.pos + s_seg.row0 + r / A.group) - A.window + 1, 0);
     };
-    // Queries, by warps 0-7: sixteen (or eight) lanes a row of D dims, eight dims a lane. The rows are copied to where their two terms will lie, all
-    // at once, and turned into them there, scaled by a power of two into fp16's range.
+    // Queries, by warps 0-7: sixteen (or eight) lanes a row of D dims, eight dims a lane. The rows are copied to where their two terms
+    // will lie, and turned into them there, scaled by a power of two into fp16's range.
     auto load_queries = [&]() {
         constexpr int kLanes = D / 8, kStep = 256 / kLanes;   // lanes of a row, rows at a time
         const int u = tid % kLanes;
-        int tok = (s_seg.r0 + tid / kLanes) / A.group, h = (s_seg.r0 + tid / kLanes) % A.group;
-        const int tok_step = kStep / A.group, h_step = kStep % A.group;
         uint8_t* const at = s_q + (u >> 3) * (kRows * 128);
-#pragma unroll 4
-        for (int row = tid / kLanes; row < kRows; row += kStep) {
-            uint8_t* dst = at + row * 128 + (((u & 7) ^ (row & 7)) << 4);
-            if (s_seg.r0 + row < s_seg.rows) {
-                const float* p = static_cast<const float*>(A.q) + (int64_t)(s_seg.row0 + tok) * A.q_stride +
-                                 (int64_t)(s_seg.head * A.group + h) * D + 8 * u;
-                copy16(dst, p);
-                copy16(dst + L::kTile, p + 4);
+        auto place_of = [&](int row) { return at + row * 128 + (((u & 7) ^ (row & 7)) << 4); };
+        copy_rows(static_cast<const float*>(A.q) + 8 * u, A, s_seg, D, tid / kLanes, kStep, kRows, [&](int row, const float* p) {
+            if (p) {
+                copy16(place_of(row), p);
+                copy16(place_of(row) + L::kTile, p + 4);
             } else {
-                *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<uint4*>(dst + L::kTile) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(place_of(row)) = *reinterpret_cast<uint4*>(place_of(row) + L::kTile) = make_uint4(0, 0, 0, 0);
             }
-            tok += tok_step;
-            h += h_step;
-            if (h >= A.group) {
-                h -= A.group;
-                ++tok;
-            }
-        }
+        });
         asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 4
-        for (int row = tid / kLanes; row < kRows; row += kStep) {
-            uint8_t* dst = at + row * 128 + (((u & 7) ^ (row & 7)) << 4);
-            float x[8];
-            *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(dst);
-            *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(dst + L::kTile);
-            float amax = 0.0f;
+        constexpr int kBatch = 4;  // rows read before the first is written: the chain of one is some hundred cycles long
+#pragma unroll 1
+        for (int row0 = tid / kLanes; row0 < kRows; row0 += kBatch * kStep) {
+            float x[kBatch][8], amax[kBatch];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float a = fabsf(x[i]);
-                if (a <= 3.402823466e38f) amax = fmaxf(amax, a);
+            for (int b = 0; b < kBatch; ++b) {
+                const uint8_t* p = place_of(row0 + b * kStep);
+                *reinterpret_cast<float4*>(x[b]) = *reinterpret_cast<const float4*>(p);
+                *reinterpret_cast<float4*>(x[b] + 4) = *reinterpret_cast<const float4*>(p + L::kTile);
             }
 #pragma unroll
-            for (int o = kLanes / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const int e = amax > 0.0f ? min(max(134 - (int)(__float_as_uint(amax) >> 23), -120), 120) : 0;
-            const float up = A.sign * exp2_int(e);
-            if (u == 0) s_c[row] = A.scale_log2 * exp2_int(-e);
-            uint32_t hi[4], lo[4];
+            for (int b = 0; b < kBatch; ++b) {
+                amax[b] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float a = x[2 * i] * up, b = x[2 * i + 1] * up;
-                const __half2 t = __floats2half2_rn(a, b);
-                const float2 f = __half22float2(t);
-                hi[i] = h2_bits(t);
-                lo[i] = h2_bits(__floats2half2_rn(a - f.x, b - f.y));
+                for (int i = 0; i < 8; ++i) {
+                    const float a = fabsf(x[b][i]);
+                    if (a <= 3.402823466e38f) amax[b] = fmaxf(amax[b], a);
+                }
             }
-            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(dst + L::kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+            for (int o = kLanes / 2; o; o >>= 1)
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) amax[b] = fmaxf(amax[b], __shfl_xor_sync(0xffffffffu, amax[b], o));
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const int row = row0 + b * kStep;
+                const int e = amax[b] > 0.0f ? min(max(134 - (int)(__float_as_uint(amax[b]) >> 23), -120), 120) : 0;
+                const float up = A.sign * exp2_int(e);
+                if (u == 0) s_c[row] = A.scale_log2 * exp2_int(-e);
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float p = x[b][2 * i] * up, q = x[b][2 * i + 1] * up;
+                    const __half2 t = __floats2half2_rn(p, q);
+                    const float2 f = __half22float2(t);
+                    hi[i] = h2_bits(t);
+                    lo[i] = h2_bits(__floats2half2_rn(p - f.x, q - f.y));
+                }
+                *reinterpret_cast<uint4*>(place_of(row)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(place_of(row) + L::kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
         }
         fence_proxy_async_smem();
         mbar_arrive(&q_full);
@@ -689,11 +740,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     float y[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) y[k] = k & 1 ? acc[(c + k) / 2].y : acc[(c + k) / 2].x;
-                    if (s_nan[1] >= 0)
-                        mark_nan<D, 16>(A, s_seg.leader, s_seg.head, lo, kv_hi - 1, kv0 + kToks * s_nan[0],
-                                        kv0 + kToks * (s_nan[1] + 1) - 1, c, y);
                     Vec<float>::store(reinterpret_cast<float*>(mine) + c, y);
                 }
+                if (s_nan[1] >= 0)
+                    mark_row<D>(A, s_seg.leader, s_seg.head, lo, kv_hi - 1, kv0 + kToks * s_nan[0], kv0 + kToks * (s_nan[1] + 1) - 1,
+                                reinterpret_cast<float*>(mine));
                 store_row_async<D>(A.plan.sums + place * D, mine);
                 A.plan.refs[place] = make_float2(m == -INFINITY ? m : weight_base(m, kTop), s_l[row]);
                 stored();
@@ -723,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix2_kernel(const __grid_const
     using L = Layout<D>;
     constexpr uint32_t kColS = 0, kColO = 256;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (an offset, so that accesses are known to be to shared memory)
     uint8_t* s_q = smem;
     uint8_t* s_kv = smem + 2 * L::kTile;
     __shared__ __align__(8) uint64_t full[L::kSlots], empty[L::kSlots], meta_full[kMetaRing], meta_empty[kMetaRing];
@@ -869,46 +920,51 @@ __global__ void __launch_bounds__(kThreads, 1) prefix2_kernel(const __grid_const
             {
                 constexpr int kLanes = D / 8, kStep = 256 / kLanes;
                 const int u = tid % kLanes;
-                int tok = (r0 + tid / kLanes) / A.group, h = (r0 + tid / kLanes) % A.group;
-                const int tok_step = kStep / A.group, h_step = kStep % A.group;
+                uint8_t* const q_at = s_q + (u >> 3) * (kRows * 128);
                 auto place_of = [&](int row) {
-                    return s_q + (row >> 7) * L::kTile + (u >> 3) * (kRows * 128) + (row & 127) * 128 + (((u & 7) ^ (row & 7)) << 4);
+                    return q_at + (row >> 7) * L::kTile + (row & 127) * 128 + (((u & 7) ^ (row & 7)) << 4);
                 };
-#pragma unroll 4
-                for (int qrow = tid / kLanes; qrow < 2 * kRows; qrow += kStep) {
-                    if (r0 + qrow < rows)
-                        copy16(place_of(qrow), static_cast<const __nv_bfloat16*>(A.q) + (int64_t)(s_seg.row0 + tok) * A.q_stride +
-                                                   (int64_t)(s_seg.head * A.group + h) * D + 8 * u);
-                    else
-                        *reinterpret_cast<uint4*>(place_of(qrow)) = make_uint4(0, 0, 0, 0);
-                    tok += tok_step;
-                    h += h_step;
-                    if (h >= A.group) {
-                        h -= A.group;
-                        ++tok;
-                    }
-                }
+                copy_rows(static_cast<const __nv_bfloat16*>(A.q) + 8 * u, A, s_seg, D, tid / kLanes, kStep, 2 * kRows,
+                          [&](int qrow, const __nv_bfloat16* p) {
+                              if (p) copy16(place_of(qrow), p);
+                              else *reinterpret_cast<uint4*>(place_of(qrow)) = make_uint4(0, 0, 0, 0);
+                          });
                 asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 4
-                for (int qrow = tid / kLanes; qrow < 2 * kRows; qrow += kStep) {
-                    uint4* const at = reinterpret_cast<uint4*>(place_of(qrow));
-                    const uint4 v = *at;
-                    uint32_t w[4] = {v.x, v.y, v.z, v.w}, top = 0;  // largest finite magnitude's bits
+                constexpr int kBatch = 4;
+#pragma unroll 1
+                for (int row0 = tid / kLanes; row0 < 2 * kRows; row0 += kBatch * kStep) {
+                    uint4 v[kBatch];
+                    uint32_t top[kBatch];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t a = w[k] & 0x7FFFu, b = (w[k] >> 16) & 0x7FFFu;
-                        if (a < 0x7F80u) top = max(top, a);
-                        if (b < 0x7F80u) top = max(top, b);
+                    for (int b = 0; b < kBatch; ++b) v[b] = *reinterpret_cast<const uint4*>(place_of(row0 + b * kStep));
+#pragma unroll
+                    for (int b = 0; b < kBatch; ++b) {
+                        // largest finite magnitude's bits
+                        const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
+                        top[b] = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t lo16 = w[k] & 0x7FFFu, hi16 = w[k] >> 16 & 0x7FFFu;
+                            if (lo16 < 0x7F80u) top[b] = max(top[b], lo16);
+                            if (hi16 < 0x7F80u) top[b] = max(top[b], hi16);
+                        }
                     }
 #pragma unroll
-                    for (int o = kLanes / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const int e = top > 0 ? min(max(134 - (int)(top >> 7), -120), 120) : 0;
-                    const float up = A.sign * exp2_int(e);
-                    if (u == 0) s_c[qrow] = A.scale_log2 * exp2_int(-e);
+                    for (int o = kLanes / 2; o; o >>= 1)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        w[k] = h2_bits(__floats2half2_rn(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up));
-                    *at = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int b = 0; b < kBatch; ++b) top[b] = max(top[b], __shfl_xor_sync(0xffffffffu, top[b], o));
+#pragma unroll
+                    for (int b = 0; b < kBatch; ++b) {
+                        const int qrow = row0 + b * kStep;
+                        const int e = top[b] > 0 ? min(max(134 - (int)(top[b] >> 7), -120), 120) : 0;
+                        const float up = A.sign * exp2_int(e);
+                        if (u == 0) s_c[qrow] = A.scale_log2 * exp2_int(-e);
+                        uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            w[k] = h2_bits(__floats2half2_rn(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up));
+                        *reinterpret_cast<uint4*>(place_of(qrow)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
                 }
             }
             fence_proxy_async_smem();
@@ -976,20 +1032,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefix2_kernel(const __grid_const
                 const int64_t place = (int64_t)s_seg.slot * (2 * kRows) + x * kRows + row;
                 // all products of both row tiles are done: the queries' and the tiles' place is free
                 uint8_t* const mine = s_q + (x * kRows + row) * kRowBytes<D>;
-#pragma unroll 1
-                for (int q = 0; q < D / 32; ++q) {
-                    uint32_t v[32];
-                    float y[32];
-                    tmem_ld32(o_at + 32 * q, v);
-                    tmem_wait_ld();
+                uint32_t v[2][32];
+                tmem_ld32(o_at, v[0]);
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) y[c] = __uint_as_float(v[c]);
-                    if (s_nan[1] >= 0 && valid)
-                        mark_nan<D, 32>(A, s_seg.leader, s_seg.head, lo, kv_hi - 1, kv0 + kToks * s_nan[0],
-                                        kv0 + kToks * (s_nan[1] + 1) - 1, 32 * q, y);
-                    if (valid) Vec<float>::store(reinterpret_cast<float*>(mine) + 32 * q, y);
+                for (int q = 0; q < D / 32; ++q) {
+                    tmem_wait_ld();
+                    if (q + 1 < D / 32) tmem_ld32(o_at + 32 * (q + 1), v[(q + 1) & 1]);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4)
+                        *reinterpret_cast<uint4*>(mine + 128 * q + 4 * c) =
+                            make_uint4(v[q & 1][c], v[q & 1][c + 1], v[q & 1][c + 2], v[q & 1][c + 3]);
                 }
                 if (valid) {
+                    if (s_nan[1] >= 0)
+                        mark_row<D>(A, s_seg.leader, s_seg.head, lo, kv_hi - 1, kv0 + kToks * s_nan[0],
+                                    kv0 + kToks * (s_nan[1] + 1) - 1, reinterpret_cast<float*>(mine));
                     store_row_async<D>(A.plan.sums + place * D, mine);
                     A.plan.refs[place] = make_float2(ref == -INFINITY ? ref : weight_base(ref, kTop - kSlack), l);
                     stored();
@@ -1043,7 +1100,7 @@ cudaError_t launch_typed(const PrefixParams& P, int ctas, cudaStream_t stream) {
 // ---- both parts ---------------------------------------------------------------------------------------------------
 // Each row's sums of its own tokens and of the pieces of the shared ones, to the largest of their references; 16 or 32 lanes a row of a
 // row tile, four dims a lane. Bound by reading the pieces, from L2.
-constexpr int kJoinRows = 16;
+constexpr int kJoinRows = 8;
 
 struct JoinParams {
     PrefixPlan plan;
@@ -1058,35 +1115,22 @@ __device__ __forceinline__ float group_max(float x, int lanes) {
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinRows * D / 4) prefix_join_kernel(const __grid_constant__ JoinParams A) {
     constexpr int kLanes = D / 4;
-    __shared__ PrefixGroup s_group;
     __shared__ float s_w[kJoinRows][kPrefixCtas];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tid = threadIdx.x, lane = tid & 31, parts = A.plan.tile_rows / kJoinRows;
+    const int tid = threadIdx.x, parts = A.plan.tile_rows / kJoinRows;
     const int64_t item = blockIdx.x / parts;
-    const int2 place = item < A.plan.items ? __ldcg(A.plan.places + item) : make_int2(0, 0);
+    const int4* p = reinterpret_cast<const int4*>(A.plan.item + item);
+    const int4 i0 = __ldcg(p), i1 = __ldcg(p + 1);
     if (item >= __ldcg(&A.plan.head->items)) return;
-    if (tid < 32) {
-        int lo = 0, hi = A.plan.groups - 1;  // the last group that begins at or before the item (one without items begins where the next does)
-        while (hi - lo >= 32) {
-            const int step = (hi - lo) / 32 + 1, i = lo + lane * step;
-            const unsigned hit = __ballot_sync(0xffffffffu, i <= hi && __ldcg(&A.plan.group[i].item0) <= item);
-            lo += max(31 - __clz(hit), 0) * step;
-            hi = min(hi, lo + step - 1);
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, lo + lane <= hi && __ldcg(&A.plan.group[lo + lane].item0) <= item);
-        lo += max(31 - __clz(hit), 0);
-        if (lane < 3) reinterpret_cast<int4*>(&s_group)[lane] = __ldcg(reinterpret_cast<const int4*>(A.plan.group + lo) + lane);
-    }
-    __syncthreads();
-    const int rel = (int)(item - s_group.item0), tile = rel / A.kv_heads, head = rel - tile * A.kv_heads;
-    const int local = (int)(blockIdx.x - item * parts) * kJoinRows + tid / kLanes, r = tile * A.plan.tile_rows + local;
+    const PrefixItem I{i0.x, i0.y, i0.z, i0.w, i1.x, i1.y, {0, 0}};
+    const int local = (int)(blockIdx.x - item * parts) * kJoinRows + tid / kLanes, r = I.r0 + local;
     const int c = 4 * (tid % kLanes);
-    const int tok = s_group.row0 + r / A.group, h = head * A.group + r % A.group;
+    const int tok = I.row0 + r / A.group, h = I.head * A.group + r % A.group;
     // (a plan that another call on this workspace has written over leads to no place outside it)
-    const bool there = r >= 0 && r < s_group.n * A.group && tok >= 0 && tok < A.m && head >= 0 && place.x >= 0 && place.y > 0 &&
-                       place.y <= kPrefixCtas && place.x + place.y <= A.plan.slots;
-    const int64_t row = (int64_t)tok * A.kv_heads * A.group + h, at = (int64_t)place.x * A.plan.tile_rows + local;
+    const bool there = r >= 0 && r < I.rows && tok >= 0 && tok < A.m && I.head >= 0 && I.head < A.kv_heads && I.slot >= 0 && I.slots > 0 &&
+                       I.slots <= kPrefixCtas && I.slot + I.slots <= A.plan.slots;
+    const int64_t row = (int64_t)tok * A.kv_heads * A.group + h, at = (int64_t)I.slot * A.plan.tile_rows + local;
     float2 own = make_float2(-INFINITY, 0.0f);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (there) {
@@ -1095,7 +1139,7 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) prefix_join_kernel(const __
     }
     // the pieces' weights, a lane each at a time
     float top = own.x, den = 0.0f;
-    for (int k = tid % kLanes; there && k < place.y; k += kLanes) {
+    for (int k = tid % kLanes; there && k < I.slots; k += kLanes) {
         const float2 f = __ldcg(A.plan.refs + at + (int64_t)k * A.plan.tile_rows);
         const float was = top;
         top = fmaxf(top, f.x);
@@ -1116,7 +1160,7 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) prefix_join_kernel(const __
     const float* x = A.plan.sums + at * D + c;
     const int64_t step = (int64_t)A.plan.tile_rows * D;
 #pragma unroll 8
-    for (int k = 0; k < place.y; ++k) {
+    for (int k = 0; k < I.slots; ++k) {
         const float4 v = __ldcg(reinterpret_cast<const float4*>(x + k * step));
         const float w = ex2(s_w[tid / kLanes][k] - use);
         sum.x = fmaf(w, v.x, sum.x); sum.y = fmaf(w, v.y, sum.y);
@@ -1161,7 +1205,7 @@ size_t layout(int batch, int groups, int m, int rep, int kv_heads, int head_dim,
     plan->group = reinterpret_cast<PrefixGroup*>(part(sizeof(PrefixGroup) * (size_t)groups));
     plan->seq = reinterpret_cast<int2*>(part(sizeof(int2) * (size_t)batch));
     plan->piece = reinterpret_cast<PrefixPiece*>(part(sizeof(PrefixPiece) * (size_t)slots));
-    plan->places = reinterpret_cast<int2*>(part(sizeof(int2) * (size_t)items));
+    plan->item = reinterpret_cast<PrefixItem*>(part(sizeof(PrefixItem) * (size_t)items));
     plan->own = reinterpret_cast<OwnTile*>(part(sizeof(OwnTile) * (size_t)owns));
     plan->pos = reinterpret_cast<int*>(part(sizeof(int) * (size_t)m));
     plan->refs = reinterpret_cast<float2*>(part(sizeof(float2) * (size_t)slots * tile_rows));

@@ -17,8 +17,10 @@ struct PrefixGroup {
     int full_lo;        // from here on every row sees them
     int leader;         // the sequence whose row of the page table is read
     int tiles, rows;    // units of 128 tokens, row tiles (0: nothing is shared)
-    int64_t unit0;      // its units' place on the line of all units, or its first CTA
+    int64_t unit0;      // its units' place on the line of all units
     int64_t item0;      // its first item
+    int cta0;           // its first CTA, where pieces are not of two items
+    int pad;
 };
 // What a CTA computes of an item.
 struct alignas(16) PrefixPiece {
@@ -31,6 +33,12 @@ struct alignas(16) PrefixPiece {
     int next;                 // the CTA's next piece (an index above this one's), or -1
     int pad;
 };
+// Where an item's partial results are, and whose they are.
+struct alignas(16) PrefixItem {
+    int slot, slots;          // the first one, and how many
+    int row0, r0, rows;       // as in PrefixPiece
+    int head, pad[2];
+};
 // A row tile of a sequence and what it sees of the sequence's own tokens.
 struct alignas(16) OwnTile {
     int seq, start, n, len;   // as SeqSpan
@@ -42,7 +50,7 @@ struct PrefixHead {
     int ctas;            // that compute the shared part
     int own_tiles;       // row tiles of the sequences
     int own_longest;     // units of the longest
-    unsigned next;       // the next (row tile, kv head) to be taken, beyond one for each CTA
+    unsigned next;       // the next (row tile, kv head) to be taken
     int64_t own_units;   // of all (row tile, kv head)
 };
 struct PrefixPlan {
@@ -50,7 +58,7 @@ struct PrefixPlan {
     PrefixGroup* group;   // [groups]
     int2* seq;            // [batch]: group (-1: none), tokens taken from its shared part
     PrefixPiece* piece;   // [kPrefixCtas + items]: a CTA's first piece, then the pieces that begin an item after another's in a CTA
-    int2* places;         // [items]: first slot, slots
+    PrefixItem* item;     // [items]
     OwnTile* own;         // [own]
     int* pos;             // [m]: positions of the groups' rows, where there is a window
     float* sums;          // [slots][tile_rows][head_dim]
