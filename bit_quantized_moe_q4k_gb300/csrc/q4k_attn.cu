@@ -31,14 +31,13 @@
 #include <atomic>
 #include <chrono>
 
-#include "q4k_paged.cuh"
-#include "q4k_prefix.cuh"
+#include "q4k_attn_few.cuh"
 
 namespace q4k {
+using namespace few;
 namespace {
 
 constexpr int kAttnWarps = 4;
-constexpr int kChunk = 16;                    // tokens a warp takes at a time
 constexpr int kUnit = kChunk * kAttnWarps;    // tokens of one unit of work
 // Units that starting and ending a tile are worth. Ragged batches of 64 up to 8192 tokens, 256 up to 2000, 40 up to
 // 30000: 102, 87, 184 us with 4; 96, 76, 174 with 10; 97, 79, 173 with 16.
@@ -53,7 +52,6 @@ constexpr int kLeast = 4;                      // units of a cluster's part of a
 constexpr int kMaxParts = 512;                // CTAs that the workspace serves
 constexpr int kJoinCost = 8;                  // units that joining a tile is worth (16: 8000 tokens 15.4 -> 17.5 us)
 static_assert(kJoinCost >= kLeast, "a tile that is shared has a unit for each cluster");
-constexpr int kListed = 16;                   // units up to which a tile is taken whole from the plan's list, whatever a CTA's share
 constexpr int kOneLevel = 16;                 // up to this many pieces of a tile are joined at once (4: 16000 tokens 17 -> 21 us)
 constexpr int kTickets = 2 * kMaxParts;       // arrival counters before the partial results: by group of pieces, by tile
 
@@ -73,51 +71,7 @@ struct AttnParams {
     unsigned long long tag;  // this launch's counters carry it in their high 48 bits: others count as 0
     int parts;          // CTAs the partial buffer holds
     int* err_flag;
-    PrefixPlan pre;     // with SH: what the tokens that sequences share gave (q4k_prefix.cu)
 };
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void mma_16816_zero(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
-}
-// Two fp32 operations in one instruction, each rounded to nearest.
-__device__ __forceinline__ void add2(float2& a, float x, float y) {
-    float2 b = make_float2(x, y);
-    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(reinterpret_cast<uint64_t&>(a)) : "l"(reinterpret_cast<uint64_t&>(b)));
-}
-__device__ __forceinline__ void fma2(float2& a, float x, float y, float scale) {  // a += (x, y) * scale
-    float2 b = make_float2(x, y), c = make_float2(scale, scale);
-    asm("fma.rn.f32x2 %0, %1, %2, %0;"
-        : "+l"(reinterpret_cast<uint64_t&>(a))
-        : "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
-}
-__device__ __forceinline__ void mul2(float2& a, float x) {
-    float2 b = make_float2(x, x);
-    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(reinterpret_cast<uint64_t&>(a)) : "l"(reinterpret_cast<uint64_t&>(b)));
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// 0x80 in each byte that is one of e4m3's two NaN codes (0x7F, 0xFF).
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t x) { return ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
 // The work of one sequence: `tiles` row tiles per kv head, each kTileCost units of nothing (so that a
 // piece of many short tiles is not longer than one of a few long ones) and `units` units of kUnit
@@ -127,8 +81,7 @@ struct SeqWork {
     int lo, tiles, units;
     int64_t total;
 };
-// SH: a sequence's work begins behind the tokens that it shares, whose part is computed elsewhere.
-template <int RT, int CL, bool SH>
+template <int RT, int CL>
 __device__ __forceinline__ SeqWork seq_work(const AttnParams& A, int i) {
     SeqWork w{};
     if (i >= A.B.batch) return w;
@@ -138,7 +91,6 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& A, int i) {
     if (w.s.n == 0 || (int64_t)w.s.n * A.group > A.max_rows) return w;
     const int first = max(w.s.len - w.s.n, 0);
     w.lo = A.window > 0 ? (max(first - A.window + 1, 0) & ~(kChunk - 1)) : 0;
-    if constexpr (SH) w.lo = max(w.lo, min(__ldcg(A.pre.seq + i).y, max(first, 0)) & ~(kChunk - 1));
     w.tiles = (w.s.n * A.group + RT - 1) / RT;
     w.units = max((w.s.len - w.lo + CL * kUnit - 1) / (CL * kUnit), 1);  // an empty sequence: its rows are zeroed
     w.total = (int64_t)w.tiles * A.kv_heads * (kTileCost + w.units);
@@ -163,12 +115,12 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v) {  // inclusive
 }
 // Move the cursor to the sequence that holds u (u >= c.begin; false past the end). `mine`: the work
 // of sequence `lane`, read once (it is all there is up to 32 sequences).
-template <int RT, bool SH>
+template <int RT>
 __device__ __forceinline__ bool seek(const AttnParams& A, int64_t u, const SeqWork& mine, Cursor* c) {
     const int lane = threadIdx.x & 31;
     int64_t acc = c->begin;
     for (int base = c->seq & ~31; base < A.B.batch; base += 32) {
-        SeqWork w = base == 0 ? mine : seq_work<RT, 1, SH>(A, base + lane);
+        SeqWork w = base == 0 ? mine : seq_work<RT, 1>(A, base + lane);
         if (base + lane < c->seq) w.total = 0;
         const int64_t inc = warp_scan(w.total);
         const unsigned hit = __ballot_sync(0xffffffffu, u < acc + inc);
@@ -189,10 +141,10 @@ __device__ __forceinline__ bool seek(const AttnParams& A, int64_t u, const SeqWo
     }
     return false;
 }
-template <int RT, bool SH>
+template <int RT>
 __device__ __forceinline__ int64_t total_work(const AttnParams& A, const SeqWork& mine) {
     int64_t t = mine.total;
-    for (int i = 32 + (threadIdx.x & 31); i < A.B.batch; i += 32) t += seq_work<RT, 1, SH>(A, i).total;
+    for (int i = 32 + (threadIdx.x & 31); i < A.B.batch; i += 32) t += seq_work<RT, 1>(A, i).total;
 #pragma unroll
     for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     return t;
@@ -208,12 +160,12 @@ struct TilePart {
     int first, j;  // its first cluster; this one's number among them
     bool more;     // there are more tiles than clusters, which then walk over them, a whole one at a time
 };
-template <int RT, int CL, bool SH>
+template <int RT, int CL>
 __device__ __forceinline__ bool tile_part(const AttnParams& A, const SeqWork& mine, int c, int clusters, Cursor* cur, TilePart* p) {
     const int lane = threadIdx.x & 31;
     int64_t tiles = (int64_t)mine.tiles * A.kv_heads, units = tiles * mine.units;
     for (int i = 32 + lane; i < A.B.batch; i += 32) {
-        const SeqWork w = seq_work<RT, CL, SH>(A, i);
+        const SeqWork w = seq_work<RT, CL>(A, i);
         tiles += (int64_t)w.tiles * A.kv_heads;
         units += (int64_t)w.tiles * A.kv_heads * w.units;
     }
@@ -226,7 +178,7 @@ __device__ __forceinline__ bool tile_part(const AttnParams& A, const SeqWork& mi
     p->more = tiles > clusters;
     int64_t acc = 0;
     for (int base = 0; base < A.B.batch; base += 32) {
-        const SeqWork w = base == 0 ? mine : seq_work<RT, CL, SH>(A, base + lane);
+        const SeqWork w = base == 0 ? mine : seq_work<RT, CL>(A, base + lane);
         const int k = w.tiles ? min(1 + (int)div_pos(w.units * spare, units), w.units <= kJoinCost ? 1 : w.units / kLeast) : 1;
         const int64_t own = (int64_t)w.tiles * A.kv_heads * k, inc = warp_scan(own);
         const unsigned hit = __ballot_sync(0xffffffffu, c < acc + inc);
@@ -296,69 +248,9 @@ __device__ __forceinline__ float peer_f32(const float* p, int rank) {
     return v;
 }
 
-// The ring of a warp: kRing stages of kPair chunks, and each chunk's page: K's scale, V's scale as
-// log2 and reciprocal, whether there is such a page.
-constexpr int kRing = 2, kPair = 2;
-template <int D> constexpr int kSlot = 2 * kChunk * D;        // a chunk: K's rows, then V's
-template <int D> constexpr int kStage = kPair * kSlot<D>;
-
-// Where 16-byte unit `u` of row `r` lies in a chunk's K or V part, as 128-byte lines of 8 units: the
-// unit's place in its line is xored with the row's parity times 4 (K at head_dim 128: a read
-// meets rows of both parities) or with twice the row's group of four (V: a read meets all four groups).
-template <int D> __device__ __forceinline__ int k_unit(int r, int u) {
-    return 16 * (D == 128 ? 8 * r + (u ^ ((r & 1) << 2)) : 4 * r + u);
-}
-template <int D> __device__ __forceinline__ int v_unit(int r, int u) {
-    const int x = D / 16 * r + u;
-    return 16 * (x ^ ((r >> 2) << 1));
-}
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
-struct ChunkMeta {
-    float ks, ev, inv;
-    int ok;
-};
-
-// The pages of a warp's chunks, 32 at a time: lane i holds those of chunks i, 32 + i, ... Page ids are
-// read two batches ahead and scales one, so that no issue waits for them.
-struct PageAhead {
-    int p0, p1, p2;
-    float ks0, vs0, ks1, vs1;
-};
-
-// log2 of a page's V scale: exact for the powers of two that the append writes.
-__device__ __forceinline__ float scale_log2_of(float s) {
-    const uint32_t b = __float_as_uint(s);
-    const float e = (float)((int)(b >> 23) - 127);
-    return (b & 0x7FFFFFu) ? e + log2f(__uint_as_float((b & 0x7FFFFFu) | 0x3F800000u)) : e;
-}
-
-// What P and so the sums of a tile are relative to, for the running maximum m (x - reference is 15 at most).
-__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? m : __fadd_ru(m, -15.0f); }
-
-// The (row tile, kv head) `t` of the plan's list: false past the last.
-__device__ __forceinline__ bool listed_tile(const AttnParams& A, int64_t t, int tiles, Cursor* c, TilePart* p) {
-    const int64_t i = t / A.kv_heads;
-    if (i >= tiles) return false;
-    const int4* at = reinterpret_cast<const int4*>(A.pre.own + i);
-    const int4 a = __ldcg(at), b = __ldcg(at + 1);
-    c->seq = min(max(a.x, 0), A.B.batch - 1);   // (not believed as far as addresses go: the workspace may be written over)
-    c->w.s.start = min(max(a.y, 0), A.B.m);
-    c->w.s.n = min(max(a.z, 0), A.B.m - c->w.s.start);
-    c->w.s.len = min(max(a.w, 0), A.B.max_pages << A.B.page_shift);
-    c->w.lo = max(b.x, 0) & ~(kChunk - 1);
-    c->w.units = b.y;
-    p->index = b.z * A.kv_heads + (int)(t - i * A.kv_heads);
-    p->k = 1;
-    p->j = 0;
-    return true;
-}
-
 // RT: query rows of a tile. fp32: 8 (two fp16 terms fill the 16 rows); bf16: 8 where a tile has no
 // more rows, else 16.
-template <typename T, int D, int RT, int CL, bool SH>
+template <typename T, int D, int RT, int CL>
 __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const __grid_constant__ AttnParams A) {
     constexpr bool HL = sizeof(T) == 4;           // two fp16 terms
     constexpr int NR = RT / 8;                    // rows of a thread: g, and g + 8
@@ -368,9 +260,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
     float* s_o = reinterpret_cast<float*>(s_mem); // [warps][RT][D], over the rings once they are read
     __shared__ float s_m[kAttnWarps * RT], s_l[kAttnWarps * RT];
     __shared__ ChunkMeta s_meta[kAttnWarps][kRing * kPair];
-    // With SH the kernel before computes the shared part and began when all before it had ended (it waited for the plan's
-    // kernel). This one reads nothing of it and runs beside it.
-    if constexpr (!SH) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int rank = CL > 1 ? cluster_rank() : 0, my_piece = CL > 1 ? (int)blockIdx.x / CL : (int)blockIdx.x;
@@ -385,32 +275,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
     __shared__ int s_pieces;
     __shared__ TilePart s_tile;
     __shared__ bool s_by_tile;
-    __shared__ bool s_shares;            // the tile's sequence shares a part, which is joined to these sums afterwards
     __shared__ struct { int c0, slot0, size, groups, first, count, last; } s_join;
-    // Behind shared prefixes the plan has a list of the row tiles. While no tile is much longer than a CTA's share of the work, the CTAs
-    // take whole ones from it, each the next that is left as it has done with one.
-    int list = 0;
-    if constexpr (SH && CL == 1) {
-        const int4 h = __ldcg(reinterpret_cast<const int4*>(&A.pre.head->ctas));
-        const int64_t load = __ldcg(&A.pre.head->own_units) / gridDim.x;
-        list = h.z <= max((int64_t)kListed, load) ? min(max(h.y, 0), (int)min(A.pre.owns, (int64_t)0x7FFFFFFF)) : 0;
-    }
-    if (SH && CL == 1 && list > 0) {
-        if (threadIdx.x == 0) {
-            Cursor c{};
-            TilePart p{};
-            s_u[0] = 0;
-            s_u[1] = listed_tile(A, atomicAdd(&A.pre.head->next, 1u), list, &c, &p);
-            s_cur = c;
-            s_tile = p;
-            s_by_tile = true;
-        }
-    } else if (warp == 0) {
-        const SeqWork mine = seq_work<RT, CL, SH>(A, lane);
+    if (warp == 0) {
+        const SeqWork mine = seq_work<RT, CL>(A, lane);
         int longest = mine.units;
         int64_t tiles = (int64_t)mine.tiles * A.kv_heads;
         for (int i = 32 + lane; CL == 1 && i < A.B.batch; i += 32) {
-            const SeqWork w = seq_work<RT, CL, SH>(A, i);
+            const SeqWork w = seq_work<RT, CL>(A, i);
             longest = max(longest, w.units);
             tiles += (int64_t)w.tiles * A.kv_heads;
         }
@@ -424,7 +295,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
         if (by_tile) {
             Cursor c{};
             TilePart p{};
-            const bool any = tile_part<RT, CL, SH>(A, mine, my_piece, gridDim.x / CL, &c, &p);
+            const bool any = tile_part<RT, CL>(A, mine, my_piece, gridDim.x / CL, &c, &p);
             if (lane == 0) {
                 s_cur = c;
                 s_tile = p;
@@ -433,7 +304,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
             }
         } else {
             s_work[lane] = mine;
-            const int64_t total = total_work<RT, SH>(A, mine);
+            const int64_t total = total_work<RT>(A, mine);
             // more such tiles than CTAs: pieces are not shorter than a whole one
             const int64_t least = longest <= kJoinCost ? kTileCost + longest : 1;
             const int pieces = (int)min((int64_t)min((int)gridDim.x, A.parts), div_pos(total + least - 1, least));
@@ -441,7 +312,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
             const int64_t u0 = any ? piece_begin(total, pieces, my_piece) : 0;
             const int64_t u1 = any ? piece_begin(total, pieces, my_piece + 1) : 0;
             Cursor c{};
-            if (any) seek<RT, SH>(A, u0, mine, &c);
+            if (any) seek<RT>(A, u0, mine, &c);
             if (lane == 0) {
                 s_cur = c;
                 s_u[0] = u0;
@@ -458,8 +329,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
     while (s_u[0] < s_u[1]) {
         const SeqSpan sp = s_cur.w.s;
         const int w_lo = s_cur.w.lo, seq = s_cur.seq;
-        unsigned taken = 0;  // the tile after this one: asked for now, looked at when this one is done
-        if (SH && CL == 1 && list > 0 && threadIdx.x == 0) taken = atomicAdd(&A.pre.head->next, 1u);
         int tile, head, ua, ub, step = 0;
         const bool by_tile = CL > 1 || s_by_tile;
         if (by_tile) {
@@ -577,7 +446,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                 s_meta[warp][k % kRing * kPair + c] = ChunkMeta{ah.ks0, scale_log2_of(ah.vs0), 1.0f / ah.vs0, ah.p0 >= 0};
         };
         for (int k = 0; k < kRing; ++k) issue(k);
-        if (SH && threadIdx.x == 64) s_shares = __ldcg(A.pre.seq + seq).x >= 0;
         scales_of(ah.p0, ah.ks0, ah.vs0);
         scales_of(ah.p1, ah.ks1, ah.vs1);
 
@@ -890,19 +758,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
         // a tile that begins in this piece, but not at its start, goes to the second slot
         constexpr int kPart = RT * (D + 2);
         float* part = A.part + ((int64_t)my_piece * 2 + (not_first ? 1 : 0)) * kPart;
-        // The row's place among all query rows, for sums that are joined to the shared part's.
-        auto leave = [&](int row, int c, float den, float m) {
-            const int64_t at = (int64_t)(sp.start + row / A.group) * A.kv_heads * A.group + head * A.group + row % A.group;
-            if (c == 0) A.pre.own_refs[at] = make_float2(reference(m), den);
-            return A.pre.own_sums + at * D + c;
-        };
-        auto store_row = [&](int r, int c, const float4& acc, float den, float m) {
+        auto store_row = [&](int r, int c, const float4& acc, float den) {
             const int row = tile * RT + r;
             if (row >= rows) return;
-            if (SH && s_shares) {
-                *reinterpret_cast<float4*>(leave(row, c, den, m)) = acc;
-                return;
-            }
             const float iv = den == 0.0f ? 0.0f : 1.0f / den;  // 0: the row sees nothing
             const float y[4] = {acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv};
             Vec<T>::store(static_cast<T*>(A.out) + (int64_t)(sp.start + row / A.group) * A.out_stride +
@@ -935,7 +793,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                 continue;
             }
             if (whole) {
-                store_row(r, c, acc, den, m);
+                store_row(r, c, acc, den);
             } else {
                 *reinterpret_cast<float4*>(part + r * D + c) = acc;
                 if (c == 0) {
@@ -977,10 +835,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                         part[RT * D + RT + r] = den;
                     }
                 } else if (const int row = tile * RT + r; row < rows) {
-                    if (SH && s_shares) {
-                        *leave(row, c, den, m) = acc;
-                        continue;
-                    }
                     const float y = den == 0.0f ? 0.0f : acc / den;  // 0: the row sees nothing
                     T* o = static_cast<T*>(A.out) + (int64_t)(sp.start + row / A.group) * A.out_stride +
                            (int64_t)(head * A.group + row % A.group) * D + c;
@@ -1031,7 +885,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
                         acc.z = fmaf(wt, v.z, acc.z); acc.w = fmaf(wt, v.w, acc.w);
                     }
                     if (to_out) {
-                        store_row(r, c, acc, den, m);
+                        store_row(r, c, acc, den);
                         continue;
                     }
                     float* x = piece(first);
@@ -1051,21 +905,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
         }
         not_first = true;
         sync_all<CL>();  // what lies over the rings has been read, by the cluster too
-        if (SH && CL == 1 && list > 0) {
-            if (threadIdx.x == 0) {
-                Cursor c{};
-                TilePart p{};
-                s_u[1] = listed_tile(A, taken, list, &c, &p);
-                s_cur = c;
-                s_tile = p;
-            }
-        } else if (by_tile) {
+        if (by_tile) {
             if (!s_tile.more) break;
             if (warp == 0) {
                 Cursor c{};
                 TilePart p{};
                 const int clusters = gridDim.x / CL, next = s_tile.first + clusters;
-                const bool any = tile_part<RT, CL, SH>(A, seq_work<RT, CL, SH>(A, lane), next, clusters, &c, &p);
+                const bool any = tile_part<RT, CL>(A, seq_work<RT, CL>(A, lane), next, clusters, &c, &p);
                 if (lane == 0) {
                     s_cur = c;
                     s_tile = p;
@@ -1076,7 +922,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
             const int64_t u = s_u[0] + step;
             Cursor c = s_cur;
             __syncwarp();
-            const bool more = u < s_u[1] && (u < c.begin + c.w.total || seek<RT, SH>(A, u, s_work[lane], &c));
+            const bool more = u < s_u[1] && (u < c.begin + c.w.total || seek<RT>(A, u, s_work[lane], &c));
             if (lane == 0) {
                 s_cur = c;
                 s_u[0] = more ? u : s_u[1];
@@ -1084,12 +930,11 @@ __global__ void __launch_bounds__(32 * kAttnWarps, kCtasPerSm) attn_kernel(const
         }
         __syncthreads();
     }
-    if constexpr (SH) asm volatile("griddepcontrol.wait;" ::: "memory");  // what comes after this kernel comes after that one, too
 }
 
 constexpr int kCluster = 8;
 
-template <typename T, int D, int RT, int CL, bool SH>
+template <typename T, int D, int RT, int CL>
 cudaError_t launch_cluster(const AttnParams& P, int max_len, cudaStream_t stream, int64_t segs, bool* fits) {
     const size_t rings = (size_t)kAttnWarps * kRing * kStage<D>, join = (size_t)(kAttnWarps + 1) * RT * D * sizeof(float);
     const size_t smem = rings > join ? rings : join;
@@ -1112,13 +957,13 @@ cudaError_t launch_cluster(const AttnParams& P, int max_len, cudaStream_t stream
     cfg.numAttrs = CL > 1 ? 2 : 1;
     int most = clusters[dev].load(std::memory_order_relaxed);
     if (most == 0) {
-        e = cudaFuncSetAttribute(attn_kernel<T, D, RT, CL, SH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = cudaFuncSetAttribute(attn_kernel<T, D, RT, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         most = P.parts;
         if (CL > 1) {
             cfg.gridDim = dim3(CL);
             int n = 0;
-            e = cudaOccupancyMaxActiveClusters(&n, attn_kernel<T, D, RT, CL, SH>, &cfg);
+            e = cudaOccupancyMaxActiveClusters(&n, attn_kernel<T, D, RT, CL>, &cfg);
             if (e != cudaSuccess) return e;
             most = n < 1 ? 1 : n < P.parts ? n : P.parts;
         }
@@ -1133,11 +978,11 @@ cudaError_t launch_cluster(const AttnParams& P, int max_len, cudaStream_t stream
     int64_t grid = segs * (units <= kJoinCost ? 1 : CL > 1 ? units / kLeast : kTileCost + units);
     if (grid > most) grid = most;
     cfg.gridDim = dim3((unsigned)(grid * CL));
-    return cudaLaunchKernelEx(&cfg, attn_kernel<T, D, RT, CL, SH>, P);
+    return cudaLaunchKernelEx(&cfg, attn_kernel<T, D, RT, CL>, P);
 }
 
-template <typename T, int D, int RT, bool SH>
-cudaError_t launch_rows(const AttnParams& P, int64_t max_rows, int max_len, cudaStream_t stream) {
+template <typename T, int D, int RT>
+cudaError_t launch_typed(const AttnParams& P, int64_t max_rows, int max_len, cudaStream_t stream) {
     const int64_t held = (int64_t)P.B.max_pages << P.B.page_shift;  // no sequence is longer than its table's row
     if (max_len > held) max_len = (int)held;
     // An upper bound of the row tiles: each sequence's last one may be part filled, and none has more than max_rows.
@@ -1147,14 +992,9 @@ cudaError_t launch_rows(const AttnParams& P, int64_t max_rows, int max_len, cuda
     // Clusters where each tile finds one (51 at once on a GB300). 4 kv heads of 8 rows of fp32: one sequence of 1000 tokens
     // 8.5 us with, 12.9 without; of 16000 17.3 and 22.7; ten of 2000 13.0 and 17.6; 64 tiles of 1000 20.6 and 17.6.
     bool fits = true;
-    const cudaError_t e = launch_cluster<T, D, RT, kCluster, SH>(P, max_len, stream, segs, &fits);
+    const cudaError_t e = launch_cluster<T, D, RT, kCluster>(P, max_len, stream, segs, &fits);
     if (e != cudaSuccess || fits) return e;
-    return launch_cluster<T, D, RT, 1, SH>(P, max_len, stream, segs, nullptr);
-}
-
-template <typename T, int D, int RT>
-cudaError_t launch_typed(const AttnParams& P, int64_t max_rows, int max_len, cudaStream_t stream) {
-    return P.pre.seq ? launch_rows<T, D, RT, true>(P, max_rows, max_len, stream) : launch_rows<T, D, RT, false>(P, max_rows, max_len, stream);
+    return launch_cluster<T, D, RT, 1>(P, max_len, stream, segs, nullptr);
 }
 
 // A value that no other launch of the process has (and, from a start that differs, hardly any other process's).
@@ -1188,17 +1028,10 @@ cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int6
                                                       out_stride, err_flag, stream);
         if (e != cudaSuccess || !few) return e;
     }
-    // bf16: tiles of 8 rows where a sequence's rows fit one (half the softmax), else 16; next to prompts
-    // the other sequences mostly decode
-    const int own_rows = dtype == Q4K_F32 || (prompts ? q_heads / kv_heads : most) <= 8 ? 8 : 16;
+    if (shared)
+        return launch_prefix(B, q, dtype, q_stride, q_heads, kv_heads, head_dim, k_cache, v_cache, k_scale, v_scale, *shared,
+                             prompts ? kFewRows : 0x7FFFFFFF, scale, window, out, out_stride, err_flag, stream);
     AttnParams P{};
-    if (shared) {
-        const cudaError_t e = launch_prefix(B, q, dtype, q_stride, q_heads, kv_heads, head_dim, k_cache, v_cache, k_scale, v_scale,
-                                            shared->group_start, shared->prefix_lens, shared->groups, shared->max_prefix,
-                                            prompts ? kFewRows : 0x7FFFFFFF, own_rows, scale, window, shared->workspace, err_flag,
-                                            &P.pre, stream);
-        if (e != cudaSuccess) return e;
-    }
     P.B = B; P.q = q; P.out = out; P.q_stride = q_stride; P.out_stride = out_stride;
     P.k_cache = k_cache; P.v_cache = v_cache; P.k_scale = k_scale; P.v_scale = v_scale;
     P.kv_heads = kv_heads; P.group = q_heads / kv_heads; P.window = window;
@@ -1209,17 +1042,16 @@ cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int6
     P.parts = num_sms() * kCtasPerSm < kMaxParts ? num_sms() * kCtasPerSm : kMaxParts;
     P.err_flag = err_flag;
     P.max_rows = prompts ? kFewRows : 0x7FFFFFFF;
-    auto own = [&](cudaError_t e) {  // joined to what is shared
-        return e != cudaSuccess || !shared ? e : launch_prefix_join(B, dtype, q_heads, kv_heads, head_dim, P.pre, out, out_stride, stream);
-    };
     const int64_t rows = prompts ? kFewRows : most;  // of a sequence, per kv head
     if (dtype == Q4K_F32)
-        return own(head_dim == 64 ? launch_typed<float, 64, 8>(P, rows, max_len, stream) : launch_typed<float, 128, 8>(P, rows, max_len, stream));
-    if (own_rows == 8)
-        return own(head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 8>(P, rows, max_len, stream)
-                                  : launch_typed<__nv_bfloat16, 128, 8>(P, rows, max_len, stream));
-    return own(head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 16>(P, rows, max_len, stream)
-                              : launch_typed<__nv_bfloat16, 128, 16>(P, rows, max_len, stream));
+        return head_dim == 64 ? launch_typed<float, 64, 8>(P, rows, max_len, stream) : launch_typed<float, 128, 8>(P, rows, max_len, stream);
+    // bf16: tiles of 8 rows where a sequence's rows fit one (half the softmax), else 16; next to prompts
+    // the other sequences mostly decode
+    if ((prompts ? P.group : most) <= 8)
+        return head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 8>(P, rows, max_len, stream)
+                              : launch_typed<__nv_bfloat16, 128, 8>(P, rows, max_len, stream);
+    return head_dim == 64 ? launch_typed<__nv_bfloat16, 64, 16>(P, rows, max_len, stream)
+                          : launch_typed<__nv_bfloat16, 128, 16>(P, rows, max_len, stream);
 }
 
 }  // namespace q4k

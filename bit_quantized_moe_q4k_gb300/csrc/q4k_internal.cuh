@@ -63,21 +63,17 @@ cudaError_t launch_attention_prompt(const PagedBatch& B, const void* q, int dtyp
                                     int kv_heads, int head_dim, const uint8_t* k_cache, const uint8_t* v_cache,
                                     const float* k_scale, const float* v_scale, int min_rows, float scale, int window,
                                     void* out, int64_t out_stride, int* err_flag, cudaStream_t stream);
-// Attention behind shared prefixes (q4k_prefix.cu, then q4k_attn.cu); PrefixPlan: q4k_prefix.cuh.
-struct PrefixPlan;
+// Attention behind shared prefixes (q4k_prefix.cu).
+struct SharedPrefix {
+    const int32_t *group_start, *prefix_lens;
+    int groups;
+    void* workspace;   // prefix_workspace_bytes, behind the attention's own
+};
 size_t prefix_workspace_bytes(int batch, int groups, int m, int q_heads, int kv_heads, int head_dim);
 cudaError_t launch_prefix(const PagedBatch& B, const void* q, int dtype, int64_t q_stride, int q_heads, int kv_heads,
                           int head_dim, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
-                          const float* v_scale, const int32_t* group_start, const int32_t* prefix_lens, int groups,
-                          int max_prefix, int max_rows, int own_rows, float scale, int window, void* workspace,
-                          int* err_flag, PrefixPlan* plan, cudaStream_t stream);
-cudaError_t launch_prefix_join(const PagedBatch& B, int dtype, int q_heads, int kv_heads, int head_dim, const PrefixPlan& plan,
-                               void* out, int64_t out_stride, cudaStream_t stream);
-struct SharedPrefix {  // what launch_attention needs of it besides the batch
-    const int32_t *group_start, *prefix_lens;
-    int groups, max_prefix;
-    void* workspace;   // behind the attention's own
-};
+                          const float* v_scale, const SharedPrefix& shared, int max_rows, float scale, int window, void* out,
+                          int64_t out_stride, int* err_flag, cudaStream_t stream);
 cudaError_t launch_attention(const PagedBatch& B, const void* q, int dtype, int64_t q_stride, int q_heads, int kv_heads,
                              int head_dim, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
                              const float* v_scale, int max_q_len, int max_len, float scale, int window, void* out,

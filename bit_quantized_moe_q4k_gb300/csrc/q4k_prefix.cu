@@ -3,8 +3,7 @@
 //
 //   out_r = (sum over shared j + sum over own j) P_j v_j / (the same of P_j),
 // a sum of two parts that are each relative to a reference of their own, 2^(x - M), and joined by 2^(M_part - M).
-// The shared part is made here, the sequences' own one by q4k_attn.cu, which runs beside it where SMs are free; prefix_join_kernel joins
-// them. (Joined by the own part's kernel as it stored, each tile waited for the shared part and then took 7 us more.)
+// The shared part is made here; the sequences' own one in q4k_own.cu, beside it where SMs are free, and there both are joined.
 //
 // prefix_plan_kernel lays the work out (q4k_prefix.cuh): one CTA, since it has to see every group before it can cut the line.
 // prefix_kernel<D> (fp32 rows, 128 a row tile) and prefix2_kernel<D> (bf16, 256) then are the prompt kernels of
@@ -23,15 +22,16 @@ namespace {
 // ---- the plan -----------------------------------------------------------------------------------------------------
 constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanSeqs = 2048, kPlanGroups = 128;  // whose lengths, and plans, are looked up in shared memory
-// Units (1.9 us each, 128 tokens of a row tile) that a piece's start and end are worth, and that an own tile takes of an SM.
-constexpr float kPieceCost = 6.0f, kOwnCost = 1.0f, kOwnUnitCost = 0.09f;
+// What a piece's start and end cost, in units (1.9 us each, 128 tokens of a row tile); what an own piece and 64 of its tokens cost of an SM.
+constexpr float kPieceCost = 6.0f, kOwnCost = 0.2f, kOwnTokensCost = 0.2f;
+// Tokens of an own piece at least: less does not pay for its start.
+constexpr int kOwnLeast = 128;
 
 struct PlanParams {
     PagedBatch B;
     const int32_t *group_start, *prefix_lens;
     PrefixPlan plan;
     int kv_heads, rep, window, max_rows;
-    int own_rows;   // of the sequences' row tiles
     int* err_flag;
 };
 
@@ -54,10 +54,10 @@ __device__ __forceinline__ int piece_of(int64_t units, int ctas, int64_t u) {  /
 }
 
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ PlanParams A) {
-    __shared__ int64_t s_own_units[kPlanWarps];
-    __shared__ int s_own[kPlanWarps], s_own_longest[kPlanWarps];
+    __shared__ int64_t s_own_tokens[kPlanWarps];
+    __shared__ int s_own[kPlanWarps], s_pieces[kPlanWarps];
     __shared__ PrefixHead s_head;
-    __shared__ int s_start[kPlanSeqs + 1], s_len[kPlanSeqs], s_from[kPlanSeqs];
+    __shared__ int s_start[kPlanSeqs + 1], s_len[kPlanSeqs], s_from[kPlanSeqs], s_piece0[kPlanSeqs];
     __shared__ PrefixGroup s_group[kPlanGroups];
     __shared__ int s_each;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -143,21 +143,25 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
         if (lane == 0) plan[g] = G;
     }
     __syncthreads();
-    // The sequences' own row tiles, counted by all warps but the first; it meanwhile finds the groups' places.
-    struct Own { SeqSpan s; int lo, tiles, units; };
+    // The sequences' own row tiles and their tokens, counted by all warps but the first; it meanwhile finds the groups' places.
+    struct Own { SeqSpan s; int from, tiles; };
     auto own_of = [&](int i) {
         Own w{};
         w.s = span(i);
         if (w.s.n == 0 || (int64_t)w.s.n * A.rep > A.max_rows) return w;
-        const int first = max(w.s.len - w.s.n, 0);
-        w.lo = max(A.window > 0 ? max(first - A.window + 1, 0) & ~15 : 0, near ? s_from[i] : A.plan.seq[i].y);
-        w.tiles = (w.s.n * A.rep + A.own_rows - 1) / A.own_rows;
-        w.units = max((w.s.len - w.lo + 63) / 64, 1);
+        w.from = near ? s_from[i] : A.plan.seq[i].y;
+        w.tiles = (w.s.n * A.rep + kOwnRows - 1) / kOwnRows;
         return w;
+    };
+    auto tokens_of = [&](const Own& w, int tile) {  // [x, y): what some row of the tile sees
+        const int first = w.s.len - w.s.n, pf = first + tile * kOwnRows / A.rep;
+        const int pl = first + (min(w.s.n * A.rep, (tile + 1) * kOwnRows) - 1) / A.rep;
+        const int lo = max(A.window > 0 ? max(pf - A.window + 1, 0) & ~15 : 0, w.from);
+        return make_int2(lo, max(max(pl + 1, 0), lo));
     };
     constexpr int kOwnThreads = kPlanThreads - 32;
     const int runs = (batch + kOwnThreads - 1) / kOwnThreads, s0 = min(max(tid - 32, 0) * runs, batch), s1 = warp ? min(s0 + runs, batch) : s0;
-    int own_before = 0;   // of this thread's run of sequences, within its warp
+    int tiles_before = 0;   // of this thread's run of sequences, within its warp
     if (warp == 0) {
         int64_t items = 0, units = 0;
         int most = 1;
@@ -176,13 +180,17 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
         }
         items = min(items, A.plan.items);
         asm volatile("bar.sync 1, %0;" ::"n"(kPlanThreads) : "memory");
-        const int own_tiles = __reduce_add_sync(0xffffffffu, lane > 0 && lane < kPlanWarps ? s_own[lane] : 0);
-        float own_units = lane > 0 && lane < kPlanWarps ? (float)s_own_units[lane] : 0.0f;
+        int64_t tokens = lane > 0 && lane < kPlanWarps ? s_own_tokens[lane] : 0;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) own_units += __shfl_xor_sync(0xffffffffu, own_units, o);
+        for (int o = 16; o; o >>= 1) tokens += __shfl_xor_sync(0xffffffffu, tokens, o);
+        const int own_tiles = __reduce_add_sync(0xffffffffu, lane > 0 && lane < kPlanWarps ? s_own[lane] : 0);
+        // Own pieces: one and a half for each warp that works on them, but not shorter than is worth a start.
+        const int64_t share = tokens * A.kv_heads / (kOwnCtas * kOwnWarps * 3 / 2);
+        const int length = (int)min(max((share + 31) & ~(int64_t)31, (int64_t)kOwnLeast), (int64_t)1 << 30);
         // How many CTAs: the sequences' own tiles run on the SMs that these leave free, and on all when they are done. Candidates in steps
         // of a sixteenth, the cheapest by estimate.
-        const float own_work = (float)A.kv_heads * (kOwnCost * (float)own_tiles + kOwnUnitCost * own_units);
+        const float own_work = (float)A.kv_heads * (kOwnCost * ((float)own_tiles + (float)tokens / (float)length) +
+                                                     kOwnTokensCost / 64.0f * (float)tokens);
         const int candidate = max(kPrefixCtas * (lane < 16 ? lane + 1 : 16) / 16, 1);
         const float shared_time = kPieceCost + ceilf((float)units / (float)candidate);
         const float left = fmaxf(own_work - (float)(kPrefixCtas - candidate) * shared_time, 0.0f) / (float)kPrefixCtas;
@@ -212,16 +220,18 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
         }
         if (lane == 0) {
             s_each = each;
-            s_head = PrefixHead{units, items, (int)ctas, 0, 0, 0, 0};
+            s_head = PrefixHead{units, items, (int)ctas, own_tiles, 0, length, 0, {0, 0, 0}};
         }
     } else {
-        int tiles = 0, longest = 0;
-        int64_t units = 0;
+        int tiles = 0;
+        int64_t tokens = 0;
         for (int i = s0; i < s1; ++i) {
             const Own w = own_of(i);
             tiles += w.tiles;
-            units += (int64_t)w.tiles * w.units;
-            longest = max(longest, w.units);
+            for (int t = 0; t < w.tiles; ++t) {
+                const int2 x = tokens_of(w, t);
+                tokens += x.y - x.x;
+            }
         }
         int inc = tiles;
 #pragma unroll
@@ -229,15 +239,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
             const int x = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += x;
         }
-        own_before = inc - tiles;
+        tiles_before = inc - tiles;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
-        longest = __reduce_max_sync(0xffffffffu, longest);
+        for (int o = 16; o; o >>= 1) tokens += __shfl_xor_sync(0xffffffffu, tokens, o);
         if (lane == 31) s_own[warp] = inc;
-        if (lane == 0) {
-            s_own_units[warp] = units;
-            s_own_longest[warp] = longest;
-        }
+        if (lane == 0) s_own_tokens[warp] = tokens;
         asm volatile("bar.arrive 1, %0;" ::"n"(kPlanThreads) : "memory");
     }
     __syncthreads();
@@ -305,23 +311,55 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
         const int t = G.tiles * j / k;
         A.plan.piece[tid] = piece_at(G, G.item0 + item, t, G.tiles * (j + 1) / k - t, tid, -1);
     }
-    // the sequences' own row tiles
-    const int counted = lane > 0 && lane < kPlanWarps ? s_own[lane] : 0;
-    int at = own_before + __reduce_add_sync(0xffffffffu, lane < warp ? counted : 0);
-    const int all_tiles = __reduce_add_sync(0xffffffffu, counted);
+    // the sequences' own row tiles, then their pieces
+    const int length = s_head.own_length, counted = lane > 0 && lane < kPlanWarps ? s_own[lane] : 0;
+    int at = tiles_before + __reduce_add_sync(0xffffffffu, lane < warp ? counted : 0);
+    auto pieces_of = [&](const int2& x) { return max((x.y - x.x + length - 1) / length, 1); };  // rows that see nothing are zeroed by one
+    int pieces = 0;
     for (int i = s0; i < s1; ++i) {
         const Own w = own_of(i);
-        for (int t = 0; t < w.tiles; ++t, ++at)
-            if (at < A.plan.owns) A.plan.own[at] = OwnTile{i, w.s.start, w.s.n, w.s.len, w.lo, w.units, t, 0};
+        for (int t = 0; t < w.tiles; ++t) pieces += pieces_of(tokens_of(w, t));
+    }
+    int inc = pieces;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    if (lane == 31) s_pieces[warp] = inc;
+    __syncthreads();
+    const int counted_pieces = lane < kPlanWarps ? s_pieces[lane] : 0;
+    const int all_pieces = __reduce_add_sync(0xffffffffu, counted_pieces);
+    int piece = inc - pieces + __reduce_add_sync(0xffffffffu, lane < warp ? counted_pieces : 0);
+    for (int i = s0; i < s1; ++i) {
+        const Own w = own_of(i);
+        const int g = w.tiles ? A.plan.seq[i].x : -1;
+        for (int t = 0; t < w.tiles; ++t, ++at) {
+            const int2 x = tokens_of(w, t);
+            const int k = pieces_of(x);
+            const int first = g < 0 ? -1 : (w.s.start - plan[g].row0) * A.rep + t * kOwnRows;
+            if (at < A.plan.owns) A.plan.own[at] = OwnTile{i, w.s.start, w.s.n, w.s.len, x.x, x.y, t, piece, k, first, g < 0 ? 0 : plan[g].item0};
+            if (at < kPlanSeqs) s_piece0[at] = piece;
+            piece += k;
+        }
+    }
+    __syncthreads();
+    const int all_tiles = (int)min((int64_t)s_head.own_tiles, A.plan.owns);  // (less only where starts fall)
+    const int most = (int)min((int64_t)all_pieces, A.plan.own_pieces);
+    for (int p = tid; p < most && all_tiles; p += kPlanThreads) {
+        int a = 0, b = all_tiles;  // the last tile that begins at or before piece p
+        while (b - a > 1) {
+            const int mid = (a + b) >> 1;
+            if ((mid < kPlanSeqs ? s_piece0[mid] : A.plan.own[mid].piece0) <= p) a = mid;
+            else b = mid;
+        }
+        const int first = a < kPlanSeqs ? s_piece0[a] : A.plan.own[a].piece0;
+        A.plan.own_piece[p] = make_int2(a, (p - first) * length);
     }
     if (tid == 0) {
         PrefixHead H = s_head;
-        H.own_tiles = all_tiles <= A.plan.owns ? all_tiles : 0;
-        for (int w = 1; w < kPlanWarps; ++w) {
-            H.own_longest = max(H.own_longest, s_own_longest[w]);
-            H.own_units += s_own_units[w];
-        }
-        H.own_units *= A.kv_heads;
+        H.own_tiles = all_tiles;
+        H.own_pieces = all_tiles ? most : 0;
         *A.plan.head = H;
     }
 }
@@ -1097,94 +1135,6 @@ cudaError_t launch_typed(const PrefixParams& P, int ctas, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, kern, P);
 }
 
-// ---- both parts ---------------------------------------------------------------------------------------------------
-// Each row's sums of its own tokens and of the pieces of the shared ones, to the largest of their references; 16 or 32 lanes a row of a
-// row tile, four dims a lane. Bound by reading the pieces, from L2.
-constexpr int kJoinRows = 8;
-
-struct JoinParams {
-    PrefixPlan plan;
-    void* out;
-    int64_t out_stride;
-    int kv_heads, group, m;
-};
-__device__ __forceinline__ float group_max(float x, int lanes) {
-    for (int o = lanes / 2; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-    return x;
-}
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinRows * D / 4) prefix_join_kernel(const __grid_constant__ JoinParams A) {
-    constexpr int kLanes = D / 4;
-    __shared__ float s_w[kJoinRows][kPrefixCtas];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tid = threadIdx.x, parts = A.plan.tile_rows / kJoinRows;
-    const int64_t item = blockIdx.x / parts;
-    const int4* p = reinterpret_cast<const int4*>(A.plan.item + item);
-    const int4 i0 = __ldcg(p), i1 = __ldcg(p + 1);
-    if (item >= __ldcg(&A.plan.head->items)) return;
-    const PrefixItem I{i0.x, i0.y, i0.z, i0.w, i1.x, i1.y, {0, 0}};
-    const int local = (int)(blockIdx.x - item * parts) * kJoinRows + tid / kLanes, r = I.r0 + local;
-    const int c = 4 * (tid % kLanes);
-    const int tok = I.row0 + r / A.group, h = I.head * A.group + r % A.group;
-    // (a plan that another call on this workspace has written over leads to no place outside it)
-    const bool there = r >= 0 && r < I.rows && tok >= 0 && tok < A.m && I.head >= 0 && I.head < A.kv_heads && I.slot >= 0 && I.slots > 0 &&
-                       I.slots <= kPrefixCtas && I.slot + I.slots <= A.plan.slots;
-    const int64_t row = (int64_t)tok * A.kv_heads * A.group + h, at = (int64_t)I.slot * A.plan.tile_rows + local;
-    float2 own = make_float2(-INFINITY, 0.0f);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (there) {
-        own = __ldcg(A.plan.own_refs + row);
-        acc = __ldcg(reinterpret_cast<const float4*>(A.plan.own_sums + row * D + c));
-    }
-    // the pieces' weights, a lane each at a time
-    float top = own.x, den = 0.0f;
-    for (int k = tid % kLanes; there && k < I.slots; k += kLanes) {
-        const float2 f = __ldcg(A.plan.refs + at + (int64_t)k * A.plan.tile_rows);
-        const float was = top;
-        top = fmaxf(top, f.x);
-        const float use = top == -INFINITY ? 0.0f : top;
-        den = fmaf(ex2(f.x - use), f.y, den * ex2(was - use));
-        s_w[tid / kLanes][k] = f.x;
-    }
-    const float mine = top;
-    top = group_max(top, kLanes);
-    const float use = top == -INFINITY ? 0.0f : top;
-    den *= ex2(mine - use);
-    for (int o = kLanes / 2; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-    const float keep = ex2(own.x - use);
-    den = fmaf(keep, own.y, den);
-    __syncwarp();
-    if (!there) return;
-    float4 sum = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
-    const float* x = A.plan.sums + at * D + c;
-    const int64_t step = (int64_t)A.plan.tile_rows * D;
-#pragma unroll 8
-    for (int k = 0; k < I.slots; ++k) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(x + k * step));
-        const float w = ex2(s_w[tid / kLanes][k] - use);
-        sum.x = fmaf(w, v.x, sum.x); sum.y = fmaf(w, v.y, sum.y);
-        sum.z = fmaf(w, v.z, sum.z); sum.w = fmaf(w, v.w, sum.w);
-    }
-    const float iv = den == 0.0f ? 0.0f : 1.0f / den;
-    const float y[4] = {sum.x * iv, sum.y * iv, sum.z * iv, sum.w * iv};
-    Vec<T>::store(static_cast<T*>(A.out) + (int64_t)tok * A.out_stride + (int64_t)h * D + c, y);
-}
-
-template <typename T, int D>
-cudaError_t launch_join(const JoinParams& P, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(P.plan.items * (P.plan.tile_rows / kJoinRows)));
-    cfg.blockDim = dim3(kJoinRows * D / 4);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, prefix_join_kernel<T, D>, P);
-}
-
 // Row tiles of all groups at most: a group's last one may be part filled.
 int64_t most_items(int batch, int groups, int m, int rep, int kv_heads, int tile_rows) {
     const int some = groups < batch ? groups : batch;
@@ -1200,23 +1150,28 @@ size_t layout(int batch, int groups, int m, int rep, int kv_heads, int head_dim,
         return p;
     };
     const int64_t items = most_items(batch, groups, m, rep, kv_heads, tile_rows), slots = items + kPrefixCtas;
-    const int64_t owns = (int64_t)m * rep / 8 + (m < batch ? m : batch);  // row tiles of eight rows and more, the last of a sequence part filled
+    // row tiles, a sequence's last part filled; their pieces: as many, and what a length of a share of all tokens adds (three for each two warps)
+    const int64_t owns = (int64_t)m * rep / kOwnRows + (m < batch ? m : batch);
+    const int64_t own_pieces = owns + kOwnCtas * kOwnWarps * 3 / 2 / kv_heads + 1;  // a piece of each kv head
     plan->head = reinterpret_cast<PrefixHead*>(part(sizeof(PrefixHead)));
     plan->group = reinterpret_cast<PrefixGroup*>(part(sizeof(PrefixGroup) * (size_t)groups));
     plan->seq = reinterpret_cast<int2*>(part(sizeof(int2) * (size_t)batch));
     plan->piece = reinterpret_cast<PrefixPiece*>(part(sizeof(PrefixPiece) * (size_t)slots));
     plan->item = reinterpret_cast<PrefixItem*>(part(sizeof(PrefixItem) * (size_t)items));
     plan->own = reinterpret_cast<OwnTile*>(part(sizeof(OwnTile) * (size_t)owns));
+    plan->own_piece = reinterpret_cast<int2*>(part(sizeof(int2) * (size_t)own_pieces));
     plan->pos = reinterpret_cast<int*>(part(sizeof(int) * (size_t)m));
     plan->refs = reinterpret_cast<float2*>(part(sizeof(float2) * (size_t)slots * tile_rows));
     plan->sums = reinterpret_cast<float*>(part(sizeof(float) * (size_t)slots * tile_rows * head_dim));
-    plan->own_refs = reinterpret_cast<float2*>(part(sizeof(float2) * (size_t)m * rep * kv_heads));
-    plan->own_sums = reinterpret_cast<float*>(part(sizeof(float) * (size_t)m * rep * kv_heads * head_dim));
+    const int64_t own_slots = own_pieces * kv_heads;
+    plan->own_refs = reinterpret_cast<float2*>(part(sizeof(float2) * (size_t)own_slots * kOwnRows));
+    plan->own_sums = reinterpret_cast<float*>(part(sizeof(float) * (size_t)own_slots * kOwnRows * head_dim));
     plan->tile_rows = tile_rows;
     plan->groups = groups;
     plan->items = items;
     plan->slots = slots;
     plan->owns = owns;
+    plan->own_pieces = own_pieces;
     return at;
 }
 
@@ -1232,14 +1187,14 @@ size_t prefix_workspace_bytes(int batch, int groups, int m, int q_heads, int kv_
 
 cudaError_t launch_prefix(const PagedBatch& B, const void* q, int dtype, int64_t q_stride, int q_heads, int kv_heads,
                           int head_dim, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
-                          const float* v_scale, const int32_t* group_start, const int32_t* prefix_lens, int groups,
-                          int max_prefix, int max_rows, int own_rows, float scale, int window, void* workspace, int* err_flag,
-                          PrefixPlan* plan, cudaStream_t stream) {
-    const int rep = q_heads / kv_heads, tile_rows = dtype == Q4K_F32 ? kRows : 2 * kRows;
-    layout(B.batch, groups, B.m, rep, kv_heads, head_dim, tile_rows, static_cast<uint8_t*>(workspace), plan);
+                          const float* v_scale, const SharedPrefix& shared, int max_rows, float scale, int window, void* out,
+                          int64_t out_stride, int* err_flag, cudaStream_t stream) {
+    const int rep = q_heads / kv_heads, tile_rows = dtype == Q4K_F32 ? kRows : 2 * kRows, groups = shared.groups;
+    PrefixPlan plan;
+    layout(B.batch, groups, B.m, rep, kv_heads, head_dim, tile_rows, static_cast<uint8_t*>(shared.workspace), &plan);
     PlanParams L{};
-    L.B = B; L.group_start = group_start; L.prefix_lens = prefix_lens; L.plan = *plan;
-    L.kv_heads = kv_heads; L.rep = rep; L.window = window; L.max_rows = max_rows; L.own_rows = own_rows; L.err_flag = err_flag;
+    L.B = B; L.group_start = shared.group_start; L.prefix_lens = shared.prefix_lens; L.plan = plan;
+    L.kv_heads = kv_heads; L.rep = rep; L.window = window; L.max_rows = max_rows; L.err_flag = err_flag;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(kPlanThreads);
@@ -1258,17 +1213,15 @@ cudaError_t launch_prefix(const PagedBatch& B, const void* q, int dtype, int64_t
     P.sign = scale < 0.0f ? -1.0f : 1.0f;
     P.err_flag = err_flag;
     P.wait_ns = wait_limit_ns();
-    P.plan = *plan;
+    P.plan = plan;
     const int ctas = kPrefixCtas;
-    if (dtype == Q4K_F32) return head_dim == 64 ? launch_typed<float, 64>(P, ctas, stream) : launch_typed<float, 128>(P, ctas, stream);
-    return head_dim == 64 ? launch_typed<__nv_bfloat16, 64>(P, ctas, stream) : launch_typed<__nv_bfloat16, 128>(P, ctas, stream);
-}
-
-cudaError_t launch_prefix_join(const PagedBatch& B, int dtype, int q_heads, int kv_heads, int head_dim, const PrefixPlan& plan,
-                               void* out, int64_t out_stride, cudaStream_t stream) {
-    JoinParams P{plan, out, out_stride, kv_heads, q_heads / kv_heads, B.m};
-    if (dtype == Q4K_F32) return head_dim == 64 ? launch_join<float, 64>(P, stream) : launch_join<float, 128>(P, stream);
-    return head_dim == 64 ? launch_join<__nv_bfloat16, 64>(P, stream) : launch_join<__nv_bfloat16, 128>(P, stream);
+    if (dtype == Q4K_F32) e = head_dim == 64 ? launch_typed<float, 64>(P, ctas, stream) : launch_typed<float, 128>(P, ctas, stream);
+    else e = head_dim == 64 ? launch_typed<__nv_bfloat16, 64>(P, ctas, stream) : launch_typed<__nv_bfloat16, 128>(P, ctas, stream);
+    if (e != cudaSuccess) return e;
+    OwnParams O{B, plan, q, out, q_stride, out_stride, k_cache, v_cache, k_scale, v_scale, kv_heads, rep, window,
+                scale * 1.44269504088896340736f, err_flag};
+    e = launch_own(O, dtype, head_dim, stream);
+    return e != cudaSuccess ? e : launch_join(O, dtype, head_dim, stream);
 }
 
 }  // namespace q4k

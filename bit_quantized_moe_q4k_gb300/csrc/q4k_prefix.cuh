@@ -1,5 +1,5 @@
-// q4k_prefix.cuh -- the plan of attention behind shared prefixes (q4k_prefix.cu makes it and computes the shared part and joins it to
-// the sequences' own parts, which q4k_attn.cu computes).
+// q4k_prefix.cuh -- the plan of attention behind shared prefixes: made, and the shared part computed, in q4k_prefix.cu; the sequences'
+// own parts, and the join of both, in q4k_own.cu.
 //
 // A group's shared part is the whole pages of its prefix that lie before every new token of its sequences. Its query rows
 // (row r: new token r / rep of the group, query head r % rep of the kv head) are cut into row tiles; an item is a
@@ -39,19 +39,24 @@ struct alignas(16) PrefixItem {
     int row0, r0, rows;       // as in PrefixPiece
     int head, pad[2];
 };
-// A row tile of a sequence and what it sees of the sequence's own tokens.
+// A row tile of a sequence (kOwnRows query rows of a kv head) and what it sees of the sequence's own tokens, in pieces for one warp each.
+constexpr int kOwnRows = 8;
 struct alignas(16) OwnTile {
     int seq, start, n, len;   // as SeqSpan
-    int lo, units;            // from token lo (a multiple of 16), in units of 64 tokens
-    int tile, pad;
+    int lo, hi;               // tokens lo (a multiple of 16) .. hi - 1 are seen by some row
+    int tile;                 // the row tile
+    int piece0, pieces;       // its first piece, and how many
+    int first;                // its first query row among those of its group, or -1: it shares nothing
+    int64_t item0;            // its group's first item
 };
 struct PrefixHead {
     int64_t units, items;
     int ctas;            // that compute the shared part
     int own_tiles;       // row tiles of the sequences
-    int own_longest;     // units of the longest
-    unsigned next;       // the next (row tile, kv head) to be taken
-    int64_t own_units;   // of all (row tile, kv head)
+    int own_pieces;      // of all row tiles; a piece of each kv head
+    int own_length;      // tokens of a piece, but for a tile's last
+    unsigned next;       // the next (piece, kv head) to be taken
+    int pad[3];
 };
 struct PrefixPlan {
     PrefixHead* head;
@@ -59,19 +64,37 @@ struct PrefixPlan {
     int2* seq;            // [batch]: group (-1: none), tokens taken from its shared part
     PrefixPiece* piece;   // [kPrefixCtas + items]: a CTA's first piece, then the pieces that begin an item after another's in a CTA
     PrefixItem* item;     // [items]
-    OwnTile* own;         // [own]
+    OwnTile* own;         // [owns]
+    int2* own_piece;      // [own_slots / kv_heads]: row tile, first token
     int* pos;             // [m]: positions of the groups' rows, where there is a window
     float* sums;          // [slots][tile_rows][head_dim]
     float2* refs;         // [slots][tile_rows]: exponent that the sums and the denominator are relative to (-inf: nothing seen), denominator
-    float* own_sums;      // [m * q_heads][head_dim]: the same of the sequences' own parts, where they share another
-    float2* own_refs;     // [m * q_heads]
+    float* own_sums;      // [own_pieces * kv_heads][kOwnRows][head_dim]: the same of the sequences' own parts
+    float2* own_refs;     // [own_pieces * kv_heads][kOwnRows]
     int tile_rows, groups;
-    int64_t items, slots, owns;   // what the workspace has room for
+    int64_t items, slots, owns, own_pieces;   // what the workspace has room for
 };
 
 // Rows up to here have partial results of at most half a gigabyte; beyond (hundreds of rows a kv head for each of thousands of
 // sequences), every sequence reads its prefix itself.
 constexpr int64_t kPrefixMaxRows = 1 << 20;
 constexpr int kPrefixCtas = 152;
+// Warps that work on own parts at a time: twelve on each of 152 SMs.
+constexpr int kOwnWarps = 4, kOwnCtas = 3 * 152;
+
+struct OwnParams {
+    PagedBatch B;
+    PrefixPlan plan;
+    const void* q;
+    void* out;
+    int64_t q_stride, out_stride;
+    const uint8_t *k_cache, *v_cache;
+    const float *k_scale, *v_scale;
+    int kv_heads, group, window;
+    float scale_log2;
+    int* err_flag;
+};
+cudaError_t launch_own(const OwnParams& P, int dtype, int head_dim, cudaStream_t stream);   // after the shared part's launch
+cudaError_t launch_join(const OwnParams& P, int dtype, int head_dim, cudaStream_t stream);
 
 }  // namespace q4k
