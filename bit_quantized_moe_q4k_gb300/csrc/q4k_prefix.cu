@@ -11,6 +11,7 @@
 // item, and leaves sums, references and denominators in fp32. No row sees less than the whole shared part unless there is a
 // window, so nearly every tile is of the kind that is multiplied whole.
 #include <atomic>
+#include <cstdlib>
 
 #include "q4k_attn_tc.cuh"
 #include "q4k_prefix.cuh"
@@ -24,14 +25,24 @@ constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanSeqs = 2048, kPlanGroups = 128;  // whose lengths, and plans, are looked up in shared memory
 // What a piece's start and end cost, in units (1.9 us each, 128 tokens of a row tile); what an own piece and 64 of its tokens cost of an SM.
 constexpr float kPieceCost = 6.0f, kOwnCost = 0.2f, kOwnTokensCost = 0.2f;
+// What a unit, and a piece's start, of a row tile of the shared part cost, in units of an own tile (8 rows). 64 groups of 2 sequences behind
+// 2048 tokens, 8 kv heads, shared 190 us and not 134; 32 of 3 behind 2048 and 8192 109 and 104, 275 and 304; 32 of 4 behind 512 and 2048
+// 65 and 60, 113 and 130; 24 of 6 behind 512 and 2048 64 and 64, 102 and 140.
+constexpr float kShareUnit = 2.0f, kShareStart = 16.0f;
 // Tokens of an own piece at least: less does not pay for its start.
 constexpr int kOwnLeast = 128;
+
+int share_setting() {
+    const char* s = getenv("Q4K_SHARE_PREFIX");
+    return s ? (atoi(s) != 0 ? 1 : 0) : -1;
+}
 
 struct PlanParams {
     PagedBatch B;
     const int32_t *group_start, *prefix_lens;
     PrefixPlan plan;
     int kv_heads, rep, window, max_rows;
+    bool always;  // share whatever can be
     int* err_flag;
 };
 
@@ -106,19 +117,21 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
         __syncwarp();
         PrefixGroup G{};
         if (!none) {
-            int least = 0x7FFFFFFF, most = -1, live = 0, rows = 0;
+            int least = 0x7FFFFFFF, most = -1, live = 0, rows = 0, tiles = 0;
             for (int i = a + lane; i < b; i += 32) {
                 const SeqSpan s = span(i);
                 if (s.n == 0) continue;
                 least = min(least, s.len - s.n);
                 most = max(most, s.len - 1);
                 rows = max(rows, s.n);
+                tiles += (int)(((int64_t)s.n * A.rep + kOwnRows - 1) / kOwnRows);
                 ++live;
             }
             least = __reduce_min_sync(0xffffffffu, least);
             most = __reduce_max_sync(0xffffffffu, most);
             rows = __reduce_max_sync(0xffffffffu, rows);
             live = __reduce_add_sync(0xffffffffu, live);
+            tiles = __reduce_add_sync(0xffffffffu, tiles);
             G.leader = a;
             if (live > 1 && (int64_t)rows * A.rep <= A.max_rows) {
                 G.row0 = span(a).start;
@@ -126,9 +139,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
                 G.from = min(prefix, max(least, 0)) >> shift << shift;
                 G.lo = A.window > 0 ? max(least - A.window + 1, 0) & ~15 : 0;
                 G.full_lo = A.window > 0 ? max(most - A.window + 1, 0) : 0;
-                if (G.from > G.lo) {
-                    G.tiles = (G.from - G.lo + kToks - 1) / kToks;
-                    G.rows = (int)(((int64_t)G.n * A.rep + A.plan.tile_rows - 1) / A.plan.tile_rows);
+                const int row_tiles = (int)(((int64_t)G.n * A.rep + A.plan.tile_rows - 1) / A.plan.tile_rows);
+                const int units = (G.from - G.lo + kToks - 1) / kToks;
+                if (units > 0 && (A.always || (float)tiles * units > (float)row_tiles * (kShareUnit * units + kShareStart))) {
+                    G.tiles = units;
+                    G.rows = row_tiles;
                     for (int i = a + lane; i < b; i += 32) {
                         A.plan.seq[i] = make_int2(g, G.from);
                         if (near) s_from[i] = G.from;
@@ -1185,6 +1200,24 @@ size_t prefix_workspace_bytes(int batch, int groups, int m, int q_heads, int kv_
     return a > b ? a : b;
 }
 
+// Whether a call is worth the plan, the shared kernel and the join: by how many units of 128 tokens, of a row tile as q4k_paged_attention
+// cuts them and a kv head, fewer it would read if its groups were equally large. On both sides of the bound, shared and not (bf16, 8 kv
+// heads, one new token each): a group of 32 behind 2048 tokens (3600) 33 and 34 us, 8 behind 8192 (2448) 36 and 32, 4 behind 512 25 and 9,
+// 16 groups of 16 behind 512 (4864) 68 and 77, 24 of 6 behind 2048 (6528) 102 and 110, 24 of 5 (3456) 105 and 93.
+// Switch (environment, read at every call): Q4K_SHARE_PREFIX=1 shares whatever can be, 0 nothing.
+constexpr int64_t kShareLeast = 4500;
+bool prefix_pays(const PagedBatch& B, int dtype, int q_heads, int kv_heads, int groups, int max_q_len, int max_prefix, int window) {
+    if (share_setting() >= 0) return share_setting() > 0;
+    int64_t tokens = (int64_t)B.max_pages << B.page_shift;
+    tokens = max_prefix < tokens ? max_prefix : tokens;
+    if (window > 0 && window < tokens) tokens = window;
+    const int64_t rep = q_heads / kv_heads, units = (tokens + kToks - 1) / kToks, rows = B.m * rep;
+    const int64_t own_rows = dtype == Q4K_F32 || max_q_len * rep <= 8 ? 8 : 16, shared_rows = dtype == Q4K_F32 ? kRows : 2 * kRows;
+    const int64_t live = B.batch < B.m ? B.batch : B.m, by_rows = (rows + own_rows - 1) / own_rows;
+    const int64_t tiles = live > by_rows ? live : by_rows, row_tiles = (groups < live ? groups : live) + rows / shared_rows;
+    return (tiles * units - row_tiles * (3 * units + 14)) * kv_heads >= kShareLeast;
+}
+
 cudaError_t launch_prefix(const PagedBatch& B, const void* q, int dtype, int64_t q_stride, int q_heads, int kv_heads,
                           int head_dim, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
                           const float* v_scale, const SharedPrefix& shared, int max_rows, float scale, int window, void* out,
@@ -1194,7 +1227,7 @@ cudaError_t launch_prefix(const PagedBatch& B, const void* q, int dtype, int64_t
     layout(B.batch, groups, B.m, rep, kv_heads, head_dim, tile_rows, static_cast<uint8_t*>(shared.workspace), &plan);
     PlanParams L{};
     L.B = B; L.group_start = shared.group_start; L.prefix_lens = shared.prefix_lens; L.plan = plan;
-    L.kv_heads = kv_heads; L.rep = rep; L.window = window; L.max_rows = max_rows; L.err_flag = err_flag;
+    L.kv_heads = kv_heads; L.rep = rep; L.window = window; L.max_rows = max_rows; L.always = share_setting() > 0; L.err_flag = err_flag;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(kPlanThreads);

@@ -497,13 +497,15 @@ int q4k_paged_attention(const void* d_q, int dtype, int m, int q_heads, int kv_h
  *   first prefix_lens[g] / page_size entries of their rows of the page table are the same (which of the rows is read is not
  *   specified). Rising, within [0, batch]; sequences before the first group or after the last share nothing.
  *   What is shared is the whole pages of the prefix that lie before every new token of the group's sequences; the sequences read all else,
- *   and groups with new tokens in fewer than two sequences, as in q4k_paged_attention.
- *   max_prefix: an upper bound of prefix_lens that chooses the kernels (below page_size: nothing is shared).
+ *   and what small groups hold in common, as in q4k_paged_attention.
+ *   max_prefix: an upper bound of prefix_lens that chooses the kernels: calls that would save too little (by batch, groups, m, heads,
+ *   max_q_len, max_prefix and window) run q4k_paged_attention's kernels and read neither group_start nor prefix_lens. Environment switch, read
+ *   at every call: Q4K_SHARE_PREFIX=1 shares all it can where max_prefix >= page_size, 0 nothing.
  *   The rest: as in q4k_paged_attention. Sequences of more than 64 query rows per kv head in calls that it gives to its prompt
  *   kernels, and calls of more than 2^20 query rows (m*q_heads), read their prefixes themselves.
- * Device flags: as in q4k_paged_attention; group_start falling or outside [0, batch] (or q_start outside its rules): nothing is shared,
- * prefix_lens outside [0, max_pages*page_size] are clamped (Q4K_ERR_SEQ).
- * Limits (Q4K_ERR_LIMIT): q4k_paged_attention's, groups <= 2^24. Three launches (one more beside prompts). Within one softmax row the
+ * Device flags: as in q4k_paged_attention; where they are read, group_start falling or outside [0, batch] (or q_start outside its rules): nothing is
+ * shared, prefix_lens outside [0, max_pages*page_size] are clamped (Q4K_ERR_SEQ).
+ * Limits (Q4K_ERR_LIMIT): q4k_paged_attention's, groups <= 2^24. Four launches where prefixes are shared (one more beside prompts). Within one softmax row the
  * fp32 sums of the two parts are joined once more: 2^-23 of the result.
  * Workspace: q4k_shared_prefix_attention_workspace_size bytes, any contents. */
 size_t q4k_shared_prefix_attention_workspace_size(int batch, int groups, int m, int q_heads, int kv_heads, int head_dim);

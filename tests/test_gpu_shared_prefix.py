@@ -20,6 +20,11 @@ pytestmark = pytest.mark.gpu
 TIMEOUT, PAGE_FLAG, SEQ_FLAG = 10, 11, 12
 
 
+@pytest.fixture(autouse=True)
+def share_whatever_can_be(monkeypatch):
+    monkeypatch.setenv("Q4K_SHARE_PREFIX", "1")
+
+
 class Shared:
     """groups: (shared tokens, [(new tokens, cached tokens behind the shared ones and before the new)]); before and behind: sequences
     outside the groups, the same with no shared tokens."""
@@ -347,3 +352,15 @@ def test_offsets_past_32_bits():
                                         dev(np.array([270], np.int32)), 1, 2, 310, 270, 0.09, 0, out, hq * d, ws, nbytes, flag)
         ref, tol = attention_ref(f64(q).reshape(3, hq, d), small, order, [1, 2], [300, 310], hq // hk, 0.09, 0, dtype)
         assert int(flag) == 0 and (np.abs(f64(out).reshape(3, hq, d) - ref) <= 2 * tol).all()
+
+
+@pytest.mark.parametrize("setting", [None, "0"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_what_is_shared_goes_by_size(dtype, setting, monkeypatch):
+    """Calls and groups on both sides of the rules: the same tokens, shared or not."""
+    monkeypatch.delenv("Q4K_SHARE_PREFIX") if setting is None else monkeypatch.setenv("Q4K_SHARE_PREFIX", setting)
+    Shared(30, [(400, samples(5))], 2, 64, 16).run(8, dtype)                                 # a small call
+    Shared(31, [(2000, samples(40, own=0))], 8, 64, 64).run(32, dtype)
+    Shared(32, [(1000, samples(2)), (1500, samples(70)), (900, samples(3, 2)), (30, samples(9))], 8, 64, 32).run(32, dtype)  # some groups of a large one
+    Shared(33, [(700, samples(2)) for _ in range(30)], 8, 64, 32).run(32, dtype, max_prefix=1 << 30)  # no group
+    Shared(34, [(1500, samples(70))], 8, 64, 32).run(32, dtype, window=300)
