@@ -6,10 +6,13 @@
 // k-th page taken (same order) is the k-th from the top. So every place follows from exclusive sums over the sequences:
 // no atomics, the same tables at every call.
 //
-// Bound by latency: one launch of one CTA, or of one cluster of eight where there is more to write. Every CTA forms the
-// sums over all sequences itself in shared memory (a few KB of lengths), and writes its share of the entries and rows,
-// finding the sequence of each by bisection of the sums. The cluster's barrier between the last read of the lengths and
-// the first write lets results take the place of inputs.
+// Bound by latency: one CTA, or one cluster of eight where there is more to write (and a second kernel for the rows of
+// long prompts). Every CTA forms the sums over all sequences itself in shared memory (a few KB of lengths), and writes
+// its share of the entries and rows, finding the sequence of each by bisection of the sums. The cluster's barrier between
+// the last read of the lengths and the first write lets results take the place of inputs.
+// A step of 7 sequences takes 3.2 us, one of 1000 with up to 6 new tokens and 6300 pages given back 7.6, prompts of 121000
+// tokens in all 8.0. The code is small on purpose: a version with all of a thread's entries and rows looked up in one
+// unrolled pass waited for instructions (9.2 us for the 1000).
 #include <atomic>
 
 #include "q4k_paged.cuh"
@@ -18,43 +21,56 @@ namespace q4k {
 namespace {
 
 constexpr int kFewThreads = 256, kManyThreads = 1024, kTablesCluster = 8;
-constexpr int kArrays = 6;  // of batch + 1 words in shared memory
+constexpr int kSumThreads = 256;  // that add the sequences up
+constexpr int kRun = 4;           // rows of a thread at a time, where there are more rows than threads
+// More rows than this are written by a kernel of their own, on all SMs. 40 sequences, in the cluster and apart: 8000 rows 5.3 and 6.2 us, 16000 6.7
+// and 6.2, 121000 13.1 and 8.0; 1000 sequences, 15000 rows 8.4 and 8.1.
+constexpr int kRowsTogether = 16384;
+constexpr int kRowsThreads = 512;
+constexpr int kArrays = 6;        // of batch + 1 words in shared memory
 
 struct TablesParams {
     const int32_t *kept, *fresh, *fixed, *held, *count;
     int32_t *free_pages, *table, *held_out, *count_out, *q_start, *seq_lens, *pos;
     int64_t* slots;
     int batch, m, max_pages, page_shift, num_pages;
+    bool rows_apart;  // positions and slots are rows_kernel's
     int* err_flag;
 };
 
-// Exclusive sums of three values a thread over the block, and their totals.
-template <int T>
-__device__ __forceinline__ void block_sums(int64_t (&v)[3], int64_t (&total)[3], int64_t (*s_warp)[32]) {
+// Exclusive sums of three values a thread over the first kSumThreads threads, and their totals for all. (Shuffles bound it: by all 32 warps of a
+// CTA, a sequence a lane, it took 2.1 us.)
+__device__ __forceinline__ void block_sums(int64_t (&v)[3], int64_t (&total)[3], int64_t (*s_warp)[kSumThreads / 32 + 1]) {
+    constexpr int kWarps = kSumThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t inc[3];
+    if (warp < kWarps) {
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        inc[k] = v[k];
+        for (int k = 0; k < 3; ++k) {
+            int64_t inc = v[k];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, inc[k], o);
-            if (lane >= o) inc[k] += x;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += x;
+            }
+            if (lane == 31) s_warp[k][warp] = inc;
+            v[k] = inc - v[k];
         }
-        if (lane == 31) s_warp[k][warp] = inc[k];
+    }
+    __syncthreads();
+    if (warp < 3) {  // the warps' sums, of one value a warp
+        int64_t x = lane < kWarps ? s_warp[warp][lane] : 0, inc = x;
+#pragma unroll
+        for (int o = 1; o <= kWarps; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane <= kWarps) s_warp[warp][lane] = inc - x;  // the total last
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-        const int64_t x = lane < T / 32 ? s_warp[k][lane] : 0;
-        int64_t before = lane < warp ? x : 0, all = x;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            before += __shfl_xor_sync(0xffffffffu, before, o);
-            all += __shfl_xor_sync(0xffffffffu, all, o);
-        }
-        total[k] = all;
-        v[k] = before + inc[k] - v[k];
+        if (warp < kWarps) v[k] += s_warp[k][warp];
+        total[k] = s_warp[k][kWarps];
     }
     __syncthreads();  // s_warp may be written again
 }
@@ -70,10 +86,62 @@ __device__ __forceinline__ int last_at_most(const int* a, int n, int x) {
     return lo;
 }
 
+// Positions and slots of the rows, R consecutive ones a thread at a time (R 4: 16-byte stores, to outputs that begin at such a boundary). Returns
+// the flag to raise, or 0.
+template <int R>
+__device__ __forceinline__ int write_rows(const TablesParams& A, const int* s_kept, const int* s_start, int rows, int most, int at, int step) {
+    int bad = 0;
+#pragma unroll 1
+    for (int r0 = at * R; r0 < most; r0 += step * R) {
+        int pos[R], id[R];
+        int i = r0 < rows ? last_at_most(s_start, A.batch, r0) : 0, last = -1;
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            const int r = r0 + u;
+            pos[u] = 0;
+            id[u] = -1;
+            if (r >= rows) continue;
+            while (r >= s_start[i + 1]) {  // (sequences without rows are passed over)
+                ++i;
+                last = -1;
+            }
+            const int e = (pos[u] = s_kept[i] + (r - s_start[i])) >> A.page_shift;
+            if (A.slots) {
+                if (u > 0 && e == last) id[u] = -2;  // the page of the row before
+                else id[u] = __ldcg(A.table + (int64_t)i * A.max_pages + e);
+                last = e;
+            }
+        }
+        int64_t slot[R];
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            if (u > 0 && id[u] == -2) id[u] = id[u - 1];
+            const bool known = (unsigned)id[u] < (unsigned)A.num_pages;
+            if (r0 + u < rows && A.slots && !known) bad = Q4K_ERR_PAGE;
+            slot[u] = known ? ((int64_t)id[u] << A.page_shift) + (pos[u] & ((1 << A.page_shift) - 1)) : -1;
+        }
+        if (R == 4 && r0 + R <= most) {
+            if (A.pos) *reinterpret_cast<int4*>(A.pos + r0) = make_int4(pos[0], pos[1 % R], pos[2 % R], pos[3 % R]);
+            if (A.slots) {
+                reinterpret_cast<longlong2*>(A.slots + r0)[0] = make_longlong2(slot[0], slot[1 % R]);
+                reinterpret_cast<longlong2*>(A.slots + r0)[1] = make_longlong2(slot[2 % R], slot[3 % R]);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < R; ++u) {
+                if (r0 + u >= most) continue;
+                if (A.pos) A.pos[r0 + u] = pos[u];
+                if (A.slots) A.slots[r0 + u] = slot[u];
+            }
+        }
+    }
+    return bad;
+}
+
 template <int T>
 __global__ void __launch_bounds__(T) tables_kernel(const __grid_constant__ TablesParams A) {
     extern __shared__ int s_mem[];
-    __shared__ int64_t s_warp[3][32];
+    __shared__ int64_t s_warp[3][kSumThreads / 32 + 1];
     const int n = A.batch, width = n + 1;
     int* s_kept = s_mem;             // tokens that stay
     int* s_start = s_mem + width;    // new tokens, then their exclusive sum
@@ -102,8 +170,8 @@ __global__ void __launch_bounds__(T) tables_kernel(const __grid_constant__ Table
         s_take[i] = f;  // until the sums
     }
     __syncthreads();
-    // each thread's run of sequences
-    const int per = (n + T - 1) / T, lo = min(tid * per, n), hi = min(lo + per, n);
+    // each thread's run of sequences, an odd number of them for the banks
+    const int per = (n + kSumThreads - 1) / kSumThreads | 1, lo = tid < kSumThreads ? min(tid * per, n) : n, hi = min(lo + per, n);
     int64_t sum[3], total[3];
     auto sums = [&]() {
         sum[0] = sum[1] = sum[2] = 0;
@@ -112,7 +180,7 @@ __global__ void __launch_bounds__(T) tables_kernel(const __grid_constant__ Table
             sum[1] += max(s_need[i] - s_base[i], 0);
             sum[2] += max(s_base[i] - s_need[i], 0);
         }
-        block_sums<T>(sum, total, s_warp);
+        block_sums(sum, total, s_warp);
     };
     sums();
     if (total[0] > A.m) {  // more rows than the outputs have: sequences in order, while they fit
@@ -169,14 +237,6 @@ __global__ void __launch_bounds__(T) tables_kernel(const __grid_constant__ Table
 
     const int taken = s_take[n], rows = s_start[n], top = (int)available, left = top - taken;
     const int at = rank * T + tid, step = ranks * T;
-    auto given = [&](int p) {  // the page at place p >= count of the stack
-        const int i = last_at_most(s_give, n, p - count);
-        return __ldcg(A.table + (int64_t)i * A.max_pages + s_need[i] + (p - count - s_give[i]));
-    };
-    auto taken_page = [&](int t) {
-        const int p = top - 1 - t;
-        return p < count ? __ldcg(A.free_pages + p) : given(p);
-    };
     for (int i = at; i <= n; i += step) {
         A.q_start[i] = s_start[i];
         if (i == n) continue;
@@ -185,36 +245,84 @@ __global__ void __launch_bounds__(T) tables_kernel(const __grid_constant__ Table
         A.held_out[i] = s_need[i] - f;
     }
     if (at == 0) *A.count_out = left;
+    // Pages: the k-th taken is the one at place top - 1 - k of the stack, and what stays on it above `count` is the pages given back that nobody took.
     // Entries taken are written where no entry is read: given-back ones lie in other sequences' rows, free pages below `count`.
-    for (int t = at; t < taken; t += step) {
-        const int i = last_at_most(s_take, n, t), id = taken_page(t);
-        if ((unsigned)id >= (unsigned)A.num_pages) bad = Q4K_ERR_PAGE;
-        A.table[(int64_t)i * A.max_pages + s_base[i] + (t - s_take[i])] = id;
-    }
-    for (int p = count + at; p < left; p += step) A.free_pages[p] = given(p);
-    if (A.pos || A.slots) {
-#pragma unroll 4
-        for (int r = at; r < A.m; r += step) {
-            int pos = 0;
-            int64_t slot = -1;
-            if (r < rows) {
-                const int i = last_at_most(s_start, n, r);
-                pos = s_kept[i] + (r - s_start[i]);
-                if (A.slots) {
-                    const int e = pos >> A.page_shift;
-                    const int id = e < s_base[i] ? __ldcg(A.table + (int64_t)i * A.max_pages + e)
-                                                 : taken_page(s_take[i] + (e - s_base[i]));
-                    if ((unsigned)id < (unsigned)A.num_pages)
-                        slot = ((int64_t)id << A.page_shift) + (pos & ((1 << A.page_shift) - 1));
-                    else
-                        bad = Q4K_ERR_PAGE;
-                }
+#pragma unroll 1
+    for (int x = at; x < max(taken, left - count); x += step) {
+#pragma unroll 1
+        for (int side = 0; side < 2; ++side) {
+            if (x >= (side ? left - count : taken)) continue;
+            const int p = side ? count + x : top - 1 - x;
+            const int32_t* from = A.free_pages + p;
+            if (p >= count) {
+                const int i = last_at_most(s_give, n, p - count);
+                from = A.table + (int64_t)i * A.max_pages + s_need[i] + (p - count - s_give[i]);
             }
-            if (A.pos) A.pos[r] = pos;
-            if (A.slots) A.slots[r] = slot;
+            const int id = __ldcg(from);
+            if (side) {
+                A.free_pages[p] = id;
+            } else {
+                const int i = last_at_most(s_take, n, x);
+                if ((unsigned)id >= (unsigned)A.num_pages) bad = Q4K_ERR_PAGE;
+                A.table[(int64_t)i * A.max_pages + s_base[i] + (x - s_take[i])] = id;
+            }
         }
     }
+    const int most = (A.pos || A.slots) && !A.rows_apart ? A.m : 0;
+    if (most > 0) {
+        if (A.slots) {  // the tables are complete
+            if (ranks > 1) asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+            else __syncthreads();
+        }
+        const bool wide = most > step && ((reinterpret_cast<uintptr_t>(A.pos) | reinterpret_cast<uintptr_t>(A.slots)) & 15) == 0;
+        if (wide) bad = max(bad, write_rows<kRun>(A, s_kept, s_start, rows, most, at, step));
+        else bad = max(bad, write_rows<1>(A, s_kept, s_start, rows, most, at, step));
+    }
     if (bad) raise_flag(A.err_flag, bad);
+}
+
+// Positions and slots from the results of the other kernel.
+__global__ void __launch_bounds__(kRowsThreads) rows_kernel(const __grid_constant__ TablesParams A) {
+    extern __shared__ int s_mem[];
+    const int n = A.batch;
+    int *s_start = s_mem, *s_kept = s_mem + n + 1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    for (int i = threadIdx.x; i <= n; i += kRowsThreads) {
+        const int a = __ldcg(A.q_start + i);
+        s_start[i] = a;
+        if (i < n) s_kept[i] = __ldcg(A.seq_lens + i) - (__ldcg(A.q_start + i + 1) - a);
+    }
+    __syncthreads();
+    const bool wide = ((reinterpret_cast<uintptr_t>(A.pos) | reinterpret_cast<uintptr_t>(A.slots)) & 15) == 0;
+    const int at = blockIdx.x * kRowsThreads + threadIdx.x, step = gridDim.x * kRowsThreads, rows = s_start[n];
+    const int bad = wide ? write_rows<kRun>(A, s_kept, s_start, rows, A.m, at, step) : write_rows<1>(A, s_kept, s_start, rows, A.m, at, step);
+    if (bad) raise_flag(A.err_flag, bad);
+}
+
+cudaError_t launch_rows(const TablesParams& P, cudaStream_t stream) {
+    static std::atomic<bool> allowed[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!allowed[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * (kTablesMaxBatch + 1) * (int)sizeof(int));
+        if (e != cudaSuccess) return e;
+        allowed[dev].store(true, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg{};
+    const int ctas = (P.m + kRun * kRowsThreads - 1) / (kRun * kRowsThreads);
+    cfg.gridDim = dim3(ctas < 2 * num_sms() ? ctas : 2 * num_sms());
+    cfg.blockDim = dim3(kRowsThreads);
+    cfg.dynamicSmemBytes = (size_t)2 * (P.batch + 1) * sizeof(int);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, rows_kernel, P);
 }
 
 template <int T>
@@ -260,7 +368,9 @@ cudaError_t launch_page_tables(const int32_t* kept, const int32_t* fresh, const 
     P.batch = batch; P.m = m; P.max_pages = max_pages; P.page_shift = page_shift; P.num_pages = num_pages;
     P.err_flag = err_flag;
     if (batch <= kFewThreads && m <= 4 * kFewThreads) return launch_tables<kFewThreads>(P, 1, stream);
-    return launch_tables<kManyThreads>(P, kTablesCluster, stream);
+    P.rows_apart = (pos || slots) && m > kRowsTogether;
+    const cudaError_t e = launch_tables<kManyThreads>(P, kTablesCluster, stream);
+    return e != cudaSuccess || !P.rows_apart ? e : launch_rows(P, stream);
 }
 
 }  // namespace q4k

@@ -539,10 +539,10 @@ int q4k_shared_prefix_attention(const void* d_q, int dtype, int m, int q_heads, 
  *   holds (Q4K_ERR_PAGE); tokens that exceed m rows, in the order of sequences, or a row of the table, or are negative, are
  *   not brought (their sequence gets no new ones; Q4K_ERR_SEQ). q_start and seq_lens tell what each got. kept, held, fixed and
  *   free_count outside what fits are clamped (Q4K_ERR_SEQ, Q4K_ERR_PAGE); a page id outside [0, num_pages) that is taken, or in
- *   whose page a new token lies, raises Q4K_ERR_PAGE. No access leaves its buffer: page_table [batch][max_pages], free_pages
+ *   whose page a new token lies (if slots are asked for), raises Q4K_ERR_PAGE. No access leaves its buffer: page_table [batch][max_pages], free_pages
  *   [num_pages].
  * batch 0 or m 0 are calls like others. Limits (Q4K_ERR_LIMIT): batch <= 8192, m <= 2^24,
- * max_pages*page_size <= 2^30. One launch. */
+ * max_pages*page_size <= 2^30. One launch, two for more than 16384 rows. */
 int q4k_page_tables(const int32_t* d_kept, const int32_t* d_new, const int32_t* d_fixed, int batch, int m, int max_pages,
                     int page_size, int num_pages, const int32_t* d_held, int32_t* d_free_pages,
                     const int32_t* d_free_count, int32_t* d_page_table, int32_t* d_held_out, int32_t* d_free_count_out,

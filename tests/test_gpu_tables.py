@@ -319,3 +319,30 @@ def test_other_stream_and_two_at_once():
     torch.cuda.synchronize()
     for s, o, w in zip(steps, outs, want):
         check(o, w, s.m)
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("batch,new_hi,kept_hi,spare,pad", [
+    (1, 17000, 50, 1100, 2), (3, 30001, 900, 9000, 7), (300, 70, 400, 9000, 9001), (5000, 9, 300, 9000, 0), (20, 3000, 200, 700, 1), (2, 0, 90, 5, 16391)])
+def test_many_rows(batch, new_hi, kept_hi, spare, pad, page, shift):
+    """More rows than one cluster writes; outputs that begin at and beside a 16-byte boundary; positions or slots alone."""
+    s = Step(batch + page, batch, page, new_hi, kept_hi, spare, 2, 30, 0.1, pad, width=(kept_hi + new_hi) // page + 4)
+    if batch == 1:
+        s.new[:], s.m = new_hi, new_hi + pad
+    want, flags = s.want()
+    assert s.m > 16384 and flags <= {PAGE_FLAG}
+    for rows in ("both", "pos", "slots"):
+        t = s.device()
+        e = lambda n, d=torch.int32: torch.full((n,), -77, dtype=d, device="cuda")  # noqa: E731
+        pos, slots = e(s.m + 8)[shift:], e(s.m + 8, torch.int64)[shift:]
+        out = dict(table=t["table"], free=t["free"], held=e(batch), count=e(1), start=e(batch + 1), lens=e(batch), pos=pos, slots=slots)
+        flag = err_flag()
+        q4k.q4k_page_tables(t["kept"], t["new"], t["fixed"], batch, s.m, s.width, page, s.pages, t["held"], t["free"], t["count"],
+                            t["table"], out["held"], out["count"], out["start"], out["lens"], pos if rows != "slots" else None,
+                            slots if rows != "pos" else None, flag)
+        for k in ("pos", "slots"):
+            if rows not in ("both", k):
+                assert (host(out.pop(k)) == -77).all()
+        check(out, {k: v for k, v in want.items() if k in out}, s.m)
+        assert int(flag) == (PAGE_FLAG if flags else 0)
