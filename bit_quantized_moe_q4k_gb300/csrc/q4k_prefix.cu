@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     for (int i = tid; i < batch; i += kPlanThreads) {
         const int a = __ldcg(A.B.q_start + i), b = __ldcg(A.B.q_start + i + 1), l = __ldcg(A.B.seq_lens + i);
         if (a < 0 || b < a || b > A.B.m) bad = true;
+        if (l < 0 || l > cap || l < b - a) raise_flag(A.err_flag, Q4K_ERR_SEQ);
         if (near) {
             s_start[i] = a;
             if (i == batch - 1) s_start[batch] = b;

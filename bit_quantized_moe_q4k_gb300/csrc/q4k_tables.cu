@@ -248,7 +248,8 @@ __global__ void __launch_bounds__(T) tables_kernel(const __grid_constant__ Table
     // Pages: the k-th taken is the one at place top - 1 - k of the stack, and what stays on it above `count` is the pages given back that nobody took.
     // Entries taken are written where no entry is read: given-back ones lie in other sequences' rows, free pages below `count`.
 #pragma unroll 1
-    for (int x = at; x < max(taken, left - count); x += step) {
+    for (int64_t y = at; y < max(taken, left - count); y += step) {
+        const int x = (int)y;
 #pragma unroll 1
         for (int side = 0; side < 2; ++side) {
             if (x >= (side ? left - count : taken)) continue;

@@ -54,7 +54,7 @@ class Shared:
         self.seed = seed
 
     def run(self, hq, dtype, window=0, gain=1.0, pad=0, check=True, flagged=0, hints=None, table=None, start=None, prefix=None,
-            times=2, max_prefix=None, ws=None):
+            times=2, max_prefix=None, ws=None, raw_lens=None, raw_starts=None):
         g = np.random.default_rng(self.seed + 1)
         hk, d, m, b = self.hk, self.d, sum(self.new), len(self.new)
         c = self.cache
@@ -70,8 +70,8 @@ class Shared:
         got = []
         for _ in range(times):
             q4k.q4k_shared_prefix_attention(
-                q, m, hq, hk, d, hq * d + pad, c.dev["k"], c.dev["v"], c.dev_scale["k"], c.dev_scale["v"], dev(q_starts(self.new)),
-                dev(np.array(self.lens, np.int32)), dev(table), b, table.shape[1], self.page, c.pages, dev(np.asarray(start, np.int32)),
+                q, m, hq, hk, d, hq * d + pad, c.dev["k"], c.dev["v"], c.dev_scale["k"], c.dev_scale["v"], dev(np.asarray(raw_starts or q_starts(self.new), np.int32)),
+                dev(np.array(raw_lens or self.lens, np.int32)), dev(table), b, table.shape[1], self.page, c.pages, dev(np.asarray(start, np.int32)),
                 dev(np.asarray(prefix, np.int32)), len(prefix), maxq, maxl,
                 int(max([0, *prefix])) if max_prefix is None else max_prefix, scale, window, out, hq * d + pad, ws, nbytes, flag)
             got.append(f64(out))
@@ -364,3 +364,54 @@ def test_what_is_shared_goes_by_size(dtype, setting, monkeypatch):
     Shared(32, [(1000, samples(2)), (1500, samples(70)), (900, samples(3, 2)), (30, samples(9))], 8, 64, 32).run(32, dtype)  # some groups of a large one
     Shared(33, [(700, samples(2)) for _ in range(30)], 8, 64, 32).run(32, dtype, max_prefix=1 << 30)  # no group
     Shared(34, [(1500, samples(70))], 8, 64, 32).run(32, dtype, window=300)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_malformed_lengths(dtype):
+    """Lengths below the new tokens, below zero: flagged, clamped; the group shares what lies before all its new tokens, here nothing."""
+    s = Shared(40, [(200, [(1, 9), (4, -202), (1, 5), (2, -202)]), (300, samples(6))], 2, 64, 16)
+    assert s.lens[1] == 2 and s.lens[3] == 0
+    raw = list(s.lens)
+    raw[3] = -7
+    s.run(8, dtype, raw_lens=raw, flagged=SEQ_FLAG)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_malformed_starts(dtype):
+    """Starts that fall or leave the rows: flagged, nothing is shared, no access leaves its buffer."""
+    s = Shared(41, [(200, samples(6, 2)), (300, samples(6))], 2, 64, 16)
+    good = q_starts(s.new).tolist()
+    for raw in ([0, 2, 4, 3, 8, 10, 12, 13, 14, 15, 16, 17, 18], [-5, *good[1:]], [*good[:-1], 1000], [18] * 13, good[::-1]):
+        s.run(8, dtype, raw_starts=raw, flagged=SEQ_FLAG, check=False, times=1)   # (rows of two sequences are either's)
+    s.run(8, dtype)
+
+
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_more_sequences_than_the_plan_holds_at_hand(dtype, window):
+    """Lengths and places of sequences, and groups, that are looked up in device memory."""
+    Shared(42, [(200, [(1 + i % 2, i % 20) for i in range(2100)])], 1, 64, 16, before=[(1, 30)] * 9).run(2, dtype, window)
+    Shared(43, [(64 + 16 * (k % 3), samples(2 + k % 3)) for k in range(200)], 1, 64, 16).run(2, dtype, window)
+    Shared(44, [(160, samples(12)) for k in range(180)], 1, 64, 16).run(1, dtype, window)   # both
+
+
+def test_more_rows_than_are_shared():
+    """q4k_paged_attention's own result, bit for bit."""
+    hq, hk, d, page, batch, n = 32, 4, 64, 16, 8200, 4
+    m, c = batch * n, Cache(45, 12, hk, page, d)
+    c.upload()
+    table, starts, lens = dev(np.resize(c.order[:12], (batch, 3)).astype(np.int32)), dev(np.arange(0, m + 1, n, dtype=np.int32)), dev(np.full(batch, 40, np.int32))
+    q = rows(np.random.default_rng(45).standard_normal((m, hq * d)), "bf16")
+    flag, outs = err_flag(), [torch.empty_like(q), torch.empty_like(q)]
+    for shared, out in enumerate(outs):
+        args = (q, m, hq, hk, d, hq * d, c.dev["k"], c.dev["v"], c.dev_scale["k"], c.dev_scale["v"], starts, lens, table, batch, 3, page, 12)
+        if shared:
+            nbytes = q4k.q4k_shared_prefix_attention_workspace_size(batch, 1, m, hq, hk, d)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+            q4k.q4k_shared_prefix_attention(*args, dev(np.array([0, batch], np.int32)), dev(np.array([32], np.int32)), 1, n, 40, 32, 0.125, 0, out,
+                                            hq * d, ws, nbytes, flag)
+        else:
+            nbytes = q4k.q4k_paged_attention_workspace_size(batch, m, hq, hk, d)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+            q4k.q4k_paged_attention(*args, n, 40, 0.125, 0, out, hq * d, ws, nbytes, flag)
+    assert int(flag) == 0 and torch.equal(*outs)

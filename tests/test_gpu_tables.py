@@ -346,3 +346,13 @@ def test_many_rows(batch, new_hi, kept_hi, spare, pad, page, shift):
                 assert (host(out.pop(k)) == -77).all()
         check(out, {k: v for k, v in want.items() if k in out}, s.m)
         assert int(flag) == (PAGE_FLAG if flags else 0)
+
+
+def test_most_sequences():
+    for new_hi in (1, 5):   # in the cluster, and with a second kernel
+        s = Step(50 + new_hi, 8192, 16, new_hi, 200, 9000, 2, 60, 0.2, 3)
+        want, flags = s.want()
+        assert not flags and (s.m > 16384) == (new_hi == 5)
+        out, flag = call(s, s.device())
+        check(out, want, s.m)
+        assert int(flag) == 0
