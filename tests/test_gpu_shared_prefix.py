@@ -382,7 +382,8 @@ def test_malformed_starts(dtype):
     s = Shared(41, [(200, samples(6, 2)), (300, samples(6))], 2, 64, 16)
     good = q_starts(s.new).tolist()
     for raw in ([0, 2, 4, 3, 8, 10, 12, 13, 14, 15, 16, 17, 18], [-5, *good[1:]], [*good[:-1], 1000], [18] * 13, good[::-1]):
-        s.run(8, dtype, raw_starts=raw, flagged=SEQ_FLAG, check=False, times=1)   # (rows of two sequences are either's)
+        flagged = 0 if raw == [18] * 13 else SEQ_FLAG   # (no sequence has rows: within the rules)
+        s.run(8, dtype, raw_starts=raw, flagged=flagged, check=False, times=1)   # (rows of two sequences are either's)
     s.run(8, dtype)
 
 
