@@ -46,6 +46,28 @@ struct VerifyParams {
 
 // NaN as -inf (such a token has no probability), +inf as the largest finite number.
 __device__ __forceinline__ float tame(float x) { return fminf(fmaxf(x, -INFINITY), kLargest); }
+// +inf as the largest finite number, NaN as it is.
+__device__ __forceinline__ float below_inf(float x) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(kLargest));
+    return y;
+}
+// Shifts of which amounts from the type's width on, negative ones among them, leave nothing.
+__device__ __forceinline__ uint32_t shr(uint32_t x, int by) {
+    uint32_t y;
+    asm("shr.u32 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(by));
+    return y;
+}
+__device__ __forceinline__ uint64_t shr(uint64_t x, int by) {
+    uint64_t y;
+    asm("shr.u64 %0, %1, %2;" : "=l"(y) : "l"(x), "r"(by));
+    return y;
+}
+__device__ __forceinline__ uint32_t shl(uint32_t x, int by) {
+    uint32_t y;
+    asm("shl.b32 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(by));
+    return y;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -345,13 +367,13 @@ struct Weigher {
         *mant = t.x + (uint32_t)(__float_as_int(fmaf(__uint_as_float(t.y), p, kRound)) - kRoundBits);
         *e = n >> 10;
     }
-    // In units of 2^-bits, cut off; 0 for tokens without probability.
+    // In units of 2^-bits, cut off; 0 for tokens without probability (their exponent is -200).
     __device__ __forceinline__ uint64_t operator()(float x) const {
         uint32_t w;
         int e;
         parts(x, &w, &e);
-        const int shift = down - e;   // w 2^-31 2^e in that unit: w 2^32 to the right
-        return shift > 63 ? 0 : ((uint64_t)w << 32) >> shift;
+        const int shift = down - e;   // w 2^-31 2^e in that unit: w 2^32 to the right, by 64 and more to nothing
+        return (uint64_t)shr(w, shift) << 32 | (shl(w, 32 - shift) | shr(w, shift - 32));
     }
     // mantissa in [2^43, 2^44) and exponent: weight = mant 2^(e - 43). False: below 2^-1000, or no probability.
     __device__ __noinline__ bool precise(float x, uint64_t* mant, int* e) const {
@@ -381,9 +403,25 @@ struct Weigher {
         return up >= 0 ? mant << up : up < -45 ? 0 : ((mant >> (-up - 1)) + 1) >> 1;
     }
 };
-// floor(f * s) for f in [0, 1] (above: s, below or NaN: 0), s < 2^63.
+// f * s for a sum s < 2^63, of which it keeps 32 bits (2^-31 of itself), and f in [0, 1], cut off.
+struct Portion {
+    uint32_t top;
+    int down;
+    __device__ __forceinline__ explicit Portion(uint64_t s) {
+        const int lead = __clzll((int64_t)(s | 1));
+        top = (uint32_t)((s << lead) >> 32);
+        down = 126 + lead;
+    }
+    __device__ __forceinline__ uint64_t operator()(float f) const {
+        const uint32_t b = __float_as_uint(f);   // f = (b << 8 | 2^31) 2^(b >> 23 - 158); zero and denormal numbers give less than 1
+        return shr((uint64_t)(b << 8 | 0x80000000u) * top, down - (int)(b >> 23));
+    }
+};
+// A probability as it counts: above 1 as 1, below 0 and NaN as 0.
+__device__ __forceinline__ float fraction(float f) { return fminf(fmaxf(f, 0.0f), 1.0f); }
+// floor(f * s), exactly.
 __device__ __forceinline__ uint64_t portion(float f, uint64_t s) {
-    const uint32_t b = __float_as_uint(fminf(fmaxf(f, 0.0f), 1.0f));
+    const uint32_t b = __float_as_uint(fraction(f));
     const uint32_t m8 = b << 8 | 0x80000000u;   // f = m8 2^(e - 158), but for zero and denormal numbers, whose product is below 1
     const uint64_t hi = (uint64_t)m8 * (uint32_t)(s >> 32) + (((uint64_t)m8 * (uint32_t)s) >> 32);  // m8 s / 2^32
     const int down = 126 - (int)(b >> 23);
@@ -605,6 +643,7 @@ __global__ void __launch_bounds__(kPickThreads, 4) verify_pick_kernel(const __gr
         // segment is off by s times the q of the tokens that are left something (which those are, S decides well enough: a token that
         // changes sides has next to nothing left). So each segment keeps both sums, and the precise S comes in afterwards.
         about = __float2ull_rn(R.sum * __int_as_float((127 + A.bits) << 23));
+        const Portion away_of(about);
         uint64_t cta_whole = 0, cta_left = 0, cta_share = 0;   // shares in units of 2^-40
         for (int sg = seg0 + warp; sg < seg1; sg += kPickWarps) {
             uint64_t all = 0, left = 0;
@@ -622,13 +661,14 @@ __global__ void __launch_bounds__(kPickThreads, 4) verify_pick_kernel(const __gr
                 for (int i = 0; i < kAhead; ++i)
 #pragma unroll
                     for (int k = 0; k < V; ++k) {
-                        const uint64_t w = W(fminf(v[i][k], kLargest));   // (-inf and NaN it takes as they are)
+                        const uint64_t w = W(below_inf(v[i][k]));
                         all += w;
                         if (q) {
-                            const uint64_t away = portion(p[i][k], about);
+                            const float f = fraction(p[i][k]);
+                            const uint64_t away = away_of(f);
                             if (w > away) {
                                 left += w - away;
-                                share += fmaxf(p[i][k], 0.0f);
+                                share += f;
                             }
                         } else if (sg * kSeg + (i0 + i) * 32 * V + lane * V + k != drafted) {
                             left += w;
