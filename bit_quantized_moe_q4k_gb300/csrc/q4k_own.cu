@@ -5,7 +5,9 @@
 // But a piece (a row tile of a kv head, over some hundred tokens) is one warp's, from its list entry to its sums in the workspace, and warps
 // share nothing: while one looks up pages or writes its sums, the other eleven of the SM stream. Own parts are short, so that in the kernel for
 // whole sequences, where four warps share a tile and wait for one another at its start, in its join and at its end, starts and ends
-// were two thirds of the time.
+// were two thirds of the time. Bound by each warp's chain of copies, products and exponentials, twelve warps an SM: 256 sequences of up to 1000
+// tokens, 8 kv heads of 128, bf16, 262 MB: 70 us alone, 3.8 TB/s. Looking a piece up while the one before it streams, and longest pieces
+// first, gave nothing (215 us for the whole call behind 32768 shared tokens, and 219).
 #include <atomic>
 
 #include "q4k_attn_few.cuh"

@@ -9,9 +9,12 @@
 // decides is computed precisely, and the whole is read in fp32:
 //   1. verify_stats_kernel: each row's largest logit and its sum of 2^(c (x - max)), c = log2(e) / T, in fp32, by chunks of
 //      rows over all SMs. Bound by the logits' bytes.
-//   2. verify_pick_kernel: a cluster of eight CTAs a sequence. An acceptance whose two sides differ by more than 2^-14 stands;
+//   2. verify_pick_kernel: a cluster of up to eight CTAs a sequence. An acceptance whose two sides differ by more than 2^-14 stands;
 //      another is computed again from weights good to 2^-41. The token is drawn in weights good to 2^-31, as 64-bit integers in units of
 //      2^-b of the row's largest, b = 62 - log2(vocabulary): their sums are exact in any order. One row of logits, and of the drafts' probabilities, is read once.
+//      Bound by instructions, 58 a token.
+// 256 sequences of 4 rows of 131072 fp32: 86 us (6.3 TB/s) and 96; 64 of up to 6 rows in bf16: 58 together; one of 5 rows of 32000: 12.
+// Both in one kernel, a cluster going through its rows one after another: 172 to 177, 62 and 15 us.
 #include <atomic>
 
 #include "q4k_paged.cuh"
