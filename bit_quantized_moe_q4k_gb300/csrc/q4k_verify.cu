@@ -27,9 +27,9 @@ constexpr int kPickThreads = 256, kPickWarps = kPickThreads / 32, kMostCluster =
 constexpr int kSeg = 512;                           // tokens of a segment, whose sum is kept
 constexpr float kGreedy = 5.421010862427522e-20f;   // 2^-64: temperatures not above choose the largest logit
 constexpr float kLargest = 3.402823466e38f;
-// The relative error of a decision's two sides in fp32 is below (1.4 |y| + 86) 2^-23, y the draft's exponent: four roundings of y
+// The relative error of a decision's two sides in fp32 is below (1.4 |y| + 94) 2^-23, y the draft's exponent: four roundings of y
 // (4 ln 2 2^-24 |y|), the same in the sum, where the mean of |y| is the distribution's entropy at most (20 bits), ex2 (2 2^-23), up to
-// nine changes of a thread's largest (18 2^-23), and some sixty additions one after another (30 2^-23).
+// thirteen changes of a thread's largest (26 2^-23), and some sixty additions one after another (30 2^-23).
 __device__ __forceinline__ float closeness(float y) { return fmaf(fabsf(y), 1.5f, 96.0f) * 1.1920929e-7f; }
 // And where it is computed from the draw's weights, 2^-31 each and cut at 2^-45 of 2^17 tokens.
 constexpr double kCloseFine = 1.0 / 67108864.0;
@@ -127,9 +127,9 @@ __device__ __forceinline__ int sequence_of(const VerifyParams& A, int r) {
 
 // ---- the rows in fp32 ---------------------------------------------------------------------------------------------
 template <typename T>
-__global__ void __launch_bounds__(kStatThreads, 4) verify_stats_kernel(const __grid_constant__ VerifyParams A) {
+__global__ void __launch_bounds__(kStatThreads, 6) verify_stats_kernel(const __grid_constant__ VerifyParams A) {
     constexpr int V = 16 / (int)sizeof(T), W = kStatThreads / 32;
-    constexpr int kUnits = 4;  // 16-byte units a thread and batch
+    constexpr int kUnits = 2;  // 16-byte units a thread and batch (4, with 4 CTAs an SM: 64 sequences of 131072 in bf16 58.4 us, with 2 and 6 56.8)
     __shared__ float s_m[W], s_s[W], s_t;
     __shared__ int s_i[W], s_seq;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -827,9 +827,9 @@ __global__ void __launch_bounds__(kPickThreads, 4) verify_pick_kernel(const __gr
 }
 
 int chunks_of(int m, int vocab) {
-    // Eight CTAs on each of 152 SMs where there are few rows (but 4096 logits a CTA at least), pieces of up to 16384 where there
-    // are many.
-    const int64_t want = (8 * 152 + (int64_t)m - 1) / (m < 1 ? 1 : m), most = (vocab + 4095) / 4096, least = (vocab + 16383) / 16384;
+    // Five CTAs on each of 152 SMs, one wave, where there are few rows (but 4096 logits a CTA at least), pieces of up to 16384 where there
+    // are many. 150 rows of 50001 logits, whole call: 20.8 us, with eight 25.7, with four 21.9.
+    const int64_t want = (5 * 152 + (int64_t)m - 1) / (m < 1 ? 1 : m), most = (vocab + 4095) / 4096, least = (vocab + 16383) / 16384;
     return (int)(want > most ? most : want < least ? least : want);
 }
 
