@@ -568,7 +568,7 @@ int q4k_page_tables(const int32_t* d_kept, const int32_t* d_new, const int32_t* 
  *   A logit of -inf or NaN has no probability, +inf counts as the largest finite number. Random numbers are meant from [0, 1):
  *   outside it u_sample counts as the nearer end, u_accept as it stands, below 0 (or NaN) as 0; negative or NaN probabilities count as 0.
  *   Decisions are those of exact arithmetic but where a random number comes next to a border: weights are good to 2^-41 of
- *   themselves in acceptances, 2^-31 in draws, and in sums cut to 2^-(62 - ceil(log2(vocab))) of the row's largest weight.
+ *   themselves in acceptances, 2^-31 in draws (and what is taken away for a draft), and in sums cut to 2^-(62 - ceil(log2(vocab))) of the row's largest weight.
  * Device flags: a draft outside [0, vocab) is rejected, a row of logits without any probability gives next -1 (Q4K_ERR_TOKEN);
  * q_start falling or outside [0, m] is clamped (Q4K_ERR_SEQ).
  * Limits (Q4K_ERR_LIMIT): vocab <= 2^20, m and batch <= 2^24. Two launches.

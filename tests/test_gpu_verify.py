@@ -346,3 +346,29 @@ def test_captured_and_on_two_streams():
         for b, (s, g) in zip(batches, made):
             acc, nxt, kept, _ = plain(b.x.float().numpy(), b.probs, b.tokens, b.start, b.t, b.ua, b.us, b.lens)
             assert [host(o).tolist() for o in s["out"]] == [acc, nxt, kept]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_largest_vocabulary(dtype):
+    Batch(60, [3, 1, 2], 1 << 20, dtype, temperature="warm").check()
+    Batch(61, [2, 2], (1 << 20) - 1, dtype, probs=False, temperature="warm").check()
+
+
+@pytest.mark.parametrize("t", [1e38, 3e38, 1e-37, 2.0 ** -63])
+def test_nan_and_infinite_logits_at_extreme_temperatures(t):
+    b = Batch(62, [2] * 20, 900, probs=False, temperature="one")
+    b.t = np.full(b.b, t, np.float32)
+    b.x[::2, 5:450] = math.nan
+    b.x[1::3, 100:600] = -math.inf
+    b.check()
+
+
+def test_kept_in_place_of_the_lengths():
+    b = Batch(63, [3, 0, 2, 5], 800)
+    want = plain(b.x.numpy(), b.probs, b.tokens, b.start, b.t, b.ua, b.us, b.lens)
+    i32 = lambda a: dev(np.asarray(a, np.int32))  # noqa: E731
+    lens, acc, nxt, flag = i32(b.lens), i32([0] * 4), i32([0] * 4), err_flag()
+    ws = torch.empty(q4k.q4k_verify_drafts_workspace_size(b.b, b.m, b.v), dtype=torch.uint8, device="cuda")
+    q4k.q4k_verify_drafts(b.x.cuda(), b.m, b.v, b.v, dev(b.probs), b.v, i32(b.tokens), i32(b.start), b.b, dev(b.t), dev(b.ua), dev(b.us), lens,
+                          acc, nxt, lens, ws, ws.numel(), flag)
+    assert [host(o).tolist() for o in (acc, nxt, lens)] == list(want[:3]) and int(flag) == 0
