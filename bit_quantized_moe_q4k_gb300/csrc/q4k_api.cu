@@ -941,7 +941,7 @@ int q4k_shared_prefix_attention(const void* d_q, int dtype, int m, int q_heads, 
     st = check_workspace(d_workspace, ws_bytes, own + align_up(more));
     if (st) return st;
     const bool share = more > 0 && max_prefix >= page_size &&
-                       prefix_pays(B, dtype, q_heads, kv_heads, groups, max_q_len, max_prefix, window);
+                       prefix_pays(B, dtype, q_heads, kv_heads, groups, max_q_len, max_len, max_prefix, window);
     SharedPrefix S{d_group_start, d_prefix_lens, groups, static_cast<uint8_t*>(d_workspace) + own};
     return cuda_status(launch_attention(B, d_q, dtype, q_stride, q_heads, kv_heads, head_dim,
                                         static_cast<const uint8_t*>(d_k_cache), static_cast<const uint8_t*>(d_v_cache),

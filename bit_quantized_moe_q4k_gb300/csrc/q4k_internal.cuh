@@ -70,7 +70,7 @@ struct SharedPrefix {
     void* workspace;   // prefix_workspace_bytes, behind the attention's own
 };
 size_t prefix_workspace_bytes(int batch, int groups, int m, int q_heads, int kv_heads, int head_dim);
-bool prefix_pays(const PagedBatch& B, int dtype, int q_heads, int kv_heads, int groups, int max_q_len, int max_prefix, int window);
+bool prefix_pays(const PagedBatch& B, int dtype, int q_heads, int kv_heads, int groups, int max_q_len, int max_len, int max_prefix, int window);
 cudaError_t launch_prefix(const PagedBatch& B, const void* q, int dtype, int64_t q_stride, int q_heads, int kv_heads,
                           int head_dim, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
                           const float* v_scale, const SharedPrefix& shared, int max_rows, float scale, int window, void* out,

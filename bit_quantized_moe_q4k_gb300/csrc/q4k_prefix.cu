@@ -1209,18 +1209,26 @@ size_t prefix_workspace_bytes(int batch, int groups, int m, int q_heads, int kv_
 // cuts them and a kv head, fewer it would read if its groups were equally large. On both sides of the bound, shared and not (bf16, 8 kv
 // heads, one new token each): a group of 32 behind 2048 tokens (3600) 33 and 34 us, 8 behind 8192 (2448) 36 and 32, 4 behind 512 25 and 9,
 // 16 groups of 16 behind 512 (4864) 68 and 77, 24 of 6 behind 2048 (6528) 102 and 110, 24 of 5 (3456) 105 and 93.
+// The sequences' own units cost more here, each 9/32 of one: 64 sequences with 8000 tokens of their own behind 2048 take 222 and 182 us, 32 with up to
+// 30000 behind 8192 191 and 171, 128 with up to 2000 behind 4096 95 and 182. max_len tells how many they may be; where that is more than
+// eight times the prefix, it is taken for a bound that says nothing, since sharing in vain loses less than not sharing.
 // Switch (environment, read at every call): Q4K_SHARE_PREFIX=1 shares whatever can be, 0 nothing.
 constexpr int64_t kShareLeast = 4500;
-bool prefix_pays(const PagedBatch& B, int dtype, int q_heads, int kv_heads, int groups, int max_q_len, int max_prefix, int window) {
+bool prefix_pays(const PagedBatch& B, int dtype, int q_heads, int kv_heads, int groups, int max_q_len, int max_len, int max_prefix, int window) {
     if (share_setting() >= 0) return share_setting() > 0;
     int64_t tokens = (int64_t)B.max_pages << B.page_shift;
+    int64_t own = max_len < tokens ? max_len : tokens;
     tokens = max_prefix < tokens ? max_prefix : tokens;
-    if (window > 0 && window < tokens) tokens = window;
+    own = own > tokens && own - tokens <= 8 * tokens ? own - tokens : 0;
+    if (window > 0) {
+        tokens = window < tokens ? window : tokens;
+        own = window < own ? window : own;
+    }
     const int64_t rep = q_heads / kv_heads, units = (tokens + kToks - 1) / kToks, rows = B.m * rep;
     const int64_t own_rows = dtype == Q4K_F32 || max_q_len * rep <= 8 ? 8 : 16, shared_rows = dtype == Q4K_F32 ? kRows : 2 * kRows;
     const int64_t live = B.batch < B.m ? B.batch : B.m, by_rows = (rows + own_rows - 1) / own_rows;
     const int64_t tiles = live > by_rows ? live : by_rows, row_tiles = (groups < live ? groups : live) + rows / shared_rows;
-    return (tiles * units - row_tiles * (3 * units + 14)) * kv_heads >= kShareLeast;
+    return (tiles * units - row_tiles * (3 * units + 14) - tiles * (own / kToks) * 9 / 32) * kv_heads >= kShareLeast;
 }
 
 cudaError_t launch_prefix(const PagedBatch& B, const void* q, int dtype, int64_t q_stride, int q_heads, int kv_heads,

@@ -499,7 +499,7 @@ int q4k_paged_attention(const void* d_q, int dtype, int m, int q_heads, int kv_h
  *   What is shared is the whole pages of the prefix that lie before every new token of the group's sequences; the sequences read all else,
  *   and what small groups hold in common, as in q4k_paged_attention.
  *   max_prefix: an upper bound of prefix_lens that chooses the kernels: calls that would save too little (by batch, groups, m, heads,
- *   max_q_len, max_prefix and window) run q4k_paged_attention's kernels and read neither group_start nor prefix_lens. Environment switch, read
+ *   max_q_len, max_len, max_prefix and window) run q4k_paged_attention's kernels and read neither group_start nor prefix_lens. Environment switch, read
  *   at every call: Q4K_SHARE_PREFIX=1 shares all it can where max_prefix >= page_size, 0 nothing.
  *   The rest: as in q4k_paged_attention. Sequences of more than 64 query rows per kv head in calls that it gives to its prompt
  *   kernels, and calls of more than 2^20 query rows (m*q_heads), read their prefixes themselves.

@@ -364,6 +364,8 @@ def test_what_is_shared_goes_by_size(dtype, setting, monkeypatch):
     Shared(32, [(1000, samples(2)), (1500, samples(70)), (900, samples(3, 2)), (30, samples(9))], 8, 64, 32).run(32, dtype)  # some groups of a large one
     Shared(33, [(700, samples(2)) for _ in range(30)], 8, 64, 32).run(32, dtype, max_prefix=1 << 30)  # no group
     Shared(34, [(1500, samples(70))], 8, 64, 32).run(32, dtype, window=300)
+    for most in (2500, 1 << 29):   # long own parts by the hint, and a hint that says nothing
+        Shared(35, [(1000, samples(70))], 8, 64, 32).run(32, dtype, hints=(1, most))
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
