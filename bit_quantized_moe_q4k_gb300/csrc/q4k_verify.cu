@@ -13,7 +13,7 @@
 //      another is computed again from weights good to 2^-41. The token is drawn in weights good to 2^-31, as 64-bit integers in units of
 //      2^-b of the row's largest, b = 62 - log2(vocabulary): their sums are exact in any order. One row of logits, and of the drafts' probabilities, is read once.
 //      Bound by instructions, 58 a token.
-// 256 sequences of 4 rows of 131072 fp32: 86 us (6.3 TB/s) and 96; 64 of up to 6 rows in bf16: 58 together; one of 5 rows of 32000: 12.
+// 256 sequences of 4 rows of 131072 fp32: 85 us (6.3 TB/s) and 96; 64 of up to 6 rows in bf16: 57 together; one of 5 rows of 32000: 12.
 // Both in one kernel, a cluster going through its rows one after another: 172 to 177, 62 and 15 us.
 #include <atomic>
 
