@@ -418,3 +418,15 @@ def test_more_rows_than_are_shared():
             ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
             q4k.q4k_paged_attention(*args, n, 40, 0.125, 0, out, hq * d, ws, nbytes, flag)
     assert int(flag) == 0 and torch.equal(*outs)
+
+
+def test_one_workspace_for_calls_in_turn():
+    """Calls of other sizes and types on the same bytes, one after another."""
+    made = [(Shared(50, [(700, samples(9))], 2, 128, 32), 8, "f32"), (Shared(51, [(300, samples(70)), (900, samples(12, 3))], 4, 64, 16), 16, "bf16"),
+            (Shared(52, [(2000, samples(7, 2))], 1, 64, 64), 4, "bf16")]
+    need = max(q4k.q4k_shared_prefix_attention_workspace_size(len(s.new), len(s.prefix), sum(s.new), hq, s.hk, s.d) for s, hq, _ in made)
+    ws = torch.full((need,), 0xA5, dtype=torch.uint8, device="cuda")
+    want = [s.run(hq, dtype) for s, hq, dtype in made]
+    for _ in range(2):
+        for (s, hq, dtype), w in zip(made, want):
+            assert np.array_equal(s.run(hq, dtype, check=False, times=1, ws=ws), w)

@@ -356,3 +356,30 @@ def test_most_sequences():
         out, flag = call(s, s.device())
         check(out, want, s.m)
         assert int(flag) == 0
+
+
+def test_captured_prompts_in_chunks():
+    """Rows by the second kernel, captured, lengths and held pages in place: each replay goes on where the last one ended."""
+    batch, chunk, page, steps = 20, 900, 32, 3
+    s = Step(70, batch, page, 0, 0, 20 * (steps * chunk // page + 1), width=steps * chunk // page + 2)
+    s.new[:], s.m = chunk, batch * chunk
+    t = s.device()
+    out, flag = call(s, t, in_place=True)   # outside a graph first: the state it leaves is put back
+    t2 = s.device()
+    for k in t:
+        t[k].copy_(t2[k])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q4k.q4k_page_tables(t["kept"], t["new"], t["fixed"], batch, s.m, s.width, page, s.pages, t["held"], t["free"], t["count"], t["table"],
+                            t["held"], t["count"], out["start"], t["kept"], out["pos"], out["slots"], flag)
+    assert s.m > 16384
+    for _ in range(steps):
+        want, flags = s.want()
+        assert not flags
+        graph.replay()
+        torch.cuda.synchronize()
+        check(dict(table=t["table"], free=t["free"], held=t["held"], count=t["count"], start=out["start"], lens=t["kept"], pos=out["pos"],
+                   slots=out["slots"]), want, s.m)
+        s.kept, s.held, s.count = np.array(want["lens"]), np.array(want["held"]), want["count"][0]
+        s.table, s.free = want["table"], want["free"]
+    assert int(flag) == 0
