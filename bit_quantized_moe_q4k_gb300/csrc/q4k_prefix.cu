@@ -33,8 +33,6 @@ constexpr float kPieceCost = 6.0f, kOwnCost = 0.2f, kOwnTokensCost = 0.2f;
 // 2048 tokens, 8 kv heads, shared 190 us and not 134; 32 of 3 behind 2048 and 8192 109 and 104, 275 and 304; 32 of 4 behind 512 and 2048
 // 65 and 60, 113 and 130; 24 of 6 behind 512 and 2048 64 and 64, 102 and 140.
 constexpr float kShareUnit = 2.0f, kShareStart = 16.0f;
-// Tokens of an own piece at least: less does not pay for its start.
-constexpr int kOwnLeast = 128;
 
 int share_setting() {
     const char* s = getenv("Q4K_SHARE_PREFIX");
@@ -205,8 +203,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
         for (int o = 16; o; o >>= 1) tokens += __shfl_xor_sync(0xffffffffu, tokens, o);
         const int own_tiles = __reduce_add_sync(0xffffffffu, lane > 0 && lane < kPlanWarps ? s_own[lane] : 0);
         // Own pieces: one and a half for each warp that works on them, but not shorter than is worth a start.
-        const int64_t share = tokens * A.kv_heads / (kOwnCtas * kOwnWarps * 3 / 2);
-        const int length = (int)min(max((share + 31) & ~(int64_t)31, (int64_t)kOwnLeast), (int64_t)1 << 30);
+        const int length = own_length(tokens, A.kv_heads);
         // How many CTAs: the sequences' own tiles run on the SMs that these leave free, and on all when they are done. Candidates in steps
         // of a sixteenth, the cheapest by estimate.
         const float own_work = (float)A.kv_heads * (kOwnCost * ((float)own_tiles + (float)tokens / (float)length) +
@@ -334,7 +331,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     // the sequences' own row tiles, then their pieces
     const int length = s_head.own_length, counted = lane > 0 && lane < kPlanWarps ? s_own[lane] : 0;
     int at = tiles_before + __reduce_add_sync(0xffffffffu, lane < warp ? counted : 0);
-    auto pieces_of = [&](const int2& x) { return max((x.y - x.x + length - 1) / length, 1); };  // rows that see nothing are zeroed by one
+    auto pieces_of = [&](const int2& x) { return pieces_of_tile(x.y - x.x, length); };
     int pieces = 0;
     for (int i = s0; i < s1; ++i) {
         const Own w = own_of(i);
@@ -377,6 +374,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
         A.plan.own_piece[p] = make_int2(a, (p - first) * length);
     }
     if (tid == 0) {
+        if (s_head.own_tiles > A.plan.owns || all_pieces > A.plan.own_pieces) raise_flag(A.err_flag, Q4K_ERR_SEQ);
         PrefixHead H = s_head;
         H.own_tiles = all_tiles;
         H.own_pieces = all_tiles ? most : 0;
@@ -1170,9 +1168,8 @@ size_t layout(int batch, int groups, int m, int rep, int kv_heads, int head_dim,
         return p;
     };
     const int64_t items = most_items(batch, groups, m, rep, kv_heads, tile_rows), slots = items + kPrefixCtas;
-    // row tiles, a sequence's last part filled; their pieces: as many, and what a length of a share of all tokens adds (three for each two warps)
-    const int64_t owns = (int64_t)m * rep / kOwnRows + (m < batch ? m : batch);
-    const int64_t own_pieces = owns + kOwnCtas * kOwnWarps * 3 / 2 / kv_heads + 1;  // a piece of each kv head
+    // row tiles, a sequence's last part filled; a piece of each kv head
+    const int64_t owns = (int64_t)m * rep / kOwnRows + (m < batch ? m : batch), own_pieces = most_own_pieces(owns, kv_heads);
     plan->head = reinterpret_cast<PrefixHead*>(part(sizeof(PrefixHead)));
     plan->group = reinterpret_cast<PrefixGroup*>(part(sizeof(PrefixGroup) * (size_t)groups));
     plan->seq = reinterpret_cast<int2*>(part(sizeof(int2) * (size_t)batch));

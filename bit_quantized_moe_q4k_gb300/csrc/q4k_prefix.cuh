@@ -8,6 +8,7 @@
 #pragma once
 
 #include "q4k_paged.cuh"
+#include "q4k_pieces.cuh"
 
 namespace q4k {
 
@@ -79,8 +80,6 @@ struct PrefixPlan {
 // sequences), every sequence reads its prefix itself.
 constexpr int64_t kPrefixMaxRows = 1 << 20;
 constexpr int kPrefixCtas = 152;
-// Warps that work on own parts at a time: twelve on each of 152 SMs.
-constexpr int kOwnWarps = 4, kOwnCtas = 3 * 152;
 
 struct OwnParams {
     PagedBatch B;

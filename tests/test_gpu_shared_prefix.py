@@ -430,3 +430,12 @@ def test_one_workspace_for_calls_in_turn():
     for _ in range(2):
         for (s, hq, dtype), w in zip(made, want):
             assert np.array_equal(s.run(hq, dtype, check=False, times=1, ws=ws), w)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("hq,hk,own", [
+    (8, 8, [11009] * 4), (8, 2, [19585] * 9), (8, 1, [32001] * 11), (4, 2, [6529] * 27),
+    (8, 1, [103252, 56271, 42002, 21075, 89009, 13510, 10247, 17084])])
+def test_own_parts_of_more_tokens_than_whole_pieces(hq, hk, own, dtype):
+    """Own tokens that are a little more than 32 k for each of the pieces that a call is cut into."""
+    Shared(60, [(128, [(1, n - 1) for n in own])], hk, 64, 64).run(hq, dtype, times=1)

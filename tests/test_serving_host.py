@@ -1,5 +1,9 @@
 """Host-side checks (no GPU) of the calls around the paged cache in a serving step: invalid arguments are refused
 with the documented status before anything is enqueued, and the bindings refuse tensors of other element types."""
+import os
+import shutil
+import subprocess
+
 import pytest
 
 import bit_quantized_moe_q4k_gb300 as q4k
@@ -156,3 +160,66 @@ def test_prefix_binding_refuses_other_element_types():
             args[at] = other
             with pytest.raises(ValueError):
                 q4k.q4k_shared_prefix_attention(*args, stream=0)
+
+
+PIECES = r"""
+#include <cstdio>
+#include <cstdlib>
+#include "q4k_pieces.cuh"
+using namespace q4k;
+static long long worst = -(1LL << 60);
+static void check(const int* tile, long long tiles, int kv_heads) {
+    int64_t tokens = 0, pieces = 0;
+    for (long long i = 0; i < tiles; ++i) tokens += tile[i];
+    const int length = own_length(tokens, kv_heads);
+    for (long long i = 0; i < tiles; ++i) pieces += pieces_of_tile(tile[i], length);
+    const long long over = pieces - most_own_pieces(tiles, kv_heads);
+    if (over > worst) worst = over;
+    if (over > 0 || length < kOwnLeast || length % 32) {
+        printf("kv_heads %d, %lld tiles, %lld tokens, length %d: %lld pieces too many\n", kv_heads, tiles, (long long)tokens, length, over);
+        exit(1);
+    }
+}
+int main() {
+    static int tile[4096];
+    const int kv[] = {1, 2, 3, 4, 5, 7, 8, 16, 24, 32, 64, 1000, 2736, 2737, 65535};
+    srand(1);
+    for (int h : kv)
+        for (int tiles = 1; tiles <= 40; ++tiles)
+            for (int k = 3; k < 40; ++k)          // equal lengths whose total is next to 32 k for each of the pieces
+                for (int off = -2; off <= 40; ++off) {
+                    const int64_t each = 32LL * k * kOwnPieces / h / tiles + off;
+                    for (int i = 0; i < tiles; ++i) tile[i] = each < 0 ? 0 : (int)each;
+                    check(tile, tiles, h);
+                }
+    for (int n = 0; n < 20000; ++n) {             // totals there, cut anywhere, and row tiles that see nothing
+        const int h = kv[rand() % 15], tiles = 2 + rand() % 300;
+        const int64_t total = 32LL * (3 + rand() % 30) * kOwnPieces / h + rand() % 600;
+        int64_t left = total;
+        for (int i = 0; i < tiles; ++i) {
+            tile[i] = i == tiles - 1 ? (int)left : (int)(left * (rand() % 1000) / 1000 / (rand() % 8 + 1));
+            left -= tile[i];
+        }
+        check(tile, tiles, h);
+    }
+    for (int h : kv) {                            // the longest rows of tables
+        for (int i = 0; i < 4096; ++i) tile[i] = (1 << 30) - i % 3;
+        check(tile, 4096, h);
+    }
+    printf("%lld\n", worst);
+    return 0;
+}
+"""
+
+
+def test_pieces_of_own_parts_have_room(tmp_path):
+    """Behind shared prefixes: as many pieces as the workspace has room for, whatever the lengths."""
+    compiler = shutil.which("g++")
+    if not compiler:
+        pytest.skip("no host compiler")
+    (tmp_path / "pieces.cpp").write_text(PIECES)
+    csrc = os.path.join(os.path.dirname(q4k.__file__), "csrc")
+    subprocess.run([compiler, "-std=c++17", "-O2", "-I", csrc, str(tmp_path / "pieces.cpp"), "-o", str(tmp_path / "pieces")], check=True)
+    r = subprocess.run([str(tmp_path / "pieces")], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
+    assert int(r.stdout) >= -1   # (the cases come next to the bound)
