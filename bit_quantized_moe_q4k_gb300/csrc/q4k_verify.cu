@@ -76,6 +76,8 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// 2^(c d) for a difference d of logits; -inf (no probability, or further apart than numbers go) gives 0 at c = 0, too.
+__device__ __forceinline__ float power(float d, float c) { return d > -INFINITY ? ex2(d * c) : 0.0f; }
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(kStatThreads, 6) verify_stats_kernel(const __g
                 for (int k = 0; k < V; ++k) {
                     const float y = tame(v[k]);
                     if (pass == 0) m = fmaxf(m, y);
-                    else s += y > -INFINITY ? ex2((y - m) * c) : 0.0f;
+                    else s += y > -INFINITY ? power(y - m, c) : 0.0f;
                 }
             }
     }
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(kStatThreads, 6) verify_stats_kernel(const __g
         if (m != top) best = 0x7FFFFFFF;
         best = __reduce_min_sync(0xffffffffu, best);
     } else {
-        s = m > -INFINITY ? s * ex2((m - top) * c) : 0.0f;
+        s = m > -INFINITY ? s * power(m - top, c) : 0.0f;
 #pragma unroll
         for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     }
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(kStatThreads, 6) verify_stats_kernel(const __g
 #pragma unroll
     for (int w = 0; w < W; ++w) {
         if (s_m[w] == -INFINITY) continue;
-        if (!greedy) sum += s_s[w] * ex2((s_m[w] - all) * c);
+        if (!greedy) sum += s_s[w] * power(s_m[w] - all, c);
         else if (s_m[w] == all) at = min(at, s_i[w]);
     }
     A.stats[blockIdx.x] = make_float4(all, sum, __int_as_float(at), 0.0f);
@@ -348,7 +350,7 @@ struct Weigher {
         // log2(e) / T in two floats (fp64 has no rate worth the name here: one quotient a thread took 8 us a CTA)
         constexpr float l_hi = 1.442695040888963407f, l_lo = (float)(1.4426950408889634074 - (double)l_hi);
         c_hi = l_hi / temperature;
-        c_lo = (fmaf(-c_hi, temperature, l_hi) + l_lo) / temperature;
+        c_lo = temperature < INFINITY ? (fmaf(-c_hi, temperature, l_hi) + l_lo) / temperature : 0.0f;   // +inf: c is 0
     }
     __device__ __forceinline__ void exponent(float x, float* y, float* yl) const {
         const float d = x - top, b = d - x, dl = (x - (d - b)) + (-top - b);  // x - top in two floats
@@ -493,19 +495,18 @@ __global__ void __launch_bounds__(kPickThreads, 4) verify_pick_kernel(const __gr
         for (int k = lane; k < A.chunks; k += 32) {
             const float4 f = __ldcg(A.stats + (int64_t)r * A.chunks + k);
             if (f.x > R.top) {
-                R.sum = R.sum * ex2((R.top - f.x) * c);
-                if (R.top == -INFINITY) R.sum = 0.0f;
+                R.sum *= power(R.top - f.x, c);
                 R.top = f.x;
                 R.best = __float_as_int(f.z);
                 R.sum += f.y;
             } else if (f.x > -INFINITY) {
-                R.sum += f.y * ex2((f.x - R.top) * c);   // an equal one of a later chunk has the higher index
+                R.sum += f.y * power(f.x - R.top, c);   // an equal one of a later chunk has the higher index
             }
         }
         float top = R.top;
 #pragma unroll
         for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        R.sum = R.top > -INFINITY ? R.sum * ex2((R.top - top) * c) : 0.0f;
+        R.sum = R.top > -INFINITY ? R.sum * power(R.top - top, c) : 0.0f;
         if (R.top != top || top == -INFINITY) R.best = 0x7FFFFFFF;
         R.top = top;
 #pragma unroll

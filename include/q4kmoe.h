@@ -564,8 +564,9 @@ int q4k_page_tables(const int32_t* d_kept, const int32_t* d_new, const int32_t* 
  *   d_logits: [m, vocab] in dtype, rows logits_stride apart; d_draft_probs: q_r in fp32 [m, vocab], rows draft_stride apart (each
  *   sequence's last row is not read), NULL: drafts without probabilities, q_r(d) = 1 (rejected: from p_r without d). Any
  *   alignment of the rows; 16-byte aligned ones are read faster. d_temperature fp32 [batch], NULL: all 1. Temperatures not above 2^-64 (0, negative, NaN) choose
- *   the largest logit, the lowest index of equal ones (p_r is 1 there). d_seq_lens and d_kept may be NULL; d_kept may be d_seq_lens.
- *   A logit of -inf or NaN has no probability, +inf counts as the largest finite number. Random numbers are meant from [0, 1):
+ *   the largest logit, the lowest index of equal ones (p_r is 1 there); at +inf all tokens that have a probability are equally likely. d_seq_lens and d_kept may be NULL; d_kept may be d_seq_lens.
+ *   A logit of -inf or NaN has no probability, +inf counts as the largest finite number; one that is further below
+ *   the row's largest than the largest finite number has none either. Random numbers are meant from [0, 1):
  *   outside it u_sample counts as the nearer end, u_accept as it stands, below 0 (or NaN) as 0; negative or NaN probabilities count as 0.
  *   Decisions are those of exact arithmetic but where a random number comes next to a border: weights are good to 2^-41 of
  *   themselves in acceptances, 2^-31 in draws (and what is taken away for a draft), and in sums cut to 2^-(62 - ceil(log2(vocab))) of the row's largest weight.

@@ -372,3 +372,32 @@ def test_kept_in_place_of_the_lengths():
     q4k.q4k_verify_drafts(b.x.cuda(), b.m, b.v, b.v, dev(b.probs), b.v, i32(b.tokens), i32(b.start), b.b, dev(b.t), dev(b.ua), dev(b.us), lens,
                           acc, nxt, lens, ws, ws.numel(), flag)
     assert [host(o).tolist() for o in (acc, nxt, lens)] == list(want[:3]) and int(flag) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("probs", [True, False])
+def test_infinite_temperature(probs, dtype):
+    """Every token whose logit is above -inf is as likely as any other."""
+    b = Batch(64, [3] * 60, 2000, dtype, probs, "one")
+    b.x[::3, 100:900] = -math.inf
+    b.x[1::7, 300:305] = math.nan
+    b.x[2::5, 1000:1003] = math.inf
+    b.t = np.full(b.b, np.inf, np.float32)
+    got, flag = b.call()
+    flat = torch.where(b.x.float() > -math.inf, 0.0, -math.inf).numpy()   # NaN: no probability
+    acc, nxt, kept, flags = plain(flat, b.probs, b.tokens, b.start, None, b.ua, b.us, b.lens, drawn=got[1])
+    assert got == [acc, nxt, kept] and not flags and flag == 0
+
+
+def test_infinite_temperature_and_logits_far_apart():
+    """A logit further below the largest than the largest finite number has no probability, at any temperature."""
+    b = Batch(65, [1] * 32, 700, probs=False, temperature="one")
+    b.x[:] = -3e38
+    b.x[:, 200:203] = 3e38
+    b.x[::2, 5] = 1e38
+    b.t = np.full(b.b, np.inf, np.float32)
+    got, flag = b.call()
+    assert flag == 0
+    for i in range(b.b):
+        left = [5, 200, 201, 202] if i % 2 == 0 else [200, 201, 202]
+        assert got[1][i] == left[int(np.float64(b.us[i]) * len(left))]
