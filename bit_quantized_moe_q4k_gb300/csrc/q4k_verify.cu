@@ -250,30 +250,32 @@ __global__ void __launch_bounds__(kStatThreads, 6) verify_stats_kernel(const __g
         unpack<T, V>(__ldcg(xu + v0), v);
         few(v0 * V - shift, v);
     }
-    if (tid < 2) {
-        const int un = tid ? u1 - 1 : u0;   // an end of the chunk that is no whole unit
-        if (un >= u0 && un < u1 && (un < w0 || un >= w1) && (tid == 0 || u1 - 1 != u0)) {
-            float v[V];
-            at_end(un, v);
-            few(un * V - shift, v);
-        }
+    const int end = tid ? u1 - 1 : u0;   // threads 0 and 1: an end of the chunk that is no whole unit
+    const bool has_end = tid < 2 && end >= u0 && end < u1 && (end < w0 || end >= w1) && (tid == 0 || u1 - 1 != u0);
+    if (has_end) {
+        float v[V];
+        at_end(end, v);
+        few(end * V - shift, v);
     }
-    if (!greedy && !(s < INFINITY && m < INFINITY)) {  // NaN, +inf or a c of 0 among them: once more, with every logit tamed
+    if (!greedy && !(s < INFINITY && m < INFINITY)) {  // NaN, +inf or a c of 0 among them: this thread's units once more, with every logit tamed
         m = -INFINITY;
         s = 0.0f;
-#pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass)
-#pragma unroll 1
-            for (int un = u0 + tid; un < u1; un += kStatThreads) {
-                float v[V];
-                at_end(un, v);
+        auto again = [&](int un, bool sums) {
+            float v[V];
+            at_end(un, v);
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const float y = tame(v[k]);
-                    if (pass == 0) m = fmaxf(m, y);
-                    else s += y > -INFINITY ? power(y - m, c) : 0.0f;
-                }
+            for (int k = 0; k < V; ++k) {
+                const float y = tame(v[k]);
+                if (!sums) m = fmaxf(m, y);
+                else s += y > -INFINITY ? power(y - m, c) : 0.0f;
             }
+        };
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+            for (int un = w0 + tid; un < w1; un += kStatThreads) again(un, pass);
+            if (has_end) again(end, pass);
+        }
     }
     // The next kernel's large CTAs are let in only now: they would take the place of this one's.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -401,3 +401,17 @@ def test_infinite_temperature_and_logits_far_apart():
     for i in range(b.b):
         left = [5, 200, 201, 202] if i % 2 == 0 else [200, 201, 202]
         assert got[1][i] == left[int(np.float64(b.us[i]) * len(left))]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("value", [math.inf, math.nan])
+@pytest.mark.parametrize("vocab,pad,shift", [(3001, 0, 0), (3001, 5, 3), (3000, 7, 1), (2999, 3, 2), (50001, 2, 1)])
+def test_one_infinite_or_nan_logit_anywhere(vocab, pad, shift, value, dtype):
+    """Rows that begin off a 16-byte boundary and end off one; next to the row's largest logit, at its ends and between."""
+    b = Batch(66 + vocab, [2] * 48, vocab, dtype, probs=False, temperature="warm", pad=pad, shift=shift)
+    g = np.random.default_rng(vocab + pad)
+    for r in range(b.m):
+        top = int(b.x[r].float().argmax())
+        at = [0, vocab - 1, max(top - 1, 0), min(top + 1, vocab - 1), 1, vocab - 2, int(g.integers(vocab)), int(g.integers(vocab))][r // 2 % 8]
+        b.x[r, at] = value
+    b.check()
