@@ -41,7 +41,7 @@ struct VerifyParams {
     const int32_t *tokens, *q_start, *seq_lens;
     const float *temperature, *u_accept, *u_sample;
     int32_t *accepted, *next, *kept;
-    float4* stats;   // [m][chunks]: largest, sum, its index (bits)
+    float4* stats;   // [m][chunks]: largest, sum, its index (bits), the sequence whose temperature it was (bits; -1: none holds the row)
     int batch, m, vocab, chunks;
     int bits;        // weights are integers in units of 2^-bits: the row's add up to 2^62 at most
     int* err_flag;
@@ -161,7 +161,10 @@ __global__ void __launch_bounds__(kStatThreads, 6) verify_stats_kernel(const __g
         }
     }
     __syncthreads();
-    if (s_seq < 0) return;
+    if (s_seq < 0) {
+        if (tid == 0) A.stats[blockIdx.x] = make_float4(-INFINITY, 0.0f, __int_as_float(0x7FFFFFFF), __int_as_float(-1));
+        return;
+    }
     const bool greedy = !(s_t > kGreedy);
     const float c = 1.44269504088896340736f / s_t;
     float m = -INFINITY, s = 0.0f;
@@ -308,7 +311,7 @@ __global__ void __launch_bounds__(kStatThreads, 6) verify_stats_kernel(const __g
         if (!greedy) sum += s_s[w] * power(s_m[w] - all, c);
         else if (s_m[w] == all) at = min(at, s_i[w]);
     }
-    A.stats[blockIdx.x] = make_float4(all, sum, __int_as_float(at), 0.0f);
+    A.stats[blockIdx.x] = make_float4(all, sum, __int_as_float(at), __int_as_float(s_seq));
 }
 
 // ---- weights of more than 24 bits ---------------------------------------------------------------------------------
@@ -495,7 +498,8 @@ __global__ void __launch_bounds__(kPickThreads, 4) verify_pick_kernel(const __gr
     auto row_of = [&](int r) {
         Row R{-INFINITY, 0.0f, 0x7FFFFFFF};
         for (int k = lane; k < A.chunks; k += 32) {
-            const float4 f = __ldcg(A.stats + (int64_t)r * A.chunks + k);
+            float4 f = __ldcg(A.stats + (int64_t)r * A.chunks + k);
+            if (__float_as_int(f.w) != seq) f.x = -INFINITY;   // (where starts fall, a row that two sequences have is one's)
             if (f.x > R.top) {
                 R.sum *= power(R.top - f.x, c);
                 R.top = f.x;
@@ -540,7 +544,7 @@ __global__ void __launch_bounds__(kPickThreads, 4) verify_pick_kernel(const __gr
             s_best[warp] = R.best;
         }
         if (!there && rank == 0 && lane == 0) raise_flag(A.err_flag, Q4K_ERR_TOKEN);
-        if (x == -INFINITY) return (int)kNo;
+        if (x == -INFINITY || R.top == -INFINITY) return (int)kNo;
         if (u == 0.0f || q == 0.0f) return (int)(!greedy || d == R.best ? kYes : kNo);
         const float need = u * q;
         if (greedy) return (int)(d == R.best && need < 1.0f ? kYes : kNo);

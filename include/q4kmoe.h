@@ -571,7 +571,7 @@ int q4k_page_tables(const int32_t* d_kept, const int32_t* d_new, const int32_t* 
  *   Decisions are those of exact arithmetic but where a random number comes next to a border: weights are good to 2^-41 of
  *   themselves in acceptances, 2^-31 in draws (and what is taken away for a draft), and in sums cut to 2^-(62 - ceil(log2(vocab))) of the row's largest weight.
  * Device flags: a draft outside [0, vocab) is rejected, a row of logits without any probability gives next -1 (Q4K_ERR_TOKEN);
- * q_start falling or outside [0, m] is clamped (Q4K_ERR_SEQ).
+ * q_start falling or outside [0, m] is clamped (Q4K_ERR_SEQ); a row that two sequences have then has no probability for one of them.
  * Limits (Q4K_ERR_LIMIT): vocab <= 2^20, m and batch <= 2^24. Two launches.
  * Workspace: q4k_verify_drafts_workspace_size bytes, any contents. */
 size_t q4k_verify_drafts_workspace_size(int batch, int m, int vocab);

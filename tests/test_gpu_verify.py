@@ -415,3 +415,16 @@ def test_one_infinite_or_nan_logit_anywhere(vocab, pad, shift, value, dtype):
         at = [0, vocab - 1, max(top - 1, 0), min(top + 1, vocab - 1), 1, vocab - 2, int(g.integers(vocab)), int(g.integers(vocab))][r // 2 % 8]
         b.x[r, at] = value
     b.check()
+
+
+@pytest.mark.parametrize("temperature", ["greedy", "warm"])
+@pytest.mark.parametrize("start", [[0, 5, 2], [0, 5, 2, 6], [-3, 2, 4, 6], [0, 2, 4, 60], [6, 4, 2, 0], [9, 9, 9, 9], [0, 6, 3, 6], [2, 4, 4, 5]])
+def test_malformed_starts_on_any_workspace(start, temperature):
+    """Results are of the inputs alone, and are tokens or -1."""
+    b = Batch(12, [2, 2, 2], 500, temperature=temperature)
+    b.start, b.b = start, len(start) - 1
+    got = [b.call(fill=fill) for fill in (0x00, 0x5A, 0x7F, 0xFF)]
+    assert all(x == got[0] for x in got)
+    (acc, nxt, kept), flag = got[0]
+    assert flag == (0 if start == [2, 4, 4, 5] else SEQ_FLAG) or flag == TOKEN_FLAG
+    assert all(0 <= a < 6 for a in acc) and all(-1 <= x < 500 for x in nxt)
