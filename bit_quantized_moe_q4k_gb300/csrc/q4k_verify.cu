@@ -31,8 +31,11 @@ constexpr float kLargest = 3.402823466e38f;
 // (4 ln 2 2^-24 |y|), the same in the sum, where the mean of |y| is the distribution's entropy at most (20 bits), ex2 (2 2^-23), up to
 // thirteen changes of a thread's largest (26 2^-23), and some sixty additions one after another (30 2^-23).
 __device__ __forceinline__ float closeness(float y) { return fmaf(fabsf(y), 1.5f, 96.0f) * 1.1920929e-7f; }
-// And where it is computed from the draw's weights, 2^-31 each and cut at 2^-45 of 2^17 tokens.
+// And where it is computed from the draw's weights: 2^-31 of themselves (the sum and the draft's, 32 times that here), and each cut to the
+// sums' unit, so that a sum of n may be n units short.
 constexpr double kCloseFine = 1.0 / 67108864.0;
+// The precise sum has this many more bits behind the unit: all its weights together are short by one unit at most.
+constexpr int kFineBits = 20;
 
 struct VerifyParams {
     const void* logits;
@@ -405,12 +408,18 @@ struct Weigher {
         *e = n >> 8;
         return true;
     }
-    __device__ __forceinline__ uint64_t precise_weight(float x) const {  // in units of 2^-bits, rounded
+    // Adds it to sums of whole units of 2^-bits and of 2^-kFineBits of them, cut off there.
+    __device__ __forceinline__ void add_precise(float x, uint64_t* units, uint64_t* parts) const {
         uint64_t mant;
         int e;
-        if (!precise(x, &mant, &e)) return 0;
-        const int up = e + 20 - down;
-        return up >= 0 ? mant << up : up < -45 ? 0 : ((mant >> (-up - 1)) + 1) >> 1;
+        if (!precise(x, &mant, &e)) return;
+        const int by = down - 20 - e;   // mant 2^(e - 43) is mant 2^-by units; by is -19 at least
+        if (by <= 0) {
+            *units += mant << -by;
+        } else {
+            *units += shr(mant, by);
+            *parts += (by < 64 ? mant << (64 - by) : shr(mant, by - 64)) >> (64 - kFineBits);
+        }
     }
 };
 // f * s for a sum s < 2^63, of which it keeps 32 bits (2^-31 of itself), and f in [0, 1], cut off.
@@ -712,12 +721,14 @@ __global__ void __launch_bounds__(kPickThreads, 4) verify_pick_kernel(const __gr
         W.parts(logit(r, d), &m32, &e);
         const double need = (double)chance(r) * (double)drafts(r, d), l = need * (double)whole, w = scalbn((double)m32, e + A.bits - 31);
         bool passes = l < w;
-        if (!(fabs(l - w) > kCloseFine * w) || e < -190) {  // closer still (or a draft below 2^-190): all to 2^-41
-            uint64_t sum = 0, mant;
+        if (!(fabs(l - w) > kCloseFine * w + need * (double)A.vocab) || e < -190) {  // closer still (or a draft below 2^-190): all to 2^-41
+            uint64_t units = 0, parts = 0, mant;
 #pragma unroll 1
-            for (int i = seg0 * kSeg + tid; i < min(seg1 * kSeg, A.vocab); i += kPickThreads) sum += W.precise_weight(tame(one(x + i)));
-            const uint64_t fine = warp_sum(gather(block_sum(sum), 0, 0).a);
-            passes = W.precise(logit(r, d), &mant, &e) && need * (double)fine < scalbn((double)mant, e + A.bits - 43);
+            for (int i = seg0 * kSeg + tid; i < min(seg1 * kSeg, A.vocab); i += kPickThreads) W.add_precise(tame(one(x + i)), &units, &parts);
+            const uint64_t a1 = block_sum(units), b1 = block_sum(parts);
+            const Values all = gather(a1, b1, 0);
+            const double fine = (double)warp_sum(all.a) + (double)warp_sum(all.b) * (1.0 / (1 << kFineBits));
+            passes = W.precise(logit(r, d), &mant, &e) && need * fine < scalbn((double)mant, e + A.bits - 43);
         }
         if (!passes) break;
         ++at;

@@ -428,3 +428,22 @@ def test_malformed_starts_on_any_workspace(start, temperature):
     (acc, nxt, kept), flag = got[0]
     assert flag == (0 if start == [2, 4, 4, 5] else SEQ_FLAG) or flag == TOKEN_FLAG
     assert all(0 <= a < 6 for a in acc) and all(-1 <= x < 500 for x in nxt)
+
+
+@pytest.mark.parametrize("vocab", [1 << 20, (1 << 19) + 1])
+def test_acceptance_next_to_the_border_behind_many_small_weights(vocab):
+    """One large weight, and as many as there are tokens a little above the unit of the sums."""
+    b = Batch(67, [2] * 8, vocab, probs=False, temperature="one")
+    want = []
+    for i in range(b.b):
+        r, d = b.start[i], 1000 * i + 3
+        b.x[r] = float(np.log((1.1, 1.5, 1.9, 2.6)[i // 2]) - 42 * np.log(2.0))
+        b.x[r, d] = 0.0
+        p = target(b.x[r].numpy(), 1.0)[d]
+        u = np.float32(p)
+        if (i % 2 == 0) == bool(np.longdouble(u) < p):   # even: on or above it
+            u = np.nextafter(u, np.float32(2.0 if i % 2 == 0 else -1.0))
+        b.tokens[r + 1], b.ua[r] = d, u
+        want.append(int(np.longdouble(u) < p))
+    acc, _ = b.check(strict=False)
+    assert acc == want and sum(want) == 4
