@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kPickThreads, 4) verify_pick_kernel(const __gr
         drafted = rejected && !A.probs ? __ldcg(A.tokens + r + 1) : -1;  // only it has nothing left
         // One pass with the sum S that fp32 gave: what is left is max(w - q S, 0), and where S is off by s, the sum of that over a
         // segment is off by s times the q of the tokens that are left something (which those are, S decides well enough: a token that
-        // changes sides has next to nothing left). So each segment keeps both sums, and the precise S comes in afterwards.
+        // changes sides has at most s q left). So each segment keeps both sums, and the precise S comes in afterwards.
         about = __float2ull_rn(R.sum * __int_as_float((127 + A.bits) << 23));
         const Portion away_of(about);
         uint64_t cta_whole = 0, cta_left = 0, cta_share = 0;   // shares in units of 2^-40
@@ -747,21 +747,37 @@ __global__ void __launch_bounds__(kPickThreads, 4) verify_pick_kernel(const __gr
     };
     left_of = corrected(left_of, (float)share_of * 9.094947e-13f);
     bool minus = rejected;
-    if (!__any_sync(0xffffffffu, left_of != 0)) {
-        // nothing is left: from the distribution itself
-        minus = false;
+    auto left_at = [&](int e) {   // what is left of a token
+        uint64_t w = e < A.vocab ? W(tame(one(x + e))) : 0;
+        if (minus && q) {
+            const uint64_t away = e < A.vocab ? portion(__ldcg(q + e), whole) : 0;
+            w = w > away ? w - away : 0;
+        } else if (minus && e == drafted) {
+            w = 0;
+        }
+        return w;
+    };
+    auto recount = [&]() {   // the segments' sums with the precise S
         uint64_t cta_left = 0;
         for (int sg = seg0 + warp; sg < seg1; sg += kPickWarps) {
             uint64_t t = 0;
 #pragma unroll 1
-            for (int e = sg * kSeg + lane; e < min((sg + 1) * kSeg, A.vocab); e += 32) t += W(tame(one(x + e)));
+            for (int e = sg * kSeg + lane; e < (sg + 1) * kSeg; e += 32) t += left_at(e);
             t = warp_sum(t);
             if (lane == 0) {
                 s_sum[sg - seg0] = t;
+                s_share[sg - seg0] = 0.0f;
                 cta_left += t;
             }
         }
-        left_of = gather(block_sum(cta_left), 0, 0).a;
+        return gather(block_sum(cta_left), 0, 0).a;
+    };
+    // Where target and draft nearly agree, the tokens that change sides are many and what is left is as little as they have: counted once
+    // more. (A draft is rejected with the probability of what is left, so this is rare where the random numbers are fair: one row of 1024 at most.)
+    if (q && warp_sum(left_of) < whole >> 10) left_of = recount();
+    if (!__any_sync(0xffffffffu, left_of != 0)) {
+        minus = false;   // nothing is left: from the distribution itself
+        left_of = recount();
     }
     const uint64_t rest = warp_sum(left_of), cta_before = warp_sum(lane < (int)rank ? left_of : 0);
     const uint64_t cta_rest = __shfl_sync(0xffffffffu, left_of, (int)rank);
@@ -770,7 +786,7 @@ __global__ void __launch_bounds__(kPickThreads, 4) verify_pick_kernel(const __gr
     if (goal >= cta_before && goal - cta_before < cta_rest) {
         // every warp finds the segment, then takes a part of it: its tokens' sums, then the place in the part that holds the goal
         uint64_t before = cta_before;
-        int sg = -1, last_sg = 0;   // last_sg: the last with something left, should rounding leave the goal behind all of them
+        int sg = -1, last_sg = 0;   // last_sg: the last with something left, should rounding put the goal behind all of them
         for (int base = 0; base < seg1 - seg0 && sg < 0; base += 32) {
             const uint64_t v = base + lane >= seg1 - seg0 ? 0
                                : minus && q              ? corrected(s_sum[base + lane], s_share[base + lane])
@@ -799,13 +815,7 @@ __global__ void __launch_bounds__(kPickThreads, 4) verify_pick_kernel(const __gr
         int mine = -1;
 #pragma unroll
         for (int k = 0; k < kMine; ++k) {
-            w[k] = e + k < A.vocab ? W(tame(one(x + e + k))) : 0;
-            if (minus && q) {
-                const uint64_t away = e + k < A.vocab ? portion(__ldcg(q + e + k), whole) : 0;
-                w[k] = w[k] > away ? w[k] - away : 0;
-            } else if (minus && e + k == drafted) {
-                w[k] = 0;
-            }
+            w[k] = left_at(e + k);
             if (w[k]) mine = e + k;
             own += w[k];
         }
@@ -834,11 +844,22 @@ __global__ void __launch_bounds__(kPickThreads, 4) verify_pick_kernel(const __gr
                 }
                 A.next[seq] = found;
             }
-        } else if (warp == kPickWarps - 1 && lane == 0 && (past || end <= goal)) {
-            int last = -1;
+        } else if (warp == kPickWarps - 1 && (past || end <= goal)) {
+            int found = -1;
 #pragma unroll
-            for (int k = 0; k < kPickWarps; ++k) last = max(last, s_best[k]);
-            A.next[seq] = last >= 0 ? last : R.best;
+            for (int k = 0; k < kPickWarps; ++k) found = max(found, s_best[k]);
+            // a segment whose sum was rounding alone: the next token that is left something, or the last one
+#pragma unroll 1
+            for (int e0 = (sg + 1) * kSeg; found < 0 && e0 < A.vocab; e0 += 32) {
+                const unsigned some = __ballot_sync(0xffffffffu, left_at(e0 + lane) != 0);
+                if (some) found = e0 + __ffs(some) - 1;
+            }
+#pragma unroll 1
+            for (int e0 = sg * kSeg - 32; found < 0 && e0 >= 0; e0 -= 32) {
+                const unsigned some = __ballot_sync(0xffffffffu, left_at(e0 + lane) != 0);
+                if (some) found = e0 + 31 - __clz(some);
+            }
+            if (lane == 0) A.next[seq] = found;
         }
     }
     sync_cluster();

@@ -570,7 +570,8 @@ int q4k_page_tables(const int32_t* d_kept, const int32_t* d_new, const int32_t* 
  *   outside it u_sample counts as the nearer end, u_accept as it stands, below 0 (or NaN) as 0; negative or NaN probabilities count as 0.
  *   Decisions are those of exact arithmetic but where a random number comes next to a border: weights are good to 2^-41 of
  *   themselves in acceptances, 2^-31 in draws (and what is taken away for a draft), and in sums cut to a unit of 2^-(62 - ceil(log2(vocab))) of the
- *   row's largest weight (in acceptances to 2^-20 of it).
+ *   row's largest weight (in acceptances to 2^-20 of it). Where a draft leaves more than 1/1024 of the distribution, tokens whose p_r and q_r agree to
+ *   some 2^-22 of themselves may count in the choice between groups of 512 tokens as if that were left of them, or nothing.
  * Device flags: a draft outside [0, vocab) is rejected, a row of logits without any probability gives next -1 (Q4K_ERR_TOKEN);
  * q_start falling or outside [0, m] is clamped (Q4K_ERR_SEQ); a row that two sequences have then has no probability for one of them.
  * Limits (Q4K_ERR_LIMIT): vocab <= 2^20, m and batch <= 2^24. Two launches.

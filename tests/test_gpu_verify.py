@@ -447,3 +447,27 @@ def test_acceptance_next_to_the_border_behind_many_small_weights(vocab):
         want.append(int(np.longdouble(u) < p))
     acc, _ = b.check(strict=False)
     assert acc == want and sum(want) == 4
+
+
+@pytest.mark.parametrize("probs_off", [0.0, 1e-7, 1e-6, 1e-5, 1e-3])
+@pytest.mark.parametrize("vocab", [3000, 50001])
+def test_draws_where_draft_and_target_nearly_agree(vocab, probs_off):
+    """A rejected draft whose probabilities are the target's but for some 2^-24 of them, so that what is left is as small: drawn in exact
+    arithmetic all the same, but for the weights' errors: 4 E of the whole sum in a cumulative one (as above); what is left of a token by
+    2^-31 of its weight and, q times the sum, by E of it."""
+    b = Batch(68 + vocab, [2] * 64, vocab, temperature="one", spread=1.0)
+    g = np.random.default_rng(vocab)
+    p = [target(x, 1.0) for x in b.x.numpy()]
+    b.probs[:] = [(q * (1 + probs_off * g.standard_normal(vocab))).astype(np.float32) for q in p]
+    b.ua[:] = 2.0   # every draft is rejected
+    got, flag = b.call()
+    assert flag == 0 and got[0] == [0] * b.b
+    e = 2.0 ** -31 + vocab * 2.0 ** -(62 - math.ceil(math.log2(vocab)))
+    for i in range(b.b):
+        r, j = b.start[i], got[1][i]
+        left = p[r] - b.probs[r].astype(np.longdouble)
+        rest = np.maximum(left, 0)
+        cum = np.cumsum(rest)
+        goal = np.longdouble(b.us[i]) * cum[-1]
+        assert 0 <= j < vocab and left[j] > -(2.0 ** -31 + e) * p[r][j]
+        assert cum[j] - rest[j] - 4 * e <= goal <= cum[j] + 4 * e
