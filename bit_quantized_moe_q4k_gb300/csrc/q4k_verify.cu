@@ -747,16 +747,13 @@ __global__ void __launch_bounds__(kPickThreads, 4) verify_pick_kernel(const __gr
     };
     left_of = corrected(left_of, (float)share_of * 9.094947e-13f);
     bool minus = rejected;
-    auto left_at = [&](int e) {   // what is left of a token
-        uint64_t w = e < A.vocab ? W(tame(one(x + e))) : 0;
-        if (minus && q) {
-            const uint64_t away = e < A.vocab ? portion(__ldcg(q + e), whole) : 0;
-            w = w > away ? w - away : 0;
-        } else if (minus && e == drafted) {
-            w = 0;
-        }
-        return w;
+    auto left_with = [&](int e, float logit_e, float prob_e) {   // what is left of token e, past the last one's -inf and 0
+        const uint64_t w = W(tame(logit_e)), away = portion(prob_e, whole);   // (a portion of 0 is 0)
+        return minus && e == drafted ? 0 : w > away ? w - away : 0;
     };
+    auto logit_at = [&](int e) { return e < A.vocab ? one(x + e) : -INFINITY; };
+    auto prob_at = [&](int e) { return minus && q && e < A.vocab ? __ldcg(q + e) : 0.0f; };
+    auto left_at = [&](int e) { return left_with(e, logit_at(e), prob_at(e)); };
     auto recount = [&]() {   // the segments' sums with the precise S
         uint64_t cta_left = 0;
         for (int sg = seg0 + warp; sg < seg1; sg += kPickWarps) {
@@ -773,13 +770,20 @@ __global__ void __launch_bounds__(kPickThreads, 4) verify_pick_kernel(const __gr
         return gather(block_sum(cta_left), 0, 0).a;
     };
     // Where target and draft nearly agree, the tokens that change sides are many and what is left is as little as they have: counted once
-    // more. (A draft is rejected with the probability of what is left, so this is rare where the random numbers are fair: one row of 1024 at most.)
-    if (q && warp_sum(left_of) < whole >> 10) left_of = recount();
-    if (!__any_sync(0xffffffffu, left_of != 0)) {
-        minus = false;   // nothing is left: from the distribution itself
-        left_of = recount();
+    // more. (A draft is rejected with the probability of what is left, so this is rare where the random numbers are fair: one row of 1024 at
+    // most.) Where nothing is left, the token is drawn from the distribution itself.
+    uint64_t rest = warp_sum(left_of);
+    if (rest < (q ? whole >> 10 : 1)) {
+        bool again = q != nullptr;
+        for (;;) {
+            if (!again) minus = false;
+            left_of = recount();
+            rest = warp_sum(left_of);
+            if (rest != 0 || !again) break;
+            again = false;
+        }
     }
-    const uint64_t rest = warp_sum(left_of), cta_before = warp_sum(lane < (int)rank ? left_of : 0);
+    const uint64_t cta_before = warp_sum(lane < (int)rank ? left_of : 0);
     const uint64_t cta_rest = __shfl_sync(0xffffffffu, left_of, (int)rank);
     // the first token whose cumulative sum exceeds u * rest: the CTA's segment that holds it, then its place there
     const uint64_t goal = min(portion(u_sample, rest), rest - 1);
@@ -812,10 +816,16 @@ __global__ void __launch_bounds__(kPickThreads, 4) verify_pick_kernel(const __gr
         constexpr int kMine = kSeg / kPickThreads;   // tokens of a lane, one after another
         const int e = sg * kSeg + (warp * 32 + lane) * kMine;
         uint64_t w[kMine], own = 0;
+        float v[kMine], p[kMine];
         int mine = -1;
 #pragma unroll
         for (int k = 0; k < kMine; ++k) {
-            w[k] = left_at(e + k);
+            v[k] = logit_at(e + k);
+            p[k] = prob_at(e + k);
+        }
+#pragma unroll
+        for (int k = 0; k < kMine; ++k) {
+            w[k] = left_with(e + k, v[k], p[k]);
             if (w[k]) mine = e + k;
             own += w[k];
         }
