@@ -120,10 +120,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
         __syncwarp();
         PrefixGroup G{};
         if (!none) {
-            int least = 0x7FFFFFFF, most = -1, live = 0, rows = 0, tiles = 0;
+            int least = 0x7FFFFFFF, most = -1, live = 0, rows = 0, tiles = 0, lead = 0x7FFFFFFF;
             for (int i = a + lane; i < b; i += 32) {
                 const SeqSpan s = span(i);
-                if (s.n == 0) continue;
+                if (s.n == 0) continue;   // nothing of such a sequence is believed: it may have ended
+                lead = min(lead, i);
                 least = min(least, s.len - s.n);
                 most = max(most, s.len - 1);
                 rows = max(rows, s.n);
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
             rows = __reduce_max_sync(0xffffffffu, rows);
             live = __reduce_add_sync(0xffffffffu, live);
             tiles = __reduce_add_sync(0xffffffffu, tiles);
-            G.leader = a;
+            G.leader = __reduce_min_sync(0xffffffffu, lead);
             if (live > 1 && (int64_t)rows * A.rep <= A.max_rows) {
                 G.row0 = span(a).start;
                 G.n = span(b - 1).start + span(b - 1).n - G.row0;

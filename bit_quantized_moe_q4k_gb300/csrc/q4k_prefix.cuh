@@ -16,7 +16,7 @@ struct PrefixGroup {
     int row0, n;        // its new tokens: rows row0 .. row0 + n - 1 of the inputs
     int lo, from;       // the shared tokens that some row sees: lo (a multiple of 16) .. from - 1
     int full_lo;        // from here on every row sees them
-    int leader;         // the sequence whose row of the page table is read
+    int leader;         // the sequence whose row of the page table is read: the first with new tokens
     int tiles, rows;    // units of 128 tokens, row tiles (0: nothing is shared)
     int64_t unit0;      // its units' place on the line of all units
     int64_t item0;      // its first item

@@ -495,7 +495,7 @@ int q4k_paged_attention(const void* d_q, int dtype, int m, int q_heads, int kv_h
  *   d_group_start [groups + 1], d_prefix_lens [groups] (device memory, int32): sequences group_start[g] ..
  *   group_start[g+1] - 1 have their first prefix_lens[g] tokens in common, and those of their pages that lie wholly in the prefix: the
  *   first prefix_lens[g] / page_size entries of their rows of the page table are the same (which of the rows is read is not
- *   specified). Rising, within [0, batch]; sequences before the first group or after the last share nothing.
+ *   specified; a sequence without new tokens may be of any length and its row may hold anything). Rising, within [0, batch]; sequences before the first group or after the last share nothing.
  *   What is shared is the whole pages of the prefix that lie before every new token of the group's sequences; the sequences read all else,
  *   and what small groups hold in common, as in q4k_paged_attention.
  *   max_prefix: an upper bound of prefix_lens that chooses the kernels: calls that would save too little (by batch, groups, m, heads,

@@ -439,3 +439,12 @@ def test_one_workspace_for_calls_in_turn():
 def test_own_parts_of_more_tokens_than_whole_pieces(hq, hk, own, dtype):
     """Own tokens that are a little more than 32 k for each of the pieces that a call is cut into."""
     Shared(60, [(128, [(1, n - 1) for n in own])], hk, 64, 64).run(hq, dtype, times=1)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_sequences_without_new_tokens_do_not_lead_their_group(dtype):
+    """Ended ones at a group's start, whose rows of the page table hold anything."""
+    s = Shared(61, [(320, [(0, -320), (0, 5), (1, 7), (2, 0)]), (300, [(0, -300), (1, 1), (1, 4)]), (96, [(0, 0), (0, 0)])], 2, 64, 16)
+    assert s.lens[0] == 0 and s.lens[4] == 0
+    s.table[[0, 4]], s.table[1] = 0x7FFFFFF0, -1
+    s.run(8, dtype)
