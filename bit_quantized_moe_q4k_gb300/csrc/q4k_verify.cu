@@ -875,10 +875,13 @@ __global__ void __launch_bounds__(kPickThreads, 4) verify_pick_kernel(const __gr
     sync_cluster();
 }
 
+// Pieces of a row: five CTAs on each of 152 SMs, one wave, where there are few rows (but 4096 logits a CTA at least), pieces of up to 16384
+// where there are many. 150 rows of 50001 logits, whole call: 20.8 us, with eight 25.7, with four 21.9.
+constexpr int kWave = 5 * 152;
+int most_chunks(int vocab) { return (vocab + 4095) / 4096; }
+int least_chunks(int vocab) { return (vocab + 16383) / 16384; }
 int chunks_of(int m, int vocab) {
-    // Five CTAs on each of 152 SMs, one wave, where there are few rows (but 4096 logits a CTA at least), pieces of up to 16384 where there
-    // are many. 150 rows of 50001 logits, whole call: 20.8 us, with eight 25.7, with four 21.9.
-    const int64_t want = (5 * 152 + (int64_t)m - 1) / (m < 1 ? 1 : m), most = (vocab + 4095) / 4096, least = (vocab + 16383) / 16384;
+    const int64_t want = (kWave + (int64_t)m - 1) / (m < 1 ? 1 : m), most = most_chunks(vocab), least = least_chunks(vocab);
     return (int)(want > most ? most : want < least ? least : want);
 }
 
@@ -918,7 +921,12 @@ cudaError_t launch_typed(const VerifyParams& P, cudaStream_t stream) {
 
 }  // namespace
 
-size_t verify_workspace_bytes(int m, int vocab) { return sizeof(float4) * (size_t)m * chunks_of(m, vocab); }
+// m * chunks_of(m, vocab) at most, and of no fewer rows more: m ceil(kWave / m) is below kWave + m.
+size_t verify_workspace_bytes(int m, int vocab) {
+    const int64_t most = (int64_t)m * most_chunks(vocab), least = (int64_t)m * least_chunks(vocab), wave = kWave + (int64_t)m;
+    const int64_t some = least > wave ? least : wave;
+    return sizeof(float4) * (size_t)(most < some ? most : some);
+}
 
 cudaError_t launch_verify(const void* logits, int dtype, int m, int vocab, int64_t logits_stride, const float* probs,
                           int64_t probs_stride, const int32_t* tokens, const int32_t* q_start, int batch,

@@ -575,7 +575,7 @@ int q4k_page_tables(const int32_t* d_kept, const int32_t* d_new, const int32_t* 
  * Device flags: a draft outside [0, vocab) is rejected, a row of logits without any probability gives next -1 (Q4K_ERR_TOKEN);
  * q_start falling or outside [0, m] is clamped (Q4K_ERR_SEQ); a row that two sequences have then has no probability for one of them.
  * Limits (Q4K_ERR_LIMIT): vocab <= 2^20, m and batch <= 2^24. Two launches.
- * Workspace: q4k_verify_drafts_workspace_size bytes, any contents. */
+ * Workspace: q4k_verify_drafts_workspace_size bytes, any contents; the size rises with m and vocab, so the largest call's serves all. */
 size_t q4k_verify_drafts_workspace_size(int batch, int m, int vocab);
 int q4k_verify_drafts(const void* d_logits, int dtype, int m, int vocab, int64_t logits_stride, const float* d_draft_probs,
                       int64_t draft_stride, const int32_t* d_tokens, const int32_t* d_q_start, int batch,

@@ -471,3 +471,15 @@ def test_draws_where_draft_and_target_nearly_agree(vocab, probs_off):
         goal = np.longdouble(b.us[i]) * cum[-1]
         assert 0 <= j < vocab and left[j] > -(2.0 ** -31 + e) * p[r][j]
         assert cum[j] - rest[j] - 4 * e <= goal <= cum[j] + 4 * e
+
+
+def test_one_workspace_for_calls_of_all_sizes():
+    """Sized for the most rows, with bytes behind it that no call touches."""
+    made = [Batch(70 + n, [3] * n, 32000, temperature="warm") for n in (1, 5, 36, 127)]
+    need = max(q4k.q4k_verify_drafts_workspace_size(b.b, b.m, b.v) for b in made)
+    assert need == q4k.q4k_verify_drafts_workspace_size(made[-1].b, made[-1].m, made[-1].v)
+    for b in made:
+        ws = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        got, flag = b.call(workspace=ws[:need])
+        assert got == list(plain(b.x.numpy(), b.probs, b.tokens, b.start, b.t, b.ua, b.us, b.lens, drawn=got[1])[:3]) and flag == 0
+        assert (ws[need:] == 0xA5).all()

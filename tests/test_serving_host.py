@@ -93,6 +93,17 @@ def test_verify_empty_and_workspace():
         assert lib.q4k_verify_drafts_workspace_size(*bad) == 0
 
 
+def test_verify_workspace_of_the_largest_call_serves_all():
+    size = q4k.load().q4k_verify_drafts_workspace_size
+    for vocab in (1, 4096, 4097, 32000, 50001, 131072, 151936, 1 << 20):
+        sizes = [size(1, m, vocab) for m in range(4000)] + [size(1, m, vocab) for m in (1 << 13, 1 << 20, 1 << 24)]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:])) and sizes[-1] > 0
+    for m in (1, 3, 108, 109, 380, 1000):
+        sizes = [size(1, m, v) for v in range(1, 1 << 18, 997)]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+    assert len({size(b, 300, 50001) for b in (0, 1, 7, 300, 1 << 24)}) == 1
+
+
 def test_verify_binding_refuses_other_element_types():
     i32, i64, f32, f16, u8 = (FakeCuda(t) for t in (torch.int32, torch.int64, torch.float32, torch.float16, torch.uint8))
     good = [f32, 7, 100, 100, f32, 100, i32, i32, 3, f32, f32, f32, i32, i32, i32, i32, u8, 1 << 20, i32]
