@@ -393,7 +393,8 @@ def q4k_shared_prefix_attention(q, m, q_heads, kv_heads, head_dim, q_stride, k_c
                                 seq_lens, page_table, batch, max_pages, page_size, num_pages, group_start, prefix_lens, groups,
                                 max_q_len, max_len, max_prefix, scale, window, out, out_stride, workspace, ws_bytes,
                                 err_flag=None, stream=None):
-    """q4k_paged_attention where the sequences of a group share a prefix, which is computed once for all of them."""
+    """q4k_paged_attention where the sequences of a group share a prefix, which is computed once for all of them (if the workspace has room
+    for that: q4k_shared_prefix_attention_workspace_size of this call's sizes)."""
     K = _kinds()
     _check((_lib or load()).q4k_shared_prefix_attention(
         _dev(q, K.rows), _row_type(K, q, out), m, q_heads, kv_heads, head_dim, q_stride, _dev(k_cache, K.e4m3),

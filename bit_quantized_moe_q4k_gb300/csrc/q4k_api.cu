@@ -938,9 +938,10 @@ int q4k_shared_prefix_attention(const void* d_q, int dtype, int m, int q_heads, 
         if (reinterpret_cast<uintptr_t>(p) & 3u) return fail(Q4K_ERR_ALIGN, "group_start and prefix_lens must be 4-byte aligned");
     const size_t own = q4k_paged_attention_workspace_size(batch, m, q_heads, kv_heads, head_dim);
     const size_t more = prefix_workspace_bytes(batch, groups, m, q_heads, kv_heads, head_dim);
-    st = check_workspace(d_workspace, ws_bytes, own + align_up(more));
+    st = check_workspace(d_workspace, ws_bytes, own);
     if (st) return st;
-    const bool share = more > 0 && max_prefix >= page_size &&
+    // (a workspace without room for the shared part: one for calls of more rows than are shared, or for q4k_paged_attention)
+    const bool share = more > 0 && ws_bytes >= own + align_up(more) && max_prefix >= page_size &&
                        prefix_pays(B, dtype, q_heads, kv_heads, groups, max_q_len, max_len, max_prefix, window);
     SharedPrefix S{d_group_start, d_prefix_lens, groups, static_cast<uint8_t*>(d_workspace) + own};
     return cuda_status(launch_attention(B, d_q, dtype, q_stride, q_heads, kv_heads, head_dim,

@@ -507,7 +507,11 @@ int q4k_paged_attention(const void* d_q, int dtype, int m, int q_heads, int kv_h
  * shared, prefix_lens outside [0, max_pages*page_size] are clamped (Q4K_ERR_SEQ).
  * Limits (Q4K_ERR_LIMIT): q4k_paged_attention's, groups <= 2^24. Four launches where prefixes are shared (one more beside prompts). Within one softmax row the
  * fp32 sums of the two parts are joined once more: 2^-23 of the result.
- * Workspace: q4k_shared_prefix_attention_workspace_size bytes, any contents. */
+ * Workspace: q4k_shared_prefix_attention_workspace_size bytes, any contents. The size rises with batch, groups and m up to 2^20 query rows; for more,
+ *   where nothing is shared, it is q4k_paged_attention's. Mostly fp32 partial results: 4*head_dim bytes for each query row, those of a sequence and kv head
+ *   rounded up to a multiple of 8, and as much again, in steps of 256 rows for each group and kv head (58 MB for 256 sequences of one token with
+ *   32/8 heads of 128, 1.1 GB for 2^20 rows of 64 sequences). A workspace that has no room for this call's, but q4k_paged_attention_workspace_size bytes, is
+ *   taken as well: the call then runs q4k_paged_attention's kernels. So of one buffer for several calls the largest size of those that are to share counts. */
 size_t q4k_shared_prefix_attention_workspace_size(int batch, int groups, int m, int q_heads, int kv_heads, int head_dim);
 int q4k_shared_prefix_attention(const void* d_q, int dtype, int m, int q_heads, int kv_heads, int head_dim, int64_t q_stride,
                                 const void* d_k_cache, const void* d_v_cache, const float* d_k_scale,

@@ -448,3 +448,23 @@ def test_sequences_without_new_tokens_do_not_lead_their_group(dtype):
     assert s.lens[0] == 0 and s.lens[4] == 0
     s.table[[0, 4]], s.table[1] = 0x7FFFFFF0, -1
     s.run(8, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_workspace_without_room_for_what_is_shared(dtype, monkeypatch):
+    """One that was sized for q4k_paged_attention, for a call of more rows than are shared, or short by 256 bytes: every sequence reads its prefix
+    itself, with q4k_paged_attention's own result."""
+    s = Shared(62, [(300, samples(5))], 2, 64, 16)
+    size = q4k.q4k_shared_prefix_attention_workspace_size
+    monkeypatch.setenv("Q4K_SHARE_PREFIX", "0")
+    want = s.run(8, dtype)
+    monkeypatch.setenv("Q4K_SHARE_PREFIX", "1")
+    assert not np.array_equal(s.run(8, dtype), want)
+    for nbytes in (q4k.q4k_paged_attention_workspace_size(5, 5, 8, 2, 64), size(5, 1, 1 << 20, 8, 2, 64), size(5, 1, 5, 8, 2, 64) - 256):
+        ws = torch.full((nbytes + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        monkeypatch.setattr(q4k, "q4k_shared_prefix_attention_workspace_size", lambda *a: nbytes)
+        assert np.array_equal(s.run(8, dtype, ws=ws[:nbytes]), want)
+        assert (ws[nbytes:] == 0xA5).all()
+    monkeypatch.setattr(q4k, "q4k_shared_prefix_attention_workspace_size", lambda *a: q4k.q4k_paged_attention_workspace_size(5, 5, 8, 2, 64) - 1)
+    with pytest.raises(q4k.Q4KError):
+        s.run(8, dtype, ws=ws)

@@ -159,6 +159,15 @@ def test_prefix_empty_and_workspace():
         assert lib.q4k_shared_prefix_attention_workspace_size(*bad) == 0
 
 
+def test_prefix_workspace_rises_with_the_call():
+    size = q4k.load().q4k_shared_prefix_attention_workspace_size
+    for hq, hk, d in ((32, 8, 128), (14, 2, 64), (8, 1, 128), (5, 5, 64)):
+        most = (1 << 20) // hq
+        for sizes in ([size(64, 3, m, hq, hk, d) for m in [*range(1, 700), 4096, most - 1, most]], [size(b, 3, 600, hq, hk, d) for b in range(1, 700)],
+                      [size(300, g, 600, hq, hk, d) for g in range(1, 400)]):
+            assert all(x <= y for x, y in zip(sizes, sizes[1:]))
+
+
 def test_prefix_binding_refuses_other_element_types():
     f32, f8, i32, u8, f16 = (FakeCuda(t) for t in (torch.float32, torch.float8_e4m3fn, torch.int32, torch.uint8, torch.float16))
     good = [f32, 3, 8, 2, 128, 1024, f8, f8, f32, f32, i32, i32, i32, 2, 4, 16, 8, i32, i32, 1, 2, 64, 32, 0.1, 0, f32, 1024, u8, 1 << 30,
