@@ -12,8 +12,8 @@
 //   2. verify_pick_kernel: a cluster of up to eight CTAs a sequence. An acceptance whose two sides differ by more than 2^-14 stands;
 //      another is computed again from weights good to 2^-41. The token is drawn in weights good to 2^-31, as 64-bit integers in units of
 //      2^-b of the row's largest, b = 62 - log2(vocabulary): their sums are exact in any order. One row of logits, and of the drafts' probabilities, is read once.
-//      Bound by instructions, 58 a token.
-// 256 sequences of 4 rows of 131072 fp32: 85 us (6.3 TB/s) and 96; 64 of up to 6 rows in bf16: 57 together; one of 5 rows of 32000: 12.
+//      Bound by instructions, 58 a token, where there are many sequences, by each CTA's chain of loads, sums and barriers where there are few.
+// 256 sequences of 4 rows of 131072 fp32: 85 us (6.3 TB/s) and 96; 64 of up to 6 rows in bf16: 57 together; one of 5 rows of 32000: 11.5.
 // Both in one kernel, a cluster going through its rows one after another: 172 to 177, 62 and 15 us.
 #include <atomic>
 
